@@ -11,7 +11,9 @@
  *   5. fastar_sparse_attn     (bucket-restricted self-attention)
  *   6. fastar_annca_select    (frame-relevant prompt tokens)
  *   7. fastar_cross_attn_subset (cross-attention over the kept prompt tokens)
- * and fastar_dense_attn is the dense baseline the speed-up is measured against.
+ * and fastar_dense_attn is the dense baseline the speed-up is measured against.  Section
+ * 10 keeps the dense path's append-only cache in 4 bits, and adds the norm and rotation
+ * of q and k per head.
  * The merge variant (technical summary §2.A, Theoretical Basis: Lemma 5.1 — merging
  * identical keys is exact when their values are averaged and their logit is shifted
  * by the group size) replaces step 3 with fastar_cache_compact_merge and step 5 with
@@ -80,6 +82,7 @@ extern "C" {
 #define FASTAR_DEV_BAD_BUCKET 2   /* a bucket id was outside [0, B)               */
 #define FASTAR_DEV_BAD_INDEX 4    /* an index list pointed outside its range      */
 #define FASTAR_DEV_TIMEOUT 8      /* a bounded on-chip wait gave up; outputs invalid */
+#define FASTAR_DEV_NONFINITE 16   /* a NaN or infinity had no 4-bit value; stored as 0 */
 
 /* ---- limits ------------------------------------------------------------------------ */
 #define FASTAR_MAX_B 256          /* buckets per head                              */
@@ -95,6 +98,7 @@ extern "C" {
 #define FASTAR_OP_MATCH_ANN 5
 #define FASTAR_OP_CROSS_ATTN 6
 #define FASTAR_OP_MATCH_PQ 7
+#define FASTAR_OP_KV4_ATTN 8
 
 /* Bytes of workspace `op` needs for the given sizes (0 if it needs none).
  * MATCH: n = Nq, M = cache capacity.  SORT: n = elements per head before the
@@ -102,6 +106,8 @@ extern "C" {
  * bucket-ordered copy of the cache K/V in it).  ANNCA: F frames, P prompt tokens.
  * MATCH_ANN: n = Nq, M, d, B, r.  CROSS_ATTN: d, P, F (the bf16 path's gathered copy of
  * the kept prompt rows).  MATCH_PQ: n = Nq, M, d (the decoded cached keys).
+ * KV4_ATTN: H = query heads, n = tokens of the call, M = cache capacity, d, B = KV heads (the
+ * partial results of the key splits; 0 where the keys are not split).
  * Unused arguments are ignored.  Returns 0 for an unknown op. */
 size_t fastar_workspace_bytes(int op, int H, int64_t n, int64_t M, int d, int B, int r,
                               int64_t P, int F);
@@ -550,6 +556,79 @@ int fastar_sinusoidal_embedding(const float* t, int nb, int dim, void* out, int6
 int fastar_dense_append(int dtype, int H, int64_t nq, int d, const void* k_cur, const void* v_cur,
                         int64_t head_stride, int64_t token_stride, void* k_cache, void* v_cache,
                         int64_t cap, int64_t at, cudaStream_t stream);
+
+/* ---- 10. an append-only cache in 4 bits, and the norm and rotation before it ----------------
+ * Not on the pages: the dense path's cache grows with the rollout; held in 4 bits (4.5 with
+ * the scales) it takes 3.6 times less memory and traffic than in bf16.  One step of a block is
+ *   fastar_qk_norm_rope (q, k) -> fastar_kv4_append (k, v) -> fastar_kv4_attn (q).
+ * The 4-bit form: 16 consecutive channels of a row share a scale s, a float8 e4m3 (one byte);
+ * a value is a 4-bit float e2m1 (sign, magnitude 0 0.5 1 1.5 2 3 4 6) times s * 2^e, with an
+ * optional exponent e per head (exps int32 [H]; NULL: 0; held to [-64, 64]) for rows whose
+ * magnitudes lie outside s's range (full precision for max|x| * 2^-e in [0.1, 2688]).
+ * codes uint8 [H, cap, d / 2], the even channel in the low nibble; scales uint8
+ * [H, cap, d / 16]; both contiguous and 16-byte aligned; cap a multiple of 16 (FASTAR_EINVAL).
+ * Every stored value is exact in bf16, fp16 and fp32 for e = 0. */
+
+/* RMS norm of every head's row of q [Hq, n, d] and k [Hk, n, d] and rotary positions of three
+ * axes, in one pass, into q_out and k_out (any strides; dtype F32 or BF16, fp32 arithmetic,
+ * rounded once):
+ *   wq / wk non-NULL (fp32 [d], 16-byte aligned): x / sqrt(mean(x^2) + eps) * w over the d
+ *   channels of the head; NULL: no norm for that tensor;
+ *   the first axis_t channels turn with the token's frame, the next axis_h with its row, the
+ *   next axis_w with its column (even widths >= 0, sum <= d; channels past the sum pass
+ *   unrotated): the pair (2j, 2j + 1) of a part of width da by pos * theta^(-2j / da), as in
+ *   fastar_rmsnorm_rope.  pos int32 [n, 3] (any sign): the tokens' (frame, row, column); NULL:
+ *   token i sits at frame f0 + i / (grid_h grid_w), row (i / grid_w) % grid_h, column
+ *   i % grid_w, f0 = t0 + *t0_dev (t0_dev optional).  Angles are formed modulo one turn, so
+ *   they hold at far positions.
+ * Hk = 0 (or Hq = 0): only the other tensor.  In place (q_out = q with the same strides) is
+ * allowed; otherwise outputs must not overlap inputs.  n <= INT32_MAX, theta > 1. */
+int fastar_qk_norm_rope(int dtype, int64_t n, int d, int Hq, const void* q, int64_t q_head_stride,
+                        int64_t q_token_stride, void* q_out, int64_t qo_head_stride, int64_t qo_token_stride, int Hk,
+                        const void* k, int64_t k_head_stride, int64_t k_token_stride, void* k_out,
+                        int64_t ko_head_stride, int64_t ko_token_stride, const float* wq, const float* wk, float eps,
+                        int axis_t, int axis_h, int axis_w, const int32_t* pos, int t0, const int32_t* t0_dev,
+                        int grid_h, int grid_w, float theta, cudaStream_t stream);
+
+/* Appends n rows of k and v [H, n, d] to the 4-bit cache: head h's rows at[h] .. at[h] + n
+ * (at int32 [H] on the device; NULL: 0).  len_out[h] = at[h] + n (optional; a different array
+ * than at, FASTAR_EINVAL otherwise).  Per 16 channels, with x' = x 2^-e:
+ *   s = e4m3(max|x'| / 6), code = e2m1(x' / s), each rounded to nearest with ties to even and
+ *   held to the largest finite value; s = 0 stores zeros.
+ * A NaN or an infinity is stored as 0, takes no part in the maximum and sets
+ * FASTAR_DEV_NONFINITE.  A start outside [0, cap] sets FASTAR_DEV_BAD_LEN and stores nothing;
+ * rows that would pass cap set it and are dropped (len_out = cap).  Rows outside the appended
+ * ones are left as they were.  n > cap: FASTAR_ECAPACITY.  dev_status optional. */
+int fastar_kv4_append(int dtype, int H, int64_t n, int d, const void* k, int64_t k_head_stride, int64_t k_token_stride,
+                      const void* v, int64_t v_head_stride, int64_t v_token_stride, const int32_t* k_exp,
+                      const int32_t* v_exp, const int32_t* at, uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                      uint8_t* v_scales, int64_t cap, int32_t* len_out, int32_t* dev_status, cudaStream_t stream);
+
+/* The values that rows first .. first + n of every head of a 4-bit K (or V) cache stand for,
+ * as out [H, n, d] of dtype (strided).  Reads what is there: the rows' lengths are the caller's.
+ * first + n > cap: FASTAR_ECAPACITY. */
+int fastar_kv4_read(int dtype, int H, int64_t n, int d, const uint8_t* codes, const uint8_t* scales,
+                    const int32_t* exps, int64_t cap, int64_t first, void* out, int64_t o_head_stride,
+                    int64_t o_token_stride, cudaStream_t stream);
+
+/* Softmax attention of q [Hq, nq, d] over the 4-bit cache; query head h reads KV head
+ * h / (Hq / Hkv) (Hq a multiple of Hkv):
+ *   O[h,t] = sum_{j < see(t)} softmax_j(q_t . k_j * scale) v_j
+ * see(t) = len, or with block > 0 the call's tokens are the cache's last nq rows and token t
+ * sees them up to the end of its own block of `block` tokens: see(t) = max(0, len - nq +
+ * min(nq, (t / block + 1) * block)); block = 1 is causal, block = a frame's tokens lets a frame
+ * see itself and the frames before it.  see(t) = 0: O = 0, lse = -inf.  len int32 [Hkv] on the
+ * device (outside [0, cap]: held to it, FASTAR_DEV_BAD_LEN); rows from len on are never used.
+ * lse float [Hq, nq] optional.  Hq * nq <= INT32_MAX (FASTAR_ECAPACITY).
+ * workspace (optional): fastar_workspace_bytes(FASTAR_OP_KV4_ATTN, Hq, nq, cap, d, Hkv, ...)
+ * bytes for the partial results of key splits; NULL: the keys are not split (slower with few
+ * rows).  Calls that share a workspace must not overlap on the GPU. */
+int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d, int64_t q_head_stride,
+                    int64_t q_token_stride, const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                    const uint8_t* v_scales, const int32_t* k_exp, const int32_t* v_exp, int64_t cap,
+                    const int32_t* len, int64_t block, float scale, void* out, int64_t o_head_stride,
+                    int64_t o_token_stride, float* lse, int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                    cudaStream_t stream);
 
 #ifdef __cplusplus
 }

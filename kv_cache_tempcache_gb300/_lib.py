@@ -18,7 +18,9 @@ LIB_PATH = os.path.join(HERE, "libfastar.so")
 F32, BF16 = 0, 1
 OK, EINVAL, EUNSUPPORTED, ECAPACITY, EWORKSPACE, ECUDA = 0, -1, -2, -3, -4, -5
 DEV_BAD_LEN, DEV_BAD_BUCKET, DEV_BAD_INDEX = 1, 2, 4
+DEV_TIMEOUT, DEV_NONFINITE = 8, 16
 OP_MATCH, OP_SORT, OP_SPARSE_ATTN, OP_ANNCA, OP_MATCH_ANN, OP_CROSS_ATTN, OP_MATCH_PQ = 1, 2, 3, 4, 5, 6, 7
+OP_KV4_ATTN = 8
 MAX_B, MAX_R, MAX_P = 256, 8, 1024
 
 _P = ctypes.c_void_p
@@ -70,6 +72,12 @@ _SIGS = {
     "fastar_layernorm_mod": [_P, _L, _L, _I, _F, _P, _P, _P, _P, _P, _P, _P, _L, _P],
     "fastar_rmsnorm_rope": [_P, _L, _L, _I, _I, _F, _P, _I, _I, _P, _I, _I, _F, _P],
     "fastar_sinusoidal_embedding": [_P, _I, _I, _P, _L, _P],
+    "fastar_qk_norm_rope": [_I, _L, _I, _I, _P, _L, _L, _P, _L, _L, _I, _P, _L, _L, _P, _L, _L, _P, _P, _F, _I, _I,
+                            _I, _P, _I, _P, _I, _I, _F, _P],
+    "fastar_kv4_append": [_I, _I, _L, _I, _P, _L, _L, _P, _L, _L, _P, _P, _P, _P, _P, _P, _P, _L, _P, _P, _P],
+    "fastar_kv4_read": [_I, _I, _L, _I, _P, _P, _P, _L, _L, _P, _L, _L, _P],
+    "fastar_kv4_attn": [_P, _I, _I, _I, _L, _I, _L, _L, _P, _P, _P, _P, _P, _P, _L, _P, _L, _F, _P, _L, _L, _P, _P,
+                        _P, _S, _P],
 }
 _RESTYPES = {"fastar_status_string": ctypes.c_char_p, "fastar_workspace_bytes": ctypes.c_size_t,
              "fastar_kernel_launches": ctypes.c_longlong, "fastar_last_cuda_error": ctypes.c_char_p}
@@ -416,6 +424,136 @@ def fastar_rmsnorm_rope(x, d, weight=None, rope=False, t0=0, grid=(1, 1), eps=1e
 def fastar_sinusoidal_embedding(t, out, stream=None):
     nb, dim = out.shape
     _call("fastar_sinusoidal_embedding", ptr(t), nb, dim, out.data_ptr(), out.stride(0), stream_handle(stream))
+
+
+# ---- the 4-bit cache, and the norm and rotation before it -------------------------------------
+
+def _expect(name, t, dtype, shape=None):
+    """Refuses what a kernel would misread: another type, shape or layout."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None:
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _expect_here(*tensors):
+    """Refuses tensors that are not on the current CUDA device (the one the call runs on)."""
+    for t in tensors:
+        if t is not None and not (t.is_cuda and t.device.index == torch.cuda.current_device()):
+            raise ValueError(f"tensors must be on the current CUDA device, not on {t.device}")
+
+
+def _expect_opt(name, t, dtype, shape=None):
+    return None if t is None else _expect(name, t, dtype, shape)
+
+
+def _expect_rows(name, t, dtype, shape):
+    """A [H, n, d] view of rows with a contiguous last dimension: (address, strides)."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    hs, ts = tok_strides(t)
+    # the stride of a dimension of one element says nothing (torch may give any)
+    H, n, d = t.shape
+    if n <= 1:
+        ts = d
+    if H <= 1:
+        hs = n * d
+    return _expect(name, t, dtype), hs, ts
+
+
+def _expect_kv4(name, codes, scales, H, d):
+    """A [H, cap, d / 2] array of codes and its [H, cap, d / 16] scales."""
+    if codes.dim() != 3:
+        raise ValueError(f"{name}_codes must be [H, cap, d / 2]")
+    cap = codes.shape[1]
+    return (_expect(name + "_codes", codes, torch.uint8, (H, cap, d // 2)),
+            _expect(name + "_scales", scales, torch.uint8, (H, cap, d // 16)), cap)
+
+
+def fastar_qk_norm_rope(q, k, q_out, k_out, wq=None, wk=None, eps=1e-6, axes=(0, 0, 0), pos=None, t0=0, t0_dev=None,
+                        grid=(1, 1), theta=10000.0, stream=None):
+    """RMS norm of every head (weights given) and rotary positions of three axes: q [Hq, n, d]
+    -> q_out, k [Hk, n, d] -> k_out (k and k_out None: q alone).  axes: the channels that turn
+    with the frame, the row and the column; pos [n, 3] int32, or the grid's positions."""
+    Hq, n, d = q.shape
+    dt = q.dtype
+    code = dtype_code(dt)
+    qa = _expect_rows("q", q, dt, (Hq, n, d)) + _expect_rows("q_out", q_out, dt, (Hq, n, d))
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    Hk, ka = 0, (None, 0, 0, None, 0, 0)
+    if k is not None:
+        Hk = k.shape[0]
+        ka = _expect_rows("k", k, dt, (Hk, n, d)) + _expect_rows("k_out", k_out, dt, (Hk, n, d))
+    _expect_here(q, q_out, k, k_out, wq, wk, pos, t0_dev)
+    _call("fastar_qk_norm_rope", code, n, d, Hq, *qa, Hk, *ka, _expect_opt("wq", wq, torch.float32, (d,)),
+          _expect_opt("wk", wk, torch.float32, (d,)), float(eps), int(axes[0]), int(axes[1]), int(axes[2]),
+          _expect_opt("pos", pos, torch.int32, (n, 3)), int(t0), _expect_opt("t0_dev", t0_dev, torch.int32, (1,)),
+          int(grid[0]), int(grid[1]), float(theta), stream_handle(stream))
+
+
+def fastar_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, at=None, len_out=None, dev_status=None, k_exp=None,
+                      v_exp=None, stream=None):
+    """Rows k, v [H, n, d] into the 4-bit cache (codes [H, cap, d / 2], scales [H, cap, d / 16],
+    uint8) from row at[h] on (int32 [H]; None: 0); len_out[h] = at[h] + n."""
+    H, n, d = k.shape
+    code = dtype_code(k.dtype)
+    kp, khs, kts = _expect_rows("k", k, k.dtype, (H, n, d))
+    vp, vhs, vts = _expect_rows("v", v, k.dtype, (H, n, d))
+    kc, ks, cap = _expect_kv4("k", k_codes, k_scales, H, d)
+    vc, vs, vcap = _expect_kv4("v", v_codes, v_scales, H, d)
+    if cap != vcap:
+        raise ValueError("K and V caches must have the same capacity")
+    i32 = torch.int32
+    _expect_here(k, v, k_codes, k_scales, v_codes, v_scales, at, len_out, dev_status, k_exp, v_exp)
+    _call("fastar_kv4_append", code, H, n, d, kp, khs, kts, vp, vhs, vts, _expect_opt("k_exp", k_exp, i32, (H,)),
+          _expect_opt("v_exp", v_exp, i32, (H,)), _expect_opt("at", at, i32, (H,)), kc, ks, vc, vs, cap,
+          _expect_opt("len_out", len_out, i32, (H,)), _expect_opt("dev_status", dev_status, i32, (1,)),
+          stream_handle(stream))
+
+
+def fastar_kv4_read(codes, scales, first, out, exps=None, stream=None):
+    """The values of rows first .. first + n of a 4-bit cache -> out [H, n, d]."""
+    H, n, d = out.shape
+    code = dtype_code(out.dtype)
+    cp, sp, cap = _expect_kv4("cache", codes, scales, H, d)
+    op, ohs, ots = _expect_rows("out", out, out.dtype, (H, n, d))
+    _expect_here(codes, scales, out, exps)
+    _call("fastar_kv4_read", code, H, n, d, cp, sp, _expect_opt("exps", exps, torch.int32, (H,)), cap, int(first), op,
+          ohs, ots, stream_handle(stream))
+
+
+def fastar_kv4_attn(q, k_codes, k_scales, v_codes, v_scales, lens, scale, out, lse=None, block=0, k_exp=None,
+                    v_exp=None, dev_status=None, workspace=None, stream=None):
+    """Attention of q [Hq, nq, d] over the first lens[h] rows of a 4-bit cache of Hkv heads
+    (Hq a multiple of Hkv); block > 0: the tokens are the cache's last nq rows and see no block
+    of that many tokens later than their own.  workspace: workspace_bytes(OP_KV4_ATTN, Hq, nq,
+    cap, d, Hkv) bytes (None: the keys are not split)."""
+    Hq, nq, d = q.shape
+    code = dtype_code(q.dtype)
+    Hkv = k_codes.shape[0]
+    qp, qhs, qts = _expect_rows("q", q, q.dtype, (Hq, nq, d))
+    op, ohs, ots = _expect_rows("out", out, q.dtype, (Hq, nq, d))
+    kc, ks, cap = _expect_kv4("k", k_codes, k_scales, Hkv, d)
+    vc, vs, vcap = _expect_kv4("v", v_codes, v_scales, Hkv, d)
+    if cap != vcap:
+        raise ValueError("K and V caches must have the same capacity")
+    i32 = torch.int32
+    nb = 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        nb = workspace.numel() * workspace.element_size()
+    _expect_here(q, k_codes, k_scales, v_codes, v_scales, lens, out, lse, k_exp, v_exp, dev_status, workspace)
+    _call("fastar_kv4_attn", qp, code, Hq, Hkv, nq, d, qhs, qts, kc, ks, vc, vs,
+          _expect_opt("k_exp", k_exp, i32, (Hkv,)), _expect_opt("v_exp", v_exp, i32, (Hkv,)), cap,
+          _expect("lens", lens, i32, (Hkv,)), int(block), float(scale), op, ohs, ots,
+          _expect_opt("lse", lse, torch.float32, (Hq, nq)), _expect_opt("dev_status", dev_status, i32, (1,)),
+          None if workspace is None else _expect("workspace", workspace, workspace.dtype), nb, stream_handle(stream))
 
 
 def fastar_dense_append(k_cur, v_cur, k_cache, v_cache, at, stream=None):

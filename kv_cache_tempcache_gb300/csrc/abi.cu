@@ -35,6 +35,13 @@ int check_tok(const void* p, int dtype, int d, int64_t hs, int64_t ts, int64_t n
   return FASTAR_OK;
 }
 
+// The 4-bit cache: a capacity in whole 16-row groups (so that a head's codes and scales
+// start on 16 bytes), and 16-byte aligned arrays.
+int check_kv4_cap(int64_t cap) { return cap < 16 || cap % 16 || cap > INT32_MAX ? FASTAR_EINVAL : FASTAR_OK; }
+int check_kv4(const void* codes, const void* scales) {
+  return codes && scales && aligned16(codes) && aligned16(scales) ? FASTAR_OK : FASTAR_EINVAL;
+}
+
 thread_local cudaError_t g_last_cuda = cudaSuccess;
 
 int cuda_rc(cudaError_t e) {
@@ -47,7 +54,7 @@ int cuda_rc(cudaError_t e) {
 
 extern "C" {
 
-int fastar_version(void) { return 110; }
+int fastar_version(void) { return 120; }
 
 const char* fastar_last_cuda_error(void) { return cudaGetErrorString(g_last_cuda); }
 
@@ -82,6 +89,9 @@ size_t fastar_workspace_bytes(int op, int H, int64_t n, int64_t M, int d, int B,
     case FASTAR_OP_CROSS_ATTN:
       if ((d != 64 && d != 128) || P < 1 || F < 1) return 0;
       return 2 * sizeof(uint16_t) * (size_t)H * F * P * d + 1024;
+    case FASTAR_OP_KV4_ATTN:
+      if ((d != 64 && d != 128) || B < 1 || H % B || M < 1 || n < 1) return 0;
+      return fastar::kv4_attn_workspace(d, H, B, n, M);
     default: return 0;
   }
 }
@@ -678,6 +688,117 @@ int fastar_dense_append(int dtype, int H, int64_t nq, int d, const void* k_cur, 
   return cuda_rc(fastar::launch_dense_append(dtype, d, H, nq, TokView{k_cur, head_stride, token_stride},
                                              TokView{v_cur, head_stride, token_stride}, k_cache, v_cache, cap,
                                              at, stream));
+}
+
+int fastar_qk_norm_rope(int dtype, int64_t n, int d, int Hq, const void* q, int64_t q_head_stride,
+                        int64_t q_token_stride, void* q_out, int64_t qo_head_stride, int64_t qo_token_stride, int Hk,
+                        const void* k, int64_t k_head_stride, int64_t k_token_stride, void* k_out,
+                        int64_t ko_head_stride, int64_t ko_token_stride, const float* wq, const float* wk, float eps,
+                        int axis_t, int axis_h, int axis_w, const int32_t* pos, int t0, const int32_t* t0_dev,
+                        int grid_h, int grid_w, float theta, cudaStream_t stream) {
+  int rc = check_dtype_d(dtype, d);
+  if (rc) return rc;
+  if (n < 0 || n > INT32_MAX || Hq < 0 || Hk < 0 || Hq > (1 << 20) || Hk > (1 << 20)) return FASTAR_EINVAL;
+  const int axes[3] = {axis_t, axis_h, axis_w};
+  int64_t sum = 0;
+  for (int a : axes) {
+    if (a < 0 || a % 2) return FASTAR_EINVAL;
+    sum += a;
+  }
+  if (sum > d || !(theta > 1.f) || !(theta < 3.0e38f)) return FASTAR_EINVAL;
+  if ((wq || wk) && (!(eps > 0.f) || !(eps < 3.0e38f))) return FASTAR_EINVAL;
+  if (sum > 0 && !pos && (grid_h < 1 || grid_w < 1)) return FASTAR_EINVAL;
+  if (n == 0 || (Hq == 0 && Hk == 0)) return FASTAR_OK;
+  if ((rc = check_tok(q, dtype, d, q_head_stride, q_token_stride, n, Hq))) return rc;
+  if ((rc = check_tok(q_out, dtype, d, qo_head_stride, qo_token_stride, n, Hq))) return rc;
+  if ((rc = check_tok(k, dtype, d, k_head_stride, k_token_stride, n, Hk))) return rc;
+  if ((rc = check_tok(k_out, dtype, d, ko_head_stride, ko_token_stride, n, Hk))) return rc;
+  if ((wq && !aligned16(wq)) || (wk && !aligned16(wk))) return FASTAR_EINVAL;
+  // in place only row by row
+  if (Hq > 0 && q == q_out && (q_head_stride != qo_head_stride || q_token_stride != qo_token_stride))
+    return FASTAR_EINVAL;
+  if (Hk > 0 && k == k_out && (k_head_stride != ko_head_stride || k_token_stride != ko_token_stride))
+    return FASTAR_EINVAL;
+  return cuda_rc(fastar::launch_qk_norm_rope(
+      dtype, d, n, Hq, TokView{q, q_head_stride, q_token_stride}, q_out, qo_head_stride, qo_token_stride, Hk,
+      TokView{k, k_head_stride, k_token_stride}, k_out, ko_head_stride, ko_token_stride, wq, wk, eps, axes, pos, t0,
+      t0_dev, grid_h < 1 ? 1 : grid_h, grid_w < 1 ? 1 : grid_w, theta, stream));
+}
+
+int fastar_kv4_append(int dtype, int H, int64_t n, int d, const void* k, int64_t k_head_stride, int64_t k_token_stride,
+                      const void* v, int64_t v_head_stride, int64_t v_token_stride, const int32_t* k_exp,
+                      const int32_t* v_exp, const int32_t* at, uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                      uint8_t* v_scales, int64_t cap, int32_t* len_out, int32_t* dev_status, cudaStream_t stream) {
+  int rc = check_dtype_d(dtype, d);
+  if (rc) return rc;
+  if (H < 0 || n < 0 || (rc = check_kv4_cap(cap)) || n > INT32_MAX) return rc ? rc : FASTAR_EINVAL;
+  if (n > cap) return FASTAR_ECAPACITY;
+  if (at && at == len_out) return FASTAR_EINVAL;   // the heads' blocks read `at` while one of them writes
+  if (H == 0 || (n == 0 && !len_out)) return FASTAR_OK;
+  if ((rc = check_tok(k, dtype, d, k_head_stride, k_token_stride, n, H))) return rc;
+  if ((rc = check_tok(v, dtype, d, v_head_stride, v_token_stride, n, H))) return rc;
+  if ((rc = check_kv4(k_codes, k_scales)) || (rc = check_kv4(v_codes, v_scales))) return rc;
+  if (k_codes == v_codes || k_scales == v_scales) return FASTAR_EINVAL;
+  return cuda_rc(fastar::launch_kv4_append(dtype, d, H, n, TokView{k, k_head_stride, k_token_stride},
+                                           TokView{v, v_head_stride, v_token_stride}, k_exp, v_exp, at, k_codes,
+                                           k_scales, v_codes, v_scales, cap, len_out, dev_status, stream));
+}
+
+int fastar_kv4_read(int dtype, int H, int64_t n, int d, const uint8_t* codes, const uint8_t* scales,
+                    const int32_t* exps, int64_t cap, int64_t first, void* out, int64_t o_head_stride,
+                    int64_t o_token_stride, cudaStream_t stream) {
+  int rc = check_dtype_d(dtype, d);
+  if (rc) return rc;
+  if (H < 0 || n < 0 || first < 0 || (rc = check_kv4_cap(cap))) return rc ? rc : FASTAR_EINVAL;
+  if (first > cap || n > cap - first) return FASTAR_ECAPACITY;
+  if (H == 0 || n == 0) return FASTAR_OK;
+  if ((rc = check_kv4(codes, scales))) return rc;
+  if ((rc = check_tok(out, dtype, d, o_head_stride, o_token_stride, n, H))) return rc;
+  return cuda_rc(fastar::launch_kv4_read(dtype, d, H, codes, scales, exps, cap, first, n, out, o_head_stride,
+                                         o_token_stride, stream));
+}
+
+int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d, int64_t q_head_stride,
+                    int64_t q_token_stride, const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                    const uint8_t* v_scales, const int32_t* k_exp, const int32_t* v_exp, int64_t cap,
+                    const int32_t* len, int64_t block, float scale, void* out, int64_t o_head_stride,
+                    int64_t o_token_stride, float* lse, int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                    cudaStream_t stream) {
+  int rc = check_dtype_d(dtype, d);
+  if (rc) return rc;
+  if (Hq < 0 || Hkv < 1 || Hq % Hkv || nq < 0 || block < 0 || (rc = check_kv4_cap(cap))) return rc ? rc : FASTAR_EINVAL;
+  if (nq > INT32_MAX || (int64_t)Hq * nq > INT32_MAX) return FASTAR_ECAPACITY;
+  if (!(scale > 0.f) || !(scale < 3.0e38f)) return FASTAR_EINVAL;
+  if (Hq == 0 || nq == 0) return FASTAR_OK;
+  if ((rc = check_tok(q, dtype, d, q_head_stride, q_token_stride, nq, Hq))) return rc;
+  if ((rc = check_tok(out, dtype, d, o_head_stride, o_token_stride, nq, Hq))) return rc;
+  if ((rc = check_kv4(k_codes, k_scales)) || (rc = check_kv4(v_codes, v_scales))) return rc;
+  if (!len) return FASTAR_EINVAL;
+  if (workspace) {
+    const size_t need = fastar::kv4_attn_workspace(d, Hq, Hkv, nq, cap);
+    if (workspace_bytes < need || !aligned16(workspace)) return FASTAR_EWORKSPACE;
+  }
+  fastar::Kv4AttnArgs a{};
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.q = TokView{q, q_head_stride, q_token_stride};
+  a.nq = nq;
+  a.kc = k_codes;
+  a.ks = k_scales;
+  a.vc = v_codes;
+  a.vs = v_scales;
+  a.k_exp = k_exp;
+  a.v_exp = v_exp;
+  a.cap = cap;
+  a.len = len;
+  a.block = block;
+  a.scale = scale;
+  a.out = out;
+  a.o_hs = o_head_stride;
+  a.o_ts = o_token_stride;
+  a.lse = lse;
+  a.status = dev_status;
+  return cuda_rc(fastar::launch_kv4_attn(dtype, d, a, workspace, stream));
 }
 
 }  // extern "C"

@@ -190,4 +190,42 @@ cudaError_t launch_dense_append(int dtype, int d, int H, int64_t nq, TokView kcu
                                 void* k_cache, void* v_cache, int64_t cap, int64_t at,
                                 cudaStream_t s);
 
+// ---- per-head norm and rotation, the 4-bit cache ------------------------------------------
+cudaError_t launch_qk_norm_rope(int dtype, int d, int64_t n, int Hq, TokView q, void* qo, int64_t qo_hs, int64_t qo_ts,
+                                int Hk, TokView k, void* ko, int64_t ko_hs, int64_t ko_ts, const float* wq,
+                                const float* wk, float eps, const int* axes, const int32_t* pos, int t0,
+                                const int32_t* t0_dev, int gh, int gw, float theta, cudaStream_t s);
+cudaError_t launch_kv4_append(int dtype, int d, int H, int64_t n, TokView k, TokView v, const int32_t* k_exp,
+                              const int32_t* v_exp, const int32_t* at, uint8_t* kc, uint8_t* ks, uint8_t* vc,
+                              uint8_t* vs, int64_t cap, int32_t* len_out, int32_t* status, cudaStream_t s);
+cudaError_t launch_kv4_read(int dtype, int d, int H, const uint8_t* codes, const uint8_t* scales, const int32_t* exps,
+                            int64_t cap, int64_t first, int64_t n, void* out, int64_t hs, int64_t ts, cudaStream_t s);
+
+constexpr int kKv4MaxSplits = 256;
+
+struct Kv4AttnArgs {
+  int Hq, Hkv;
+  TokView q;
+  int64_t nq;
+  const uint8_t *kc, *ks, *vc, *vs;   // [Hkv, cap, d / 2] codes and [Hkv, cap, d / 16] scales
+  const int32_t *k_exp, *v_exp;       // [Hkv] or null
+  int64_t cap;
+  const int32_t* len;                 // [Hkv]
+  int64_t block;                      // 0, or the tokens of a block that sees no later one
+  float scale;
+  void* out;
+  int64_t o_hs, o_ts;
+  float* lse;
+  int32_t* status;
+  // filled in by the launcher: splits of the keys and their partials (fp32; maximum and sum)
+  int splits;
+  float* part_o;                      // [splits, Hq, nq, d]
+  float2* part_ml;                    // [splits, Hq, nq]
+};
+
+// Splits of the keys for these sizes, and the bytes of their partials (0: one split).
+int kv4_attn_splits(int dtype, int d, int Hq, int Hkv, int64_t nq, int64_t cap);
+size_t kv4_attn_workspace(int d, int Hq, int Hkv, int64_t nq, int64_t cap);
+cudaError_t launch_kv4_attn(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStream_t s);
+
 }  // namespace fastar

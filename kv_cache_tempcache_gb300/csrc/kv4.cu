@@ -1,0 +1,223 @@
+// Writing rows of K and V into the 4-bit cache, and reading rows back as the values they
+// stand for.  Both are bound by HBM: one pass, 16 channels (one scale) to a lane, d / 16
+// lanes to a row, so a warp's codes and scales leave (or arrive) as one contiguous run of
+// 256 and 32 bytes.
+//
+// The scale is s = e4m3(max|x| / 6), the code e2m1(x / s), both rounded to nearest with ties
+// to even and held to the largest finite value.  Both roundings are exact decisions:
+//  - max|x| / 6 is formed rounded to odd (towards zero, the last bit set when inexact),
+//    which a second rounding to 4 bits cannot send to the wrong side of a middle;
+//  - a bf16 x has 8 significant bits and the middle of two codes times s at most 7, so x/s
+//    is the middle itself or at least 2^-8 away from it (relative).  x * (1/s) in fp32 is
+//    within 2^-23 of x/s; rounded to 17 bits it is the middle exactly when x/s is, and the
+//    conversion then breaks the tie as the definition does;
+//  - an fp32 x is compared with the seven middles themselves (exact in fp32).
+// A NaN or an infinity has no 4-bit value: it is stored as 0, takes no part in the maximum
+// and sets a status bit, so the cache never holds one.
+#include <climits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "kv4.cuh"
+#include "tmap.h"
+
+namespace fastar {
+
+namespace {
+
+constexpr int kThreadsQ = 256;
+
+struct Kv4AppendDev {
+  int H;
+  int64_t n, cap;
+  const void *k, *v;
+  int64_t k_hs, k_ts, v_hs, v_ts;
+  const int32_t *k_exp, *v_exp, *at;
+  uint8_t *kc, *ks, *vc, *vs;
+  int32_t* len_out;
+  int32_t* status;
+};
+
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* f) {
+  load8(p, f);
+  load8(p + 8, f + 8);
+}
+__device__ __forceinline__ void load16(const float* p, float* f) {
+  load8(p, f);
+  load8(p + 8, f + 8);
+}
+
+// e4m3 of a / 6 (a >= 0, finite), as its byte.
+__device__ __forceinline__ uint32_t scale_byte(float a) {
+  a = fminf(a, 3.0e38f);   // 2^-e may have carried a finite value to infinity
+  float r = __fdiv_rz(a, 6.0f);
+  if (fmaf(r, 6.0f, -a) != 0.f) r = __int_as_float(__float_as_int(r) | 1);
+  uint16_t b;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(0.f), "f"(r));
+  return b & 0xffu;
+}
+
+// Codes of two values a (low nibble) and b, already divided by the scale.
+__device__ __forceinline__ uint32_t pair_code(float a, float b) {
+  uint32_t r;
+  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float snap17(float r) { return __int_as_float((__float_as_int(r) + 0x40) & ~0x7f); }
+
+// The 16 codes of x (two words) and the scale's byte.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t quantise16(float* x, float down, uint2& codes, bool& bad) {
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const bool fin = (__float_as_uint(x[i]) & 0x7f800000u) != 0x7f800000u;
+    bad |= !fin;
+    x[i] = fin ? x[i] * down : 0.f;
+    a = fmaxf(a, fabsf(x[i]));
+  }
+  const uint32_t sb = scale_byte(a);
+  const float s = __half2float(__ushort_as_half((uint16_t)(kv4::scale_f16x2(sb) & 0xffffu)));
+  uint32_t w[2] = {0u, 0u};
+  if (kBf16) {
+    const float inv = s > 0.f ? 1.0f / s : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2)
+      w[i >> 3] |= pair_code(snap17(x[i] * inv), snap17(x[i + 1] * inv)) << (4 * (i & 7));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float m = fabsf(x[i]);
+      uint32_t c = __float_as_uint(x[i]) >> 31 << 3;
+      if (s > 0.f)
+        c += (m > 0.25f * s) + (m >= 0.75f * s) + (m > 1.25f * s) + (m >= 1.75f * s) + (m > 2.5f * s) +
+             (m >= 3.5f * s) + (m > 5.0f * s);
+      w[i >> 3] |= c << (4 * (i & 7));
+    }
+  }
+  codes = make_uint2(w[0], w[1]);
+  return sb;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreadsQ) kv4_append_kernel(const Kv4AppendDev a) {
+  constexpr int LPR = D / 16;                 // lanes of a row
+  constexpr int RB = kThreadsQ / LPR;         // rows of a block
+  constexpr bool kBf16 = sizeof(T) == 2;
+  const int64_t per = (a.n + RB - 1) / RB > 0 ? (a.n + RB - 1) / RB : 1;   // blocks of a head
+  const int h = (int)(blockIdx.x / per);
+  const int64_t t = (int64_t)(blockIdx.x % per) * RB + threadIdx.x / LPR;
+  const int li = threadIdx.x % LPR;
+  const int64_t at = a.at ? a.at[h] : 0;
+  const bool sane = at >= 0 && at <= a.cap;
+  if (blockIdx.x % per == 0 && threadIdx.x == 0) {
+    if (!sane || at + a.n > a.cap) flag_status(a.status, FASTAR_DEV_BAD_LEN);
+    if (a.len_out) {
+      const int64_t end = sane ? at + a.n : at < 0 ? 0 : a.cap;
+      a.len_out[h] = (int32_t)(end < a.cap ? end : a.cap);
+    }
+  }
+  if (t >= a.n || !sane || at + t >= a.cap) return;
+  float k[16], v[16];
+  load16(static_cast<const T*>(a.k) + h * a.k_hs + t * a.k_ts + li * 16, k);
+  load16(static_cast<const T*>(a.v) + h * a.v_hs + t * a.v_ts + li * 16, v);
+  const int64_t row = (int64_t)h * a.cap + at + t;
+  bool bad = false;
+  uint2 c;
+  uint32_t sb = quantise16<kBf16>(k, kv4::pow2i(-kv4::head_exp(a.k_exp, h)), c, bad);
+  reinterpret_cast<uint2*>(a.kc)[row * LPR + li] = c;
+  a.ks[row * LPR + li] = (uint8_t)sb;
+  sb = quantise16<kBf16>(v, kv4::pow2i(-kv4::head_exp(a.v_exp, h)), c, bad);
+  reinterpret_cast<uint2*>(a.vc)[row * LPR + li] = c;
+  a.vs[row * LPR + li] = (uint8_t)sb;
+  if (bad) flag_status(a.status, FASTAR_DEV_NONFINITE);
+}
+
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float* f) {
+  uint4 u[2];
+  uint32_t* w = reinterpret_cast<uint32_t*>(u);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+    w[e] = *reinterpret_cast<uint32_t*>(&h);
+  }
+  reinterpret_cast<uint4*>(p)[0] = u[0];
+  reinterpret_cast<uint4*>(p)[1] = u[1];
+}
+__device__ __forceinline__ void store16(float* p, const float* f) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    reinterpret_cast<float4*>(p)[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreadsQ)
+    kv4_read_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, const int32_t* exps,
+                    int64_t cap, int64_t first, int64_t n, T* __restrict__ out, int64_t hs, int64_t ts) {
+  constexpr int LPR = D / 16;
+  constexpr int RB = kThreadsQ / LPR;
+  const int64_t per = (n + RB - 1) / RB;
+  const int h = (int)(blockIdx.x / per);
+  const int64_t t = (int64_t)(blockIdx.x % per) * RB + threadIdx.x / LPR;
+  const int li = threadIdx.x % LPR;
+  if (t >= n) return;
+  const int64_t row = (int64_t)h * cap + first + t;
+  const uint2 c = reinterpret_cast<const uint2*>(codes)[row * LPR + li];
+  const uint32_t s2 = kv4::scale_f16x2(scales[row * LPR + li]);
+  const float up = kv4::pow2i(kv4::head_exp(exps, h));
+  uint32_t p[8];
+  kv4::unpack8(c.x, s2, p);
+  kv4::unpack8(c.y, s2, p + 4);
+  float f[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = kv4::f16x2_to_f32(p[i]);
+    f[2 * i] = x.x * up;
+    f[2 * i + 1] = x.y * up;
+  }
+  store16(out + h * hs + t * ts + li * 16, f);
+}
+
+template <typename T, int D>
+cudaError_t append_go(const Kv4AppendDev& a, cudaStream_t s) {
+  constexpr int RB = kThreadsQ / (D / 16);
+  const int64_t per = a.n > 0 ? (a.n + RB - 1) / RB : 1;
+  if (per * a.H > INT_MAX) return cudaErrorInvalidConfiguration;
+  kv4_append_kernel<T, D><<<(unsigned)(per * a.H), kThreadsQ, 0, s>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t read_go(int H, const uint8_t* codes, const uint8_t* scales, const int32_t* exps, int64_t cap, int64_t first,
+                    int64_t n, void* out, int64_t hs, int64_t ts, cudaStream_t s) {
+  constexpr int RB = kThreadsQ / (D / 16);
+  const int64_t blocks = (n + RB - 1) / RB * H;
+  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  kv4_read_kernel<T, D><<<(unsigned)blocks, kThreadsQ, 0, s>>>(codes, scales, exps, cap, first, n,
+                                                               static_cast<T*>(out), hs, ts);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_append(int dtype, int d, int H, int64_t n, TokView k, TokView v, const int32_t* k_exp,
+                              const int32_t* v_exp, const int32_t* at, uint8_t* kc, uint8_t* ks, uint8_t* vc,
+                              uint8_t* vs, int64_t cap, int32_t* len_out, int32_t* status, cudaStream_t s) {
+  Kv4AppendDev a{H, n, cap, k.p, v.p, k.hs, k.ts, v.hs, v.ts, k_exp, v_exp, at, kc, ks, vc, vs, len_out, status};
+  if (dtype == FASTAR_BF16) return d == 128 ? append_go<__nv_bfloat16, 128>(a, s) : append_go<__nv_bfloat16, 64>(a, s);
+  return d == 128 ? append_go<float, 128>(a, s) : append_go<float, 64>(a, s);
+}
+
+cudaError_t launch_kv4_read(int dtype, int d, int H, const uint8_t* codes, const uint8_t* scales, const int32_t* exps,
+                            int64_t cap, int64_t first, int64_t n, void* out, int64_t hs, int64_t ts, cudaStream_t s) {
+  if (dtype == FASTAR_BF16)
+    return d == 128 ? read_go<__nv_bfloat16, 128>(H, codes, scales, exps, cap, first, n, out, hs, ts, s)
+                    : read_go<__nv_bfloat16, 64>(H, codes, scales, exps, cap, first, n, out, hs, ts, s);
+  return d == 128 ? read_go<float, 128>(H, codes, scales, exps, cap, first, n, out, hs, ts, s)
+                  : read_go<float, 64>(H, codes, scales, exps, cap, first, n, out, hs, ts, s);
+}
+
+}  // namespace fastar

@@ -1,0 +1,76 @@
+// The 4-bit form of a cache row, shared by the kernels that write and read it: 16
+// consecutive channels share a scale s (e4m3, one byte); a value is a 4-bit e2m1 number
+// (0 0.5 1 1.5 2 3 4 6 and a sign) times s, times 2^e with a per-head exponent e.  Two
+// channels to a byte, the even one in the low nibble.
+//
+// e2m1 has 2 significant bits and e4m3 4, so a product code * s has at most 6 and lies in
+// [2^-10, 2688]: it is exact in fp16, in bf16 and in fp32.  The matrix products therefore
+// work on fp16 rows that ARE the cache's values; nothing is rounded by unpacking them.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace fastar {
+namespace kv4 {
+
+// The scale byte (e4m3) in both halves of an fp16 pair.
+__device__ __forceinline__ uint32_t scale_f16x2(uint32_t byte) {
+  uint32_t r;
+  const uint16_t b = (uint16_t)((byte & 0xffu) | ((byte & 0xffu) << 8));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Eight codes (channels 0..7 from the low nibble up) times the scale: four fp16 pairs.
+__device__ __forceinline__ void unpack8(uint32_t codes, uint32_t s2, uint32_t* out) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
+      : "r"(codes));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = mul_f16x2(out[i], s2);
+}
+
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// A head's exponent, held to the range in which every product stays a normal fp32.
+__device__ __forceinline__ int head_exp(const int32_t* e, int h) {
+  return e ? max(-64, min(64, e[h])) : 0;
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// A head's length, held to [0, cap].
+__device__ __forceinline__ int64_t head_len(const int32_t* len, int h, int64_t cap, int32_t* status) {
+  const int64_t n = len[h];
+  if (n < 0 || n > cap) {
+    flag_status(status, FASTAR_DEV_BAD_LEN);
+    return n < 0 ? 0 : cap;
+  }
+  return n;
+}
+
+// How many of a head's `len` rows token t of a call's nq sees: all of them, or with blocks
+// of `block` tokens those up to the end of the token's own block, where the nq tokens are
+// the cache's last nq rows.  May be 0 (a cache shorter than the call).
+__device__ __forceinline__ int64_t visible(int64_t len, int64_t nq, int64_t t, int64_t block) {
+  if (block <= 0) return len;
+  int64_t end = (t / block + 1) * block;
+  end = end < nq ? end : nq;
+  const int64_t v = len - nq + end;
+  return v < 0 ? 0 : v;
+}
+
+}  // namespace kv4
+}  // namespace fastar

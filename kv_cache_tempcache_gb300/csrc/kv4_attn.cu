@@ -1,0 +1,256 @@
+// Softmax attention over the 4-bit cache: the plan (which kernel, how many splits of the
+// keys), the fp32 kernel, and the kernel that joins the splits.
+//
+// The G = Hq / Hkv query heads that share a KV head see the same keys, so the rows of a KV
+// head's work are all (head, token) pairs, r = g * nq + t: the cache is read once for the
+// G heads.  With few rows the keys are cut into S splits, one block each, whose partial
+// (sum of p v, maximum, sum of p) go to the workspace in fp32 and are joined by a second
+// launch.
+#include <climits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "kv4.cuh"
+#include "tmap.h"
+
+namespace fastar {
+
+namespace {
+
+// ---- the fp32 kernel -----------------------------------------------------------------------
+// Kept for fp32 queries (bf16 goes to the tensor cores): one block takes 8 rows of a KV head
+// and a range of keys, unpacks 64 keys at a time to fp32 in shared memory and forms the 8 x 64
+// logits, their softmax and 8 x d outputs with fp32 arithmetic throughout.  Bound: the fp32
+// units (2 flops a row, key and channel twice over), and below them latency.
+constexpr int kRows = 8, kKeys = 64, kThreadsF = 128;
+
+template <int D>
+struct FSmem {
+  float k[kKeys][D + 4];
+  float v[kKeys][D];
+  float q[kRows][D];
+  float p[kRows][kKeys];
+  float alpha[kRows], l[kRows], m[kRows];
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreadsF) kv4_attn_f32_kernel(const Kv4AttnArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  FSmem<D>& sm = *reinterpret_cast<FSmem<D>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.Hq / a.Hkv;
+  const int64_t rows = (int64_t)G * a.nq;
+  const int64_t groups = (rows + kRows - 1) / kRows;
+  int64_t u = blockIdx.x;
+  const int split = (int)(u % a.splits);
+  u /= a.splits;
+  const int64_t r0 = u % groups * kRows;
+  const int h = (int)(u / groups);
+  const int64_t len = kv4::head_len(a.len, h, a.cap, a.status);
+  // the keys that any of the rows sees, cut evenly into whole tiles
+  int64_t most = 0;
+  for (int i = 0; i < kRows; ++i)
+    if (r0 + i < rows) {
+      const int64_t v = kv4::visible(len, a.nq, (r0 + i) % a.nq, a.block);
+      most = v > most ? v : most;
+    }
+  const int64_t tiles = (most + kKeys - 1) / kKeys;
+  const int64_t j0 = tiles * split / a.splits * kKeys;
+  const int64_t j1 = tiles * (split + 1) / a.splits * kKeys < most ? tiles * (split + 1) / a.splits * kKeys : most;
+  const float sl = a.scale * kv4::pow2i(kv4::head_exp(a.k_exp, h));
+
+  for (int i = tid; i < kRows * D; i += kThreadsF) {
+    const int64_t r = r0 + i / D;
+    const int64_t g = r / a.nq;
+    sm.q[i / D][i % D] =
+        r < rows ? to_f(static_cast<const T*>(a.q.p)[(h * G + g) * a.q.hs + (r - g * a.nq) * a.q.ts + i % D]) : 0.f;
+  }
+  if (tid < kRows) {
+    sm.m[tid] = neg_inf();
+    sm.l[tid] = 0.f;
+  }
+  constexpr int CPT = kRows * D / kThreadsF;     // outputs of a thread: one channel, CPT rows
+  const int oc = tid % D, or0 = tid / D * CPT;
+  float o[CPT];
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) o[i] = 0.f;
+
+  for (int64_t j = j0; j < j1; j += kKeys) {
+    __syncthreads();
+    const int nk = (int)(j1 - j < kKeys ? j1 - j : kKeys);
+    for (int i = tid; i < kKeys * (D / 8); i += kThreadsF) {
+      const int row = i / (D / 8), c = i % (D / 8);
+      uint32_t pk[4] = {0, 0, 0, 0}, pv[4] = {0, 0, 0, 0};   // rows past the range count as 0
+      if (row < nk) {
+        const int64_t at = (int64_t)h * a.cap + j + row;
+        kv4::unpack8(reinterpret_cast<const uint32_t*>(a.kc)[at * (D / 8) + c],
+                     kv4::scale_f16x2(a.ks[at * (D / 16) + c / 2]), pk);
+        kv4::unpack8(reinterpret_cast<const uint32_t*>(a.vc)[at * (D / 8) + c],
+                     kv4::scale_f16x2(a.vs[at * (D / 16) + c / 2]), pv);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = kv4::f16x2_to_f32(pk[e]), y = kv4::f16x2_to_f32(pv[e]);
+        *reinterpret_cast<float2*>(&sm.k[row][c * 8 + 2 * e]) = x;
+        *reinterpret_cast<float2*>(&sm.v[row][c * 8 + 2 * e]) = y;
+      }
+    }
+    __syncthreads();
+    // warp w: rows 2w and 2w + 1; lane: keys lane and lane + 32
+#pragma unroll
+    for (int rr = 0; rr < 2; ++rr) {
+      const int row = warp * 2 + rr;
+      const int64_t r = r0 + row;
+      const int64_t see = r < rows ? kv4::visible(len, a.nq, r % a.nq, a.block) - j : 0;
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll 8
+      for (int c = 0; c < D; c += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(&sm.q[row][c]);
+        const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[lane][c]);
+        const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[lane + 32][c]);
+        s0 = fmaf(x.x, k0.x, fmaf(x.y, k0.y, fmaf(x.z, k0.z, fmaf(x.w, k0.w, s0))));
+        s1 = fmaf(x.x, k1.x, fmaf(x.y, k1.y, fmaf(x.z, k1.z, fmaf(x.w, k1.w, s1))));
+      }
+      const int64_t lim = see < nk ? see : nk;
+      s0 = lane < lim ? s0 * sl : neg_inf();
+      s1 = lane + 32 < lim ? s1 * sl : neg_inf();
+      float mx = fmaxf(s0, s1);
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+      const float mo = sm.m[row], mn = fmaxf(mo, mx);
+      const float ref = mn == neg_inf() ? 0.f : mn;
+      const float p0 = expf(s0 - ref), p1 = expf(s1 - ref);
+      const float al = expf(mo - ref);
+      const float sum = warp_sum(p0 + p1);
+      sm.p[row][lane] = p0;
+      sm.p[row][lane + 32] = p1;
+      __syncwarp();
+      if (lane == 0) {
+        sm.alpha[row] = al;
+        sm.l[row] = sm.l[row] * al + sum;
+        sm.m[row] = mn;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) o[i] *= sm.alpha[or0 + i];
+#pragma unroll 4
+    for (int key = 0; key < kKeys; ++key) {
+      const float v = sm.v[key][oc];
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) o[i] = fmaf(sm.p[or0 + i][key], v, o[i]);
+    }
+  }
+  __syncthreads();
+  const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int64_t r = r0 + or0 + i;
+    if (r >= rows) continue;
+    const int64_t g = r / a.nq, t = r - g * a.nq, head = h * G + g;
+    const float l = sm.l[or0 + i], m = sm.m[or0 + i];
+    if (a.splits > 1) {
+      const int64_t at = (split * (int64_t)a.Hq + head) * a.nq + t;
+      a.part_o[at * D + oc] = o[i] * up;
+      if (oc == 0) a.part_ml[at] = make_float2(m, l);
+    } else {
+      static_cast<T*>(a.out)[head * a.o_hs + t * a.o_ts + oc] = from_f<T>(l > 0.f || l != l ? o[i] * up / l : 0.f);
+      if (oc == 0 && a.lse) a.lse[head * a.nq + t] = l > 0.f || l != l ? m + logf(l) : neg_inf();
+    }
+  }
+}
+
+// ---- joining the splits ----------------------------------------------------------------------
+// O = sum_s e^(m_s - m) o_s / sum_s e^(m_s - m) l_s over a row's S partials, m = max_s m_s; one
+// warp a row, D / 32 channels a lane.  The partials are summed in the order of the splits, so
+// results do not change from run to run.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnArgs a) {
+  constexpr int CPL = D / 32;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = (int64_t)a.Hq * a.nq;
+  pdl_wait();
+  if (row >= rows) return;
+  float m = neg_inf();
+  for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, a.part_ml[s * rows + row].x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  const float ref = m == neg_inf() ? 0.f : m;
+  float l = 0.f, o[CPL];
+#pragma unroll
+  for (int i = 0; i < CPL; ++i) o[i] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 ml = a.part_ml[s * rows + row];
+    const float w = expf(ml.x - ref);
+    l = fmaf(w, ml.y, l);
+    const float* p = a.part_o + (s * rows + row) * D + lane * CPL;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) o[i] = fmaf(w, p[i], o[i]);
+  }
+  const bool live = l > 0.f || l != l;
+  const int64_t head = row / a.nq, t = row - head * a.nq;
+  T* out = static_cast<T*>(a.out) + head * a.o_hs + t * a.o_ts + lane * CPL;
+#pragma unroll
+  for (int i = 0; i < CPL; ++i) out[i] = from_f<T>(live ? o[i] / l : 0.f);
+  if (lane == 0 && a.lse) a.lse[row] = live ? m + logf(l) : neg_inf();
+}
+
+template <typename T, int D>
+cudaError_t join_go(const Kv4AttnArgs& a, cudaStream_t s) {
+  const int64_t rows = (int64_t)a.Hq * a.nq;
+  const cudaError_t e = launch_dependent(kv4_join_kernel<T, D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t f32_go(const Kv4AttnArgs& a, cudaStream_t s) {
+  const int64_t rows = (int64_t)(a.Hq / a.Hkv) * a.nq;
+  const int64_t blocks = (rows + kRows - 1) / kRows * a.Hkv * a.splits;
+  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = opt_in_smem((const void*)kv4_attn_f32_kernel<T, D>, (int)sizeof(FSmem<D>));
+  if (e != cudaSuccess) return e;
+  kv4_attn_f32_kernel<T, D><<<(unsigned)blocks, kThreadsF, sizeof(FSmem<D>), s>>>(a);
+  count_launches(1);
+  const cudaError_t r = cudaGetLastError();
+  return r != cudaSuccess || a.splits == 1 ? r : join_go<T, D>(a, s);
+}
+
+// Splits of the keys: enough blocks for two a multiprocessor, but no split under 256 keys.
+int splits_for(int64_t blocks, int64_t cap) {
+  const int64_t want = (2 * (int64_t)sm_count() + blocks - 1) / blocks;
+  const int64_t most = cap / 256;
+  int64_t s = want < most ? want : most;
+  if (s > kKv4MaxSplits) s = kKv4MaxSplits;
+  return s < 1 ? 1 : (int)s;
+}
+
+}  // namespace
+
+int kv4_attn_splits(int dtype, int d, int Hq, int Hkv, int64_t nq, int64_t cap) {
+  const int64_t rows = (int64_t)(Hq / Hkv) * nq;
+  return splits_for((rows + kRows - 1) / kRows * Hkv, cap);
+}
+
+size_t kv4_attn_workspace(int d, int Hq, int Hkv, int64_t nq, int64_t cap) {
+  int s = 1;
+  for (int dt : {FASTAR_F32, FASTAR_BF16}) {
+    const int x = kv4_attn_splits(dt, d, Hq, Hkv, nq, cap);
+    s = x > s ? x : s;
+  }
+  return s == 1 ? 0 : (size_t)s * Hq * nq * (d + 2) * sizeof(float);
+}
+
+cudaError_t launch_kv4_attn(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStream_t s) {
+  a.splits = ws ? kv4_attn_splits(dtype, d, a.Hq, a.Hkv, a.nq, a.cap) : 1;
+  if (a.splits > 1) {
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * a.Hq * a.nq * d);
+  }
+  if (dtype == FASTAR_BF16) return d == 128 ? f32_go<__nv_bfloat16, 128>(a, s) : f32_go<__nv_bfloat16, 64>(a, s);
+  return d == 128 ? f32_go<float, 128>(a, s) : f32_go<float, 64>(a, s);
+}
+
+}  // namespace fastar
