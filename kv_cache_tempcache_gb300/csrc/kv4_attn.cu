@@ -18,7 +18,7 @@ namespace fastar {
 namespace {
 
 // ---- the fp32 kernel -----------------------------------------------------------------------
-// Kept for fp32 queries (bf16 goes to the tensor cores): one block takes 8 rows of a KV head
+// For fp32 queries (bf16 ones go to the tensor cores, kv4_attn_tc.cu): one block takes 8 rows of a KV head
 // and a range of keys, unpacks 64 keys at a time to fp32 in shared memory and forms the 8 x 64
 // logits, their softmax and 8 x d outputs with fp32 arithmetic throughout.  Bound: the fp32
 // units (2 flops a row, key and channel twice over), and below them latency.
@@ -33,7 +33,7 @@ struct FSmem {
   float alpha[kRows], l[kRows], m[kRows];
 };
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreadsF) kv4_attn_f32_kernel(const Kv4AttnArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   FSmem<D>& sm = *reinterpret_cast<FSmem<D>*>(smem_raw);
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreadsF) kv4_attn_f32_kernel(const Kv4AttnAr
     const int64_t r = r0 + i / D;
     const int64_t g = r / a.nq;
     sm.q[i / D][i % D] =
-        r < rows ? to_f(static_cast<const T*>(a.q.p)[(h * G + g) * a.q.hs + (r - g * a.nq) * a.q.ts + i % D]) : 0.f;
+        r < rows ? static_cast<const float*>(a.q.p)[(h * G + g) * a.q.hs + (r - g * a.nq) * a.q.ts + i % D] : 0.f;
   }
   if (tid < kRows) {
     sm.m[tid] = neg_inf();
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreadsF) kv4_attn_f32_kernel(const Kv4AttnAr
       a.part_o[at * D + oc] = o[i] * up;
       if (oc == 0) a.part_ml[at] = make_float2(m, l);
     } else {
-      static_cast<T*>(a.out)[head * a.o_hs + t * a.o_ts + oc] = from_f<T>(l > 0.f || l != l ? o[i] * up / l : 0.f);
+      static_cast<float*>(a.out)[head * a.o_hs + t * a.o_ts + oc] = l > 0.f || l != l ? o[i] * up / l : 0.f;
       if (oc == 0 && a.lse) a.lse[head * a.nq + t] = l > 0.f || l != l ? m + logf(l) : neg_inf();
     }
   }
@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnArgs a) {
 #pragma unroll 4
   for (int s = 0; s < a.splits; ++s) {
     const float2 ml = a.part_ml[s * rows + row];
+    if (ml.y == 0.f) continue;          // a split in which the row sees no key: o is not written
     const float w = expf(ml.x - ref);
     l = fmaf(w, ml.y, l);
     const float* p = a.part_o + (s * rows + row) * D + lane * CPL;
@@ -205,21 +206,21 @@ cudaError_t join_go(const Kv4AttnArgs& a, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t f32_go(const Kv4AttnArgs& a, cudaStream_t s) {
   const int64_t rows = (int64_t)(a.Hq / a.Hkv) * a.nq;
   const int64_t blocks = (rows + kRows - 1) / kRows * a.Hkv * a.splits;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = opt_in_smem((const void*)kv4_attn_f32_kernel<T, D>, (int)sizeof(FSmem<D>));
+  const cudaError_t e = opt_in_smem((const void*)kv4_attn_f32_kernel<D>, (int)sizeof(FSmem<D>));
   if (e != cudaSuccess) return e;
-  kv4_attn_f32_kernel<T, D><<<(unsigned)blocks, kThreadsF, sizeof(FSmem<D>), s>>>(a);
+  kv4_attn_f32_kernel<D><<<(unsigned)blocks, kThreadsF, sizeof(FSmem<D>), s>>>(a);
   count_launches(1);
   const cudaError_t r = cudaGetLastError();
-  return r != cudaSuccess || a.splits == 1 ? r : join_go<T, D>(a, s);
+  return r != cudaSuccess || a.splits == 1 ? r : join_go<float, D>(a, s);
 }
 
-// Splits of the keys: enough blocks for two a multiprocessor, but no split under 256 keys.
-int splits_for(int64_t blocks, int64_t cap) {
+// Splits of the keys for the fp32 kernel: two blocks a multiprocessor, none under 256 keys.
+int splits_f32(int64_t blocks, int64_t cap) {
   const int64_t want = (2 * (int64_t)sm_count() + blocks - 1) / blocks;
   const int64_t most = cap / 256;
   int64_t s = want < most ? want : most;
@@ -227,11 +228,33 @@ int splits_for(int64_t blocks, int64_t cap) {
   return s < 1 ? 1 : (int)s;
 }
 
+// Splits for the tensor-core kernel, by a model of its time over a full cache: waves of CTAs,
+// each a fixed part and so much a key tile, plus the partials' way through memory and the
+// join.  It takes the fewest splits that are within 2 % of the best.
+int splits_tc(int d, int64_t rows, int Hkv, int64_t cap) {
+  const int64_t sms = sm_count(), items = (rows + 255) / 256 * Hkv, tiles = (cap + 127) / 128;
+  const double tile = (rows > 128 ? 1.2 : 0.75) * (d == 128 ? 1.0 : 0.7), fixed = 6.0;
+  auto cost = [&](int64_t s) {
+    const double waves = (double)((items * s + sms - 1) / sms);
+    const double join = s > 1 ? 4.0 + 2e-6 * s * rows * Hkv * (d + 2) * 4 / 4.0 : 0.0;
+    return waves * (fixed + (double)((tiles + s - 1) / s) * tile) + join;
+  };
+  int64_t most = (4 * sms + items - 1) / items;
+  if (most > tiles) most = tiles;
+  if (most > kKv4MaxSplits) most = kKv4MaxSplits;
+  double best = cost(1);
+  int64_t pick = 1;
+  for (int64_t s = 2; s <= most; ++s)
+    if (cost(s) < 0.98 * best) best = cost(s), pick = s;
+  return (int)pick;
+}
+
 }  // namespace
 
 int kv4_attn_splits(int dtype, int d, int Hq, int Hkv, int64_t nq, int64_t cap) {
   const int64_t rows = (int64_t)(Hq / Hkv) * nq;
-  return splits_for((rows + kRows - 1) / kRows * Hkv, cap);
+  if (dtype == FASTAR_BF16) return splits_tc(d, rows, Hkv, cap);
+  return splits_f32((rows + kRows - 1) / kRows * Hkv, cap);
 }
 
 size_t kv4_attn_workspace(int d, int Hq, int Hkv, int64_t nq, int64_t cap) {
@@ -249,8 +272,10 @@ cudaError_t launch_kv4_attn(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStrea
     a.part_o = static_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * a.Hq * a.nq * d);
   }
-  if (dtype == FASTAR_BF16) return d == 128 ? f32_go<__nv_bfloat16, 128>(a, s) : f32_go<__nv_bfloat16, 64>(a, s);
-  return d == 128 ? f32_go<float, 128>(a, s) : f32_go<float, 64>(a, s);
+  if (dtype == FASTAR_F32) return d == 128 ? f32_go<128>(a, s) : f32_go<64>(a, s);
+  const cudaError_t e = launch_kv4_attn_tc(d, a, s);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  return d == 128 ? join_go<__nv_bfloat16, 128>(a, s) : join_go<__nv_bfloat16, 64>(a, s);
 }
 
 }  // namespace fastar

@@ -1,0 +1,539 @@
+// Softmax attention over the 4-bit cache on the 5th-generation tensor cores (bf16 queries).
+//
+// One CTA takes 256 rows ((query head, token) pairs of a KV head) as two tiles of 128 and a
+// range of keys, 128 at a time:
+//   warps 0-3 / 4-7    softmax of row tile 0 / 1, one row per thread: logits from TMEM, the
+//                      running maximum (the sums are rescaled only when it grows by more than
+//                      2^8), P as fp16 over the consumed logits in TMEM, and the output at the end;
+//   warps 8-11 / 12-15 unpack K / V: codes and scales from global memory into registers a tile
+//                      ahead, fp16 rows into a two-stage ring of 128-byte-swizzled tiles;
+//   warp 16            owns TMEM and issues tcgen05.mma from one thread: S = Q K^T of both row
+//                      tiles, O += P V (P from TMEM).
+// The order of issue is PV0(j) QK0(j+1) PV1(j) QK1(j+1): while the softmax of one row tile
+// runs, the tensor cores work for the other, so a logit buffer a tile is enough and two
+// accumulators of 128 columns fit TMEM beside them.
+//
+// Numbers: a cache value (code times scale) is exact in fp16 (kv4.cuh).  A query row is scaled
+// by a power of two that puts its largest element in [2^12, 2^13) and rounded to fp16: bf16's 8
+// bits fit fp16's 11, so only elements 2^-26 of the row's largest and below are not exact (and
+// off by at most 2^-37 of it); the power returns in the row's logit scale.  P in fp16 has an
+// error of 2^-11, an eighth of bf16's.  Logits, maxima, sums and outputs are fp32.
+//
+// Keys past a row's last visible one get P = 0; rows past the CTA's last key are stored as
+// zeros in shared memory, so what lies behind the cache's length cannot reach a sum as 0 * NaN.
+// Every wait is bounded; a timeout sets FASTAR_DEV_TIMEOUT and unwinds.
+#include <climits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "kv4.cuh"
+#include "tc.cuh"
+#include "tmap.h"
+
+namespace fastar {
+
+namespace {
+
+constexpr int kRT = 128;               // rows of a row tile
+constexpr int kKT = 128;               // keys of a tile
+constexpr int kStages = 2;
+constexpr int kSoftWarps = 8, kUnpackWarps = 8;
+constexpr int kMmaWarp = kSoftWarps + kUnpackWarps;
+constexpr int kThreadsT = (kMmaWarp + 1) * 32;
+constexpr int kBlk = 128 * 128;        // 128 rows x 64 fp16 (128-byte swizzle)
+
+struct alignas(16) Kv4Ctl {
+  uint64_t q_full[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t s_full[2], p_full[2], pv_done[2], fin;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D>
+struct Kv4Layout {
+  static constexpr int KH = D / 64;
+  static constexpr size_t tile = (size_t)KH * kBlk;
+  static constexpr size_t q = 0;
+  static constexpr size_t k = q + 2 * tile;
+  static constexpr size_t v = k + kStages * tile;
+  static constexpr size_t ctl = v + kStages * tile;
+  static constexpr size_t bytes = ctl + sizeof(Kv4Ctl) + 1024;
+  static constexpr uint32_t s_col = 0, o_col = 256;   // two 128-column buffers each
+};
+
+// fp16 operands, fp32 sums; bit 16: B is MN-major.
+constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort));
+}
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Largest of 32 logits; kFull = false: of the first `valid`.
+template <bool kFull>
+__device__ __forceinline__ float max_of32(const float* x, int valid) {
+  float m = neg_inf();
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float a = kFull || i < valid ? x[i] : neg_inf(), b = kFull || i + 1 < valid ? x[i + 1] : neg_inf();
+    m = max3f(m, a, b);
+  }
+  return m;
+}
+
+template <bool kFull>
+__device__ __forceinline__ float row_max(uint32_t s, int valid) {
+  float m = neg_inf();
+#pragma unroll
+  for (int c = 0; c < kKT; c += 64) {
+    float x[64];
+    tc::tmem_ld32(s + (uint32_t)c, x);
+    tc::tmem_ld32(s + (uint32_t)(c + 32), x + 32);
+    tc::tmem_wait_ld();
+    tc::tmem_pin32(x);
+    tc::tmem_pin32(x + 32);
+    m = max3f(m, max_of32<kFull>(x, valid - c), max_of32<kFull>(x + 32, valid - c - 32));
+  }
+  return m;
+}
+
+// P = 2^(s sl2 - m) as fp16 pairs over the logits' own columns (chunk c of 32 logits becomes
+// columns 16 c .. 16 c + 15, which are read by then); returns the row's sum of P.
+template <bool kFull>
+__device__ __forceinline__ float row_exp(uint32_t s, int valid, float sl2, float m) {
+  const float nm = m == neg_inf() ? 0.f : -m;
+  float xa[32], xb[32];
+  float s0 = 0.f, s1 = 0.f;
+  tc::tmem_ld32(s, xa);
+  tc::tmem_wait_ld();
+  tc::tmem_pin32(xa);
+#pragma unroll
+  for (int c = 0; c < kKT / 32; ++c) {
+    float* cur = (c & 1) ? xb : xa;
+    float* nxt = (c & 1) ? xa : xb;
+    if (c + 1 < kKT / 32) tc::tmem_ld32(s + (uint32_t)((c + 1) * 32), nxt);
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      float a0 = fmaf(cur[i], sl2, nm), a1 = fmaf(cur[i + 1], sl2, nm);
+      if (!kFull) {
+        a0 = c * 32 + i < valid ? a0 : neg_inf();
+        a1 = c * 32 + i + 1 < valid ? a1 : neg_inf();
+      }
+      const float p0 = ex2f(a0), p1 = ex2f(a1);
+      s0 += p0;
+      s1 += p1;
+      pk[i >> 1] = pack_f16(p0, p1);
+    }
+    tmem_st16(s + (uint32_t)(c * 16), pk);
+    if (c + 1 < kKT / 32) {
+      tc::tmem_wait_ld();
+      tc::tmem_pin32(nxt);
+    }
+  }
+  return s0 + s1;
+}
+
+// Row r of a KV head's work: its query head and token.
+struct RowOf {
+  int64_t head, t;
+};
+__device__ __forceinline__ RowOf row_of(const Kv4AttnArgs& a, int h, int64_t r) {
+  const int64_t g = r / a.nq;
+  return RowOf{h * (int64_t)(a.Hq / a.Hkv) + g, r - g * a.nq};
+}
+
+// A row that sees no key: zeros and lse = -inf (in a split: an empty partial).
+template <int D>
+__device__ __forceinline__ void store_empty(const Kv4AttnArgs& a, int split, RowOf w) {
+  if (a.splits > 1) {
+    a.part_ml[(split * (int64_t)a.Hq + w.head) * a.nq + w.t] = make_float2(neg_inf(), 0.f);
+    return;
+  }
+  uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + w.head * a.o_hs + w.t * a.o_ts);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) p[i] = make_uint4(0, 0, 0, 0);
+  if (a.lse) a.lse[w.head * a.nq + w.t] = neg_inf();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4AttnArgs a, int row_tiles) {
+  using Lay = Kv4Layout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  Kv4Ctl& sm = *reinterpret_cast<Kv4Ctl*>(base + Lay::ctl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // the work item: KV head, 256 rows, split of the keys.  The row tiles that see most keys
+  // (the last ones of a call in blocks) start first.
+  int64_t u = blockIdx.x;
+  const int split = (int)(u % a.splits);
+  u /= a.splits;
+  const int rt = row_tiles - 1 - (int)(u % row_tiles);
+  const int h = (int)(u / row_tiles);
+  const int64_t rows = (int64_t)(a.Hq / a.Hkv) * a.nq;
+  const int64_t r0 = (int64_t)rt * (2 * kRT);
+  const int64_t rlast = (r0 + 2 * kRT < rows ? r0 + 2 * kRT : rows) - 1;
+  const int nt = rlast - r0 >= kRT ? 2 : 1;             // row tiles with rows
+  const int64_t len = kv4::head_len(a.len, h, a.cap, a.status);
+  // the last key that any of the rows sees: rows of two heads include a last token
+  const int64_t most = r0 / a.nq != rlast / a.nq ? len : kv4::visible(len, a.nq, rlast % a.nq, a.block);
+  const int64_t tiles = (most + kKT - 1) / kKT;
+  const int64_t j0 = tiles * split / a.splits;
+  const int T = (int)(tiles * (split + 1) / a.splits - j0);
+  const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
+
+  if (T == 0) {                                          // no keys: uniform over the CTA
+    const int64_t r = r0 + threadIdx.x;
+    if (threadIdx.x < 2 * kRT && r < rows) store_empty<D>(a, split, row_of(a, h, r));
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.q_full[i], kRT);
+      tc::mbar_init(&sm.s_full[i], 1);
+      tc::mbar_init(&sm.p_full[i], 4);
+      tc::mbar_init(&sm.pv_done[i], 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(&sm.k_full[i], 128);
+      tc::mbar_init(&sm.k_empty[i], 1);
+      tc::mbar_init(&sm.v_full[i], 128);
+      tc::mbar_init(&sm.v_empty[i], 1);
+    }
+    tc::mbar_init(&sm.fin, 1);
+    sm.abort = 0;
+    tc::mbar_fence_init();
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(&sm.tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort = &sm.abort;
+
+  if (warp < kSoftWarps) {
+    // ---------------- softmax ----------------
+    const int w = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const int64_t r = r0 + w * kRT + row;
+    const bool has = r < rows;
+    const RowOf at = has ? row_of(a, h, r) : RowOf{0, 0};
+    float sl2 = 0.f;
+    if (w < nt) {
+      // this thread's query row: its largest magnitude, then fp16 at a power of two
+      uint4 x[D / 8];
+      uint32_t big = 0;
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + at.head * a.q.hs +
+                                                      at.t * a.q.ts);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) x[c] = has ? p[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          big = max(big, v[e] & 0x7fffu);
+          big = max(big, (v[e] >> 16) & 0x7fffu);
+        }
+      }
+      // exponent of the largest (subnormals count as 2^-126); a row that is zero or not finite
+      // stays as it is
+      const int ex = (int)(big >> 7);
+      int qe = ex == 0 ? -126 - 12 : ex - 127 - 12;
+      if (qe < -120) qe = -120;
+      if (big == 0 || ex == 255) qe = 0;
+      const float down = kv4::pow2i(-qe);
+      sl2 = a.scale * kv4::pow2i(qe) * kv4::pow2i(kv4::head_exp(a.k_exp, h)) * 1.4426950408889634f;
+      uint8_t* dst = base + Lay::q + (size_t)w * Lay::tile;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e] = pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * kBlk + tc::sw128_off(row, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      tc::fence_proxy_async();
+      tc::mbar_arrive(&sm.q_full[w]);
+
+      const int64_t see = (has ? kv4::visible(len, a.nq, at.t, a.block) : 0) - j0 * kKT;   // from the split's first key
+      const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t s_addr = lane_addr + Lay::s_col + (uint32_t)(w * 128);
+      const uint32_t o_addr = lane_addr + Lay::o_col + (uint32_t)(w * 128);
+      float m = neg_inf(), l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < T; ++j) {
+        if (!wait_warp(&sm.s_full[w], j & 1, abort)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        const int64_t left = see - (int64_t)j * kKT;
+        const int valid = left >= kKT ? kKT : left > 0 ? (int)left : 0;
+        const bool full = __all_sync(0xffffffffu, valid == kKT);
+        // the scale is positive: the largest scaled logit is the largest logit, scaled
+        const float mt = (full ? row_max<true>(s_addr, valid) : row_max<false>(s_addr, valid)) * sl2;
+        float alpha = 1.f;
+        bool resc = false;
+        if (mt > m + 8.f) {
+          resc = m != neg_inf();
+          alpha = resc ? ex2f(m - mt) : 0.f;
+          m = mt;
+        }
+        if (__any_sync(0xffffffffu, resc)) {
+          // O holds the products of the tiles before: they have to have landed
+          if (!wait_warp(&sm.pv_done[w], (j - 1) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const float f = resc ? alpha : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tc::tmem_ld32(o_addr + (uint32_t)c, o);
+            tc::tmem_wait_ld();
+            tc::tmem_pin32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= f;
+            tc::tmem_st32(o_addr + (uint32_t)c, o);
+          }
+          tc::tmem_wait_st();
+        }
+        const float sum = full ? row_exp<true>(s_addr, valid, sl2, m) : row_exp<false>(s_addr, valid, sl2, m);
+        l = l * alpha + sum;
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.p_full[w]);
+      }
+      if (ok && wait_warp(&sm.pv_done[w], (T - 1) & 1, abort)) {
+        tc::tc_fence_after();
+        // the TMEM loads are the warp's: rows past the last load too, and store nothing
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          __syncwarp();
+          tc::tmem_ld32(o_addr + (uint32_t)c, o);
+          tc::tmem_wait_ld();
+          tc::tmem_pin32(o);
+          if (!has) continue;
+          const bool live = l > 0.f || l != l;
+          if (a.splits > 1) {
+            const int64_t pa = (split * (int64_t)a.Hq + at.head) * a.nq + at.t;
+            float4* p4 = reinterpret_cast<float4*>(a.part_o + pa * D + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              p4[i] = make_float4(o[4 * i] * up, o[4 * i + 1] * up, o[4 * i + 2] * up, o[4 * i + 3] * up);
+          } else {
+            const float f = live ? up / l : 0.f;
+            uint4* p4 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at.head * a.o_hs +
+                                                 at.t * a.o_ts + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                __nv_bfloat162 h2 = __floats2bfloat162_rn(o[8 * i + 2 * e] * f, o[8 * i + 2 * e + 1] * f);
+                v[e] = live ? *reinterpret_cast<uint32_t*>(&h2) : 0u;
+              }
+              p4[i] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          }
+        }
+        if (has) {
+          const bool live = l > 0.f || l != l;
+          const float mn = m * 0.6931471805599453f;
+          if (a.splits > 1)
+            a.part_ml[(split * (int64_t)a.Hq + at.head) * a.nq + at.t] = make_float2(live ? mn : neg_inf(), l);
+          else if (a.lse)
+            a.lse[at.head * a.nq + at.t] = live ? mn + logf(l) : neg_inf();
+        }
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    // ---------------- unpack K (warps 8-11) or V (warps 12-15) ----------------
+    constexpr int PARTS = D / 32;                        // 16-byte runs of 32 codes in a row
+    const bool isk = warp < kSoftWarps + 4;
+    const int t = threadIdx.x & 127;
+    const uint8_t* codes = isk ? a.kc : a.vc;
+    const uint8_t* scales = isk ? a.ks : a.vs;
+    uint8_t* ring = base + (isk ? Lay::k : Lay::v);
+    uint64_t* full = isk ? sm.k_full : sm.v_full;
+    uint64_t* empty = isk ? sm.k_empty : sm.v_empty;
+    const int part = t % PARTS, row0 = t / PARTS;
+    const bool swap = part >= 2;     // parts 2 and 3 write their 16-byte chunks in another order,
+                                     // so that the 8 lanes of a store phase hit 8 different banks
+    uint4 c[PARTS];
+    uint32_t s[PARTS];
+    auto load = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < PARTS; ++i) {
+        const int64_t key = (j0 + j) * kKT + row0 + i * (128 / PARTS);
+        c[i] = make_uint4(0, 0, 0, 0);
+        s[i] = 0;
+        if (key < most) {
+          const int64_t rowi = (int64_t)h * a.cap + key;
+          c[i] = __ldg(reinterpret_cast<const uint4*>(codes + rowi * (D / 2)) + part);
+          s[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + rowi * (D / 16)) + part);
+        }
+      }
+    };
+    load(0);
+    for (int j = 0; j < T; ++j) {
+      const int st = j % kStages;
+      if (!tc::mbar_wait(&empty[st], ((j / kStages) & 1) ^ 1, abort)) break;
+      uint8_t* tile = ring + (size_t)st * Lay::tile;
+#pragma unroll
+      for (int i = 0; i < PARTS; ++i) {
+        const int row = row0 + i * (128 / PARTS);
+        uint32_t wv[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+        uint32_t s0 = kv4::scale_f16x2(s[i]), s1 = kv4::scale_f16x2(s[i] >> 8);
+        if (PARTS == 4 && swap) {
+          uint32_t x = wv[0];
+          wv[0] = wv[2], wv[2] = x;
+          x = wv[1];
+          wv[1] = wv[3], wv[3] = x;
+          x = s0;
+          s0 = s1, s1 = x;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t o[4];
+          kv4::unpack8(wv[e], e < 2 ? s0 : s1, o);
+          const int ch = part * 4 + (PARTS == 4 && swap ? e ^ 2 : e);
+          *reinterpret_cast<uint4*>(tile + (ch >> 3) * kBlk + tc::sw128_off(row, ch & 7)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      if (j + 1 < T) load(j + 1);
+      tc::fence_proxy_async();
+      tc::mbar_arrive(&full[st]);
+    }
+  } else if (lane == 0) {
+    // ---------------- MMA issue ----------------
+    constexpr uint32_t idesc_qk = idesc_f16(kRT, kKT, false), idesc_pv = idesc_f16(kRT, D, true);
+    const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(base + Lay::q));
+    const uint64_t k_desc = tc::sw128_desc(tc::smem_u32(base + Lay::k));
+    const uint64_t v_desc = tc::sw128_mn_desc(tc::smem_u32(base + Lay::v), kBlk);
+    auto qk = [&](int w, int j) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = (uint32_t)((k >> 2) * kBlk + (k & 3) * 32);
+        mma_ss(tmem + Lay::s_col + (uint32_t)(w * 128), q_desc + ((w * Lay::tile + off) >> 4),
+               k_desc + (((j % kStages) * Lay::tile + off) >> 4), idesc_qk, k > 0 ? 1u : 0u);
+      }
+      tc::mma_commit(&sm.s_full[w]);
+    };
+    auto pv = [&](int w, int j) {
+#pragma unroll
+      for (int k = 0; k < kKT / 16; ++k)
+        mma_ts(tmem + Lay::o_col + (uint32_t)(w * 128), tmem + Lay::s_col + (uint32_t)(w * 128 + k * 8),
+               v_desc + (((j % kStages) * Lay::tile + k * 2048) >> 4), idesc_pv, (j > 0 || k > 0) ? 1u : 0u);
+      tc::mma_commit(&sm.pv_done[w]);
+    };
+    bool ok = true;
+    for (int w = 0; w < nt && ok; ++w) {
+      ok = tc::mbar_wait(&sm.q_full[w], 0, abort) && tc::mbar_wait(&sm.k_full[0], 0, abort);
+      if (!ok) break;
+      tc::tc_fence_after();
+      qk(w, 0);
+    }
+    if (ok) tc::mma_commit(&sm.k_empty[0]);
+    for (int j = 0; j < T && ok; ++j) {
+      const int st = j % kStages, nst = (j + 1) % kStages;
+      for (int w = 0; w < nt; ++w) {
+        ok = tc::mbar_wait(&sm.p_full[w], j & 1, abort) && tc::mbar_wait(&sm.v_full[st], (j / kStages) & 1, abort);
+        if (!ok) break;
+        tc::tc_fence_after();
+        pv(w, j);
+        if (w == nt - 1) tc::mma_commit(&sm.v_empty[st]);
+        if (j + 1 < T) {
+          ok = tc::mbar_wait(&sm.k_full[nst], ((j + 1) / kStages) & 1, abort);
+          if (!ok) break;
+          tc::tc_fence_after();
+          qk(w, j + 1);
+        }
+      }
+      if (!ok) break;
+      if (j + 1 < T) tc::mma_commit(&sm.k_empty[nst]);
+    }
+    // every issued product ends before TMEM is given back
+    tc::mma_commit(&sm.fin);
+    volatile int never = 0;
+    tc::mbar_wait(&sm.fin, 0, &never, 400000000LL);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && sm.abort) flag_status(a.status, FASTAR_DEV_TIMEOUT);
+}
+
+template <int D>
+cudaError_t tc_go(const Kv4AttnArgs& a, cudaStream_t s) {
+  const int64_t rows = (int64_t)(a.Hq / a.Hkv) * a.nq;
+  const int64_t rt = (rows + 2 * kRT - 1) / (2 * kRT);
+  const int64_t blocks = rt * a.Hkv * a.splits;
+  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = opt_in_smem((const void*)kv4_attn_tc_kernel<D>, (int)Kv4Layout<D>::bytes);
+  if (e != cudaSuccess) return e;
+  kv4_attn_tc_kernel<D><<<(unsigned)blocks, kThreadsT, Kv4Layout<D>::bytes, s>>>(a, (int)rt);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_attn_tc(int d, const Kv4AttnArgs& a, cudaStream_t s) {
+  return d == 128 ? tc_go<128>(a, s) : tc_go<64>(a, s);
+}
+
+}  // namespace fastar
