@@ -5,9 +5,9 @@
 //   warps 0-3 / 4-7    softmax of row tile 0 / 1, one row per thread: logits from TMEM, the
 //                      running maximum (the sums are rescaled only when it grows by more than
 //                      2^8), P as fp16 over the consumed logits in TMEM, and the output at the end;
-//   warps 8-11 / 12-15 unpack K / V: codes and scales from global memory into registers a tile
-//                      ahead, fp16 rows into a two-stage ring of 128-byte-swizzled tiles;
-//   warp 16            owns TMEM and issues tcgen05.mma from one thread: S = Q K^T of both row
+//   warps 8-11         unpack K and V: packed tiles (three on their way, brought by bulk copies that
+//                      warp 13 issues) into two-stage rings of 128-byte-swizzled fp16 tiles;
+//   warp 12            owns TMEM and issues tcgen05.mma from one thread: S = Q K^T of both row
 //                      tiles, O += P V (P from TMEM).
 // The order of issue is PV0(j) QK0(j+1) PV1(j) QK1(j+1): while the softmax of one row tile
 // runs, the tensor cores work for the other, so a logit buffer a tile is enough and two
@@ -36,15 +36,20 @@ namespace {
 
 constexpr int kRT = 128;               // rows of a row tile
 constexpr int kKT = 128;               // keys of a tile
-constexpr int kStages = 2;
-constexpr int kSoftWarps = 8, kUnpackWarps = 8;
+constexpr int kStages = 2;             // fp16 tiles of K and of V
+constexpr int kIn = 3;                 // packed tiles on their way
+constexpr int kSoftWarps = 8, kUnpackWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kUnpackWarps;
-constexpr int kThreadsT = (kMmaWarp + 1) * 32;
+constexpr int kThreadsT = 512;         // the last warpgroup is the MMA warp and three idle ones
+// Registers: 512 threads x 128 at launch = 65,536 = 256 softmax threads x 200 + 256 others x 56.
+constexpr int kRegsSoft = 200, kRegsRest = 56;
+static_assert(2 * 128 * (kRegsSoft + kRegsRest) <= kThreadsT * 128, "the launch's registers bound the shares");
 constexpr int kBlk = 128 * 128;        // 128 rows x 64 fp16 (128-byte swizzle)
 
 struct alignas(16) Kv4Ctl {
+  uint64_t in_full[kIn], in_empty[kIn];                // packed tiles: K 0, V 0, K 1, V 1, ...
   uint64_t q_full[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_full[2], pv_done[2], fin;
+  uint64_t s_full[2], p_full[2][2], pv_done[2], fin;   // P: the first and the second 64 keys
   uint32_t tmem_base;
   int abort;
 };
@@ -56,7 +61,9 @@ struct Kv4Layout {
   static constexpr size_t q = 0;
   static constexpr size_t k = q + 2 * tile;
   static constexpr size_t v = k + kStages * tile;
-  static constexpr size_t ctl = v + kStages * tile;
+  static constexpr size_t in_codes = (size_t)kKT * D / 2, in_tile = in_codes + (size_t)kKT * D / 16;
+  static constexpr size_t in = v + kStages * tile;
+  static constexpr size_t ctl = in + kIn * in_tile;
   static constexpr size_t bytes = ctl + sizeof(Kv4Ctl) + 1024;
   static constexpr uint32_t s_col = 0, o_col = 256;   // two 128-column buffers each
 };
@@ -108,69 +115,41 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
-// Largest of 32 logits; kFull = false: of the first `valid`.
-template <bool kFull>
-__device__ __forceinline__ float max_of32(const float* x, int valid) {
-  float m = neg_inf();
+// Largest of the 128 logits in registers.
+__device__ __forceinline__ float row_max(const float* x) {
+  float m[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+  for (int i = 0; i < kKT; i += 2) m[(i >> 1) & 3] = max3f(m[(i >> 1) & 3], x[i], x[i + 1]);
+  return fmaxf(max3f(m[0], m[1], m[2]), m[3]);
+}
+
+// (a, b) * s + c and (a, b) + (c, d), two lanes an instruction.
+__device__ __forceinline__ void fma2(float& a, float& b, float s, float c) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mov.b64 z, {%3, %3};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(s), "f"(c));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n"
+      " mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+
+// P = 2^(s sl2 - m) of 32 logits as fp16 pairs into 16 TMEM columns; adds to the row's sum.
+__device__ __forceinline__ void row_exp32(float* x, float sl2, float nm, uint32_t dst, float& s0, float& s1) {
+  uint32_t pk[16];
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
-    const float a = kFull || i < valid ? x[i] : neg_inf(), b = kFull || i + 1 < valid ? x[i + 1] : neg_inf();
-    m = max3f(m, a, b);
+    float a = x[i], b = x[i + 1];
+    fma2(a, b, sl2, nm);
+    a = ex2f(a);
+    b = ex2f(b);
+    add2(s0, s1, a, b);
+    pk[i >> 1] = pack_f16(a, b);
   }
-  return m;
-}
-
-template <bool kFull>
-__device__ __forceinline__ float row_max(uint32_t s, int valid) {
-  float m = neg_inf();
-#pragma unroll
-  for (int c = 0; c < kKT; c += 64) {
-    float x[64];
-    tc::tmem_ld32(s + (uint32_t)c, x);
-    tc::tmem_ld32(s + (uint32_t)(c + 32), x + 32);
-    tc::tmem_wait_ld();
-    tc::tmem_pin32(x);
-    tc::tmem_pin32(x + 32);
-    m = max3f(m, max_of32<kFull>(x, valid - c), max_of32<kFull>(x + 32, valid - c - 32));
-  }
-  return m;
-}
-
-// P = 2^(s sl2 - m) as fp16 pairs over the logits' own columns (chunk c of 32 logits becomes
-// columns 16 c .. 16 c + 15, which are read by then); returns the row's sum of P.
-template <bool kFull>
-__device__ __forceinline__ float row_exp(uint32_t s, int valid, float sl2, float m) {
-  const float nm = m == neg_inf() ? 0.f : -m;
-  float xa[32], xb[32];
-  float s0 = 0.f, s1 = 0.f;
-  tc::tmem_ld32(s, xa);
-  tc::tmem_wait_ld();
-  tc::tmem_pin32(xa);
-#pragma unroll
-  for (int c = 0; c < kKT / 32; ++c) {
-    float* cur = (c & 1) ? xb : xa;
-    float* nxt = (c & 1) ? xa : xb;
-    if (c + 1 < kKT / 32) tc::tmem_ld32(s + (uint32_t)((c + 1) * 32), nxt);
-    uint32_t pk[16];
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      float a0 = fmaf(cur[i], sl2, nm), a1 = fmaf(cur[i + 1], sl2, nm);
-      if (!kFull) {
-        a0 = c * 32 + i < valid ? a0 : neg_inf();
-        a1 = c * 32 + i + 1 < valid ? a1 : neg_inf();
-      }
-      const float p0 = ex2f(a0), p1 = ex2f(a1);
-      s0 += p0;
-      s1 += p1;
-      pk[i >> 1] = pack_f16(p0, p1);
-    }
-    tmem_st16(s + (uint32_t)(c * 16), pk);
-    if (c + 1 < kKT / 32) {
-      tc::tmem_wait_ld();
-      tc::tmem_pin32(nxt);
-    }
-  }
-  return s0 + s1;
+  tmem_st16(dst, pk);
 }
 
 // Row r of a KV head's work: its query head and token.
@@ -232,7 +211,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.q_full[i], kRT);
       tc::mbar_init(&sm.s_full[i], 1);
-      tc::mbar_init(&sm.p_full[i], 4);
+      tc::mbar_init(&sm.p_full[i][0], 4);
+      tc::mbar_init(&sm.p_full[i][1], 4);
       tc::mbar_init(&sm.pv_done[i], 1);
     }
     for (int i = 0; i < kStages; ++i) {
@@ -240,6 +220,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       tc::mbar_init(&sm.k_empty[i], 1);
       tc::mbar_init(&sm.v_full[i], 128);
       tc::mbar_init(&sm.v_empty[i], 1);
+    }
+    for (int i = 0; i < kIn; ++i) {
+      tc::mbar_init(&sm.in_full[i], 1);
+      tc::mbar_init(&sm.in_empty[i], 4);
     }
     tc::mbar_init(&sm.fin, 1);
     sm.abort = 0;
@@ -257,6 +241,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
 
   if (warp < kSoftWarps) {
     // ---------------- softmax ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     const int w = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const int64_t r = r0 + w * kRT + row;
@@ -288,6 +273,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       if (big == 0 || ex == 255) qe = 0;
       const float down = kv4::pow2i(-qe);
       sl2 = a.scale * kv4::pow2i(qe) * kv4::pow2i(kv4::head_exp(a.k_exp, h)) * 1.4426950408889634f;
+      sl2 = fmaxf(sl2, 1.2e-38f);      // a product of scales under fp32's range: still positive
       uint8_t* dst = base + Lay::q + (size_t)w * Lay::tile;
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
@@ -301,7 +287,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       tc::fence_proxy_async();
       tc::mbar_arrive(&sm.q_full[w]);
 
-      const int64_t see = (has ? kv4::visible(len, a.nq, at.t, a.block) : 0) - j0 * kKT;   // from the split's first key
+      // keys the row sees from the split's first on (a row that is not there: as the last)
+      const int64_t see = (has ? kv4::visible(len, a.nq, at.t, a.block) : most) - j0 * kKT;
       const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t s_addr = lane_addr + Lay::s_col + (uint32_t)(w * 128);
       const uint32_t o_addr = lane_addr + Lay::o_col + (uint32_t)(w * 128);
@@ -314,10 +301,25 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
         }
         tc::tc_fence_after();
         const int64_t left = see - (int64_t)j * kKT;
-        const int valid = left >= kKT ? kKT : left > 0 ? (int)left : 0;
-        const bool full = __all_sync(0xffffffffu, valid == kKT);
+        float x[kKT];
+        tc::tmem_ld32(s_addr, x);
+        tc::tmem_ld32(s_addr + 32, x + 32);
+        tc::tmem_ld32(s_addr + 64, x + 64);
+        tc::tmem_ld32(s_addr + 96, x + 96);
+        tc::tmem_wait_ld();
+        tc::tmem_pin32(x);
+        tc::tmem_pin32(x + 32);
+        tc::tmem_pin32(x + 64);
+        tc::tmem_pin32(x + 96);
+        // keys that the row does not see: only in its last tiles, so the loop's hot path stays
+        // one copy of the code (it is bound by instruction fetches when it holds two)
+        if (__any_sync(0xffffffffu, left < kKT)) {
+          const int valid = left > 0 ? (int)(left < kKT ? left : kKT) : 0;
+#pragma unroll
+          for (int i = 0; i < kKT; ++i) x[i] = i < valid ? x[i] : neg_inf();
+        }
         // the scale is positive: the largest scaled logit is the largest logit, scaled
-        const float mt = (full ? row_max<true>(s_addr, valid) : row_max<false>(s_addr, valid)) * sl2;
+        const float mt = row_max(x) * sl2;
         float alpha = 1.f;
         bool resc = false;
         if (mt > m + 8.f) {
@@ -345,12 +347,20 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
           }
           tc::tmem_wait_st();
         }
-        const float sum = full ? row_exp<true>(s_addr, valid, sl2, m) : row_exp<false>(s_addr, valid, sl2, m);
-        l = l * alpha + sum;
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.p_full[w]);
+        // P over the logits' own columns, in halves of 64 keys, each handed to the MMAs as it lands
+        const float nm = m == neg_inf() ? 0.f : -m;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          row_exp32(x + 32 * c, sl2, nm, s_addr + (uint32_t)(16 * c), l0, l1);
+          if (c & 1) {
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.p_full[w][c >> 1]);
+          }
+        }
+        l = l * alpha + (l0 + l1);
       }
       if (ok && wait_warp(&sm.pv_done[w], (T - 1) & 1, abort)) {
         tc::tc_fence_after();
@@ -397,66 +407,85 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       }
     }
   } else if (warp < kMmaWarp) {
-    // ---------------- unpack K (warps 8-11) or V (warps 12-15) ----------------
+    // ---------------- unpack K and V ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     constexpr int PARTS = D / 32;                        // 16-byte runs of 32 codes in a row
-    const bool isk = warp < kSoftWarps + 4;
     const int t = threadIdx.x & 127;
-    const uint8_t* codes = isk ? a.kc : a.vc;
-    const uint8_t* scales = isk ? a.ks : a.vs;
-    uint8_t* ring = base + (isk ? Lay::k : Lay::v);
-    uint64_t* full = isk ? sm.k_full : sm.v_full;
-    uint64_t* empty = isk ? sm.k_empty : sm.v_empty;
     const int part = t % PARTS, row0 = t / PARTS;
     const bool swap = part >= 2;     // parts 2 and 3 write their 16-byte chunks in another order,
                                      // so that the 8 lanes of a store phase hit 8 different banks
-    uint4 c[PARTS];
-    uint32_t s[PARTS];
-    auto load = [&](int j) {
+    // K and V tiles take turns through one copy of the code, kept small: the softmax warps'
+    // straight-line code shares the instruction caches with it
+#pragma unroll 1
+    for (int n = 0; n < 2 * T; ++n) {
+      const int j = n >> 1, st = j % kStages, in = n % kIn;
+      const bool isv = n & 1;
+      uint64_t* empty = isv ? &sm.v_empty[st] : &sm.k_empty[st];
+      uint64_t* full = isv ? &sm.v_full[st] : &sm.k_full[st];
+      if (!wait_warp(&sm.in_full[in], (n / kIn) & 1, abort) || !wait_warp(empty, ((j / kStages) & 1) ^ 1, abort)) break;
+      const uint8_t* packed = base + Lay::in + in * Lay::in_tile;
+      uint8_t* tile = base + (isv ? Lay::v : Lay::k) + (size_t)st * Lay::tile;
+      // rows past the last key hold what is in memory there, or nothing: they count as 0
+      const int64_t left = most - (j0 + j) * kKT;
+#pragma unroll 1
+      for (int i = 0; i < PARTS; i += 2) {
+        uint4 c[2];
+        uint32_t s[2];
 #pragma unroll
-      for (int i = 0; i < PARTS; ++i) {
-        const int64_t key = (j0 + j) * kKT + row0 + i * (128 / PARTS);
-        c[i] = make_uint4(0, 0, 0, 0);
-        s[i] = 0;
-        if (key < most) {
-          const int64_t rowi = (int64_t)h * a.cap + key;
-          c[i] = __ldg(reinterpret_cast<const uint4*>(codes + rowi * (D / 2)) + part);
-          s[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + rowi * (D / 16)) + part);
+        for (int k = 0; k < 2; ++k) {
+          c[k] = reinterpret_cast<const uint4*>(packed)[(i + k) * 128 + t];
+          s[k] = reinterpret_cast<const uint16_t*>(packed + Lay::in_codes)[(i + k) * 128 + t];
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int row = row0 + (i + k) * (128 / PARTS);
+          if (row >= left) c[k] = make_uint4(0, 0, 0, 0), s[k] = 0;
+          uint32_t wv[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+          uint32_t s0 = kv4::scale_f16x2(s[k]), s1 = kv4::scale_f16x2(s[k] >> 8);
+          if (PARTS == 4 && swap) {
+            uint32_t x = wv[0];
+            wv[0] = wv[2], wv[2] = x;
+            x = wv[1];
+            wv[1] = wv[3], wv[3] = x;
+            x = s0;
+            s0 = s1, s1 = x;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t o[4];
+            kv4::unpack8(wv[e], e < 2 ? s0 : s1, o);
+            const int ch = part * 4 + (PARTS == 4 && swap ? e ^ 2 : e);
+            *reinterpret_cast<uint4*>(tile + (ch >> 3) * kBlk + tc::sw128_off(row, ch & 7)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
         }
       }
-    };
-    load(0);
-    for (int j = 0; j < T; ++j) {
-      const int st = j % kStages;
-      if (!tc::mbar_wait(&empty[st], ((j / kStages) & 1) ^ 1, abort)) break;
-      uint8_t* tile = ring + (size_t)st * Lay::tile;
-#pragma unroll
-      for (int i = 0; i < PARTS; ++i) {
-        const int row = row0 + i * (128 / PARTS);
-        uint32_t wv[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-        uint32_t s0 = kv4::scale_f16x2(s[i]), s1 = kv4::scale_f16x2(s[i] >> 8);
-        if (PARTS == 4 && swap) {
-          uint32_t x = wv[0];
-          wv[0] = wv[2], wv[2] = x;
-          x = wv[1];
-          wv[1] = wv[3], wv[3] = x;
-          x = s0;
-          s0 = s1, s1 = x;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t o[4];
-          kv4::unpack8(wv[e], e < 2 ? s0 : s1, o);
-          const int ch = part * 4 + (PARTS == 4 && swap ? e ^ 2 : e);
-          *reinterpret_cast<uint4*>(tile + (ch >> 3) * kBlk + tc::sw128_off(row, ch & 7)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      }
-      if (j + 1 < T) load(j + 1);
       tc::fence_proxy_async();
-      tc::mbar_arrive(&full[st]);
+      tc::mbar_arrive(full);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.in_empty[in]);
     }
-  } else if (lane == 0) {
-    // ---------------- MMA issue ----------------
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == kMmaWarp + 1 && lane == 0) {
+      // ---------------- packed tiles into shared memory (one thread) ----------------
+      // Whole 16-row groups: the capacity is a multiple of 16, so the group that holds the last
+      // key lies within the head's rows, and sizes and addresses are multiples of 16 bytes.
+      for (int n = 0; n < 2 * T; ++n) {
+        const int in = n % kIn;
+        if (!tc::mbar_wait(&sm.in_empty[in], ((n / kIn) & 1) ^ 1, abort)) break;
+        const int64_t key = (j0 + (n >> 1)) * kKT;
+        const int64_t left = (most - key + 15) & ~(int64_t)15;
+        const uint32_t nr = left < kKT ? (uint32_t)left : kKT;
+        const int64_t at = (int64_t)h * a.cap + key;
+        uint8_t* dst = base + Lay::in + in * Lay::in_tile;
+        tc::mbar_arrive_tx(&sm.in_full[in], nr * (D / 2 + D / 16));
+        tc::bulk_load(dst, ((n & 1) ? a.vc : a.kc) + at * (D / 2), nr * (D / 2), &sm.in_full[in]);
+        tc::bulk_load(dst + Lay::in_codes, ((n & 1) ? a.vs : a.ks) + at * (D / 16), nr * (D / 16), &sm.in_full[in]);
+      }
+    }
+    // ---------------- MMA issue (one thread) ----------------
+    if (warp == kMmaWarp && lane == 0) {
     constexpr uint32_t idesc_qk = idesc_f16(kRT, kKT, false), idesc_pv = idesc_f16(kRT, D, true);
     const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(base + Lay::q));
     const uint64_t k_desc = tc::sw128_desc(tc::smem_u32(base + Lay::k));
@@ -470,12 +499,12 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       }
       tc::mma_commit(&sm.s_full[w]);
     };
-    auto pv = [&](int w, int j) {
+    // the products of one half (64 keys) of tile j
+    auto pv = [&](int w, int j, int half) {
 #pragma unroll
-      for (int k = 0; k < kKT / 16; ++k)
+      for (int k = half * 4; k < half * 4 + 4; ++k)
         mma_ts(tmem + Lay::o_col + (uint32_t)(w * 128), tmem + Lay::s_col + (uint32_t)(w * 128 + k * 8),
                v_desc + (((j % kStages) * Lay::tile + k * 2048) >> 4), idesc_pv, (j > 0 || k > 0) ? 1u : 0u);
-      tc::mma_commit(&sm.pv_done[w]);
     };
     bool ok = true;
     for (int w = 0; w < nt && ok; ++w) {
@@ -488,10 +517,15 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     for (int j = 0; j < T && ok; ++j) {
       const int st = j % kStages, nst = (j + 1) % kStages;
       for (int w = 0; w < nt; ++w) {
-        ok = tc::mbar_wait(&sm.p_full[w], j & 1, abort) && tc::mbar_wait(&sm.v_full[st], (j / kStages) & 1, abort);
+        ok = tc::mbar_wait(&sm.v_full[st], (j / kStages) & 1, abort) && tc::mbar_wait(&sm.p_full[w][0], j & 1, abort);
         if (!ok) break;
         tc::tc_fence_after();
-        pv(w, j);
+        pv(w, j, 0);
+        ok = tc::mbar_wait(&sm.p_full[w][1], j & 1, abort);
+        if (!ok) break;
+        tc::tc_fence_after();
+        pv(w, j, 1);
+        tc::mma_commit(&sm.pv_done[w]);
         if (w == nt - 1) tc::mma_commit(&sm.v_empty[st]);
         if (j + 1 < T) {
           ok = tc::mbar_wait(&sm.k_full[nst], ((j + 1) / kStages) & 1, abort);
@@ -507,6 +541,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     tc::mma_commit(&sm.fin);
     volatile int never = 0;
     tc::mbar_wait(&sm.fin, 0, &never, 400000000LL);
+    }
   }
   tc::tc_fence_before();
   __syncthreads();
