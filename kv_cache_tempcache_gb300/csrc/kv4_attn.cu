@@ -232,14 +232,15 @@ int splits_f32(int64_t blocks, int64_t cap) {
 // each a fixed part and so much a key tile, plus the partials' way through memory and the
 // join.  It takes the fewest splits that are within 2 % of the best.
 int splits_tc(int d, int64_t rows, int Hkv, int64_t cap) {
-  const int64_t sms = sm_count(), items = (rows + 255) / 256 * Hkv, tiles = (cap + 127) / 128;
-  const double tile = (rows > 128 ? 1.2 : 0.75) * (d == 128 ? 1.0 : 0.7), fixed = 6.0;
+  const int cta = d / 64;                 // CTAs that work as one (kv4_attn_tc.cu)
+  const int64_t slots = sm_count() / cta, items = (rows + 256 * cta - 1) / (256 * cta) * Hkv, tiles = (cap + 127) / 128;
+  const double tile = (rows > 128 * cta ? 1.3 : 0.9) * (d == 128 ? 1.0 : 0.7), fixed = 6.0;
   auto cost = [&](int64_t s) {
-    const double waves = (double)((items * s + sms - 1) / sms);
+    const double waves = (double)((items * s + slots - 1) / slots);
     const double join = s > 1 ? 4.0 + 2e-6 * s * rows * Hkv * (d + 2) * 4 / 4.0 : 0.0;
     return waves * (fixed + (double)((tiles + s - 1) / s) * tile) + join;
   };
-  int64_t most = (4 * sms + items - 1) / items;
+  int64_t most = (4 * slots + items - 1) / items;
   if (most > tiles) most = tiles;
   if (most > kKv4MaxSplits) most = kKv4MaxSplits;
   double best = cost(1);

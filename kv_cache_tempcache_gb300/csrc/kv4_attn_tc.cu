@@ -1,17 +1,25 @@
 // Softmax attention over the 4-bit cache on the 5th-generation tensor cores (bf16 queries).
 //
-// One CTA takes 256 rows ((query head, token) pairs of a KV head) as two tiles of 128 and a
-// range of keys, 128 at a time:
+// A CTA takes two tiles of 128 rows ((query head, token) pairs of a KV head) and a range of keys,
+// 128 at a time; at d = 128 two CTAs of a cluster work as a pair (cta_group::2): every product
+// has 256 rows, 128 of each CTA, and each CTA holds half of its K or V operand (64 of the keys
+// of Q K^T, 64 of the channels of P V).
 //   warps 0-3 / 4-7    softmax of row tile 0 / 1, one row per thread: logits from TMEM, the
 //                      running maximum (the sums are rescaled only when it grows by more than
 //                      2^8), P as fp16 over the consumed logits in TMEM, and the output at the end;
 //   warps 8-11         unpack K and V: packed tiles (three on their way, brought by bulk copies that
-//                      warp 13 issues) into two-stage rings of 128-byte-swizzled fp16 tiles;
-//   warp 12            owns TMEM and issues tcgen05.mma from one thread: S = Q K^T of both row
-//                      tiles, O += P V (P from TMEM).
+//                      warp 13 issues) into rings of 128-byte-swizzled fp16 tiles;
+//   warp 12            owns TMEM and issues tcgen05.mma from one thread (of the pair's first CTA):
+//                      S = Q K^T of both row tiles, O += P V (P from TMEM).
 // The order of issue is PV0(j) QK0(j+1) PV1(j) QK1(j+1): while the softmax of one row tile
 // runs, the tensor cores work for the other, so a logit buffer a tile is enough and two
-// accumulators of 128 columns fit TMEM beside them.
+// accumulators of 128 columns fit TMEM beside them.  (Two buffers of 64 keys a row tile, so that
+// the softmax never waits, were slower: an MMA of 64 columns runs at little over half the rate.)
+//
+// What bounds it: a 128-key tile is 2048 clocks of MMA a CTA at d = 128.  Shared memory was the
+// limit of one CTA alone: operands 192 KB, unpacked tiles 64 KB written, 18 KB in and out, 2300
+// clocks at 128 bytes each; a pair halves the K and V part (operands 128 KB, 32 KB written).
+// Instruction fetches come next: hot code is one copy, rare paths (masks, rescaling) lie apart.
 //
 // Numbers: a cache value (code times scale) is exact in fp16 (kv4.cuh).  A query row is scaled
 // by a power of two that puts its largest element in [2^12, 2^13) and rounded to fp16: bf16's 8
@@ -34,17 +42,16 @@ namespace fastar {
 
 namespace {
 
-constexpr int kRT = 128;               // rows of a row tile
+constexpr int kRT = 128;               // rows of a row tile in a CTA
 constexpr int kKT = 128;               // keys of a tile
-constexpr int kStages = 2;             // fp16 tiles of K and of V
+constexpr int kStages = 3;             // fp16 tiles of K and of V
 constexpr int kIn = 3;                 // packed tiles on their way
 constexpr int kSoftWarps = 8, kUnpackWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kUnpackWarps;
-constexpr int kThreadsT = 512;         // the last warpgroup is the MMA warp and three idle ones
+constexpr int kThreadsT = 512;         // the last warpgroup: MMA warp, copy warp, two idle ones
 // Registers: 512 threads x 128 at launch = 65,536 = 256 softmax threads x 200 + 256 others x 56.
 constexpr int kRegsSoft = 200, kRegsRest = 56;
 static_assert(2 * 128 * (kRegsSoft + kRegsRest) <= kThreadsT * 128, "the launch's registers bound the shares");
-constexpr int kBlk = 128 * 128;        // 128 rows x 64 fp16 (128-byte swizzle)
 
 struct alignas(16) Kv4Ctl {
   uint64_t in_full[kIn], in_empty[kIn];                // packed tiles: K 0, V 0, K 1, V 1, ...
@@ -54,18 +61,24 @@ struct alignas(16) Kv4Ctl {
   int abort;
 };
 
+// One CTA (d = 64) or a pair (d = 128).  What a CTA holds of a tile: KR keys of K in blocks of
+// 64 channels, all 128 keys of V with 64 channels.
 template <int D>
 struct Kv4Layout {
-  static constexpr int KH = D / 64;
-  static constexpr size_t tile = (size_t)KH * kBlk;
-  static constexpr size_t q = 0;
-  static constexpr size_t k = q + 2 * tile;
-  static constexpr size_t v = k + kStages * tile;
+  static constexpr int kCta = D / 64;
+  static constexpr int KR = kKT / kCta;
+  static constexpr size_t q_tile = (size_t)kRT * D * 2, q_blk = kRT * 128;
+  static constexpr size_t k_tile = (size_t)KR * D * 2, k_blk = KR * 128;
+  static constexpr size_t v_tile = (size_t)kKT * 128;
   static constexpr size_t in_codes = (size_t)kKT * D / 2, in_tile = in_codes + (size_t)kKT * D / 16;
-  static constexpr size_t in = v + kStages * tile;
+  static constexpr size_t q = 0;
+  static constexpr size_t k = q + 2 * q_tile;
+  static constexpr size_t v = k + kStages * k_tile;
+  static constexpr size_t in = v + kStages * v_tile;
   static constexpr size_t ctl = in + kIn * in_tile;
   static constexpr size_t bytes = ctl + sizeof(Kv4Ctl) + 1024;
   static constexpr uint32_t s_col = 0, o_col = 256;   // two 128-column buffers each
+  static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
 };
 
 // fp16 operands, fp32 sums; bit 16: B is MN-major.
@@ -73,19 +86,92 @@ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+template <int kCta>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
+  if (kCta == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
 }
+template <int kCta>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
+  if (kCta == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
 }
-
+// Arrives once on the barrier (of a pair: on both CTAs' barriers at this offset) when every
+// product this thread has issued is complete.
+template <int kCta>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (kCta == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            tc::smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    tc::mma_commit(bar);
+}
+template <int kCta>
+__device__ __forceinline__ void tmem_alloc512(uint32_t* dst) {
+  if (kCta == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(dst)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tc::tmem_alloc(dst, 512);
+    tc::tmem_relinquish();
+  }
+}
+template <int kCta>
+__device__ __forceinline__ void tmem_free512(uint32_t taddr) {
+  if (kCta == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+  else
+    tc::tmem_dealloc(taddr, 512);
+}
+// True in one lane of a converged warp; the compiler knows that a branch on it runs one thread
+// (a branch on the lane number makes it wrap every MMA in code that unifies its operands).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Arrives on the barrier of the pair's first CTA, where the products are issued.  What the
+// arrival announces lies in the arriving CTA's own shared memory or TMEM, is read there by
+// its own tensor core, and has been handed to the async proxy (fence.proxy.async) or to
+// tcgen05 (its before_thread_sync fence) first; so the arrival needs no fence over the
+// cluster's memory (a cluster-scope release took about 1000 clocks a tile).
+template <int kCta>
+__device__ __forceinline__ void arrive_issuer(uint64_t* bar) {
+  if (kCta == 2)
+    asm volatile(
+        "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
+        " mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(tc::smem_u32(bar))
+        : "memory");
+  else
+    tc::mbar_arrive(bar);
+}
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort));
 }
@@ -115,7 +201,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
-// Largest of the 128 logits in registers.
+// Largest of the logits in registers.
 __device__ __forceinline__ float row_max(const float* x) {
   float m[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
@@ -137,11 +223,10 @@ __device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
       : "f"(c), "f"(d));
 }
 
-// P = 2^(s sl2 - m) of 32 logits as fp16 pairs into 16 TMEM columns; adds to the row's sum.
-__device__ __forceinline__ void row_exp32(float* x, float sl2, float nm, uint32_t dst, float& s0, float& s1) {
-  uint32_t pk[16];
+// P = 2^(s sl2 - m) of 64 logits as fp16 pairs; adds to the row's sum.
+__device__ __forceinline__ void row_exp64(const float* x, float sl2, float nm, uint32_t* pk, float& s0, float& s1) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) {
+  for (int i = 0; i < 64; i += 2) {
     float a = x[i], b = x[i + 1];
     fma2(a, b, sl2, nm);
     a = ex2f(a);
@@ -149,7 +234,6 @@ __device__ __forceinline__ void row_exp32(float* x, float sl2, float nm, uint32_
     add2(s0, s1, a, b);
     pk[i >> 1] = pack_f16(a, b);
   }
-  tmem_st16(dst, pk);
 }
 
 // Row r of a KV head's work: its query head and token.
@@ -177,48 +261,49 @@ __device__ __forceinline__ void store_empty(const Kv4AttnArgs& a, int split, Row
 template <int D>
 __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4AttnArgs a, int row_tiles) {
   using Lay = Kv4Layout<D>;
+  constexpr int kCta = Lay::kCta;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Kv4Ctl& sm = *reinterpret_cast<Kv4Ctl*>(base + Lay::ctl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kCta == 2 ? (int)cta_rank() : 0;
 
-  // the work item: KV head, 256 rows, split of the keys.  The row tiles that see most keys
-  // (the last ones of a call in blocks) start first.
-  int64_t u = blockIdx.x;
+  // the work item (the same for both CTAs of a pair): KV head, row tiles, split of the keys.
+  // The rows that see most keys (the last ones of a call in blocks) start first.
+  int64_t u = blockIdx.x / kCta;
   const int split = (int)(u % a.splits);
   u /= a.splits;
   const int rt = row_tiles - 1 - (int)(u % row_tiles);
   const int h = (int)(u / row_tiles);
   const int64_t rows = (int64_t)(a.Hq / a.Hkv) * a.nq;
-  const int64_t r0 = (int64_t)rt * (2 * kRT);
-  const int64_t rlast = (r0 + 2 * kRT < rows ? r0 + 2 * kRT : rows) - 1;
-  const int nt = rlast - r0 >= kRT ? 2 : 1;             // row tiles with rows
+  const int64_t r0 = (int64_t)rt * (2 * kRT * kCta);
+  const int64_t rlast = (r0 + 2 * kRT * kCta < rows ? r0 + 2 * kRT * kCta : rows) - 1;
+  const int nt = rlast - r0 >= kRT * kCta ? 2 : 1;      // row tiles with rows
   const int64_t len = kv4::head_len(a.len, h, a.cap, a.status);
   // the last key that any of the rows sees: rows of two heads include a last token
   const int64_t most = r0 / a.nq != rlast / a.nq ? len : kv4::visible(len, a.nq, rlast % a.nq, a.block);
   const int64_t tiles = (most + kKT - 1) / kKT;
   const int64_t j0 = tiles * split / a.splits;
   const int T = (int)(tiles * (split + 1) / a.splits - j0);
-  const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
 
-  if (T == 0) {                                          // no keys: uniform over the CTA
-    const int64_t r = r0 + threadIdx.x;
+  if (T == 0) {                                          // no keys: uniform over the pair
+    const int64_t r = r0 + (int64_t)(threadIdx.x / kRT) * (kRT * kCta) + rank * kRT + threadIdx.x % kRT;
     if (threadIdx.x < 2 * kRT && r < rows) store_empty<D>(a, split, row_of(a, h, r));
     return;
   }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sm.q_full[i], kRT);
+      tc::mbar_init(&sm.q_full[i], 4 * kCta);
       tc::mbar_init(&sm.s_full[i], 1);
-      tc::mbar_init(&sm.p_full[i][0], 4);
-      tc::mbar_init(&sm.p_full[i][1], 4);
+      tc::mbar_init(&sm.p_full[i][0], 4 * kCta);
+      tc::mbar_init(&sm.p_full[i][1], 4 * kCta);
       tc::mbar_init(&sm.pv_done[i], 1);
     }
     for (int i = 0; i < kStages; ++i) {
-      tc::mbar_init(&sm.k_full[i], 128);
+      tc::mbar_init(&sm.k_full[i], 4 * kCta);
       tc::mbar_init(&sm.k_empty[i], 1);
-      tc::mbar_init(&sm.v_full[i], 128);
+      tc::mbar_init(&sm.v_full[i], 4 * kCta);
       tc::mbar_init(&sm.v_empty[i], 1);
     }
     for (int i = 0; i < kIn; ++i) {
@@ -229,12 +314,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     sm.abort = 0;
     tc::mbar_fence_init();
   }
-  if (warp == kMmaWarp) {
-    tc::tmem_alloc(&sm.tmem_base, 512);
-    tc::tmem_relinquish();
-  }
+  if (warp == kMmaWarp) tmem_alloc512<kCta>(&sm.tmem_base);
   tc::tc_fence_before();
   __syncthreads();
+  if (kCta == 2) pair_sync();                            // the other CTA's barriers are ready too
   tc::tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
@@ -244,21 +327,20 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     const int w = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
-    const int64_t r = r0 + w * kRT + row;
+    const int64_t r = r0 + (int64_t)w * (kRT * kCta) + rank * kRT + row;
     const bool has = r < rows;
     const RowOf at = has ? row_of(a, h, r) : RowOf{0, 0};
-    float sl2 = 0.f;
     if (w < nt) {
       // this thread's query row: its largest magnitude, then fp16 at a power of two
-      uint4 x[D / 8];
+      uint4 xq[D / 8];
       uint32_t big = 0;
       const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + at.head * a.q.hs +
                                                       at.t * a.q.ts);
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) x[c] = has ? p[c] : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < D / 8; ++c) xq[c] = has ? p[c] : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
-        const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+        const uint32_t v[4] = {xq[c].x, xq[c].y, xq[c].z, xq[c].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           big = max(big, v[e] & 0x7fffu);
@@ -272,98 +354,111 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       if (qe < -120) qe = -120;
       if (big == 0 || ex == 255) qe = 0;
       const float down = kv4::pow2i(-qe);
-      sl2 = a.scale * kv4::pow2i(qe) * kv4::pow2i(kv4::head_exp(a.k_exp, h)) * 1.4426950408889634f;
+      float sl2 = a.scale * kv4::pow2i(qe) * kv4::pow2i(kv4::head_exp(a.k_exp, h)) * 1.4426950408889634f;
       sl2 = fmaxf(sl2, 1.2e-38f);      // a product of scales under fp32's range: still positive
-      uint8_t* dst = base + Lay::q + (size_t)w * Lay::tile;
+      uint8_t* dst = base + Lay::q + (size_t)w * Lay::q_tile;
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
-        const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+        const uint32_t v[4] = {xq[c].x, xq[c].y, xq[c].z, xq[c].w};
         uint32_t o[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           o[e] = pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * kBlk + tc::sw128_off(row, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * Lay::q_blk + tc::sw128_off(row, c & 7)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
       }
       tc::fence_proxy_async();
-      tc::mbar_arrive(&sm.q_full[w]);
+      __syncwarp();
+      if (lane == 0) arrive_issuer<kCta>(&sm.q_full[w]);
 
       // keys the row sees from the split's first on (a row that is not there: as the last)
       const int64_t see = (has ? kv4::visible(len, a.nq, at.t, a.block) : most) - j0 * kKT;
       const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t s_addr = lane_addr + Lay::s_col + (uint32_t)(w * 128);
       const uint32_t o_addr = lane_addr + Lay::o_col + (uint32_t)(w * 128);
-      float m = neg_inf(), l = 0.f;
+      float m = neg_inf(), l0 = 0.f, l1 = 0.f;
       bool ok = true;
+#pragma unroll 1
       for (int j = 0; j < T; ++j) {
         if (!wait_warp(&sm.s_full[w], j & 1, abort)) {
           ok = false;
           break;
         }
         tc::tc_fence_after();
-        const int64_t left = see - (int64_t)j * kKT;
         float x[kKT];
         tc::tmem_ld32(s_addr, x);
         tc::tmem_ld32(s_addr + 32, x + 32);
         tc::tmem_ld32(s_addr + 64, x + 64);
         tc::tmem_ld32(s_addr + 96, x + 96);
+        const int64_t left = see - (int64_t)j * kKT;
+        const bool cut = __any_sync(0xffffffffu, left < kKT);
         tc::tmem_wait_ld();
         tc::tmem_pin32(x);
         tc::tmem_pin32(x + 32);
         tc::tmem_pin32(x + 64);
         tc::tmem_pin32(x + 96);
-        // keys that the row does not see: only in its last tiles, so the loop's hot path stays
-        // one copy of the code (it is bound by instruction fetches when it holds two)
-        if (__any_sync(0xffffffffu, left < kKT)) {
+        if (__builtin_expect(cut, 0)) {                  // keys that the row does not see
           const int valid = left > 0 ? (int)(left < kKT ? left : kKT) : 0;
 #pragma unroll
           for (int i = 0; i < kKT; ++i) x[i] = i < valid ? x[i] : neg_inf();
         }
-        // the scale is positive: the largest scaled logit is the largest logit, scaled
-        const float mt = row_max(x) * sl2;
-        float alpha = 1.f;
-        bool resc = false;
-        if (mt > m + 8.f) {
-          resc = m != neg_inf();
-          alpha = resc ? ex2f(m - mt) : 0.f;
-          m = mt;
-        }
-        if (__any_sync(0xffffffffu, resc)) {
-          // O holds the products of the tiles before: they have to have landed
-          if (!wait_warp(&sm.pv_done[w], (j - 1) & 1, abort)) {
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const float f = resc ? alpha : 1.f;
+        // The first half's P is formed with the maximum of the tiles before, beside this tile's
+        // own maximum (exponentials and maxima run on different units); it is kept unless a row's
+        // maximum has grown by more than 2^8, which after the first tiles is rare.
+        uint32_t pk[32];
+        float nm, h0, h1;
+        while (true) {
+          nm = m == neg_inf() ? 0.f : -m;
+          h0 = l0;
+          h1 = l1;
+          row_exp64(x, sl2, nm, pk, h0, h1);
+          // the scale is positive: the largest scaled logit is the largest logit, scaled
+          const float mt = row_max(x) * sl2;
+          if (__builtin_expect(!__any_sync(0xffffffffu, mt > m + 8.f), 1)) break;
+          const bool grow = mt > m + 8.f, resc = grow && m != neg_inf();
+          const float f = resc ? ex2f(m - mt) : 1.f;
+          if (grow) m = mt;
+          if (__any_sync(0xffffffffu, resc)) {
+            // O holds the products of the tiles before: they have to have landed
+            ok = wait_warp(&sm.pv_done[w], (j - 1) & 1, abort);
+            if (!ok) break;
+            tc::tc_fence_after();
+            l0 *= f;
+            l1 *= f;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tc::tmem_ld32(o_addr + (uint32_t)c, o);
-            tc::tmem_wait_ld();
-            tc::tmem_pin32(o);
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              tc::tmem_ld16(o_addr + (uint32_t)c, o);
+              tc::tmem_wait_ld();
+              tc::tmem_pin16(o);
+              uint32_t ou[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= f;
-            tc::tmem_st32(o_addr + (uint32_t)c, o);
-          }
-          tc::tmem_wait_st();
-        }
-        // P over the logits' own columns, in halves of 64 keys, each handed to the MMAs as it lands
-        const float nm = m == neg_inf() ? 0.f : -m;
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          row_exp32(x + 32 * c, sl2, nm, s_addr + (uint32_t)(16 * c), l0, l1);
-          if (c & 1) {
+              for (int i = 0; i < 16; ++i) ou[i] = __float_as_uint(o[i] * f);
+              tmem_st16(o_addr + (uint32_t)c, ou);
+            }
             tc::tmem_wait_st();
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sm.p_full[w][c >> 1]);
           }
         }
-        l = l * alpha + (l0 + l1);
+        if (!ok) break;
+        // P over the logits' own columns, in halves of 64 keys, each handed to the MMAs as it lands
+        l0 = h0;
+        l1 = h1;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1) row_exp64(x + 64, sl2, nm, pk, l0, l1);
+          tmem_st16(s_addr + (uint32_t)(32 * half), pk);
+          tmem_st16(s_addr + (uint32_t)(32 * half + 16), pk + 16);
+          tc::tmem_wait_st();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_issuer<kCta>(&sm.p_full[w][half]);
+        }
       }
+      const float l = l0 + l1;
       if (ok && wait_warp(&sm.pv_done[w], (T - 1) & 1, abort)) {
         tc::tc_fence_after();
+        const bool live = l > 0.f || l != l;
+        const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
         // the TMEM loads are the warp's: rows past the last load too, and store nothing
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -373,7 +468,6 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
           tc::tmem_wait_ld();
           tc::tmem_pin32(o);
           if (!has) continue;
-          const bool live = l > 0.f || l != l;
           if (a.splits > 1) {
             const int64_t pa = (split * (int64_t)a.Hq + at.head) * a.nq + at.t;
             float4* p4 = reinterpret_cast<float4*>(a.part_o + pa * D + c);
@@ -397,7 +491,6 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
           }
         }
         if (has) {
-          const bool live = l > 0.f || l != l;
           const float mn = m * 0.6931471805599453f;
           if (a.splits > 1)
             a.part_ml[(split * (int64_t)a.Hq + at.head) * a.nq + at.t] = make_float2(live ? mn : neg_inf(), l);
@@ -409,11 +502,12 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
   } else if (warp < kMmaWarp) {
     // ---------------- unpack K and V ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    constexpr int PARTS = D / 32;                        // 16-byte runs of 32 codes in a row
+    // A thread takes two runs of 32 codes (16 bytes) of a tile: of K's KR rows x D channels, or of
+    // V's 128 rows x this CTA's 64 channels.  With four runs to a row (K at d = 128) runs 2 and
+    // 3 write their 16-byte chunks in another order: so the 8 lanes of a store phase always
+    // hit 8 different bank groups of the swizzled tile.
     const int t = threadIdx.x & 127;
-    const int part = t % PARTS, row0 = t / PARTS;
-    const bool swap = part >= 2;     // parts 2 and 3 write their 16-byte chunks in another order,
-                                     // so that the 8 lanes of a store phase hit 8 different banks
+    constexpr int KP = D / 32;                            // runs of a row of K
     // K and V tiles take turns through one copy of the code, kept small: the softmax warps'
     // straight-line code shares the instruction caches with it
 #pragma unroll 1
@@ -422,147 +516,177 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       const bool isv = n & 1;
       uint64_t* empty = isv ? &sm.v_empty[st] : &sm.k_empty[st];
       uint64_t* full = isv ? &sm.v_full[st] : &sm.k_full[st];
+      const int part = isv || KP == 2 ? t & 1 : t & 3, row0 = isv || KP == 2 ? t >> 1 : t >> 2;
+      const int rstep = isv || KP == 2 ? 64 : 32;
+      const int flip = part & 2;
+      // the run's place in the packed tile: 16 bytes of codes, two scales
+      const int run0 = isv ? row0 * KP + (kCta == 2 ? 2 * rank : 0) + part : t;
+      const int runstep = rstep * KP;
       if (!wait_warp(&sm.in_full[in], (n / kIn) & 1, abort) || !wait_warp(empty, ((j / kStages) & 1) ^ 1, abort)) break;
       const uint8_t* packed = base + Lay::in + in * Lay::in_tile;
-      uint8_t* tile = base + (isv ? Lay::v : Lay::k) + (size_t)st * Lay::tile;
+      uint8_t* tile = base + (isv ? Lay::v + (size_t)st * Lay::v_tile : Lay::k + (size_t)st * Lay::k_tile);
       // rows past the last key hold what is in memory there, or nothing: they count as 0
-      const int64_t left = most - (j0 + j) * kKT;
-#pragma unroll 1
-      for (int i = 0; i < PARTS; i += 2) {
-        uint4 c[2];
-        uint32_t s[2];
+      const int64_t left = most - (j0 + j) * kKT - (isv ? 0 : rank * Lay::KR);
+      uint4 c[2];
+      uint32_t s[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          c[k] = reinterpret_cast<const uint4*>(packed)[(i + k) * 128 + t];
-          s[k] = reinterpret_cast<const uint16_t*>(packed + Lay::in_codes)[(i + k) * 128 + t];
+      for (int k = 0; k < 2; ++k) {
+        c[k] = reinterpret_cast<const uint4*>(packed)[run0 + k * runstep];
+        s[k] = reinterpret_cast<const uint16_t*>(packed + Lay::in_codes)[run0 + k * runstep];
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = row0 + k * rstep;
+        if (row >= left) c[k] = make_uint4(0, 0, 0, 0), s[k] = 0;
+        uint32_t wv[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+        uint32_t s0 = kv4::scale_f16x2(s[k]), s1 = kv4::scale_f16x2(s[k] >> 8);
+        if (KP == 4 && flip) {
+          uint32_t x = wv[0];
+          wv[0] = wv[2], wv[2] = x;
+          x = wv[1];
+          wv[1] = wv[3], wv[3] = x;
+          x = s0;
+          s0 = s1, s1 = x;
         }
+        uint8_t* dst = tile + (KP == 4 && flip ? Lay::k_blk : 0);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int row = row0 + (i + k) * (128 / PARTS);
-          if (row >= left) c[k] = make_uint4(0, 0, 0, 0), s[k] = 0;
-          uint32_t wv[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
-          uint32_t s0 = kv4::scale_f16x2(s[k]), s1 = kv4::scale_f16x2(s[k] >> 8);
-          if (PARTS == 4 && swap) {
-            uint32_t x = wv[0];
-            wv[0] = wv[2], wv[2] = x;
-            x = wv[1];
-            wv[1] = wv[3], wv[3] = x;
-            x = s0;
-            s0 = s1, s1 = x;
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t o[4];
-            kv4::unpack8(wv[e], e < 2 ? s0 : s1, o);
-            const int ch = part * 4 + (PARTS == 4 && swap ? e ^ 2 : e);
-            *reinterpret_cast<uint4*>(tile + (ch >> 3) * kBlk + tc::sw128_off(row, ch & 7)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-          }
+        for (int e = 0; e < 4; ++e) {
+          uint32_t o[4];
+          kv4::unpack8(wv[e], e < 2 ? s0 : s1, o);
+          *reinterpret_cast<uint4*>(dst + tc::sw128_off(row, (part & 1) * 4 + (e ^ flip))) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
       tc::fence_proxy_async();
-      tc::mbar_arrive(full);
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.in_empty[in]);
+      if (lane == 0) {
+        arrive_issuer<kCta>(full);
+        tc::mbar_arrive(&sm.in_empty[in]);
+      }
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kMmaWarp + 1 && lane == 0) {
       // ---------------- packed tiles into shared memory (one thread) ----------------
       // Whole 16-row groups: the capacity is a multiple of 16, so the group that holds the last
-      // key lies within the head's rows, and sizes and addresses are multiples of 16 bytes.
+      // key lies within the head's rows, and sizes and addresses are multiples of 16 bytes.  Of
+      // K only this CTA's rows; of V whole rows (a bulk copy is contiguous).
       for (int n = 0; n < 2 * T; ++n) {
         const int in = n % kIn;
+        const bool isv = n & 1;
         if (!tc::mbar_wait(&sm.in_empty[in], ((n / kIn) & 1) ^ 1, abort)) break;
-        const int64_t key = (j0 + (n >> 1)) * kKT;
+        const int64_t key = (j0 + (n >> 1)) * kKT + (isv ? 0 : rank * Lay::KR);
+        const int want = isv ? kKT : Lay::KR;
         const int64_t left = (most - key + 15) & ~(int64_t)15;
-        const uint32_t nr = left < kKT ? (uint32_t)left : kKT;
+        const uint32_t nr = left < 0 ? 0u : left < want ? (uint32_t)left : (uint32_t)want;
         const int64_t at = (int64_t)h * a.cap + key;
         uint8_t* dst = base + Lay::in + in * Lay::in_tile;
         tc::mbar_arrive_tx(&sm.in_full[in], nr * (D / 2 + D / 16));
-        tc::bulk_load(dst, ((n & 1) ? a.vc : a.kc) + at * (D / 2), nr * (D / 2), &sm.in_full[in]);
-        tc::bulk_load(dst + Lay::in_codes, ((n & 1) ? a.vs : a.ks) + at * (D / 16), nr * (D / 16), &sm.in_full[in]);
+        if (nr == 0) continue;
+        tc::bulk_load(dst, (isv ? a.vc : a.kc) + at * (D / 2), nr * (D / 2), &sm.in_full[in]);
+        tc::bulk_load(dst + Lay::in_codes, (isv ? a.vs : a.ks) + at * (D / 16), nr * (D / 16), &sm.in_full[in]);
       }
     }
-    // ---------------- MMA issue (one thread) ----------------
-    if (warp == kMmaWarp && lane == 0) {
-    constexpr uint32_t idesc_qk = idesc_f16(kRT, kKT, false), idesc_pv = idesc_f16(kRT, D, true);
-    const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(base + Lay::q));
-    const uint64_t k_desc = tc::sw128_desc(tc::smem_u32(base + Lay::k));
-    const uint64_t v_desc = tc::sw128_mn_desc(tc::smem_u32(base + Lay::v), kBlk);
-    auto qk = [&](int w, int j) {
+    // ---------------- MMA issue (one thread of the pair; its warp runs along) ----------------
+    if (warp == kMmaWarp && rank == 0) {
+      constexpr uint32_t idesc_qk = idesc_f16(kRT * kCta, kKT, false), idesc_pv = idesc_f16(kRT * kCta, D, true);
+      const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(base + Lay::q));
+      const uint64_t k_desc = tc::sw128_desc(tc::smem_u32(base + Lay::k));
+      const uint64_t v_desc = tc::sw128_mn_desc(tc::smem_u32(base + Lay::v), Lay::v_tile);
+      // the products of one half (64 keys) of a tile; `first` starts the accumulator
+      auto pv = [&](int w, int st, int half, bool first) {
+        const uint64_t vd = v_desc + ((st * Lay::v_tile + half * 8192) >> 4);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (uint32_t)((k >> 2) * kBlk + (k & 3) * 32);
-        mma_ss(tmem + Lay::s_col + (uint32_t)(w * 128), q_desc + ((w * Lay::tile + off) >> 4),
-               k_desc + (((j % kStages) * Lay::tile + off) >> 4), idesc_qk, k > 0 ? 1u : 0u);
-      }
-      tc::mma_commit(&sm.s_full[w]);
-    };
-    // the products of one half (64 keys) of tile j
-    auto pv = [&](int w, int j, int half) {
-#pragma unroll
-      for (int k = half * 4; k < half * 4 + 4; ++k)
-        mma_ts(tmem + Lay::o_col + (uint32_t)(w * 128), tmem + Lay::s_col + (uint32_t)(w * 128 + k * 8),
-               v_desc + (((j % kStages) * Lay::tile + k * 2048) >> 4), idesc_pv, (j > 0 || k > 0) ? 1u : 0u);
-    };
-    bool ok = true;
-    for (int w = 0; w < nt && ok; ++w) {
-      ok = tc::mbar_wait(&sm.q_full[w], 0, abort) && tc::mbar_wait(&sm.k_full[0], 0, abort);
-      if (!ok) break;
-      tc::tc_fence_after();
-      qk(w, 0);
-    }
-    if (ok) tc::mma_commit(&sm.k_empty[0]);
-    for (int j = 0; j < T && ok; ++j) {
-      const int st = j % kStages, nst = (j + 1) % kStages;
-      for (int w = 0; w < nt; ++w) {
-        ok = tc::mbar_wait(&sm.v_full[st], (j / kStages) & 1, abort) && tc::mbar_wait(&sm.p_full[w][0], j & 1, abort);
-        if (!ok) break;
-        tc::tc_fence_after();
-        pv(w, j, 0);
-        ok = tc::mbar_wait(&sm.p_full[w][1], j & 1, abort);
-        if (!ok) break;
-        tc::tc_fence_after();
-        pv(w, j, 1);
-        tc::mma_commit(&sm.pv_done[w]);
-        if (w == nt - 1) tc::mma_commit(&sm.v_empty[st]);
-        if (j + 1 < T) {
-          ok = tc::mbar_wait(&sm.k_full[nst], ((j + 1) / kStages) & 1, abort);
+        for (int k = 0; k < 4; ++k)
+          mma_ts<kCta>(tmem + Lay::o_col + (uint32_t)(w * 128),
+                       tmem + Lay::s_col + (uint32_t)(w * 128 + half * 32 + k * 8), vd + ((k * 2048) >> 4), idesc_pv,
+                       !first || k > 0 ? 1u : 0u);
+      };
+      bool ok = true;
+      int st = 0, nst = 0;
+      uint32_t ph = 0, nph = 0;                           // of V tile j and of K tile j + 1
+#pragma unroll 1
+      for (int j = -1; j < T && ok; ++j) {                // P V of tile j (from 0 on), Q K^T of tile j + 1
+        const bool more = j + 1 < T;
+        ok = (j < 0 || wait_warp(&sm.v_full[st], ph, abort)) && (!more || wait_warp(&sm.k_full[nst], nph, abort));
+#pragma unroll 1
+        for (int w = 0; w < nt && ok; ++w) {
+          if (j >= 0) {
+#pragma unroll 1
+            for (int half = 0; half < 2 && ok; ++half) {
+              ok = wait_warp(&sm.p_full[w][half], j & 1, abort);
+              if (!ok) break;
+              tc::tc_fence_after();
+              if (elect_one()) pv(w, st, half, j == 0 && half == 0);
+              __syncwarp();
+            }
+          } else {
+            ok = wait_warp(&sm.q_full[w], 0, abort);
+          }
           if (!ok) break;
           tc::tc_fence_after();
-          qk(w, j + 1);
+          if (elect_one()) {
+            if (j >= 0) {
+              commit<kCta>(&sm.pv_done[w]);
+              if (w == nt - 1) commit<kCta>(&sm.v_empty[st]);
+            }
+            if (more) {
+              // logits of row tile w and the K tile in stage nst
+              const uint64_t qd = q_desc + ((w * Lay::q_tile) >> 4), kd = k_desc + ((nst * Lay::k_tile) >> 4);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                mma_ss<kCta>(tmem + Lay::s_col + (uint32_t)(w * 128),
+                             qd + (((k >> 2) * Lay::q_blk + (k & 3) * 32) >> 4),
+                             kd + (((k >> 2) * Lay::k_blk + (k & 3) * 32) >> 4), idesc_qk, k > 0 ? 1u : 0u);
+              commit<kCta>(&sm.s_full[w]);
+              if (w == nt - 1) commit<kCta>(&sm.k_empty[nst]);
+            }
+          }
+          __syncwarp();
         }
+        if (j >= 0 && ++st == kStages) st = 0, ph ^= 1;
+        if (++nst == kStages) nst = 0, nph ^= 1;
       }
-      if (!ok) break;
-      if (j + 1 < T) tc::mma_commit(&sm.k_empty[nst]);
-    }
-    // every issued product ends before TMEM is given back
-    tc::mma_commit(&sm.fin);
-    volatile int never = 0;
-    tc::mbar_wait(&sm.fin, 0, &never, 400000000LL);
+      // every issued product ends before TMEM is given back
+      if (elect_one()) commit<kCta>(&sm.fin);
+      __syncwarp();
+      volatile int never = 0;
+      tc::mbar_wait(&sm.fin, 0, &never, 400000000LL);
     }
   }
   tc::tc_fence_before();
   __syncthreads();
+  if (kCta == 2) pair_sync();            // neither CTA leaves while the other may signal or use it
   if (warp == kMmaWarp) {
     tc::tc_fence_after();
-    tc::tmem_dealloc(tmem, 512);
+    tmem_free512<kCta>(tmem);
   }
   if (threadIdx.x == 0 && sm.abort) flag_status(a.status, FASTAR_DEV_TIMEOUT);
 }
 
 template <int D>
 cudaError_t tc_go(const Kv4AttnArgs& a, cudaStream_t s) {
+  using Lay = Kv4Layout<D>;
   const int64_t rows = (int64_t)(a.Hq / a.Hkv) * a.nq;
-  const int64_t rt = (rows + 2 * kRT - 1) / (2 * kRT);
-  const int64_t blocks = rt * a.Hkv * a.splits;
+  const int64_t rt = (rows + 2 * kRT * Lay::kCta - 1) / (2 * kRT * Lay::kCta);
+  const int64_t blocks = rt * a.Hkv * a.splits * Lay::kCta;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = opt_in_smem((const void*)kv4_attn_tc_kernel<D>, (int)Kv4Layout<D>::bytes);
+  cudaError_t e = opt_in_smem((const void*)kv4_attn_tc_kernel<D>, (int)Lay::bytes);
   if (e != cudaSuccess) return e;
-  kv4_attn_tc_kernel<D><<<(unsigned)blocks, kThreadsT, Kv4Layout<D>::bytes, s>>>(a, (int)rt);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreadsT);
+  cfg.dynamicSmemBytes = Lay::bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = Lay::kCta;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv4_attn_tc_kernel<D>, a, (int)rt);
   count_launches(1);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
