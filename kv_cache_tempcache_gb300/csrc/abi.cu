@@ -791,7 +791,7 @@ int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d
   a.v_exp = v_exp;
   a.cap = cap;
   a.len = len;
-  a.block = block;
+  a.block = block < nq ? block : nq;   // one block of all the call's tokens is the largest
   a.scale = scale;
   a.out = out;
   a.o_hs = o_head_stride;

@@ -66,7 +66,7 @@ __device__ __forceinline__ int64_t head_len(const int32_t* len, int h, int64_t c
 // the cache's last nq rows.  May be 0 (a cache shorter than the call).
 __device__ __forceinline__ int64_t visible(int64_t len, int64_t nq, int64_t t, int64_t block) {
   if (block <= 0) return len;
-  int64_t end = (t / block + 1) * block;
+  int64_t end = (int64_t)((uint32_t)t / (uint32_t)block + 1) * block;   // both fit 31 bits
   end = end < nq ? end : nq;
   const int64_t v = len - nq + end;
   return v < 0 ? 0 : v;

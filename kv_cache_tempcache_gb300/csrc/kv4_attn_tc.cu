@@ -5,8 +5,8 @@
 // has 256 rows, 128 of each CTA, and each CTA holds half of its K or V operand (64 of the keys
 // of Q K^T, 64 of the channels of P V).
 //   warps 0-3 / 4-7    softmax of row tile 0 / 1, one row per thread: logits from TMEM, the
-//                      running maximum (the sums are rescaled only when it grows by more than
-//                      2^8), P as fp16 over the consumed logits in TMEM, and the output at the end;
+//                      exponentials against a reference that is moved, and the sums rescaled, only when
+//                      a P would pass 2^15, P as fp16 over the consumed logits in TMEM, and the output at the end;
 //   warps 8-11         unpack K and V: packed tiles (three on their way, brought by bulk copies that
 //                      warp 13 issues) into rings of 128-byte-swizzled fp16 tiles;
 //   warp 12            owns TMEM and issues tcgen05.mma from one thread (of the pair's first CTA):
@@ -201,11 +201,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
-// Largest of the logits in registers.
+// Largest of n logits in registers.
+template <int n>
 __device__ __forceinline__ float row_max(const float* x) {
   float m[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-  for (int i = 0; i < kKT; i += 2) m[(i >> 1) & 3] = max3f(m[(i >> 1) & 3], x[i], x[i + 1]);
+  for (int i = 0; i < n; i += 2) m[(i >> 1) & 3] = max3f(m[(i >> 1) & 3], x[i], x[i + 1]);
   return fmaxf(max3f(m[0], m[1], m[2]), m[3]);
 }
 
@@ -241,8 +242,8 @@ struct RowOf {
   int64_t head, t;
 };
 __device__ __forceinline__ RowOf row_of(const Kv4AttnArgs& a, int h, int64_t r) {
-  const int64_t g = r / a.nq;
-  return RowOf{h * (int64_t)(a.Hq / a.Hkv) + g, r - g * a.nq};
+  const uint32_t nq = (uint32_t)a.nq, g = (uint32_t)r / nq;       // Hq * nq fits 31 bits
+  return RowOf{h * (int64_t)(a.Hq / a.Hkv) + g, (int64_t)((uint32_t)r - g * nq)};
 }
 
 // A row that sees no key: zeros and lse = -inf (in a split: an empty partial).
@@ -402,23 +403,25 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
 #pragma unroll
           for (int i = 0; i < kKT; ++i) x[i] = i < valid ? x[i] : neg_inf();
         }
-        // The first half's P is formed with the maximum of the tiles before, beside this tile's
-        // own maximum (exponentials and maxima run on different units); it is kept unless a row's
-        // maximum has grown by more than 2^8, which after the first tiles is rare.
+        // P is formed with the reference m of the tiles before (the first tile's maximum to begin
+        // with), which is moved only when a P would pass 2^15, half of what fp16 holds: the sum of
+        // the first half's P tells for that half, the second half's own maximum, taken beside
+        // the first half's exponentials, for the other.  After the first tiles that is rare.
+        if (__builtin_expect(j == 0, 0)) m = row_max<kKT>(x) * sl2;
         uint32_t pk[32];
         float nm, h0, h1;
         while (true) {
           nm = m == neg_inf() ? 0.f : -m;
-          h0 = l0;
-          h1 = l1;
+          h0 = h1 = 0.f;
           row_exp64(x, sl2, nm, pk, h0, h1);
+          const bool grow = h0 + h1 > 32768.f || row_max<64>(x + 64) * sl2 > 15.f - nm;
+          if (__builtin_expect(!__any_sync(0xffffffffu, grow), 1)) break;
           // the scale is positive: the largest scaled logit is the largest logit, scaled
-          const float mt = row_max(x) * sl2;
-          if (__builtin_expect(!__any_sync(0xffffffffu, mt > m + 8.f), 1)) break;
-          const bool grow = mt > m + 8.f, resc = grow && m != neg_inf();
-          const float f = resc ? ex2f(m - mt) : 1.f;
-          if (grow) m = mt;
-          if (__any_sync(0xffffffffu, resc)) {
+          const float mt = row_max<kKT>(x) * sl2;
+          const bool resc = grow && mt > -nm;
+          const float f = resc ? ex2f(-nm - mt) : 1.f;
+          if (resc) m = mt;
+          if (j > 0) {
             // O holds the products of the tiles before: they have to have landed
             ok = wait_warp(&sm.pv_done[w], (j - 1) & 1, abort);
             if (!ok) break;
@@ -441,8 +444,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
         }
         if (!ok) break;
         // P over the logits' own columns, in halves of 64 keys, each handed to the MMAs as it lands
-        l0 = h0;
-        l1 = h1;
+        l0 += h0;
+        l1 += h1;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (half == 1) row_exp64(x + 64, sl2, nm, pk, l0, l1);
