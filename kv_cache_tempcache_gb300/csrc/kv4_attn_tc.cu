@@ -56,7 +56,7 @@ static_assert(2 * 128 * (kRegsSoft + kRegsRest) <= kThreadsT * 128, "the launch'
 struct alignas(16) Kv4Ctl {
   uint64_t in_full[kIn], in_empty[kIn];                // packed tiles: K 0, V 0, K 1, V 1, ...
   uint64_t q_full[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_full[2][2], pv_done[2], fin;   // P: the first and the second 64 keys
+  uint64_t s_full[2], p_full[2][2], fin;   // P: the first and the second 64 keys
   uint32_t tmem_base;
   int abort;
 };
@@ -299,7 +299,6 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       tc::mbar_init(&sm.s_full[i], 1);
       tc::mbar_init(&sm.p_full[i][0], 4 * kCta);
       tc::mbar_init(&sm.p_full[i][1], 4 * kCta);
-      tc::mbar_init(&sm.pv_done[i], 1);
     }
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(&sm.k_full[i], 4 * kCta);
@@ -422,10 +421,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
           const float f = resc ? ex2f(-nm - mt) : 1.f;
           if (resc) m = mt;
           if (j > 0) {
-            // O holds the products of the tiles before: they have to have landed
-            ok = wait_warp(&sm.pv_done[w], (j - 1) & 1, abort);
-            if (!ok) break;
-            tc::tc_fence_after();
+            // O holds the products of the tiles before: these logits were issued after them, by the
+            // same thread, and their arrival says that all it had issued is complete
             l0 *= f;
             l1 *= f;
 #pragma unroll 1
@@ -442,7 +439,6 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
             tc::tmem_wait_st();
           }
         }
-        if (!ok) break;
         // P over the logits' own columns, in halves of 64 keys, each handed to the MMAs as it lands
         l0 += h0;
         l1 += h1;
@@ -458,7 +454,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
         }
       }
       const float l = l0 + l1;
-      if (ok && wait_warp(&sm.pv_done[w], (T - 1) & 1, abort)) {
+      if (ok && wait_warp(&sm.fin, 0, abort)) {
         tc::tc_fence_after();
         const bool live = l > 0.f || l != l;
         const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
@@ -590,69 +586,57 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
         tc::bulk_load(dst + Lay::in_codes, (isv ? a.vs : a.ks) + at * (D / 16), nr * (D / 16), &sm.in_full[in]);
       }
     }
-    // ---------------- MMA issue (one thread of the pair; its warp runs along) ----------------
-    if (warp == kMmaWarp && rank == 0) {
+    // ---------------- MMA issue (one thread of the pair) ----------------
+    if (warp == kMmaWarp && rank == 0 && elect_one()) {
       constexpr uint32_t idesc_qk = idesc_f16(kRT * kCta, kKT, false), idesc_pv = idesc_f16(kRT * kCta, D, true);
       const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(base + Lay::q));
       const uint64_t k_desc = tc::sw128_desc(tc::smem_u32(base + Lay::k));
       const uint64_t v_desc = tc::sw128_mn_desc(tc::smem_u32(base + Lay::v), Lay::v_tile);
-      // the products of one half (64 keys) of a tile; `first` starts the accumulator
-      auto pv = [&](int w, int st, int half, bool first) {
-        const uint64_t vd = v_desc + ((st * Lay::v_tile + half * 8192) >> 4);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ts<kCta>(tmem + Lay::o_col + (uint32_t)(w * 128),
-                       tmem + Lay::s_col + (uint32_t)(w * 128 + half * 32 + k * 8), vd + ((k * 2048) >> 4), idesc_pv,
-                       !first || k > 0 ? 1u : 0u);
-      };
       bool ok = true;
       int st = 0, nst = 0;
       uint32_t ph = 0, nph = 0;                           // of V tile j and of K tile j + 1
 #pragma unroll 1
       for (int j = -1; j < T && ok; ++j) {                // P V of tile j (from 0 on), Q K^T of tile j + 1
         const bool more = j + 1 < T;
-        ok = (j < 0 || wait_warp(&sm.v_full[st], ph, abort)) && (!more || wait_warp(&sm.k_full[nst], nph, abort));
-#pragma unroll 1
-        for (int w = 0; w < nt && ok; ++w) {
+        const uint64_t vd = v_desc + ((st * Lay::v_tile) >> 4), kd = k_desc + ((nst * Lay::k_tile) >> 4);
+        ok = (j < 0 || tc::mbar_wait(&sm.v_full[st], ph, abort)) &&
+             (!more || tc::mbar_wait(&sm.k_full[nst], nph, abort));
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {                     // unrolled: descriptors and columns are constants
+          if (w >= nt || !ok) break;
           if (j >= 0) {
-#pragma unroll 1
-            for (int half = 0; half < 2 && ok; ++half) {
-              ok = wait_warp(&sm.p_full[w][half], j & 1, abort);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {        // 64 keys at a time, as their P lands
+              ok = tc::mbar_wait(&sm.p_full[w][half], j & 1, abort);
               if (!ok) break;
               tc::tc_fence_after();
-              if (elect_one()) pv(w, st, half, j == 0 && half == 0);
-              __syncwarp();
-            }
-          } else {
-            ok = wait_warp(&sm.q_full[w], 0, abort);
-          }
-          if (!ok) break;
-          tc::tc_fence_after();
-          if (elect_one()) {
-            if (j >= 0) {
-              commit<kCta>(&sm.pv_done[w]);
-              if (w == nt - 1) commit<kCta>(&sm.v_empty[st]);
-            }
-            if (more) {
-              // logits of row tile w and the K tile in stage nst
-              const uint64_t qd = q_desc + ((w * Lay::q_tile) >> 4), kd = k_desc + ((nst * Lay::k_tile) >> 4);
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k)
-                mma_ss<kCta>(tmem + Lay::s_col + (uint32_t)(w * 128),
-                             qd + (((k >> 2) * Lay::q_blk + (k & 3) * 32) >> 4),
-                             kd + (((k >> 2) * Lay::k_blk + (k & 3) * 32) >> 4), idesc_qk, k > 0 ? 1u : 0u);
-              commit<kCta>(&sm.s_full[w]);
-              if (w == nt - 1) commit<kCta>(&sm.k_empty[nst]);
+              for (int k = 4 * half; k < 4 * half + 4; ++k)
+                mma_ts<kCta>(tmem + Lay::o_col + w * 128, tmem + Lay::s_col + w * 128 + k * 8, vd + ((k * 2048) >> 4),
+                             idesc_pv, j > 0 || k > 0 ? 1u : 0u);
             }
+            if (!ok) break;
+            if (w == nt - 1) commit<kCta>(&sm.v_empty[st]);
+          } else {
+            ok = tc::mbar_wait(&sm.q_full[w], 0, abort);
+            if (!ok) break;
+            tc::tc_fence_after();
           }
-          __syncwarp();
+          if (more) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss<kCta>(tmem + Lay::s_col + w * 128,
+                           q_desc + ((w * Lay::q_tile + (k >> 2) * Lay::q_blk + (k & 3) * 32) >> 4),
+                           kd + (((k >> 2) * Lay::k_blk + (k & 3) * 32) >> 4), idesc_qk, k > 0 ? 1u : 0u);
+            commit<kCta>(&sm.s_full[w]);
+            if (w == nt - 1) commit<kCta>(&sm.k_empty[nst]);
+          }
         }
         if (j >= 0 && ++st == kStages) st = 0, ph ^= 1;
         if (++nst == kStages) nst = 0, nph ^= 1;
       }
-      // every issued product ends before TMEM is given back
-      if (elect_one()) commit<kCta>(&sm.fin);
-      __syncwarp();
+      // the outputs are complete; and every issued product ends before TMEM is given back
+      commit<kCta>(&sm.fin);
       volatile int never = 0;
       tc::mbar_wait(&sm.fin, 0, &never, 400000000LL);
     }
