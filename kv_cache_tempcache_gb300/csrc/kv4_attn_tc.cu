@@ -4,17 +4,22 @@
 // 128 at a time; at d = 128 two CTAs of a cluster work as a pair (cta_group::2): every product
 // has 256 rows, 128 of each CTA, and each CTA holds half of its K or V operand (64 of the keys
 // of Q K^T, 64 of the channels of P V).
-//   warps 0-3 / 4-7    softmax of row tile 0 / 1, one row per thread: logits from TMEM, the
-//                      exponentials against a reference that is moved, and the sums rescaled, only when
-//                      a P would pass 2^15, P as fp16 over the consumed logits in TMEM, and the output at the end;
-//   warps 8-11         unpack K and V: packed tiles (three on their way, brought by bulk copies that
-//                      warp 13 issues) into rings of 128-byte-swizzled fp16 tiles;
-//   warp 12            owns TMEM and issues tcgen05.mma from one thread (of the pair's first CTA):
+//   warps 0-15         softmax: two threads a row, 64 of a tile's 128 keys each (warps 0-3 and 4-7 of
+//                      row tile 0, 8-11 and 12-15 of row tile 1): logits from TMEM, exponentials
+//                      against a reference that is moved, and the sums rescaled, only when a P
+//                      would pass 2^15, P as fp16 over the consumed logits in TMEM, the output;
+//   warps 16-19        unpack K and V: packed tiles (three on their way, brought by bulk copies that
+//                      warp 21 issues) into rings of 128-byte-swizzled fp16 tiles;
+//   warp 20            owns TMEM and issues tcgen05.mma from one thread (of the pair's first CTA):
 //                      S = Q K^T of both row tiles, O += P V (P from TMEM).
 // The order of issue is PV0(j) QK0(j+1) PV1(j) QK1(j+1): while the softmax of one row tile
 // runs, the tensor cores work for the other, so a logit buffer a tile is enough and two
 // accumulators of 128 columns fit TMEM beside them.  (Two buffers of 64 keys a row tile, so that
 // the softmax never waits, were slower: an MMA of 64 columns runs at little over half the rate.)
+// A row tile's turn is PV, QK and the softmax between them; with one thread a row the softmax
+// was the longest part, which is why it has two.
+// Where the rows fill only one row tile, both halves of the CTA take it: one the even key
+// tiles, the other the odd ones, and the two results are joined in shared memory at the end.
 //
 // What bounds it: a 128-key tile is 2048 clocks of MMA a CTA at d = 128.  Shared memory was the
 // limit of one CTA alone: operands 192 KB, unpacked tiles 64 KB written, 18 KB in and out, 2300
@@ -46,19 +51,21 @@ constexpr int kRT = 128;               // rows of a row tile in a CTA
 constexpr int kKT = 128;               // keys of a tile
 constexpr int kStages = 3;             // fp16 tiles of K and of V
 constexpr int kIn = 3;                 // packed tiles on their way
-constexpr int kSoftWarps = 8, kUnpackWarps = 4;
+constexpr int kSoftWarps = 16, kUnpackWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kUnpackWarps;
-constexpr int kThreadsT = 512;         // the last warpgroup: MMA warp, copy warp, two idle ones
-// Registers: 512 threads x 128 at launch = 65,536 = 256 softmax threads x 200 + 256 others x 56.
-constexpr int kRegsSoft = 200, kRegsRest = 56;
-static_assert(2 * 128 * (kRegsSoft + kRegsRest) <= kThreadsT * 128, "the launch's registers bound the shares");
+constexpr int kThreadsT = 768;         // the last warpgroup: MMA warp, copy warp, two idle ones
+// Registers: 768 threads x 80 at launch = 61,440 = 512 softmax threads x 96 + 256 others x 48.
+constexpr int kRegsSoft = 96, kRegsRest = 48;
+static_assert(512 * kRegsSoft + 256 * kRegsRest <= kThreadsT * 80, "the launch's registers bound the shares");
 
 struct alignas(16) Kv4Ctl {
   uint64_t in_full[kIn], in_empty[kIn];                // packed tiles: K 0, V 0, K 1, V 1, ...
   uint64_t q_full[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_full[2][2], fin;   // P: the first and the second 64 keys
+  uint64_t s_full[2], p_full[2][2], fin;               // by row tile (P: first 32 keys of each half, last 32)
   uint32_t tmem_base;
   int abort;
+  float ex[2][2][kRT];                                 // a row's two threads: half, row tile, row
+  float mx[kRT];
 };
 
 // One CTA (d = 64) or a pair (d = 128).  What a CTA holds of a tile: KR keys of K in blocks of
@@ -224,10 +231,11 @@ __device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
       : "f"(c), "f"(d));
 }
 
-// P = 2^(s sl2 - m) of 64 logits as fp16 pairs; adds to the row's sum.
-__device__ __forceinline__ void row_exp64(const float* x, float sl2, float nm, uint32_t* pk, float& s0, float& s1) {
+// P = 2^(s sl2 - m) of 32 logits as fp16 pairs into 16 TMEM columns; adds to the row's sum.
+__device__ __forceinline__ void row_exp32(const float* x, float sl2, float nm, uint32_t dst, float& s0, float& s1) {
+  uint32_t pk[16];
 #pragma unroll
-  for (int i = 0; i < 64; i += 2) {
+  for (int i = 0; i < 32; i += 2) {
     float a = x[i], b = x[i + 1];
     fma2(a, b, sl2, nm);
     a = ex2f(a);
@@ -235,6 +243,7 @@ __device__ __forceinline__ void row_exp64(const float* x, float sl2, float nm, u
     add2(s0, s1, a, b);
     pk[i >> 1] = pack_f16(a, b);
   }
+  tmem_st16(dst, pk);
 }
 
 // Row r of a KV head's work: its query head and token.
@@ -295,10 +304,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sm.q_full[i], 4 * kCta);
+      tc::mbar_init(&sm.q_full[i], 8 * kCta);
       tc::mbar_init(&sm.s_full[i], 1);
-      tc::mbar_init(&sm.p_full[i][0], 4 * kCta);
-      tc::mbar_init(&sm.p_full[i][1], 4 * kCta);
+      tc::mbar_init(&sm.p_full[i][0], 8 * kCta);
+      tc::mbar_init(&sm.p_full[i][1], 8 * kCta);
     }
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(&sm.k_full[i], 4 * kCta);
@@ -322,31 +331,34 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
 
+  const bool both = nt == 1;              // one row tile: even key tiles and odd key tiles
   if (warp < kSoftWarps) {
     // ---------------- softmax ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    const int w = warp >> 2;
+    const int w = warp >> 3, half = (warp >> 2) & 1;      // row tile (or parity of the key tiles), half
     const int row = (warp & 3) * 32 + lane;
-    const int64_t r = r0 + (int64_t)w * (kRT * kCta) + rank * kRT + row;
+    const int pair_bar = 1 + w * 4 + (warp & 3);          // the two warps of these rows
+    const int64_t r = r0 + (both ? 0 : (int64_t)w * (kRT * kCta)) + rank * kRT + row;
     const bool has = r < rows;
     const RowOf at = has ? row_of(a, h, r) : RowOf{0, 0};
-    if (w < nt) {
-      // this thread's query row: its largest magnitude, then fp16 at a power of two
-      uint4 xq[D / 8];
+    constexpr int HD = D / 2;                             // channels of a row of Q, and of O, a thread takes
+    float sl2;
+    {
+      // the query row: its largest magnitude, then fp16 at a power of two
+      uint4 xq[HD / 8];
       uint32_t big = 0;
       const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + at.head * a.q.hs +
-                                                      at.t * a.q.ts);
+                                                      at.t * a.q.ts + half * HD);
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) xq[c] = has ? p[c] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
+      for (int c = 0; c < HD / 8; ++c) {
+        xq[c] = has ? p[c] : make_uint4(0, 0, 0, 0);
         const uint32_t v[4] = {xq[c].x, xq[c].y, xq[c].z, xq[c].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          big = max(big, v[e] & 0x7fffu);
-          big = max(big, (v[e] >> 16) & 0x7fffu);
-        }
+        for (int e = 0; e < 4; ++e) big = max(big, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
       }
+      sm.ex[half][w][row] = __uint_as_float(big);
+      tc::named_bar(pair_bar, 64);
+      big = max(big, __float_as_uint(sm.ex[half ^ 1][w][row]));
       // exponent of the largest (subnormals count as 2^-126); a row that is zero or not finite
       // stays as it is
       const int ex = (int)(big >> 7);
@@ -354,148 +366,200 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       if (qe < -120) qe = -120;
       if (big == 0 || ex == 255) qe = 0;
       const float down = kv4::pow2i(-qe);
-      float sl2 = a.scale * kv4::pow2i(qe) * kv4::pow2i(kv4::head_exp(a.k_exp, h)) * 1.4426950408889634f;
+      sl2 = a.scale * kv4::pow2i(qe) * kv4::pow2i(kv4::head_exp(a.k_exp, h)) * 1.4426950408889634f;
       sl2 = fmaxf(sl2, 1.2e-38f);      // a product of scales under fp32's range: still positive
-      uint8_t* dst = base + Lay::q + (size_t)w * Lay::q_tile;
+      if (w == 0 || !both) {
+        uint8_t* dst = base + Lay::q + (size_t)w * Lay::q_tile;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint32_t v[4] = {xq[c].x, xq[c].y, xq[c].z, xq[c].w};
-        uint32_t o[4];
+        for (int c = 0; c < HD / 8; ++c) {
+          const uint32_t v[4] = {xq[c].x, xq[c].y, xq[c].z, xq[c].w};
+          uint32_t o[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[e] = pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * Lay::q_blk + tc::sw128_off(row, c & 7)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
-      }
-      tc::fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) arrive_issuer<kCta>(&sm.q_full[w]);
-
-      // keys the row sees from the split's first on (a row that is not there: as the last)
-      const int64_t see = (has ? kv4::visible(len, a.nq, at.t, a.block) : most) - j0 * kKT;
-      const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-      const uint32_t s_addr = lane_addr + Lay::s_col + (uint32_t)(w * 128);
-      const uint32_t o_addr = lane_addr + Lay::o_col + (uint32_t)(w * 128);
-      float m = neg_inf(), l0 = 0.f, l1 = 0.f;
-      bool ok = true;
-#pragma unroll 1
-      for (int j = 0; j < T; ++j) {
-        if (!wait_warp(&sm.s_full[w], j & 1, abort)) {
-          ok = false;
-          break;
+          for (int e = 0; e < 4; ++e)
+            o[e] = pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
+          const int ch = half * (HD / 8) + c;
+          *reinterpret_cast<uint4*>(dst + (ch >> 3) * Lay::q_blk + tc::sw128_off(row, ch & 7)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
-        tc::tc_fence_after();
-        float x[kKT];
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive_issuer<kCta>(&sm.q_full[w]);
+      }
+    }
+    // keys the row sees from this thread's first on (a row that is not there: as the last)
+    int64_t left = (has ? kv4::visible(len, a.nq, at.t, a.block) : most) - j0 * kKT - half * 64 - (both ? w * kKT : 0);
+    const int step = both ? 2 : 1, count = both ? (T - w + 1) >> 1 : T;      // this row tile's key tiles
+    const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_addr = lane_addr + Lay::s_col + (uint32_t)(w * 128 + half * 64);
+    const uint32_t o_addr = lane_addr + Lay::o_col + (uint32_t)(w * 128 + half * HD);
+    float m = 0.f, l0 = 0.f, l1 = 0.f;      // m: the reference, in log2 units
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i, left -= step * kKT) {
+      const bool alive = wait_warp(&sm.s_full[w], i & 1, abort);
+      tc::tc_fence_after();
+      const bool cut = __any_sync(0xffffffffu, left < 64);
+      const int valid = left < 64 ? left > 0 ? (int)left : 0 : 64;          // keys that the row sees
+      float mt;
+      {
+        float x[64];
         tc::tmem_ld32(s_addr, x);
         tc::tmem_ld32(s_addr + 32, x + 32);
-        tc::tmem_ld32(s_addr + 64, x + 64);
-        tc::tmem_ld32(s_addr + 96, x + 96);
-        const int64_t left = see - (int64_t)j * kKT;
-        const bool cut = __any_sync(0xffffffffu, left < kKT);
         tc::tmem_wait_ld();
         tc::tmem_pin32(x);
         tc::tmem_pin32(x + 32);
-        tc::tmem_pin32(x + 64);
-        tc::tmem_pin32(x + 96);
-        if (__builtin_expect(cut, 0)) {                  // keys that the row does not see
-          const int valid = left > 0 ? (int)(left < kKT ? left : kKT) : 0;
+        if (__builtin_expect(cut, 0)) {
 #pragma unroll
-          for (int i = 0; i < kKT; ++i) x[i] = i < valid ? x[i] : neg_inf();
+          for (int c = 0; c < 64; ++c) x[c] = c < valid ? x[c] : neg_inf();
         }
-        // P is formed with the reference m of the tiles before (the first tile's maximum to begin
-        // with), which is moved only when a P would pass 2^15, half of what fp16 holds: the sum of
-        // the first half's P tells for that half, the second half's own maximum, taken beside
-        // the first half's exponentials, for the other.  After the first tiles that is rare.
-        if (__builtin_expect(j == 0, 0)) m = row_max<kKT>(x) * sl2;
-        uint32_t pk[32];
-        float nm, h0, h1;
-        while (true) {
-          nm = m == neg_inf() ? 0.f : -m;
-          h0 = h1 = 0.f;
-          row_exp64(x, sl2, nm, pk, h0, h1);
-          const bool grow = h0 + h1 > 32768.f || row_max<64>(x + 64) * sl2 > 15.f - nm;
-          if (__builtin_expect(!__any_sync(0xffffffffu, grow), 1)) break;
-          // the scale is positive: the largest scaled logit is the largest logit, scaled
-          const float mt = row_max<kKT>(x) * sl2;
-          const bool resc = grow && mt > -nm;
-          const float f = resc ? ex2f(-nm - mt) : 1.f;
-          if (resc) m = mt;
-          if (j > 0) {
-            // O holds the products of the tiles before: these logits were issued after them, by the
-            // same thread, and their arrival says that all it had issued is complete
-            l0 *= f;
-            l1 *= f;
+        // the scale is positive: the largest scaled logit is the largest logit, scaled
+        mt = row_max<64>(x) * sl2;
+      }
+      // Both warps of the rows move the reference together: when a P would pass 2^15, half of
+      // what fp16 holds, and at the first tile.
+      if (__builtin_expect(tc::named_bar_or(pair_bar, 64, mt > m + 15.f || i == 0 || !alive), 0)) {
+        sm.ex[half][w][row] = mt;
+        // the warps leave together as well
+        if (tc::named_bar_or(pair_bar, 64, !alive)) {
+          ok = false;
+          break;
+        }
+        mt = fmaxf(mt, sm.ex[half ^ 1][w][row]);
+        float f = 1.f;
+        if (i == 0) {
+          m = mt == neg_inf() ? 0.f : mt;
+        } else if (mt > m) {
+          f = ex2f(m - mt);
+          m = mt;
+          l0 *= f;
+          l1 *= f;
+        }
+        __syncwarp();
+        if (i > 0) {
+          // O holds the products of the tiles before: these logits were issued after them, by the
+          // same thread, and their arrival says that all it had issued is complete
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              float o[16];
-              tc::tmem_ld16(o_addr + (uint32_t)c, o);
-              tc::tmem_wait_ld();
-              tc::tmem_pin16(o);
-              uint32_t ou[16];
+          for (int c = 0; c < HD; c += 16) {
+            float o[16];
+            tc::tmem_ld16(o_addr + (uint32_t)c, o);
+            tc::tmem_wait_ld();
+            tc::tmem_pin16(o);
+            uint32_t ou[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) ou[i] = __float_as_uint(o[i] * f);
-              tmem_st16(o_addr + (uint32_t)c, ou);
-            }
-            tc::tmem_wait_st();
+            for (int e = 0; e < 16; ++e) ou[e] = __float_as_uint(o[e] * f);
+            tmem_st16(o_addr + (uint32_t)c, ou);
           }
-        }
-        // P over the logits' own columns, in halves of 64 keys, each handed to the MMAs as it lands
-        l0 += h0;
-        l1 += h1;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (half == 1) row_exp64(x + 64, sl2, nm, pk, l0, l1);
-          tmem_st16(s_addr + (uint32_t)(32 * half), pk);
-          tmem_st16(s_addr + (uint32_t)(32 * half + 16), pk + 16);
           tc::tmem_wait_st();
           tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_issuer<kCta>(&sm.p_full[w][half]);
+        }
+        tc::named_bar(pair_bar, 64);                      // all of O is rescaled before either half's P goes
+        tc::tc_fence_after();
+      }
+      // P over the logits' own columns: 32 logits are read again and become 16 columns, over
+      // logits that have been read.  A loop, not unrolled: straight-line code for all 64 was
+      // slower, waiting for instructions.
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        float x[32];
+        tc::tmem_ld32(s_addr + (uint32_t)(32 * c), x);
+        tc::tmem_wait_ld();
+        tc::tmem_pin32(x);
+        if (__builtin_expect(cut, 0)) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = 32 * c + e < valid ? x[e] : neg_inf();
+        }
+        row_exp32(x, sl2, -m, s_addr + (uint32_t)(16 * c), l0, l1);
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_issuer<kCta>(&sm.p_full[w][c]);
+      }
+    }
+    // the outputs; barriers first, so that every thread passes them whatever has failed
+    ok = wait_warp(&sm.fin, 0, abort) && ok;
+    tc::tc_fence_after();
+    float l = l0 + l1;
+    sm.ex[half][w][row] = l;
+    float4* shared_o = reinterpret_cast<float4*>(base + Lay::q);    // Q has been used: 128 rows x D floats
+    constexpr int CH = D / 4;                                       // 16-byte chunks of a row
+    if (both && w == 1) {
+      if (half == 0) sm.mx[row] = m;
+      if (ok && count > 0)
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 16) {
+          float o[16];
+          tc::tmem_ld16(o_addr + (uint32_t)c, o);
+          tc::tmem_wait_ld();
+          tc::tmem_pin16(o);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            shared_o[row * CH + (((half * HD + c) / 4 + e) ^ (row & (CH - 1)))] =
+                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+    }
+    tc::named_bar(9, kSoftWarps * 32);
+    l += sm.ex[half ^ 1][w][row];
+    if (ok && !(both && w == 1)) {
+      float f0 = 1.f, f1 = 0.f;             // weights of this sum and of the odd tiles'
+      if (both && T > 1) {
+        const float lo = sm.ex[0][1][row] + sm.ex[1][1][row], mo = sm.mx[row];
+        if (lo != 0.f) {                    // the odd tiles hold a key that the row sees
+          const float mn = fmaxf(m, mo);
+          f0 = ex2f(m - mn);
+          f1 = ex2f(mo - mn);
+          l = l * f0 + lo * f1;
+          m = mn;
         }
       }
-      const float l = l0 + l1;
-      if (ok && wait_warp(&sm.fin, 0, abort)) {
-        tc::tc_fence_after();
-        const bool live = l > 0.f || l != l;
-        const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
-        // the TMEM loads are the warp's: rows past the last load too, and store nothing
+      const bool live = l > 0.f || l != l;
+      const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
+      const float f = a.splits > 1 ? up : live ? up / l : 0.f;
+      // the TMEM loads are the warp's: rows past the last load too, and store nothing
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          __syncwarp();
-          tc::tmem_ld32(o_addr + (uint32_t)c, o);
-          tc::tmem_wait_ld();
-          tc::tmem_pin32(o);
-          if (!has) continue;
-          if (a.splits > 1) {
-            const int64_t pa = (split * (int64_t)a.Hq + at.head) * a.nq + at.t;
-            float4* p4 = reinterpret_cast<float4*>(a.part_o + pa * D + c);
+      for (int c = 0; c < HD; c += 16) {
+        float o[16];
+        __syncwarp();
+        tc::tmem_ld16(o_addr + (uint32_t)c, o);
+        tc::tmem_wait_ld();
+        tc::tmem_pin16(o);
+        if (!has) continue;
+        if (f1 != 0.f) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              p4[i] = make_float4(o[4 * i] * up, o[4 * i + 1] * up, o[4 * i + 2] * up, o[4 * i + 3] * up);
-          } else {
-            const float f = live ? up / l : 0.f;
-            uint4* p4 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at.head * a.o_hs +
-                                                 at.t * a.o_ts + c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t v[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                __nv_bfloat162 h2 = __floats2bfloat162_rn(o[8 * i + 2 * e] * f, o[8 * i + 2 * e + 1] * f);
-                v[e] = live ? *reinterpret_cast<uint32_t*>(&h2) : 0u;
-              }
-              p4[i] = make_uint4(v[0], v[1], v[2], v[3]);
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float4 v = shared_o[row * CH + (((half * HD + c) / 4 + e) ^ (row & (CH - 1)))];
+            o[4 * e] = o[4 * e] * f0 + v.x * f1;
+            o[4 * e + 1] = o[4 * e + 1] * f0 + v.y * f1;
+            o[4 * e + 2] = o[4 * e + 2] * f0 + v.z * f1;
+            o[4 * e + 3] = o[4 * e + 3] * f0 + v.w * f1;
           }
         }
-        if (has) {
-          const float mn = m * 0.6931471805599453f;
-          if (a.splits > 1)
-            a.part_ml[(split * (int64_t)a.Hq + at.head) * a.nq + at.t] = make_float2(live ? mn : neg_inf(), l);
-          else if (a.lse)
-            a.lse[at.head * a.nq + at.t] = live ? mn + logf(l) : neg_inf();
+        if (a.splits > 1) {
+          const int64_t pa = (split * (int64_t)a.Hq + at.head) * a.nq + at.t;
+          float4* p4 = reinterpret_cast<float4*>(a.part_o + pa * D + half * HD + c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            p4[e] = make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
+        } else {
+          uint4* p4 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at.head * a.o_hs + at.t * a.o_ts +
+                                               half * HD + c);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              __nv_bfloat162 h2 = __floats2bfloat162_rn(o[8 * e + 2 * k] * f, o[8 * e + 2 * k + 1] * f);
+              v[k] = live ? *reinterpret_cast<uint32_t*>(&h2) : 0u;
+            }
+            p4[e] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
         }
+      }
+      if (has && half == 0) {
+        const float mn = m * 0.6931471805599453f;
+        if (a.splits > 1)
+          a.part_ml[(split * (int64_t)a.Hq + at.head) * a.nq + at.t] = make_float2(live ? mn : neg_inf(), l);
+        else if (a.lse)
+          a.lse[at.head * a.nq + at.t] = live ? mn + logf(l) : neg_inf();
       }
     }
   } else if (warp < kMmaWarp) {
@@ -593,47 +657,57 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       const uint64_t k_desc = tc::sw128_desc(tc::smem_u32(base + Lay::k));
       const uint64_t v_desc = tc::sw128_mn_desc(tc::smem_u32(base + Lay::v), Lay::v_tile);
       bool ok = true;
-      int st = 0, nst = 0;
-      uint32_t ph = 0, nph = 0;                           // of V tile j and of K tile j + 1
+      const int step = both ? 2 : 1;
+      int kst[2], vst[2], count[2];                       // stages of K and V, key tiles by row tile
+      uint32_t kph[2], vph[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        kst[w] = vst[w] = both ? w : 0;
+        kph[w] = vph[w] = 0;
+        count[w] = both ? (T - w + 1) >> 1 : T;
+      }
 #pragma unroll 1
-      for (int j = -1; j < T && ok; ++j) {                // P V of tile j (from 0 on), Q K^T of tile j + 1
-        const bool more = j + 1 < T;
-        const uint64_t vd = v_desc + ((st * Lay::v_tile) >> 4), kd = k_desc + ((nst * Lay::k_tile) >> 4);
-        ok = (j < 0 || tc::mbar_wait(&sm.v_full[st], ph, abort)) &&
-             (!more || tc::mbar_wait(&sm.k_full[nst], nph, abort));
+      for (int i = -1; i < count[0] && ok; ++i) {         // P V of tile i (from 0 on), Q K^T of tile i + 1
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {                     // unrolled: descriptors and columns are constants
-          if (w >= nt || !ok) break;
-          if (j >= 0) {
+        for (int w = 0; w < 2; ++w) {                     // unrolled: columns are constants
+          if (i >= 0 && i < count[w]) {
+            ok = tc::mbar_wait(&sm.v_full[vst[w]], vph[w], abort);
+            if (!ok) break;
+            const uint64_t vd = v_desc + ((vst[w] * Lay::v_tile) >> 4);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {        // 64 keys at a time, as their P lands
-              ok = tc::mbar_wait(&sm.p_full[w][half], j & 1, abort);
+            for (int c = 0; c < 2; ++c) {                 // 32 keys of both halves at a time, as their P lands
+              ok = tc::mbar_wait(&sm.p_full[w][c], i & 1, abort);
               if (!ok) break;
               tc::tc_fence_after();
 #pragma unroll
-              for (int k = 4 * half; k < 4 * half + 4; ++k)
-                mma_ts<kCta>(tmem + Lay::o_col + w * 128, tmem + Lay::s_col + w * 128 + k * 8, vd + ((k * 2048) >> 4),
-                             idesc_pv, j > 0 || k > 0 ? 1u : 0u);
+              for (int k = 0; k < 4; ++k) {
+                const int key = (k >> 1) * 64 + c * 32 + (k & 1) * 16;
+                mma_ts<kCta>(tmem + Lay::o_col + w * 128, tmem + Lay::s_col + w * 128 + (k >> 1) * 64 + c * 16 + (k & 1) * 8,
+                             vd + ((key * 128) >> 4), idesc_pv, i > 0 || c > 0 || k > 0 ? 1u : 0u);
+              }
             }
             if (!ok) break;
-            if (w == nt - 1) commit<kCta>(&sm.v_empty[st]);
-          } else {
-            ok = tc::mbar_wait(&sm.q_full[w], 0, abort);
+            if (w == 1 || both) commit<kCta>(&sm.v_empty[vst[w]]);
+            vst[w] += step;
+            if (vst[w] >= kStages) vst[w] -= kStages, vph[w] ^= 1;
+          }
+          if (i + 1 < count[w]) {
+            ok = (i >= 0 || tc::mbar_wait(&sm.q_full[both ? 0 : w], 0, abort)) &&
+                 tc::mbar_wait(&sm.k_full[kst[w]], kph[w], abort);
             if (!ok) break;
             tc::tc_fence_after();
-          }
-          if (more) {
+            const uint64_t qd = q_desc + (((both ? 0 : w) * Lay::q_tile) >> 4);
+            const uint64_t kd = k_desc + ((kst[w] * Lay::k_tile) >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              mma_ss<kCta>(tmem + Lay::s_col + w * 128,
-                           q_desc + ((w * Lay::q_tile + (k >> 2) * Lay::q_blk + (k & 3) * 32) >> 4),
+              mma_ss<kCta>(tmem + Lay::s_col + w * 128, qd + (((k >> 2) * Lay::q_blk + (k & 3) * 32) >> 4),
                            kd + (((k >> 2) * Lay::k_blk + (k & 3) * 32) >> 4), idesc_qk, k > 0 ? 1u : 0u);
             commit<kCta>(&sm.s_full[w]);
-            if (w == nt - 1) commit<kCta>(&sm.k_empty[nst]);
+            if (w == 1 || both) commit<kCta>(&sm.k_empty[kst[w]]);
+            kst[w] += step;
+            if (kst[w] >= kStages) kst[w] -= kStages, kph[w] ^= 1;
           }
         }
-        if (j >= 0 && ++st == kStages) st = 0, ph ^= 1;
-        if (++nst == kStages) nst = 0, nph ^= 1;
       }
       // the outputs are complete; and every issued product ends before TMEM is given back
       commit<kCta>(&sm.fin);

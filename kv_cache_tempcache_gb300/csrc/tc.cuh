@@ -217,6 +217,17 @@ __device__ __forceinline__ bool named_bar_and(int id, int count, bool v) {
   return r != 0;
 }
 
+// Named barrier over `count` threads that also returns whether any of them passed v = true.
+__device__ __forceinline__ bool named_bar_or(int id, int count, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, %3, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
+}
+
 // Byte offset of 16-byte chunk `c` (0..7) of row `row` inside a 128-byte-swizzled
 // tile (1024-byte aligned): the chunk index is XOR-ed with row mod 8.
 __device__ __forceinline__ uint32_t sw128_off(int row, int c) {
