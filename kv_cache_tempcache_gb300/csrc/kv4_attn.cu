@@ -228,19 +228,25 @@ int splits_f32(int64_t blocks, int64_t cap) {
   return s < 1 ? 1 : (int)s;
 }
 
-// Splits for the tensor-core kernel, by a model of its time over a full cache: waves of CTAs,
-// each a fixed part and so much a key tile, plus the partials' way through memory and the
-// join.  It takes the fewest splits that are within 2 % of the best.
+// Splits for the tensor-core kernel, by a model of its time over a full cache: waves of CTAs
+// (pairs of them at d = 128), each a fixed part and so much a key tile; items with one row
+// tile, half as long a tile, fill the last wave's gaps; and with splits the partials' way through
+// memory and the join.  The fewest splits within 2 % of the best.  (Measured: 1.5 us a tile of
+// 128 keys and 512 rows at d = 128, 8 us around them.)
 int splits_tc(int d, int64_t rows, int Hkv, int64_t cap) {
   const int cta = d / 64;                 // CTAs that work as one (kv4_attn_tc.cu)
-  const int64_t slots = sm_count() / cta, items = (rows + 256 * cta - 1) / (256 * cta) * Hkv, tiles = (cap + 127) / 128;
-  const double tile = (rows > 128 * cta ? 1.3 : 0.9) * (d == 128 ? 1.0 : 0.7), fixed = 6.0;
+  const int64_t slots = sm_count() / cta, tiles = (cap + 127) / 128;
+  const int64_t half = (rows - 1) % (256 * cta) < 128 * cta ? Hkv : 0;
+  const int64_t full = (rows + 256 * cta - 1) / (256 * cta) * Hkv - half;
+  const double tile = 1.5, fixed = 8.0;
   auto cost = [&](int64_t s) {
-    const double waves = (double)((items * s + slots - 1) / slots);
+    const int64_t waves = (full * s + slots - 1) / slots, gaps = 2 * (waves * slots - full * s);
+    const int64_t rest = half * s > gaps ? (half * s - gaps + slots - 1) / slots : 0;
+    const double keys = (double)((tiles + s - 1) / s) * tile;
     const double join = s > 1 ? 4.0 + 2e-6 * s * rows * Hkv * (d + 2) * 4 / 4.0 : 0.0;
-    return waves * (fixed + (double)((tiles + s - 1) / s) * tile) + join;
+    return waves * (fixed + keys) + rest * (fixed + 0.6 * keys) + join;
   };
-  int64_t most = (4 * slots + items - 1) / items;
+  int64_t most = (4 * slots + full + half - 1) / (full + half);
   if (most > tiles) most = tiles;
   if (most > kKv4MaxSplits) most = kKv4MaxSplits;
   double best = cost(1);

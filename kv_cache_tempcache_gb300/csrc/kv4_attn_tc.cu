@@ -8,9 +8,9 @@
 //                      row tile 0, 8-11 and 12-15 of row tile 1): logits from TMEM, exponentials
 //                      against a reference that is moved, and the sums rescaled, only when a P
 //                      would pass 2^15, P as fp16 over the consumed logits in TMEM, the output;
-//   warps 16-19        unpack K and V: packed tiles (three on their way, brought by bulk copies that
-//                      warp 21 issues) into rings of 128-byte-swizzled fp16 tiles;
-//   warp 20            owns TMEM and issues tcgen05.mma from one thread (of the pair's first CTA):
+//   warps 16-19, 20-23 unpack K, V: packed tiles (four on their way, brought by bulk copies that
+//                      warp 25 issues) into rings of 128-byte-swizzled fp16 tiles;
+//   warp 24            owns TMEM and issues tcgen05.mma from one thread (of the pair's first CTA):
 //                      S = Q K^T of both row tiles, O += P V (P from TMEM).
 // The order of issue is PV0(j) QK0(j+1) PV1(j) QK1(j+1): while the softmax of one row tile
 // runs, the tensor cores work for the other, so a logit buffer a tile is enough and two
@@ -50,13 +50,13 @@ namespace {
 constexpr int kRT = 128;               // rows of a row tile in a CTA
 constexpr int kKT = 128;               // keys of a tile
 constexpr int kStages = 3;             // fp16 tiles of K and of V
-constexpr int kIn = 3;                 // packed tiles on their way
-constexpr int kSoftWarps = 16, kUnpackWarps = 4;
+constexpr int kIn = 4;                 // packed tiles on their way
+constexpr int kSoftWarps = 16, kUnpackWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kUnpackWarps;
-constexpr int kThreadsT = 768;         // the last warpgroup: MMA warp, copy warp, two idle ones
-// Registers: 768 threads x 80 at launch = 61,440 = 512 softmax threads x 96 + 256 others x 48.
-constexpr int kRegsSoft = 96, kRegsRest = 48;
-static_assert(512 * kRegsSoft + 256 * kRegsRest <= kThreadsT * 80, "the launch's registers bound the shares");
+constexpr int kThreadsT = 896;         // the last warpgroup: MMA warp, copy warp, two idle ones
+// Registers: 896 threads x 72 at launch = 64,512 >= 512 softmax threads x 88 + 384 others x 48.
+constexpr int kRegsSoft = 88, kRegsRest = 48;
+static_assert(512 * kRegsSoft + 384 * kRegsRest <= kThreadsT * 72, "the launch's registers bound the shares");
 
 struct alignas(16) Kv4Ctl {
   uint64_t in_full[kIn], in_empty[kIn];                // packed tiles: K 0, V 0, K 1, V 1, ...
@@ -279,13 +279,17 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
   const int rank = kCta == 2 ? (int)cta_rank() : 0;
 
   // the work item (the same for both CTAs of a pair): KV head, row tiles, split of the keys.
-  // The rows that see most keys (the last ones of a call in blocks) start first.
-  int64_t u = blockIdx.x / kCta;
-  const int split = (int)(u % a.splits);
-  u /= a.splits;
-  const int rt = row_tiles - 1 - (int)(u % row_tiles);
-  const int h = (int)(u / row_tiles);
+  // The rows that see most keys (the last ones of a call in blocks) start first, but a last
+  // item with one row tile, which takes half as long, goes to the end, where it fills gaps.
   const int64_t rows = (int64_t)(a.Hq / a.Hkv) * a.nq;
+  const bool odd = row_tiles > 1 && (rows - 1) % (2 * kRT * kCta) < kRT * kCta;
+  const int full_tiles = row_tiles - odd;
+  uint32_t u = blockIdx.x / kCta;
+  const int split = (int)(u % (uint32_t)a.splits);
+  u /= (uint32_t)a.splits;
+  const bool last = u >= (uint32_t)(a.Hkv * full_tiles);
+  const int h = (int)(last ? u - (uint32_t)(a.Hkv * full_tiles) : u / (uint32_t)full_tiles);
+  const int rt = last ? full_tiles : full_tiles - 1 - (int)(u % (uint32_t)full_tiles);
   const int64_t r0 = (int64_t)rt * (2 * kRT * kCta);
   const int64_t rlast = (r0 + 2 * kRT * kCta < rows ? r0 + 2 * kRT * kCta : rows) - 1;
   const int nt = rlast - r0 >= kRT * kCta ? 2 : 1;      // row tiles with rows
@@ -455,10 +459,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
         tc::named_bar(pair_bar, 64);                      // all of O is rescaled before either half's P goes
         tc::tc_fence_after();
       }
-      // P over the logits' own columns: 32 logits are read again and become 16 columns, over
-      // logits that have been read.  A loop, not unrolled: straight-line code for all 64 was
-      // slower, waiting for instructions.
-#pragma unroll 1
+      // P over the logits' own columns: 32 logits are read again (held since the maximum, 64 took
+      // registers that the loads and exponentials need to overlap) and become 16 columns, over
+      // logits that have been read
+#pragma unroll
       for (int c = 0; c < 2; ++c) {
         float x[32];
         tc::tmem_ld32(s_addr + (uint32_t)(32 * c), x);
@@ -571,12 +575,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     // hit 8 different bank groups of the swizzled tile.
     const int t = threadIdx.x & 127;
     constexpr int KP = D / 32;                            // runs of a row of K
-    // K and V tiles take turns through one copy of the code, kept small: the softmax warps'
-    // straight-line code shares the instruction caches with it
+    const bool isv = warp >= kSoftWarps + 4;              // warps 16-19: K, 20-23: V
 #pragma unroll 1
-    for (int n = 0; n < 2 * T; ++n) {
+    for (int n = isv; n < 2 * T; n += 2) {
       const int j = n >> 1, st = j % kStages, in = n % kIn;
-      const bool isv = n & 1;
       uint64_t* empty = isv ? &sm.v_empty[st] : &sm.k_empty[st];
       uint64_t* full = isv ? &sm.v_full[st] : &sm.k_full[st];
       const int part = isv || KP == 2 ? t & 1 : t & 3, row0 = isv || KP == 2 ? t >> 1 : t >> 2;
