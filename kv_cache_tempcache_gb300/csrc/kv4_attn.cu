@@ -228,6 +228,17 @@ int splits_f32(int64_t blocks, int64_t cap) {
   return s < 1 ? 1 : (int)s;
 }
 
+// Rows of a KV head that take the few-rows kernel (kv4_attn_few.cu).
+constexpr int64_t kFewRows = 16;
+
+// Splits for it: one CTA a multiprocessor, but none under 512 keys (64 a warp).
+int splits_few(int Hkv, int64_t cap) {
+  const int64_t want = sm_count() / Hkv, most = cap / 512;
+  int64_t s = want < most ? want : most;
+  if (s > kKv4MaxSplits) s = kKv4MaxSplits;
+  return s < 1 ? 1 : (int)s;
+}
+
 // Splits for the tensor-core kernel, by a model of its time over a full cache: waves of CTAs
 // (pairs of them at d = 128), each a fixed part and so much a key tile; items with one row
 // tile, half as long a tile, fill the last wave's gaps; and with splits the partials' way through
@@ -260,7 +271,7 @@ int splits_tc(int d, int64_t rows, int Hkv, int64_t cap) {
 
 int kv4_attn_splits(int dtype, int d, int Hq, int Hkv, int64_t nq, int64_t cap) {
   const int64_t rows = (int64_t)(Hq / Hkv) * nq;
-  if (dtype == FASTAR_BF16) return splits_tc(d, rows, Hkv, cap);
+  if (dtype == FASTAR_BF16) return rows <= kFewRows ? splits_few(Hkv, cap) : splits_tc(d, rows, Hkv, cap);
   return splits_f32((rows + kRows - 1) / kRows * Hkv, cap);
 }
 
@@ -280,7 +291,8 @@ cudaError_t launch_kv4_attn(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStrea
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * a.Hq * a.nq * d);
   }
   if (dtype == FASTAR_F32) return d == 128 ? f32_go<128>(a, s) : f32_go<64>(a, s);
-  const cudaError_t e = launch_kv4_attn_tc(d, a, s);
+  const bool few = (int64_t)(a.Hq / a.Hkv) * a.nq <= kFewRows;
+  const cudaError_t e = few ? launch_kv4_attn_few(d, a, s) : launch_kv4_attn_tc(d, a, s);
   if (e != cudaSuccess || a.splits == 1) return e;
   return d == 128 ? join_go<__nv_bfloat16, 128>(a, s) : join_go<__nv_bfloat16, 64>(a, s);
 }
