@@ -177,32 +177,46 @@ __global__ void __launch_bounds__(kWarpsW * 32, 1) kv4_attn_few_kernel(const Kv4
     const uint8_t* st = ring + (i % kStagesW) * Lay::stage;
     if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[i % kStagesW], (i / kStagesW) & 1, abort))) break;
     const int nk = len - key < kKeysW ? (int)(len - key) : kKeysW;
-    // ---- S = Q K^T: 8 keys at a time, a lane's share of key g of them ----
+    // ---- S = Q K^T: a lane's share of key g of 8; two times 8 keys side by side and two sums
+    // each, so that four products are in flight ----
     float s[8][4];
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-      const int k = n * 8 + g;
-      uint32_t b[D / 8];
-      if (D == 128) {
-        const uint4 c = reinterpret_cast<const uint4*>(st)[k * 4 + t];
-        uint32_t sc = reinterpret_cast<const uint16_t*>(st + 2 * Lay::codes)[k * 4 + t];
-        if (k >= nk) sc = 0;               // rows behind the length count as 0, whatever lies there
-        const uint32_t s0 = kv4::scale_f16x2(sc), s1 = kv4::scale_f16x2(sc >> 8);
-        kv4::unpack8(c.x, s0, b);
-        kv4::unpack8(c.y, s0, b + 4);
-        kv4::unpack8(c.z, s1, b + 8 % (D / 8));
-        kv4::unpack8(c.w, s1, b + 12 % (D / 8));
-      } else {
-        const uint2 c = reinterpret_cast<const uint2*>(st)[k * 4 + t];
-        uint32_t sc = (st + 2 * Lay::codes)[k * 4 + t];
-        if (k >= nk) sc = 0;
-        const uint32_t s0 = kv4::scale_f16x2(sc);
-        kv4::unpack8(c.x, s0, b);
-        kv4::unpack8(c.y, s0, b + 4);
-      }
+    for (int n = 0; n < 8; n += 2) {
+      uint32_t b[2][D / 8];
 #pragma unroll
-      for (int q = 0; q < D / 16; ++q) mma16816(s[n], qa[q], b[2 * q], b[2 * q + 1]);
+      for (int e = 0; e < 2; ++e) {
+        const int k = (n + e) * 8 + g;
+        if (D == 128) {
+          const uint4 c = reinterpret_cast<const uint4*>(st)[k * 4 + t];
+          uint32_t sc = reinterpret_cast<const uint16_t*>(st + 2 * Lay::codes)[k * 4 + t];
+          if (k >= nk) sc = 0;             // rows behind the length count as 0, whatever lies there
+          const uint32_t s0 = kv4::scale_f16x2(sc), s1 = kv4::scale_f16x2(sc >> 8);
+          kv4::unpack8(c.x, s0, b[e]);
+          kv4::unpack8(c.y, s0, b[e] + 4);
+          kv4::unpack8(c.z, s1, b[e] + 8 % (D / 8));
+          kv4::unpack8(c.w, s1, b[e] + 12 % (D / 8));
+        } else {
+          const uint2 c = reinterpret_cast<const uint2*>(st)[k * 4 + t];
+          uint32_t sc = (st + 2 * Lay::codes)[k * 4 + t];
+          if (k >= nk) sc = 0;
+          const uint32_t s0 = kv4::scale_f16x2(sc);
+          kv4::unpack8(c.x, s0, b[e]);
+          kv4::unpack8(c.y, s0, b[e] + 4);
+        }
+      }
+      float u[2][2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) u[e][0][x] = u[e][1][x] = 0.f;
+#pragma unroll
+      for (int q = 0; q < D / 16; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) mma16816(u[e][q & 1], qa[q], b[e][2 * q], b[e][2 * q + 1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[n + e][x] = u[e][0][x] + u[e][1][x];
     }
     // ---- masks, reference, P ----
     if (see[0] - key < kKeysW || see[1] - key < kKeysW) {
