@@ -428,50 +428,64 @@ def fastar_sinusoidal_embedding(t, out, stream=None):
 
 # ---- the 4-bit cache, and the norm and rotation before it -------------------------------------
 
-def _expect(name, t, dtype, shape=None):
-    """Refuses what a kernel would misread: another type, shape or layout."""
-    if t.dtype != dtype:
+# Every check below refuses what a kernel would misread.  They run on each call of a step that
+# may be a few microseconds of device time, so they ask each tensor for as little as they can.
+
+def _wrong(name, t, dtype, shape):
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None:
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _dense(name, t, dtype, shape):
+    """Address of a contiguous tensor of this type and shape (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _wrong(name, t, dtype, shape)
     return t.data_ptr()
 
 
-def _expect_here(*tensors):
-    """Refuses tensors that are not on the current CUDA device (the one the call runs on)."""
-    for t in tensors:
-        if t is not None and not (t.is_cuda and t.device.index == torch.cuda.current_device()):
-            raise ValueError(f"tensors must be on the current CUDA device, not on {t.device}")
-
-
-def _expect_opt(name, t, dtype, shape=None):
-    return None if t is None else _expect(name, t, dtype, shape)
-
-
-def _expect_rows(name, t, dtype, shape):
-    """A [H, n, d] view of rows with a contiguous last dimension: (address, strides)."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    hs, ts = tok_strides(t)
-    # the stride of a dimension of one element says nothing (torch may give any)
-    H, n, d = t.shape
+def _rows(name, t, dtype, shape):
+    """A [H, n, d] view of rows with a contiguous last dimension: (address, head stride, token
+    stride).  The stride of a dimension of one element says nothing (torch may give any)."""
+    if t.dtype is not dtype or t.shape != shape:
+        _wrong(name, t, dtype, shape)
+    hs, ts, cs = t.stride()
+    if cs != 1:
+        raise ValueError("token tensors must be [H, N, d] views with a contiguous last dimension")
+    H, n, d = shape
     if n <= 1:
         ts = d
     if H <= 1:
         hs = n * d
-    return _expect(name, t, dtype), hs, ts
+    return t.data_ptr(), hs, ts
 
 
-def _expect_kv4(name, codes, scales, H, d):
-    """A [H, cap, d / 2] array of codes and its [H, cap, d / 16] scales."""
-    if codes.dim() != 3:
-        raise ValueError(f"{name}_codes must be [H, cap, d / 2]")
-    cap = codes.shape[1]
-    return (_expect(name + "_codes", codes, torch.uint8, (H, cap, d // 2)),
-            _expect(name + "_scales", scales, torch.uint8, (H, cap, d // 16)), cap)
+def _launch(name, stream, tensors, *args):
+    """Calls an entry point on the current device, where every tensor has to be."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            g = t.get_device()
+            if dev is None:
+                dev = g
+            elif g != dev:
+                raise ValueError("tensors must be on the current CUDA device, all of them")
+    if dev is not None and (dev < 0 or dev != torch._C._cuda_getDevice()):
+        raise ValueError("tensors must be on the current CUDA device")
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    rc = getattr(_lib or load(), name)(*args, s)
+    if rc != OK:
+        raise FastarError(name, rc, load().fastar_last_cuda_error().decode() if rc == ECUDA else None)
+
+
+def _rows3(t, name):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be a [H, N, d] view")
+    return t.shape
 
 
 def fastar_qk_norm_rope(q, k, q_out, k_out, wq=None, wk=None, eps=1e-6, axes=(0, 0, 0), pos=None, t0=0, t0_dev=None,
@@ -479,52 +493,57 @@ def fastar_qk_norm_rope(q, k, q_out, k_out, wq=None, wk=None, eps=1e-6, axes=(0,
     """RMS norm of every head (weights given) and rotary positions of three axes: q [Hq, n, d]
     -> q_out, k [Hk, n, d] -> k_out (k and k_out None: q alone).  axes: the channels that turn
     with the frame, the row and the column; pos [n, 3] int32, or the grid's positions."""
-    Hq, n, d = q.shape
+    shape = _rows3(q, "q")
+    Hq, n, d = shape
     dt = q.dtype
     code = dtype_code(dt)
-    qa = _expect_rows("q", q, dt, (Hq, n, d)) + _expect_rows("q_out", q_out, dt, (Hq, n, d))
+    qp, qhs, qts = _rows("q", q, dt, shape)
+    qo, qohs, qots = _rows("q_out", q_out, dt, shape)
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
-    Hk, ka = 0, (None, 0, 0, None, 0, 0)
+    Hk, kp, khs, kts, ko, kohs, kots = 0, None, 0, 0, None, 0, 0
     if k is not None:
         Hk = k.shape[0]
-        ka = _expect_rows("k", k, dt, (Hk, n, d)) + _expect_rows("k_out", k_out, dt, (Hk, n, d))
-    _expect_here(q, q_out, k, k_out, wq, wk, pos, t0_dev)
-    _call("fastar_qk_norm_rope", code, n, d, Hq, *qa, Hk, *ka, _expect_opt("wq", wq, torch.float32, (d,)),
-          _expect_opt("wk", wk, torch.float32, (d,)), float(eps), int(axes[0]), int(axes[1]), int(axes[2]),
-          _expect_opt("pos", pos, torch.int32, (n, 3)), int(t0), _expect_opt("t0_dev", t0_dev, torch.int32, (1,)),
-          int(grid[0]), int(grid[1]), float(theta), stream_handle(stream))
+        kp, khs, kts = _rows("k", k, dt, (Hk, n, d))
+        ko, kohs, kots = _rows("k_out", k_out, dt, (Hk, n, d))
+    f32, i32 = torch.float32, torch.int32
+    _launch("fastar_qk_norm_rope", stream, (q, q_out, k, k_out, wq, wk, pos, t0_dev), code, n, d, Hq, qp, qhs, qts, qo,
+            qohs, qots, Hk, kp, khs, kts, ko, kohs, kots, _dense("wq", wq, f32, (d,)), _dense("wk", wk, f32, (d,)),
+            eps, axes[0], axes[1], axes[2], _dense("pos", pos, i32, (n, 3)), t0, _dense("t0_dev", t0_dev, i32, (1,)),
+            grid[0], grid[1], theta)
 
 
 def fastar_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, at=None, len_out=None, dev_status=None, k_exp=None,
                       v_exp=None, stream=None):
     """Rows k, v [H, n, d] into the 4-bit cache (codes [H, cap, d / 2], scales [H, cap, d / 16],
     uint8) from row at[h] on (int32 [H]; None: 0); len_out[h] = at[h] + n."""
-    H, n, d = k.shape
-    code = dtype_code(k.dtype)
-    kp, khs, kts = _expect_rows("k", k, k.dtype, (H, n, d))
-    vp, vhs, vts = _expect_rows("v", v, k.dtype, (H, n, d))
-    kc, ks, cap = _expect_kv4("k", k_codes, k_scales, H, d)
-    vc, vs, vcap = _expect_kv4("v", v_codes, v_scales, H, d)
-    if cap != vcap:
-        raise ValueError("K and V caches must have the same capacity")
-    i32 = torch.int32
-    _expect_here(k, v, k_codes, k_scales, v_codes, v_scales, at, len_out, dev_status, k_exp, v_exp)
-    _call("fastar_kv4_append", code, H, n, d, kp, khs, kts, vp, vhs, vts, _expect_opt("k_exp", k_exp, i32, (H,)),
-          _expect_opt("v_exp", v_exp, i32, (H,)), _expect_opt("at", at, i32, (H,)), kc, ks, vc, vs, cap,
-          _expect_opt("len_out", len_out, i32, (H,)), _expect_opt("dev_status", dev_status, i32, (1,)),
-          stream_handle(stream))
+    shape = _rows3(k, "k")
+    H, n, d = shape
+    dt, u8, i32 = k.dtype, torch.uint8, torch.int32
+    code = dtype_code(dt)
+    kp, khs, kts = _rows("k", k, dt, shape)
+    vp, vhs, vts = _rows("v", v, dt, shape)
+    cap = _rows3(k_codes, "k_codes")[1]
+    cs, ss = (H, cap, d // 2), (H, cap, d // 16)
+    _launch("fastar_kv4_append", stream,
+            (k, v, k_codes, k_scales, v_codes, v_scales, at, len_out, dev_status, k_exp, v_exp), code, H, n, d, kp, khs,
+            kts, vp, vhs, vts, _dense("k_exp", k_exp, i32, (H,)), _dense("v_exp", v_exp, i32, (H,)),
+            _dense("at", at, i32, (H,)), _dense("k_codes", k_codes, u8, cs), _dense("k_scales", k_scales, u8, ss),
+            _dense("v_codes", v_codes, u8, cs), _dense("v_scales", v_scales, u8, ss), cap,
+            _dense("len_out", len_out, i32, (H,)), _dense("dev_status", dev_status, i32, (1,)))
 
 
 def fastar_kv4_read(codes, scales, first, out, exps=None, stream=None):
     """The values of rows first .. first + n of a 4-bit cache -> out [H, n, d]."""
-    H, n, d = out.shape
+    shape = _rows3(out, "out")
+    H, n, d = shape
     code = dtype_code(out.dtype)
-    cp, sp, cap = _expect_kv4("cache", codes, scales, H, d)
-    op, ohs, ots = _expect_rows("out", out, out.dtype, (H, n, d))
-    _expect_here(codes, scales, out, exps)
-    _call("fastar_kv4_read", code, H, n, d, cp, sp, _expect_opt("exps", exps, torch.int32, (H,)), cap, int(first), op,
-          ohs, ots, stream_handle(stream))
+    op, ohs, ots = _rows("out", out, out.dtype, shape)
+    cap = _rows3(codes, "codes")[1]
+    u8 = torch.uint8
+    _launch("fastar_kv4_read", stream, (codes, scales, out, exps), code, H, n, d,
+            _dense("codes", codes, u8, (H, cap, d // 2)), _dense("scales", scales, u8, (H, cap, d // 16)),
+            _dense("exps", exps, torch.int32, (H,)), cap, int(first), op, ohs, ots)
 
 
 def fastar_kv4_attn(q, k_codes, k_scales, v_codes, v_scales, lens, scale, out, lse=None, block=0, k_exp=None,
@@ -533,27 +552,26 @@ def fastar_kv4_attn(q, k_codes, k_scales, v_codes, v_scales, lens, scale, out, l
     (Hq a multiple of Hkv); block > 0: the tokens are the cache's last nq rows and see no block
     of that many tokens later than their own.  workspace: workspace_bytes(OP_KV4_ATTN, Hq, nq,
     cap, d, Hkv) bytes (None: the keys are not split)."""
-    Hq, nq, d = q.shape
-    code = dtype_code(q.dtype)
-    Hkv = k_codes.shape[0]
-    qp, qhs, qts = _expect_rows("q", q, q.dtype, (Hq, nq, d))
-    op, ohs, ots = _expect_rows("out", out, q.dtype, (Hq, nq, d))
-    kc, ks, cap = _expect_kv4("k", k_codes, k_scales, Hkv, d)
-    vc, vs, vcap = _expect_kv4("v", v_codes, v_scales, Hkv, d)
-    if cap != vcap:
-        raise ValueError("K and V caches must have the same capacity")
-    i32 = torch.int32
-    nb = 0
+    shape = _rows3(q, "q")
+    Hq, nq, d = shape
+    dt, u8, i32 = q.dtype, torch.uint8, torch.int32
+    code = dtype_code(dt)
+    qp, qhs, qts = _rows("q", q, dt, shape)
+    op, ohs, ots = _rows("out", out, dt, shape)
+    Hkv, cap, _ = _rows3(k_codes, "k_codes")
+    cs, ss = (Hkv, cap, d // 2), (Hkv, cap, d // 16)
+    wp, nb = None, 0
     if workspace is not None:
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        nb = workspace.numel() * workspace.element_size()
-    _expect_here(q, k_codes, k_scales, v_codes, v_scales, lens, out, lse, k_exp, v_exp, dev_status, workspace)
-    _call("fastar_kv4_attn", qp, code, Hq, Hkv, nq, d, qhs, qts, kc, ks, vc, vs,
-          _expect_opt("k_exp", k_exp, i32, (Hkv,)), _expect_opt("v_exp", v_exp, i32, (Hkv,)), cap,
-          _expect("lens", lens, i32, (Hkv,)), int(block), float(scale), op, ohs, ots,
-          _expect_opt("lse", lse, torch.float32, (Hq, nq)), _expect_opt("dev_status", dev_status, i32, (1,)),
-          None if workspace is None else _expect("workspace", workspace, workspace.dtype), nb, stream_handle(stream))
+        wp, nb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch("fastar_kv4_attn", stream,
+            (q, out, k_codes, k_scales, v_codes, v_scales, lens, lse, k_exp, v_exp, dev_status, workspace), qp, code,
+            Hq, Hkv, nq, d, qhs, qts, _dense("k_codes", k_codes, u8, cs), _dense("k_scales", k_scales, u8, ss),
+            _dense("v_codes", v_codes, u8, cs), _dense("v_scales", v_scales, u8, ss),
+            _dense("k_exp", k_exp, i32, (Hkv,)), _dense("v_exp", v_exp, i32, (Hkv,)), cap,
+            _dense("lens", lens, i32, (Hkv,)), block, scale, op, ohs, ots,
+            _dense("lse", lse, torch.float32, (Hq, nq)), _dense("dev_status", dev_status, i32, (1,)), wp, nb)
 
 
 def fastar_dense_append(k_cur, v_cur, k_cache, v_cache, at, stream=None):

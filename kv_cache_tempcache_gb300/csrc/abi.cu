@@ -774,10 +774,7 @@ int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d
   if ((rc = check_tok(out, dtype, d, o_head_stride, o_token_stride, nq, Hq))) return rc;
   if ((rc = check_kv4(k_codes, k_scales)) || (rc = check_kv4(v_codes, v_scales))) return rc;
   if (!len) return FASTAR_EINVAL;
-  if (workspace) {
-    const size_t need = fastar::kv4_attn_workspace(d, Hq, Hkv, nq, cap);
-    if (workspace_bytes < need || !aligned16(workspace)) return FASTAR_EWORKSPACE;
-  }
+  if (workspace && !aligned16(workspace)) return FASTAR_EWORKSPACE;
   fastar::Kv4AttnArgs a{};
   a.Hq = Hq;
   a.Hkv = Hkv;
@@ -798,7 +795,9 @@ int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d
   a.o_ts = o_token_stride;
   a.lse = lse;
   a.status = dev_status;
-  return cuda_rc(fastar::launch_kv4_attn(dtype, d, a, workspace, stream));
+  cudaError_t err = cudaSuccess;
+  if (!fastar::launch_kv4_attn(dtype, d, a, workspace, workspace_bytes, stream, &err)) return FASTAR_EWORKSPACE;
+  return cuda_rc(err);
 }
 
 }  // extern "C"

@@ -226,7 +226,8 @@ struct Kv4AttnArgs {
 // Splits of the keys for these sizes, and the bytes of their partials (0: one split).
 int kv4_attn_splits(int dtype, int d, int Hq, int Hkv, int64_t nq, int64_t cap);
 size_t kv4_attn_workspace(int d, int Hq, int Hkv, int64_t nq, int64_t cap);
-cudaError_t launch_kv4_attn(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStream_t s);
+// False if the workspace is too small for the call's splits (nothing is enqueued).
+bool launch_kv4_attn(int dtype, int d, Kv4AttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s, cudaError_t* err);
 cudaError_t launch_kv4_attn_tc(int d, const Kv4AttnArgs& a, cudaStream_t s);
 cudaError_t launch_kv4_attn_few(int d, const Kv4AttnArgs& a, cudaStream_t s);   // up to 16 rows a KV head
 

@@ -251,7 +251,7 @@ int splits_tc(int d, int64_t rows, int Hkv, int64_t cap) {
   const int64_t full = (rows + 256 * cta - 1) / (256 * cta) * Hkv - half;
   const double tile = 1.5, fixed = 8.0;
   auto cost = [&](int64_t s) {
-    const int64_t waves = (full * s + slots - 1) / slots, gaps = 2 * (waves * slots - full * s);
+    const int64_t waves = (full * s + slots - 1) / slots, gaps = (waves * slots - full * s) * 8 / 5;
     const int64_t rest = half * s > gaps ? (half * s - gaps + slots - 1) / slots : 0;
     const double keys = (double)((tiles + s - 1) / s) * tile;
     const double join = s > 1 ? 4.0 + 2e-6 * s * rows * Hkv * (d + 2) * 4 / 4.0 : 0.0;
@@ -262,9 +262,27 @@ int splits_tc(int d, int64_t rows, int Hkv, int64_t cap) {
   if (most > kKv4MaxSplits) most = kKv4MaxSplits;
   double best = cost(1);
   int64_t pick = 1;
-  for (int64_t s = 2; s <= most; ++s)
-    if (cost(s) < 0.98 * best) best = cost(s), pick = s;
+  for (int64_t s = 2; s <= most; s += 1 + s / 8) {   // every few: this runs on each call
+    const double c = cost(s);
+    if (c < 0.98 * best) best = c, pick = s;
+  }
   return (int)pick;
+}
+
+size_t partial_bytes(int splits, int d, int Hq, int64_t nq) {
+  return splits == 1 ? 0 : (size_t)splits * Hq * nq * (d + 2) * sizeof(float);
+}
+
+cudaError_t run(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStream_t s) {
+  if (a.splits > 1) {
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * a.Hq * a.nq * d);
+  }
+  if (dtype == FASTAR_F32) return d == 128 ? f32_go<128>(a, s) : f32_go<64>(a, s);
+  const bool few = (int64_t)(a.Hq / a.Hkv) * a.nq <= kFewRows;
+  const cudaError_t e = few ? launch_kv4_attn_few(d, a, s) : launch_kv4_attn_tc(d, a, s);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  return d == 128 ? join_go<__nv_bfloat16, 128>(a, s) : join_go<__nv_bfloat16, 64>(a, s);
 }
 
 }  // namespace
@@ -281,20 +299,14 @@ size_t kv4_attn_workspace(int d, int Hq, int Hkv, int64_t nq, int64_t cap) {
     const int x = kv4_attn_splits(dt, d, Hq, Hkv, nq, cap);
     s = x > s ? x : s;
   }
-  return s == 1 ? 0 : (size_t)s * Hq * nq * (d + 2) * sizeof(float);
+  return partial_bytes(s, d, Hq, nq);
 }
 
-cudaError_t launch_kv4_attn(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStream_t s) {
+bool launch_kv4_attn(int dtype, int d, Kv4AttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s, cudaError_t* err) {
   a.splits = ws ? kv4_attn_splits(dtype, d, a.Hq, a.Hkv, a.nq, a.cap) : 1;
-  if (a.splits > 1) {
-    a.part_o = static_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * a.Hq * a.nq * d);
-  }
-  if (dtype == FASTAR_F32) return d == 128 ? f32_go<128>(a, s) : f32_go<64>(a, s);
-  const bool few = (int64_t)(a.Hq / a.Hkv) * a.nq <= kFewRows;
-  const cudaError_t e = few ? launch_kv4_attn_few(d, a, s) : launch_kv4_attn_tc(d, a, s);
-  if (e != cudaSuccess || a.splits == 1) return e;
-  return d == 128 ? join_go<__nv_bfloat16, 128>(a, s) : join_go<__nv_bfloat16, 64>(a, s);
+  if (a.splits > 1 && ws_bytes < partial_bytes(a.splits, d, a.Hq, a.nq)) return false;
+  *err = run(dtype, d, a, ws, s);
+  return true;
 }
 
 }  // namespace fastar
