@@ -172,23 +172,49 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnArgs a) {
   const int64_t rows = (int64_t)a.Hq * a.nq;
   pdl_wait();
   if (row >= rows) return;
+  // lane s % 32 reads split s's maximum and sum; then the outputs, eight splits' loads at a time
+  constexpr int kPer = kKv4MaxSplits / 32;
+  float2 ml[kPer];
   float m = neg_inf();
-  for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, a.part_ml[s * rows + row].x);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    ml[i] = make_float2(neg_inf(), 0.f);
+    if (32 * i + lane < a.splits) ml[i] = a.part_ml[(32 * i + lane) * rows + row];
+    if (ml[i].y != 0.f) m = fmaxf(m, ml[i].x);
+  }
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   const float ref = m == neg_inf() ? 0.f : m;
   float l = 0.f, o[CPL];
 #pragma unroll
   for (int i = 0; i < CPL; ++i) o[i] = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 ml = a.part_ml[s * rows + row];
-    if (ml.y == 0.f) continue;          // a split in which the row sees no key: o is not written
-    const float w = expf(ml.x - ref);
-    l = fmaf(w, ml.y, l);
-    const float* p = a.part_o + (s * rows + row) * D + lane * CPL;
 #pragma unroll
-    for (int i = 0; i < CPL; ++i) o[i] = fmaf(w, p[i], o[i]);
+  for (int i = 0; i < kPer; ++i) {
+    if (32 * i >= a.splits) break;
+    const float w = ml[i].y != 0.f ? expf(ml[i].x - ref) : 0.f;
+    const int here = a.splits - 32 * i < 32 ? a.splits - 32 * i : 32;
+#pragma unroll 1
+    for (int s0 = 0; s0 < here; s0 += 8) {
+      float p[8][CPL], ws[8], ls[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const int src = s0 + s < 32 ? s0 + s : 31;
+        ls[s] = __shfl_sync(0xffffffffu, ml[i].y, src);
+        ws[s] = __shfl_sync(0xffffffffu, w, src);
+        // a split in which the row sees no key: its outputs are not written
+        const bool in = s0 + s < here && ls[s] != 0.f;
+        const float* src_o = a.part_o + ((32 * i + s0 + s) * rows + row) * D + lane * CPL;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) p[s][c] = in ? src_o[c] : 0.f;
+        if (!in) ws[s] = ls[s] = 0.f;
+      }
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        l = fmaf(ws[s], ls[s], l);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) o[c] = fmaf(ws[s], p[s][c], o[c]);
+      }
+    }
   }
   const bool live = l > 0.f || l != l;
   const int64_t head = row / a.nq, t = row - head * a.nq;

@@ -2,17 +2,21 @@
 // head, as in single-token steps.
 //
 // Bound: the cache's bytes.  A row tile of the tcgen05 kernel is 128 or 256 rows, so with a few
-// rows it spends most of its time unpacking for products that are nearly empty; here the 16
-// rows are one m16n8k16 product (mma.sync: its rate is not what bounds this), and the unpacked
-// codes go from registers straight into the product's operand, without shared memory between.
-//   S[16 rows, 8 keys] += Q[16, 16 channels] K^T,   O[16, 8 channels] += P[16, 16 keys] V
-// A product may sum its channels in any order as long as both operands agree, so lane t of a
-// quad takes channels t d/4 .. (t + 1) d/4 of a key: 16 consecutive bytes of codes at d = 128.
-// The columns of P V may be any channels: lane group g takes d/8 consecutive ones; the pairs
-// of keys that the operand wants side by side are made from two rows by byte permutes.
-// Each warp runs alone over every eighth block of 64 keys of its CTA's range: three blocks on
-// their way by bulk copies, its own reference, sums and outputs; the eight warps' results are
-// joined in shared memory, in warp order, at the end, and the CTAs' by the join kernel.
+// rows it spends most of its time unpacking for products that are nearly empty; here the rows
+// are the 8 columns (twice, above 8 rows) of m16n8k16 products (mma.sync: its rate is not what
+// bounds this), and the unpacked codes go from registers straight into the products' operands,
+// without shared memory between:
+//   S^T[16 keys, 8 rows] += K[16, 16 channels] Q^T,   O^T[16 channels, 8 rows] += V^T[16, 16 keys] P^T
+// P^T is S^T's registers after an 8 x 8 transpose (movmatrix).  A product may sum its channels in
+// any order as long as both operands agree, so lane t of a quad takes channels t d/4 .. of a key,
+// 16 consecutive bytes of codes at d = 128; and V^T's rows may be any channels: lane group g
+// takes d/8 consecutive ones, and the pairs of keys that the operand wants side by side are
+// paired as codes, before they are unpacked.
+// Each warp runs alone over its share of the CTA's blocks of 32 keys: three (six) blocks on
+// their way by bulk copies, its own reference, sums and outputs; the warps' results are joined in
+// shared memory, in warp order, at the end, and the CTAs' by the join kernel.
+// (With the rows as the products' 16 rows, half of them empty up to 8, 8 warps of 250 registers
+// waited for one another's latencies: one token over 131,071 rows of 8 heads 45 us.)
 // Queries, P and references as in the tcgen05 kernel (kv4_attn_tc.cu): fp16 rows at a power of
 // two, P in fp16 against a reference that moves only when a P would pass 2^15.
 #include <climits>
@@ -27,16 +31,19 @@ namespace fastar {
 
 namespace {
 
-constexpr int kWarpsW = 8, kKeysW = 64, kStagesW = 3;
+constexpr int kKeysW = 32;
 
-template <int D>
+// NR: groups of 8 rows.
+template <int D, int NR>
 struct FewLayout {
+  static constexpr int warps = NR == 1 ? 16 : 8, stages = NR == 1 ? 3 : 6;
   static constexpr int codes = kKeysW * D / 2, scales = kKeysW * D / 16;
   static constexpr int stage = 2 * (codes + scales);                 // K codes, V codes, K scales, V scales
-  static constexpr int ring = kWarpsW * kStagesW * stage;
-  static constexpr int red = kWarpsW * 16 * D * 4;                   // the joined outputs, over the ring
+  static constexpr int ring = warps * stages * stage;
+  static constexpr int red = warps * 8 * NR * D * 4;                 // the joined outputs, over the ring
   static constexpr int ctl = ring > red ? ring : red;
-  static constexpr int bytes = ctl + kWarpsW * kStagesW * 8 + kWarpsW * 16 * 8 + 16 + 128;
+  static constexpr int bytes = ctl + warps * stages * 8 + warps * 8 * NR * 8 + 16 + 128;
+  static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
 };
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -45,6 +52,23 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       "%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Eight bytes of codes as four fp16 pairs each (scaled): cvt takes a byte of a register at no cost.
+__device__ __forceinline__ void unpack_bytes(uint32_t w, uint32_t s2, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  uint32_t o[4];
+  kv4::unpack8(w, s2, o);
+  a = o[0], b = o[1], c = o[2], d = o[3];
+}
+// The codes of two keys, channel by channel side by side: even channels of the word, odd ones.
+__device__ __forceinline__ void pair_codes(uint32_t ka, uint32_t kb, uint32_t& even, uint32_t& odd) {
+  even = (ka & 0x0f0f0f0fu) | ((kb << 4) & 0xf0f0f0f0u);
+  odd = ((ka >> 4) & 0x0f0f0f0fu) | (kb & 0xf0f0f0f0u);
+}
+// The fp16 pair of two scale bytes (lo, hi), and one of them twice.
+__device__ __forceinline__ uint32_t scales_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
 }
 __device__ __forceinline__ float ex2w(float x) {
   float y;
@@ -60,290 +84,315 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   v = max(v, __shfl_xor_sync(0xffffffffu, v, 1));
   return max(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
-__device__ __forceinline__ float quad_maxf(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+// Over the eight lanes of equal t.
+__device__ __forceinline__ float group_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
 }
-__device__ __forceinline__ float quad_sum(float v) {
-  v += __shfl_xor_sync(0xffffffffu, v, 1);
-  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+__device__ __forceinline__ float group_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
+}
+// Lane (g, t) holds elements (g, 2t), (g, 2t + 1) of an 8 x 8 matrix of 16-bit values; gets (2t, g), (2t + 1, g).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
-// A thread's share of two query rows (channels t D/4 ..) as product operands: a[s] of step s;
-// returns each row's logit scale in log2 units.
+// A lane's share of query row r (channels t D/4 ..) as product operands: qb[s] of step s; returns
+// the row's logit scale in log2 units.
 template <int D>
-__device__ __forceinline__ void load_q(const Kv4AttnArgs& a, int h, int rows, int g, int t, uint32_t (*qa)[4], float* sl2) {
-  constexpr int CH = D / 4;                 // channels of this thread
-  const float ks = kv4::pow2i(kv4::head_exp(a.k_exp, h));
+__device__ __forceinline__ float load_q(const Kv4AttnArgs& a, int h, int rows, int r, int t, uint32_t (*qb)[2]) {
+  constexpr int CH = D / 4;                 // channels of this lane
+  uint32_t x[CH / 2];
+  uint32_t big = 0;
+  if (r < rows) {
+    const uint32_t nq = (uint32_t)a.nq, gh = (uint32_t)r / nq;
+    const int64_t head = h * (int64_t)(a.Hq / a.Hkv) + gh;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + head * a.q.hs +
+                                                      (int64_t)((uint32_t)r - gh * nq) * a.q.ts + t * CH);
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const int r = g + 8 * p;
-    uint32_t x[CH / 2];
-    uint32_t big = 0;
-    if (r < rows) {
-      const uint32_t nq = (uint32_t)a.nq, gh = (uint32_t)r / nq;
-      const int64_t head = h * (int64_t)(a.Hq / a.Hkv) + gh;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + head * a.q.hs +
-                                                        (int64_t)((uint32_t)r - gh * nq) * a.q.ts + t * CH);
-#pragma unroll
-      for (int i = 0; i < CH / 8; ++i) {
-        const uint4 u = src[i];
-        x[4 * i] = u.x, x[4 * i + 1] = u.y, x[4 * i + 2] = u.z, x[4 * i + 3] = u.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < CH / 2; ++i) x[i] = 0;
+    for (int i = 0; i < CH / 8; ++i) {
+      const uint4 u = src[i];
+      x[4 * i] = u.x, x[4 * i + 1] = u.y, x[4 * i + 2] = u.z, x[4 * i + 3] = u.w;
     }
+  } else {
 #pragma unroll
-    for (int i = 0; i < CH / 2; ++i) big = max(big, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
-    big = quad_max(big);
-    const int ex = (int)(big >> 7);
-    int qe = ex == 0 ? -126 - 12 : ex - 127 - 12;
-    if (qe < -120) qe = -120;
-    if (big == 0 || ex == 255) qe = 0;
-    const float down = kv4::pow2i(-qe);
-    sl2[p] = fmaxf(a.scale * kv4::pow2i(qe) * ks * 1.4426950408889634f, 1.2e-38f);
-#pragma unroll
-    for (int i = 0; i < CH / 2; ++i)        // pair i of the thread's channels: step i / 2, first or second pair
-      qa[i >> 1][p + 2 * (i & 1)] = pack_f16w(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xffff0000u) * down);
+    for (int i = 0; i < CH / 2; ++i) x[i] = 0;
   }
+#pragma unroll
+  for (int i = 0; i < CH / 2; ++i) big = max(big, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
+  big = quad_max(big);
+  const int ex = (int)(big >> 7);
+  int qe = ex == 0 ? -126 - 12 : ex - 127 - 12;
+  if (qe < -120) qe = -120;
+  if (big == 0 || ex == 255) qe = 0;
+  const float down = kv4::pow2i(-qe);
+#pragma unroll
+  for (int i = 0; i < CH / 2; ++i)          // pair i of the lane's channels: step i / 2, first or second pair
+    qb[i >> 1][i & 1] = pack_f16w(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xffff0000u) * down);
+  return fmaxf(a.scale * kv4::pow2i(qe) * kv4::pow2i(kv4::head_exp(a.k_exp, h)) * 1.4426950408889634f, 1.2e-38f);
 }
 
-// kTwo: more than 8 rows (else the product's upper 8 rows are empty and skipped).
-template <int D, bool kTwo>
-__global__ void __launch_bounds__(kWarpsW * 32, 1) kv4_attn_few_kernel(const Kv4AttnArgs a) {
-  using Lay = FewLayout<D>;
-  constexpr int NT = D / 8;                 // column tiles of O
-  constexpr int RH = kTwo ? 2 : 1;
+template <int D, int NR>
+__global__ void __launch_bounds__(FewLayout<D, NR>::warps * 32, 1) kv4_attn_few_kernel(const Kv4AttnArgs a) {
+  using Lay = FewLayout<D, NR>;
+  constexpr int W = Lay::warps, ST = Lay::stages, MT = D / 16;       // MT: row tiles of O^T
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~(uintptr_t)127);
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + Lay::ctl);
-  float2* wml = reinterpret_cast<float2*>(bars + kWarpsW * kStagesW);      // [warp][16]
-  int* abort_flag = reinterpret_cast<int*>(wml + kWarpsW * 16);
+  float2* wml = reinterpret_cast<float2*>(bars + W * ST);            // [warp][8 NR]
+  int* abort_flag = reinterpret_cast<int*>(wml + W * 8 * NR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int split = (int)(blockIdx.x % (uint32_t)a.splits), h = (int)(blockIdx.x / (uint32_t)a.splits);
   const int rows = (a.Hq / a.Hkv) * (int)a.nq;
+  // the last key any row sees: with blocks, that of the last token, which some row is: all of them
   const int64_t len = kv4::head_len(a.len, h, a.cap, a.status);
-  // the last key any row sees: with blocks, that of the last token, which some row is; that is len
   const uint32_t blocks = (uint32_t)((len + kKeysW - 1) / kKeysW);
   const uint32_t b0 = (uint32_t)((uint64_t)blocks * split / (uint32_t)a.splits);
   const uint32_t b1 = (uint32_t)((uint64_t)blocks * (split + 1) / (uint32_t)a.splits);
-  const int count = b0 + warp < b1 ? (int)((b1 - b0 - warp + kWarpsW - 1) / kWarpsW) : 0;   // this warp's blocks
+  const int count = b0 + warp < b1 ? (int)((b1 - b0 - warp + W - 1) / W) : 0;   // this warp's blocks
   pdl_trigger();                            // the join's CTAs may come and wait
 
-  uint64_t* full = bars + warp * kStagesW;
+  uint64_t* full = bars + warp * ST;
   if (lane == 0) {
-    for (int i = 0; i < kStagesW; ++i) tc::mbar_init(&full[i], 1);
+    for (int i = 0; i < ST; ++i) tc::mbar_init(&full[i], 1);
     if (warp == 0) *abort_flag = 0;
     tc::mbar_fence_init();
   }
-  uint8_t* ring = base + warp * kStagesW * Lay::stage;
+  uint8_t* ring = base + warp * ST * Lay::stage;
   // one lane brings block i of the warp: whole 16-row groups, which lie within the head's rows
-  auto fetch = [&](int i) {
-    const int64_t key = (int64_t)(b0 + warp + (uint32_t)i * kWarpsW) * kKeysW;
+  auto fetch = [&](int i, int st) {
+    const int64_t key = (int64_t)(b0 + warp + (uint32_t)i * W) * kKeysW;
     const int64_t left = (len - key + 15) & ~(int64_t)15;
     const uint32_t nr = left < kKeysW ? (uint32_t)left : kKeysW;
     const int64_t at = (int64_t)h * a.cap + key;
-    uint8_t* dst = ring + (i % kStagesW) * Lay::stage;
-    uint64_t* bar = &full[i % kStagesW];
-    tc::mbar_arrive_tx(bar, 2 * nr * (D / 2 + D / 16));
-    tc::bulk_load(dst, a.kc + at * (D / 2), nr * (D / 2), bar);
-    tc::bulk_load(dst + 2 * Lay::codes, a.ks + at * (D / 16), nr * (D / 16), bar);
-    tc::bulk_load(dst + Lay::codes, a.vc + at * (D / 2), nr * (D / 2), bar);
-    tc::bulk_load(dst + 2 * Lay::codes + Lay::scales, a.vs + at * (D / 16), nr * (D / 16), bar);
+    uint8_t* dst = ring + st * Lay::stage;
+    tc::mbar_arrive_tx(&full[st], 2 * nr * (D / 2 + D / 16));
+    tc::bulk_load(dst, a.kc + at * (D / 2), nr * (D / 2), &full[st]);
+    tc::bulk_load(dst + 2 * Lay::codes, a.ks + at * (D / 16), nr * (D / 16), &full[st]);
+    tc::bulk_load(dst + Lay::codes, a.vc + at * (D / 2), nr * (D / 2), &full[st]);
+    tc::bulk_load(dst + 2 * Lay::codes + Lay::scales, a.vs + at * (D / 16), nr * (D / 16), &full[st]);
   };
   if (lane == 0)
-    for (int i = 0; i < kStagesW && i < count; ++i) fetch(i);
+    for (int i = 0; i < ST && i < count; ++i) fetch(i, i);
   __syncthreads();                          // the barriers and the flag are set for every lane
 
-  uint32_t qa[D / 16][4];
-  float sl2[2];
-  load_q<D>(a, h, rows, g, t, qa, sl2);
-  int64_t see[2];                           // how many keys the thread's two rows see
+  uint32_t qb[NR][D / 16][2];
+  float sl2[NR][2], m[NR][2], l[NR][2];     // of rows 2t and 2t + 1 of each group
+  int see[NR][2];                           // how many keys they see
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const uint32_t r = (uint32_t)(g + 8 * p), nq = (uint32_t)a.nq;
-    see[p] = (int)r < rows ? kv4::visible(len, a.nq, r % nq, a.block) : len;
+  for (int n = 0; n < NR; ++n) {
+    const float s = load_q<D>(a, h, rows, 8 * n + g, t, qb[n]);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      sl2[n][p] = __shfl_sync(0xffffffffu, s, (2 * t + p) * 4);
+      const uint32_t r = (uint32_t)(8 * n + 2 * t + p), nq = (uint32_t)a.nq;
+      see[n][p] = (int)((int)r < rows ? kv4::visible(len, a.nq, r % nq, a.block) : len);
+      m[n][p] = l[n][p] = 0.f;
+    }
   }
-  float m[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
-  float o[NT][4];
+  float o[NR][MT][4];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
   volatile int* abort = abort_flag;
 
+  int stage = 0;
+  uint32_t ph = 0;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
-    const int64_t key = (int64_t)(b0 + warp + (uint32_t)i * kWarpsW) * kKeysW;
-    const uint8_t* st = ring + (i % kStagesW) * Lay::stage;
-    if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[i % kStagesW], (i / kStagesW) & 1, abort))) break;
-    const int nk = len - key < kKeysW ? (int)(len - key) : kKeysW;
-    // ---- S = Q K^T: a lane's share of key g of 8; two times 8 keys side by side and two sums
-    // each, so that four products are in flight ----
-    float s[8][4];
+    const int key = (int)(b0 + warp + (uint32_t)i * W) * kKeysW;        // the capacity fits 31 bits
+    uint8_t* st = ring + stage * Lay::stage;
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[stage], ph, abort))) break;
+    if ((int)len - key < kKeysW) {
+      // rows behind the length count as 0, whatever lies there: their scales do (a scale each of
+      // K's and V's D / 16 a row; a lane a row)
+      if (lane >= (int)len - key)
+        for (int x = 0; x < D / 16; ++x)
+          st[2 * Lay::codes + lane * (D / 16) + x] = st[2 * Lay::codes + Lay::scales + lane * (D / 16) + x] = 0;
+      __syncwarp();
+    }
+    // ---- S^T = K Q^T: 16 keys at a time, a lane's shares of keys g and g + 8 of them ----
+    float s[NR][2][4];
 #pragma unroll
-    for (int n = 0; n < 8; n += 2) {
-      uint32_t b[2][D / 8];
+    for (int kt = 0; kt < 2; ++kt) {
+      uint32_t kf[2][D / 8];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int k = (n + e) * 8 + g;
+        const int k = kt * 16 + e * 8 + g;
         if (D == 128) {
           const uint4 c = reinterpret_cast<const uint4*>(st)[k * 4 + t];
-          uint32_t sc = reinterpret_cast<const uint16_t*>(st + 2 * Lay::codes)[k * 4 + t];
-          if (k >= nk) sc = 0;             // rows behind the length count as 0, whatever lies there
-          const uint32_t s0 = kv4::scale_f16x2(sc), s1 = kv4::scale_f16x2(sc >> 8);
-          kv4::unpack8(c.x, s0, b[e]);
-          kv4::unpack8(c.y, s0, b[e] + 4);
-          kv4::unpack8(c.z, s1, b[e] + 8 % (D / 8));
-          kv4::unpack8(c.w, s1, b[e] + 12 % (D / 8));
+          const uint32_t s2 = scales_f16x2(reinterpret_cast<const uint16_t*>(st + 2 * Lay::codes)[k * 4 + t]);
+          const uint32_t s0 = __byte_perm(s2, 0, 0x1010), s1 = __byte_perm(s2, 0, 0x3232);
+          kv4::unpack8(c.x, s0, kf[e]);
+          kv4::unpack8(c.y, s0, kf[e] + 4);
+          kv4::unpack8(c.z, s1, kf[e] + 8 % (D / 8));
+          kv4::unpack8(c.w, s1, kf[e] + 12 % (D / 8));
         } else {
           const uint2 c = reinterpret_cast<const uint2*>(st)[k * 4 + t];
-          uint32_t sc = (st + 2 * Lay::codes)[k * 4 + t];
-          if (k >= nk) sc = 0;
-          const uint32_t s0 = kv4::scale_f16x2(sc);
-          kv4::unpack8(c.x, s0, b[e]);
-          kv4::unpack8(c.y, s0, b[e] + 4);
+          const uint32_t s0 = kv4::scale_f16x2((st + 2 * Lay::codes)[k * 4 + t]);
+          kv4::unpack8(c.x, s0, kf[e]);
+          kv4::unpack8(c.y, s0, kf[e] + 4);
         }
       }
-      float u[2][2][4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int n = 0; n < NR; ++n) {
+        float u[2][4];                      // two sums, so that two products are in flight
 #pragma unroll
-        for (int x = 0; x < 4; ++x) u[e][0][x] = u[e][1][x] = 0.f;
+        for (int x = 0; x < 4; ++x) u[0][x] = u[1][x] = 0.f;
 #pragma unroll
-      for (int q = 0; q < D / 16; ++q)
+        for (int q = 0; q < D / 16; ++q) {
+          const uint32_t ka[4] = {kf[0][2 * q], kf[1][2 * q], kf[0][2 * q + 1], kf[1][2 * q + 1]};
+          mma16816(u[q & 1], ka, qb[n][q][0], qb[n][q][1]);
+        }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) mma16816(u[e][q & 1], qa[q], b[e][2 * q], b[e][2 * q + 1]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[n + e][x] = u[e][0][x] + u[e][1][x];
+        for (int x = 0; x < 4; ++x) s[n][kt][x] = u[0][x] + u[1][x];
+      }
     }
     // ---- masks, reference, P ----
-    if (see[0] - key < kKeysW || see[1] - key < kKeysW) {
+    bool cut = false;
 #pragma unroll
-      for (int p = 0; p < RH; ++p) {
-        const int valid = see[p] - key < kKeysW ? (int)(see[p] - key) : kKeysW;
+    for (int n = 0; n < NR; ++n) cut |= min(see[n][0], see[n][1]) - key < kKeysW;
+    if (__any_sync(0xffffffffu, cut)) {
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (n * 8 + 2 * t + e >= valid) s[n][2 * p + e] = neg_inf();
-      }
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (key + kt * 16 + (x >> 1) * 8 + g >= see[n][x & 1]) s[n][kt][x] = neg_inf();
     }
-    __syncwarp();
-    float mt[2] = {neg_inf(), neg_inf()};
+    float mt[NR][2];
+    bool grow = i == 0;
 #pragma unroll
-    for (int p = 0; p < RH; ++p) {
-#pragma unroll
-      for (int n = 0; n < 8; ++n) mt[p] = fmaxf(mt[p], fmaxf(s[n][2 * p], s[n][2 * p + 1]));
-      mt[p] *= sl2[p];
-    }
-    if (__any_sync(0xffffffffu, i == 0 || mt[0] > m[0] + 15.f || (kTwo && mt[1] > m[1] + 15.f))) {
-#pragma unroll
-      for (int p = 0; p < RH; ++p) {
-        const float mx = quad_maxf(mt[p]);
-        float f = 1.f;
-        if (i == 0) {
-          m[p] = mx == neg_inf() ? 0.f : mx;
-        } else if (mx > m[p]) {
-          f = ex2w(m[p] - mx);
-          m[p] = mx;
-        }
-        l[p] *= f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) o[n][2 * p] *= f, o[n][2 * p + 1] *= f;
-      }
-    }
-    uint32_t pa[4][4];
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        if (p < RH) {
-          const float e0 = ex2w(fmaf(s[n][2 * p], sl2[p], -m[p])), e1 = ex2w(fmaf(s[n][2 * p + 1], sl2[p], -m[p]));
-          l[p] += e0 + e1;
-          pa[n >> 1][p + 2 * (n & 1)] = pack_f16w(e0, e1);
-        } else {
-          pa[n >> 1][p + 2 * (n & 1)] = 0u;
-        }
+        mt[n][p] = fmaxf(fmaxf(s[n][0][p], s[n][0][2 + p]), fmaxf(s[n][1][p], s[n][1][2 + p])) * sl2[n][p];
+        grow |= mt[n][p] > m[n][p] + 15.f;
       }
-    // ---- O += P V: 16 keys at a time; a lane's keys 2t, 2t + 1, 2t + 8, 2t + 9, channels g D/8 .. ----
+    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t v[4][NT / 2];
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int k = q * 16 + 2 * t + (e & 1) + 8 * (e >> 1);
-        uint32_t sc = (st + 2 * Lay::codes + Lay::scales)[D == 128 ? k * 8 + g : k * 4 + (g >> 1)];
-        if (k >= nk) sc = 0;
-        const uint32_t s0 = kv4::scale_f16x2(sc);
+        for (int p = 0; p < 2; ++p) {
+          const float mx = group_max(mt[n][p]);
+          float f = 1.f;
+          if (i == 0) {
+            m[n][p] = mx == neg_inf() ? 0.f : mx;
+          } else if (mx > m[n][p]) {
+            f = ex2w(m[n][p] - mx);
+            m[n][p] = mx;
+          }
+          l[n][p] *= f;
+#pragma unroll
+          for (int x = 0; x < MT; ++x) o[n][x][p] *= f, o[n][x][2 + p] *= f;
+        }
+    }
+    uint32_t pb[NR][2][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float e0 = ex2w(fmaf(s[n][kt][2 * e], sl2[n][0], -m[n][0]));
+          const float e1 = ex2w(fmaf(s[n][kt][2 * e + 1], sl2[n][1], -m[n][1]));
+          l[n][0] += e0;
+          l[n][1] += e1;
+          pb[n][kt][e] = transpose8(pack_f16w(e0, e1));
+        }
+    // ---- O^T += V^T P^T: a lane's keys 2t, 2t + 1, 2t + 8, 2t + 9 of 16, channels g D/8 .. ----
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      // va[x]: the operand of row tile x: channels 2 x (rows g) and 2 x + 1 (rows g + 8), each a
+      // pair of keys: the codes are paired before they are unpacked
+      uint32_t va[MT][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {         // keys 2t, 2t + 1 of the first or second 8
+        const int k = kt * 16 + 8 * e + 2 * t;
+        const uint8_t* sc = st + 2 * Lay::codes + Lay::scales + (D == 128 ? k * 8 + g : k * 4 + (g >> 1));
+        const uint32_t s2 = scales_f16x2(sc[0] | (uint32_t)sc[D / 16] << 8);
         if (D == 128) {
-          const uint2 c = reinterpret_cast<const uint2*>(st + Lay::codes)[k * 8 + g];
-          kv4::unpack8(c.x, s0, v[e]);
-          kv4::unpack8(c.y, s0, v[e] + NT / 4);
+          const uint2 ca = reinterpret_cast<const uint2*>(st + Lay::codes)[k * 8 + g];
+          const uint2 cb = reinterpret_cast<const uint2*>(st + Lay::codes)[(k + 1) * 8 + g];
+          uint32_t even, odd;
+          pair_codes(ca.x, cb.x, even, odd);
+          unpack_bytes(even, s2, va[0][2 * e], va[1][2 * e], va[2][2 * e], va[3][2 * e]);
+          unpack_bytes(odd, s2, va[0][2 * e + 1], va[1][2 * e + 1], va[2][2 * e + 1], va[3][2 * e + 1]);
+          pair_codes(ca.y, cb.y, even, odd);
+          unpack_bytes(even, s2, va[4 % MT][2 * e], va[5 % MT][2 * e], va[6 % MT][2 * e], va[7 % MT][2 * e]);
+          unpack_bytes(odd, s2, va[4 % MT][2 * e + 1], va[5 % MT][2 * e + 1], va[6 % MT][2 * e + 1],
+                       va[7 % MT][2 * e + 1]);
         } else {
-          kv4::unpack8(reinterpret_cast<const uint32_t*>(st + Lay::codes)[k * 8 + g], s0, v[e]);
+          const uint32_t* c = reinterpret_cast<const uint32_t*>(st + Lay::codes) + k * 8 + g;
+          uint32_t even, odd;
+          pair_codes(c[0], c[8], even, odd);
+          unpack_bytes(even, s2, va[0][2 * e], va[1][2 * e], va[2][2 * e], va[3][2 * e]);
+          unpack_bytes(odd, s2, va[0][2 * e + 1], va[1][2 * e + 1], va[2][2 * e + 1], va[3][2 * e + 1]);
         }
       }
 #pragma unroll
-      for (int n = 0; n < NT; n += 2) {
-        mma16816(o[n], pa[q], __byte_perm(v[0][n >> 1], v[1][n >> 1], 0x5410),
-                 __byte_perm(v[2][n >> 1], v[3][n >> 1], 0x5410));
-        mma16816(o[n + 1], pa[q], __byte_perm(v[0][n >> 1], v[1][n >> 1], 0x7632),
-                 __byte_perm(v[2][n >> 1], v[3][n >> 1], 0x7632));
-      }
+      for (int x = 0; x < MT; ++x)
+#pragma unroll
+        for (int n = 0; n < NR; ++n) mma16816(o[n][x], va[x], pb[n][kt][0], pb[n][kt][1]);
     }
     __syncwarp();                           // every lane has read the block
-    if (lane == 0 && i + kStagesW < count) fetch(i + kStagesW);
+    if (lane == 0 && i + ST < count) fetch(i + ST, stage);
+    if (++stage == ST) stage = 0, ph ^= 1;
   }
 
-  // ---- the eight warps' results, in warp order ----
+  // ---- the warps' results, in warp order ----
 #pragma unroll
-  for (int p = 0; p < RH; ++p) {
-    l[p] = quad_sum(l[p]);
-    if (t == 0) wml[warp * 16 + g + 8 * p] = make_float2(m[p], l[p]);
-  }
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      l[n][p] = group_sum(l[n][p]);
+      if (g == 0) wml[warp * 8 * NR + 8 * n + 2 * t + p] = make_float2(m[n][p], l[n][p]);
+    }
   __syncthreads();
-  float* red = reinterpret_cast<float*>(base);          // the ring has been used: [warp][16][D]
-#pragma unroll
-  for (int p = 0; p < RH; ++p) {
-    const int r = g + 8 * p;
+  // the largest reference of a row's warps that hold a key it sees
+  auto top = [&](int r) {
     float mx = neg_inf();
 #pragma unroll
-    for (int w = 0; w < kWarpsW; ++w) {
-      const float2 x = wml[w * 16 + r];
+    for (int w = 0; w < W; ++w) {
+      const float2 x = wml[w * 8 * NR + r];
       if (x.y != 0.f) mx = fmaxf(mx, x.x);
     }
-    const float f = l[p] != 0.f ? ex2w(m[p] - mx) : 0.f;
-    if (r < rows) {
-      // a thread's columns of tile n: channels 2t D/8 + n and (2t + 1) D/8 + n
+    return mx;
+  };
+  float* red = reinterpret_cast<float*>(base);          // the ring has been used: [warp][8 NR][D]
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float4* dst = reinterpret_cast<float4*>(red + (warp * 16 + r) * D + (2 * t + e) * (D / 8));
+  for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; n += 4)
-          dst[n >> 2] = make_float4(o[n][2 * p + e] * f, o[n + 1][2 * p + e] * f, o[n + 2][2 * p + e] * f,
-                                    o[n + 3][2 * p + e] * f);
-      }
+    for (int p = 0; p < 2; ++p) {
+      const int r = 8 * n + 2 * t + p;
+      const float f = l[n][p] != 0.f ? ex2w(m[n][p] - top(r)) : 0.f;
+      // a lane's channels g D/8 + 2 x and + 2 x + 1 of row r
+      float4* dst = reinterpret_cast<float4*>(red + (warp * 8 * NR + r) * D + g * (D / 8));
+      if (r < rows)
+#pragma unroll
+        for (int x = 0; x < MT; x += 2)
+          dst[x >> 1] = make_float4(o[n][x][p] * f, o[n][x][2 + p] * f, o[n][x + 1][p] * f, o[n][x + 1][2 + p] * f);
     }
-  }
   __syncthreads();
   const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
-  for (int x = threadIdx.x; x < rows * (D / 4); x += kWarpsW * 32) {
+  for (int x = threadIdx.x; x < rows * (D / 4); x += W * 32) {
     const int r = x / (D / 4), c = x % (D / 4) * 4;
-    float mx = neg_inf(), sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarpsW; ++w) {
-      const float2 y = wml[w * 16 + r];
-      if (y.y != 0.f) mx = fmaxf(mx, y.x);
-    }
+    const float mx = top(r);
+    float sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kWarpsW; ++w) {
-      const float2 y = wml[w * 16 + r];
+    for (int w = 0; w < W; ++w) {
+      const float2 y = wml[w * 8 * NR + r];
       if (y.y == 0.f) continue;             // no key of that warp's that the row sees
       sum += y.y * ex2w(y.x - mx);
-      const float4 z = *reinterpret_cast<const float4*>(red + (w * 16 + r) * D + c);
+      const float4 z = *reinterpret_cast<const float4*>(red + (w * 8 * NR + r) * D + c);
       acc.x += z.x, acc.y += z.y, acc.z += z.z, acc.w += z.w;
     }
     const bool live = sum > 0.f || sum != sum;
@@ -365,13 +414,14 @@ __global__ void __launch_bounds__(kWarpsW * 32, 1) kv4_attn_few_kernel(const Kv4
   if (threadIdx.x == 0 && *abort) flag_status(a.status, FASTAR_DEV_TIMEOUT);
 }
 
-template <int D, bool kTwo>
+template <int D, int NR>
 cudaError_t few_go(const Kv4AttnArgs& a, cudaStream_t s) {
+  using Lay = FewLayout<D, NR>;
   const int64_t blocks = (int64_t)a.Hkv * a.splits;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = opt_in_smem((const void*)kv4_attn_few_kernel<D, kTwo>, FewLayout<D>::bytes);
+  const cudaError_t e = opt_in_smem((const void*)kv4_attn_few_kernel<D, NR>, Lay::bytes);
   if (e != cudaSuccess) return e;
-  kv4_attn_few_kernel<D, kTwo><<<(unsigned)blocks, kWarpsW * 32, FewLayout<D>::bytes, s>>>(a);
+  kv4_attn_few_kernel<D, NR><<<(unsigned)blocks, Lay::warps * 32, Lay::bytes, s>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -380,8 +430,8 @@ cudaError_t few_go(const Kv4AttnArgs& a, cudaStream_t s) {
 
 cudaError_t launch_kv4_attn_few(int d, const Kv4AttnArgs& a, cudaStream_t s) {
   const bool two = (int64_t)(a.Hq / a.Hkv) * a.nq > 8;
-  if (d == 128) return two ? few_go<128, true>(a, s) : few_go<128, false>(a, s);
-  return two ? few_go<64, true>(a, s) : few_go<64, false>(a, s);
+  if (d == 128) return two ? few_go<128, 2>(a, s) : few_go<128, 1>(a, s);
+  return two ? few_go<64, 2>(a, s) : few_go<64, 1>(a, s);
 }
 
 }  // namespace fastar
