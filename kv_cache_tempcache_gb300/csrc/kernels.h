@@ -219,12 +219,13 @@ struct Kv4AttnArgs {
   int32_t* status;
   // filled in by the launcher: splits of the keys and their partials (fp32; maximum and sum)
   int splits;
+  int min_tiles;                      // key tiles of 128 a split should have (tcgen05 kernel)
   float* part_o;                      // [splits, Hq, nq, d]
   float2* part_ml;                    // [splits, Hq, nq]
 };
 
 // Splits of the keys for these sizes, and the bytes of their partials (0: one split).
-int kv4_attn_splits(int dtype, int d, int Hq, int Hkv, int64_t nq, int64_t cap);
+int kv4_attn_splits(int dtype, int d, int Hq, int Hkv, int64_t nq, int64_t cap, int* min_tiles);
 size_t kv4_attn_workspace(int d, int Hq, int Hkv, int64_t nq, int64_t cap);
 // False if the workspace is too small for the call's splits (nothing is enqueued).
 bool launch_kv4_attn(int dtype, int d, Kv4AttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s, cudaError_t* err);

@@ -270,14 +270,17 @@ int splits_few(int Hkv, int64_t cap) {
 // tile, half as long a tile, fill the last wave's gaps; and with splits the partials' way through
 // memory and the join.  The fewest splits within 2 % of the best.  (Measured: 1.5 us a tile of
 // 128 keys and 512 rows at d = 128, 8 us around them.)
-int splits_tc(int d, int64_t rows, int Hkv, int64_t cap) {
+// The cache's lengths are the device's, and may be far below its capacity: *min_tiles is what the
+// kernel keeps a split's key tiles to, 3 where all the splits run at once, else 40, beside which
+// the fixed part is small.
+int splits_tc(int d, int64_t rows, int Hkv, int64_t cap, int* min_tiles) {
   const int cta = d / 64;                 // CTAs that work as one (kv4_attn_tc.cu)
   const int64_t slots = sm_count() / cta, tiles = (cap + 127) / 128;
   const int64_t half = (rows - 1) % (256 * cta) < 128 * cta ? Hkv : 0;
   const int64_t full = (rows + 256 * cta - 1) / (256 * cta) * Hkv - half;
   const double tile = 1.5, fixed = 8.0;
   auto cost = [&](int64_t s) {
-    const int64_t waves = (full * s + slots - 1) / slots, gaps = (waves * slots - full * s) * 8 / 5;
+    const int64_t waves = (full * s + slots - 1) / slots, gaps = 2 * (waves * slots - full * s);
     const int64_t rest = half * s > gaps ? (half * s - gaps + slots - 1) / slots : 0;
     const double keys = (double)((tiles + s - 1) / s) * tile;
     const double join = s > 1 ? 4.0 + 2e-6 * s * rows * Hkv * (d + 2) * 4 / 4.0 : 0.0;
@@ -292,6 +295,7 @@ int splits_tc(int d, int64_t rows, int Hkv, int64_t cap) {
     const double c = cost(s);
     if (c < 0.98 * best) best = c, pick = s;
   }
+  *min_tiles = (full + half) * pick <= slots ? 3 : 40;
   return (int)pick;
 }
 
@@ -313,23 +317,28 @@ cudaError_t run(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStream_t s) {
 
 }  // namespace
 
-int kv4_attn_splits(int dtype, int d, int Hq, int Hkv, int64_t nq, int64_t cap) {
+int kv4_attn_splits(int dtype, int d, int Hq, int Hkv, int64_t nq, int64_t cap, int* min_tiles) {
   const int64_t rows = (int64_t)(Hq / Hkv) * nq;
-  if (dtype == FASTAR_BF16) return rows <= kFewRows ? splits_few(Hkv, cap) : splits_tc(d, rows, Hkv, cap);
+  if (dtype == FASTAR_BF16 && rows > kFewRows) {
+    int unused;
+    return splits_tc(d, rows, Hkv, cap, min_tiles ? min_tiles : &unused);
+  }
+  if (dtype == FASTAR_BF16) return splits_few(Hkv, cap);
   return splits_f32((rows + kRows - 1) / kRows * Hkv, cap);
 }
 
 size_t kv4_attn_workspace(int d, int Hq, int Hkv, int64_t nq, int64_t cap) {
   int s = 1;
   for (int dt : {FASTAR_F32, FASTAR_BF16}) {
-    const int x = kv4_attn_splits(dt, d, Hq, Hkv, nq, cap);
+    const int x = kv4_attn_splits(dt, d, Hq, Hkv, nq, cap, nullptr);
     s = x > s ? x : s;
   }
   return partial_bytes(s, d, Hq, nq);
 }
 
 bool launch_kv4_attn(int dtype, int d, Kv4AttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s, cudaError_t* err) {
-  a.splits = ws ? kv4_attn_splits(dtype, d, a.Hq, a.Hkv, a.nq, a.cap) : 1;
+  a.min_tiles = 1;
+  a.splits = ws ? kv4_attn_splits(dtype, d, a.Hq, a.Hkv, a.nq, a.cap, &a.min_tiles) : 1;
   if (a.splits > 1 && ws_bytes < partial_bytes(a.splits, d, a.Hq, a.nq)) return false;
   *err = run(dtype, d, a, ws, s);
   return true;

@@ -281,32 +281,17 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
   // the work item (the same for both CTAs of a pair): KV head, row tiles, split of the keys.
   // The rows that see most keys (the last ones of a call in blocks) start first, but a last
   // item with one row tile, which takes half as long, goes to the end, where it fills gaps.
-  const int64_t rows = (int64_t)(a.Hq / a.Hkv) * a.nq;
+  const uint32_t rows = (uint32_t)(a.Hq / a.Hkv) * (uint32_t)a.nq, nq = (uint32_t)a.nq;      // Hq * nq fits 31 bits
   const bool odd = row_tiles > 1 && (rows - 1) % (2 * kRT * kCta) < kRT * kCta;
   const int full_tiles = row_tiles - odd;
   uint32_t u = blockIdx.x / kCta;
-  const int split = (int)(u % (uint32_t)a.splits);
+  const uint32_t split = u % (uint32_t)a.splits;
   u /= (uint32_t)a.splits;
   const bool last = u >= (uint32_t)(a.Hkv * full_tiles);
   const int h = (int)(last ? u - (uint32_t)(a.Hkv * full_tiles) : u / (uint32_t)full_tiles);
   const int rt = last ? full_tiles : full_tiles - 1 - (int)(u % (uint32_t)full_tiles);
-  const int64_t r0 = (int64_t)rt * (2 * kRT * kCta);
-  const int64_t rlast = (r0 + 2 * kRT * kCta < rows ? r0 + 2 * kRT * kCta : rows) - 1;
-  const int nt = rlast - r0 >= kRT * kCta ? 2 : 1;      // row tiles with rows
   const int64_t len = kv4::head_len(a.len, h, a.cap, a.status);
-  // the last key that any of the rows sees: rows of two heads include a last token
-  const int64_t most = r0 / a.nq != rlast / a.nq ? len : kv4::visible(len, a.nq, rlast % a.nq, a.block);
-  const int64_t tiles = (most + kKT - 1) / kKT;
-  const int64_t j0 = tiles * split / a.splits;
-  const int T = (int)(tiles * (split + 1) / a.splits - j0);
-
-  if (T == 0) {                                          // no keys: uniform over the pair
-    const int64_t r = r0 + (int64_t)(threadIdx.x / kRT) * (kRT * kCta) + rank * kRT + threadIdx.x % kRT;
-    if (threadIdx.x < 2 * kRT && r < rows) store_empty<D>(a, split, row_of(a, h, r));
-    return;
-  }
-
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0) {                                // while the length is on its way
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.q_full[i], 8 * kCta);
       tc::mbar_init(&sm.s_full[i], 1);
@@ -327,6 +312,41 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     sm.abort = 0;
     tc::mbar_fence_init();
   }
+  const uint32_t r0 = (uint32_t)rt * (2 * kRT * kCta);
+  const uint32_t rlast = (r0 + 2 * kRT * kCta < rows ? r0 + 2 * kRT * kCta : rows) - 1;
+  const int nt = rlast - r0 >= kRT * kCta ? 2 : 1;      // row tiles with rows
+  const bool both = nt == 1;              // one row tile: even key tiles and odd key tiles
+  // a query row's share of 16 bytes, 16 (8) lanes a row: warp x of a row tile loads its rows 16 x ..
+  // on, all of them before anything waits
+  constexpr int QL = D / 8, QR = 32 / QL, QN = 16 / QR;
+  uint4 xq[QN];
+  if (warp < kSoftWarps && !(both && warp >= 8)) {
+#pragma unroll
+    for (int i = 0; i < QN; ++i) {
+      const uint32_t r = r0 + (uint32_t)((warp >> 3) * (kRT * kCta) + rank * kRT + (warp & 7) * 16 + i * QR + lane / QL);
+      xq[i] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const RowOf at = row_of(a, h, r);
+        xq[i] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + at.head * a.q.hs +
+                                               at.t * a.q.ts)[lane % QL];
+      }
+    }
+  }
+  // the last key that any of the rows sees: rows of two heads include a last token
+  const int64_t most = r0 / nq != rlast / nq ? len : kv4::visible(len, a.nq, rlast % nq, a.block);
+  const uint32_t tiles = (uint32_t)((most + kKT - 1) / kKT);      // times the splits fits 32 bits
+  // the splits were chosen for a full cache: a shorter one takes fewer, the others are empty
+  uint32_t splits = tiles / (uint32_t)a.min_tiles;
+  splits = splits < 1 ? 1u : splits < (uint32_t)a.splits ? splits : (uint32_t)a.splits;
+  const int64_t j0 = split < splits ? tiles * split / splits : 0;
+  const int T = split < splits ? (int)(tiles * (split + 1) / splits - (uint32_t)j0) : 0;
+
+  if (T == 0) {                                          // no keys: uniform over the pair
+    const uint32_t r = r0 + threadIdx.x / kRT * (kRT * kCta) + rank * kRT + threadIdx.x % kRT;
+    if (threadIdx.x < 2 * kRT && r < rows) store_empty<D>(a, (int)split, row_of(a, h, r));
+    return;
+  }
+
   if (warp == kMmaWarp) tmem_alloc512<kCta>(&sm.tmem_base);
   tc::tc_fence_before();
   __syncthreads();
@@ -335,61 +355,51 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
 
-  const bool both = nt == 1;              // one row tile: even key tiles and odd key tiles
   if (warp < kSoftWarps) {
     // ---------------- softmax ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     const int w = warp >> 3, half = (warp >> 2) & 1;      // row tile (or parity of the key tiles), half
     const int row = (warp & 3) * 32 + lane;
     const int pair_bar = 1 + w * 4 + (warp & 3);          // the two warps of these rows
-    const int64_t r = r0 + (both ? 0 : (int64_t)w * (kRT * kCta)) + rank * kRT + row;
+    const uint32_t r = r0 + (both ? 0u : (uint32_t)(w * (kRT * kCta))) + (uint32_t)(rank * kRT + row);
     const bool has = r < rows;
     const RowOf at = has ? row_of(a, h, r) : RowOf{0, 0};
-    constexpr int HD = D / 2;                             // channels of a row of Q, and of O, a thread takes
-    float sl2;
-    {
-      // the query row: its largest magnitude, then fp16 at a power of two
-      uint4 xq[HD / 8];
-      uint32_t big = 0;
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + at.head * a.q.hs +
-                                                      at.t * a.q.ts + half * HD);
+    constexpr int HD = D / 2;                             // channels of a row of O a thread takes
+    if (!(both && w == 1)) {
+      // query rows: a row's largest magnitude, then fp16 at a power of two
+      uint8_t* dst = base + Lay::q + (size_t)w * Lay::q_tile;
 #pragma unroll
-      for (int c = 0; c < HD / 8; ++c) {
-        xq[c] = has ? p[c] : make_uint4(0, 0, 0, 0);
-        const uint32_t v[4] = {xq[c].x, xq[c].y, xq[c].z, xq[c].w};
+      for (int i = 0; i < QN; ++i) {
+        const uint32_t v[4] = {xq[i].x, xq[i].y, xq[i].z, xq[i].w};
+        uint32_t big = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) big = max(big, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
-      }
-      sm.ex[half][w][row] = __uint_as_float(big);
-      tc::named_bar(pair_bar, 64);
-      big = max(big, __float_as_uint(sm.ex[half ^ 1][w][row]));
-      // exponent of the largest (subnormals count as 2^-126); a row that is zero or not finite
-      // stays as it is
-      const int ex = (int)(big >> 7);
-      int qe = ex == 0 ? -126 - 12 : ex - 127 - 12;
-      if (qe < -120) qe = -120;
-      if (big == 0 || ex == 255) qe = 0;
-      const float down = kv4::pow2i(-qe);
-      sl2 = a.scale * kv4::pow2i(qe) * kv4::pow2i(kv4::head_exp(a.k_exp, h)) * 1.4426950408889634f;
-      sl2 = fmaxf(sl2, 1.2e-38f);      // a product of scales under fp32's range: still positive
-      if (w == 0 || !both) {
-        uint8_t* dst = base + Lay::q + (size_t)w * Lay::q_tile;
 #pragma unroll
-        for (int c = 0; c < HD / 8; ++c) {
-          const uint32_t v[4] = {xq[c].x, xq[c].y, xq[c].z, xq[c].w};
-          uint32_t o[4];
+        for (int x = QL / 2; x > 0; x >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, x));
+        // exponent of the largest (subnormals count as 2^-126); a row that is zero or not finite
+        // stays as it is
+        const int ex = (int)(big >> 7);
+        int qe = ex == 0 ? -126 - 12 : ex - 127 - 12;
+        if (qe < -120) qe = -120;
+        if (big == 0 || ex == 255) qe = 0;
+        const float down = kv4::pow2i(-qe);
+        const int qr = (warp & 7) * 16 + i * QR + lane / QL, ch = lane % QL;
+        uint32_t o[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            o[e] = pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
-          const int ch = half * (HD / 8) + c;
-          *reinterpret_cast<uint4*>(dst + (ch >> 3) * Lay::q_blk + tc::sw128_off(row, ch & 7)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        tc::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) arrive_issuer<kCta>(&sm.q_full[w]);
+        for (int e = 0; e < 4; ++e)
+          o[e] = pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
+        *reinterpret_cast<uint4*>(dst + (ch >> 3) * Lay::q_blk + tc::sw128_off(qr, ch & 7)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+        if (ch == 0) sm.ex[0][w][qr] = kv4::pow2i(qe);
       }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_issuer<kCta>(&sm.q_full[w]);
     }
+    tc::named_bar(9, kSoftWarps * 32);
+    float sl2 = a.scale * sm.ex[0][both ? 0 : w][row] * kv4::pow2i(kv4::head_exp(a.k_exp, h)) * 1.4426950408889634f;
+    sl2 = fmaxf(sl2, 1.2e-38f);            // a product of scales under fp32's range: still positive
+    tc::named_bar(9, kSoftWarps * 32);     // ex is used again below
     // keys the row sees from this thread's first on (a row that is not there: as the last)
     int64_t left = (has ? kv4::visible(len, a.nq, at.t, a.block) : most) - j0 * kKT - half * 64 - (both ? w * kKT : 0);
     const int step = both ? 2 : 1, count = both ? (T - w + 1) >> 1 : T;      // this row tile's key tiles
@@ -515,53 +525,69 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
           m = mn;
         }
       }
-      const bool live = l > 0.f || l != l;
+      const bool live = l > 0.f || l != l, partial = a.splits > 1;
       const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
-      const float f = a.splits > 1 ? up : live ? up / l : 0.f;
-      // the TMEM loads are the warp's: rows past the last load too, and store nothing
+      const float f = partial ? up : live ? up / l : 0.f;
+      // Rows of 128 bytes (32 fp32 or 64 bf16 channels; 64 bytes of 32 bf16) go through shared
+      // memory (the ring of K has been used; 4 KB a warp), so that they leave as whole runs; written
+      // 16 bytes a thread, a row each, they took 5 us of a CTA.
+      uint8_t* stg = base + Lay::k + warp * 4096;
+      uint8_t* out = partial ? reinterpret_cast<uint8_t*>(a.part_o) : static_cast<uint8_t*>(a.out);
+      const int64_t off = partial ? (((int64_t)split * a.Hq + at.head) * a.nq + at.t) * D * 4 + half * HD * 4
+                                  : (at.head * a.o_hs + at.t * a.o_ts + half * HD) * 2;
+      const int cp = partial ? 32 : HD, esz = partial ? 4 : 2, nc = cp * esz / 16;   // channels and 16-byte chunks a pass
 #pragma unroll 1
-      for (int c = 0; c < HD; c += 16) {
-        float o[16];
-        __syncwarp();
-        tc::tmem_ld16(o_addr + (uint32_t)c, o);
-        tc::tmem_wait_ld();
-        tc::tmem_pin16(o);
-        if (!has) continue;
-        if (f1 != 0.f) {
+      for (int c0 = 0; c0 < HD; c0 += cp) {
+#pragma unroll 1
+        for (int c = c0; c < c0 + cp; c += 16) {
+          float o[16];
+          __syncwarp();
+          tc::tmem_ld16(o_addr + (uint32_t)c, o);
+          tc::tmem_wait_ld();
+          tc::tmem_pin16(o);
+          if (f1 != 0.f) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 v = shared_o[row * CH + (((half * HD + c) / 4 + e) ^ (row & (CH - 1)))];
-            o[4 * e] = o[4 * e] * f0 + v.x * f1;
-            o[4 * e + 1] = o[4 * e + 1] * f0 + v.y * f1;
-            o[4 * e + 2] = o[4 * e + 2] * f0 + v.z * f1;
-            o[4 * e + 3] = o[4 * e + 3] * f0 + v.w * f1;
-          }
-        }
-        if (a.splits > 1) {
-          const int64_t pa = (split * (int64_t)a.Hq + at.head) * a.nq + at.t;
-          float4* p4 = reinterpret_cast<float4*>(a.part_o + pa * D + half * HD + c);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            p4[e] = make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
-        } else {
-          uint4* p4 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at.head * a.o_hs + at.t * a.o_ts +
-                                               half * HD + c);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              __nv_bfloat162 h2 = __floats2bfloat162_rn(o[8 * e + 2 * k] * f, o[8 * e + 2 * k + 1] * f);
-              v[k] = live ? *reinterpret_cast<uint32_t*>(&h2) : 0u;
+            for (int e = 0; e < 4; ++e) {
+              const float4 v = shared_o[row * CH + (((half * HD + c) / 4 + e) ^ (row & (CH - 1)))];
+              o[4 * e] = o[4 * e] * f0 + v.x * f1;
+              o[4 * e + 1] = o[4 * e + 1] * f0 + v.y * f1;
+              o[4 * e + 2] = o[4 * e + 2] * f0 + v.z * f1;
+              o[4 * e + 3] = o[4 * e + 3] * f0 + v.w * f1;
             }
-            p4[e] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+          const int ch = (c - c0) * esz / 16;
+          if (partial) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<float4*>(stg + tc::sw128_off(lane, ch + e)) =
+                  make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                __nv_bfloat162 h2 = __floats2bfloat162_rn(o[8 * e + 2 * k] * f, o[8 * e + 2 * k + 1] * f);
+                v[k] = live ? *reinterpret_cast<uint32_t*>(&h2) : 0u;
+              }
+              *reinterpret_cast<uint4*>(stg + tc::sw128_off(lane, ch + e)) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
           }
         }
+        __syncwarp();
+        for (int x = lane; x < 32 * nc; x += 32) {
+          const int sr = x / nc, ch = x % nc;
+          const int64_t to = __shfl_sync(0xffffffffu, off, sr);
+          const bool there = __shfl_sync(0xffffffffu, (int)has, sr);
+          const uint4 v = *reinterpret_cast<const uint4*>(stg + tc::sw128_off(sr, ch));
+          if (there) *reinterpret_cast<uint4*>(out + to + c0 * esz + ch * 16) = v;
+        }
+        __syncwarp();
       }
       if (has && half == 0) {
         const float mn = m * 0.6931471805599453f;
         if (a.splits > 1)
-          a.part_ml[(split * (int64_t)a.Hq + at.head) * a.nq + at.t] = make_float2(live ? mn : neg_inf(), l);
+          a.part_ml[((int64_t)split * a.Hq + at.head) * a.nq + at.t] = make_float2(live ? mn : neg_inf(), l);
         else if (a.lse)
           a.lse[at.head * a.nq + at.t] = live ? mn + logf(l) : neg_inf();
       }
