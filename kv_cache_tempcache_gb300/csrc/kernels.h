@@ -219,7 +219,7 @@ struct Kv4AttnArgs {
   int32_t* status;
   // filled in by the launcher: splits of the keys and their partials (fp32; maximum and sum)
   int splits;
-  int min_tiles;                      // key tiles of 128 a split should have (tcgen05 kernel)
+  int min_tiles;                      // tcgen05 kernel: key tiles of 128 a split should have (else 0)
   float* part_o;                      // [splits, Hq, nq, d]
   float2* part_ml;                    // [splits, Hq, nq]
 };

@@ -72,5 +72,26 @@ __device__ __forceinline__ int64_t visible(int64_t len, int64_t nq, int64_t t, i
   return v < 0 ? 0 : v;
 }
 
+// Query rows of an item of the tcgen05 kernel: two tiles of 128 in each of d / 64 CTAs.
+__host__ __device__ constexpr uint32_t item_rows(int d) { return 4u * (uint32_t)d; }
+
+// What the rows [r0, r0 + item_rows) of a KV head with `len` cached rows work on: the last key
+// that any of them sees (rows of two query heads include a last token, which sees all), and the
+// splits of the keys in use.  The launch's splits were chosen for a full cache; a shorter one
+// takes fewer, none under min_tiles tiles of 128 keys.
+struct ItemKeys {
+  int64_t most;
+  uint32_t tiles, splits;
+};
+__device__ __forceinline__ ItemKeys item_keys(int64_t len, uint32_t nq, int64_t block, uint32_t r0, uint32_t rlast,
+                                              int splits, int min_tiles) {
+  ItemKeys k;
+  k.most = r0 / nq != rlast / nq ? len : visible(len, nq, rlast % nq, block);
+  k.tiles = (uint32_t)((k.most + 127) / 128);
+  const uint32_t s = k.tiles / (uint32_t)min_tiles;
+  k.splits = s < 1 ? 1u : s < (uint32_t)splits ? s : (uint32_t)splits;
+  return k;
+}
+
 }  // namespace kv4
 }  // namespace fastar

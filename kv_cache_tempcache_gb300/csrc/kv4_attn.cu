@@ -163,8 +163,10 @@ __global__ void __launch_bounds__(kThreadsF) kv4_attn_f32_kernel(const Kv4AttnAr
 // ---- joining the splits ----------------------------------------------------------------------
 // O = sum_s e^(m_s - m) o_s / sum_s e^(m_s - m) l_s over a row's S partials, m = max_s m_s; one
 // warp a row, D / 32 channels a lane.  The partials are summed in the order of the splits, so
-// results do not change from run to run.
-template <typename T, int D>
+// results do not change from run to run.  A split in which the row sees no key has l = 0 and
+// nothing in o; (inf, 0) for the first split says that the output is in place already.
+// Bound: latency, so the loads do not wait for one another (kFew: at most 8 splits, all at once).
+template <typename T, int D, bool kFew>
 __global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnArgs a) {
   constexpr int CPL = D / 32;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -172,47 +174,72 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnArgs a) {
   const int64_t rows = (int64_t)a.Hq * a.nq;
   pdl_wait();
   if (row >= rows) return;
-  // lane s % 32 reads split s's maximum and sum; then the outputs, eight splits' loads at a time
-  constexpr int kPer = kKv4MaxSplits / 32;
-  float2 ml[kPer];
-  float m = neg_inf();
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    ml[i] = make_float2(neg_inf(), 0.f);
-    if (32 * i + lane < a.splits) ml[i] = a.part_ml[(32 * i + lane) * rows + row];
-    if (ml[i].y != 0.f) m = fmaxf(m, ml[i].x);
-  }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  const float ref = m == neg_inf() ? 0.f : m;
-  float l = 0.f, o[CPL];
+  float m = neg_inf(), l = 0.f, o[CPL];
 #pragma unroll
   for (int i = 0; i < CPL; ++i) o[i] = 0.f;
+  if (kFew) {
+    float2 ml[8];
+    float p[8][CPL];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (32 * i >= a.splits) break;
-    const float w = ml[i].y != 0.f ? expf(ml[i].x - ref) : 0.f;
-    const int here = a.splits - 32 * i < 32 ? a.splits - 32 * i : 32;
+    for (int s = 0; s < 8; ++s) ml[s] = s < a.splits ? a.part_ml[s * rows + row] : make_float2(neg_inf(), 0.f);
+    if (ml[0].x == -neg_inf() && ml[0].y == 0.f) return;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const float* src = a.part_o + (s * rows + row) * D + lane * CPL;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) p[s][c] = ml[s].y != 0.f ? src[c] : 0.f;
+    }
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (ml[s].y != 0.f) m = fmaxf(m, ml[s].x);
+    const float ref = m == neg_inf() ? 0.f : m;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const bool in = ml[s].y != 0.f;
+      const float w = in ? expf(ml[s].x - ref) : 0.f;
+      l = fmaf(w, ml[s].y, l);
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) o[c] = fmaf(w, p[s][c], o[c]);
+    }
+  } else {
+    // lane s % 32 reads split s's maximum and sum; then the outputs, eight splits' loads at a time
+    constexpr int kPer = kKv4MaxSplits / 32;
+    float2 ml[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      ml[i] = make_float2(neg_inf(), 0.f);
+      if (32 * i + lane < a.splits) ml[i] = a.part_ml[(32 * i + lane) * rows + row];
+      if (ml[i].y != 0.f) m = fmaxf(m, ml[i].x);
+    }
+    if (__any_sync(0xffffffffu, lane == 0 && ml[0].x == -neg_inf() && ml[0].y == 0.f)) return;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    const float ref = m == neg_inf() ? 0.f : m;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (32 * i >= a.splits) break;
+      const float w = ml[i].y != 0.f ? expf(ml[i].x - ref) : 0.f;
+      const int here = a.splits - 32 * i < 32 ? a.splits - 32 * i : 32;
 #pragma unroll 1
-    for (int s0 = 0; s0 < here; s0 += 8) {
-      float p[8][CPL], ws[8], ls[8];
+      for (int s0 = 0; s0 < here; s0 += 8) {
+        float p[8][CPL], ws[8], ls[8];
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const int src = s0 + s < 32 ? s0 + s : 31;
-        ls[s] = __shfl_sync(0xffffffffu, ml[i].y, src);
-        ws[s] = __shfl_sync(0xffffffffu, w, src);
-        // a split in which the row sees no key: its outputs are not written
-        const bool in = s0 + s < here && ls[s] != 0.f;
-        const float* src_o = a.part_o + ((32 * i + s0 + s) * rows + row) * D + lane * CPL;
+        for (int s = 0; s < 8; ++s) {
+          const int src = s0 + s < 32 ? s0 + s : 31;
+          ls[s] = __shfl_sync(0xffffffffu, ml[i].y, src);
+          ws[s] = __shfl_sync(0xffffffffu, w, src);
+          const bool in = s0 + s < here && ls[s] != 0.f;
+          const float* src_o = a.part_o + ((32 * i + s0 + s) * rows + row) * D + lane * CPL;
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) p[s][c] = in ? src_o[c] : 0.f;
-        if (!in) ws[s] = ls[s] = 0.f;
-      }
+          for (int c = 0; c < CPL; ++c) p[s][c] = in ? src_o[c] : 0.f;
+          if (!in) ws[s] = ls[s] = 0.f;
+        }
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        l = fmaf(ws[s], ls[s], l);
+        for (int s = 0; s < 8; ++s) {
+          l = fmaf(ws[s], ls[s], l);
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) o[c] = fmaf(ws[s], p[s][c], o[c]);
+          for (int c = 0; c < CPL; ++c) o[c] = fmaf(ws[s], p[s][c], o[c]);
+        }
       }
     }
   }
@@ -227,7 +254,9 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnArgs a) {
 template <typename T, int D>
 cudaError_t join_go(const Kv4AttnArgs& a, cudaStream_t s) {
   const int64_t rows = (int64_t)a.Hq * a.nq;
-  const cudaError_t e = launch_dependent(kv4_join_kernel<T, D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a);
+  const dim3 grid((unsigned)((rows + 3) / 4));
+  const cudaError_t e = a.splits <= 8 ? launch_dependent(kv4_join_kernel<T, D, true>, grid, dim3(128), 0, s, a)
+                                      : launch_dependent(kv4_join_kernel<T, D, false>, grid, dim3(128), 0, s, a);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -295,7 +324,7 @@ int splits_tc(int d, int64_t rows, int Hkv, int64_t cap, int* min_tiles) {
     const double c = cost(s);
     if (c < 0.98 * best) best = c, pick = s;
   }
-  *min_tiles = (full + half) * pick <= slots ? 3 : 40;
+  if (min_tiles) *min_tiles = (full + half) * pick <= slots ? 3 : 40;
   return (int)pick;
 }
 
@@ -310,6 +339,7 @@ cudaError_t run(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStream_t s) {
   }
   if (dtype == FASTAR_F32) return d == 128 ? f32_go<128>(a, s) : f32_go<64>(a, s);
   const bool few = (int64_t)(a.Hq / a.Hkv) * a.nq <= kFewRows;
+  if (!few && a.min_tiles == 0) a.min_tiles = 1;         // one split
   const cudaError_t e = few ? launch_kv4_attn_few(d, a, s) : launch_kv4_attn_tc(d, a, s);
   if (e != cudaSuccess || a.splits == 1) return e;
   return d == 128 ? join_go<__nv_bfloat16, 128>(a, s) : join_go<__nv_bfloat16, 64>(a, s);
@@ -319,10 +349,7 @@ cudaError_t run(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStream_t s) {
 
 int kv4_attn_splits(int dtype, int d, int Hq, int Hkv, int64_t nq, int64_t cap, int* min_tiles) {
   const int64_t rows = (int64_t)(Hq / Hkv) * nq;
-  if (dtype == FASTAR_BF16 && rows > kFewRows) {
-    int unused;
-    return splits_tc(d, rows, Hkv, cap, min_tiles ? min_tiles : &unused);
-  }
+  if (dtype == FASTAR_BF16 && rows > kFewRows) return splits_tc(d, rows, Hkv, cap, min_tiles);
   if (dtype == FASTAR_BF16) return splits_few(Hkv, cap);
   return splits_f32((rows + kRows - 1) / kRows * Hkv, cap);
 }
@@ -337,7 +364,7 @@ size_t kv4_attn_workspace(int d, int Hq, int Hkv, int64_t nq, int64_t cap) {
 }
 
 bool launch_kv4_attn(int dtype, int d, Kv4AttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s, cudaError_t* err) {
-  a.min_tiles = 1;
+  a.min_tiles = 0;
   a.splits = ws ? kv4_attn_splits(dtype, d, a.Hq, a.Hkv, a.nq, a.cap, &a.min_tiles) : 1;
   if (a.splits > 1 && ws_bytes < partial_bytes(a.splits, d, a.Hq, a.nq)) return false;
   *err = run(dtype, d, a, ws, s);

@@ -255,13 +255,9 @@ __device__ __forceinline__ RowOf row_of(const Kv4AttnArgs& a, int h, int64_t r) 
   return RowOf{h * (int64_t)(a.Hq / a.Hkv) + g, (int64_t)((uint32_t)r - g * nq)};
 }
 
-// A row that sees no key: zeros and lse = -inf (in a split: an empty partial).
+// A row that sees no key: zeros and lse = -inf.
 template <int D>
-__device__ __forceinline__ void store_empty(const Kv4AttnArgs& a, int split, RowOf w) {
-  if (a.splits > 1) {
-    a.part_ml[(split * (int64_t)a.Hq + w.head) * a.nq + w.t] = make_float2(neg_inf(), 0.f);
-    return;
-  }
+__device__ __forceinline__ void store_empty(const Kv4AttnArgs& a, RowOf w) {
   uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + w.head * a.o_hs + w.t * a.o_ts);
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) p[i] = make_uint4(0, 0, 0, 0);
@@ -279,17 +275,21 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
   const int rank = kCta == 2 ? (int)cta_rank() : 0;
 
   // the work item (the same for both CTAs of a pair): KV head, row tiles, split of the keys.
-  // The rows that see most keys (the last ones of a call in blocks) start first, but a last
-  // item with one row tile, which takes half as long, goes to the end, where it fills gaps.
+  // First splits first (a short cache uses no others); in a call in blocks the rows that see most
+  // keys first, of all heads; a last item with one row tile, which takes half as long, at the
+  // end, where it fills gaps.
   const uint32_t rows = (uint32_t)(a.Hq / a.Hkv) * (uint32_t)a.nq, nq = (uint32_t)a.nq;      // Hq * nq fits 31 bits
   const bool odd = row_tiles > 1 && (rows - 1) % (2 * kRT * kCta) < kRT * kCta;
   const int full_tiles = row_tiles - odd;
   uint32_t u = blockIdx.x / kCta;
-  const uint32_t split = u % (uint32_t)a.splits;
-  u /= (uint32_t)a.splits;
-  const bool last = u >= (uint32_t)(a.Hkv * full_tiles);
-  const int h = (int)(last ? u - (uint32_t)(a.Hkv * full_tiles) : u / (uint32_t)full_tiles);
-  const int rt = last ? full_tiles : full_tiles - 1 - (int)(u % (uint32_t)full_tiles);
+  const uint32_t all = (uint32_t)(a.Hkv * full_tiles);
+  const bool last = u >= all * (uint32_t)a.splits;
+  if (last) u -= all * (uint32_t)a.splits;
+  const uint32_t split = last ? u / (uint32_t)a.Hkv : u / all;
+  u -= split * (last ? (uint32_t)a.Hkv : all);
+  const int h = (int)(last ? u : a.block > 0 ? u % (uint32_t)a.Hkv : u / (uint32_t)full_tiles);
+  const int rt = last ? full_tiles
+                      : full_tiles - 1 - (int)(a.block > 0 ? u / (uint32_t)a.Hkv : u % (uint32_t)full_tiles);
   const int64_t len = kv4::head_len(a.len, h, a.cap, a.status);
   if (threadIdx.x == 0) {                                // while the length is on its way
     for (int i = 0; i < 2; ++i) {
@@ -316,6 +316,21 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
   const uint32_t rlast = (r0 + 2 * kRT * kCta < rows ? r0 + 2 * kRT * kCta : rows) - 1;
   const int nt = rlast - r0 >= kRT * kCta ? 2 : 1;      // row tiles with rows
   const bool both = nt == 1;              // one row tile: even key tiles and odd key tiles
+  const kv4::ItemKeys keys = kv4::item_keys(len, nq, a.block, r0, rlast, a.splits, a.min_tiles);
+  const int64_t most = keys.most;
+  if (split >= keys.splits || (keys.splits == 1 && a.splits > 1)) {
+    // what the join reads of a split that is not in use, and of the first where the output is in place
+    const uint32_t r = r0 + threadIdx.x / kRT * (kRT * kCta) + rank * kRT + threadIdx.x % kRT;
+    if (threadIdx.x < 2 * kRT && r < rows) {
+      const RowOf w = row_of(a, h, r);
+      a.part_ml[((int64_t)split * a.Hq + w.head) * a.nq + w.t] = make_float2(split == 0 ? -neg_inf() : neg_inf(), 0.f);
+    }
+    if (split > 0) return;
+  }
+  const bool partial = keys.splits > 1;
+  const int64_t j0 = keys.tiles * split / keys.splits;   // tiles times splits fits 32 bits
+  const int T = (int)(keys.tiles * (split + 1) / keys.splits - (uint32_t)j0);
+
   // a query row's share of 16 bytes, 16 (8) lanes a row: warp x of a row tile loads its rows 16 x ..
   // on, all of them before anything waits
   constexpr int QL = D / 8, QR = 32 / QL, QN = 16 / QR;
@@ -332,18 +347,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       }
     }
   }
-  // the last key that any of the rows sees: rows of two heads include a last token
-  const int64_t most = r0 / nq != rlast / nq ? len : kv4::visible(len, a.nq, rlast % nq, a.block);
-  const uint32_t tiles = (uint32_t)((most + kKT - 1) / kKT);      // times the splits fits 32 bits
-  // the splits were chosen for a full cache: a shorter one takes fewer, the others are empty
-  uint32_t splits = tiles / (uint32_t)a.min_tiles;
-  splits = splits < 1 ? 1u : splits < (uint32_t)a.splits ? splits : (uint32_t)a.splits;
-  const int64_t j0 = split < splits ? tiles * split / splits : 0;
-  const int T = split < splits ? (int)(tiles * (split + 1) / splits - (uint32_t)j0) : 0;
-
-  if (T == 0) {                                          // no keys: uniform over the pair
+  if (T == 0) {                                          // no keys at all: uniform over the pair
     const uint32_t r = r0 + threadIdx.x / kRT * (kRT * kCta) + rank * kRT + threadIdx.x % kRT;
-    if (threadIdx.x < 2 * kRT && r < rows) store_empty<D>(a, (int)split, row_of(a, h, r));
+    if (threadIdx.x < 2 * kRT && r < rows) store_empty<D>(a, row_of(a, h, r));
     return;
   }
 
@@ -525,7 +531,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
           m = mn;
         }
       }
-      const bool live = l > 0.f || l != l, partial = a.splits > 1;
+      const bool live = l > 0.f || l != l;
       const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
       const float f = partial ? up : live ? up / l : 0.f;
       // Rows of 128 bytes (32 fp32 or 64 bf16 channels; 64 bytes of 32 bf16) go through shared
@@ -586,7 +592,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       }
       if (has && half == 0) {
         const float mn = m * 0.6931471805599453f;
-        if (a.splits > 1)
+        if (partial)
           a.part_ml[((int64_t)split * a.Hq + at.head) * a.nq + at.t] = make_float2(live ? mn : neg_inf(), l);
         else if (a.lse)
           a.lse[at.head * a.nq + at.t] = live ? mn + logf(l) : neg_inf();
