@@ -6,8 +6,10 @@ autoregressive video diffusion transformer (technical summary, Key Results: Roll
 Forcing / LongVie2 on Wan-family backbones).  This module supplies that transformer's
 shape so that a chunk can be denoised end to end: every block is
     h  = LN(x) * (1 + scale1) + shift1                      (adaLN)
-    q, k, v = h W_qkv^T + b;  q, k <- RMSNorm, rotary positions (frame, row, column)
-    x += gate1 * (SelfAttn(q, k, v) W_o^T + b)               (FAST-AR: TempCache + AnnSA, or dense)
+    q, k, v = h W_qkv^T + b;  q, k <- RMSNorm (of the row, or of each head), rotary positions
+                                                    (frame, row, column)
+    x += gate1 * (SelfAttn(q, k, v) W_o^T + b)               (FAST-AR: TempCache + AnnSA, or dense
+                                                              over a bf16 or a 4-bit cache)
     x += CrossAttn(RMSNorm(LN_affine(x) W_q^T + b), text) W_o^T + b   (FAST-AR: AnnCA, or dense)
     x += gate2 * (GELU(LN(x) * (1 + scale2) + shift2) W_1^T + b) W_2^T + b)
 with (shift, scale, gate) x 2 = the block's modulation + a projection of the timestep
@@ -29,7 +31,7 @@ from typing import List, Optional
 import torch
 
 from . import _lib as L
-from .layer import DenseLayer, FastARLayer
+from .layer import DenseLayer, FastARLayer, KV4Layer
 
 
 @dataclasses.dataclass(frozen=True)
@@ -48,6 +50,7 @@ class DiTConfig:
     steps: int = 4              # denoising steps per chunk
     eps: float = 1e-6
     theta: float = 10000.0
+    qk_norm: str = "row"        # "row": RMS norm over all heads together; "head": of each head
     # FAST-AR attention (the Wan-1.3B layer of the benchmark)
     M: int = 9360
     B: int = 64
@@ -64,6 +67,12 @@ class DiTConfig:
     @property
     def tokens(self) -> int:
         return self.frames * self.grid_h * self.grid_w
+
+    @property
+    def axes(self):
+        """Channels of a head that turn with the frame, the row and the column."""
+        part = 2 * (self.d // 6)
+        return self.d - 2 * part, part, part
 
     def replace(self, **kw) -> "DiTConfig":
         return dataclasses.replace(self, **kw)
@@ -84,13 +93,16 @@ class _Block:
 
 class DiT:
     """Parameters, buffers and the denoising step of the transformer.  attention is
-    "fastar" (TempCache + AnnSA + AnnCA per block) or "dense" (append-only caches)."""
+    "fastar" (TempCache + AnnSA + AnnCA per block), "dense" (append-only caches) or "dense4"
+    (append-only caches in 4 bits)."""
 
     def __init__(self, cfg: DiTConfig, attention: str = "fastar", seed: int = 0, device="cuda",
                  dense_capacity: int = 0):
         L.load()
         if cfg.dim % 256 or cfg.ffn % 256 or cfg.text_dim % 64 or cfg.dim % cfg.heads:
             raise ValueError("dimensions must suit the GEMM tiles (multiples of 256 / 64)")
+        if cfg.qk_norm not in ("row", "head"):
+            raise ValueError(f"unknown qk_norm {cfg.qk_norm!r}")
         self.cfg, self.attention = cfg, attention
         dev = torch.device(device)
         self.dev = dev
@@ -105,6 +117,7 @@ class DiT:
             return torch.randn(n, generator=g, device=dev) * s
 
         D, N = cfg.dim, cfg.tokens
+        nw = cfg.d if cfg.qk_norm == "head" else D      # weights of a norm of queries or keys
         self.patch_w = torch.zeros(D, LAT_LD, dtype=bf, device=dev)
         self.patch_w[:, :cfg.patch_ch] = w(D, cfg.patch_ch)
         self.patch_b = vec(D)
@@ -118,13 +131,13 @@ class DiT:
             b = _Block()
             b.mod = torch.randn(6, D, generator=g, device=dev) / math.sqrt(D)
             b.qkv_w, b.qkv_b = w(3 * D, D), vec(3 * D)
-            b.norm_q, b.norm_k = (1 + vec(D, 0.1)), (1 + vec(D, 0.1))
+            b.norm_q, b.norm_k = (1 + vec(nw, 0.1)), (1 + vec(nw, 0.1))
             b.o_w, b.o_b = w(D, D), vec(D)
             b.norm3_w, b.norm3_b = (1 + vec(D, 0.1)), vec(D)
             b.cq_w, b.cq_b = w(D, D), vec(D)
             b.ck_w, b.ck_b = w(D, D), vec(D)
             b.cv_w, b.cv_b = w(D, D), vec(D)
-            b.norm_cq, b.norm_ck = (1 + vec(D, 0.1)), (1 + vec(D, 0.1))
+            b.norm_cq, b.norm_ck = (1 + vec(nw, 0.1)), (1 + vec(nw, 0.1))
             b.co_w, b.co_b = w(D, D), vec(D)
             b.f1_w, b.f1_b = w(cfg.ffn, D), vec(cfg.ffn)
             b.f2_w, b.f2_b = w(D, cfg.ffn), vec(D)
@@ -162,7 +175,8 @@ class DiT:
                                                               dim=-1).to(bf))
         else:
             cap = max(dense_capacity, N)
-            self.attn = [DenseLayer(H, d, N, cap, cfg.text_len, dtype=bf, device=dev) for _ in range(cfg.layers)]
+            layer = KV4Layer if attention == "dense4" else DenseLayer
+            self.attn = [layer(H, d, N, cap, cfg.text_len, dtype=bf, device=dev) for _ in range(cfg.layers)]
         self.frame0 = 0
         self._graphs = {}
 
@@ -171,6 +185,26 @@ class DiT:
         """[N, H*d] token-major -> [H, N, d] view."""
         N = t2d.shape[0]
         return t2d.view(N, self.cfg.heads, self.cfg.d).transpose(0, 1)
+
+    def _norm(self, x, weight):
+        """RMS norm of cross-attention queries or keys x [n, D], in place."""
+        if self.cfg.qk_norm == "head":
+            h = self._heads(x)
+            L.fastar_qk_norm_rope(h, None, h, None, wq=weight, eps=self.cfg.eps)
+        else:
+            L.fastar_rmsnorm_rope(x, self.cfg.d, weight=weight, eps=self.cfg.eps)
+
+    def _norm_rope(self, q, k, b):
+        """RMS norm and rotary positions of the block's queries and keys, in place."""
+        cfg, D = self.cfg, self.cfg.dim
+        if cfg.qk_norm == "head":
+            L.fastar_qk_norm_rope(q, k, q, k, wq=b.norm_q, wk=b.norm_k, eps=cfg.eps, axes=cfg.axes,
+                                  t0_dev=self.frame_dev, grid=(cfg.grid_h, cfg.grid_w), theta=cfg.theta)
+            return
+        L.fastar_rmsnorm_rope(self.qkv[:, :D], cfg.d, weight=b.norm_q, rope=True, t0_dev=self.frame_dev,
+                              grid=(cfg.grid_h, cfg.grid_w), eps=cfg.eps, theta=cfg.theta)
+        L.fastar_rmsnorm_rope(self.qkv[:, D:2 * D], cfg.d, weight=b.norm_k, rope=True, t0_dev=self.frame_dev,
+                              grid=(cfg.grid_h, cfg.grid_w), eps=cfg.eps, theta=cfg.theta)
 
     # ---- set-up ----------------------------------------------------------------------------
     def set_text(self, text: torch.Tensor):
@@ -186,7 +220,7 @@ class DiT:
         v = torch.empty(P, D, dtype=torch.bfloat16, device=self.dev)
         for b, a in zip(self.blocks, self.attn):
             L.fastar_gemm(ctx, b.ck_w, k, bias=b.ck_b, dev_status=self.status)
-            L.fastar_rmsnorm_rope(k, cfg.d, weight=b.norm_ck, eps=cfg.eps)
+            self._norm(k, b.norm_ck)
             L.fastar_gemm(ctx, b.cv_w, v, bias=b.cv_b, dev_status=self.status)
             a.set_prompt(self._heads(k).contiguous(), self._heads(v).contiguous())
 
@@ -214,17 +248,14 @@ class DiT:
             L.fastar_layernorm_mod(self.x, self.h, eps=cfg.eps, shift_a=b.mod[0], shift_b=e0[0], scale_a=b.mod[1],
                                    scale_b=e0[1])
             L.fastar_gemm(self.h, b.qkv_w, self.qkv, bias=b.qkv_b, dev_status=st)
-            L.fastar_rmsnorm_rope(self.qkv[:, :D], cfg.d, weight=b.norm_q, rope=True, t0_dev=self.frame_dev,
-                                  grid=(cfg.grid_h, cfg.grid_w), eps=cfg.eps, theta=cfg.theta)
-            L.fastar_rmsnorm_rope(self.qkv[:, D:2 * D], cfg.d, weight=b.norm_k, rope=True, t0_dev=self.frame_dev,
-                                  grid=(cfg.grid_h, cfg.grid_w), eps=cfg.eps, theta=cfg.theta)
+            self._norm_rope(q, k, b)
             a.step_self(q, k, v, out=o, advance=advance)
             if probe is not None:
                 probe("self", i, a, q, k, v, o)
             L.fastar_gemm(self.o, b.o_w, self.x, bias=b.o_b, R=self.x, gate_a=b.mod[2], gate_b=e0[2], dev_status=st)
             L.fastar_layernorm_mod(self.x, self.h, eps=cfg.eps, weight=b.norm3_w, bias=b.norm3_b)
             L.fastar_gemm(self.h, b.cq_w, self.qc, bias=b.cq_b, dev_status=st)
-            L.fastar_rmsnorm_rope(self.qc, cfg.d, weight=b.norm_cq, eps=cfg.eps)
+            self._norm(self.qc, b.norm_cq)
             a.step_cross(self._heads(self.qc), out=o)
             if probe is not None:
                 probe("cross", i, a, self._heads(self.qc), o)
@@ -255,6 +286,8 @@ class DiT:
         for a in self.attn:
             if self.attention == "fastar":
                 a.cur = 1 - a.cur
+            elif self.attention == "dense4":
+                a.commit(cfg.tokens)
             else:
                 a.n += cfg.tokens
         self.frame0 += cfg.frames
@@ -264,11 +297,13 @@ class DiT:
     def _graph_key(self):
         if self.attention == "fastar":
             return ("fastar", self.attn[0].cur)
+        if self.attention == "dense4":
+            return ("dense4",)                             # the lengths are on the device
         return ("dense", self.attn[0].n)
 
     def capture(self):
         """The current denoising step as a CUDA graph (FAST-AR: one per cache half, kept;
-        dense: one per cache length)."""
+        dense: one per cache length; dense4: one)."""
         key = self._graph_key()
         if key in self._graphs:
             return self._graphs[key]
@@ -316,6 +351,6 @@ class DiT:
     def status_word(self) -> int:
         st = int(self.status.item())
         for a in self.attn:
-            if self.attention == "fastar":
+            if self.attention in ("fastar", "dense4"):
                 st |= a.status()
         return st

@@ -1,0 +1,114 @@
+"""The DiT with its append-only caches in 4 bits (attention = "dense4") and with norms of each
+head: every block's self-attention against the float64 oracle on the block's own inputs and the
+cache's own values, three chunks, two steps each; one captured step for every length; the layer's
+history; a full cache.  The attention bound is the one of the 4-bit cache's tests."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_kv4 as T
+from kv_cache_tempcache_gb300 import _lib as L
+from kv_cache_tempcache_gb300.dit import DiT, DiTConfig
+from kv_cache_tempcache_gb300.layer import KV4Layer
+from oracle import kv4_oracle as K
+
+pytestmark = pytest.mark.gpu
+
+SMALL = DiTConfig(dim=256, heads=2, ffn=512, layers=2, text_dim=256, text_len=64, frames=2, grid_h=4, grid_w=20,
+                  steps=2, name="dit_small", qk_norm="head")
+
+
+def _dit(cfg=SMALL, chunks=3):
+    dit = DiT(cfg, "dense4", seed=3, dense_capacity=chunks * cfg.tokens)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dit.set_text(torch.randn(cfg.text_len, cfg.text_dim, generator=g, device="cuda").bfloat16())
+    return dit, g
+
+
+def _noise(cfg, g):
+    return torch.randn(cfg.tokens, cfg.patch_ch, generator=g, device="cuda").bfloat16()
+
+
+def test_blocks_attend_over_the_cache_they_filled():
+    cfg = SMALL
+    dit, g = _dit()
+    for b in dit.blocks:
+        b.norm_q.fill_(1.0)
+    seen = []
+
+    def probe(what, i, a, q, *rest):
+        if what != "self":
+            return
+        k, v, out = rest
+        torch.cuda.synchronize()
+        n = a.n + cfg.tokens
+        assert a.len.tolist() == [a.n] * cfg.heads and a.len_cur.tolist() == [n] * cfg.heads
+        # the norm of each head: unit mean square up to bf16's rounding of each channel (2^-8 of it)
+        ms = (q.double() ** 2).mean(-1)
+        assert ((ms - 1).abs() <= 2.0 ** -7 + 2.0 ** -12).all()
+        codes, scales = K.quantise(T._np(k))
+        assert np.array_equal(a.k_codes[:, a.n:n].cpu().numpy(), codes)
+        assert np.array_equal(a.k_scales[:, a.n:n].cpu().numpy(), scales)
+        vals = [K.values(c[:, :n].cpu().numpy(), s[:, :n].cpu().numpy())
+                for c, s in ((a.k_codes, a.k_scales), (a.v_codes, a.v_scales))]
+        T._check_attn(out, a.lse_self, q, vals[0], vals[1], [n] * cfg.heads, 1 / math.sqrt(cfg.d), 0)
+        seen.append((i, n))
+
+    for chunk in range(3):
+        dit.denoise_chunk(_noise(cfg, g), use_graph=False, probe=probe)
+    torch.cuda.synchronize()
+    assert dit.status_word() == 0
+    assert seen == [(i, (c + 1) * cfg.tokens) for c in range(3) for _ in range(cfg.steps) for i in range(cfg.layers)]
+
+
+def test_one_captured_step_serves_every_length():
+    outs = []
+    for use_graph in (False, True):
+        dit, g = _dit()
+        outs.append([dit.denoise_chunk(_noise(SMALL, g), use_graph=use_graph).clone() for _ in range(3)])
+        torch.cuda.synchronize()
+        assert dit.status_word() == 0
+        if use_graph:
+            assert list(dit._graphs) == [("dense4",)]
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_row_norms_and_the_dense_path_with_head_norms_run():
+    for cfg, attention in ((SMALL.replace(qk_norm="row"), "dense4"), (SMALL, "dense")):
+        dit = DiT(cfg, attention, seed=3, dense_capacity=cfg.tokens)
+        g = torch.Generator(device="cuda").manual_seed(5)
+        dit.set_text(torch.randn(cfg.text_len, cfg.text_dim, generator=g, device="cuda").bfloat16())
+        out = dit.denoise_chunk(_noise(cfg, g))
+        torch.cuda.synchronize()
+        assert torch.isfinite(out.float()).all() and dit.status_word() == 0
+
+
+def test_an_unknown_norm_is_refused():
+    with pytest.raises(ValueError, match="qk_norm"):
+        DiT(SMALL.replace(qk_norm="none"), "dense4")
+
+
+def test_layer_history_shared_heads_and_frames():
+    H, Hkv, d, nq = 4, 2, 64, 40
+    layer = KV4Layer(H, d, nq, 100, 8, Hkv=Hkv, block=20)
+    assert layer.cap == 112
+    x = T._rand((2, Hkv, 50, d), 30).bfloat16()
+    layer.load_history(x[0], x[1])
+    q, kv = T._rand((H, nq, d), 31, 1.5).bfloat16(), T._rand((2, Hkv, nq, d), 32).bfloat16()
+    for _ in range(2):                                   # a step that is not kept leaves no trace
+        layer.step_self(q, kv[0], kv[1], advance=False)
+    out = layer.step_self(q, kv[0], kv[1])
+    torch.cuda.synchronize()
+    assert layer.n == 90 and layer.len.tolist() == [90, 90] and layer.status() == 0
+    k, v = layer.history()
+    torch.cuda.synchronize()
+    want = [np.concatenate((K.values(*K.quantise(T._np(a))), K.values(*K.quantise(T._np(b)))), axis=1)
+            for a, b in ((x[0], kv[0]), (x[1], kv[1]))]
+    assert np.array_equal(T._np(k), want[0]) and np.array_equal(T._np(v), want[1])
+    T._check_attn(out, layer.lse_self, q, want[0], want[1], [90, 90], 1 / math.sqrt(d), 20)
+    layer.step_self(q, kv[0], kv[1])                      # 130 rows do not fit 112
+    torch.cuda.synchronize()
+    assert layer.status() == L.DEV_BAD_LEN and layer.len.tolist() == [112, 112]
