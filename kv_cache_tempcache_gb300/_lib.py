@@ -429,63 +429,55 @@ def fastar_sinusoidal_embedding(t, out, stream=None):
 # ---- the 4-bit cache, and the norm and rotation before it -------------------------------------
 
 # Every check below refuses what a kernel would misread.  They run on each call of a step that
-# may be a few microseconds of device time, so they ask each tensor for as little as they can.
+# may be a few microseconds of device time, so a call asks for everything in one expression, and
+# only what fails it is looked at again, tensor by tensor, for the message.
 
-def _wrong(name, t, dtype, shape):
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
+_U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
 
 
-def _dense(name, t, dtype, shape):
-    """Address of a contiguous tensor of this type and shape (None: NULL)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _wrong(name, t, dtype, shape)
-    return t.data_ptr()
+def _refuse(rows, dense):
+    """Raises for the first tensor that is not as expected.  rows: (name, [H, n, d] view, dtype,
+    shape); dense: (name, contiguous tensor or None, dtype, shape)."""
+    for name, t, dtype, shape in rows + dense:
+        if t is None:
+            continue
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    for name, t, _, _ in rows:
+        if t is not None and t.stride(2) != 1:
+            raise ValueError(f"{name}: token tensors must be [H, N, d] views with a contiguous last dimension")
+    for name, t, _, _ in dense:
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    raise ValueError("tensors must be on the current CUDA device, all of them")
 
 
-def _rows(name, t, dtype, shape):
-    """A [H, n, d] view of rows with a contiguous last dimension: (address, head stride, token
-    stride).  The stride of a dimension of one element says nothing (torch may give any)."""
-    if t.dtype is not dtype or t.shape != shape:
-        _wrong(name, t, dtype, shape)
-    hs, ts, cs = t.stride()
-    if cs != 1:
-        raise ValueError("token tensors must be [H, N, d] views with a contiguous last dimension")
-    H, n, d = shape
-    if n <= 1:
-        ts = d
-    if H <= 1:
-        hs = n * d
-    return t.data_ptr(), hs, ts
+def _dims3(name, t):
+    s = t.shape
+    if len(s) != 3:
+        raise ValueError(f"{name} must have three dimensions, not {len(s)}")
+    return s
 
 
-def _launch(name, stream, tensors, *args):
-    """Calls an entry point on the current device, where every tensor has to be."""
-    dev = None
-    for t in tensors:
-        if t is not None:
-            g = t.get_device()
-            if dev is None:
-                dev = g
-            elif g != dev:
-                raise ValueError("tensors must be on the current CUDA device, all of them")
-    if dev is not None and (dev < 0 or dev != torch._C._cuda_getDevice()):
-        raise ValueError("tensors must be on the current CUDA device")
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    rc = getattr(_lib or load(), name)(*args, s)
-    if rc != OK:
-        raise FastarError(name, rc, load().fastar_last_cuda_error().decode() if rc == ECUDA else None)
+def _strides(t, H, n, d):
+    """Head and token strides; the stride of a dimension of one element says nothing (torch may
+    give any)."""
+    hs, ts, _ = t.stride()
+    return (hs if H > 1 else n * d), (ts if n > 1 else d)
 
 
-def _rows3(t, name):
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be a [H, N, d] view")
-    return t.shape
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _raise(name, rc):
+    raise FastarError(name, rc, load().fastar_last_cuda_error().decode() if rc == ECUDA else None)
 
 
 def fastar_qk_norm_rope(q, k, q_out, k_out, wq=None, wk=None, eps=1e-6, axes=(0, 0, 0), pos=None, t0=0, t0_dev=None,
@@ -493,57 +485,103 @@ def fastar_qk_norm_rope(q, k, q_out, k_out, wq=None, wk=None, eps=1e-6, axes=(0,
     """RMS norm of every head (weights given) and rotary positions of three axes: q [Hq, n, d]
     -> q_out, k [Hk, n, d] -> k_out (k and k_out None: q alone).  axes: the channels that turn
     with the frame, the row and the column; pos [n, 3] int32, or the grid's positions."""
-    shape = _rows3(q, "q")
-    Hq, n, d = shape
-    dt = q.dtype
+    Hq, n, d = qs = _dims3("q", q)
+    dt, dev = q.dtype, q.get_device()
     code = dtype_code(dt)
-    qp, qhs, qts = _rows("q", q, dt, shape)
-    qo, qohs, qots = _rows("q_out", q_out, dt, shape)
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
-    Hk, kp, khs, kts, ko, kohs, kots = 0, None, 0, 0, None, 0, 0
+    ks = (0 if k is None else k.shape[0], n, d)
+    if not (
+            dev >= 0 and dev == torch._C._cuda_getDevice()
+            and q.stride(2) == 1
+            and q_out.dtype is dt and q_out.shape == qs and q_out.stride(2) == 1 and q_out.get_device() == dev
+            and (k is None or k.dtype is dt and k.shape == ks and k.stride(2) == 1 and k.get_device() == dev
+                 and k_out.dtype is dt and k_out.shape == ks and k_out.stride(2) == 1 and k_out.get_device() == dev)
+            and (wq is None or wq.dtype is _F32 and wq.shape == (d,) and wq.is_contiguous() and wq.get_device() == dev)
+            and (wk is None or wk.dtype is _F32 and wk.shape == (d,) and wk.is_contiguous() and wk.get_device() == dev)
+            and (pos is None or pos.dtype is _I32 and pos.shape == (n, 3) and pos.is_contiguous()
+                 and pos.get_device() == dev)
+            and (t0_dev is None or t0_dev.dtype is _I32 and t0_dev.shape == (1,) and t0_dev.get_device() == dev)):
+        _refuse([("q", q, dt, qs), ("q_out", q_out, dt, qs), ("k", k, dt, ks), ("k_out", k_out, dt, ks)],
+                [("wq", wq, _F32, (d,)), ("wk", wk, _F32, (d,)), ("pos", pos, _I32, (n, 3)),
+                 ("t0_dev", t0_dev, _I32, (1,))])
+    qhs, qts = _strides(q, Hq, n, d)
+    qohs, qots = _strides(q_out, Hq, n, d)
+    khs = kts = kohs = kots = 0
     if k is not None:
-        Hk = k.shape[0]
-        kp, khs, kts = _rows("k", k, dt, (Hk, n, d))
-        ko, kohs, kots = _rows("k_out", k_out, dt, (Hk, n, d))
-    f32, i32 = torch.float32, torch.int32
-    _launch("fastar_qk_norm_rope", stream, (q, q_out, k, k_out, wq, wk, pos, t0_dev), code, n, d, Hq, qp, qhs, qts, qo,
-            qohs, qots, Hk, kp, khs, kts, ko, kohs, kots, _dense("wq", wq, f32, (d,)), _dense("wk", wk, f32, (d,)),
-            eps, axes[0], axes[1], axes[2], _dense("pos", pos, i32, (n, 3)), t0, _dense("t0_dev", t0_dev, i32, (1,)),
-            grid[0], grid[1], theta)
+        khs, kts = _strides(k, ks[0], n, d)
+        kohs, kots = _strides(k_out, ks[0], n, d)
+    rc = (_lib or load()).fastar_qk_norm_rope(
+        code, n, d, Hq, q.data_ptr(), qhs, qts, q_out.data_ptr(), qohs, qots, ks[0], _ptr(k), khs, kts, _ptr(k_out),
+        kohs, kots, _ptr(wq), _ptr(wk), eps, axes[0], axes[1], axes[2], _ptr(pos), t0, _ptr(t0_dev), grid[0], grid[1],
+        theta, _stream(stream, dev))
+    if rc:
+        _raise("fastar_qk_norm_rope", rc)
 
 
 def fastar_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, at=None, len_out=None, dev_status=None, k_exp=None,
                       v_exp=None, stream=None):
     """Rows k, v [H, n, d] into the 4-bit cache (codes [H, cap, d / 2], scales [H, cap, d / 16],
     uint8) from row at[h] on (int32 [H]; None: 0); len_out[h] = at[h] + n."""
-    shape = _rows3(k, "k")
-    H, n, d = shape
-    dt, u8, i32 = k.dtype, torch.uint8, torch.int32
+    H, n, d = rs = _dims3("k", k)
+    dt, dev = k.dtype, k.get_device()
     code = dtype_code(dt)
-    kp, khs, kts = _rows("k", k, dt, shape)
-    vp, vhs, vts = _rows("v", v, dt, shape)
-    cap = _rows3(k_codes, "k_codes")[1]
-    cs, ss = (H, cap, d // 2), (H, cap, d // 16)
-    _launch("fastar_kv4_append", stream,
-            (k, v, k_codes, k_scales, v_codes, v_scales, at, len_out, dev_status, k_exp, v_exp), code, H, n, d, kp, khs,
-            kts, vp, vhs, vts, _dense("k_exp", k_exp, i32, (H,)), _dense("v_exp", v_exp, i32, (H,)),
-            _dense("at", at, i32, (H,)), _dense("k_codes", k_codes, u8, cs), _dense("k_scales", k_scales, u8, ss),
-            _dense("v_codes", v_codes, u8, cs), _dense("v_scales", v_scales, u8, ss), cap,
-            _dense("len_out", len_out, i32, (H,)), _dense("dev_status", dev_status, i32, (1,)))
+    cap = _dims3("k_codes", k_codes)[1]
+    cs, ss, hs = (H, cap, d // 2), (H, cap, d // 16), (H,)
+    if not (
+            dev >= 0 and dev == torch._C._cuda_getDevice()
+            and k.stride(2) == 1
+            and v.dtype is dt and v.shape == rs and v.stride(2) == 1 and v.get_device() == dev
+            and k_codes.dtype is _U8 and k_codes.shape == cs and k_codes.is_contiguous() and k_codes.get_device() == dev
+            and k_scales.dtype is _U8 and k_scales.shape == ss and k_scales.is_contiguous()
+            and k_scales.get_device() == dev
+            and v_codes.dtype is _U8 and v_codes.shape == cs and v_codes.is_contiguous() and v_codes.get_device() == dev
+            and v_scales.dtype is _U8 and v_scales.shape == ss and v_scales.is_contiguous()
+            and v_scales.get_device() == dev
+            and (at is None or at.dtype is _I32 and at.shape == hs and at.is_contiguous() and at.get_device() == dev)
+            and (len_out is None or len_out.dtype is _I32 and len_out.shape == hs and len_out.is_contiguous()
+                 and len_out.get_device() == dev)
+            and (dev_status is None or dev_status.dtype is _I32 and dev_status.shape == (1,)
+                 and dev_status.get_device() == dev)
+            and (k_exp is None or k_exp.dtype is _I32 and k_exp.shape == hs and k_exp.is_contiguous()
+                 and k_exp.get_device() == dev)
+            and (v_exp is None or v_exp.dtype is _I32 and v_exp.shape == hs and v_exp.is_contiguous()
+                 and v_exp.get_device() == dev)):
+        _refuse([("k", k, dt, rs), ("v", v, dt, rs)],
+                [("k_codes", k_codes, _U8, cs), ("k_scales", k_scales, _U8, ss), ("v_codes", v_codes, _U8, cs),
+                 ("v_scales", v_scales, _U8, ss), ("at", at, _I32, hs), ("len_out", len_out, _I32, hs),
+                 ("dev_status", dev_status, _I32, (1,)), ("k_exp", k_exp, _I32, hs), ("v_exp", v_exp, _I32, hs)])
+    khs, kts = _strides(k, H, n, d)
+    vhs, vts = _strides(v, H, n, d)
+    rc = (_lib or load()).fastar_kv4_append(
+        code, H, n, d, k.data_ptr(), khs, kts, v.data_ptr(), vhs, vts, _ptr(k_exp), _ptr(v_exp), _ptr(at),
+        k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), cap, _ptr(len_out),
+        _ptr(dev_status), _stream(stream, dev))
+    if rc:
+        _raise("fastar_kv4_append", rc)
 
 
 def fastar_kv4_read(codes, scales, first, out, exps=None, stream=None):
     """The values of rows first .. first + n of a 4-bit cache -> out [H, n, d]."""
-    shape = _rows3(out, "out")
-    H, n, d = shape
-    code = dtype_code(out.dtype)
-    op, ohs, ots = _rows("out", out, out.dtype, shape)
-    cap = _rows3(codes, "codes")[1]
-    u8 = torch.uint8
-    _launch("fastar_kv4_read", stream, (codes, scales, out, exps), code, H, n, d,
-            _dense("codes", codes, u8, (H, cap, d // 2)), _dense("scales", scales, u8, (H, cap, d // 16)),
-            _dense("exps", exps, torch.int32, (H,)), cap, int(first), op, ohs, ots)
+    H, n, d = rs = _dims3("out", out)
+    dt, dev = out.dtype, out.get_device()
+    code = dtype_code(dt)
+    cap = _dims3("codes", codes)[1]
+    cs, ss = (H, cap, d // 2), (H, cap, d // 16)
+    if not (
+            dev >= 0 and dev == torch._C._cuda_getDevice()
+            and out.stride(2) == 1
+            and codes.dtype is _U8 and codes.shape == cs and codes.is_contiguous() and codes.get_device() == dev
+            and scales.dtype is _U8 and scales.shape == ss and scales.is_contiguous() and scales.get_device() == dev
+            and (exps is None or exps.dtype is _I32 and exps.shape == (H,) and exps.is_contiguous()
+                 and exps.get_device() == dev)):
+        _refuse([("out", out, dt, rs)],
+                [("codes", codes, _U8, cs), ("scales", scales, _U8, ss), ("exps", exps, _I32, (H,))])
+    ohs, ots = _strides(out, H, n, d)
+    rc = (_lib or load()).fastar_kv4_read(code, H, n, d, codes.data_ptr(), scales.data_ptr(), _ptr(exps), cap, int(first),
+                                          out.data_ptr(), ohs, ots, _stream(stream, dev))
+    if rc:
+        _raise("fastar_kv4_read", rc)
 
 
 def fastar_kv4_attn(q, k_codes, k_scales, v_codes, v_scales, lens, scale, out, lse=None, block=0, k_exp=None,
@@ -552,26 +590,46 @@ def fastar_kv4_attn(q, k_codes, k_scales, v_codes, v_scales, lens, scale, out, l
     (Hq a multiple of Hkv); block > 0: the tokens are the cache's last nq rows and see no block
     of that many tokens later than their own.  workspace: workspace_bytes(OP_KV4_ATTN, Hq, nq,
     cap, d, Hkv) bytes (None: the keys are not split)."""
-    shape = _rows3(q, "q")
-    Hq, nq, d = shape
-    dt, u8, i32 = q.dtype, torch.uint8, torch.int32
+    Hq, nq, d = rs = _dims3("q", q)
+    dt, dev = q.dtype, q.get_device()
     code = dtype_code(dt)
-    qp, qhs, qts = _rows("q", q, dt, shape)
-    op, ohs, ots = _rows("out", out, dt, shape)
-    Hkv, cap, _ = _rows3(k_codes, "k_codes")
-    cs, ss = (Hkv, cap, d // 2), (Hkv, cap, d // 16)
-    wp, nb = None, 0
-    if workspace is not None:
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        wp, nb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _launch("fastar_kv4_attn", stream,
-            (q, out, k_codes, k_scales, v_codes, v_scales, lens, lse, k_exp, v_exp, dev_status, workspace), qp, code,
-            Hq, Hkv, nq, d, qhs, qts, _dense("k_codes", k_codes, u8, cs), _dense("k_scales", k_scales, u8, ss),
-            _dense("v_codes", v_codes, u8, cs), _dense("v_scales", v_scales, u8, ss),
-            _dense("k_exp", k_exp, i32, (Hkv,)), _dense("v_exp", v_exp, i32, (Hkv,)), cap,
-            _dense("lens", lens, i32, (Hkv,)), block, scale, op, ohs, ots,
-            _dense("lse", lse, torch.float32, (Hq, nq)), _dense("dev_status", dev_status, i32, (1,)), wp, nb)
+    Hkv, cap, _ = _dims3("k_codes", k_codes)
+    cs, ss, hs = (Hkv, cap, d // 2), (Hkv, cap, d // 16), (Hkv,)
+    if not (
+            dev >= 0 and dev == torch._C._cuda_getDevice()
+            and q.stride(2) == 1
+            and out.dtype is dt and out.shape == rs and out.stride(2) == 1 and out.get_device() == dev
+            and k_codes.dtype is _U8 and k_codes.is_contiguous() and k_codes.shape == cs and k_codes.get_device() == dev
+            and k_scales.dtype is _U8 and k_scales.shape == ss and k_scales.is_contiguous()
+            and k_scales.get_device() == dev
+            and v_codes.dtype is _U8 and v_codes.shape == cs and v_codes.is_contiguous() and v_codes.get_device() == dev
+            and v_scales.dtype is _U8 and v_scales.shape == ss and v_scales.is_contiguous()
+            and v_scales.get_device() == dev
+            and lens.dtype is _I32 and lens.shape == hs and lens.is_contiguous() and lens.get_device() == dev
+            and (lse is None or lse.dtype is _F32 and lse.shape == (Hq, nq) and lse.is_contiguous()
+                 and lse.get_device() == dev)
+            and (dev_status is None or dev_status.dtype is _I32 and dev_status.shape == (1,)
+                 and dev_status.get_device() == dev)
+            and (k_exp is None or k_exp.dtype is _I32 and k_exp.shape == hs and k_exp.is_contiguous()
+                 and k_exp.get_device() == dev)
+            and (v_exp is None or v_exp.dtype is _I32 and v_exp.shape == hs and v_exp.is_contiguous()
+                 and v_exp.get_device() == dev)
+            and (workspace is None or workspace.is_contiguous() and workspace.get_device() == dev)):
+        dense = [("k_codes", k_codes, _U8, cs), ("k_scales", k_scales, _U8, ss), ("v_codes", v_codes, _U8, cs),
+                 ("v_scales", v_scales, _U8, ss), ("lens", lens, _I32, hs), ("lse", lse, _F32, (Hq, nq)),
+                 ("dev_status", dev_status, _I32, (1,)), ("k_exp", k_exp, _I32, hs), ("v_exp", v_exp, _I32, hs)]
+        if workspace is not None:
+            dense.append(("workspace", workspace, workspace.dtype, workspace.shape))
+        _refuse([("q", q, dt, rs), ("out", out, dt, rs)], dense)
+    qhs, qts = _strides(q, Hq, nq, d)
+    ohs, ots = _strides(out, Hq, nq, d)
+    rc = (_lib or load()).fastar_kv4_attn(
+        q.data_ptr(), code, Hq, Hkv, nq, d, qhs, qts, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+        v_scales.data_ptr(), _ptr(k_exp), _ptr(v_exp), cap, lens.data_ptr(), block, scale, out.data_ptr(), ohs, ots,
+        _ptr(lse), _ptr(dev_status), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream, dev))
+    if rc:
+        _raise("fastar_kv4_attn", rc)
 
 
 def fastar_dense_append(k_cur, v_cur, k_cache, v_cache, at, stream=None):
