@@ -230,6 +230,7 @@ size_t kv4_attn_workspace(int d, int Hq, int Hkv, int64_t nq, int64_t cap);
 // False if the workspace is too small for the call's splits (nothing is enqueued).
 bool launch_kv4_attn(int dtype, int d, Kv4AttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s, cudaError_t* err);
 cudaError_t launch_kv4_attn_tc(int d, const Kv4AttnArgs& a, cudaStream_t s);
-cudaError_t launch_kv4_attn_few(int d, const Kv4AttnArgs& a, cudaStream_t s);   // up to 16 rows a KV head
+// bf16: up to 16 rows a KV head; fp32: any
+cudaError_t launch_kv4_attn_few(int dtype, int d, const Kv4AttnArgs& a, cudaStream_t s);
 
 }  // namespace fastar

@@ -1,5 +1,5 @@
 // Softmax attention over the 4-bit cache: the plan (which kernel, how many splits of the
-// keys), the fp32 kernel, and the kernel that joins the splits.
+// keys) and the kernel that joins the splits.
 //
 // The G = Hq / Hkv query heads that share a KV head see the same keys, so the rows of a KV
 // head's work are all (head, token) pairs, r = g * nq + t: the cache is read once for the
@@ -16,149 +16,6 @@
 namespace fastar {
 
 namespace {
-
-// ---- the fp32 kernel -----------------------------------------------------------------------
-// For fp32 queries (bf16 ones go to the tensor cores, kv4_attn_tc.cu): one block takes 8 rows of a KV head
-// and a range of keys, unpacks 64 keys at a time to fp32 in shared memory and forms the 8 x 64
-// logits, their softmax and 8 x d outputs with fp32 arithmetic throughout.  Bound: the fp32
-// units (2 flops a row, key and channel twice over), and below them latency.
-constexpr int kRows = 8, kKeys = 64, kThreadsF = 128;
-
-template <int D>
-struct FSmem {
-  float k[kKeys][D + 4];
-  float v[kKeys][D];
-  float q[kRows][D];
-  float p[kRows][kKeys];
-  float alpha[kRows], l[kRows], m[kRows];
-};
-
-template <int D>
-__global__ void __launch_bounds__(kThreadsF) kv4_attn_f32_kernel(const Kv4AttnArgs a) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  FSmem<D>& sm = *reinterpret_cast<FSmem<D>*>(smem_raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = a.Hq / a.Hkv;
-  const int64_t rows = (int64_t)G * a.nq;
-  const int64_t groups = (rows + kRows - 1) / kRows;
-  int64_t u = blockIdx.x;
-  const int split = (int)(u % a.splits);
-  u /= a.splits;
-  const int64_t r0 = u % groups * kRows;
-  const int h = (int)(u / groups);
-  const int64_t len = kv4::head_len(a.len, h, a.cap, a.status);
-  // the keys that any of the rows sees, cut evenly into whole tiles
-  int64_t most = 0;
-  for (int i = 0; i < kRows; ++i)
-    if (r0 + i < rows) {
-      const int64_t v = kv4::visible(len, a.nq, (r0 + i) % a.nq, a.block);
-      most = v > most ? v : most;
-    }
-  const int64_t tiles = (most + kKeys - 1) / kKeys;
-  const int64_t j0 = tiles * split / a.splits * kKeys;
-  const int64_t j1 = tiles * (split + 1) / a.splits * kKeys < most ? tiles * (split + 1) / a.splits * kKeys : most;
-  const float sl = a.scale * kv4::pow2i(kv4::head_exp(a.k_exp, h));
-
-  for (int i = tid; i < kRows * D; i += kThreadsF) {
-    const int64_t r = r0 + i / D;
-    const int64_t g = r / a.nq;
-    sm.q[i / D][i % D] =
-        r < rows ? static_cast<const float*>(a.q.p)[(h * G + g) * a.q.hs + (r - g * a.nq) * a.q.ts + i % D] : 0.f;
-  }
-  if (tid < kRows) {
-    sm.m[tid] = neg_inf();
-    sm.l[tid] = 0.f;
-  }
-  constexpr int CPT = kRows * D / kThreadsF;     // outputs of a thread: one channel, CPT rows
-  const int oc = tid % D, or0 = tid / D * CPT;
-  float o[CPT];
-#pragma unroll
-  for (int i = 0; i < CPT; ++i) o[i] = 0.f;
-
-  for (int64_t j = j0; j < j1; j += kKeys) {
-    __syncthreads();
-    const int nk = (int)(j1 - j < kKeys ? j1 - j : kKeys);
-    for (int i = tid; i < kKeys * (D / 8); i += kThreadsF) {
-      const int row = i / (D / 8), c = i % (D / 8);
-      uint32_t pk[4] = {0, 0, 0, 0}, pv[4] = {0, 0, 0, 0};   // rows past the range count as 0
-      if (row < nk) {
-        const int64_t at = (int64_t)h * a.cap + j + row;
-        kv4::unpack8(reinterpret_cast<const uint32_t*>(a.kc)[at * (D / 8) + c],
-                     kv4::scale_f16x2(a.ks[at * (D / 16) + c / 2]), pk);
-        kv4::unpack8(reinterpret_cast<const uint32_t*>(a.vc)[at * (D / 8) + c],
-                     kv4::scale_f16x2(a.vs[at * (D / 16) + c / 2]), pv);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 x = kv4::f16x2_to_f32(pk[e]), y = kv4::f16x2_to_f32(pv[e]);
-        *reinterpret_cast<float2*>(&sm.k[row][c * 8 + 2 * e]) = x;
-        *reinterpret_cast<float2*>(&sm.v[row][c * 8 + 2 * e]) = y;
-      }
-    }
-    __syncthreads();
-    // warp w: rows 2w and 2w + 1; lane: keys lane and lane + 32
-#pragma unroll
-    for (int rr = 0; rr < 2; ++rr) {
-      const int row = warp * 2 + rr;
-      const int64_t r = r0 + row;
-      const int64_t see = r < rows ? kv4::visible(len, a.nq, r % a.nq, a.block) - j : 0;
-      float s0 = 0.f, s1 = 0.f;
-#pragma unroll 8
-      for (int c = 0; c < D; c += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(&sm.q[row][c]);
-        const float4 k0 = *reinterpret_cast<const float4*>(&sm.k[lane][c]);
-        const float4 k1 = *reinterpret_cast<const float4*>(&sm.k[lane + 32][c]);
-        s0 = fmaf(x.x, k0.x, fmaf(x.y, k0.y, fmaf(x.z, k0.z, fmaf(x.w, k0.w, s0))));
-        s1 = fmaf(x.x, k1.x, fmaf(x.y, k1.y, fmaf(x.z, k1.z, fmaf(x.w, k1.w, s1))));
-      }
-      const int64_t lim = see < nk ? see : nk;
-      s0 = lane < lim ? s0 * sl : neg_inf();
-      s1 = lane + 32 < lim ? s1 * sl : neg_inf();
-      float mx = fmaxf(s0, s1);
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-      const float mo = sm.m[row], mn = fmaxf(mo, mx);
-      const float ref = mn == neg_inf() ? 0.f : mn;
-      const float p0 = expf(s0 - ref), p1 = expf(s1 - ref);
-      const float al = expf(mo - ref);
-      const float sum = warp_sum(p0 + p1);
-      sm.p[row][lane] = p0;
-      sm.p[row][lane + 32] = p1;
-      __syncwarp();
-      if (lane == 0) {
-        sm.alpha[row] = al;
-        sm.l[row] = sm.l[row] * al + sum;
-        sm.m[row] = mn;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < CPT; ++i) o[i] *= sm.alpha[or0 + i];
-#pragma unroll 4
-    for (int key = 0; key < kKeys; ++key) {
-      const float v = sm.v[key][oc];
-#pragma unroll
-      for (int i = 0; i < CPT; ++i) o[i] = fmaf(sm.p[or0 + i][key], v, o[i]);
-    }
-  }
-  __syncthreads();
-  const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
-#pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    const int64_t r = r0 + or0 + i;
-    if (r >= rows) continue;
-    const int64_t g = r / a.nq, t = r - g * a.nq, head = h * G + g;
-    const float l = sm.l[or0 + i], m = sm.m[or0 + i];
-    if (a.splits > 1) {
-      const int64_t at = (split * (int64_t)a.Hq + head) * a.nq + t;
-      a.part_o[at * D + oc] = o[i] * up;
-      if (oc == 0) a.part_ml[at] = make_float2(m, l);
-    } else {
-      static_cast<float*>(a.out)[head * a.o_hs + t * a.o_ts + oc] = l > 0.f || l != l ? o[i] * up / l : 0.f;
-      if (oc == 0 && a.lse) a.lse[head * a.nq + t] = l > 0.f || l != l ? m + logf(l) : neg_inf();
-    }
-  }
-}
 
 // ---- joining the splits ----------------------------------------------------------------------
 // O = sum_s e^(m_s - m) o_s / sum_s e^(m_s - m) l_s over a row's S partials, m = max_s m_s; one
@@ -261,34 +118,14 @@ cudaError_t join_go(const Kv4AttnArgs& a, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int D>
-cudaError_t f32_go(const Kv4AttnArgs& a, cudaStream_t s) {
-  const int64_t rows = (int64_t)(a.Hq / a.Hkv) * a.nq;
-  const int64_t blocks = (rows + kRows - 1) / kRows * a.Hkv * a.splits;
-  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = opt_in_smem((const void*)kv4_attn_f32_kernel<D>, (int)sizeof(FSmem<D>));
-  if (e != cudaSuccess) return e;
-  kv4_attn_f32_kernel<D><<<(unsigned)blocks, kThreadsF, sizeof(FSmem<D>), s>>>(a);
-  count_launches(1);
-  const cudaError_t r = cudaGetLastError();
-  return r != cudaSuccess || a.splits == 1 ? r : join_go<float, D>(a, s);
-}
-
-// Splits of the keys for the fp32 kernel: two blocks a multiprocessor, none under 256 keys.
-int splits_f32(int64_t blocks, int64_t cap) {
-  const int64_t want = (2 * (int64_t)sm_count() + blocks - 1) / blocks;
-  const int64_t most = cap / 256;
-  int64_t s = want < most ? want : most;
-  if (s > kKv4MaxSplits) s = kKv4MaxSplits;
-  return s < 1 ? 1 : (int)s;
-}
-
-// Rows of a KV head that take the few-rows kernel (kv4_attn_few.cu).
+// Rows of a KV head that take the few-rows kernel (kv4_attn_few.cu) in bf16; in fp32 all do.
 constexpr int64_t kFewRows = 16;
 
-// Splits for it: one CTA a multiprocessor, but none under 512 keys (64 a warp).
-int splits_few(int Hkv, int64_t cap) {
-  const int64_t want = sm_count() / Hkv, most = cap / 512;
+// Splits for it: one CTA a multiprocessor, but none under 1024 keys, two blocks a warp (what a
+// split saves below that, the join costs).  items: KV heads, in fp32
+// times groups of 8 rows.
+int splits_few(int64_t items, int64_t cap) {
+  const int64_t want = sm_count() / items, most = cap / 1024;
   int64_t s = want < most ? want : most;
   if (s > kKv4MaxSplits) s = kKv4MaxSplits;
   return s < 1 ? 1 : (int)s;
@@ -337,11 +174,11 @@ cudaError_t run(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStream_t s) {
     a.part_o = static_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * a.Hq * a.nq * d);
   }
-  if (dtype == FASTAR_F32) return d == 128 ? f32_go<128>(a, s) : f32_go<64>(a, s);
-  const bool few = (int64_t)(a.Hq / a.Hkv) * a.nq <= kFewRows;
+  const bool few = dtype == FASTAR_F32 || (int64_t)(a.Hq / a.Hkv) * a.nq <= kFewRows;
   if (!few && a.min_tiles == 0) a.min_tiles = 1;         // one split
-  const cudaError_t e = few ? launch_kv4_attn_few(d, a, s) : launch_kv4_attn_tc(d, a, s);
+  const cudaError_t e = few ? launch_kv4_attn_few(dtype, d, a, s) : launch_kv4_attn_tc(d, a, s);
   if (e != cudaSuccess || a.splits == 1) return e;
+  if (dtype == FASTAR_F32) return d == 128 ? join_go<float, 128>(a, s) : join_go<float, 64>(a, s);
   return d == 128 ? join_go<__nv_bfloat16, 128>(a, s) : join_go<__nv_bfloat16, 64>(a, s);
 }
 
@@ -349,9 +186,8 @@ cudaError_t run(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStream_t s) {
 
 int kv4_attn_splits(int dtype, int d, int Hq, int Hkv, int64_t nq, int64_t cap, int* min_tiles) {
   const int64_t rows = (int64_t)(Hq / Hkv) * nq;
-  if (dtype == FASTAR_BF16 && rows > kFewRows) return splits_tc(d, rows, Hkv, cap, min_tiles);
-  if (dtype == FASTAR_BF16) return splits_few(Hkv, cap);
-  return splits_f32((rows + kRows - 1) / kRows * Hkv, cap);
+  if (dtype == FASTAR_F32) return splits_few((rows + 7) / 8 * Hkv, cap);
+  return rows <= kFewRows ? splits_few(Hkv, cap) : splits_tc(d, rows, Hkv, cap, min_tiles);
 }
 
 size_t kv4_attn_workspace(int d, int Hq, int Hkv, int64_t nq, int64_t cap) {

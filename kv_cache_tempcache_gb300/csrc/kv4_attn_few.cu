@@ -1,5 +1,5 @@
-// Softmax attention over the 4-bit cache for few rows: up to 16 (query head, token) pairs of a KV
-// head, as in single-token steps.
+// Softmax attention over the 4-bit cache for few rows, as in single-token steps: up to 16 (query
+// head, token) pairs of a KV head in bf16; and for fp32 queries, 8 rows a CTA.
 //
 // Bound: the cache's bytes.  A row tile of the tcgen05 kernel is 128 or 256 rows, so with a few
 // rows it spends most of its time unpacking for products that are nearly empty; here the rows
@@ -17,7 +17,11 @@
 // shared memory, in warp order, at the end, and the CTAs' by the join kernel.
 // (With the rows as the products' 16 rows, half of them empty up to 8, 8 warps of 250 registers
 // waited for one another's latencies: one token over 131,071 rows of 8 heads 45 us.)
-// Queries, P and references as in the tcgen05 kernel (kv4_attn_tc.cu): fp16 rows at a power of
+// fp32: a query row (24 bits) is three fp16 rows, P two (22 bits), each a product of its own on
+// the codes unpacked once; the unpacking, not the products, is most of the work.  The reference
+// lies 14 below the maximum there, so that P's parts keep 22 bits down to 2^-17 of the largest
+// and 2^-39 of it below.
+// Queries, P and references otherwise as in the tcgen05 kernel (kv4_attn_tc.cu): fp16 rows at a power of
 // two, P in fp16 against a reference that moves only when a P would pass 2^15.
 #include <climits>
 
@@ -34,9 +38,10 @@ namespace {
 constexpr int kKeysW = 32;
 
 // NR: groups of 8 rows.
-template <int D, int NR>
+template <typename T, int D, int NR>
 struct FewLayout {
-  static constexpr int warps = NR == 1 ? 16 : 8, stages = NR == 1 ? 3 : 6;
+  static constexpr bool f32 = sizeof(T) == 4;
+  static constexpr int warps = NR == 1 && !f32 ? 16 : 8, stages = NR == 1 && !f32 ? 3 : 6;
   static constexpr int codes = kKeysW * D / 2, scales = kKeysW * D / 16;
   static constexpr int stage = 2 * (codes + scales);                 // K codes, V codes, K scales, V scales
   static constexpr int ring = warps * stages * stage;
@@ -102,44 +107,54 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return r;
 }
 
-// A lane's share of query row r (channels t D/4 ..) as product operands: qb[s] of step s; returns
-// the row's logit scale in log2 units.
-template <int D>
-__device__ __forceinline__ float load_q(const Kv4AttnArgs& a, int h, int rows, int r, int t, uint32_t (*qb)[2]) {
+// A lane's share of query row r (channels t D/4 ..) as product operands: qb[part][s] of step s;
+// returns the row's logit scale in log2 units.
+template <typename T, int D, int QP>
+__device__ __forceinline__ float load_q(const Kv4AttnArgs& a, int h, uint32_t rows, uint32_t r, int t,
+                                        uint32_t (*qb)[D / 16][2]) {
   constexpr int CH = D / 4;                 // channels of this lane
-  uint32_t x[CH / 2];
-  uint32_t big = 0;
+  float x[CH];
+  uint32_t big = 0;                         // the largest magnitude's bits
   if (r < rows) {
-    const uint32_t nq = (uint32_t)a.nq, gh = (uint32_t)r / nq;
+    const uint32_t nq = (uint32_t)a.nq, gh = r / nq;
     const int64_t head = h * (int64_t)(a.Hq / a.Hkv) + gh;
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + head * a.q.hs +
-                                                      (int64_t)((uint32_t)r - gh * nq) * a.q.ts + t * CH);
+    const T* src = static_cast<const T*>(a.q.p) + head * a.q.hs + (int64_t)(r - gh * nq) * a.q.ts + t * CH;
 #pragma unroll
-    for (int i = 0; i < CH / 8; ++i) {
-      const uint4 u = src[i];
-      x[4 * i] = u.x, x[4 * i + 1] = u.y, x[4 * i + 2] = u.z, x[4 * i + 3] = u.w;
-    }
+    for (int i = 0; i < CH; i += 8) load8(src + i, x + i);
   } else {
 #pragma unroll
-    for (int i = 0; i < CH / 2; ++i) x[i] = 0;
+    for (int i = 0; i < CH; ++i) x[i] = 0.f;
   }
 #pragma unroll
-  for (int i = 0; i < CH / 2; ++i) big = max(big, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
+  for (int i = 0; i < CH; ++i) big = max(big, __float_as_uint(x[i]) & 0x7fffffffu);
   big = quad_max(big);
-  const int ex = (int)(big >> 7);
+  const int ex = (int)(big >> 23);
   int qe = ex == 0 ? -126 - 12 : ex - 127 - 12;
   if (qe < -120) qe = -120;
   if (big == 0 || ex == 255) qe = 0;
   const float down = kv4::pow2i(-qe);
 #pragma unroll
-  for (int i = 0; i < CH / 2; ++i)          // pair i of the lane's channels: step i / 2, first or second pair
-    qb[i >> 1][i & 1] = pack_f16w(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xffff0000u) * down);
-  return fmaxf(a.scale * kv4::pow2i(qe) * kv4::pow2i(kv4::head_exp(a.k_exp, h)) * 1.4426950408889634f, 1.2e-38f);
+  for (int i = 0; i < CH / 2; ++i) {        // pair i of the lane's channels: step i / 2, first or second pair
+    float a0 = x[2 * i] * down, a1 = x[2 * i + 1] * down;
+#pragma unroll
+    for (int part = 0; part < QP; ++part) {
+      const uint32_t p = pack_f16w(a0, a1);
+      qb[part][i >> 1][i & 1] = p;
+      const float2 f = kv4::f16x2_to_f32(p);
+      a0 -= f.x;
+      a1 -= f.y;
+    }
+  }
+  // a product of scales outside fp32's range: positive and finite
+  return fminf(fmaxf(a.scale * kv4::pow2i(qe) * kv4::pow2i(kv4::head_exp(a.k_exp, h)) * 1.4426950408889634f, 1.2e-38f),
+               3.0e38f);
 }
 
-template <int D, int NR>
-__global__ void __launch_bounds__(FewLayout<D, NR>::warps * 32, 1) kv4_attn_few_kernel(const Kv4AttnArgs a) {
-  using Lay = FewLayout<D, NR>;
+template <typename T, int D, int NR>
+__global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_few_kernel(const Kv4AttnArgs a) {
+  using Lay = FewLayout<T, D, NR>;
+  constexpr int QP = Lay::f32 ? 3 : 1, PP = Lay::f32 ? 2 : 1;        // fp16 parts of Q and of P
+  constexpr float kTop = Lay::f32 ? 14.f : 0.f;                      // log2 of the largest P at first
   constexpr int W = Lay::warps, ST = Lay::stages, MT = D / 16;       // MT: row tiles of O^T
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~(uintptr_t)127);
@@ -147,10 +162,14 @@ __global__ void __launch_bounds__(FewLayout<D, NR>::warps * 32, 1) kv4_attn_few_
   float2* wml = reinterpret_cast<float2*>(bars + W * ST);            // [warp][8 NR]
   int* abort_flag = reinterpret_cast<int*>(wml + W * 8 * NR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int split = (int)(blockIdx.x % (uint32_t)a.splits), h = (int)(blockIdx.x / (uint32_t)a.splits);
-  const int rows = (a.Hq / a.Hkv) * (int)a.nq;
-  // the last key any row sees: with blocks, that of the last token, which some row is: all of them
-  const int64_t len = kv4::head_len(a.len, h, a.cap, a.status);
+  const uint32_t rows = (uint32_t)(a.Hq / a.Hkv) * (uint32_t)a.nq, groups = (rows + 8 * NR - 1) / (8 * NR);
+  const int split = (int)(blockIdx.x % (uint32_t)a.splits);
+  const uint32_t gr = blockIdx.x / (uint32_t)a.splits % groups;
+  const int h = (int)(blockIdx.x / ((uint32_t)a.splits * groups));
+  const uint32_t r0 = gr * 8 * NR, rlast = (r0 + 8 * NR < rows ? r0 + 8 * NR : rows) - 1;
+  // the keys that any of the rows sees
+  const int64_t cached = kv4::head_len(a.len, h, a.cap, a.status);
+  const int64_t len = kv4::item_keys(cached, (uint32_t)a.nq, a.block, r0, rlast, 1, 1).most;
   const uint32_t blocks = (uint32_t)((len + kKeysW - 1) / kKeysW);
   const uint32_t b0 = (uint32_t)((uint64_t)blocks * split / (uint32_t)a.splits);
   const uint32_t b1 = (uint32_t)((uint64_t)blocks * (split + 1) / (uint32_t)a.splits);
@@ -181,17 +200,17 @@ __global__ void __launch_bounds__(FewLayout<D, NR>::warps * 32, 1) kv4_attn_few_
     for (int i = 0; i < ST && i < count; ++i) fetch(i, i);
   __syncthreads();                          // the barriers and the flag are set for every lane
 
-  uint32_t qb[NR][D / 16][2];
+  uint32_t qb[NR][QP][D / 16][2];
   float sl2[NR][2], m[NR][2], l[NR][2];     // of rows 2t and 2t + 1 of each group
   int see[NR][2];                           // how many keys they see
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
-    const float s = load_q<D>(a, h, rows, 8 * n + g, t, qb[n]);
+    const float s = load_q<T, D, QP>(a, h, rows, r0 + 8 * n + g, t, qb[n]);
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       sl2[n][p] = __shfl_sync(0xffffffffu, s, (2 * t + p) * 4);
-      const uint32_t r = (uint32_t)(8 * n + 2 * t + p), nq = (uint32_t)a.nq;
-      see[n][p] = (int)((int)r < rows ? kv4::visible(len, a.nq, r % nq, a.block) : len);
+      const uint32_t r = r0 + (uint32_t)(8 * n + 2 * t + p), nq = (uint32_t)a.nq;
+      see[n][p] = (int)(r < rows ? kv4::visible(cached, a.nq, r % nq, a.block) : len);
       m[n][p] = l[n][p] = 0.f;
     }
   }
@@ -248,7 +267,8 @@ __global__ void __launch_bounds__(FewLayout<D, NR>::warps * 32, 1) kv4_attn_few_
 #pragma unroll
         for (int q = 0; q < D / 16; ++q) {
           const uint32_t ka[4] = {kf[0][2 * q], kf[1][2 * q], kf[0][2 * q + 1], kf[1][2 * q + 1]};
-          mma16816(u[q & 1], ka, qb[n][q][0], qb[n][q][1]);
+#pragma unroll
+          for (int part = 0; part < QP; ++part) mma16816(u[(q + part) & 1], ka, qb[n][part][q][0], qb[n][part][q][1]);
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[n][kt][x] = u[0][x] + u[1][x];
@@ -281,7 +301,7 @@ __global__ void __launch_bounds__(FewLayout<D, NR>::warps * 32, 1) kv4_attn_few_
       for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const float mx = group_max(mt[n][p]);
+          const float mx = group_max(mt[n][p]) - kTop;
           float f = 1.f;
           if (i == 0) {
             m[n][p] = mx == neg_inf() ? 0.f : mx;
@@ -294,18 +314,25 @@ __global__ void __launch_bounds__(FewLayout<D, NR>::warps * 32, 1) kv4_attn_few_
           for (int x = 0; x < MT; ++x) o[n][x][p] *= f, o[n][x][2 + p] *= f;
         }
     }
-    uint32_t pb[NR][2][2];
+    uint32_t pb[NR][PP][2][2];
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float e0 = ex2w(fmaf(s[n][kt][2 * e], sl2[n][0], -m[n][0]));
-          const float e1 = ex2w(fmaf(s[n][kt][2 * e + 1], sl2[n][1], -m[n][1]));
+          float e0 = ex2w(fmaf(s[n][kt][2 * e], sl2[n][0], -m[n][0]));
+          float e1 = ex2w(fmaf(s[n][kt][2 * e + 1], sl2[n][1], -m[n][1]));
           l[n][0] += e0;
           l[n][1] += e1;
-          pb[n][kt][e] = transpose8(pack_f16w(e0, e1));
+#pragma unroll
+          for (int part = 0; part < PP; ++part) {
+            const uint32_t x = pack_f16w(e0, e1);
+            pb[n][part][kt][e] = transpose8(x);
+            const float2 y = kv4::f16x2_to_f32(x);
+            e0 -= y.x;
+            e1 -= y.y;
+          }
         }
     // ---- O^T += V^T P^T: a lane's keys 2t, 2t + 1, 2t + 8, 2t + 9 of 16, channels g D/8 .. ----
 #pragma unroll
@@ -340,7 +367,9 @@ __global__ void __launch_bounds__(FewLayout<D, NR>::warps * 32, 1) kv4_attn_few_
 #pragma unroll
       for (int x = 0; x < MT; ++x)
 #pragma unroll
-        for (int n = 0; n < NR; ++n) mma16816(o[n][x], va[x], pb[n][kt][0], pb[n][kt][1]);
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int part = 0; part < PP; ++part) mma16816(o[n][x], va[x], pb[n][part][kt][0], pb[n][part][kt][1]);
     }
     __syncwarp();                           // every lane has read the block
     if (lane == 0 && i + ST < count) fetch(i + ST, stage);
@@ -375,14 +404,14 @@ __global__ void __launch_bounds__(FewLayout<D, NR>::warps * 32, 1) kv4_attn_few_
       const float f = l[n][p] != 0.f ? ex2w(m[n][p] - top(r)) : 0.f;
       // a lane's channels g D/8 + 2 x and + 2 x + 1 of row r
       float4* dst = reinterpret_cast<float4*>(red + (warp * 8 * NR + r) * D + g * (D / 8));
-      if (r < rows)
+      if (r0 + r <= rlast)
 #pragma unroll
         for (int x = 0; x < MT; x += 2)
           dst[x >> 1] = make_float4(o[n][x][p] * f, o[n][x][2 + p] * f, o[n][x + 1][p] * f, o[n][x + 1][2 + p] * f);
     }
   __syncthreads();
   const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
-  for (int x = threadIdx.x; x < rows * (D / 4); x += W * 32) {
+  for (int x = threadIdx.x; x < (int)(rlast - r0 + 1) * (D / 4); x += W * 32) {
     const int r = x / (D / 4), c = x % (D / 4) * 4;
     const float mx = top(r);
     float sum = 0.f;
@@ -396,8 +425,8 @@ __global__ void __launch_bounds__(FewLayout<D, NR>::warps * 32, 1) kv4_attn_few_
       acc.x += z.x, acc.y += z.y, acc.z += z.z, acc.w += z.w;
     }
     const bool live = sum > 0.f || sum != sum;
-    const uint32_t nq = (uint32_t)a.nq, gh = (uint32_t)r / nq;
-    const int64_t head = h * (int64_t)(a.Hq / a.Hkv) + gh, tok = (uint32_t)r - gh * nq;
+    const uint32_t nq = (uint32_t)a.nq, gh = (r0 + (uint32_t)r) / nq;
+    const int64_t head = h * (int64_t)(a.Hq / a.Hkv) + gh, tok = r0 + (uint32_t)r - gh * nq;
     const float mn = mx * 0.6931471805599453f;
     if (a.splits > 1) {
       const int64_t at = (split * (int64_t)a.Hq + head) * a.nq + tok;
@@ -405,33 +434,39 @@ __global__ void __launch_bounds__(FewLayout<D, NR>::warps * 32, 1) kv4_attn_few_
       if (c == 0) a.part_ml[at] = make_float2(live ? mn : neg_inf(), sum);
     } else {
       const float f = live ? up / sum : 0.f;
-      __nv_bfloat162 v[2] = {__floats2bfloat162_rn(acc.x * f, acc.y * f), __floats2bfloat162_rn(acc.z * f, acc.w * f)};
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + head * a.o_hs + tok * a.o_ts + c) =
-          *reinterpret_cast<uint2*>(v);
+      T* dst = static_cast<T*>(a.out) + head * a.o_hs + tok * a.o_ts + c;
+      if (Lay::f32) {
+        *reinterpret_cast<float4*>(dst) = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+      } else {
+        __nv_bfloat162 v[2] = {__floats2bfloat162_rn(acc.x * f, acc.y * f), __floats2bfloat162_rn(acc.z * f, acc.w * f)};
+        *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(v);
+      }
       if (c == 0 && a.lse) a.lse[head * a.nq + tok] = live ? mn + logf(sum) : neg_inf();
     }
   }
   if (threadIdx.x == 0 && *abort) flag_status(a.status, FASTAR_DEV_TIMEOUT);
 }
 
-template <int D, int NR>
+template <typename T, int D, int NR>
 cudaError_t few_go(const Kv4AttnArgs& a, cudaStream_t s) {
-  using Lay = FewLayout<D, NR>;
-  const int64_t blocks = (int64_t)a.Hkv * a.splits;
+  using Lay = FewLayout<T, D, NR>;
+  const int64_t rows = (int64_t)(a.Hq / a.Hkv) * a.nq;
+  const int64_t blocks = (rows + 8 * NR - 1) / (8 * NR) * a.Hkv * a.splits;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = opt_in_smem((const void*)kv4_attn_few_kernel<D, NR>, Lay::bytes);
+  const cudaError_t e = opt_in_smem((const void*)kv4_attn_few_kernel<T, D, NR>, Lay::bytes);
   if (e != cudaSuccess) return e;
-  kv4_attn_few_kernel<D, NR><<<(unsigned)blocks, Lay::warps * 32, Lay::bytes, s>>>(a);
+  kv4_attn_few_kernel<T, D, NR><<<(unsigned)blocks, Lay::warps * 32, Lay::bytes, s>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_attn_few(int d, const Kv4AttnArgs& a, cudaStream_t s) {
+cudaError_t launch_kv4_attn_few(int dtype, int d, const Kv4AttnArgs& a, cudaStream_t s) {
+  if (dtype == FASTAR_F32) return d == 128 ? few_go<float, 128, 1>(a, s) : few_go<float, 64, 1>(a, s);
   const bool two = (int64_t)(a.Hq / a.Hkv) * a.nq > 8;
-  if (d == 128) return two ? few_go<128, 2>(a, s) : few_go<128, 1>(a, s);
-  return two ? few_go<64, 2>(a, s) : few_go<64, 1>(a, s);
+  if (d == 128) return two ? few_go<__nv_bfloat16, 128, 2>(a, s) : few_go<__nv_bfloat16, 128, 1>(a, s);
+  return two ? few_go<__nv_bfloat16, 64, 2>(a, s) : few_go<__nv_bfloat16, 64, 1>(a, s);
 }
 
 }  // namespace fastar

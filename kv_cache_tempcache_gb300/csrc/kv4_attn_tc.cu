@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     }
     tc::named_bar(9, kSoftWarps * 32);
     float sl2 = a.scale * sm.ex[0][both ? 0 : w][row] * kv4::pow2i(kv4::head_exp(a.k_exp, h)) * 1.4426950408889634f;
-    sl2 = fmaxf(sl2, 1.2e-38f);            // a product of scales under fp32's range: still positive
+    sl2 = fminf(fmaxf(sl2, 1.2e-38f), 3.0e38f);   // a product of scales outside fp32's range: positive and finite
     tc::named_bar(9, kSoftWarps * 32);     // ex is used again below
     // keys the row sees from this thread's first on (a row that is not there: as the last)
     int64_t left = (has ? kv4::visible(len, a.nq, at.t, a.block) : most) - j0 * kKT - half * 64 - (both ? w * kKT : 0);

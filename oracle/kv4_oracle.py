@@ -37,7 +37,7 @@ def quantise(x, e=0):
 
 def values(codes, scales, e=0):
     """The rows [..., d] that codes and scales stand for."""
-    c = np.stack((codes & 15, codes >> 4), -1).reshape(*codes.shape[:-1], -1)
+    c = np.stack((codes & 15, codes >> 4), -1).reshape(*codes.shape[:-1], 2 * codes.shape[-1])
     v = np.where(c >= 8, -1.0, 1.0) * E2M1[c & 7]
     return v * np.repeat(E4M3[scales], 16, axis=-1) * 2.0 ** e
 

@@ -13,10 +13,13 @@ under the softmax), E = sum_c |q_c| max_j |k_jc| * scale (no logit's products su
     however little the other v add up to in that channel (where the strongest key's value is a
     stored 0, O is made of small p alone).  It is at most 2^-25 sum_j |v_j| over a sum of p that
     is at least 1 (the reference maximum was some key's logit, whose p is 1, or is below one);
+  - fp32 calls hold p in two fp16 parts of 22 bits (2^-22 relative, in 2 e's doubled terms: n 2^-22
+    covers it), and the small ones, whose second part lies below fp16's range, to 2^-25 of a scale
+    on which the largest p is at least 2^13: 2^-38 sum_j |v_j|;
   - an exponential under fp32's range is 0: 2^-126 sum_j |v_j| in the same way;
   - sums over n keys in fp32: n 2^-23 relative at most;
   - the output's rounding: 2^-8 |O| in bf16, 2^-24 |O| in fp32.
-  |O - want| <= half |want| + A (4 e + n 2^-22 + [bf16] 2^-11) + sum_j |v_j| ([bf16] 2^-25 + 2^-126)
+  |O - want| <= half |want| + A (4 e + n 2^-22 + [bf16] 2^-11) + sum_j |v_j| ([bf16] 2^-25, [fp32] 2^-38)
   |lse - want| <= 2 e + n 2^-22 + 2^-22 (1 + |want|)."""
 import math
 
@@ -211,7 +214,7 @@ def _check_attn(out, lse, q, kv, vv, lens, scale, block):
     tol = half * np.abs(want) + A * (4 * e + n * 2.0 ** -22 + (2.0 ** -11 if bf16 else 0))[..., None]
     lost = np.stack([np.abs(vv[h * len(lens) // q.shape[0], :lens[h * len(lens) // q.shape[0]]]).sum(0)
                      for h in range(q.shape[0])])
-    tol += lost[:, None] * ((2.0 ** -25 if bf16 else 0) + 2.0 ** -126)
+    tol += lost[:, None] * ((2.0 ** -25 if bf16 else 2.0 ** -38) + 2.0 ** -126)
     err = np.abs(_np(out) - want)
     assert not np.isnan(err).any()
     assert (err <= tol).all(), f"{int((err > tol).sum())} of {err.size} outside; worst ratio {(err / np.maximum(tol, 1e-300)).max():.2f}"
@@ -277,6 +280,55 @@ def test_many_rows(Hkv, G, nq, d, cap, lens, block):
     c = _filled(Hkv, cap, d, cap + nq)
     q = _rand((nq, Hkv * G, d), nq, 1.5).bfloat16().transpose(0, 1)
     _attend(q, c, lens, block)
+
+
+@pytest.mark.parametrize("Hkv,G,nq,d,cap,lens,block", [
+    (1, 1, 300, 128, 912, [899], 100), (2, 2, 90, 64, 2064, [2050, 0], 1), (3, 1, 17, 128, 3008, [3000, 5, 1025], 0)])
+def test_many_fp32_rows(Hkv, G, nq, d, cap, lens, block):
+    c = _filled(Hkv, cap, d, cap + nq)
+    q = _rand((nq, Hkv * G, d), nq, 1.5).transpose(0, 1)
+    _attend(q, c, lens, block)
+
+
+@pytest.mark.parametrize("nq,block", [(1100, 0), (1100, 500), (2100, 0), (2100, 500)])
+def test_splits_follow_the_lengths(nq, block):
+    # heads that fill the cache, half fill it, need no split, hold less than the call's tokens, or
+    # nothing; the last rows of a head fill one row tile; with 2100 tokens the keys are split
+    H, d, cap = 24, 128, 16000
+    lens = [200 + 37 * h for h in range(H)]
+    lens[:6] = [16000, 11000, 0, 1, 1099, 5200]
+    c = _empty_cache(H, cap, d)
+    x = _rand((2, H, 1100, d), 40).bfloat16()
+    for at in range(0, 15400, 1100):                       # the same rows over and over, scaled
+        y = (x * (1 + at / 20000)).bfloat16()
+        L.fastar_kv4_append(y[0], y[1], *c, _i32([at] * H))
+    n = 16000 - 15400
+    L.fastar_kv4_append(x[0, :, :n], x[1, :, :n], *c, _i32([15400] * H))
+    q = _rand((nq, H, d), 41, 1.5).bfloat16().transpose(0, 1)
+    assert nq == 1100 or L.workspace_bytes(L.OP_KV4_ATTN, H, nq, cap, d, H) > 0
+    vals = [np.zeros((H, cap, d)) for _ in range(2)]
+    for i in range(2):
+        codes, scales = c[2 * i].cpu().numpy(), c[2 * i + 1].cpu().numpy()
+        for h, m in enumerate(lens):
+            vals[i][h, :m] = K.values(codes[h, :m], scales[h, :m])
+    a = _attend(q, c, lens, block, vals)
+    b = _attend(q, c, lens, block, vals, split=(True,))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_a_zero_query_under_the_largest_scales():
+    c = _filled(1, 64, 64, 50)
+    for nq in (2, 200):
+        for dt in (torch.bfloat16, torch.float32):
+            q = torch.zeros(1, nq, 64, dtype=dt, device=DEV)
+            out, lse = torch.empty_like(q), torch.empty(1, nq, device=DEV)
+            L.fastar_kv4_attn(q, *c, _i32([61]), 2.9e38, out, lse, k_exp=_i32([64]))
+            torch.cuda.synchronize()
+            want = K.values(c[2][0, :61].cpu().numpy(), c[3][0, :61].cpu().numpy()).mean(0)
+            # uniform weights: 61 fp32 products and sums (61 2^-23), and the output's rounding
+            half = 2.0 ** -8 if dt == torch.bfloat16 else 2.0 ** -24
+            assert (np.abs(_np(out)[0] - want) <= half * np.abs(want) + 61 * 2.0 ** -22 * 6).all()
+            assert (np.abs(_np(lse) - math.log(61)) <= 2.0 ** -20).all()
 
 
 @pytest.mark.parametrize("dtype,nq", [("f32", 5), ("bf16", 1), ("bf16", 5), ("bf16", 300)])
