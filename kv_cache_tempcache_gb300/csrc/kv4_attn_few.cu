@@ -18,9 +18,9 @@
 // (With the rows as the products' 16 rows, half of them empty up to 8, 8 warps of 250 registers
 // waited for one another's latencies: one token over 131,071 rows of 8 heads 45 us.)
 // fp32: a query row (24 bits) is three fp16 rows, P two (22 bits), each a product of its own on
-// the codes unpacked once; the unpacking, not the products, is most of the work.  The reference
-// lies 14 below the maximum there, so that P's parts keep 22 bits down to 2^-17 of the largest
-// and 2^-39 of it below.
+// the codes unpacked once; the unpacking, not the products, is most of the work.  P goes into
+// its parts times 2^14, so that they keep 22 bits down to 2^-17 of the largest and 2^-39 of it
+// below.
 // Queries, P and references otherwise as in the tcgen05 kernel (kv4_attn_tc.cu): fp16 rows at a power of
 // two, P in fp16 against a reference that moves only when a P would pass 2^15.
 #include <climits>
@@ -154,7 +154,7 @@ template <typename T, int D, int NR>
 __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_few_kernel(const Kv4AttnArgs a) {
   using Lay = FewLayout<T, D, NR>;
   constexpr int QP = Lay::f32 ? 3 : 1, PP = Lay::f32 ? 2 : 1;        // fp16 parts of Q and of P
-  constexpr float kTop = Lay::f32 ? 14.f : 0.f;                      // log2 of the largest P at first
+  constexpr float kUp = Lay::f32 ? 0x1p14f : 1.f, kRoom = Lay::f32 ? 1.f : 15.f;   // P kUp 2^kRoom is at most 2^15
   constexpr int W = Lay::warps, ST = Lay::stages, MT = D / 16;       // MT: row tiles of O^T
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~(uintptr_t)127);
@@ -294,14 +294,14 @@ __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_f
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         mt[n][p] = fmaxf(fmaxf(s[n][0][p], s[n][0][2 + p]), fmaxf(s[n][1][p], s[n][1][2 + p])) * sl2[n][p];
-        grow |= mt[n][p] > m[n][p] + 15.f;
+        grow |= mt[n][p] > m[n][p] + kRoom;
       }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const float mx = group_max(mt[n][p]) - kTop;
+          const float mx = group_max(mt[n][p]);
           float f = 1.f;
           if (i == 0) {
             m[n][p] = mx == neg_inf() ? 0.f : mx;
@@ -325,6 +325,8 @@ __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_f
           float e1 = ex2w(fmaf(s[n][kt][2 * e + 1], sl2[n][1], -m[n][1]));
           l[n][0] += e0;
           l[n][1] += e1;
+          e0 *= kUp;
+          e1 *= kUp;
 #pragma unroll
           for (int part = 0; part < PP; ++part) {
             const uint32_t x = pack_f16w(e0, e1);
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_f
           dst[x >> 1] = make_float4(o[n][x][p] * f, o[n][x][2 + p] * f, o[n][x + 1][p] * f, o[n][x + 1][2 + p] * f);
     }
   __syncthreads();
-  const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
+  const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h)) / kUp;
   for (int x = threadIdx.x; x < (int)(rlast - r0 + 1) * (D / 4); x += W * 32) {
     const int r = x / (D / 4), c = x % (D / 4) * 4;
     const float mx = top(r);
