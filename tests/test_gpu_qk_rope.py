@@ -133,3 +133,17 @@ def test_captured_graph_follows_the_device_frame():
     g.replay()
     torch.cuda.synchronize()
     _check(qo, q, wq, 1e-6, (44, 42, 42), K.grid_positions(100, 777, 4, 5))
+
+
+def test_rows_whose_squares_overflow_fp32():
+    # the mean of squares is infinite in fp32: every finite channel is x * 0, an infinite one NaN
+    x = torch.full((3, 2, 128), 1e25, device="cuda")
+    x[1, 1] = 1.0
+    x[1, 1, 7] = float("inf")
+    x[2] = 1.0
+    out = torch.empty_like(x)
+    L.fastar_qk_norm_rope(x, None, out, None, wq=torch.ones(128, device="cuda"))
+    torch.cuda.synchronize()
+    assert (out[0] == 0).all() and (out[1, 0] == 0).all()
+    assert torch.isnan(out[1, 1, 7]) and int(torch.isnan(out).sum()) == 1 and (out[1, 1].nan_to_num() == 0).all()
+    assert (out[2] - 1).abs().max() <= 2.0 ** -19 + 5e-7      # 1 / sqrt(1 + 1e-6), as the bound above
