@@ -276,10 +276,17 @@ class DiT:
 
     def step(self, t: float, t_next: float, commit: bool):
         """One denoising step, eagerly (FAST-AR: the caches advance only when commit)."""
+        self._room()
         self.set_time(t, t_next)
         self._enqueue_step(advance=False)
         if commit:
             self._commit()
+
+    def _room(self):
+        # a captured step finds its lengths on the device: a full 4-bit cache is refused here, as the
+        # dense path's append refuses it
+        if self.attention == "dense4" and self.attn[0].n + self.cfg.tokens > self.attn[0].cap:
+            raise L.FastarError("fastar_kv4_append", L.ECAPACITY)
 
     def _commit(self):
         cfg = self.cfg
@@ -331,6 +338,7 @@ class DiT:
         cfg = self.cfg
         if probe is not None and use_graph:
             raise ValueError("a probe needs eager steps (use_graph=False)")
+        self._room()
         self.lat.zero_()
         self.lat[:, :cfg.patch_ch].copy_(noise)
         ts = timesteps(cfg.steps)

@@ -524,9 +524,9 @@ class KV4Layer:
         self.vp.copy_(vp)
 
     def commit(self, n):
-        """Keeps the n rows that the last step_self appended."""
+        """Keeps the n rows that the last step_self appended (of a full cache those that it took)."""
         self.len.copy_(self.len_cur)
-        self.n += n
+        self.n = min(self.n + n, self.cap)
 
     def step_self(self, q, k_cur, v_cur, out=None, advance: bool = True):
         """Appends the chunk behind the committed rows (kept with advance=True, else overwritten
@@ -538,7 +538,7 @@ class KV4Layer:
         L.fastar_kv4_attn(q, self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.len_cur, self.scale, o,
                           self.lse_self, block=self.block, dev_status=self.dev_status, workspace=self.ws)
         if advance:
-            self.commit(q.shape[1])
+            self.commit(k_cur.shape[1])
         return o
 
     def step_cross(self, q, out=None):

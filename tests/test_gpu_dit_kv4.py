@@ -112,3 +112,29 @@ def test_layer_history_shared_heads_and_frames():
     layer.step_self(q, kv[0], kv[1])                      # 130 rows do not fit 112
     torch.cuda.synchronize()
     assert layer.status() == L.DEV_BAD_LEN and layer.len.tolist() == [112, 112]
+
+
+def test_layer_counts_the_rows_that_the_cache_took():
+    layer = KV4Layer(2, 64, 24, 64, 8)
+    x, q = T._rand((2, 2, 40, 64), 40).bfloat16(), T._rand((2, 24, 64), 41).bfloat16()
+    layer.step_self(q, x[0], x[1])                        # more keys than queries
+    torch.cuda.synchronize()
+    assert layer.n == 40 and layer.len.tolist() == [40, 40] and layer.status() == 0
+    layer.step_self(q, x[0], x[1])                        # 24 of 40 rows fit
+    k, _ = layer.history()
+    torch.cuda.synchronize()
+    assert layer.n == 64 and layer.len.tolist() == [64, 64] and layer.status() == L.DEV_BAD_LEN
+    want = K.values(*K.quantise(T._np(x[0])))
+    assert np.array_equal(T._np(k), np.concatenate((want, want[:, :24]), axis=1))
+
+
+@pytest.mark.parametrize("use_graph", [False, True])
+def test_a_chunk_past_the_capacity_is_refused(use_graph):
+    dit, g = _dit(chunks=1)
+    dit.denoise_chunk(_noise(SMALL, g), use_graph=use_graph)
+    with pytest.raises(L.FastarError, match="capacity"):
+        dit.denoise_chunk(_noise(SMALL, g), use_graph=use_graph)
+    with pytest.raises(L.FastarError, match="capacity"):
+        dit.step(1.0, 0.5, commit=False)
+    torch.cuda.synchronize()
+    assert dit.status_word() == 0 and dit.attn[0].n == SMALL.tokens
