@@ -91,6 +91,7 @@ size_t fastar_workspace_bytes(int op, int H, int64_t n, int64_t M, int d, int B,
       return 2 * sizeof(uint16_t) * (size_t)H * F * P * d + 1024;
     case FASTAR_OP_KV4_ATTN:
       if ((d != 64 && d != 128) || B < 1 || H % B || M < 1 || n < 1) return 0;
+      if (M > INT32_MAX || n > INT32_MAX || H * n > INT32_MAX) return 0;   // fastar_kv4_attn refuses them
       return fastar::kv4_attn_workspace(d, H, B, n, M);
     default: return 0;
   }

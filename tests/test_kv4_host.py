@@ -91,7 +91,8 @@ def test_attention_refusals(lib, kw, code):
 def test_workspace(lib):
     # one token over a long cache: partial outputs, maxima and sums of at least two splits
     assert L.workspace_bytes(L.OP_KV4_ATTN, 32, 1, 131072, 128, 8) >= 2 * 32 * 130 * 4
-    for bad in (dict(n=0), dict(M=0), dict(d=96), dict(B=0), dict(B=5)):
+    for bad in (dict(n=0), dict(M=0), dict(d=96), dict(B=0), dict(B=5), dict(n=2 ** 62), dict(n=2 ** 26),
+                dict(M=2 ** 62)):                          # the last three: sizes that the call refuses
         a = dict(H=32, n=1, M=131072, d=128, B=8)
         a.update(bad)
         assert L.workspace_bytes(L.OP_KV4_ATTN, a["H"], a["n"], a["M"], a["d"], a["B"]) == 0
