@@ -619,7 +619,9 @@ int fastar_kv4_read(int dtype, int H, int64_t n, int d, const uint8_t* codes, co
  * min(nq, (t / block + 1) * block)); block = 1 is causal, block = a frame's tokens lets a frame
  * see itself and the frames before it.  see(t) = 0: O = 0, lse = -inf.  len int32 [Hkv] on the
  * device (outside [0, cap]: held to it, FASTAR_DEV_BAD_LEN); rows from len on are never used.
- * Scale bytes are taken as fastar_kv4_append writes them (finite, not negative).
+ * Scale bytes are taken as fastar_kv4_append writes them (finite, not negative).  A row of q with
+ * a NaN or an infinity gives NaN (zeros if none of its logits is above -infinity), and no other
+ * row is touched.
  * lse float [Hq, nq] optional.  Hq * nq <= INT32_MAX (FASTAR_ECAPACITY).
  * workspace (optional): fastar_workspace_bytes(FASTAR_OP_KV4_ATTN, Hq, nq, cap, d, Hkv, ...)
  * bytes for the partial results of key splits; NULL: the keys are not split (slower with few

@@ -223,8 +223,9 @@ __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_f
 
   int stage = 0;
   uint32_t ph = 0;
+  int i = 0;
 #pragma unroll 1
-  for (int i = 0; i < count; ++i) {
+  for (; i < count; ++i) {
     const int key = (int)(b0 + warp + (uint32_t)i * W) * kKeysW;        // the capacity fits 31 bits
     uint8_t* st = ring + stage * Lay::stage;
     if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[stage], ph, abort))) break;
@@ -375,6 +376,12 @@ __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_f
     }
     __syncwarp();                           // every lane has read the block
     if (lane == 0 && i + ST < count) fetch(i + ST, stage);
+    if (++stage == ST) stage = 0, ph ^= 1;
+  }
+  // after a wait that gave up: the copies in flight land before the ring is used or given back
+  volatile int never = 0;
+  for (int x = i; x < count && x < i + ST; ++x) {
+    tc::mbar_wait(&full[stage], ph, &never, 400000000LL);
     if (++stage == ST) stage = 0, ph ^= 1;
   }
 

@@ -668,7 +668,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       // Whole 16-row groups: the capacity is a multiple of 16, so the group that holds the last
       // key lies within the head's rows, and sizes and addresses are multiples of 16 bytes.  Of
       // K only this CTA's rows; of V whole rows (a bulk copy is contiguous).
-      for (int n = 0; n < 2 * T; ++n) {
+      int n = 0;
+      for (; n < 2 * T; ++n) {
         const int in = n % kIn;
         const bool isv = n & 1;
         if (!tc::mbar_wait(&sm.in_empty[in], ((n / kIn) & 1) ^ 1, abort)) break;
@@ -683,6 +684,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
         tc::bulk_load(dst, (isv ? a.vc : a.kc) + at * (D / 2), nr * (D / 2), &sm.in_full[in]);
         tc::bulk_load(dst + Lay::in_codes, (isv ? a.vs : a.ks) + at * (D / 16), nr * (D / 16), &sm.in_full[in]);
       }
+      // the last copies land before this thread leaves, whether or not anyone waits for them
+      volatile int never = 0;
+      for (int x = n < kIn ? 0 : n - kIn; x < n; ++x) tc::mbar_wait(&sm.in_full[x % kIn], (x / kIn) & 1, &never, 400000000LL);
     }
     // ---------------- MMA issue (one thread of the pair) ----------------
     if (warp == kMmaWarp && rank == 0 && elect_one()) {
