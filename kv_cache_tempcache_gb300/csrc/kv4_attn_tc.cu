@@ -58,10 +58,24 @@ constexpr int kThreadsT = 896;         // the last warpgroup: MMA warp, copy war
 constexpr int kRegsSoft = 88, kRegsRest = 48;
 static_assert(512 * kRegsSoft + 384 * kRegsRest <= kThreadsT * 72, "the launch's registers bound the shares");
 
+// What a CTA works on (the same for both of a pair).
+struct Kv4Item {
+  int64_t len, most;       // the head's cached rows; keys that any of the CTA's rows sees
+  uint32_t rows, r0;       // rows of a KV head, the item's first
+  uint32_t j0, split;      // first key tile
+  int h, group, nt, T;     // KV head, its query heads, row tiles with rows, key tiles (-1: a split that is not in use)
+  bool partial;            // one of several splits
+};
+
+// Threads at the barriers that hold the unpacking of all but the first tile of K back until the query
+// rows, which the first product waits for, are done (the softmax warps arrive, four warps wait).
+constexpr int kHeld = (kSoftWarps + 4) * 32;
+
 struct alignas(16) Kv4Ctl {
   uint64_t in_full[kIn], in_empty[kIn];                // packed tiles: K 0, V 0, K 1, V 1, ...
   uint64_t q_full[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t s_full[2], p_full[2][2], fin;               // by row tile (P: first 32 keys of each half, last 32)
+  Kv4Item item;
   uint32_t tmem_base;
   int abort;
   float ex[2][2][kRT];                                 // a row's two threads: half, row tile, row
@@ -132,6 +146,10 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
   else
     tc::mma_commit(bar);
 }
+// Arrives at a named barrier at which others wait.
+__device__ __forceinline__ void bar_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
 template <int kCta>
 __device__ __forceinline__ void tmem_alloc512(uint32_t* dst) {
   if (kCta == 2) {
@@ -161,9 +179,11 @@ __device__ __forceinline__ uint32_t cta_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void pair_sync() {
-  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
-}
+// The pair's barrier.  The relaxed arrival does not wait for the thread's own loads and stores (a
+// releasing one cost 1000 to 2000 clocks): what the other CTA relies on is the initialised barriers
+// (mbar_fence_init before it) and that nothing is signalled any more.
+__device__ __forceinline__ void pair_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void pair_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // Arrives on the barrier of the pair's first CTA, where the products are issued.  What the
 // arrival announces lies in the arriving CTA's own shared memory or TMEM, is read there by
 // its own tensor core, and has been handed to the async proxy (fence.proxy.async) or to
@@ -250,9 +270,9 @@ __device__ __forceinline__ void row_exp32(const float* x, float sl2, float nm, u
 struct RowOf {
   int64_t head, t;
 };
-__device__ __forceinline__ RowOf row_of(const Kv4AttnArgs& a, int h, int64_t r) {
+__device__ __forceinline__ RowOf row_of(const Kv4AttnArgs& a, const Kv4Item& it, int64_t r) {
   const uint32_t nq = (uint32_t)a.nq, g = (uint32_t)r / nq;       // Hq * nq fits 31 bits
-  return RowOf{h * (int64_t)(a.Hq / a.Hkv) + g, (int64_t)((uint32_t)r - g * nq)};
+  return RowOf{it.h * (int64_t)it.group + g, (int64_t)((uint32_t)r - g * nq)};
 }
 
 // A row that sees no key: zeros and lse = -inf.
@@ -262,6 +282,47 @@ __device__ __forceinline__ void store_empty(const Kv4AttnArgs& a, RowOf w) {
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) p[i] = make_uint4(0, 0, 0, 0);
   if (a.lse) a.lse[w.head * a.nq + w.t] = neg_inf();
+}
+
+// The work item of this block.  First splits first (a short cache uses no others); in a call in
+// blocks the rows that see most keys first, of all heads; a last item with one row tile, which
+// takes half as long, at the end, where it fills gaps.
+template <int kCta>
+__device__ __forceinline__ Kv4Item item_of(const Kv4AttnArgs& a, int row_tiles) {
+  Kv4Item it;
+  it.group = a.Hq / a.Hkv;
+  const uint32_t rows = it.rows = (uint32_t)it.group * (uint32_t)a.nq, nq = (uint32_t)a.nq;      // Hq * nq fits 31 bits
+  const bool odd = row_tiles > 1 && (rows - 1) % (2 * kRT * kCta) < kRT * kCta;
+  const int full_tiles = row_tiles - odd;
+  uint32_t u = blockIdx.x / kCta;
+  const uint32_t all = (uint32_t)(a.Hkv * full_tiles);
+  const bool last = u >= all * (uint32_t)a.splits;
+  if (last) u -= all * (uint32_t)a.splits;
+  it.split = a.splits == 1 ? 0u : last ? u / (uint32_t)a.Hkv : u / all;
+  u -= it.split * (last ? (uint32_t)a.Hkv : all);
+  uint32_t rt = (uint32_t)full_tiles;
+  if (last) {
+    it.h = (int)u;
+  } else if (a.block > 0) {
+    const uint32_t x = u / (uint32_t)a.Hkv;
+    it.h = (int)(u - x * (uint32_t)a.Hkv);
+    rt = (uint32_t)full_tiles - 1 - x;
+  } else {
+    it.h = (int)(u / (uint32_t)full_tiles);
+    rt = (uint32_t)full_tiles - 1 - (u - (uint32_t)it.h * (uint32_t)full_tiles);
+  }
+  it.len = kv4::head_len(a.len, it.h, a.cap, a.status);
+  it.r0 = rt * (2 * kRT * kCta);
+  const uint32_t rlast = (it.r0 + 2 * kRT * kCta < rows ? it.r0 + 2 * kRT * kCta : rows) - 1;
+  it.nt = rlast - it.r0 >= kRT * kCta ? 2 : 1;
+  const kv4::ItemKeys keys = kv4::item_keys(it.len, nq, a.block, it.r0, rlast, a.splits, a.min_tiles);
+  it.most = keys.most;
+  it.partial = keys.splits > 1;
+  it.j0 = it.partial ? keys.tiles * it.split / keys.splits : 0u;     // tiles times splits fits 32 bits
+  it.T = it.split >= keys.splits ? -1
+         : it.partial            ? (int)(keys.tiles * (it.split + 1) / keys.splits - it.j0)
+                                 : (int)keys.tiles;
+  return it;
 }
 
 template <int D>
@@ -274,24 +335,18 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kCta == 2 ? (int)cta_rank() : 0;
 
-  // the work item (the same for both CTAs of a pair): KV head, row tiles, split of the keys.
-  // First splits first (a short cache uses no others); in a call in blocks the rows that see most
-  // keys first, of all heads; a last item with one row tile, which takes half as long, at the
-  // end, where it fills gaps.
-  const uint32_t rows = (uint32_t)(a.Hq / a.Hkv) * (uint32_t)a.nq, nq = (uint32_t)a.nq;      // Hq * nq fits 31 bits
-  const bool odd = row_tiles > 1 && (rows - 1) % (2 * kRT * kCta) < kRT * kCta;
-  const int full_tiles = row_tiles - odd;
-  uint32_t u = blockIdx.x / kCta;
-  const uint32_t all = (uint32_t)(a.Hkv * full_tiles);
-  const bool last = u >= all * (uint32_t)a.splits;
-  if (last) u -= all * (uint32_t)a.splits;
-  const uint32_t split = last ? u / (uint32_t)a.Hkv : u / all;
-  u -= split * (last ? (uint32_t)a.Hkv : all);
-  const int h = (int)(last ? u : a.block > 0 ? u % (uint32_t)a.Hkv : u / (uint32_t)full_tiles);
-  const int rt = last ? full_tiles
-                      : full_tiles - 1 - (int)(a.block > 0 ? u / (uint32_t)a.Hkv : u % (uint32_t)full_tiles);
-  const int64_t len = kv4::head_len(a.len, h, a.cap, a.status);
-  if (threadIdx.x == 0) {                                // while the length is on its way
+  // Before the loop a CTA has only latencies to wait for, and instructions to fetch that run once:
+  // one thread finds the item (its divisions in all 28 warps took 5000 clocks), another sets the
+  // barriers up, and rolled loops move the query rows.
+  if (threadIdx.x == (kMmaWarp + 1) * 32) {
+    for (int i = 0; i < kIn; ++i) {
+      tc::mbar_init(&sm.in_full[i], 1);
+      tc::mbar_init(&sm.in_empty[i], 4);
+    }
+    tc::mbar_fence_init();
+    sm.item = item_of<kCta>(a, row_tiles);
+  }
+  if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.q_full[i], 8 * kCta);
       tc::mbar_init(&sm.s_full[i], 1);
@@ -304,61 +359,27 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       tc::mbar_init(&sm.v_full[i], 4 * kCta);
       tc::mbar_init(&sm.v_empty[i], 1);
     }
-    for (int i = 0; i < kIn; ++i) {
-      tc::mbar_init(&sm.in_full[i], 1);
-      tc::mbar_init(&sm.in_empty[i], 4);
-    }
     tc::mbar_init(&sm.fin, 1);
     sm.abort = 0;
     tc::mbar_fence_init();
   }
-  const uint32_t r0 = (uint32_t)rt * (2 * kRT * kCta);
-  const uint32_t rlast = (r0 + 2 * kRT * kCta < rows ? r0 + 2 * kRT * kCta : rows) - 1;
-  const int nt = rlast - r0 >= kRT * kCta ? 2 : 1;      // row tiles with rows
-  const bool both = nt == 1;              // one row tile: even key tiles and odd key tiles
-  const kv4::ItemKeys keys = kv4::item_keys(len, nq, a.block, r0, rlast, a.splits, a.min_tiles);
-  const int64_t most = keys.most;
-  if (split >= keys.splits || (keys.splits == 1 && a.splits > 1)) {
-    // what the join reads of a split that is not in use, and of the first where the output is in place
+  __syncthreads();
+  const Kv4Item& it = sm.item;
+  const uint32_t rows = it.rows, r0 = it.r0, split = it.split;
+  const int h = it.h, T = it.T;
+  const bool partial = it.partial, both = it.nt == 1;    // both: one row tile, even key tiles and odd key tiles
+  if (T <= 0 || (a.splits > 1 && !partial)) {
     const uint32_t r = r0 + threadIdx.x / kRT * (kRT * kCta) + rank * kRT + threadIdx.x % kRT;
     if (threadIdx.x < 2 * kRT && r < rows) {
-      const RowOf w = row_of(a, h, r);
-      a.part_ml[((int64_t)split * a.Hq + w.head) * a.nq + w.t] = make_float2(split == 0 ? -neg_inf() : neg_inf(), 0.f);
+      const RowOf w = row_of(a, it, r);
+      // what the join reads of a split that is not in use, and of the first where the output is in place
+      if (a.splits > 1)
+        a.part_ml[((int64_t)split * a.Hq + w.head) * a.nq + w.t] = make_float2(split == 0 ? -neg_inf() : neg_inf(), 0.f);
+      if (T == 0) store_empty<D>(a, w);                  // no keys at all
     }
-    if (split > 0) return;
+    if (T <= 0) return;                                  // both CTAs of a pair
   }
-  const bool partial = keys.splits > 1;
-  const int64_t j0 = keys.tiles * split / keys.splits;   // tiles times splits fits 32 bits
-  const int T = (int)(keys.tiles * (split + 1) / keys.splits - (uint32_t)j0);
-
-  // a query row's share of 16 bytes, 16 (8) lanes a row: warp x of a row tile loads its rows 16 x ..
-  // on, all of them before anything waits
-  constexpr int QL = D / 8, QR = 32 / QL, QN = 16 / QR;
-  uint4 xq[QN];
-  if (warp < kSoftWarps && !(both && warp >= 8)) {
-#pragma unroll
-    for (int i = 0; i < QN; ++i) {
-      const uint32_t r = r0 + (uint32_t)((warp >> 3) * (kRT * kCta) + rank * kRT + (warp & 7) * 16 + i * QR + lane / QL);
-      xq[i] = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        const RowOf at = row_of(a, h, r);
-        xq[i] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + at.head * a.q.hs +
-                                               at.t * a.q.ts)[lane % QL];
-      }
-    }
-  }
-  if (T == 0) {                                          // no keys at all: uniform over the pair
-    const uint32_t r = r0 + threadIdx.x / kRT * (kRT * kCta) + rank * kRT + threadIdx.x % kRT;
-    if (threadIdx.x < 2 * kRT && r < rows) store_empty<D>(a, row_of(a, h, r));
-    return;
-  }
-
-  if (warp == kMmaWarp) tmem_alloc512<kCta>(&sm.tmem_base);
-  tc::tc_fence_before();
-  __syncthreads();
-  if (kCta == 2) pair_sync();                            // the other CTA's barriers are ready too
-  tc::tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  if (kCta == 2) pair_arrive();                          // this CTA's barriers are ready
   volatile int* abort = &sm.abort;
 
   if (warp < kSoftWarps) {
@@ -369,19 +390,42 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     const int pair_bar = 1 + w * 4 + (warp & 3);          // the two warps of these rows
     const uint32_t r = r0 + (both ? 0u : (uint32_t)(w * (kRT * kCta))) + (uint32_t)(rank * kRT + row);
     const bool has = r < rows;
-    const RowOf at = has ? row_of(a, h, r) : RowOf{0, 0};
     constexpr int HD = D / 2;                             // channels of a row of O a thread takes
-    if (!(both && w == 1)) {
-      // query rows: a row's largest magnitude, then fp16 at a power of two
-      uint8_t* dst = base + Lay::q + (size_t)w * Lay::q_tile;
+    // Query rows: warp x of a row tile brings its rows 16 x .. on, four lanes a row, to where the product
+    // wants them, then turns them to fp16 in place.  Odd rows take the halves of a block's 16-byte
+    // chunks the other way round, so that 8 lanes hit 8 bank groups.
+    constexpr int QC = D / 32;                            // a lane's chunks of a row
+    const bool mine = !(both && w == 1);
+    const int qr = (warp & 7) * 16 + (lane >> 2), qc = (lane & 3) ^ ((lane >> 2 & 1) << 2);
+    uint8_t* qd = base + Lay::q + (size_t)w * Lay::q_tile;
+    auto chunk = [&](int i, int j) {                      // chunk j of the lane's row i
+      return qd + (j >> 1) * Lay::q_blk + tc::sw128_off(qr + i * 8, qc ^ ((j & 1) << 2));
+    };
+    if (mine) {
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t x = r0 + (uint32_t)(w * (kRT * kCta) + rank * kRT + qr + i * 8);
+        const RowOf from = row_of(a, it, x < rows ? x : r0);
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.p) + from.head * a.q.hs + from.t * a.q.ts;
 #pragma unroll
-      for (int i = 0; i < QN; ++i) {
-        const uint32_t v[4] = {xq[i].x, xq[i].y, xq[i].z, xq[i].w};
-        uint32_t big = 0;
+        for (int j = 0; j < QC; ++j)
+          tc::cp_async16(tc::smem_u32(chunk(i, j)), src + (j >> 1) * 64 + (qc ^ ((j & 1) << 2)) * 8, x < rows ? 16 : 0);
+      }
+      tc::cp_async_commit();
+      tc::cp_async_wait<0>();
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        uint32_t v[4 * QC], big2 = 0;                     // a row's largest magnitude, two channels at a time
 #pragma unroll
-        for (int e = 0; e < 4; ++e) big = max(big, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
+        for (int j = 0; j < QC; ++j) {
+          const uint4 c = *reinterpret_cast<const uint4*>(chunk(i, j));
+          v[4 * j] = c.x, v[4 * j + 1] = c.y, v[4 * j + 2] = c.z, v[4 * j + 3] = c.w;
+        }
 #pragma unroll
-        for (int x = QL / 2; x > 0; x >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, x));
+        for (int e = 0; e < 4 * QC; ++e) big2 = __vmaxu2(big2, v[e] & 0x7fff7fffu);
+        big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, 1));
+        big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, 2));
+        const uint32_t big = max(big2 & 0xffffu, big2 >> 16);
         // exponent of the largest (subnormals count as 2^-126); a row that is zero or not finite
         // stays as it is
         const int ex = (int)(big >> 7);
@@ -389,25 +433,32 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
         if (qe < -120) qe = -120;
         if (big == 0 || ex == 255) qe = 0;
         const float down = kv4::pow2i(-qe);
-        const int qr = (warp & 7) * 16 + i * QR + lane / QL, ch = lane % QL;
-        uint32_t o[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[e] = pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
-        *reinterpret_cast<uint4*>(dst + (ch >> 3) * Lay::q_blk + tc::sw128_off(qr, ch & 7)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
-        if (ch == 0) sm.ex[0][w][qr] = kv4::pow2i(qe);
+        for (int j = 0; j < QC; ++j) {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[e] = pack_f16(__uint_as_float(v[4 * j + e] << 16) * down, __uint_as_float(v[4 * j + e] & 0xffff0000u) * down);
+          *reinterpret_cast<uint4*>(chunk(i, j)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        if ((lane & 3) == 0) sm.ex[0][w][qr + i * 8] = kv4::pow2i(qe);
       }
       tc::fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) arrive_issuer<kCta>(&sm.q_full[w]);
     }
-    tc::named_bar(9, kSoftWarps * 32);
+    bar_arrive(11, kHeld);
+    bar_arrive(12, kHeld);
+    tc::named_bar(10, (kSoftWarps + 1) * 32);             // TMEM is there, and ex
+    tc::tc_fence_after();
+    if (kCta == 2) pair_wait();                           // the other CTA's barriers are ready
+    if (mine && lane == 0) arrive_issuer<kCta>(&sm.q_full[w]);
+    const uint32_t tmem = sm.tmem_base;
+    const RowOf at = has ? row_of(a, it, r) : RowOf{0, 0};
+    // keys the row sees from this thread's first on (a row that is not there: as the last)
+    int left = max(0, (int)(has ? kv4::visible(it.len, a.nq, at.t, a.block) : it.most) - (int)it.j0 * kKT - half * 64 -
+                          (both ? w * kKT : 0));          // capacities fit 31 bits
     float sl2 = a.scale * sm.ex[0][both ? 0 : w][row] * kv4::pow2i(kv4::head_exp(a.k_exp, h)) * 1.4426950408889634f;
     sl2 = fminf(fmaxf(sl2, 1.2e-38f), 3.0e38f);   // a product of scales outside fp32's range: positive and finite
     tc::named_bar(9, kSoftWarps * 32);     // ex is used again below
-    // keys the row sees from this thread's first on (a row that is not there: as the last)
-    int64_t left = (has ? kv4::visible(len, a.nq, at.t, a.block) : most) - j0 * kKT - half * 64 - (both ? w * kKT : 0);
     const int step = both ? 2 : 1, count = both ? (T - w + 1) >> 1 : T;      // this row tile's key tiles
     const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_addr = lane_addr + Lay::s_col + (uint32_t)(w * 128 + half * 64);
@@ -415,11 +466,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     float m = 0.f, l0 = 0.f, l1 = 0.f;      // m: the reference, in log2 units
     bool ok = true;
 #pragma unroll 1
-    for (int i = 0; i < count; ++i, left -= step * kKT) {
+    for (int i = 0; i < count; ++i, left = max(0, left - step * kKT)) {
       const bool alive = wait_warp(&sm.s_full[w], i & 1, abort);
       tc::tc_fence_after();
       const bool cut = __any_sync(0xffffffffu, left < 64);
-      const int valid = left < 64 ? left > 0 ? (int)left : 0 : 64;          // keys that the row sees
+      const int valid = min(left, 64);          // keys that the row sees
       float mt;
       {
         float x[64];
@@ -539,9 +590,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       // 16 bytes a thread, a row each, they took 5 us of a CTA.
       uint8_t* stg = base + Lay::k + warp * 4096;
       uint8_t* out = partial ? reinterpret_cast<uint8_t*>(a.part_o) : static_cast<uint8_t*>(a.out);
-      const int64_t off = partial ? (((int64_t)split * a.Hq + at.head) * a.nq + at.t) * D * 4 + half * HD * 4
-                                  : (at.head * a.o_hs + at.t * a.o_ts + half * HD) * 2;
-      const int cp = partial ? 32 : HD, esz = partial ? 4 : 2, nc = cp * esz / 16;   // channels and 16-byte chunks a pass
+      const int64_t off = !has     ? -1
+                          : partial ? (((int64_t)split * a.Hq + at.head) * a.nq + at.t) * D * 4 + half * HD * 4
+                                    : (at.head * a.o_hs + at.t * a.o_ts + half * HD) * 2;
+      const int cp = partial ? 32 : HD, esz = partial ? 4 : 2;   // channels a pass
+      const int nc = HD == 64 ? 8 : cp * esz / 16;               // 16-byte chunks of a pass's row
 #pragma unroll 1
       for (int c0 = 0; c0 < HD; c0 += cp) {
 #pragma unroll 1
@@ -581,12 +634,12 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
           }
         }
         __syncwarp();
-        for (int x = lane; x < 32 * nc; x += 32) {
-          const int sr = x / nc, ch = x % nc;
+#pragma unroll 4
+        for (int i = 0; i < nc; ++i) {
+          const int sr = (i * 32 + lane) / nc, ch = (i * 32 + lane) % nc;
           const int64_t to = __shfl_sync(0xffffffffu, off, sr);
-          const bool there = __shfl_sync(0xffffffffu, (int)has, sr);
           const uint4 v = *reinterpret_cast<const uint4*>(stg + tc::sw128_off(sr, ch));
-          if (there) *reinterpret_cast<uint4*>(out + to + c0 * esz + ch * 16) = v;
+          if (to >= 0) *reinterpret_cast<uint4*>(out + to + c0 * esz + ch * 16) = v;
         }
         __syncwarp();
       }
@@ -601,6 +654,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
   } else if (warp < kMmaWarp) {
     // ---------------- unpack K and V ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (kCta == 2) pair_wait();
     // A thread takes two runs of 32 codes (16 bytes) of a tile: of K's KR rows x D channels, or of
     // V's 128 rows x this CTA's 64 channels.  With four runs to a row (K at d = 128) runs 2 and
     // 3 write their 16-byte chunks in another order: so the 8 lanes of a store phase always
@@ -619,11 +673,12 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       // the run's place in the packed tile: 16 bytes of codes, two scales
       const int run0 = isv ? row0 * KP + (kCta == 2 ? 2 * rank : 0) + part : t;
       const int runstep = rstep * KP;
+      if (n == (isv ? 1 : 2)) tc::named_bar(isv ? 12 : 11, kHeld);
       if (!wait_warp(&sm.in_full[in], (n / kIn) & 1, abort) || !wait_warp(empty, ((j / kStages) & 1) ^ 1, abort)) break;
       const uint8_t* packed = base + Lay::in + in * Lay::in_tile;
       uint8_t* tile = base + (isv ? Lay::v + (size_t)st * Lay::v_tile : Lay::k + (size_t)st * Lay::k_tile);
       // rows past the last key hold what is in memory there, or nothing: they count as 0
-      const int64_t left = most - (j0 + j) * kKT - (isv ? 0 : rank * Lay::KR);
+      const int left = (int)it.most - (int)(it.j0 + j) * kKT - (isv ? 0 : rank * Lay::KR);
       uint4 c[2];
       uint32_t s[2];
 #pragma unroll
@@ -663,26 +718,33 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == kMmaWarp) {
+      tmem_alloc512<kCta>(&sm.tmem_base);
+      tc::tc_fence_before();
+      tc::named_bar(10, (kSoftWarps + 1) * 32);
+      tc::tc_fence_after();
+    }
+    if (kCta == 2) pair_wait();
     if (warp == kMmaWarp + 1 && lane == 0) {
       // ---------------- packed tiles into shared memory (one thread) ----------------
       // Whole 16-row groups: the capacity is a multiple of 16, so the group that holds the last
       // key lies within the head's rows, and sizes and addresses are multiples of 16 bytes.  Of
       // K only this CTA's rows; of V whole rows (a bulk copy is contiguous).
+      const int64_t first = (int64_t)it.h * a.cap;
+      const uint32_t most = (uint32_t)it.most, j0 = it.j0;      // capacities fit 31 bits
       int n = 0;
       for (; n < 2 * T; ++n) {
         const int in = n % kIn;
         const bool isv = n & 1;
         if (!tc::mbar_wait(&sm.in_empty[in], ((n / kIn) & 1) ^ 1, abort)) break;
-        const int64_t key = (j0 + (n >> 1)) * kKT + (isv ? 0 : rank * Lay::KR);
-        const int want = isv ? kKT : Lay::KR;
-        const int64_t left = (most - key + 15) & ~(int64_t)15;
-        const uint32_t nr = left < 0 ? 0u : left < want ? (uint32_t)left : (uint32_t)want;
-        const int64_t at = (int64_t)h * a.cap + key;
+        const uint32_t key = (j0 + (uint32_t)(n >> 1)) * kKT + (isv ? 0u : (uint32_t)(rank * Lay::KR));
+        const uint32_t nr = key < most ? min((most - key + 15) & ~15u, (uint32_t)(isv ? kKT : Lay::KR)) : 0u;
         uint8_t* dst = base + Lay::in + in * Lay::in_tile;
         tc::mbar_arrive_tx(&sm.in_full[in], nr * (D / 2 + D / 16));
         if (nr == 0) continue;
-        tc::bulk_load(dst, (isv ? a.vc : a.kc) + at * (D / 2), nr * (D / 2), &sm.in_full[in]);
-        tc::bulk_load(dst + Lay::in_codes, (isv ? a.vs : a.ks) + at * (D / 16), nr * (D / 16), &sm.in_full[in]);
+        tc::bulk_load(dst, (isv ? a.vc : a.kc) + (first + key) * (D / 2), nr * (D / 2), &sm.in_full[in]);
+        tc::bulk_load(dst + Lay::in_codes, (isv ? a.vs : a.ks) + (first + key) * (D / 16), nr * (D / 16),
+                      &sm.in_full[in]);
       }
       // the last copies land before this thread leaves, whether or not anyone waits for them
       volatile int never = 0;
@@ -690,6 +752,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     }
     // ---------------- MMA issue (one thread of the pair) ----------------
     if (warp == kMmaWarp && rank == 0 && elect_one()) {
+      const uint32_t tmem = sm.tmem_base;
       constexpr uint32_t idesc_qk = idesc_f16(kRT * kCta, kKT, false), idesc_pv = idesc_f16(kRT * kCta, D, true);
       const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(base + Lay::q));
       const uint64_t k_desc = tc::sw128_desc(tc::smem_u32(base + Lay::k));
@@ -755,10 +818,15 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (kCta == 2) pair_sync();            // neither CTA leaves while the other may signal or use it
+  if (kCta == 2) {                       // neither CTA leaves while the other may signal or use it
+    // (after a wait that gave up, signals may be on their way to the other CTA: they land first)
+    if (*abort) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    pair_arrive();
+    pair_wait();
+  }
   if (warp == kMmaWarp) {
     tc::tc_fence_after();
-    tmem_free512<kCta>(tmem);
+    tmem_free512<kCta>(sm.tmem_base);
   }
   if (threadIdx.x == 0 && sm.abort) flag_status(a.status, FASTAR_DEV_TIMEOUT);
 }
