@@ -217,7 +217,10 @@ struct Kv4AttnArgs {
   int64_t o_hs, o_ts;
   float* lse;
   int32_t* status;
-  // filled in by the launcher: splits of the keys and their partials (fp32; maximum and sum)
+  // filled in by the launcher: query heads and rows of a KV head, splits of the keys and their
+  // partials (fp32; maximum and sum)
+  int group;
+  uint32_t rows;
   int splits;
   int min_tiles;                      // tcgen05 kernel: key tiles of 128 a split should have (else 0)
   float* part_o;                      // [splits, Hq, nq, d]

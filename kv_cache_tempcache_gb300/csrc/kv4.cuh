@@ -86,10 +86,17 @@ struct ItemKeys {
 __device__ __forceinline__ ItemKeys item_keys(int64_t len, uint32_t nq, int64_t block, uint32_t r0, uint32_t rlast,
                                               int splits, int min_tiles) {
   ItemKeys k;
-  k.most = r0 / nq != rlast / nq ? len : visible(len, nq, rlast % nq, block);
+  k.most = len;
+  k.splits = 1;
+  if (block > 0) {
+    const uint32_t g = rlast / nq, first = g * nq;                 // the last row's query head, its first row
+    if (r0 >= first) k.most = visible(len, nq, rlast - first, block);
+  }
   k.tiles = (uint32_t)((k.most + 127) / 128);
-  const uint32_t s = k.tiles / (uint32_t)min_tiles;
-  k.splits = s < 1 ? 1u : s < (uint32_t)splits ? s : (uint32_t)splits;
+  if (splits > 1) {
+    const uint32_t s = k.tiles / (uint32_t)min_tiles;
+    k.splits = s < 1 ? 1u : s < (uint32_t)splits ? s : (uint32_t)splits;
+  }
   return k;
 }
 

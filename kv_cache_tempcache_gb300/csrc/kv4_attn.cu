@@ -174,7 +174,7 @@ cudaError_t run(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStream_t s) {
     a.part_o = static_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * a.Hq * a.nq * d);
   }
-  const bool few = dtype == FASTAR_F32 || (int64_t)(a.Hq / a.Hkv) * a.nq <= kFewRows;
+  const bool few = dtype == FASTAR_F32 || a.rows <= kFewRows;
   if (!few && a.min_tiles == 0) a.min_tiles = 1;         // one split
   const cudaError_t e = few ? launch_kv4_attn_few(dtype, d, a, s) : launch_kv4_attn_tc(d, a, s);
   if (e != cudaSuccess || a.splits == 1) return e;
@@ -200,6 +200,8 @@ size_t kv4_attn_workspace(int d, int Hq, int Hkv, int64_t nq, int64_t cap) {
 }
 
 bool launch_kv4_attn(int dtype, int d, Kv4AttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s, cudaError_t* err) {
+  a.group = a.Hq / a.Hkv;
+  a.rows = (uint32_t)(a.group * a.nq);       // Hq * nq fits 31 bits
   a.min_tiles = 0;
   a.splits = ws ? kv4_attn_splits(dtype, d, a.Hq, a.Hkv, a.nq, a.cap, &a.min_tiles) : 1;
   if (a.splits > 1 && ws_bytes < partial_bytes(a.splits, d, a.Hq, a.nq)) return false;

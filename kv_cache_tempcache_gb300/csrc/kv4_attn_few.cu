@@ -117,7 +117,7 @@ __device__ __forceinline__ float load_q(const Kv4AttnArgs& a, int h, uint32_t ro
   uint32_t big = 0;                         // the largest magnitude's bits
   if (r < rows) {
     const uint32_t nq = (uint32_t)a.nq, gh = r / nq;
-    const int64_t head = h * (int64_t)(a.Hq / a.Hkv) + gh;
+    const int64_t head = h * (int64_t)a.group + gh;
     const T* src = static_cast<const T*>(a.q.p) + head * a.q.hs + (int64_t)(r - gh * nq) * a.q.ts + t * CH;
 #pragma unroll
     for (int i = 0; i < CH; i += 8) load8(src + i, x + i);
@@ -162,10 +162,10 @@ __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_f
   float2* wml = reinterpret_cast<float2*>(bars + W * ST);            // [warp][8 NR]
   int* abort_flag = reinterpret_cast<int*>(wml + W * 8 * NR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t rows = (uint32_t)(a.Hq / a.Hkv) * (uint32_t)a.nq, groups = (rows + 8 * NR - 1) / (8 * NR);
-  const int split = (int)(blockIdx.x % (uint32_t)a.splits);
-  const uint32_t gr = blockIdx.x / (uint32_t)a.splits % groups;
-  const int h = (int)(blockIdx.x / ((uint32_t)a.splits * groups));
+  const uint32_t rows = a.rows, groups = (rows + 8 * NR - 1) / (8 * NR);
+  const int split = (int)blockIdx.y;
+  const int h = (int)(groups == 1 ? blockIdx.x : blockIdx.x / groups);
+  const uint32_t gr = blockIdx.x - (uint32_t)h * groups;
   const uint32_t r0 = gr * 8 * NR, rlast = (r0 + 8 * NR < rows ? r0 + 8 * NR : rows) - 1;
   // the keys that any of the rows sees
   const int64_t cached = kv4::head_len(a.len, h, a.cap, a.status);
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_f
     for (int p = 0; p < 2; ++p) {
       sl2[n][p] = __shfl_sync(0xffffffffu, s, (2 * t + p) * 4);
       const uint32_t r = r0 + (uint32_t)(8 * n + 2 * t + p), nq = (uint32_t)a.nq;
-      see[n][p] = (int)(r < rows ? kv4::visible(cached, a.nq, r % nq, a.block) : len);
+      see[n][p] = (int)(r < rows ? a.block > 0 ? kv4::visible(cached, a.nq, r % nq, a.block) : cached : len);
       m[n][p] = l[n][p] = 0.f;
     }
   }
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_f
     }
     const bool live = sum > 0.f || sum != sum;
     const uint32_t nq = (uint32_t)a.nq, gh = (r0 + (uint32_t)r) / nq;
-    const int64_t head = h * (int64_t)(a.Hq / a.Hkv) + gh, tok = r0 + (uint32_t)r - gh * nq;
+    const int64_t head = h * (int64_t)a.group + gh, tok = r0 + (uint32_t)r - gh * nq;
     const float mn = mx * 0.6931471805599453f;
     if (a.splits > 1) {
       const int64_t at = (split * (int64_t)a.Hq + head) * a.nq + tok;
@@ -459,12 +459,11 @@ __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_f
 template <typename T, int D, int NR>
 cudaError_t few_go(const Kv4AttnArgs& a, cudaStream_t s) {
   using Lay = FewLayout<T, D, NR>;
-  const int64_t rows = (int64_t)(a.Hq / a.Hkv) * a.nq;
-  const int64_t blocks = (rows + 8 * NR - 1) / (8 * NR) * a.Hkv * a.splits;
+  const int64_t blocks = ((int64_t)a.rows + 8 * NR - 1) / (8 * NR) * a.Hkv;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
   const cudaError_t e = opt_in_smem((const void*)kv4_attn_few_kernel<T, D, NR>, Lay::bytes);
   if (e != cudaSuccess) return e;
-  kv4_attn_few_kernel<T, D, NR><<<(unsigned)blocks, Lay::warps * 32, Lay::bytes, s>>>(a);
+  kv4_attn_few_kernel<T, D, NR><<<dim3((unsigned)blocks, (unsigned)a.splits), Lay::warps * 32, Lay::bytes, s>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -473,7 +472,7 @@ cudaError_t few_go(const Kv4AttnArgs& a, cudaStream_t s) {
 
 cudaError_t launch_kv4_attn_few(int dtype, int d, const Kv4AttnArgs& a, cudaStream_t s) {
   if (dtype == FASTAR_F32) return d == 128 ? few_go<float, 128, 1>(a, s) : few_go<float, 64, 1>(a, s);
-  const bool two = (int64_t)(a.Hq / a.Hkv) * a.nq > 8;
+  const bool two = a.rows > 8;
   if (d == 128) return two ? few_go<__nv_bfloat16, 128, 2>(a, s) : few_go<__nv_bfloat16, 128, 1>(a, s);
   return two ? few_go<__nv_bfloat16, 64, 2>(a, s) : few_go<__nv_bfloat16, 64, 1>(a, s);
 }

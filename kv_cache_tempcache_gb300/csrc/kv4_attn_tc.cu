@@ -290,8 +290,8 @@ __device__ __forceinline__ void store_empty(const Kv4AttnArgs& a, RowOf w) {
 template <int kCta>
 __device__ __forceinline__ Kv4Item item_of(const Kv4AttnArgs& a, int row_tiles) {
   Kv4Item it;
-  it.group = a.Hq / a.Hkv;
-  const uint32_t rows = it.rows = (uint32_t)it.group * (uint32_t)a.nq, nq = (uint32_t)a.nq;      // Hq * nq fits 31 bits
+  it.group = a.group;
+  const uint32_t rows = it.rows = a.rows, nq = (uint32_t)a.nq;      // Hq * nq fits 31 bits
   const bool odd = row_tiles > 1 && (rows - 1) % (2 * kRT * kCta) < kRT * kCta;
   const int full_tiles = row_tiles - odd;
   uint32_t u = blockIdx.x / kCta;
@@ -522,9 +522,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
           }
           tc::tmem_wait_st();
           tc::tc_fence_before();
+          tc::named_bar(pair_bar, 64);                    // all of O is rescaled before either half's P goes
+          tc::tc_fence_after();
         }
-        tc::named_bar(pair_bar, 64);                      // all of O is rescaled before either half's P goes
-        tc::tc_fence_after();
       }
       // P over the logits' own columns: 32 logits are read again (held since the maximum, 64 took
       // registers that the loads and exponentials need to overlap) and become 16 columns, over
@@ -834,8 +834,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
 template <int D>
 cudaError_t tc_go(const Kv4AttnArgs& a, cudaStream_t s) {
   using Lay = Kv4Layout<D>;
-  const int64_t rows = (int64_t)(a.Hq / a.Hkv) * a.nq;
-  const int64_t rt = (rows + 2 * kRT * Lay::kCta - 1) / (2 * kRT * Lay::kCta);
+  const int64_t rt = ((int64_t)a.rows + 2 * kRT * Lay::kCta - 1) / (2 * kRT * Lay::kCta);
   const int64_t blocks = rt * a.Hkv * a.splits * Lay::kCta;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
   cudaError_t e = opt_in_smem((const void*)kv4_attn_tc_kernel<D>, (int)Lay::bytes);
