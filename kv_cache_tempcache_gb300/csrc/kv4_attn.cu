@@ -24,13 +24,8 @@ namespace {
 // nothing in o; (inf, 0) for the first split says that the output is in place already.
 // Bound: latency, so the loads do not wait for one another (kFew: at most 8 splits, all at once).
 template <typename T, int D, bool kFew>
-__global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnArgs a) {
+__device__ __forceinline__ void join_row(const Kv4AttnArgs& a, int64_t row, int64_t rows, int lane) {
   constexpr int CPL = D / 32;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = (int64_t)a.Hq * a.nq;
-  pdl_wait();
-  if (row >= rows) return;
   float m = neg_inf(), l = 0.f, o[CPL];
 #pragma unroll
   for (int i = 0; i < CPL; ++i) o[i] = 0.f;
@@ -108,12 +103,31 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnArgs a) {
   if (lane == 0 && a.lse) a.lse[row] = live ? m + logf(l) : neg_inf();
 }
 
+// A warp takes `per` rows, at most 32: with more than one it looks at all their first splits at once,
+// so that a call of many rows whose outputs are in place costs little.
+template <typename T, int D, bool kFew>
+__global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnArgs a, int per) {
+  const int64_t rows = (int64_t)a.Hq * a.nq, row0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * per;
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  if (row0 >= rows) return;
+  uint32_t todo = 1;
+  if (per > 1) {
+    const bool in = lane < per && row0 + lane < rows;
+    const float2 ml = in ? a.part_ml[row0 + lane] : make_float2(0.f, 0.f);
+    todo = __ballot_sync(0xffffffffu, in && !(ml.x == -neg_inf() && ml.y == 0.f));
+  }
+  for (; todo; todo &= todo - 1) join_row<T, D, kFew>(a, row0 + __ffs(todo) - 1, rows, lane);
+}
+
 template <typename T, int D>
 cudaError_t join_go(const Kv4AttnArgs& a, cudaStream_t s) {
-  const int64_t rows = (int64_t)a.Hq * a.nq;
-  const dim3 grid((unsigned)((rows + 3) / 4));
-  const cudaError_t e = a.splits <= 8 ? launch_dependent(kv4_join_kernel<T, D, true>, grid, dim3(128), 0, s, a)
-                                      : launch_dependent(kv4_join_kernel<T, D, false>, grid, dim3(128), 0, s, a);
+  // a row a warp up to as many rows as are resident at once, then up to 8
+  const int64_t rows = (int64_t)a.Hq * a.nq, resident = 48 * (int64_t)sm_count();
+  const int per = rows <= resident ? 1 : rows <= 8 * resident ? (int)((rows + resident - 1) / resident) : 8;
+  const dim3 grid((unsigned)((rows + 4 * per - 1) / (4 * per)));
+  const cudaError_t e = a.splits <= 8 ? launch_dependent(kv4_join_kernel<T, D, true>, grid, dim3(128), 0, s, a, per)
+                                      : launch_dependent(kv4_join_kernel<T, D, false>, grid, dim3(128), 0, s, a, per);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
