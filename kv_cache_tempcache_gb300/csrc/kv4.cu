@@ -1,20 +1,25 @@
 // Writing rows of K and V into the 4-bit cache, and reading rows back as the values they
-// stand for.  Both are bound by HBM.
+// stand for.  Both are bound by HBM in their bytes (2 read and 0.56 written a value, or the other
+// way round), and near it by the integer operations of the conversions.
 // Writing: a lane takes the 16 channels of a scale, d / 16 lanes a row, so a warp's codes and
 // scales leave as contiguous runs of 256 and 32 bytes.  4680 rows of K and V of 12 heads of 128
-// take 10.4 us (3.5 TB/s); with 8 channels a lane, whose scales two lanes form twice, 13.4.
+// take 8.2 us with the inputs partly in L2 (10.4 with the rounding by integer
+// operations and a check a channel for infinities; with 8 channels a lane, whose scales two lanes form twice,
+// 13.4).
 // Reading: 8 channels a lane, four rows at once, so that a warp's stores of 16-bit rows are runs
-// of 512 bytes.  14,033 rows back take 20.1 us (5.5 TB/s); with 16 channels a lane, whose 16-byte
-// stores lie 32 bytes apart, 23.4.
+// of 512 bytes.  14,033 rows of 12 heads back take 19.8 us (5.6 TB/s of 6.8 for a copy); with 16
+// channels a lane, whose 16-byte stores lie 32 bytes apart, 23.4.
 //
 // The scale is s = e4m3(max|x| / 6), the code e2m1(x / s), both rounded to nearest with ties
 // to even and held to the largest finite value.  Both roundings are exact decisions:
 //  - max|x| / 6 is formed rounded to odd (towards zero, the last bit set when inexact),
 //    which a second rounding to 4 bits cannot send to the wrong side of a middle;
 //  - a bf16 x has 8 significant bits and the middle of two codes times s at most 7, so x/s
-//    is the middle itself or at least 2^-8 away from it (relative).  x * (1/s) in fp32 is
-//    within 2^-23 of x/s; rounded to 17 bits it is the middle exactly when x/s is, and the
-//    conversion then breaks the tie as the definition does;
+//    is the middle itself or at least 2^-8 away from it (relative), 2^-10 at the least.  x * (1/s)
+//    is within 2^-21 of x/s (up to 8; above 6 the code is 6 whatever it is), and added to 1536 it
+//    is rounded to a multiple of 2^-13: to the middle exactly when x/s is it (a multiple of
+//    2^-2), else to its own side; the conversion then breaks the tie as the definition does.
+//    Adding and taking 1536 away run beside the integer operations, which bound this kernel;
 //  - an fp32 x is compared with the seven middles themselves (exact in fp32).
 // A NaN or an infinity has no 4-bit value: it is stored as 0, takes no part in the maximum
 // and sets a status bit, so the cache never holds one.
@@ -43,13 +48,17 @@ struct Kv4AppendDev {
   int32_t* status;
 };
 
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* f) {
-  load8(p, f);
-  load8(p + 8, f + 8);
-}
-__device__ __forceinline__ void load16(const float* p, float* f) {
-  load8(p, f);
-  load8(p + 8, f + 8);
+// 16 channels as they lie in memory.
+template <typename T>
+struct Row16 {
+  uint4 u[sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Row16<T> load16(const T* p) {
+  Row16<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T); ++i) r.u[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
 }
 
 // e4m3 of a / 6 (a >= 0, finite), as its byte.
@@ -69,37 +78,66 @@ __device__ __forceinline__ uint32_t pair_code(float a, float b) {
   return r;
 }
 
-__device__ __forceinline__ float snap17(float r) { return __int_as_float((__float_as_int(r) + 0x40) & ~0x7f); }
+__device__ __forceinline__ float scale_of(uint32_t sb) {
+  return __half2float(__ushort_as_half((uint16_t)(kv4::scale_f16x2(sb) & 0xffffu)));
+}
 
-// The 16 codes of x (two words) and the scale's byte.
-template <bool kBf16>
-__device__ __forceinline__ uint32_t quantise16(float* x, float down, uint2& codes, bool& bad) {
-  float a = 0.f;
+// The 16 codes of a row's share (two words) and the scale's byte; down = 2^-e.
+__device__ __forceinline__ uint32_t quantise16(const Row16<__nv_bfloat16>& r, float down, uint2& codes, bool& bad) {
+  uint32_t x[8] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w, r.u[1].x, r.u[1].y, r.u[1].z, r.u[1].w};
+  auto largest = [&]() {                     // the largest magnitude's bits, two channels at a time
+    uint32_t b = x[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) b = __vmaxu2(b, x[i] & 0x7fff7fffu);
+    return max(b & 0xffffu, b >> 16);
+  };
+  uint32_t big = largest();
+  if (big >= 0x7f80u) {                      // a value that is not finite
+    bad = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((x[i] & 0x7f80u) == 0x7f80u) x[i] &= 0xffff0000u;
+      if ((x[i] & 0x7f800000u) == 0x7f800000u) x[i] &= 0xffffu;
+    }
+    big = largest();
+  }
+  const uint32_t sb = scale_byte(__uint_as_float(big << 16) * down);
+  const float s = scale_of(sb), inv = s > 0.f ? 1.0f / s * down : 0.f;
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float lo = __uint_as_float(x[i] << 16), hi = __uint_as_float(x[i] & 0xffff0000u);
+    const float a = fmaf(lo, inv, 1536.f) - 1536.f, b = fmaf(hi, inv, 1536.f) - 1536.f;
+    // the sign of what became 0 too (in the low half, bit 15 of x[i], and of its float)
+    w[i >> 2] |= pair_code(__uint_as_float(__float_as_uint(a) | (__float_as_uint(lo) & 0x80000000u)),
+                           __uint_as_float(__float_as_uint(b) | (x[i] & 0x80000000u)))
+                 << (8 * (i & 3));
+  }
+  codes = make_uint2(w[0], w[1]);
+  return sb;
+}
+__device__ __forceinline__ uint32_t quantise16(const Row16<float>& r, float down, uint2& codes, bool& bad) {
+  float x[16], a = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const bool fin = (__float_as_uint(x[i]) & 0x7f800000u) != 0x7f800000u;
+    const uint4& u = r.u[i >> 2];
+    const uint32_t v = (i & 3) == 0 ? u.x : (i & 3) == 1 ? u.y : (i & 3) == 2 ? u.z : u.w;
+    const bool fin = (v & 0x7f800000u) != 0x7f800000u;
     bad |= !fin;
-    x[i] = fin ? x[i] * down : 0.f;
+    x[i] = fin ? __uint_as_float(v) * down : 0.f;
     a = fmaxf(a, fabsf(x[i]));
   }
   const uint32_t sb = scale_byte(a);
-  const float s = __half2float(__ushort_as_half((uint16_t)(kv4::scale_f16x2(sb) & 0xffffu)));
+  const float s = scale_of(sb);
   uint32_t w[2] = {0u, 0u};
-  if (kBf16) {
-    const float inv = s > 0.f ? 1.0f / s : 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; i += 2)
-      w[i >> 3] |= pair_code(snap17(x[i] * inv), snap17(x[i + 1] * inv)) << (4 * (i & 7));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float m = fabsf(x[i]);
-      uint32_t c = __float_as_uint(x[i]) >> 31 << 3;
-      if (s > 0.f)
-        c += (m > 0.25f * s) + (m >= 0.75f * s) + (m > 1.25f * s) + (m >= 1.75f * s) + (m > 2.5f * s) +
-             (m >= 3.5f * s) + (m > 5.0f * s);
-      w[i >> 3] |= c << (4 * (i & 7));
-    }
+  for (int i = 0; i < 16; ++i) {
+    const float m = fabsf(x[i]);
+    uint32_t c = __float_as_uint(x[i]) >> 31 << 3;
+    if (s > 0.f)
+      c += (m > 0.25f * s) + (m >= 0.75f * s) + (m > 1.25f * s) + (m >= 1.75f * s) + (m > 2.5f * s) +
+           (m >= 3.5f * s) + (m > 5.0f * s);
+    w[i >> 3] |= c << (4 * (i & 7));
   }
   codes = make_uint2(w[0], w[1]);
   return sb;
@@ -109,7 +147,6 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreadsQ) kv4_append_kernel(const Kv4AppendDev a) {
   constexpr int LPR = D / 16;                 // lanes of a row
   constexpr int RB = kThreadsQ / LPR;         // rows of a block
-  constexpr bool kBf16 = sizeof(T) == 2;
   const int64_t per = (a.n + RB - 1) / RB > 0 ? (a.n + RB - 1) / RB : 1;   // blocks of a head
   const int h = (int)(blockIdx.x / per);
   const int64_t t = (int64_t)(blockIdx.x % per) * RB + threadIdx.x / LPR;
@@ -124,16 +161,15 @@ __global__ void __launch_bounds__(kThreadsQ) kv4_append_kernel(const Kv4AppendDe
     }
   }
   if (t >= a.n || !sane || at + t >= a.cap) return;
-  float k[16], v[16];
-  load16(static_cast<const T*>(a.k) + h * a.k_hs + t * a.k_ts + li * 16, k);
-  load16(static_cast<const T*>(a.v) + h * a.v_hs + t * a.v_ts + li * 16, v);
+  const Row16<T> k = load16(static_cast<const T*>(a.k) + h * a.k_hs + t * a.k_ts + li * 16);
+  const Row16<T> v = load16(static_cast<const T*>(a.v) + h * a.v_hs + t * a.v_ts + li * 16);
   const int64_t row = (int64_t)h * a.cap + at + t;
   bool bad = false;
   uint2 c;
-  uint32_t sb = quantise16<kBf16>(k, kv4::pow2i(-kv4::head_exp(a.k_exp, h)), c, bad);
+  uint32_t sb = quantise16(k, kv4::pow2i(-kv4::head_exp(a.k_exp, h)), c, bad);
   reinterpret_cast<uint2*>(a.kc)[row * LPR + li] = c;
   a.ks[row * LPR + li] = (uint8_t)sb;
-  sb = quantise16<kBf16>(v, kv4::pow2i(-kv4::head_exp(a.v_exp, h)), c, bad);
+  sb = quantise16(v, kv4::pow2i(-kv4::head_exp(a.v_exp, h)), c, bad);
   reinterpret_cast<uint2*>(a.vc)[row * LPR + li] = c;
   a.vs[row * LPR + li] = (uint8_t)sb;
   if (bad) flag_status(a.status, FASTAR_DEV_NONFINITE);
