@@ -132,17 +132,21 @@ cudaError_t join_go(const Kv4AttnArgs& a, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Rows of a KV head that take the few-rows kernel (kv4_attn_few.cu) in bf16; in fp32 all do.
+// Rows of a KV head that take the few-rows kernel (kv4_attn_few.cu) in bf16; in fp32 all do.  At 16
+// rows it and the tcgen05 kernel take 21 and 23 us over 9000 rows of 8 heads, 64 and 119 over
+// 131,071, 17 and 19 over 9000 rows of 64 channels; above 16 it would read the cache twice.
 constexpr int64_t kFewRows = 16;
 
-// Splits for it: one CTA a multiprocessor, but none under 1024 keys, two blocks a warp (what a
-// split saves below that, the join costs).  items: KV heads, in fp32
-// times groups of 8 rows.
-int splits_few(int64_t items, int64_t cap) {
-  const int64_t want = sm_count() / items, most = cap / 1024;
+// Splits for it: one CTA a multiprocessor, but none under a block of 32 keys a warp, and none at
+// all for fewer than three of those (there the join costs more than they save; 1000 rows: 13 us
+// either way).  Against two blocks a warp: one token of 12 heads over 2000 rows 19 -> 15 us, twelve
+// tokens 19 -> 17, five fp32 tokens of 16 heads over 3000 rows 18 -> 17.  items: KV heads, in fp32
+// times groups of 8 rows; warps: of a CTA.
+int splits_few(int64_t items, int64_t cap, int warps) {
+  const int64_t want = sm_count() / items, most = cap / (32 * warps);
   int64_t s = want < most ? want : most;
   if (s > kKv4MaxSplits) s = kKv4MaxSplits;
-  return s < 1 ? 1 : (int)s;
+  return s < 1 || most < 3 ? 1 : (int)s;
 }
 
 // Splits for the tensor-core kernel, by a model of its time over a full cache: waves of CTAs
@@ -200,8 +204,8 @@ cudaError_t run(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStream_t s) {
 
 int kv4_attn_splits(int dtype, int d, int Hq, int Hkv, int64_t nq, int64_t cap, int* min_tiles) {
   const int64_t rows = (int64_t)(Hq / Hkv) * nq;
-  if (dtype == FASTAR_F32) return splits_few((rows + 7) / 8 * Hkv, cap);
-  return rows <= kFewRows ? splits_few(Hkv, cap) : splits_tc(d, rows, Hkv, cap, min_tiles);
+  if (dtype == FASTAR_F32) return splits_few((rows + 7) / 8 * Hkv, cap, 8);
+  return rows <= kFewRows ? splits_few(Hkv, cap, rows > 8 ? 8 : 16) : splits_tc(d, rows, Hkv, cap, min_tiles);
 }
 
 size_t kv4_attn_workspace(int d, int Hq, int Hkv, int64_t nq, int64_t cap) {
