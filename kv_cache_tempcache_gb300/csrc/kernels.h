@@ -222,6 +222,7 @@ struct Kv4AttnArgs {
   int group;
   uint32_t rows;
   int splits;
+  bool alone;                         // tcgen05 kernel, d = 128: single CTAs instead of pairs
   int min_tiles;                      // tcgen05 kernel: key tiles of 128 a split should have (else 0)
   float* part_o;                      // [splits, Hq, nq, d]
   float2* part_ml;                    // [splits, Hq, nq]

@@ -149,16 +149,27 @@ int splits_few(int64_t items, int64_t cap, int warps) {
   return s < 1 || most < 3 ? 1 : (int)s;
 }
 
+// The tensor-core kernel at d = 128: CTAs alone where the rows are one tile of 128 and the full cache
+// gives each multiprocessor two key tiles or more, else in pairs.  A pair halves the unpacking,
+// which bounds it with many rows; with one tile half its rows are empty, and what bounds it is one
+// tile's way from product to product, of which single CTAs run twice as many.  32 rows over
+// 131,071 keys of 8 heads take 76 us alone and 119 in pairs, 64 over 2000 of 12 heads 20 either
+// way, 64 over 500 of 12 heads 17 and 15.
+bool tc_alone(int d, int64_t rows, int Hkv, int64_t cap) {
+  return d == 128 && rows <= 128 && (cap + 127) / 128 * Hkv >= 2 * sm_count();
+}
+
 // Splits for the tensor-core kernel, by a model of its time over a full cache: waves of CTAs
 // (pairs of them at d = 128), each a fixed part and so much a key tile; items with one row
 // tile, half as long a tile, fill the last wave's gaps; and with splits the partials' way through
 // memory and the join.  The fewest splits within 2 % of the best.  (Measured: 1.5 us a tile of
-// 128 keys and 512 rows at d = 128, 8 us around them.)
+// 128 keys and 512 rows at d = 128, 8 us around them; 1.2 us a tile of a CTA alone.)
 // The cache's lengths are the device's, and may be far below its capacity: *min_tiles is what the
 // kernel keeps a split's key tiles to, 3 where all the splits run at once, else 40, beside which
 // the fixed part is small.
 int splits_tc(int d, int64_t rows, int Hkv, int64_t cap, int* min_tiles) {
-  const int cta = d / 64;                 // CTAs that work as one (kv4_attn_tc.cu)
+  const bool alone = tc_alone(d, rows, Hkv, cap);
+  const int cta = alone ? 1 : d / 64;     // CTAs that work as one (kv4_attn_tc.cu)
   const int64_t slots = sm_count() / cta, tiles = (cap + 127) / 128;
   const int64_t half = (rows - 1) % (256 * cta) < 128 * cta ? Hkv : 0;
   const int64_t full = (rows + 256 * cta - 1) / (256 * cta) * Hkv - half;
@@ -166,7 +177,7 @@ int splits_tc(int d, int64_t rows, int Hkv, int64_t cap, int* min_tiles) {
   auto cost = [&](int64_t s) {
     const int64_t waves = (full * s + slots - 1) / slots, gaps = 2 * (waves * slots - full * s);
     const int64_t rest = half * s > gaps ? (half * s - gaps + slots - 1) / slots : 0;
-    const double keys = (double)((tiles + s - 1) / s) * tile;
+    const double keys = (double)((tiles + s - 1) / s) * (alone ? 1.5 * tile : tile);
     const double join = s > 1 ? 4.0 + 2e-6 * s * rows * Hkv * (d + 2) * 4 / 4.0 : 0.0;
     return waves * (fixed + keys) + rest * (fixed + 0.6 * keys) + join;
   };
@@ -193,6 +204,7 @@ cudaError_t run(int dtype, int d, Kv4AttnArgs a, void* ws, cudaStream_t s) {
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * a.Hq * a.nq * d);
   }
   const bool few = dtype == FASTAR_F32 || a.rows <= kFewRows;
+  a.alone = tc_alone(d, a.rows, a.Hkv, a.cap);
   if (!few && a.min_tiles == 0) a.min_tiles = 1;         // one split
   const cudaError_t e = few ? launch_kv4_attn_few(dtype, d, a, s) : launch_kv4_attn_tc(d, a, s);
   if (e != cudaSuccess || a.splits == 1) return e;

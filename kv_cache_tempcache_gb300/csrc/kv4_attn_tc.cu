@@ -82,20 +82,25 @@ struct alignas(16) Kv4Ctl {
   float mx[kRT];
 };
 
-// One CTA (d = 64) or a pair (d = 128).  What a CTA holds of a tile: KR keys of K in blocks of
-// 64 channels, all 128 keys of V with 64 channels.
-template <int D>
+// C CTAs work as one: at d = 64 one, at d = 128 a pair, or one for calls of a single row tile (kOne).
+// What a CTA holds of a tile: KR keys of K, all 128 keys of V with D / C channels; in blocks of 64
+// channels.
+template <int D, int C>
 struct Kv4Layout {
-  static constexpr int kCta = D / 64;
+  static constexpr int kCta = C;
+  static constexpr bool kOne = D > 64 * C;
+  static constexpr int stages = kOne ? 2 : kStages;
   static constexpr int KR = kKT / kCta;
   static constexpr size_t q_tile = (size_t)kRT * D * 2, q_blk = kRT * 128;
   static constexpr size_t k_tile = (size_t)KR * D * 2, k_blk = KR * 128;
-  static constexpr size_t v_tile = (size_t)kKT * 128;
+  static constexpr size_t v_tile = (size_t)kKT * (D / C) * 2, v_blk = kKT * 128;
   static constexpr size_t in_codes = (size_t)kKT * D / 2, in_tile = in_codes + (size_t)kKT * D / 16;
   static constexpr size_t q = 0;
-  static constexpr size_t k = q + 2 * q_tile;
-  static constexpr size_t v = k + kStages * k_tile;
-  static constexpr size_t in = v + kStages * v_tile;
+  static constexpr size_t k = q + (kOne ? 1 : 2) * q_tile;
+  static constexpr size_t v = k + stages * k_tile;
+  static constexpr size_t in = v + stages * v_tile;
+  // at the end: the odd tiles' output (128 rows of D floats), and 4 KB a softmax warp
+  static constexpr size_t odd_o = kOne ? k : q, out = kOne ? v : k;
   static constexpr size_t ctl = in + kIn * in_tile;
   static constexpr size_t bytes = ctl + sizeof(Kv4Ctl) + 1024;
   static constexpr uint32_t s_col = 0, o_col = 256;   // two 128-column buffers each
@@ -325,10 +330,10 @@ __device__ __forceinline__ Kv4Item item_of(const Kv4AttnArgs& a, int row_tiles) 
   return it;
 }
 
-template <int D>
+template <int D, int C>
 __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4AttnArgs a, int row_tiles) {
-  using Lay = Kv4Layout<D>;
-  constexpr int kCta = Lay::kCta;
+  using Lay = Kv4Layout<D, C>;
+  constexpr int kCta = C;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Kv4Ctl& sm = *reinterpret_cast<Kv4Ctl*>(base + Lay::ctl);
@@ -551,7 +556,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     tc::tc_fence_after();
     float l = l0 + l1;
     sm.ex[half][w][row] = l;
-    float4* shared_o = reinterpret_cast<float4*>(base + Lay::q);    // Q has been used: 128 rows x D floats
+    float4* shared_o = reinterpret_cast<float4*>(base + Lay::odd_o);   // Q, or K, has been used
     constexpr int CH = D / 4;                                       // 16-byte chunks of a row
     if (both && w == 1) {
       if (half == 0) sm.mx[row] = m;
@@ -586,9 +591,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
       const float f = partial ? up : live ? up / l : 0.f;
       // Rows of 128 bytes (32 fp32 or 64 bf16 channels; 64 bytes of 32 bf16) go through shared
-      // memory (the ring of K has been used; 4 KB a warp), so that they leave as whole runs; written
+      // memory (the ring of K, or of V, has been used), so that they leave as whole runs; written
       // 16 bytes a thread, a row each, they took 5 us of a CTA.
-      uint8_t* stg = base + Lay::k + warp * 4096;
+      uint8_t* stg = base + Lay::out + warp * 4096;
       uint8_t* out = partial ? reinterpret_cast<uint8_t*>(a.part_o) : static_cast<uint8_t*>(a.out);
       const int64_t off = !has     ? -1
                           : partial ? (((int64_t)split * a.Hq + at.head) * a.nq + at.t) * D * 4 + half * HD * 4
@@ -655,58 +660,63 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     // ---------------- unpack K and V ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (kCta == 2) pair_wait();
-    // A thread takes two runs of 32 codes (16 bytes) of a tile: of K's KR rows x D channels, or of
-    // V's 128 rows x this CTA's 64 channels.  With four runs to a row (K at d = 128) runs 2 and
+    // A thread takes two (four) runs of 32 codes (16 bytes) of a tile: of K's KR rows x D channels, or
+    // of V's 128 rows x this CTA's channels.  With four runs to a row (K at d = 128) runs 2 and
     // 3 write their 16-byte chunks in another order: so the 8 lanes of a store phase always
     // hit 8 different bank groups of the swizzled tile.
     const int t = threadIdx.x & 127;
-    constexpr int KP = D / 32;                            // runs of a row of K
+    constexpr int KP = D / 32, VP = D / C / 32;           // runs of a row of K, of V
+    constexpr int kRuns = Lay::kOne ? 4 : 2;
     const bool isv = warp >= kSoftWarps + 4;              // warps 16-19: K, 20-23: V
 #pragma unroll 1
     for (int n = isv; n < 2 * T; n += 2) {
-      const int j = n >> 1, st = j % kStages, in = n % kIn;
+      const int j = n >> 1, st = j % Lay::stages, in = n % kIn;
       uint64_t* empty = isv ? &sm.v_empty[st] : &sm.k_empty[st];
       uint64_t* full = isv ? &sm.v_full[st] : &sm.k_full[st];
-      const int part = isv || KP == 2 ? t & 1 : t & 3, row0 = isv || KP == 2 ? t >> 1 : t >> 2;
-      const int rstep = isv || KP == 2 ? 64 : 32;
+      const bool two = KP == 2 || (VP == 2 && isv);       // runs to a row: two, or four
+      const int part = two ? t & 1 : t & 3, row0 = two ? t >> 1 : t >> 2;
+      const int rstep = two ? 64 : 32;
       const int flip = part & 2;
       // the run's place in the packed tile: 16 bytes of codes, two scales
-      const int run0 = isv ? row0 * KP + (kCta == 2 ? 2 * rank : 0) + part : t;
+      const int run0 = isv && VP < KP ? row0 * KP + 2 * rank + part : t;
       const int runstep = rstep * KP;
       if (n == (isv ? 1 : 2)) tc::named_bar(isv ? 12 : 11, kHeld);
-      if (!wait_warp(&sm.in_full[in], (n / kIn) & 1, abort) || !wait_warp(empty, ((j / kStages) & 1) ^ 1, abort)) break;
+      if (!wait_warp(&sm.in_full[in], (n / kIn) & 1, abort) || !wait_warp(empty, ((j / Lay::stages) & 1) ^ 1, abort)) break;
       const uint8_t* packed = base + Lay::in + in * Lay::in_tile;
       uint8_t* tile = base + (isv ? Lay::v + (size_t)st * Lay::v_tile : Lay::k + (size_t)st * Lay::k_tile);
       // rows past the last key hold what is in memory there, or nothing: they count as 0
       const int left = (int)it.most - (int)(it.j0 + j) * kKT - (isv ? 0 : rank * Lay::KR);
-      uint4 c[2];
-      uint32_t s[2];
+#pragma unroll 1
+      for (int g = 0; g < kRuns; g += 2) {
+        uint4 c[2];
+        uint32_t s[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        c[k] = reinterpret_cast<const uint4*>(packed)[run0 + k * runstep];
-        s[k] = reinterpret_cast<const uint16_t*>(packed + Lay::in_codes)[run0 + k * runstep];
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int row = row0 + k * rstep;
-        if (row >= left) c[k] = make_uint4(0, 0, 0, 0), s[k] = 0;
-        uint32_t wv[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
-        uint32_t s0 = kv4::scale_f16x2(s[k]), s1 = kv4::scale_f16x2(s[k] >> 8);
-        if (KP == 4 && flip) {
-          uint32_t x = wv[0];
-          wv[0] = wv[2], wv[2] = x;
-          x = wv[1];
-          wv[1] = wv[3], wv[3] = x;
-          x = s0;
-          s0 = s1, s1 = x;
+        for (int k = 0; k < 2; ++k) {
+          c[k] = reinterpret_cast<const uint4*>(packed)[run0 + (g + k) * runstep];
+          s[k] = reinterpret_cast<const uint16_t*>(packed + Lay::in_codes)[run0 + (g + k) * runstep];
         }
-        uint8_t* dst = tile + (KP == 4 && flip ? Lay::k_blk : 0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t o[4];
-          kv4::unpack8(wv[e], e < 2 ? s0 : s1, o);
-          *reinterpret_cast<uint4*>(dst + tc::sw128_off(row, (part & 1) * 4 + (e ^ flip))) =
-              make_uint4(o[0], o[1], o[2], o[3]);
+        for (int k = 0; k < 2; ++k) {
+          const int row = row0 + (g + k) * rstep;
+          if (row >= left) c[k] = make_uint4(0, 0, 0, 0), s[k] = 0;
+          uint32_t wv[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+          uint32_t s0 = kv4::scale_f16x2(s[k]), s1 = kv4::scale_f16x2(s[k] >> 8);
+          if (KP == 4 && flip) {
+            uint32_t x = wv[0];
+            wv[0] = wv[2], wv[2] = x;
+            x = wv[1];
+            wv[1] = wv[3], wv[3] = x;
+            x = s0;
+            s0 = s1, s1 = x;
+          }
+          uint8_t* dst = tile + (KP == 4 && flip ? Lay::k_blk : 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t o[4];
+            kv4::unpack8(wv[e], e < 2 ? s0 : s1, o);
+            *reinterpret_cast<uint4*>(dst + tc::sw128_off(row, (part & 1) * 4 + (e ^ flip))) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
         }
       }
       tc::fence_proxy_async();
@@ -756,7 +766,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       constexpr uint32_t idesc_qk = idesc_f16(kRT * kCta, kKT, false), idesc_pv = idesc_f16(kRT * kCta, D, true);
       const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(base + Lay::q));
       const uint64_t k_desc = tc::sw128_desc(tc::smem_u32(base + Lay::k));
-      const uint64_t v_desc = tc::sw128_mn_desc(tc::smem_u32(base + Lay::v), Lay::v_tile);
+      const uint64_t v_desc = tc::sw128_mn_desc(tc::smem_u32(base + Lay::v), Lay::v_blk);
       bool ok = true;
       const int step = both ? 2 : 1;
       int kst[2], vst[2], count[2];                       // stages of K and V, key tiles by row tile
@@ -790,7 +800,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
             if (!ok) break;
             if (w == 1 || both) commit<kCta>(&sm.v_empty[vst[w]]);
             vst[w] += step;
-            if (vst[w] >= kStages) vst[w] -= kStages, vph[w] ^= 1;
+            if (vst[w] >= Lay::stages) vst[w] -= Lay::stages, vph[w] ^= 1;
           }
           if (i + 1 < count[w]) {
             ok = (i >= 0 || tc::mbar_wait(&sm.q_full[both ? 0 : w], 0, abort)) &&
@@ -806,7 +816,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
             commit<kCta>(&sm.s_full[w]);
             if (w == 1 || both) commit<kCta>(&sm.k_empty[kst[w]]);
             kst[w] += step;
-            if (kst[w] >= kStages) kst[w] -= kStages, kph[w] ^= 1;
+            if (kst[w] >= Lay::stages) kst[w] -= Lay::stages, kph[w] ^= 1;
           }
         }
       }
@@ -831,13 +841,13 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
   if (threadIdx.x == 0 && sm.abort) flag_status(a.status, FASTAR_DEV_TIMEOUT);
 }
 
-template <int D>
+template <int D, int C>
 cudaError_t tc_go(const Kv4AttnArgs& a, cudaStream_t s) {
-  using Lay = Kv4Layout<D>;
+  using Lay = Kv4Layout<D, C>;
   const int64_t rt = ((int64_t)a.rows + 2 * kRT * Lay::kCta - 1) / (2 * kRT * Lay::kCta);
   const int64_t blocks = rt * a.Hkv * a.splits * Lay::kCta;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  cudaError_t e = opt_in_smem((const void*)kv4_attn_tc_kernel<D>, (int)Lay::bytes);
+  cudaError_t e = opt_in_smem((const void*)kv4_attn_tc_kernel<D, C>, (int)Lay::bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
@@ -850,7 +860,7 @@ cudaError_t tc_go(const Kv4AttnArgs& a, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv4_attn_tc_kernel<D>, a, (int)rt);
+  e = cudaLaunchKernelEx(&cfg, kv4_attn_tc_kernel<D, C>, a, (int)rt);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -858,7 +868,8 @@ cudaError_t tc_go(const Kv4AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_kv4_attn_tc(int d, const Kv4AttnArgs& a, cudaStream_t s) {
-  return d == 128 ? tc_go<128>(a, s) : tc_go<64>(a, s);
+  if (d == 64) return tc_go<64, 1>(a, s);
+  return a.alone ? tc_go<128, 1>(a, s) : tc_go<128, 2>(a, s);
 }
 
 }  // namespace fastar

@@ -283,6 +283,19 @@ def test_many_rows(Hkv, G, nq, d, cap, lens, block):
 
 
 @pytest.mark.parametrize("Hkv,G,nq,d,cap,lens,block", [
+    (1, 1, 17, 128, 16, [0], 0), (1, 1, 17, 128, 16, [1], 1), (4, 4, 8, 128, 400, [127, 128, 129, 385], 0),
+    (2, 1, 128, 128, 272, [257, 100], 1), (1, 8, 16, 128, 1040, [1025], 5), (3, 1, 64, 128, 4112, [4100, 0, 2000], 0),
+    (2, 1, 100, 128, 60000, [60000, 777], 0), (40, 1, 33, 128, 1008, [25 * h + 8 for h in range(40)], 11),
+    (20, 2, 11, 128, 3008, [3000] * 20, 0)])
+def test_rows_of_one_tile(Hkv, G, nq, d, cap, lens, block):
+    # 17 to 128 rows a KV head: one row tile, on even and odd key tiles; by CTAs alone where the cache
+    # is large (the last three), else in pairs
+    c = _filled(Hkv, cap, d, cap + nq)
+    q = _rand((nq, Hkv * G, d), nq, 1.5).bfloat16().transpose(0, 1)
+    _attend(q, c, lens, block)
+
+
+@pytest.mark.parametrize("Hkv,G,nq,d,cap,lens,block", [
     (1, 1, 300, 128, 912, [899], 100), (2, 2, 90, 64, 2064, [2050, 0], 1), (3, 1, 17, 128, 3008, [3000, 5, 1025], 0)])
 def test_many_fp32_rows(Hkv, G, nq, d, cap, lens, block):
     c = _filled(Hkv, cap, d, cap + nq)
