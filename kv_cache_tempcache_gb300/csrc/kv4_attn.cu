@@ -153,7 +153,7 @@ int splits_few(int64_t items, int64_t cap, int warps) {
 // gives each multiprocessor two key tiles or more, else in pairs.  A pair halves the unpacking,
 // which bounds it with many rows; with one tile half its rows are empty, and what bounds it is one
 // tile's way from product to product, of which single CTAs run twice as many.  32 rows over
-// 131,071 keys of 8 heads take 76 us alone and 119 in pairs, 64 over 2000 of 12 heads 20 either
+// 131,071 keys of 8 heads take 74 us alone and 119 in pairs, 64 over 2000 of 12 heads 20 either
 // way, 64 over 500 of 12 heads 17 and 15.
 bool tc_alone(int d, int64_t rows, int Hkv, int64_t cap) {
   return d == 128 && rows <= 128 && (cap + 127) / 128 * Hkv >= 2 * sm_count();

@@ -50,7 +50,7 @@ namespace {
 constexpr int kRT = 128;               // rows of a row tile in a CTA
 constexpr int kKT = 128;               // keys of a tile
 constexpr int kStages = 3;             // fp16 tiles of K and of V
-constexpr int kIn = 4;                 // packed tiles on their way
+constexpr int kIn = 4, kMaxIn = 6;     // packed tiles on their way
 constexpr int kSoftWarps = 16, kUnpackWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kUnpackWarps;
 constexpr int kThreadsT = 896;         // the last warpgroup: MMA warp, copy warp, two idle ones
@@ -72,7 +72,7 @@ struct Kv4Item {
 constexpr int kHeld = (kSoftWarps + 4) * 32;
 
 struct alignas(16) Kv4Ctl {
-  uint64_t in_full[kIn], in_empty[kIn];                // packed tiles: K 0, V 0, K 1, V 1, ...
+  uint64_t in_full[kMaxIn], in_empty[kMaxIn];          // packed tiles: K 0, V 0, K 1, V 1, ...
   uint64_t q_full[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t s_full[2], p_full[2][2], fin;               // by row tile (P: first 32 keys of each half, last 32)
   Kv4Item item;
@@ -89,7 +89,7 @@ template <int D, int C>
 struct Kv4Layout {
   static constexpr int kCta = C;
   static constexpr bool kOne = D > 64 * C;
-  static constexpr int stages = kOne ? 2 : kStages;
+  static constexpr int stages = kOne ? 2 : kStages, ins = kOne ? kMaxIn : kIn;
   static constexpr int KR = kKT / kCta;
   static constexpr size_t q_tile = (size_t)kRT * D * 2, q_blk = kRT * 128;
   static constexpr size_t k_tile = (size_t)KR * D * 2, k_blk = KR * 128;
@@ -101,7 +101,7 @@ struct Kv4Layout {
   static constexpr size_t in = v + stages * v_tile;
   // at the end: the odd tiles' output (128 rows of D floats), and 4 KB a softmax warp
   static constexpr size_t odd_o = kOne ? k : q, out = kOne ? v : k;
-  static constexpr size_t ctl = in + kIn * in_tile;
+  static constexpr size_t ctl = in + ins * in_tile;
   static constexpr size_t bytes = ctl + sizeof(Kv4Ctl) + 1024;
   static constexpr uint32_t s_col = 0, o_col = 256;   // two 128-column buffers each
   static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
   // one thread finds the item (its divisions in all 28 warps took 5000 clocks), another sets the
   // barriers up, and rolled loops move the query rows.
   if (threadIdx.x == (kMmaWarp + 1) * 32) {
-    for (int i = 0; i < kIn; ++i) {
+    for (int i = 0; i < Lay::ins; ++i) {
       tc::mbar_init(&sm.in_full[i], 1);
       tc::mbar_init(&sm.in_empty[i], 4);
     }
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     const bool isv = warp >= kSoftWarps + 4;              // warps 16-19: K, 20-23: V
 #pragma unroll 1
     for (int n = isv; n < 2 * T; n += 2) {
-      const int j = n >> 1, st = j % Lay::stages, in = n % kIn;
+      const int j = n >> 1, st = j % Lay::stages, in = n % Lay::ins;
       uint64_t* empty = isv ? &sm.v_empty[st] : &sm.k_empty[st];
       uint64_t* full = isv ? &sm.v_full[st] : &sm.k_full[st];
       const bool two = KP == 2 || (VP == 2 && isv);       // runs to a row: two, or four
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       const int run0 = isv && VP < KP ? row0 * KP + 2 * rank + part : t;
       const int runstep = rstep * KP;
       if (n == (isv ? 1 : 2)) tc::named_bar(isv ? 12 : 11, kHeld);
-      if (!wait_warp(&sm.in_full[in], (n / kIn) & 1, abort) || !wait_warp(empty, ((j / Lay::stages) & 1) ^ 1, abort)) break;
+      if (!wait_warp(&sm.in_full[in], (n / Lay::ins) & 1, abort) || !wait_warp(empty, ((j / Lay::stages) & 1) ^ 1, abort)) break;
       const uint8_t* packed = base + Lay::in + in * Lay::in_tile;
       uint8_t* tile = base + (isv ? Lay::v + (size_t)st * Lay::v_tile : Lay::k + (size_t)st * Lay::k_tile);
       // rows past the last key hold what is in memory there, or nothing: they count as 0
@@ -744,9 +744,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       const uint32_t most = (uint32_t)it.most, j0 = it.j0;      // capacities fit 31 bits
       int n = 0;
       for (; n < 2 * T; ++n) {
-        const int in = n % kIn;
+        const int in = n % Lay::ins;
         const bool isv = n & 1;
-        if (!tc::mbar_wait(&sm.in_empty[in], ((n / kIn) & 1) ^ 1, abort)) break;
+        if (!tc::mbar_wait(&sm.in_empty[in], ((n / Lay::ins) & 1) ^ 1, abort)) break;
         const uint32_t key = (j0 + (uint32_t)(n >> 1)) * kKT + (isv ? 0u : (uint32_t)(rank * Lay::KR));
         const uint32_t nr = key < most ? min((most - key + 15) & ~15u, (uint32_t)(isv ? kKT : Lay::KR)) : 0u;
         uint8_t* dst = base + Lay::in + in * Lay::in_tile;
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       }
       // the last copies land before this thread leaves, whether or not anyone waits for them
       volatile int never = 0;
-      for (int x = n < kIn ? 0 : n - kIn; x < n; ++x) tc::mbar_wait(&sm.in_full[x % kIn], (x / kIn) & 1, &never, 400000000LL);
+      for (int x = n < Lay::ins ? 0 : n - Lay::ins; x < n; ++x) tc::mbar_wait(&sm.in_full[x % Lay::ins], (x / Lay::ins) & 1, &never, 400000000LL);
     }
     // ---------------- MMA issue (one thread of the pair) ----------------
     if (warp == kMmaWarp && rank == 0 && elect_one()) {
