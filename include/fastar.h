@@ -633,6 +633,16 @@ int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d
                     int64_t o_token_stride, float* lse, int32_t* dev_status, void* workspace, size_t workspace_bytes,
                     cudaStream_t stream);
 
+/* The four calls above with their arguments in one array of n 64-bit words, in the order of their
+ * declarations: integers and addresses as they are, floats as the bits of a double.  For bindings
+ * that pay for each argument (ctypes: 75 ns, 2 us for all of fastar_kv4_attn's).  A call or a
+ * number of words that is not one of theirs, or an int that does not fit 32 bits: FASTAR_EINVAL. */
+#define FASTAR_CALL_QK_NORM_ROPE 0   /* n = 30 */
+#define FASTAR_CALL_KV4_APPEND 1     /* n = 21 */
+#define FASTAR_CALL_KV4_READ 2       /* n = 13 */
+#define FASTAR_CALL_KV4_ATTN 3       /* n = 26 */
+int fastar_packed_call(int call, const void* words, int n);
+
 #ifdef __cplusplus
 }
 #endif

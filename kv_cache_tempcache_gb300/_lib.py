@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -78,6 +79,7 @@ _SIGS = {
     "fastar_kv4_read": [_I, _I, _L, _I, _P, _P, _P, _L, _L, _P, _L, _L, _P],
     "fastar_kv4_attn": [_P, _I, _I, _I, _L, _I, _L, _L, _P, _P, _P, _P, _P, _P, _L, _P, _L, _F, _P, _L, _L, _P, _P,
                         _P, _S, _P],
+    "fastar_packed_call": [_I, _P, _I],
 }
 _RESTYPES = {"fastar_status_string": ctypes.c_char_p, "fastar_workspace_bytes": ctypes.c_size_t,
              "fastar_kernel_launches": ctypes.c_longlong, "fastar_last_cuda_error": ctypes.c_char_p}
@@ -435,6 +437,19 @@ def fastar_sinusoidal_embedding(t, out, stream=None):
 _U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
 
 
+def _packer(call, name):
+    """(call, pack, n) for fastar_packed_call: the arguments of `name` as 64-bit words.  One ctypes
+    argument instead of up to thirty, 2 us less a call."""
+    args = _SIGS[name]
+    return call, struct.Struct("=" + "".join("d" if a is _F else "q" for a in args)).pack, len(args)
+
+
+_CALL_ROPE, _PACK_ROPE, _N_ROPE = _packer(0, "fastar_qk_norm_rope")
+_CALL_APPEND, _PACK_APPEND, _N_APPEND = _packer(1, "fastar_kv4_append")
+_CALL_READ, _PACK_READ, _N_READ = _packer(2, "fastar_kv4_read")
+_CALL_ATTN, _PACK_ATTN, _N_ATTN = _packer(3, "fastar_kv4_attn")
+
+
 def _refuse(rows, dense):
     """Raises for the first tensor that is not as expected.  rows: (name, [H, n, d] view, dtype,
     shape); dense: (name, contiguous tensor or None, dtype, shape)."""
@@ -461,15 +476,14 @@ def _dims3(name, t):
     return s
 
 
-def _strides(t, H, n, d):
+def _strides(st, H, n, d):
     """Head and token strides; the stride of a dimension of one element says nothing (torch may
     give any)."""
-    hs, ts, _ = t.stride()
-    return (hs if H > 1 else n * d), (ts if n > 1 else d)
+    return (st[0] if H > 1 else n * d), (st[1] if n > 1 else d)
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
 def _stream(stream, dev):
@@ -493,10 +507,12 @@ def fastar_qk_norm_rope(q, k, q_out, k_out, wq=None, wk=None, eps=1e-6, axes=(0,
     ks = (0 if k is None else k.shape[0], n, d)
     if not (
             dev >= 0 and dev == torch._C._cuda_getDevice()
-            and q.stride(2) == 1
-            and q_out.dtype is dt and q_out.shape == qs and q_out.stride(2) == 1 and q_out.get_device() == dev
-            and (k is None or k.dtype is dt and k.shape == ks and k.stride(2) == 1 and k.get_device() == dev
-                 and k_out.dtype is dt and k_out.shape == ks and k_out.stride(2) == 1 and k_out.get_device() == dev)
+            and (q_st := q.stride())[2] == 1
+            and q_out.dtype is dt and q_out.shape == qs and (qo_st := q_out.stride())[2] == 1
+            and q_out.get_device() == dev
+            and (k is None or k.dtype is dt and k.shape == ks and (k_st := k.stride())[2] == 1 and k.get_device() == dev
+                 and k_out.dtype is dt and k_out.shape == ks and (ko_st := k_out.stride())[2] == 1
+                 and k_out.get_device() == dev)
             and (wq is None or wq.dtype is _F32 and wq.shape == (d,) and wq.is_contiguous() and wq.get_device() == dev)
             and (wk is None or wk.dtype is _F32 and wk.shape == (d,) and wk.is_contiguous() and wk.get_device() == dev)
             and (pos is None or pos.dtype is _I32 and pos.shape == (n, 3) and pos.is_contiguous()
@@ -505,16 +521,16 @@ def fastar_qk_norm_rope(q, k, q_out, k_out, wq=None, wk=None, eps=1e-6, axes=(0,
         _refuse([("q", q, dt, qs), ("q_out", q_out, dt, qs), ("k", k, dt, ks), ("k_out", k_out, dt, ks)],
                 [("wq", wq, _F32, (d,)), ("wk", wk, _F32, (d,)), ("pos", pos, _I32, (n, 3)),
                  ("t0_dev", t0_dev, _I32, (1,))])
-    qhs, qts = _strides(q, Hq, n, d)
-    qohs, qots = _strides(q_out, Hq, n, d)
+    qhs, qts = _strides(q_st, Hq, n, d)
+    qohs, qots = _strides(qo_st, Hq, n, d)
     khs = kts = kohs = kots = 0
     if k is not None:
-        khs, kts = _strides(k, ks[0], n, d)
-        kohs, kots = _strides(k_out, ks[0], n, d)
-    rc = (_lib or load()).fastar_qk_norm_rope(
+        khs, kts = _strides(k_st, ks[0], n, d)
+        kohs, kots = _strides(ko_st, ks[0], n, d)
+    rc = (_lib or load()).fastar_packed_call(_CALL_ROPE, _PACK_ROPE(
         code, n, d, Hq, q.data_ptr(), qhs, qts, q_out.data_ptr(), qohs, qots, ks[0], _ptr(k), khs, kts, _ptr(k_out),
         kohs, kots, _ptr(wq), _ptr(wk), eps, axes[0], axes[1], axes[2], _ptr(pos), t0, _ptr(t0_dev), grid[0], grid[1],
-        theta, _stream(stream, dev))
+        theta, _stream(stream, dev)), _N_ROPE)
     if rc:
         _raise("fastar_qk_norm_rope", rc)
 
@@ -530,8 +546,8 @@ def fastar_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, at=None, len_o
     cs, ss, hs = (H, cap, d // 2), (H, cap, d // 16), (H,)
     if not (
             dev >= 0 and dev == torch._C._cuda_getDevice()
-            and k.stride(2) == 1
-            and v.dtype is dt and v.shape == rs and v.stride(2) == 1 and v.get_device() == dev
+            and (k_st := k.stride())[2] == 1
+            and v.dtype is dt and v.shape == rs and (v_st := v.stride())[2] == 1 and v.get_device() == dev
             and k_codes.dtype is _U8 and k_codes.shape == cs and k_codes.is_contiguous() and k_codes.get_device() == dev
             and k_scales.dtype is _U8 and k_scales.shape == ss and k_scales.is_contiguous()
             and k_scales.get_device() == dev
@@ -551,12 +567,12 @@ def fastar_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, at=None, len_o
                 [("k_codes", k_codes, _U8, cs), ("k_scales", k_scales, _U8, ss), ("v_codes", v_codes, _U8, cs),
                  ("v_scales", v_scales, _U8, ss), ("at", at, _I32, hs), ("len_out", len_out, _I32, hs),
                  ("dev_status", dev_status, _I32, (1,)), ("k_exp", k_exp, _I32, hs), ("v_exp", v_exp, _I32, hs)])
-    khs, kts = _strides(k, H, n, d)
-    vhs, vts = _strides(v, H, n, d)
-    rc = (_lib or load()).fastar_kv4_append(
+    khs, kts = _strides(k_st, H, n, d)
+    vhs, vts = _strides(v_st, H, n, d)
+    rc = (_lib or load()).fastar_packed_call(_CALL_APPEND, _PACK_APPEND(
         code, H, n, d, k.data_ptr(), khs, kts, v.data_ptr(), vhs, vts, _ptr(k_exp), _ptr(v_exp), _ptr(at),
         k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), cap, _ptr(len_out),
-        _ptr(dev_status), _stream(stream, dev))
+        _ptr(dev_status), _stream(stream, dev)), _N_APPEND)
     if rc:
         _raise("fastar_kv4_append", rc)
 
@@ -570,16 +586,17 @@ def fastar_kv4_read(codes, scales, first, out, exps=None, stream=None):
     cs, ss = (H, cap, d // 2), (H, cap, d // 16)
     if not (
             dev >= 0 and dev == torch._C._cuda_getDevice()
-            and out.stride(2) == 1
+            and (o_st := out.stride())[2] == 1
             and codes.dtype is _U8 and codes.shape == cs and codes.is_contiguous() and codes.get_device() == dev
             and scales.dtype is _U8 and scales.shape == ss and scales.is_contiguous() and scales.get_device() == dev
             and (exps is None or exps.dtype is _I32 and exps.shape == (H,) and exps.is_contiguous()
                  and exps.get_device() == dev)):
         _refuse([("out", out, dt, rs)],
                 [("codes", codes, _U8, cs), ("scales", scales, _U8, ss), ("exps", exps, _I32, (H,))])
-    ohs, ots = _strides(out, H, n, d)
-    rc = (_lib or load()).fastar_kv4_read(code, H, n, d, codes.data_ptr(), scales.data_ptr(), _ptr(exps), cap, int(first),
-                                          out.data_ptr(), ohs, ots, _stream(stream, dev))
+    ohs, ots = _strides(o_st, H, n, d)
+    rc = (_lib or load()).fastar_packed_call(_CALL_READ, _PACK_READ(
+        code, H, n, d, codes.data_ptr(), scales.data_ptr(), _ptr(exps), cap, int(first), out.data_ptr(), ohs, ots,
+        _stream(stream, dev)), _N_READ)
     if rc:
         _raise("fastar_kv4_read", rc)
 
@@ -597,8 +614,8 @@ def fastar_kv4_attn(q, k_codes, k_scales, v_codes, v_scales, lens, scale, out, l
     cs, ss, hs = (Hkv, cap, d // 2), (Hkv, cap, d // 16), (Hkv,)
     if not (
             dev >= 0 and dev == torch._C._cuda_getDevice()
-            and q.stride(2) == 1
-            and out.dtype is dt and out.shape == rs and out.stride(2) == 1 and out.get_device() == dev
+            and (q_st := q.stride())[2] == 1
+            and out.dtype is dt and out.shape == rs and (o_st := out.stride())[2] == 1 and out.get_device() == dev
             and k_codes.dtype is _U8 and k_codes.is_contiguous() and k_codes.shape == cs and k_codes.get_device() == dev
             and k_scales.dtype is _U8 and k_scales.shape == ss and k_scales.is_contiguous()
             and k_scales.get_device() == dev
@@ -621,13 +638,13 @@ def fastar_kv4_attn(q, k_codes, k_scales, v_codes, v_scales, lens, scale, out, l
         if workspace is not None:
             dense.append(("workspace", workspace, workspace.dtype, workspace.shape))
         _refuse([("q", q, dt, rs), ("out", out, dt, rs)], dense)
-    qhs, qts = _strides(q, Hq, nq, d)
-    ohs, ots = _strides(out, Hq, nq, d)
-    rc = (_lib or load()).fastar_kv4_attn(
+    qhs, qts = _strides(q_st, Hq, nq, d)
+    ohs, ots = _strides(o_st, Hq, nq, d)
+    rc = (_lib or load()).fastar_packed_call(_CALL_ATTN, _PACK_ATTN(
         q.data_ptr(), code, Hq, Hkv, nq, d, qhs, qts, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
         v_scales.data_ptr(), _ptr(k_exp), _ptr(v_exp), cap, lens.data_ptr(), block, scale, out.data_ptr(), ohs, ots,
         _ptr(lse), _ptr(dev_status), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream, dev))
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream, dev)), _N_ATTN)
     if rc:
         _raise("fastar_kv4_attn", rc)
 

@@ -2,6 +2,10 @@
 // Every check runs on the host before anything is enqueued.
 #include <atomic>
 #include <cstdint>
+#include <cstring>
+#include <tuple>
+#include <type_traits>
+#include <utility>
 
 #include "fastar.h"
 #include "kernels.h"
@@ -40,6 +44,35 @@ int check_tok(const void* p, int dtype, int d, int64_t hs, int64_t ts, int64_t n
 int check_kv4_cap(int64_t cap) { return cap < 16 || cap % 16 || cap > INT32_MAX ? FASTAR_EINVAL : FASTAR_OK; }
 int check_kv4(const void* codes, const void* scales) {
   return codes && scales && aligned16(codes) && aligned16(scales) ? FASTAR_OK : FASTAR_EINVAL;
+}
+
+// fastar_packed_call: a 64-bit word as an argument of type T; false if an int does not fit.
+template <typename T>
+bool from_word(int64_t w, T& v) {
+  if constexpr (std::is_pointer_v<T>) {
+    v = reinterpret_cast<T>(w);
+  } else if constexpr (std::is_same_v<T, float>) {
+    double d;
+    std::memcpy(&d, &w, sizeof(d));
+    v = (float)d;
+  } else {
+    v = (T)w;
+    if constexpr (sizeof(T) < 8) return (int64_t)v == w;
+  }
+  return true;
+}
+template <typename... A, size_t... I>
+int call_words(int (*fn)(A...), const int64_t* w, std::index_sequence<I...>) {
+  std::tuple<A...> a;
+  if (!(from_word(w[I], std::get<I>(a)) && ...)) return FASTAR_EINVAL;
+  return fn(std::get<I>(a)...);
+}
+template <typename... A>
+int call_packed(int (*fn)(A...), const void* words, int n) {
+  if (!words || n != (int)sizeof...(A)) return FASTAR_EINVAL;
+  int64_t w[sizeof...(A)];
+  std::memcpy(w, words, sizeof(w));
+  return call_words(fn, w, std::index_sequence_for<A...>{});
 }
 
 thread_local cudaError_t g_last_cuda = cudaSuccess;
@@ -799,6 +832,16 @@ int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d
   cudaError_t err = cudaSuccess;
   if (!fastar::launch_kv4_attn(dtype, d, a, workspace, workspace_bytes, stream, &err)) return FASTAR_EWORKSPACE;
   return cuda_rc(err);
+}
+
+int fastar_packed_call(int call, const void* words, int n) {
+  switch (call) {
+    case FASTAR_CALL_QK_NORM_ROPE: return call_packed(fastar_qk_norm_rope, words, n);
+    case FASTAR_CALL_KV4_APPEND: return call_packed(fastar_kv4_append, words, n);
+    case FASTAR_CALL_KV4_READ: return call_packed(fastar_kv4_read, words, n);
+    case FASTAR_CALL_KV4_ATTN: return call_packed(fastar_kv4_attn, words, n);
+    default: return FASTAR_EINVAL;
+  }
 }
 
 }  // extern "C"

@@ -129,3 +129,32 @@ def test_bindings_refuse_other_shapes_types_and_devices(lib):
         L.fastar_qk_norm_rope(k, k, k, None)
     with pytest.raises(ValueError, match="shape"):
         L.fastar_qk_norm_rope(k, k, k, _rows(n=5))
+
+
+def test_packed_calls(lib):
+    # the arguments as 64-bit words: refused like the calls themselves, and by their own number and range
+    def words(name, args):
+        return L._packer(0, name)[1](*args)
+
+    read = [L.BF16, 2, 4, 128, FAKE, FAKE, 0, 64, 0, FAKE, 512, 128, 0]
+    for change, code in (({2: 0}, L.OK), ({7: 65}, L.EINVAL), ({0: 7}, L.EUNSUPPORTED), ({8: 61}, L.ECAPACITY),
+                         ({1: 2 ** 31}, L.EINVAL), ({3: 128 + 2 ** 32}, L.EINVAL), ({4: 0}, L.EINVAL)):
+        a = list(read)
+        for i, v in change.items():
+            a[i] = v
+        assert lib.fastar_packed_call(2, words("fastar_kv4_read", a), 13) == code, change
+    good = words("fastar_kv4_read", read[:2] + [0] + read[3:])
+    assert lib.fastar_packed_call(2, good, 13) == L.OK
+    for call, w, n in ((2, good, 12), (2, good, 14), (4, good, 13), (-1, good, 13), (2, None, 13)):
+        assert lib.fastar_packed_call(call, w, n) == L.EINVAL
+    # a float travels as a double's bits: the scale of the attention, the base of the rotation
+    attn = [FAKE, L.BF16, 2, 2, 0, 128, 512, 128, FAKE, FAKE, FAKE, FAKE, 0, 0, 64, FAKE, 0, 0.1, FAKE, 512, 128, 0, 0,
+            0, 0, 0]
+    assert lib.fastar_packed_call(3, words("fastar_kv4_attn", attn), 26) == L.OK
+    attn[17] = -0.1
+    assert lib.fastar_packed_call(3, words("fastar_kv4_attn", attn), 26) == L.EINVAL
+    rope_args = [L.BF16, 0, 128, 2, FAKE, 512, 128, FAKE, 512, 128, 0, 0, 0, 0, 0, 0, 0, 0, 0, 1e-6, 44, 42, 42, 0, 0, 0, 3,
+                 4, 1e4, 0]
+    assert lib.fastar_packed_call(0, words("fastar_qk_norm_rope", rope_args), 30) == L.OK
+    rope_args[28] = 0.5
+    assert lib.fastar_packed_call(0, words("fastar_qk_norm_rope", rope_args), 30) == L.EINVAL
