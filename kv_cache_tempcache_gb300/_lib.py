@@ -431,10 +431,15 @@ def fastar_sinusoidal_embedding(t, out, stream=None):
 # ---- the 4-bit cache, and the norm and rotation before it -------------------------------------
 
 # Every check below refuses what a kernel would misread.  They run on each call of a step that
-# may be a few microseconds of device time, so a call asks for everything in one expression, and
-# only what fails it is looked at again, tensor by tensor, for the message.
+# may be a few microseconds of device time, so a call asks for everything in one expression, without
+# helpers (a Python call is 0.1 us), and only what fails it is looked at again, tensor by tensor,
+# for the message.  The stride of a dimension of one element says nothing (torch may give any):
+# a call passes the dense one.
 
 _U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
+_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+_device = getattr(torch._C, "_cuda_getDevice", None)                  # not in builds without CUDA
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _packer(call, name):
@@ -476,18 +481,8 @@ def _dims3(name, t):
     return s
 
 
-def _strides(st, H, n, d):
-    """Head and token strides; the stride of a dimension of one element says nothing (torch may
-    give any)."""
-    return (st[0] if H > 1 else n * d), (st[1] if n > 1 else d)
-
-
-def _ptr(t):
-    return 0 if t is None else t.data_ptr()
-
-
-def _stream(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+def _raise_dtype(dt):
+    raise TypeError(f"unsupported dtype {dt}")
 
 
 def _raise(name, rc):
@@ -501,12 +496,12 @@ def fastar_qk_norm_rope(q, k, q_out, k_out, wq=None, wk=None, eps=1e-6, axes=(0,
     with the frame, the row and the column; pos [n, 3] int32, or the grid's positions."""
     Hq, n, d = qs = _dims3("q", q)
     dt, dev = q.dtype, q.get_device()
-    code = dtype_code(dt)
+    code = _CODES[dt] if dt in _CODES else _raise_dtype(dt)
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
     ks = (0 if k is None else k.shape[0], n, d)
     if not (
-            dev >= 0 and dev == torch._C._cuda_getDevice()
+            dev >= 0 and dev == _device()
             and (q_st := q.stride())[2] == 1
             and q_out.dtype is dt and q_out.shape == qs and (qo_st := q_out.stride())[2] == 1
             and q_out.get_device() == dev
@@ -521,16 +516,17 @@ def fastar_qk_norm_rope(q, k, q_out, k_out, wq=None, wk=None, eps=1e-6, axes=(0,
         _refuse([("q", q, dt, qs), ("q_out", q_out, dt, qs), ("k", k, dt, ks), ("k_out", k_out, dt, ks)],
                 [("wq", wq, _F32, (d,)), ("wk", wk, _F32, (d,)), ("pos", pos, _I32, (n, 3)),
                  ("t0_dev", t0_dev, _I32, (1,))])
-    qhs, qts = _strides(q_st, Hq, n, d)
-    qohs, qots = _strides(qo_st, Hq, n, d)
-    khs = kts = kohs = kots = 0
-    if k is not None:
-        khs, kts = _strides(k_st, ks[0], n, d)
-        kohs, kots = _strides(ko_st, ks[0], n, d)
+    Hk = ks[0]
+    if k is None:
+        k_st = ko_st = (0, 0)
     rc = (_lib or load()).fastar_packed_call(_CALL_ROPE, _PACK_ROPE(
-        code, n, d, Hq, q.data_ptr(), qhs, qts, q_out.data_ptr(), qohs, qots, ks[0], _ptr(k), khs, kts, _ptr(k_out),
-        kohs, kots, _ptr(wq), _ptr(wk), eps, axes[0], axes[1], axes[2], _ptr(pos), t0, _ptr(t0_dev), grid[0], grid[1],
-        theta, _stream(stream, dev)), _N_ROPE)
+        code, n, d, Hq, q.data_ptr(), q_st[0] if Hq > 1 else n * d, q_st[1] if n > 1 else d,
+        q_out.data_ptr(), qo_st[0] if Hq > 1 else n * d, qo_st[1] if n > 1 else d,
+        Hk, 0 if k is None else k.data_ptr(), k_st[0] if Hk > 1 else n * d, k_st[1] if n > 1 else d,
+        0 if k is None else k_out.data_ptr(), ko_st[0] if Hk > 1 else n * d, ko_st[1] if n > 1 else d,
+        0 if wq is None else wq.data_ptr(), 0 if wk is None else wk.data_ptr(), eps, axes[0], axes[1], axes[2],
+        0 if pos is None else pos.data_ptr(), t0, 0 if t0_dev is None else t0_dev.data_ptr(), grid[0], grid[1], theta,
+        _current_stream(dev) if stream is None else stream.cuda_stream), _N_ROPE)
     if rc:
         _raise("fastar_qk_norm_rope", rc)
 
@@ -541,11 +537,11 @@ def fastar_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, at=None, len_o
     uint8) from row at[h] on (int32 [H]; None: 0); len_out[h] = at[h] + n."""
     H, n, d = rs = _dims3("k", k)
     dt, dev = k.dtype, k.get_device()
-    code = dtype_code(dt)
+    code = _CODES[dt] if dt in _CODES else _raise_dtype(dt)
     cap = _dims3("k_codes", k_codes)[1]
     cs, ss, hs = (H, cap, d // 2), (H, cap, d // 16), (H,)
     if not (
-            dev >= 0 and dev == torch._C._cuda_getDevice()
+            dev >= 0 and dev == _device()
             and (k_st := k.stride())[2] == 1
             and v.dtype is dt and v.shape == rs and (v_st := v.stride())[2] == 1 and v.get_device() == dev
             and k_codes.dtype is _U8 and k_codes.shape == cs and k_codes.is_contiguous() and k_codes.get_device() == dev
@@ -567,12 +563,14 @@ def fastar_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, at=None, len_o
                 [("k_codes", k_codes, _U8, cs), ("k_scales", k_scales, _U8, ss), ("v_codes", v_codes, _U8, cs),
                  ("v_scales", v_scales, _U8, ss), ("at", at, _I32, hs), ("len_out", len_out, _I32, hs),
                  ("dev_status", dev_status, _I32, (1,)), ("k_exp", k_exp, _I32, hs), ("v_exp", v_exp, _I32, hs)])
-    khs, kts = _strides(k_st, H, n, d)
-    vhs, vts = _strides(v_st, H, n, d)
     rc = (_lib or load()).fastar_packed_call(_CALL_APPEND, _PACK_APPEND(
-        code, H, n, d, k.data_ptr(), khs, kts, v.data_ptr(), vhs, vts, _ptr(k_exp), _ptr(v_exp), _ptr(at),
-        k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), cap, _ptr(len_out),
-        _ptr(dev_status), _stream(stream, dev)), _N_APPEND)
+        code, H, n, d, k.data_ptr(), k_st[0] if H > 1 else n * d, k_st[1] if n > 1 else d,
+        v.data_ptr(), v_st[0] if H > 1 else n * d, v_st[1] if n > 1 else d,
+        0 if k_exp is None else k_exp.data_ptr(), 0 if v_exp is None else v_exp.data_ptr(),
+        0 if at is None else at.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+        v_scales.data_ptr(), cap, 0 if len_out is None else len_out.data_ptr(),
+        0 if dev_status is None else dev_status.data_ptr(),
+        _current_stream(dev) if stream is None else stream.cuda_stream), _N_APPEND)
     if rc:
         _raise("fastar_kv4_append", rc)
 
@@ -581,11 +579,11 @@ def fastar_kv4_read(codes, scales, first, out, exps=None, stream=None):
     """The values of rows first .. first + n of a 4-bit cache -> out [H, n, d]."""
     H, n, d = rs = _dims3("out", out)
     dt, dev = out.dtype, out.get_device()
-    code = dtype_code(dt)
+    code = _CODES[dt] if dt in _CODES else _raise_dtype(dt)
     cap = _dims3("codes", codes)[1]
     cs, ss = (H, cap, d // 2), (H, cap, d // 16)
     if not (
-            dev >= 0 and dev == torch._C._cuda_getDevice()
+            dev >= 0 and dev == _device()
             and (o_st := out.stride())[2] == 1
             and codes.dtype is _U8 and codes.shape == cs and codes.is_contiguous() and codes.get_device() == dev
             and scales.dtype is _U8 and scales.shape == ss and scales.is_contiguous() and scales.get_device() == dev
@@ -593,10 +591,10 @@ def fastar_kv4_read(codes, scales, first, out, exps=None, stream=None):
                  and exps.get_device() == dev)):
         _refuse([("out", out, dt, rs)],
                 [("codes", codes, _U8, cs), ("scales", scales, _U8, ss), ("exps", exps, _I32, (H,))])
-    ohs, ots = _strides(o_st, H, n, d)
     rc = (_lib or load()).fastar_packed_call(_CALL_READ, _PACK_READ(
-        code, H, n, d, codes.data_ptr(), scales.data_ptr(), _ptr(exps), cap, int(first), out.data_ptr(), ohs, ots,
-        _stream(stream, dev)), _N_READ)
+        code, H, n, d, codes.data_ptr(), scales.data_ptr(), 0 if exps is None else exps.data_ptr(), cap, first,
+        out.data_ptr(), o_st[0] if H > 1 else n * d, o_st[1] if n > 1 else d,
+        _current_stream(dev) if stream is None else stream.cuda_stream), _N_READ)
     if rc:
         _raise("fastar_kv4_read", rc)
 
@@ -609,11 +607,11 @@ def fastar_kv4_attn(q, k_codes, k_scales, v_codes, v_scales, lens, scale, out, l
     cap, d, Hkv) bytes (None: the keys are not split)."""
     Hq, nq, d = rs = _dims3("q", q)
     dt, dev = q.dtype, q.get_device()
-    code = dtype_code(dt)
+    code = _CODES[dt] if dt in _CODES else _raise_dtype(dt)
     Hkv, cap, _ = _dims3("k_codes", k_codes)
     cs, ss, hs = (Hkv, cap, d // 2), (Hkv, cap, d // 16), (Hkv,)
     if not (
-            dev >= 0 and dev == torch._C._cuda_getDevice()
+            dev >= 0 and dev == _device()
             and (q_st := q.stride())[2] == 1
             and out.dtype is dt and out.shape == rs and (o_st := out.stride())[2] == 1 and out.get_device() == dev
             and k_codes.dtype is _U8 and k_codes.is_contiguous() and k_codes.shape == cs and k_codes.get_device() == dev
@@ -638,13 +636,14 @@ def fastar_kv4_attn(q, k_codes, k_scales, v_codes, v_scales, lens, scale, out, l
         if workspace is not None:
             dense.append(("workspace", workspace, workspace.dtype, workspace.shape))
         _refuse([("q", q, dt, rs), ("out", out, dt, rs)], dense)
-    qhs, qts = _strides(q_st, Hq, nq, d)
-    ohs, ots = _strides(o_st, Hq, nq, d)
     rc = (_lib or load()).fastar_packed_call(_CALL_ATTN, _PACK_ATTN(
-        q.data_ptr(), code, Hq, Hkv, nq, d, qhs, qts, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-        v_scales.data_ptr(), _ptr(k_exp), _ptr(v_exp), cap, lens.data_ptr(), block, scale, out.data_ptr(), ohs, ots,
-        _ptr(lse), _ptr(dev_status), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream, dev)), _N_ATTN)
+        q.data_ptr(), code, Hq, Hkv, nq, d, q_st[0] if Hq > 1 else nq * d, q_st[1] if nq > 1 else d,
+        k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+        0 if k_exp is None else k_exp.data_ptr(), 0 if v_exp is None else v_exp.data_ptr(), cap, lens.data_ptr(), block,
+        scale, out.data_ptr(), o_st[0] if Hq > 1 else nq * d, o_st[1] if nq > 1 else d,
+        0 if lse is None else lse.data_ptr(), 0 if dev_status is None else dev_status.data_ptr(),
+        0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        _current_stream(dev) if stream is None else stream.cuda_stream), _N_ATTN)
     if rc:
         _raise("fastar_kv4_attn", rc)
 
