@@ -290,15 +290,17 @@ __device__ __forceinline__ void store_empty(const Kv4AttnArgs& a, RowOf w) {
 }
 
 // The work item of this block.  First splits first (a short cache uses no others); in a call in
-// blocks the rows that see most keys first, of all heads; a last item with one row tile, which
-// takes half as long, at the end, where it fills gaps.
+// blocks the rows that see most keys first, of all heads.  A last item with one row tile takes 0.6
+// of a full one's time: it comes at the end, where it fills gaps, or in a call in blocks behind the
+// 0.4 of the row tiles that take longer (first chunk in frames: 92 us of the longest chain of
+// items become 88).
 template <int kCta>
 __device__ __forceinline__ Kv4Item item_of(const Kv4AttnArgs& a, int row_tiles) {
   Kv4Item it;
   it.group = a.group;
   const uint32_t rows = it.rows = a.rows, nq = (uint32_t)a.nq;      // Hq * nq fits 31 bits
   const bool odd = row_tiles > 1 && (rows - 1) % (2 * kRT * kCta) < kRT * kCta;
-  const int full_tiles = row_tiles - odd;
+  const int full_tiles = a.block > 0 ? row_tiles : row_tiles - odd;     // in blocks: the odd one among them
   uint32_t u = blockIdx.x / kCta;
   const uint32_t all = (uint32_t)(a.Hkv * full_tiles);
   const bool last = u >= all * (uint32_t)a.splits;
@@ -311,7 +313,8 @@ __device__ __forceinline__ Kv4Item item_of(const Kv4AttnArgs& a, int row_tiles) 
   } else if (a.block > 0) {
     const uint32_t x = u / (uint32_t)a.Hkv;
     it.h = (int)(u - x * (uint32_t)a.Hkv);
-    rt = (uint32_t)full_tiles - 1 - x;
+    const uint32_t full = (uint32_t)(row_tiles - odd), at = odd ? (2 * full + 4) / 5 : full;
+    rt = x < at ? full - 1 - x : x == at ? full : full - x;
   } else {
     it.h = (int)(u / (uint32_t)full_tiles);
     rt = (uint32_t)full_tiles - 1 - (u - (uint32_t)it.h * (uint32_t)full_tiles);
