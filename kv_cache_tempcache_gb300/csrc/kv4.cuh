@@ -72,10 +72,7 @@ __device__ __forceinline__ int64_t visible(int64_t len, int64_t nq, int64_t t, i
   return v < 0 ? 0 : v;
 }
 
-// Query rows of an item of the tcgen05 kernel: two tiles of 128 in each of d / 64 CTAs.
-__host__ __device__ constexpr uint32_t item_rows(int d) { return 4u * (uint32_t)d; }
-
-// What the rows [r0, r0 + item_rows) of a KV head with `len` cached rows work on: the last key
+// What the rows r0 .. rlast of a KV head with `len` cached rows work on: the last key
 // that any of them sees (rows of two query heads include a last token, which sees all), and the
 // splits of the keys in use.  The launch's splits were chosen for a full cache; a shorter one
 // takes fewer, none under min_tiles tiles of 128 keys.
