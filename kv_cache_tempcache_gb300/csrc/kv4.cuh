@@ -52,13 +52,15 @@ __device__ __forceinline__ int head_exp(const int32_t* e, int h) {
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
 // A head's length, held to [0, cap].
-__device__ __forceinline__ int64_t head_len(const int32_t* len, int h, int64_t cap, int32_t* status) {
-  const int64_t n = len[h];
+__device__ __forceinline__ int64_t held_len(int64_t n, int64_t cap, int32_t* status) {
   if (n < 0 || n > cap) {
     flag_status(status, FASTAR_DEV_BAD_LEN);
     return n < 0 ? 0 : cap;
   }
   return n;
+}
+__device__ __forceinline__ int64_t head_len(const int32_t* len, int h, int64_t cap, int32_t* status) {
+  return held_len(len[h], cap, status);
 }
 
 // How many of a head's `len` rows token t of a call's nq sees: all of them, or with blocks

@@ -298,10 +298,10 @@ __device__ __forceinline__ void store_empty(const Kv4AttnArgs& a, RowOf w) {
 // 0.4 of the row tiles that take longer (first chunk in frames: 92 us of the longest chain of
 // items become 88).
 template <int kCta>
-__device__ __forceinline__ Kv4Item item_of(const Kv4AttnArgs& a, int row_tiles) {
+__device__ __forceinline__ Kv4Item item_place(const Kv4AttnArgs& a, int row_tiles) {
   Kv4Item it;
   it.group = a.group;
-  const uint32_t rows = it.rows = a.rows, nq = (uint32_t)a.nq;      // Hq * nq fits 31 bits
+  const uint32_t rows = it.rows = a.rows;
   const bool odd = row_tiles > 1 && (rows - 1) % (2 * kRT * kCta) < kRT * kCta;
   const int full_tiles = a.block > 0 ? row_tiles : row_tiles - odd;     // in blocks: the odd one among them
   uint32_t u = blockIdx.x / kCta;
@@ -322,18 +322,23 @@ __device__ __forceinline__ Kv4Item item_of(const Kv4AttnArgs& a, int row_tiles) 
     it.h = (int)(u / (uint32_t)full_tiles);
     rt = (uint32_t)full_tiles - 1 - (u - (uint32_t)it.h * (uint32_t)full_tiles);
   }
-  it.len = kv4::head_len(a.len, it.h, a.cap, a.status);
   it.r0 = rt * (2 * kRT * kCta);
-  const uint32_t rlast = (it.r0 + 2 * kRT * kCta < rows ? it.r0 + 2 * kRT * kCta : rows) - 1;
-  it.nt = rlast - it.r0 >= kRT * kCta ? 2 : 1;
-  const kv4::ItemKeys keys = kv4::item_keys(it.len, nq, a.block, it.r0, rlast, a.splits, a.min_tiles);
+  it.nt = rows - it.r0 > kRT * kCta ? 2 : 1;
+  return it;
+}
+// The keys it works on, from the head's length.
+template <int kCta>
+__device__ __forceinline__ void item_keys_of(const Kv4AttnArgs& a, Kv4Item& it, int64_t len) {
+  it.len = len;
+  const uint32_t rlast = (it.r0 + 2 * kRT * kCta < it.rows ? it.r0 + 2 * kRT * kCta : it.rows) - 1;
+  const kv4::ItemKeys keys =
+      kv4::item_keys(len, (uint32_t)a.nq, a.block, it.r0, rlast, a.splits, a.min_tiles);
   it.most = keys.most;
   it.partial = keys.splits > 1;
   it.j0 = it.partial ? keys.tiles * it.split / keys.splits : 0u;     // tiles times splits fits 32 bits
   it.T = it.split >= keys.splits ? -1
          : it.partial            ? (int)(keys.tiles * (it.split + 1) / keys.splits - it.j0)
                                  : (int)keys.tiles;
-  return it;
 }
 
 template <int D, int C>
@@ -348,14 +353,18 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
 
   // Before the loop a CTA has only latencies to wait for, and instructions to fetch that run once:
   // one thread finds the item (its divisions in all 28 warps took 5000 clocks), another sets the
-  // barriers up, and rolled loops move the query rows.
-  if (threadIdx.x == (kMmaWarp + 1) * 32) {
+  // barriers up, and rolled loops move the query rows, which come while the length is on its way.
+  const bool finder = threadIdx.x == (kMmaWarp + 1) * 32;
+  int cached = 0;                        // the head's length, on its way across the first barrier
+  if (finder) {
     for (int i = 0; i < Lay::ins; ++i) {
       tc::mbar_init(&sm.in_full[i], 1);
       tc::mbar_init(&sm.in_empty[i], 4);
     }
     tc::mbar_fence_init();
-    sm.item = item_of<kCta>(a, row_tiles);
+    const Kv4Item place = item_place<kCta>(a, row_tiles);
+    cached = a.len[place.h];
+    sm.item = place;
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -375,6 +384,31 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     tc::mbar_fence_init();
   }
   __syncthreads();
+  // Query rows: warp x of a row tile brings its rows 16 x .. on, four lanes a row, to where the product
+  // wants them, then turns them to fp16 in place.  Odd rows take the halves of a block's 16-byte
+  // chunks the other way round, so that 8 lanes hit 8 bank groups.
+  constexpr int QC = D / 32;                              // a lane's chunks of a row
+  const int qw = warp >> 3;                               // row tile
+  const bool mine = warp < kSoftWarps && !(sm.item.nt == 1 && qw == 1);
+  const int qr = (warp & 7) * 16 + (lane >> 2), qc = (lane & 3) ^ ((lane >> 2 & 1) << 2);
+  uint8_t* qd = base + Lay::q + (size_t)qw * Lay::q_tile;
+  auto chunk = [&](int i, int j) {                        // chunk j of the lane's row i
+    return qd + (j >> 1) * Lay::q_blk + tc::sw128_off(qr + i * 8, qc ^ ((j & 1) << 2));
+  };
+  if (mine) {
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t x = sm.item.r0 + (uint32_t)(qw * (kRT * kCta) + rank * kRT + qr + i * 8);
+      const RowOf from = row_of(a, sm.item, x < a.rows ? x : sm.item.r0);
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.p) + from.head * a.q.hs + from.t * a.q.ts;
+#pragma unroll
+      for (int j = 0; j < QC; ++j)
+        tc::cp_async16(tc::smem_u32(chunk(i, j)), src + (j >> 1) * 64 + (qc ^ ((j & 1) << 2)) * 8, x < a.rows ? 16 : 0);
+    }
+    tc::cp_async_commit();
+  }
+  if (finder) item_keys_of<kCta>(a, sm.item, kv4::held_len(cached, a.cap, a.status));   // fields that no one reads yet
+  __syncthreads();
   const Kv4Item& it = sm.item;
   const uint32_t rows = it.rows, r0 = it.r0, split = it.split;
   const int h = it.h, T = it.T;
@@ -388,7 +422,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
         a.part_ml[((int64_t)split * a.Hq + w.head) * a.nq + w.t] = make_float2(split == 0 ? -neg_inf() : neg_inf(), 0.f);
       if (T == 0) store_empty<D>(a, w);                  // no keys at all
     }
-    if (T <= 0) return;                                  // both CTAs of a pair
+    if (T <= 0) {                                        // both CTAs of a pair
+      tc::cp_async_wait<0>();
+      return;
+    }
   }
   if (kCta == 2) pair_arrive();                          // this CTA's barriers are ready
   volatile int* abort = &sm.abort;
@@ -402,27 +439,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
     const uint32_t r = r0 + (both ? 0u : (uint32_t)(w * (kRT * kCta))) + (uint32_t)(rank * kRT + row);
     const bool has = r < rows;
     constexpr int HD = D / 2;                             // channels of a row of O a thread takes
-    // Query rows: warp x of a row tile brings its rows 16 x .. on, four lanes a row, to where the product
-    // wants them, then turns them to fp16 in place.  Odd rows take the halves of a block's 16-byte
-    // chunks the other way round, so that 8 lanes hit 8 bank groups.
-    constexpr int QC = D / 32;                            // a lane's chunks of a row
-    const bool mine = !(both && w == 1);
-    const int qr = (warp & 7) * 16 + (lane >> 2), qc = (lane & 3) ^ ((lane >> 2 & 1) << 2);
-    uint8_t* qd = base + Lay::q + (size_t)w * Lay::q_tile;
-    auto chunk = [&](int i, int j) {                      // chunk j of the lane's row i
-      return qd + (j >> 1) * Lay::q_blk + tc::sw128_off(qr + i * 8, qc ^ ((j & 1) << 2));
-    };
     if (mine) {
-#pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t x = r0 + (uint32_t)(w * (kRT * kCta) + rank * kRT + qr + i * 8);
-        const RowOf from = row_of(a, it, x < rows ? x : r0);
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.p) + from.head * a.q.hs + from.t * a.q.ts;
-#pragma unroll
-        for (int j = 0; j < QC; ++j)
-          tc::cp_async16(tc::smem_u32(chunk(i, j)), src + (j >> 1) * 64 + (qc ^ ((j & 1) << 2)) * 8, x < rows ? 16 : 0);
-      }
-      tc::cp_async_commit();
       tc::cp_async_wait<0>();
 #pragma unroll 1
       for (int i = 0; i < 2; ++i) {
