@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_f
   float2* wml = reinterpret_cast<float2*>(bars + W * ST);            // [warp][8 NR]
   int* abort_flag = reinterpret_cast<int*>(wml + W * 8 * NR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  pdl_wait();                               // the launch overlaps the end of the kernel before
   const uint32_t rows = a.rows, groups = (rows + 8 * NR - 1) / (8 * NR);
   const int split = (int)blockIdx.y;
   const int h = (int)(groups == 1 ? blockIdx.x : blockIdx.x / groups);
@@ -461,11 +462,12 @@ cudaError_t few_go(const Kv4AttnArgs& a, cudaStream_t s) {
   using Lay = FewLayout<T, D, NR>;
   const int64_t blocks = ((int64_t)a.rows + 8 * NR - 1) / (8 * NR) * a.Hkv;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = opt_in_smem((const void*)kv4_attn_few_kernel<T, D, NR>, Lay::bytes);
+  cudaError_t e = opt_in_smem((const void*)kv4_attn_few_kernel<T, D, NR>, Lay::bytes);
   if (e != cudaSuccess) return e;
-  kv4_attn_few_kernel<T, D, NR><<<dim3((unsigned)blocks, (unsigned)a.splits), Lay::warps * 32, Lay::bytes, s>>>(a);
+  e = launch_dependent(kv4_attn_few_kernel<T, D, NR>, dim3((unsigned)blocks, (unsigned)a.splits), dim3(Lay::warps * 32),
+                       Lay::bytes, s, a);
   count_launches(1);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace

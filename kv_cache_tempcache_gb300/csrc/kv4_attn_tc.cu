@@ -350,6 +350,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
   Kv4Ctl& sm = *reinterpret_cast<Kv4Ctl*>(base + Lay::ctl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kCta == 2 ? (int)cta_rank() : 0;
+  pdl_wait();                            // the launch overlaps the end of the kernel before
 
   // Before the loop a CTA has only latencies to wait for, and instructions to fetch that run once:
   // one thread finds the item (its divisions in all 28 warps took 5000 clocks), another sets the
@@ -877,12 +878,14 @@ cudaError_t tc_go(const Kv4AttnArgs& a, cudaStream_t s) {
   cfg.blockDim = dim3(kThreadsT);
   cfg.dynamicSmemBytes = Lay::bytes;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = Lay::kCta;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kv4_attn_tc_kernel<D, C>, a, (int)rt);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();

@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kWarpsR * 32)
     qk_norm_rope_kernel(const RopeDev a, const __grid_constant__ RopeTable tab) {
   // steps and weights in shared memory: read by lane from the kernel's parameters (a lane each
   // another address, one after the other) they took 3 of 15 us
+  pdl_wait();                      // the launch overlaps the end of the kernel before
   __shared__ __align__(16) uint64_t steps[64];
   __shared__ uint8_t axes[64];
   __shared__ __align__(16) float ws[2][D];
@@ -239,16 +240,12 @@ cudaError_t rope_go(RopeDev a, const RopeTable& tab, bool all, cudaStream_t s) {
   const int64_t most = one ? 0x7fffffff : 4 * sms;
   const unsigned grid = (unsigned)(blocks < most ? blocks : most);
   constexpr int kAhead = sizeof(T) == 2 ? 3 : 2;
-  if (one && all)
-    qk_norm_rope_kernel<T, D, true, 1><<<grid, kWarpsR * 32, 0, s>>>(a, tab);
-  else if (one)
-    qk_norm_rope_kernel<T, D, false, 1><<<grid, kWarpsR * 32, 0, s>>>(a, tab);
-  else if (all)
-    qk_norm_rope_kernel<T, D, true, kAhead><<<grid, kWarpsR * 32, 0, s>>>(a, tab);
-  else
-    qk_norm_rope_kernel<T, D, false, kAhead><<<grid, kWarpsR * 32, 0, s>>>(a, tab);
+  const auto kernel = one ? all ? qk_norm_rope_kernel<T, D, true, 1> : qk_norm_rope_kernel<T, D, false, 1>
+                      : all ? qk_norm_rope_kernel<T, D, true, kAhead>
+                            : qk_norm_rope_kernel<T, D, false, kAhead>;
+  const cudaError_t e = launch_dependent(kernel, dim3(grid), dim3(kWarpsR * 32), 0, s, a, tab);
   count_launches(1);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
