@@ -506,3 +506,47 @@ def test_norm_append_attend_as_a_block_runs_them():
         assert np.array_equal(c[0][:, at:at + n].cpu().numpy(), wc) and np.array_equal(c[1][:, at:at + n].cpu().numpy(), wsc)
         vals = [K.values(c[2 * i].cpu().numpy(), c[2 * i + 1].cpu().numpy()) for i in range(2)]
         _check_attn(out, lse, q, vals[0], vals[1], lens.tolist(), 1 / math.sqrt(d), 65)
+
+
+@pytest.mark.parametrize("dtype,G,nq,d", [("bf16", 4, 1, 128), ("bf16", 1, 40, 128), ("bf16", 2, 300, 64), ("f32", 1, 3, 64)])
+def test_a_run_of_calls_equals_one_with_a_wait_after_each(dtype, G, nq, d):
+    # launches overlap the kernel before them: every call reads what the last one wrote, into buffers
+    # and a workspace that the next one uses again
+    Hkv, cap, steps = 4, 12000, 40
+    dt = DT[dtype]
+    nb = L.workspace_bytes(L.OP_KV4_ATTN, Hkv * G, nq, cap, d, Hkv)
+    results = []
+    for wait in (True, False):
+        c = _empty_cache(Hkv, cap, d)
+        start = _rand((2, Hkv, 5000, d), 50).to(dt)
+        lens, lens2 = _i32([0] * Hkv), _i32([0] * Hkv)
+        L.fastar_kv4_append(start[0], start[1], *c, lens, lens2)
+        q = _rand((Hkv * G, nq, d), 51).to(dt)
+        k, v = _rand((Hkv, nq, d), 52).to(dt), _rand((Hkv, nq, d), 53).to(dt)
+        out, lse = torch.empty_like(q), torch.empty(Hkv * G, nq, device=DEV)
+        ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=DEV)
+        w = torch.ones(d, device=DEV)
+        torch.cuda.synchronize()
+        for i in range(steps):
+            a, b = (lens2, lens) if i % 2 == 0 else (lens, lens2)
+            L.fastar_qk_norm_rope(q, k, q, k, wq=w, wk=w, axes=(d // 2, d // 4, d // 4), t0=i, grid=(5, 7))
+            if wait:
+                torch.cuda.synchronize()
+            L.fastar_kv4_append(k, v, *c, a, b)
+            if wait:
+                torch.cuda.synchronize()
+            L.fastar_kv4_attn(q, *c, b, 0.3, out, lse, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+            L.fastar_kv4_read(c[2], c[3], 4990 + i, v)            # the next rows of V: what the cache holds
+            if wait:
+                torch.cuda.synchronize()
+            L.fastar_qk_norm_rope(out, None, q, None, wq=w)       # the next queries: this attention's outputs
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        results.append([x.clone() for x in (*c, q, k, v, out, lse, a, b)])
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
+    assert torch.isfinite(results[0][7].float()).all()
+    assert results[0][-1].tolist() == [min(cap, 5000 + steps * nq)] * Hkv
