@@ -621,7 +621,8 @@ int fastar_kv4_read(int dtype, int H, int64_t n, int d, const uint8_t* codes, co
  * device (outside [0, cap]: held to it, FASTAR_DEV_BAD_LEN); rows from len on are never used.
  * Scale bytes are taken as fastar_kv4_append writes them (finite, not negative).  A row of q with
  * a NaN or an infinity gives NaN (zeros if none of its logits is above -infinity), and no other
- * row is touched.
+ * row is touched.  Every weight is held to 2^-11 of itself (bf16) or 2^-22 (dtype F32) down to about
+ * 2^-24 and 2^-17 of the row's largest, and below that to 2^-35 and 2^-39 of the largest.
  * lse float [Hq, nq] optional.  Hq * nq <= INT32_MAX (FASTAR_ECAPACITY).
  * workspace (optional): fastar_workspace_bytes(FASTAR_OP_KV4_ATTN, Hq, nq, cap, d, Hkv, ...)
  * bytes for the partial results of key splits; NULL: the keys are not split (slower with few

@@ -22,7 +22,7 @@
 // its parts times 2^14, so that they keep 22 bits down to 2^-17 of the largest and 2^-39 of it
 // below.
 // Queries, P and references otherwise as in the tcgen05 kernel (kv4_attn_tc.cu): fp16 rows at a power of
-// two, P in fp16 against a reference that moves only when a P would pass 2^15.
+// two, P in fp16 against a reference that moves only when a P would pass what fp16 holds.
 #include <climits>
 
 #include "common.cuh"
@@ -154,7 +154,8 @@ template <typename T, int D, int NR>
 __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_few_kernel(const Kv4AttnArgs a) {
   using Lay = FewLayout<T, D, NR>;
   constexpr int QP = Lay::f32 ? 3 : 1, PP = Lay::f32 ? 2 : 1;        // fp16 parts of Q and of P
-  constexpr float kUp = Lay::f32 ? 0x1p14f : 1.f, kRoom = Lay::f32 ? 1.f : 15.f;   // P kUp 2^kRoom is at most 2^15
+  constexpr float kUp = Lay::f32 ? 0x1p14f : 1.f, kRoom = Lay::f32 ? 1.f : kv4::kTop;   // P is at most 2^kRoom
+  constexpr float kLift = Lay::f32 ? 0.f : kv4::kLift, kUnlift = Lay::f32 ? 1.f : kv4::kUnlift;
   constexpr int W = Lay::warps, ST = Lay::stages, MT = D / 16;       // MT: row tiles of O^T
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~(uintptr_t)127);
@@ -289,27 +290,27 @@ __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_f
           for (int x = 0; x < 4; ++x)
             if (key + kt * 16 + (x >> 1) * 8 + g >= see[n][x & 1]) s[n][kt][x] = neg_inf();
     }
-    float mt[NR][2];
+    float top[NR][2];                       // the largest logits, not scaled yet
     bool grow = i == 0;
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        mt[n][p] = fmaxf(fmaxf(s[n][0][p], s[n][0][2 + p]), fmaxf(s[n][1][p], s[n][1][2 + p])) * sl2[n][p];
-        grow |= mt[n][p] > m[n][p] + kRoom;
+        top[n][p] = fmaxf(fmaxf(s[n][0][p], s[n][0][2 + p]), fmaxf(s[n][1][p], s[n][1][2 + p]));
+        grow |= fmaf(top[n][p], sl2[n][p], -m[n][p]) > kRoom;
       }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const float mx = group_max(mt[n][p]);
+          const float mx = group_max(top[n][p]) * sl2[n][p], to = mx - kLift;
           float f = 1.f;
           if (i == 0) {
-            m[n][p] = mx == neg_inf() ? 0.f : mx;
-          } else if (mx > m[n][p]) {
-            f = ex2w(m[n][p] - mx);
-            m[n][p] = mx;
+            m[n][p] = mx == neg_inf() ? 0.f : to;
+          } else if (to > m[n][p]) {
+            f = ex2w(m[n][p] - to);
+            m[n][p] = to;
           }
           l[n][p] *= f;
 #pragma unroll
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_f
           dst[x >> 1] = make_float4(o[n][x][p] * f, o[n][x][2 + p] * f, o[n][x + 1][p] * f, o[n][x + 1][2 + p] * f);
     }
   __syncthreads();
-  const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h)) / kUp;
+  const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h)) / kUp * kUnlift;
   for (int x = threadIdx.x; x < (int)(rlast - r0 + 1) * (D / 4); x += W * 32) {
     const int r = x / (D / 4), c = x % (D / 4) * 4;
     const float mx = top(r);
@@ -435,9 +436,10 @@ __global__ void __launch_bounds__(FewLayout<T, D, NR>::warps * 32, 1) kv4_attn_f
       acc.x += z.x, acc.y += z.y, acc.z += z.z, acc.w += z.w;
     }
     const bool live = sum > 0.f || sum != sum;
+    sum *= kUnlift;
     const uint32_t nq = (uint32_t)a.nq, gh = (r0 + (uint32_t)r) / nq;
     const int64_t head = h * (int64_t)a.group + gh, tok = r0 + (uint32_t)r - gh * nq;
-    const float mn = mx * 0.6931471805599453f;
+    const float mn = (mx + kLift) * 0.6931471805599453f;
     if (a.splits > 1) {
       const int64_t at = (split * (int64_t)a.Hq + head) * a.nq + tok;
       *reinterpret_cast<float4*>(a.part_o + at * D + c) = make_float4(acc.x * up, acc.y * up, acc.z * up, acc.w * up);

@@ -7,7 +7,7 @@
 //   warps 0-15         softmax: two threads a row, 64 of a tile's 128 keys each (warps 0-3 and 4-7 of
 //                      row tile 0, 8-11 and 12-15 of row tile 1): logits from TMEM, exponentials
 //                      against a reference that is moved, and the sums rescaled, only when a P
-//                      would pass 2^15, P as fp16 over the consumed logits in TMEM, the output;
+//                      would pass what fp16 holds, P as fp16 over the consumed logits in TMEM, the output;
 //   warps 16-19, 20-23 unpack K, V: packed tiles (four on their way, brought by bulk copies that
 //                      warp 25 issues) into rings of 128-byte-swizzled fp16 tiles;
 //   warp 24            owns TMEM and issues tcgen05.mma from one thread (of the pair's first CTA):
@@ -33,7 +33,8 @@
 // by a power of two that puts its largest element in [2^12, 2^13) and rounded to fp16: bf16's 8
 // bits fit fp16's 11, so only elements 2^-26 of the row's largest and below are not exact (and
 // off by at most 2^-37 of it); the power returns in the row's logit scale.  P in fp16 has an
-// error of 2^-11, an eighth of bf16's.  Logits, maxima, sums and outputs are fp32.
+// error of 2^-11, an eighth of bf16's, down to 2^-24 of the row's largest, and 2^-35 of that
+// below (kv4.cuh: the reference's lift).  Logits, maxima, sums and outputs are fp32.
 //
 // Keys past a row's last visible one get P = 0; rows past the CTA's last key are stored as
 // zeros in shared memory, so what lies behind the cache's length cannot reach a sum as 0 * NaN.
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
       tc::tc_fence_after();
       const bool cut = __any_sync(0xffffffffu, left < 64);
       const int valid = min(left, 64);          // keys that the row sees
-      float mt;
+      float top;                                // the largest of them, not scaled yet
       {
         float x[64];
         tc::tmem_ld32(s_addr, x);
@@ -512,12 +513,13 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
 #pragma unroll
           for (int c = 0; c < 64; ++c) x[c] = c < valid ? x[c] : neg_inf();
         }
-        // the scale is positive: the largest scaled logit is the largest logit, scaled
-        mt = row_max<64>(x) * sl2;
+        top = row_max<64>(x);
       }
-      // Both warps of the rows move the reference together: when a P would pass 2^15, half of
-      // what fp16 holds, and at the first tile.
-      if (__builtin_expect(tc::named_bar_or(pair_bar, 64, mt > m + 15.f || i == 0 || !alive), 0)) {
+      // Both warps of the rows move the reference together: when a P would pass what fp16 holds (the scale
+      // is positive, so the largest logit has the largest P; its exponent is formed as row_exp32
+      // forms it), and at the first tile.
+      if (__builtin_expect(tc::named_bar_or(pair_bar, 64, fmaf(top, sl2, -m) > kv4::kTop || i == 0 || !alive), 0)) {
+        float mt = top * sl2;
         sm.ex[half][w][row] = mt;
         // the warps leave together as well
         if (tc::named_bar_or(pair_bar, 64, !alive)) {
@@ -527,10 +529,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
         mt = fmaxf(mt, sm.ex[half ^ 1][w][row]);
         float f = 1.f;
         if (i == 0) {
-          m = mt == neg_inf() ? 0.f : mt;
-        } else if (mt > m) {
-          f = ex2f(m - mt);
-          m = mt;
+          m = mt == neg_inf() ? 0.f : mt - kv4::kLift;
+        } else if (const float to = mt - kv4::kLift; to > m) {
+          f = ex2f(m - to);
+          m = to;
           l0 *= f;
           l1 *= f;
         }
@@ -612,7 +614,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
         }
       }
       const bool live = l > 0.f || l != l;
-      const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h));
+      l *= kv4::kUnlift;
+      const float up = kv4::pow2i(kv4::head_exp(a.v_exp, h)) * kv4::kUnlift;
       const float f = partial ? up : live ? up / l : 0.f;
       // Rows of 128 bytes (32 fp32 or 64 bf16 channels; 64 bytes of 32 bf16) go through shared
       // memory (the ring of K, or of V, has been used), so that they leave as whole runs; written
@@ -673,7 +676,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv4_attn_tc_kernel(const Kv4Attn
         __syncwarp();
       }
       if (has && half == 0) {
-        const float mn = m * 0.6931471805599453f;
+        const float mn = (m + kv4::kLift) * 0.6931471805599453f;
         if (partial)
           a.part_ml[((int64_t)split * a.Hq + at.head) * a.nq + at.t] = make_float2(live ? mn : neg_inf(), l);
         else if (a.lse)
