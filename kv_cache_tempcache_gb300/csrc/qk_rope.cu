@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(kWarpsR * 32)
           for (int o = LPR / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
           // 1 / sqrt to an ulp: the approximate one and a Newton step
           const float z = q * (1.0f / D) + a.eps, y0 = rsqrtf(z);
-          // (of an infinite sum of squares 0, not 0 * infinity)
-          r = y0 > 0.f ? y0 * fmaf(-0.5f * z * y0, y0, 1.5f) : 0.f;
+          // (of an infinite sum of squares 0, not 0 * infinity; of a NaN, NaN in the whole row)
+          r = y0 == 0.f ? 0.f : y0 * fmaf(-0.5f * z * y0, y0, 1.5f);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {

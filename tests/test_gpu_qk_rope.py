@@ -147,3 +147,23 @@ def test_rows_whose_squares_overflow_fp32():
     assert (out[0] == 0).all() and (out[1, 0] == 0).all()
     assert torch.isnan(out[1, 1, 7]) and int(torch.isnan(out).sum()) == 1 and (out[1, 1].nan_to_num() == 0).all()
     assert (out[2] - 1).abs().max() <= 2.0 ** -19 + 5e-7      # 1 / sqrt(1 + 1e-6), as the bound above
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,Hq,Hk,d", [(3, 2, 1, 64), (3, 5, 3, 128), (2000, 12, 4, 128), (4000, 10, 5, 64)])
+def test_a_nan_makes_its_normed_row_nan_and_no_other(dtype, n, Hq, Hk, d):
+    # the mean of the row's squares is NaN, and so is every channel, turned or not
+    _, q, k, wq, wk = _make(n, Hq, Hk, d, DT[dtype], 11)
+    axes = (d // 4, d // 4, d // 4)
+    ref = [torch.empty_like(q), torch.empty_like(k)]
+    L.fastar_qk_norm_rope(q, k, *ref, wq=wq, wk=wk, axes=axes, grid=(5, 7))
+    q, k = q.clone(), k.clone()
+    rows = [(q, (1, n // 2)), (q, (0, 0)), (k, (Hk - 1, n - 1))]
+    for i, (t, at) in enumerate(rows):
+        t[at][(7 * i + 3, d - 1, 0)[i]] = float("nan")       # channels that turn, and one past the axes
+    out = [torch.empty_like(q), torch.empty_like(k)]
+    L.fastar_qk_norm_rope(q, k, *out, wq=wq, wk=wk, axes=axes, grid=(5, 7))
+    torch.cuda.synchronize()
+    for x, y, r in zip((q, k), out, ref):
+        bad = torch.isnan(x).any(-1)
+        assert torch.isnan(y[bad]).all() and torch.equal(y[~bad], r[~bad])
