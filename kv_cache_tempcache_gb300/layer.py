@@ -477,9 +477,10 @@ class DenseLayer:
 class KV4Layer:
     """DenseLayer with its append-only cache in 4 bits (a float4 e2m1 a value, a float8 scale to
     16 channels): 3.6 times smaller than in bf16.  Lengths live on the device, so one captured
-    step serves every length.  cap: rows a head, rounded up to a multiple of 16; Hkv: heads of the
-    cache (default H; H must be a multiple of it); block: tokens of a frame that sees itself and
-    the frames before it in the chunk, not those after it (0: the chunk sees all of itself)."""
+    step serves every length (with advance=True each replay keeps its chunk).  cap: rows a head,
+    rounded up to a multiple of 16; Hkv: heads of the cache (default H; H must be a multiple of
+    it); block: tokens of a frame that sees itself and the frames before it in the chunk, not
+    those after it (0: the chunk sees all of itself)."""
 
     def __init__(self, H, d, Nq, cap, P, dtype=torch.bfloat16, device="cuda", scale=None, Hkv=None, block=0):
         L.load()
@@ -494,7 +495,8 @@ class KV4Layer:
         self.len_cur = torch.zeros(Hkv, dtype=torch.int32, device=dev)    # with the current chunk
         self.kp = torch.zeros((H, P, d), dtype=dtype, device=dev)
         self.vp = torch.zeros((H, P, d), dtype=dtype, device=dev)
-        self.n = 0
+        self._n = 0                      # committed rows, while the host knows them: see n
+        self._replayed = False
         self.o_self = torch.zeros((H, Nq, d), dtype=dtype, device=dev)
         self.o_cross = torch.zeros((H, Nq, d), dtype=dtype, device=dev)
         self.lse_self = _f32(H, Nq, dev=dev)
@@ -503,17 +505,34 @@ class KV4Layer:
         nb = L.workspace_bytes(L.OP_KV4_ATTN, H, Nq, self.cap, d, Hkv)
         self.ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
 
+    @property
+    def n(self) -> int:
+        """The committed rows.  Once a commit has been captured only the device knows how often it
+        was replayed: from then on this waits for the current stream and reads the lengths."""
+        return int(self.len.max()) if self._replayed else self._n
+
+    @n.setter
+    def n(self, rows):
+        self.len.fill_(rows)
+        self._n = int(rows)
+
+    def _keep(self, n):
+        self.len.copy_(self.len_cur)
+        if torch.cuda.is_current_stream_capturing():
+            self._replayed = True        # the copy has not run, and may run any number of times
+        elif not self._replayed:
+            self._n = n
+
     def load_history(self, k, v):
         """k, v [Hkv, n, d]: the cache holds these rows and no others."""
-        n = k.shape[1]
         L.fastar_kv4_append(k, v, self.k_codes, self.k_scales, self.v_codes, self.v_scales, None, self.len_cur,
                             self.dev_status)
-        self.len.copy_(self.len_cur)
-        self.n = n
+        self._keep(k.shape[1])
 
     def history(self, dtype=torch.bfloat16):
         """The committed rows as the values they stand for: k, v [Hkv, n, d]."""
-        k = torch.empty((self.Hkv, self.n, self.d), dtype=dtype, device=self.len.device)
+        n = self.n
+        k = torch.empty((self.Hkv, n, self.d), dtype=dtype, device=self.len.device)
         v = torch.empty_like(k)
         L.fastar_kv4_read(self.k_codes, self.k_scales, 0, k)
         L.fastar_kv4_read(self.v_codes, self.v_scales, 0, v)
@@ -525,8 +544,7 @@ class KV4Layer:
 
     def commit(self, n):
         """Keeps the n rows that the last step_self appended (of a full cache those that it took)."""
-        self.len.copy_(self.len_cur)
-        self.n = min(self.n + n, self.cap)
+        self._keep(min(self._n + n, self.cap))
 
     def step_self(self, q, k_cur, v_cur, out=None, advance: bool = True):
         """Appends the chunk behind the committed rows (kept with advance=True, else overwritten

@@ -138,3 +138,45 @@ def test_a_chunk_past_the_capacity_is_refused(use_graph):
         dit.step(1.0, 0.5, commit=False)
     torch.cuda.synchronize()
     assert dit.status_word() == 0 and dit.attn[0].n == SMALL.tokens
+
+
+def test_a_captured_step_of_the_layer_keeps_its_chunks():
+    H, d, nq, chunks = 2, 64, 20, 4
+    x = T._rand((3, chunks, H, nq, d), 45).bfloat16()
+    layers = [KV4Layer(H, d, nq, 96, 8) for _ in range(2)]
+    bufs = [torch.empty_like(x[0, 0]) for _ in range(3)]
+    outs = [[], []]
+    for layer in layers:
+        layer.load_history(x[1, 0, :, :10], x[2, 0, :, :10])
+    eager, layer = layers
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for b in bufs:
+            b.zero_()
+        layer.step(*bufs, advance=False)                       # warm-up outside the capture
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        layer.step(*bufs)
+    torch.cuda.synchronize()
+    assert layer.n == 10 and layer.history()[0].shape == (H, 10, d)      # nothing has run yet
+    for i in range(chunks):
+        outs[0].append(eager.step_self(*x[:, i]).clone())
+        for b, t in zip(bufs, x[:, i]):
+            b.copy_(t)
+        g.replay()
+        outs[1].append(layer.o_self.clone())
+        assert layer.n == eager.n == 10 + (i + 1) * nq and layer.len.tolist() == [layer.n] * H
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    for a, b in zip(eager.history(), layer.history()):
+        assert a.shape == (H, 90, d) and torch.equal(a, b)
+    layer.load_history(x[1, 1, :, :7], x[2, 1, :, :7])                   # and an eager call after replays
+    assert layer.n == 7
+    layer.step_self(*x[:, 2])
+    torch.cuda.synchronize()
+    assert layer.n == 27 and layer.len.tolist() == [27, 27] and layer.status() == 0
+    for a in layers:                                                     # rows can be given up
+        a.n = 7
+        assert a.n == 7 and a.len.tolist() == [7, 7] and a.history()[0].shape == (H, 7, d)
