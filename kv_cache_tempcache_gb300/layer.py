@@ -549,15 +549,35 @@ class KV4Layer:
     def step_self(self, q, k_cur, v_cur, out=None, advance: bool = True):
         """Appends the chunk behind the committed rows (kept with advance=True, else overwritten
         by the next step) and attends over every key so far -> out ([H, Nq, d] view; default
-        o_self)."""
+        o_self).  Rows past the capacity are dropped and set DEV_BAD_LEN in status(); each token then
+        attends over the rows it may see of those that the cache took.  (A replayed step in blocks
+        cannot know that rows are missing and counts blocks from the capacity's end: its
+        outputs are not to be used once status() says so.)"""
         o = self.o_self if out is None else out
         L.fastar_kv4_append(k_cur, v_cur, self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.len,
                             self.len_cur, self.dev_status)
-        L.fastar_kv4_attn(q, self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.len_cur, self.scale, o,
-                          self.lse_self, block=self.block, dev_status=self.dev_status, workspace=self.ws)
+        lost = 0
+        if self.block and not torch.cuda.is_current_stream_capturing():
+            lost = max(0, self.n + k_cur.shape[1] - self.cap)
+        if lost:
+            self._attend_cut(q, o, max(0, q.shape[1] - lost))
+        else:
+            self._attend(q, o, self.lse_self, self.block, self.ws)
         if advance:
             self.commit(k_cur.shape[1])
         return o
+
+    def _attend(self, q, out, lse, block, ws):
+        L.fastar_kv4_attn(q, self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.len_cur, self.scale, out,
+                          lse, block=block, dev_status=self.dev_status, workspace=ws)
+
+    def _attend_cut(self, q, out, c):
+        # the cache's last rows are the first c tokens', which see no block later than their own; the
+        # tokens whose rows were dropped see all that is there
+        for part, block in ((slice(0, c), self.block), (slice(c, None), 0)):
+            lse = torch.empty(self.H, q[:, part].shape[1], dtype=torch.float32, device=q.device)
+            self._attend(q[:, part], out[:, part], lse, block, None)
+            self.lse_self[:, part] = lse
 
     def step_cross(self, q, out=None):
         o = self.o_cross if out is None else out

@@ -180,3 +180,36 @@ def test_a_captured_step_of_the_layer_keeps_its_chunks():
     for a in layers:                                                     # rows can be given up
         a.n = 7
         assert a.n == 7 and a.len.tolist() == [7, 7] and a.history()[0].shape == (H, 7, d)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,nq,block,cap", [(90, 40, 20, 112), (90, 40, 7, 96), (112, 40, 20, 112), (150, 200, 50, 272),
+                                            (100, 300, 100, 304)])
+def test_frames_that_a_full_cache_cuts(dtype, n, nq, block, cap):
+    # rows past the capacity are dropped and flagged; every token sees what is left of the rows it may
+    # see, and none of a later frame's
+    H, d = 2, 64
+    layer = KV4Layer(H, d, nq, cap, 8, dtype=dtype, block=block)
+    x = T._rand((2, H, n, d), 46).to(dtype)
+    layer.load_history(x[0], x[1])
+    q, kv = T._rand((H, nq, d), 47, 1.5).to(dtype), T._rand((2, H, nq, d), 48).to(dtype)
+    out = layer.step_self(q, kv[0], kv[1])
+    torch.cuda.synchronize()
+    assert layer.status() == L.DEV_BAD_LEN and layer.n == cap and layer.len.tolist() == [cap] * H
+    vals = [np.concatenate((K.values(*K.quantise(T._np(a))), K.values(*K.quantise(T._np(b)))), axis=1)[:, :cap]
+            for a, b in ((x[0], kv[0]), (x[1], kv[1]))]
+    for t in range(0, nq, block):
+        f = slice(t, min(nq, t + block))
+        T._check_attn(out[:, f], layer.lse_self[:, f], q[:, f], vals[0], vals[1], [min(cap, n + f.stop)] * H,
+                      1 / math.sqrt(d), 0)
+
+
+@pytest.mark.parametrize("n,nq,block,cap", [(0, 200, 50, 112), (20, 300, 100, 272)])
+def test_a_chunk_larger_than_the_cache_is_refused(n, nq, block, cap):
+    layer = KV4Layer(2, 64, nq, cap, 8, block=block)
+    x = T._rand((3, 2, nq, 64), 49).bfloat16()
+    layer.load_history(x[1, :, :n], x[2, :, :n])
+    with pytest.raises(L.FastarError, match="capacity"):
+        layer.step_self(*x)
+    torch.cuda.synchronize()
+    assert layer.n == n and layer.len.tolist() == [n, n] and layer.status() == 0
