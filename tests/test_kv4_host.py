@@ -158,3 +158,21 @@ def test_packed_calls(lib):
     assert lib.fastar_packed_call(0, words("fastar_qk_norm_rope", rope_args), 30) == L.OK
     rope_args[28] = 0.5
     assert lib.fastar_packed_call(0, words("fastar_qk_norm_rope", rope_args), 30) == L.EINVAL
+
+
+def test_kernels_that_wait_for_the_one_before_make_no_promise_that_nothing_writes():
+    """A kernel launched while its predecessor still writes must not take that memory as __restrict__: the
+    compiler may then load it before the wait.  The 4-bit cache's kernels and the norm's."""
+    import glob
+    import os
+    import re
+    from kv_cache_tempcache_gb300 import build_lib
+    waiting = 0
+    for path in glob.glob(os.path.join(build_lib.CSRC, "kv4*.cu")) + [os.path.join(build_lib.CSRC, "qk_rope.cu")]:
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        for kernel in text.split("__global__")[1:]:
+            head, body = kernel.split("{", 1)
+            if "pdl_wait()" in body.split("__global__")[0]:
+                waiting += 1
+                assert "__restrict__" not in head, (path, head)
+    assert waiting == 6                                     # norm, append, read, the two attentions, the join
