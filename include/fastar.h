@@ -591,8 +591,8 @@ int fastar_qk_norm_rope(int dtype, int64_t n, int d, int Hq, const void* q, int6
                         int grid_h, int grid_w, float theta, cudaStream_t stream);
 
 /* Appends n rows of k and v [H, n, d] to the 4-bit cache: head h's rows at[h] .. at[h] + n
- * (at int32 [H] on the device; NULL: 0).  len_out[h] = at[h] + n (optional; a different array
- * than at, FASTAR_EINVAL otherwise).  Per 16 channels, with x' = x 2^-e:
+ * (at int32 [H] on the device; NULL: 0).  len_out[h] = at[h] + n (optional; no element in
+ * common with at, FASTAR_EINVAL otherwise).  Per 16 channels, with x' = x 2^-e:
  *   s = e4m3(max|x'| / 6), code = e2m1(x' / s), each rounded to nearest with ties to even and
  *   held to the largest finite value; s = 0 stores zeros.
  * A NaN or an infinity is stored as 0, takes no part in the maximum and sets

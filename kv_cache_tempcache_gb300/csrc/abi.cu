@@ -767,7 +767,10 @@ int fastar_kv4_append(int dtype, int H, int64_t n, int d, const void* k, int64_t
   if (rc) return rc;
   if (H < 0 || n < 0 || (rc = check_kv4_cap(cap)) || n > INT32_MAX) return rc ? rc : FASTAR_EINVAL;
   if (n > cap) return FASTAR_ECAPACITY;
-  if (at && at == len_out) return FASTAR_EINVAL;   // the heads' blocks read `at` while one of them writes
+  if (at && len_out) {   // the heads' blocks read `at` while one of them writes: no element in common
+    const uintptr_t p = reinterpret_cast<uintptr_t>(at), o = reinterpret_cast<uintptr_t>(len_out);
+    if ((p < o ? o - p : p - o) < (uintptr_t)H * sizeof(int32_t)) return FASTAR_EINVAL;
+  }
   if (H == 0 || (n == 0 && !len_out)) return FASTAR_OK;
   if ((rc = check_tok(k, dtype, d, k_head_stride, k_token_stride, n, H))) return rc;
   if ((rc = check_tok(v, dtype, d, v_head_stride, v_token_stride, n, H))) return rc;

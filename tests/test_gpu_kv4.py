@@ -550,3 +550,15 @@ def test_a_run_of_calls_equals_one_with_a_wait_after_each(dtype, G, nq, d):
         assert torch.equal(x, y)
     assert torch.isfinite(results[0][7].float()).all()
     assert results[0][-1].tolist() == [min(cap, 5000 + steps * nq)] * Hkv
+
+
+def test_lengths_side_by_side_in_one_buffer():
+    H, n, d = 3, 5, 64
+    k = _rand((H, n, d), 60).bfloat16()
+    for a, b in ((slice(0, H), slice(H, 2 * H)), (slice(H, 2 * H), slice(0, H))):
+        buf = _i32([4, 5, 6] * 2)
+        L.fastar_kv4_append(k, k, *_empty_cache(H, 16, d), buf[a], buf[b])
+        with pytest.raises(L.FastarError):
+            L.fastar_kv4_append(k, k, *_empty_cache(H, 16, d), buf[:H], buf[1:H + 1])
+        torch.cuda.synchronize()
+        assert buf[a].tolist() == [4, 5, 6] and buf[b].tolist() == [9, 10, 11]

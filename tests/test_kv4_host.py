@@ -176,3 +176,9 @@ def test_kernels_that_wait_for_the_one_before_make_no_promise_that_nothing_write
                 waiting += 1
                 assert "__restrict__" not in head, (path, head)
     assert waiting == 6                                     # norm, append, read, the two attentions, the join
+
+
+@pytest.mark.parametrize("H", [2, 5])
+def test_lengths_that_are_read_and_written_share_no_element(lib, H):
+    for off in range(-4 * (H - 1), 4 * H, 4):
+        assert append(lib, H=H, at=FAKE + 256, len_out=FAKE + 256 + off) == L.EINVAL, off
