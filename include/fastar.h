@@ -573,7 +573,9 @@ int fastar_dense_append(int dtype, int H, int64_t nq, int d, const void* k_cur, 
  * axes, in one pass, into q_out and k_out (any strides; dtype F32 or BF16, fp32 arithmetic,
  * rounded once):
  *   wq / wk non-NULL (fp32 [d], 16-byte aligned): x / sqrt(mean(x^2) + eps) * w over the d
- *   channels of the head; NULL: no norm for that tensor;
+ *   channels of the head; NULL: no norm for that tensor.  The squares are summed in fp32: a row
+ *   with finite channels past 2^63 (9e18) may sum to infinity, and its finite channels are
+ *   then 0.  A NaN makes its whole row NaN;
  *   the first axis_t channels turn with the token's frame, the next axis_h with its row, the
  *   next axis_w with its column (even widths >= 0, sum <= d; channels past the sum pass
  *   unrotated): the pair (2j, 2j + 1) of a part of width da by pos * theta^(-2j / da), as in
@@ -623,6 +625,8 @@ int fastar_kv4_read(int dtype, int H, int64_t n, int d, const uint8_t* codes, co
  * a NaN or an infinity gives NaN (zeros if none of its logits is above -infinity), and no other
  * row is touched.  Every weight is held to 2^-11 of itself (bf16) or 2^-22 (dtype F32) down to about
  * 2^-24 and 2^-17 of the row's largest, and below that to 2^-35 and 2^-39 of the largest.
+ * Logits are fp32: past 2^24 of them (in units of log 2) fp32 no longer tells neighbours apart, and rows
+ * with logits past 2^25 may come out as NaN or zeros.
  * lse float [Hq, nq] optional.  Hq * nq <= INT32_MAX (FASTAR_ECAPACITY).
  * workspace (optional): fastar_workspace_bytes(FASTAR_OP_KV4_ATTN, Hq, nq, cap, d, Hkv, ...)
  * bytes for the partial results of key splits; NULL: the keys are not split (slower with few

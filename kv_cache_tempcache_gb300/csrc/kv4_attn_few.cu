@@ -1,7 +1,9 @@
 // Softmax attention over the 4-bit cache for few rows, as in single-token steps: up to 16 (query
 // head, token) pairs of a KV head in bf16; and for fp32 queries, 8 rows a CTA.
 //
-// Bound: the cache's bytes.  A row tile of the tcgen05 kernel is 128 or 256 rows, so with a few
+// Bound: the cache's bytes, for which it still takes twice the time: no unit is full over a long cache (issue
+// slots 50 %, integer 49 %, DRAM 52 %), a warp's chain of waits, products and exponentials is what
+// it waits for, with four warps a scheduler.  A row tile of the tcgen05 kernel is 128 or 256 rows, so with a few
 // rows it spends most of its time unpacking for products that are nearly empty; here the rows
 // are the 8 columns (twice, above 8 rows) of m16n8k16 products (mma.sync: its rate is not what
 // bounds this), and the unpacked codes go from registers straight into the products' operands,

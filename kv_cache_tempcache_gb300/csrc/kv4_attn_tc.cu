@@ -25,9 +25,9 @@
 // limit of one CTA alone: operands 192 KB, unpacked tiles 64 KB written, 18 KB in and out, 2300
 // clocks at 128 bytes each; a pair halves the K and V part (operands 128 KB, 32 KB written).
 // Instruction fetches come next: hot code is one copy, rare paths (masks, rescaling) lie apart.
-// Measured, 12 heads of 128: 4680 tokens over 93,600 rows 1.80 ms (1495 TFLOP/s, 0.77 of the bf16
-// rate measured for a library product), 2850 clocks a tile; the first 4680 tokens in three frames
-// 97 us, of which a CTA's start and end are 6 us an item.
+// Measured, 12 heads of 128, in a replayed graph: 4680 tokens over 93,600 rows 1.81 ms (1490 TFLOP/s, 0.77
+// of the bf16 rate measured for a library product; as one call 1.86 ms), 2850 clocks a tile; the
+// first 4680 tokens in three frames 98 us, of which a CTA's start and end are 6 us an item.
 //
 // Numbers: a cache value (code times scale) is exact in fp16 (kv4.cuh).  A query row is scaled
 // by a power of two that puts its largest element in [2^12, 2^13) and rounded to fp16: bf16's 8

@@ -12,8 +12,9 @@
 //
 // Angles: the step theta^(-2j/width) / 2 pi, in turns, is a 64-bit binary fraction (formed on
 // the host in double), and position * step is taken modulo one turn by the wrap-around of
-// the 64-bit product.  So a far position costs no accuracy (2^24 positions away the error is
-// 2^-31 turns), where the fp32 product pos * step loses a bit of the angle with every
+// the 64-bit product.  So a far position costs no accuracy: the top 32 bits of the turn go to fp32,
+// which rounds them by 2^-26 turns at the most wherever the token is (2^24 positions away the
+// step's own error adds some 2^-30), where the fp32 product pos * step loses a bit of the angle with every
 // doubling of the position; no 64-bit float arithmetic runs on the device.
 #include <climits>
 #include <cmath>
@@ -257,7 +258,7 @@ cudaError_t launch_qk_norm_rope(int dtype, int d, int64_t n, int Hq, TokView q, 
   RopeTable tab;
   int j = 0;
   for (int a = 0; a < 3; ++a) {
-    // the steps of an axis as a geometric sequence: 32 products add 2^-48 to the relative error
+    // the steps of an axis as a geometric sequence: at most 63 products, which add 2^-46 to the relative error
     const double ratio = axes[a] > 0 ? std::pow((double)theta, -2.0 / axes[a]) : 1.0;
     double f = 0.15915494309189535;   // 1 / 2 pi turns
     for (int i = 0; i < axes[a] / 2; ++i, ++j, f *= ratio) {
