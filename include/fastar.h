@@ -13,7 +13,8 @@
  *   7. fastar_cross_attn_subset (cross-attention over the kept prompt tokens)
  * and fastar_dense_attn is the dense baseline the speed-up is measured against.  Section
  * 10 keeps the dense path's append-only cache in 4 bits, and adds the norm and rotation
- * of q and k per head.
+ * of q and k per head.  Section 11 is a cache in pages, and attention over a window of its
+ * rows and its first rows.
  * The merge variant (technical summary §2.A, Theoretical Basis: Lemma 5.1 — merging
  * identical keys is exact when their values are averaged and their logit is shifted
  * by the group size) replaces step 3 with fastar_cache_compact_merge and step 5 with
@@ -99,6 +100,7 @@ extern "C" {
 #define FASTAR_OP_CROSS_ATTN 6
 #define FASTAR_OP_MATCH_PQ 7
 #define FASTAR_OP_KV4_ATTN 8
+#define FASTAR_OP_PAGED_ATTN 9
 
 /* Bytes of workspace `op` needs for the given sizes (0 if it needs none).
  * MATCH: n = Nq, M = cache capacity.  SORT: n = elements per head before the
@@ -108,6 +110,9 @@ extern "C" {
  * the kept prompt rows).  MATCH_PQ: n = Nq, M, d (the decoded cached keys).
  * KV4_ATTN: H = query heads, n = tokens of the call, M = cache capacity, d, B = KV heads (the
  * partial results of the key splits; 0 where the keys are not split).
+ * PAGED_ATTN: H = query heads, n = tokens of the call, M = rows of a sequence's pages (with a
+ * window, window + sinks if that is less), d, B = KV heads, r = most tokens of a sequence, P =
+ * sequences (the partial results of the key splits; 0 where the keys are not split).
  * Unused arguments are ignored.  Returns 0 for an unknown op. */
 size_t fastar_workspace_bytes(int op, int H, int64_t n, int64_t M, int d, int B, int r,
                               int64_t P, int F);
@@ -638,7 +643,71 @@ int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d
                     int64_t o_token_stride, float* lse, int32_t* dev_status, void* workspace, size_t workspace_bytes,
                     cudaStream_t stream);
 
-/* The four calls above with their arguments in one array of n 64-bit words, in the order of their
+/* ---- 11. a cache in pages, and attention over a window of it with its first rows -------------
+ * Not on the pages: the other bounded cache of rollouts, which keeps the last rows and the first
+ * ones (sinks) and gives the memory of those between back.  Pools k_pool, v_pool of `pages` pages of
+ * `page` rows: element (page, h, slot, c) lies at page * page_stride + h * head_stride +
+ * slot * row_stride + c (elements; the same strides for both), so that pages of [H, page, d] and of
+ * [page, H, d] both work.  page is 16, 32, 64 or 128; pools and strides 16-byte aligned.
+ * Row r of sequence b of B is slot r % page of page table[b * max_pages + r / page] (int32 on the
+ * device); a sequence has max_pages * page rows at most (at most 2^30, FASTAR_ECAPACITY).  The T
+ * tokens of a call (at most 2^30) lie behind one another, sequence b's are cu[b] .. cu[b + 1]
+ * (int32 [B + 1] on the device, not falling; NULL: T / B tokens each, T a multiple of B); at[b]
+ * (int32 [B] on the device) rows come before them: token i of a sequence is its row at + i.  Tokens
+ * past cu[B] belong to no sequence: nothing of theirs is read for others or written.
+ *   cu that falls or leaves [0, T], or at outside [0, max_pages * page]: FASTAR_DEV_BAD_LEN, and the
+ *   sequence is skipped.  A table entry outside [0, pages) where it is needed:
+ *   FASTAR_DEV_BAD_INDEX.  B <= 65535 (FASTAR_ECAPACITY).  dev_status optional. */
+
+/* The call's rows of k and v [Hk, T, d] into their pages, k with RMS norm (wk non-NULL) and rotary
+ * positions on the way, and q [Hq, T, d] in the same way to q_out (q and q_out NULL: not).  Norm,
+ * axes, theta and accuracy as in fastar_qk_norm_rope; a token's position is pos int32 [T, 3] or, NULL, its
+ * row r = at + i on the grid: frame r / (grid_h grid_w), row (r / grid_w) % grid_h, column
+ * r % grid_w (grid 1 x 1: r itself turns the first axis).  v goes as it is.
+ * len_out[b] = at + tokens (optional; held to the sequence's rows; no element in common with at,
+ * FASTAR_EINVAL otherwise; of a skipped sequence 0).
+ * Rows past the sequence's last are dropped and set FASTAR_DEV_BAD_LEN, rows whose table
+ * entry is no page are dropped and set FASTAR_DEV_BAD_INDEX; their q_out is written all the same.
+ * Other rows of the pools are left as they were.  Of two tokens whose rows share a slot (two
+ * sequences with one page in common) either may stay.  In place (q_out = q with the same strides) is
+ * allowed; otherwise outputs must not overlap inputs, nor the pools one another. */
+int fastar_paged_append(int dtype, int B, int64_t T, const int32_t* cu, int d, int Hq, const void* q,
+                        int64_t q_head_stride, int64_t q_token_stride, void* q_out, int64_t qo_head_stride,
+                        int64_t qo_token_stride, int Hk, const void* k, int64_t k_head_stride, int64_t k_token_stride,
+                        const void* v, int64_t v_head_stride, int64_t v_token_stride, const float* wq, const float* wk,
+                        float eps, int axis_t, int axis_h, int axis_w, const int32_t* pos, int grid_h, int grid_w,
+                        float theta, void* k_pool, void* v_pool, int64_t pages, int page, int64_t page_stride,
+                        int64_t head_stride, int64_t row_stride, const int32_t* table, int64_t max_pages,
+                        const int32_t* at, int32_t* len_out, int32_t* dev_status, cudaStream_t stream);
+
+/* Softmax attention of q [Hq, T, d] over the pages; query head h reads KV head h / (Hq / Hkv).
+ * With n tokens of the sequence in the call, the end of token i is E = at + n, or with block > 0
+ * E = at + min(n, (i / block + 1) * block) (1: causal; a frame's tokens: a frame sees itself and the
+ * frames before it).  It sees the rows j < E with
+ *   j >= E - window  or  j < sinks       (window > 0; window = 0: all of them)
+ * of those that the sequence's pages hold:
+ *   O[h,i] = sum_j softmax_j(q_i . k_j * scale) v_j;  no row: O = 0, lse = -inf.
+ * Rows that no token of the sequence sees are not used, and table entries of pages without a row
+ * in [E - window of the first token, E of the last) or before sinks are not looked at (give such
+ * pages back).  What a token does not see cannot reach its output, whatever its bits.  A row of a
+ * page that is needed and missing counts as zeros (FASTAR_DEV_BAD_INDEX).
+ * max_q: the most tokens of a sequence (host; FASTAR_EINVAL outside [1, T]).  Of a longer one the first max_q
+ * are done, the others' outputs are left as they were, FASTAR_DEV_BAD_LEN is set.
+ * Every weight is held to 2^-8 of itself (bf16) or in fp32 (dtype F32); logits, maxima and sums in fp32.
+ * A row of q with a NaN or an infinity gives NaN (zeros if none of its logits is above
+ * -infinity), and no other row is touched.
+ * lse float [Hq, T] optional.  Hq * T <= INT32_MAX (FASTAR_ECAPACITY).
+ * workspace (optional): fastar_workspace_bytes(FASTAR_OP_PAGED_ATTN, ...) bytes for the partial
+ * results of key splits; fewer bytes: fewer splits; NULL: none (slower with few rows).  Calls that
+ * share a workspace must not overlap on the GPU. */
+int fastar_paged_attn(const void* q, int dtype, int B, int64_t T, const int32_t* cu, int64_t max_q, int Hq, int Hkv,
+                      int d, int64_t q_head_stride, int64_t q_token_stride, const void* k_pool, const void* v_pool,
+                      int64_t pages, int page, int64_t page_stride, int64_t head_stride, int64_t row_stride,
+                      const int32_t* table, int64_t max_pages, const int32_t* at, int64_t block, int64_t window,
+                      int64_t sinks, float scale, void* out, int64_t o_head_stride, int64_t o_token_stride, float* lse,
+                      int32_t* dev_status, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* The calls of sections 10 and 11 with their arguments in one array of n 64-bit words, in the order of their
  * declarations: integers and addresses as they are, floats as the bits of a double.  For bindings
  * that pay for each argument (ctypes: 75 ns, 2 us for all of fastar_kv4_attn's).  A call or a
  * number of words that is not one of theirs, or an int that does not fit 32 bits: FASTAR_EINVAL. */
@@ -646,6 +715,8 @@ int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d
 #define FASTAR_CALL_KV4_APPEND 1     /* n = 21 */
 #define FASTAR_CALL_KV4_READ 2       /* n = 13 */
 #define FASTAR_CALL_KV4_ATTN 3       /* n = 26 */
+#define FASTAR_CALL_PAGED_APPEND 4   /* n = 42 */
+#define FASTAR_CALL_PAGED_ATTN 5     /* n = 33 */
 int fastar_packed_call(int call, const void* words, int n);
 
 #ifdef __cplusplus

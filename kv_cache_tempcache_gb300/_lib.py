@@ -21,7 +21,7 @@ OK, EINVAL, EUNSUPPORTED, ECAPACITY, EWORKSPACE, ECUDA = 0, -1, -2, -3, -4, -5
 DEV_BAD_LEN, DEV_BAD_BUCKET, DEV_BAD_INDEX = 1, 2, 4
 DEV_TIMEOUT, DEV_NONFINITE = 8, 16
 OP_MATCH, OP_SORT, OP_SPARSE_ATTN, OP_ANNCA, OP_MATCH_ANN, OP_CROSS_ATTN, OP_MATCH_PQ = 1, 2, 3, 4, 5, 6, 7
-OP_KV4_ATTN = 8
+OP_KV4_ATTN, OP_PAGED_ATTN = 8, 9
 MAX_B, MAX_R, MAX_P = 256, 8, 1024
 
 _P = ctypes.c_void_p
@@ -79,6 +79,10 @@ _SIGS = {
     "fastar_kv4_read": [_I, _I, _L, _I, _P, _P, _P, _L, _L, _P, _L, _L, _P],
     "fastar_kv4_attn": [_P, _I, _I, _I, _L, _I, _L, _L, _P, _P, _P, _P, _P, _P, _L, _P, _L, _F, _P, _L, _L, _P, _P,
                         _P, _S, _P],
+    "fastar_paged_append": [_I, _I, _L, _P, _I, _I, _P, _L, _L, _P, _L, _L, _I, _P, _L, _L, _P, _L, _L, _P, _P, _F, _I,
+                            _I, _I, _P, _I, _I, _F, _P, _P, _L, _I, _L, _L, _L, _P, _L, _P, _P, _P, _P],
+    "fastar_paged_attn": [_P, _I, _I, _L, _P, _L, _I, _I, _I, _L, _L, _P, _P, _L, _I, _L, _L, _L, _P, _L, _P, _L, _L,
+                          _L, _F, _P, _L, _L, _P, _P, _P, _S, _P],
     "fastar_packed_call": [_I, _P, _I],
 }
 _RESTYPES = {"fastar_status_string": ctypes.c_char_p, "fastar_workspace_bytes": ctypes.c_size_t,
@@ -428,7 +432,7 @@ def fastar_sinusoidal_embedding(t, out, stream=None):
     _call("fastar_sinusoidal_embedding", ptr(t), nb, dim, out.data_ptr(), out.stride(0), stream_handle(stream))
 
 
-# ---- the 4-bit cache, and the norm and rotation before it -------------------------------------
+# ---- the 4-bit cache, the norm and rotation before it, the paged cache -------------------------
 
 # Every check below refuses what a kernel would misread.  They run on each call of a step that
 # may be a few microseconds of device time, so a call asks for everything in one expression, without
@@ -453,6 +457,8 @@ _CALL_ROPE, _PACK_ROPE, _N_ROPE = _packer(0, "fastar_qk_norm_rope")
 _CALL_APPEND, _PACK_APPEND, _N_APPEND = _packer(1, "fastar_kv4_append")
 _CALL_READ, _PACK_READ, _N_READ = _packer(2, "fastar_kv4_read")
 _CALL_ATTN, _PACK_ATTN, _N_ATTN = _packer(3, "fastar_kv4_attn")
+_CALL_PAPPEND, _PACK_PAPPEND, _N_PAPPEND = _packer(4, "fastar_paged_append")
+_CALL_PATTN, _PACK_PATTN, _N_PATTN = _packer(5, "fastar_paged_attn")
 
 
 def _refuse(rows, dense):
@@ -646,6 +652,130 @@ def fastar_kv4_attn(q, k_codes, k_scales, v_codes, v_scales, lens, scale, out, l
         _current_stream(dev) if stream is None else stream.cuda_stream), _N_ATTN)
     if rc:
         _raise("fastar_kv4_attn", rc)
+
+
+def _refuse_paged(rows, dense, k_pool, v_pool, dt, Hk, d, table, at, cu):
+    """As _refuse, for the calls over a paged cache."""
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+        if t.dtype is not dt:
+            raise ValueError(f"{name} must be {dt}, not {t.dtype}")
+        if t.dim() != 4 or t.shape[1] != Hk or t.shape[3] != d:
+            raise ValueError(f"{name} must have the shape [pages, {Hk}, page, {d}], not {tuple(t.shape)}")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name} must have a contiguous last dimension")
+    if k_pool.shape != v_pool.shape or k_pool.stride() != v_pool.stride():
+        raise ValueError("k_pool and v_pool must share shape and strides")
+    if table.dim() != 2:
+        raise ValueError(f"table must have two dimensions, not {table.dim()}")
+    B = table.shape[0]
+    _refuse(rows, [("table", table, _I32, table.shape), ("at", at, _I32, (B,)), ("cu", cu, _I32, (B + 1,))] + dense)
+
+
+def fastar_paged_append(k, v, k_pool, v_pool, table, at, len_out=None, q=None, q_out=None, cu=None, wq=None, wk=None,
+                        eps=1e-6, axes=(0, 0, 0), pos=None, grid=(1, 1), theta=10000.0, dev_status=None, stream=None):
+    """Rows k, v [Hk, T, d] of the sequences' tokens into the pages of k_pool, v_pool [pages, Hk, page, d]
+    (any strides, the same for both) that table [B, max_pages] (int32) names, behind at[b] earlier rows
+    (int32 [B]); cu [B + 1] (int32): where each sequence's tokens begin (None: T / B tokens each).  k is
+    normed (wk given) and turned by its row's position on the grid, or pos [T, 3]; q [Hq, T, d] likewise into
+    q_out.  len_out[b] = at[b] + its tokens."""
+    Hk, T, d = ks = _dims3("k", k)
+    dt, dev = k.dtype, k.get_device()
+    code = _CODES[dt] if dt in _CODES else _raise_dtype(dt)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    Hq = 0 if q is None else _dims3("q", q)[0]
+    qs = (Hq, T, d)
+    p_sh, p_st = k_pool.shape, k_pool.stride()
+    if not (
+            dev >= 0 and dev == _device()
+            and (k_st := k.stride())[2] == 1
+            and v.dtype is dt and v.shape == ks and (v_st := v.stride())[2] == 1 and v.get_device() == dev
+            and len(p_sh) == 4 and p_sh[1] == Hk and p_sh[3] == d and k_pool.dtype is dt and p_st[3] == 1
+            and k_pool.get_device() == dev
+            and v_pool.dtype is dt and v_pool.shape == p_sh and v_pool.stride() == p_st and v_pool.get_device() == dev
+            and table.dtype is _I32 and len(t_sh := table.shape) == 2 and table.is_contiguous()
+            and table.get_device() == dev
+            and at.dtype is _I32 and at.shape == (t_sh[0],) and at.is_contiguous() and at.get_device() == dev
+            and (q is None or q.dtype is dt and q.shape == qs and (q_st := q.stride())[2] == 1 and q.get_device() == dev
+                 and q_out.dtype is dt and q_out.shape == qs and (qo_st := q_out.stride())[2] == 1
+                 and q_out.get_device() == dev)
+            and (cu is None or cu.dtype is _I32 and cu.shape == (t_sh[0] + 1,) and cu.is_contiguous()
+                 and cu.get_device() == dev)
+            and (len_out is None or len_out.dtype is _I32 and len_out.shape == (t_sh[0],) and len_out.is_contiguous()
+                 and len_out.get_device() == dev)
+            and (wq is None or wq.dtype is _F32 and wq.shape == (d,) and wq.is_contiguous() and wq.get_device() == dev)
+            and (wk is None or wk.dtype is _F32 and wk.shape == (d,) and wk.is_contiguous() and wk.get_device() == dev)
+            and (pos is None or pos.dtype is _I32 and pos.shape == (T, 3) and pos.is_contiguous()
+                 and pos.get_device() == dev)
+            and (dev_status is None or dev_status.dtype is _I32 and dev_status.shape == (1,)
+                 and dev_status.get_device() == dev)):
+        _refuse_paged([("k", k, dt, ks), ("v", v, dt, ks), ("q", q, dt, qs), ("q_out", q_out, dt, qs)],
+                      [("len_out", len_out, _I32, table.shape[:1]), ("wq", wq, _F32, (d,)), ("wk", wk, _F32, (d,)),
+                       ("pos", pos, _I32, (T, 3)), ("dev_status", dev_status, _I32, (1,))],
+                      k_pool, v_pool, dt, Hk, d, table, at, cu)
+    if q is None:
+        q_st = qo_st = (0, 0)
+    B, max_pages = t_sh
+    rc = (_lib or load()).fastar_packed_call(_CALL_PAPPEND, _PACK_PAPPEND(
+        code, B, T, 0 if cu is None else cu.data_ptr(), d, Hq, 0 if q is None else q.data_ptr(),
+        q_st[0] if Hq > 1 else T * d, q_st[1] if T > 1 else d, 0 if q is None else q_out.data_ptr(),
+        qo_st[0] if Hq > 1 else T * d, qo_st[1] if T > 1 else d, Hk, k.data_ptr(), k_st[0] if Hk > 1 else T * d,
+        k_st[1] if T > 1 else d, v.data_ptr(), v_st[0] if Hk > 1 else T * d, v_st[1] if T > 1 else d,
+        0 if wq is None else wq.data_ptr(), 0 if wk is None else wk.data_ptr(), eps, axes[0], axes[1], axes[2],
+        0 if pos is None else pos.data_ptr(), grid[0], grid[1], theta, k_pool.data_ptr(), v_pool.data_ptr(), p_sh[0],
+        p_sh[2], p_st[0] if p_sh[0] > 1 else d, p_st[1] if Hk > 1 else d, p_st[2], table.data_ptr(), max_pages,
+        at.data_ptr(), 0 if len_out is None else len_out.data_ptr(), 0 if dev_status is None else dev_status.data_ptr(),
+        _current_stream(dev) if stream is None else stream.cuda_stream), _N_PAPPEND)
+    if rc:
+        _raise("fastar_paged_append", rc)
+
+
+def fastar_paged_attn(q, k_pool, v_pool, table, at, scale, out, lse=None, cu=None, max_q=None, block=0, window=0,
+                      sinks=0, dev_status=None, workspace=None, stream=None):
+    """Attention of the sequences' tokens q [Hq, T, d] over the pages of k_pool, v_pool [pages, Hkv, page, d]
+    that table [B, max_pages] names, the tokens' own rows (behind at[b] earlier ones) among them.  block: 0,
+    or the tokens of a block that sees no later one (1: causal); window > 0: only the last `window` rows before
+    the token's end, and the first `sinks`.  cu [B + 1] as in fastar_paged_append; max_q: the most tokens
+    of a sequence (None: T, with cu None T / B).  workspace: workspace_bytes(OP_PAGED_ATTN, Hq, T,
+    max_pages * page, d, Hkv, r=max_q, P=B) bytes (None: the keys are not split)."""
+    Hq, T, d = qs = _dims3("q", q)
+    dt, dev = q.dtype, q.get_device()
+    code = _CODES[dt] if dt in _CODES else _raise_dtype(dt)
+    p_sh, p_st = k_pool.shape, k_pool.stride()
+    if not (
+            dev >= 0 and dev == _device()
+            and (q_st := q.stride())[2] == 1
+            and out.dtype is dt and out.shape == qs and (o_st := out.stride())[2] == 1 and out.get_device() == dev
+            and len(p_sh) == 4 and p_sh[3] == d and k_pool.dtype is dt and p_st[3] == 1 and k_pool.get_device() == dev
+            and v_pool.dtype is dt and v_pool.shape == p_sh and v_pool.stride() == p_st and v_pool.get_device() == dev
+            and table.dtype is _I32 and len(t_sh := table.shape) == 2 and table.is_contiguous()
+            and table.get_device() == dev
+            and at.dtype is _I32 and at.shape == (t_sh[0],) and at.is_contiguous() and at.get_device() == dev
+            and (cu is None or cu.dtype is _I32 and cu.shape == (t_sh[0] + 1,) and cu.is_contiguous()
+                 and cu.get_device() == dev)
+            and (lse is None or lse.dtype is _F32 and lse.shape == (Hq, T) and lse.is_contiguous()
+                 and lse.get_device() == dev)
+            and (dev_status is None or dev_status.dtype is _I32 and dev_status.shape == (1,)
+                 and dev_status.get_device() == dev)
+            and (workspace is None or workspace.is_contiguous() and workspace.get_device() == dev)):
+        dense = [("lse", lse, _F32, (Hq, T)), ("dev_status", dev_status, _I32, (1,))]
+        if workspace is not None:
+            dense.append(("workspace", workspace, workspace.dtype, workspace.shape))
+        _refuse_paged([("q", q, dt, qs), ("out", out, dt, qs)], dense, k_pool, v_pool, dt,
+                      k_pool.shape[1] if k_pool.dim() == 4 else 0, d, table, at, cu)
+    B, max_pages = t_sh
+    if max_q is None:
+        max_q = T if cu is not None else T // max(B, 1)
+    rc = (_lib or load()).fastar_packed_call(_CALL_PATTN, _PACK_PATTN(
+        q.data_ptr(), code, B, T, 0 if cu is None else cu.data_ptr(), max_q, Hq, p_sh[1], d,
+        q_st[0] if Hq > 1 else T * d, q_st[1] if T > 1 else d, k_pool.data_ptr(), v_pool.data_ptr(), p_sh[0], p_sh[2],
+        p_st[0] if p_sh[0] > 1 else d, p_st[1] if p_sh[1] > 1 else d, p_st[2], table.data_ptr(), max_pages,
+        at.data_ptr(), block, window, sinks, scale, out.data_ptr(), o_st[0] if Hq > 1 else T * d,
+        o_st[1] if T > 1 else d, 0 if lse is None else lse.data_ptr(), 0 if dev_status is None else dev_status.data_ptr(),
+        0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        _current_stream(dev) if stream is None else stream.cuda_stream), _N_PATTN)
+    if rc:
+        _raise("fastar_paged_attn", rc)
 
 
 def fastar_dense_append(k_cur, v_cur, k_cache, v_cache, at, stream=None):

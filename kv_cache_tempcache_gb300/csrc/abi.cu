@@ -46,6 +46,25 @@ int check_kv4(const void* codes, const void* scales) {
   return codes && scales && aligned16(codes) && aligned16(scales) ? FASTAR_OK : FASTAR_EINVAL;
 }
 
+// Pools of pages, the table and the sequences of a call.
+int check_pools(const void* k, const void* v, int dtype, int d, int H, int64_t pages, int page, int64_t ps, int64_t hs,
+                int64_t rs) {
+  if (page != 16 && page != 32 && page != 64 && page != 128) return FASTAR_EINVAL;
+  if (pages < 1 || pages > INT32_MAX) return FASTAR_EINVAL;
+  if (!k || !v || !aligned16(k) || !aligned16(v) || k == v) return FASTAR_EINVAL;
+  const int64_t es = (int64_t)esize(dtype);
+  if (rs < d || ps < d || hs < 0 || (H > 1 && hs < d)) return FASTAR_EINVAL;
+  if (((rs * es) & 15) || ((ps * es) & 15) || ((hs * es) & 15)) return FASTAR_EINVAL;
+  return FASTAR_OK;
+}
+int check_paged(int B, int64_t T, const int32_t* cu, int page, int64_t max_pages) {
+  if (B < 1 || T < 0 || max_pages < 1 || page < 1) return FASTAR_EINVAL;
+  if (B > 65535 || T > fastar::kPagedMax || max_pages > fastar::kPagedMax / page) return FASTAR_ECAPACITY;
+  if (!cu && T % B) return FASTAR_EINVAL;
+  return FASTAR_OK;
+}
+int held32(int64_t x) { return (int)(x < INT32_MAX ? x : INT32_MAX); }
+
 // fastar_packed_call: a 64-bit word as an argument of type T; false if an int does not fit.
 template <typename T>
 bool from_word(int64_t w, T& v) {
@@ -126,6 +145,10 @@ size_t fastar_workspace_bytes(int op, int H, int64_t n, int64_t M, int d, int B,
       if ((d != 64 && d != 128) || B < 1 || H % B || M < 1 || n < 1) return 0;
       if (M > INT32_MAX || n > INT32_MAX || H * n > INT32_MAX) return 0;   // fastar_kv4_attn refuses them
       return fastar::kv4_attn_workspace(d, H, B, n, M);
+    case FASTAR_OP_PAGED_ATTN:
+      if ((d != 64 && d != 128) || B < 1 || H < 1 || H % B || M < 1 || n < 1 || r < 1 || P < 1) return 0;
+      if (n > fastar::kPagedMax || H * n > INT32_MAX || r > n || P > 65535) return 0;   // the call refuses them
+      return fastar::paged_attn_workspace(d, H, B, n, (int)P, r, M < fastar::kPagedMax ? M : fastar::kPagedMax);
     default: return 0;
   }
 }
@@ -837,12 +860,125 @@ int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d
   return cuda_rc(err);
 }
 
+int fastar_paged_append(int dtype, int B, int64_t T, const int32_t* cu, int d, int Hq, const void* q,
+                        int64_t q_head_stride, int64_t q_token_stride, void* q_out, int64_t qo_head_stride,
+                        int64_t qo_token_stride, int Hk, const void* k, int64_t k_head_stride, int64_t k_token_stride,
+                        const void* v, int64_t v_head_stride, int64_t v_token_stride, const float* wq, const float* wk,
+                        float eps, int axis_t, int axis_h, int axis_w, const int32_t* pos, int grid_h, int grid_w,
+                        float theta, void* k_pool, void* v_pool, int64_t pages, int page, int64_t page_stride,
+                        int64_t head_stride, int64_t row_stride, const int32_t* table, int64_t max_pages,
+                        const int32_t* at, int32_t* len_out, int32_t* dev_status, cudaStream_t stream) {
+  int rc = check_dtype_d(dtype, d);
+  if (rc) return rc;
+  if (Hq < 0 || Hk < 1 || Hq > (1 << 20) || Hk > (1 << 20)) return FASTAR_EINVAL;
+  if ((rc = check_pools(k_pool, v_pool, dtype, d, Hk, pages, page, page_stride, head_stride, row_stride))) return rc;
+  if ((rc = check_paged(B, T, cu, page, max_pages))) return rc;
+  const int axes[3] = {axis_t, axis_h, axis_w};
+  int64_t sum = 0;
+  for (int a : axes) {
+    if (a < 0 || a % 2) return FASTAR_EINVAL;
+    sum += a;
+  }
+  if (sum > d || !(theta > 1.f) || !(theta < 3.0e38f)) return FASTAR_EINVAL;
+  if ((wq || wk) && (!(eps > 0.f) || !(eps < 3.0e38f))) return FASTAR_EINVAL;
+  if (sum > 0 && !pos && (grid_h < 1 || grid_w < 1)) return FASTAR_EINVAL;
+  if ((wq && !aligned16(wq)) || (wk && !aligned16(wk))) return FASTAR_EINVAL;
+  if (!table || !at) return FASTAR_EINVAL;
+  if (len_out) {   // the tokens' blocks read `at` while one of them writes: no element in common
+    const uintptr_t p = reinterpret_cast<uintptr_t>(at), o = reinterpret_cast<uintptr_t>(len_out);
+    if ((p < o ? o - p : p - o) < (uintptr_t)B * sizeof(int32_t)) return FASTAR_EINVAL;
+  }
+  if (T == 0 && !len_out) return FASTAR_OK;
+  if ((rc = check_tok(k, dtype, d, k_head_stride, k_token_stride, T, Hk))) return rc;
+  if ((rc = check_tok(v, dtype, d, v_head_stride, v_token_stride, T, Hk))) return rc;
+  if (T > 0 && !q != !q_out) return FASTAR_EINVAL;
+  const bool with_q = q && Hq > 0;
+  if (with_q) {
+    if ((rc = check_tok(q, dtype, d, q_head_stride, q_token_stride, T, Hq))) return rc;
+    if ((rc = check_tok(q_out, dtype, d, qo_head_stride, qo_token_stride, T, Hq))) return rc;
+    // in place only row by row
+    if (q == q_out && (q_head_stride != qo_head_stride || q_token_stride != qo_token_stride)) return FASTAR_EINVAL;
+  }
+  fastar::PagedAppendArgs a{};
+  a.B = B;
+  a.Hq = with_q ? Hq : 0;
+  a.Hk = Hk;
+  a.T = T;
+  a.cu = cu;
+  a.q = TokView{q, q_head_stride, q_token_stride};
+  a.k = TokView{k, k_head_stride, k_token_stride};
+  a.v = TokView{v, v_head_stride, v_token_stride};
+  a.qo = with_q ? q_out : nullptr;
+  a.qo_hs = qo_head_stride;
+  a.qo_ts = qo_token_stride;
+  a.wq = wq;
+  a.wk = wk;
+  a.eps = eps;
+  a.pos = pos;
+  a.gh = grid_h < 1 ? 1 : grid_h;
+  a.gw = grid_w < 1 ? 1 : grid_w;
+  a.pool = fastar::PagedPools{k_pool, v_pool, pages, page_stride, head_stride, row_stride, __builtin_ctz(page)};
+  a.table = table;
+  a.max_pages = max_pages;
+  a.at = at;
+  a.len_out = len_out;
+  a.status = dev_status;
+  return cuda_rc(fastar::launch_paged_append(dtype, d, a, axes, theta, stream));
+}
+
+int fastar_paged_attn(const void* q, int dtype, int B, int64_t T, const int32_t* cu, int64_t max_q, int Hq, int Hkv,
+                      int d, int64_t q_head_stride, int64_t q_token_stride, const void* k_pool, const void* v_pool,
+                      int64_t pages, int page, int64_t page_stride, int64_t head_stride, int64_t row_stride,
+                      const int32_t* table, int64_t max_pages, const int32_t* at, int64_t block, int64_t window,
+                      int64_t sinks, float scale, void* out, int64_t o_head_stride, int64_t o_token_stride, float* lse,
+                      int32_t* dev_status, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  int rc = check_dtype_d(dtype, d);
+  if (rc) return rc;
+  if (Hq < 0 || Hkv < 1 || Hq % Hkv || Hq > (1 << 20) || block < 0 || window < 0 || sinks < 0) return FASTAR_EINVAL;
+  if ((rc = check_pools(k_pool, v_pool, dtype, d, Hkv, pages, page, page_stride, head_stride, row_stride))) return rc;
+  if ((rc = check_paged(B, T, cu, page, max_pages))) return rc;
+  if ((int64_t)Hq * T > INT32_MAX) return FASTAR_ECAPACITY;
+  if (!(scale > 0.f) || !(scale < 3.0e38f)) return FASTAR_EINVAL;
+  if (Hq == 0 || T == 0) return FASTAR_OK;
+  if (max_q < 1 || max_q > T) return FASTAR_EINVAL;
+  if ((rc = check_tok(q, dtype, d, q_head_stride, q_token_stride, T, Hq))) return rc;
+  if ((rc = check_tok(out, dtype, d, o_head_stride, o_token_stride, T, Hq))) return rc;
+  if (!table || !at) return FASTAR_EINVAL;
+  if (workspace && !aligned16(workspace)) return FASTAR_EWORKSPACE;
+  fastar::PagedAttnArgs a{};
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.q = TokView{q, q_head_stride, q_token_stride};
+  a.T = T;
+  a.cu = cu;
+  a.max_q = (int)max_q;
+  a.pool = fastar::PagedPools{const_cast<void*>(k_pool), const_cast<void*>(v_pool), pages, page_stride, head_stride,
+                              row_stride, __builtin_ctz(page)};
+  a.table = table;
+  a.max_pages = max_pages;
+  a.cap = max_pages * page;
+  a.at = at;
+  a.block = (int)(block < T ? block : T);   // one block of all the call's tokens is the largest
+  a.window = held32(window);
+  a.sinks = held32(sinks);
+  a.scale = scale;
+  a.out = out;
+  a.o_hs = o_head_stride;
+  a.o_ts = o_token_stride;
+  a.lse = lse;
+  a.status = dev_status;
+  return cuda_rc(fastar::launch_paged_attn(dtype, d, a, workspace, workspace_bytes, stream));
+}
+
 int fastar_packed_call(int call, const void* words, int n) {
   switch (call) {
     case FASTAR_CALL_QK_NORM_ROPE: return call_packed(fastar_qk_norm_rope, words, n);
     case FASTAR_CALL_KV4_APPEND: return call_packed(fastar_kv4_append, words, n);
     case FASTAR_CALL_KV4_READ: return call_packed(fastar_kv4_read, words, n);
     case FASTAR_CALL_KV4_ATTN: return call_packed(fastar_kv4_attn, words, n);
+    case FASTAR_CALL_PAGED_APPEND: return call_packed(fastar_paged_append, words, n);
+    case FASTAR_CALL_PAGED_ATTN: return call_packed(fastar_paged_attn, words, n);
     default: return FASTAR_EINVAL;
   }
 }

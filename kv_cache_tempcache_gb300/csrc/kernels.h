@@ -237,4 +237,58 @@ cudaError_t launch_kv4_attn_tc(int d, const Kv4AttnArgs& a, cudaStream_t s);
 // bf16: up to 16 rows a KV head; fp32: any
 cudaError_t launch_kv4_attn_few(int dtype, int d, const Kv4AttnArgs& a, cudaStream_t s);
 
+// ---- the paged cache ----------------------------------------------------------------------
+constexpr int64_t kPagedMax = (int64_t)1 << 30;    // rows of a table, tokens of a call
+
+// Pools of pages: element (page, h, slot, c) at p + page * ps + h * hs + slot * rs + c.
+struct PagedPools {
+  void *k, *v;
+  int64_t pages, ps, hs, rs;
+  int page_shift;                     // log2 of the rows of a page
+};
+struct PagedAppendArgs {
+  int B, Hq, Hk;
+  int64_t T;
+  const int32_t* cu;                  // [B + 1] or null: T / B tokens each
+  TokView q, k, v;
+  void* qo;                           // null: k and v only
+  int64_t qo_hs, qo_ts;
+  const float *wq, *wk;               // [d] or null
+  float eps;
+  const int32_t* pos;                 // [T, 3] or null: from the row
+  int gh, gw;
+  PagedPools pool;
+  const int32_t* table;               // [B, max_pages]
+  int64_t max_pages;
+  const int32_t* at;                  // [B]
+  int32_t *len_out, *status;
+  int part_shift;                     // log2 of the warps per token (by the launcher)
+};
+cudaError_t launch_paged_append(int dtype, int d, PagedAppendArgs a, const int* axes, float theta, cudaStream_t s);
+
+struct PagedAttnArgs {
+  int B, Hq, Hkv;
+  TokView q;
+  int64_t T;
+  const int32_t* cu;                  // [B + 1] or null
+  int max_q;                          // tokens of a sequence that are worked on
+  PagedPools pool;
+  const int32_t* table;               // [B, max_pages]
+  int64_t max_pages, cap;             // cap: rows of a sequence's pages
+  const int32_t* at;                  // [B]
+  int block, window, sinks;
+  float scale;
+  void* out;
+  int64_t o_hs, o_ts;
+  float* lse;                         // [Hq, T] or null
+  int32_t* status;
+  // filled in by the launcher: query heads of a KV head, splits of the keys, the key tiles a split
+  // should have, the partials (fp32; maximum and sum)
+  int group, splits, min_tiles;
+  float* part_o;                      // [splits, T, Hq, d]
+  float2* part_ml;                    // [splits, T, Hq]
+};
+size_t paged_attn_workspace(int d, int Hq, int Hkv, int64_t T, int B, int max_q, int64_t cap);
+cudaError_t launch_paged_attn(int dtype, int d, PagedAttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s);
+
 }  // namespace fastar

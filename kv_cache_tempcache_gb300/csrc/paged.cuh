@@ -1,0 +1,116 @@
+// What the kernels over a paged cache share: where a sequence's tokens and rows lie, which rows a
+// token sees, and how the rows of a piece of work become a list of key tiles.
+//
+// Row r of sequence b is slot r % page of page table[b, r / page].  Token i of a sequence is its
+// row at + i; its end is E(i) = at + nq, or with blocks at + min(nq, (i / block + 1) block); it
+// sees the rows j < min(E, cap) with j >= E - window (all with window 0) or j < sinks.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace fastar {
+namespace paged {
+
+// The tokens of sequence b: cu[b] .. cu[b] + nq of the call's, behind `at` earlier rows.  nq = 0 where cu
+// or at make no sense (FASTAR_DEV_BAD_LEN).
+struct Seq {
+  int t0, nq, at;
+};
+__device__ __forceinline__ Seq sequence(const int32_t* cu, const int32_t* at, int B, int64_t T, int64_t cap, int b,
+                                        int32_t* status) {
+  Seq s;
+  if (cu) {
+    s.t0 = cu[b];
+    const int t1 = cu[b + 1];
+    s.nq = t1 - s.t0;
+    if (s.t0 < 0 || t1 < s.t0 || t1 > T) s.t0 = 0, s.nq = -1;
+  } else {
+    s.nq = (int)(T / B);
+    s.t0 = b * s.nq;
+  }
+  s.at = at[b];
+  if (s.nq < 0 || s.at < 0 || s.at > cap) {
+    flag_status(status, FASTAR_DEV_BAD_LEN);
+    s.nq = 0;
+    s.at = 0;
+  }
+  return s;
+}
+
+// The rows that token i sees: [lo, hi) and [0, sk).  T and cap are at most 2^30, block at most T.
+struct Sees {
+  int lo, hi, sk;
+};
+__device__ __forceinline__ Sees sees(const PagedAttnArgs& a, const Seq& s, int i) {
+  int e = s.nq;
+  if (a.block > 0) e = min(e, (int)(((uint32_t)i / (uint32_t)a.block + 1) * (uint32_t)a.block));
+  e += s.at;
+  Sees v;
+  v.hi = min(e, (int)a.cap);
+  v.lo = a.window > 0 ? min(max(0, e - a.window), v.hi) : 0;
+  v.sk = a.window > 0 ? min(a.sinks, v.hi) : 0;
+  return v;
+}
+
+// Which of the n <= 32 keys from `key` on are seen, as bits.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t seen32(const Sees& v, int key) {
+  return (below(v.hi - key) & ~below(v.lo - key)) | below(v.sk - key);
+}
+
+// The key tiles of kTile rows that tokens ta .. tb (the first and the last of a piece of work) need:
+// tiles [0, s1) and [w0, w1), in this order.  Ends and window starts only grow with the token.
+template <int kTile>
+struct Tiles {
+  Sees first, last;
+  int s1, w0, n;
+  __device__ __forceinline__ void set(const PagedAttnArgs& a, const Seq& s, int ta, int tb) {
+    first = sees(a, s, ta);
+    last = sees(a, s, tb);
+    s1 = (last.sk + kTile - 1) / kTile;
+    w0 = first.lo / kTile;
+    int w1 = (last.hi + kTile - 1) / kTile;
+    if (last.hi <= first.lo) w1 = w0;
+    if (s1 >= w0) {                      // one run of tiles
+      w1 = max(w1, s1);
+      s1 = w0 = 0;
+    }
+    n = s1 + w1 - w0;
+  }
+  // the first row of tile j
+  __device__ __forceinline__ int key(int j) const { return (j < s1 ? j : j - s1 + w0) * kTile; }
+  // rows that some token sees
+  __device__ __forceinline__ bool any(int row) const { return (row >= first.lo && row < last.hi) || row < last.sk; }
+  __device__ __forceinline__ bool any(int from, int to) const {     // of rows [from, to)
+    return (to > first.lo && from < last.hi) || from < last.sk;
+  }
+  // every token sees all the rows of the tile at `key`
+  __device__ __forceinline__ bool all(int key) const {
+    return key + kTile <= first.hi && (key >= last.lo || key + kTile <= first.sk);
+  }
+};
+
+// The page of a table's entry; -1 and FASTAR_DEV_BAD_INDEX for one that is not there.
+__device__ __forceinline__ int page_of(const int32_t* row, int p, int64_t pages, int32_t* status) {
+  const int x = row[p];
+  if (x >= 0 && x < pages) return x;
+  flag_status(status, FASTAR_DEV_BAD_INDEX);
+  return -1;
+}
+
+// The splits of a piece of work's n tiles that are in use, none under min_tiles tiles; tiles j0 .. j1
+// are split s's.
+struct Split {
+  int used, j0, j1;
+};
+__device__ __forceinline__ Split split_of(int n, int s, int splits, int min_tiles) {
+  Split r;
+  r.used = splits > 1 ? max(1, min(splits, n / min_tiles)) : 1;
+  r.j0 = (int)((int64_t)n * s / r.used);
+  r.j1 = s < r.used ? (int)((int64_t)n * (s + 1) / r.used) : r.j0;
+  return r;
+}
+
+}  // namespace paged
+}  // namespace fastar

@@ -1,0 +1,142 @@
+// Softmax attention over a paged cache: the plan (which kernel, how many splits of the keys) and the
+// kernel that joins the splits.
+//
+// The G = Hq / Hkv query heads that share a KV head see the same keys, so the rows of a piece of work
+// are (token, head) pairs, r = t * G + g: the cache is read once for the G heads, and neighbouring rows
+// see nearly the same keys.  With few rows the keys are cut into splits, a block each, whose
+// partials (sum of p v, maximum, sum of p) go to the workspace in fp32 and are joined by a second
+// launch.
+#include <climits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "paged.cuh"
+#include "paged_attn.h"
+#include "tmap.h"
+
+namespace fastar {
+
+namespace {
+
+constexpr int kMaxSplits = 256;
+
+// ---- joining the splits ----------------------------------------------------------------------
+// O = sum_s e^(m_s - m) o_s / sum_s e^(m_s - m) l_s over a row's partials, m = max_s m_s; one warp a
+// row, D / 32 channels a lane.  The partials are summed in the order of the splits, so results do
+// not change from run to run.  A split in which the row sees no key, or that is not in use, has
+// l = 0 and nothing in o; (inf, 0) for the first split says that the output is in place already.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnArgs a) {
+  constexpr int CPL = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);       // (sequence, token, head)
+  pdl_wait();
+  const int64_t per = (int64_t)a.max_q * a.Hq;
+  if (u >= per * a.B) return;
+  const int b = (int)(u / per);
+  const paged::Seq s = paged::sequence(a.cu, a.at, a.B, a.T, a.cap, b, nullptr);
+  const int i = (int)(u - b * per) / a.Hq, head = (int)(u - b * per) - i * a.Hq;
+  if (i >= s.nq) return;
+  const int64_t rows = a.T * a.Hq, row = (int64_t)(s.t0 + i) * a.Hq + head;
+  constexpr int kPer = kMaxSplits / 32;
+  float m = neg_inf(), l = 0.f, o[CPL];
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) o[c] = 0.f;
+  // lane s % 32 reads split s's maximum and sum; then the outputs, eight splits' loads at a time
+  float2 ml[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    ml[k] = make_float2(neg_inf(), 0.f);
+    if (32 * k + lane < a.splits) ml[k] = a.part_ml[(32 * k + lane) * rows + row];
+    if (ml[k].y != 0.f) m = fmaxf(m, ml[k].x);
+  }
+  if (__any_sync(0xffffffffu, lane == 0 && ml[0].x == -neg_inf() && ml[0].y == 0.f)) return;
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  const float ref = m == neg_inf() ? 0.f : m;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (32 * k >= a.splits) break;
+    const float w = ml[k].y != 0.f ? expf(ml[k].x - ref) : 0.f;
+    const int here = a.splits - 32 * k < 32 ? a.splits - 32 * k : 32;
+#pragma unroll 1
+    for (int s0 = 0; s0 < here; s0 += 8) {
+      float p[8][CPL], wt[8], ls[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int src = s0 + x < 32 ? s0 + x : 31;
+        ls[x] = __shfl_sync(0xffffffffu, ml[k].y, src);
+        wt[x] = __shfl_sync(0xffffffffu, w, src);
+        const bool in = s0 + x < here && ls[x] != 0.f;
+        const float* src_o = a.part_o + ((32 * k + s0 + x) * rows + row) * D + lane * CPL;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) p[x][c] = in ? src_o[c] : 0.f;
+        if (!in) wt[x] = ls[x] = 0.f;
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        l = fmaf(wt[x], ls[x], l);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) o[c] = fmaf(wt[x], p[x][c], o[c]);
+      }
+    }
+  }
+  const bool live = l > 0.f || l != l;
+  T* out = static_cast<T*>(a.out) + head * a.o_hs + (s.t0 + i) * a.o_ts + lane * CPL;
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) out[c] = from_f<T>(live ? o[c] / l : 0.f);
+  if (lane == 0 && a.lse) a.lse[head * a.T + s.t0 + i] = live ? m + logf(l) : neg_inf();
+}
+
+template <typename T, int D>
+cudaError_t join_go(const PagedAttnArgs& a, cudaStream_t s) {
+  const int64_t blocks = ((int64_t)a.B * a.max_q * a.Hq + 3) / 4;
+  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = launch_dependent(paged_join_kernel<T, D>, dim3((unsigned)blocks), dim3(128), 0, s, a);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Splits: one CTA a multiprocessor, none under two key tiles of a full cache.
+int splits_simple(int64_t items, int64_t cap) {
+  const int64_t want = sm_count() / items, most = cap / (2 * kSimpleKeys);
+  int64_t s = want < most ? want : most;
+  if (s > kMaxSplits) s = kMaxSplits;
+  return s < 1 ? 1 : (int)s;
+}
+
+size_t split_bytes(int d, int Hq, int64_t T) { return (size_t)T * Hq * (d + 2) * sizeof(float); }
+
+int plan_splits(int d, int Hq, int Hkv, int B, int max_q, int64_t cap) {
+  const int64_t rows = (int64_t)(Hq / Hkv) * max_q;
+  return splits_simple((rows + kSimpleRows - 1) / kSimpleRows * Hkv * B, cap);
+}
+
+}  // namespace
+
+size_t paged_attn_workspace(int d, int Hq, int Hkv, int64_t T, int B, int max_q, int64_t cap) {
+  const int s = plan_splits(d, Hq, Hkv, B, max_q, cap);
+  return s == 1 ? 0 : s * split_bytes(d, Hq, T);
+}
+
+cudaError_t launch_paged_attn(int dtype, int d, PagedAttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s) {
+  a.group = a.Hq / a.Hkv;
+  // keys that a token sees at most
+  int64_t most = a.cap;
+  if (a.window > 0 && (int64_t)a.window + a.sinks < most) most = (int64_t)a.window + a.sinks;
+  a.splits = ws ? plan_splits(d, a.Hq, a.Hkv, a.B, a.max_q, most) : 1;
+  const size_t each = split_bytes(d, a.Hq, a.T);
+  if (a.splits > 1 && ws_bytes / each < (size_t)a.splits) a.splits = (int)(ws_bytes / each);
+  if (a.splits < 1) a.splits = 1;
+  a.min_tiles = 2;
+  if (a.splits > 1) {
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * a.T * a.Hq * d);
+  }
+  const cudaError_t e = launch_paged_attn_simple(dtype, d, a, s);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  if (dtype == FASTAR_F32) return d == 128 ? join_go<float, 128>(a, s) : join_go<float, 64>(a, s);
+  return d == 128 ? join_go<__nv_bfloat16, 128>(a, s) : join_go<__nv_bfloat16, 64>(a, s);
+}
+
+}  // namespace fastar

@@ -1,0 +1,11 @@
+// The kernels of the attention over a paged cache, between the plan and the kernels' files.
+#pragma once
+
+#include "kernels.h"
+
+namespace fastar {
+
+constexpr int kSimpleRows = 32, kSimpleKeys = 64;
+cudaError_t launch_paged_attn_simple(int dtype, int d, const PagedAttnArgs& a, cudaStream_t s);
+
+}  // namespace fastar

@@ -9,18 +9,12 @@
 // lane holds the same channels of every head, so a token's rotations are formed once for all its
 // rows (two pairs a lane, passed round by shuffles), and multiplied with the weights: a pair is
 // then r (A v0 - B v1), r (C v0 + D v1) with r = 1 / |row|'s root mean square.
-//
-// Angles: the step theta^(-2j/width) / 2 pi, in turns, is a 64-bit binary fraction (formed on
-// the host in double), and position * step is taken modulo one turn by the wrap-around of
-// the 64-bit product.  So a far position costs no accuracy: the top 32 bits of the turn go to fp32,
-// which rounds them by 2^-26 turns at the most wherever the token is (2^24 positions away the
-// step's own error adds some 2^-30), where the fp32 product pos * step loses a bit of the angle with every
-// doubling of the position; no 64-bit float arithmetic runs on the device.
+// Angles: rope.cuh.
 #include <climits>
-#include <cmath>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "rope.cuh"
 #include "tmap.h"
 
 namespace fastar {
@@ -28,11 +22,6 @@ namespace fastar {
 namespace {
 
 constexpr int kWarpsR = 4;
-
-struct RopeTable {
-  uint64_t step[64];   // turns per position as a fraction of 2^64, one per pair
-  uint8_t axis[64];    // 0 frame, 1 row, 2 column, 3: the pair does not turn
-};
 
 struct RopeDev {
   int Hq, Hk;
@@ -48,45 +37,6 @@ struct RopeDev {
   int gh, gw;
   int part_shift;          // log2 of the warps per token
 };
-
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) {
-  uint4 u;
-  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-    w[e] = *reinterpret_cast<uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = u;
-}
-__device__ __forceinline__ void store8(float* p, const float* f) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-
-// 16 channels of a row as they lie in memory, and as fp32.
-template <typename T>
-struct Raw {
-  uint4 u[sizeof(T)];
-};
-__device__ __forceinline__ void expand(const Raw<__nv_bfloat16>& r, float* f) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t w[4] = {r.u[i].x, r.u[i].y, r.u[i].z, r.u[i].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
-      f[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
-  }
-}
-__device__ __forceinline__ void expand(const Raw<float>& r, float* f) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[4 * i] = __uint_as_float(r.u[i].x), f[4 * i + 1] = __uint_as_float(r.u[i].y);
-    f[4 * i + 2] = __uint_as_float(r.u[i].z), f[4 * i + 3] = __uint_as_float(r.u[i].w);
-  }
-}
 
 // Inputs and outputs may be the same tensor: every lane reads its channels before it writes
 // them and no other lane does.  kAll: every pair turns.
@@ -139,9 +89,7 @@ __global__ void __launch_bounds__(kWarpsR * 32)
       }
       auto one = [&](int j, float& sn, float& cs) {
         const int ax = axes[j];
-        const int p = ax == 0 ? p3[0] : ax == 1 ? p3[1] : p3[2];
-        const uint64_t turn = (uint64_t)(int64_t)p * steps[j];       // modulo one turn
-        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn, &cs);
+        rope_turn(ax == 0 ? p3[0] : ax == 1 ? p3[1] : p3[2], steps[j], sn, cs);
       };
       if (D == 128) {
         one(2 * lane, sn0, cs0);
@@ -192,27 +140,8 @@ __global__ void __launch_bounds__(kWarpsR * 32)
         float f[16];
         expand(v[i], f);
         if (kAhead > 1) load(v[i], x + kAhead * (int)parts);
-        float r = 1.f;
-        if (norm) {
-          float q0 = 0.f, q1 = 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) q0 = fmaf(f[e], f[e], q0), q1 = fmaf(f[e + 1], f[e + 1], q1);
-          float q = q0 + q1;
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-          // 1 / sqrt to an ulp: the approximate one and a Newton step
-          const float z = q * (1.0f / D) + a.eps, y0 = rsqrtf(z);
-          // (of an infinite sum of squares 0, not 0 * infinity; of a NaN, NaN in the whole row)
-          r = y0 == 0.f ? 0.f : y0 * fmaf(-0.5f * z * y0, y0, 1.5f);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float a0 = f[2 * e], a1 = f[2 * e + 1];
-          // a pair that does not turn is not multiplied by (1, 0): its neighbour may be infinite
-          const bool turns = kAll || axes[li * 8 + e] < 3;
-          f[2 * e] = (turns ? A[e] * a0 - B[e] * a1 : A[e] * a0) * r;
-          f[2 * e + 1] = (turns ? C[e] * a0 + E[e] * a1 : E[e] * a1) * r;
-        }
+        const float r = norm ? rms_scale<D>(f, a.eps) : 1.f;
+        turn16<kAll>(f, A, B, C, E, r, axes + li * 8);
         const int h = (isk ? x - gq : x) * RW + sub;
         if (h < (isk ? a.Hk : a.Hq)) {
           T* p = (isk ? static_cast<T*>(a.ko) + h * a.ko_hs + (int64_t)tok * a.ko_ts
@@ -255,22 +184,8 @@ cudaError_t launch_qk_norm_rope(int dtype, int d, int64_t n, int Hq, TokView q, 
                                 int Hk, TokView k, void* ko, int64_t ko_hs, int64_t ko_ts, const float* wq,
                                 const float* wk, float eps, const int* axes, const int32_t* pos, int t0,
                                 const int32_t* t0_dev, int gh, int gw, float theta, cudaStream_t s) {
-  RopeTable tab;
-  int j = 0;
-  for (int a = 0; a < 3; ++a) {
-    // the steps of an axis as a geometric sequence: at most 63 products, which add 2^-46 to the relative error
-    const double ratio = axes[a] > 0 ? std::pow((double)theta, -2.0 / axes[a]) : 1.0;
-    double f = 0.15915494309189535;   // 1 / 2 pi turns
-    for (int i = 0; i < axes[a] / 2; ++i, ++j, f *= ratio) {
-      tab.step[j] = (uint64_t)(f * 18446744073709551616.0);
-      tab.axis[j] = (uint8_t)a;
-    }
-  }
-  const bool all = 2 * j == d;
-  for (; j < 64; ++j) {
-    tab.step[j] = 0;
-    tab.axis[j] = 3;
-  }
+  bool all;
+  const RopeTable tab = rope_table(d, axes, theta, &all);
   RopeDev a{};
   a.Hq = Hq, a.Hk = Hk, a.n = n;
   a.q = q.p, a.q_hs = q.hs, a.q_ts = q.ts;

@@ -1,0 +1,503 @@
+"""GPU parity of the paged cache (fastar_paged_append, fastar_paged_attn) against its float64 oracle.
+
+Appended rows: v is moved bit for bit; k and q_out within half a rounding of the type (2^-8, 2^-24 of the
+value) plus the fp32 arithmetic before it, 2^-19 of the pair's magnitudes (as the norm and rotation
+alone, test_gpu_qk_rope.py).
+
+Attention, from the oracle's own quantities: A = sum_j p_j |v_j| (the mean of |v| under the
+softmax), E = the largest sum_c |q_c k_c| * scale of a row, n the rows it sees:
+  - a logit is d products summed in fp32, 2 d 2^-24 E at most, then one product; e^x adds 2^-22 and
+    the argument's own rounding 2^-23 E; so every p is off by e = (d 2^-23 + 2^-22) E + 2^-22 relative
+    (for e < 1/16: doubled covers e^e - 1), and the quotient of two such sums by 2 e;
+  - bf16 calls hold p in bf16: 2^-8 relative, at every magnitude (bf16 has fp32's exponents);
+  - an exponential under fp32's range is 0: 2^-100 sum_j |v_j| covers it;
+  - sums over n keys in fp32: n 2^-23 relative at most, the tensor cores' additions truncate: doubled;
+  - the output's rounding: 2^-8 |O| in bf16, 2^-24 |O| in fp32.
+  |O - want| <= half |want| + A (4 e + n 2^-22 + [bf16] 2^-8) + 2^-100 n max |v|
+  |lse - want| <= 2 e + n 2^-22 + 2^-22 (1 + |want|)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from kv_cache_tempcache_gb300 import _lib as L
+from oracle import paged_oracle as P
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+DEV = "cuda"
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def _rand(shape, seed, std=1.0):
+    return torch.randn(*shape, generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV) * std
+
+
+def pool_like(pages, H, page, d, dt, layout, fill):
+    """[pages, H, page, d], stored so or as [pages, page, H, d]."""
+    if layout == "hnd":
+        return torch.full((pages, H, page, d), fill, dtype=dt, device=DEV)
+    return torch.full((pages, page, H, d), fill, dtype=dt, device=DEV).transpose(1, 2)
+
+
+def tables(need, page, width, seed, spare=2):
+    """A table of pages dealt out at random, -1 where none is needed; and the number of pages."""
+    rng = np.random.default_rng(seed)
+    table = np.full((len(need), width), -1, np.int32)
+    n = sum(len(p) for p in need)
+    ids = rng.permutation(n + spare)[:n]
+    at = 0
+    for b, p in enumerate(need):
+        table[b, list(p)] = ids[at:at + len(p)]
+        at += len(p)
+    return table, n + spare
+
+
+# ---- append ------------------------------------------------------------------------------------
+
+def run_append(dtype, nq, at, Hq, Hk, d, page, layout, norm, axes, grid, pos, use_cu=True, tail=0, width=None, seed=0,
+               in_place=False, theta=1e4):
+    dt, B, T = DT[dtype], len(nq), sum(nq) + tail
+    width = width or max(-(-(a + n) // page) for a, n in zip(at, nq))
+    table, pages = tables([range(min(width, -(-(a + n) // page))) for a, n in zip(at, nq)], page, width, seed)
+    qkv = _rand((T, Hq + 2 * Hk, d), seed + 1, 2.0).to(dt)
+    before = qkv.clone()
+    q, k, v = (x.transpose(0, 1) for x in qkv.split((Hq, Hk, Hk), 1))
+    kp, vp = pool_like(pages, Hk, page, d, dt, layout, 3.0), pool_like(pages, Hk, page, d, dt, layout, 5.0)
+    wq, wk = (1 + 0.1 * _rand((d,), seed + 2), 1 + 0.1 * _rand((d,), seed + 3)) if norm else (None, None)
+    p3 = np.random.default_rng(seed).integers(-50000, 50000, (T, 3)).astype(np.int32) if pos else None
+    cu = np.concatenate(([0], np.cumsum(nq))) if use_cu else None
+    len_out, status = _i32([-7] * B), _i32([0])
+    qo = q if in_place else torch.full((Hq, T, d), 7.0, dtype=dt, device=DEV) if Hq else None
+    want = P.append(_np(k), _np(v), _np(kp), _np(vp), table, at, cu, _np(q) if Hq else None,
+                    None if wq is None else _np(wq), None if wk is None else _np(wk), 1e-6, axes, p3, grid, theta)
+    L.fastar_paged_append(k, v, kp, vp, _i32(table), _i32(at), len_out, q=q if Hq else None, q_out=qo,
+                          cu=None if cu is None else _i32(cu), wq=wq, wk=wk, eps=1e-6, axes=axes,
+                          pos=None if p3 is None else torch.from_numpy(p3).cuda(), grid=grid, theta=theta,
+                          dev_status=status)
+    torch.cuda.synchronize()
+    wk_, wv, wq_, done, lens, k_pair, q_pair = want
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    assert np.array_equal(_np(vp), wv)
+    assert (np.abs(_np(kp) - wk_) <= half * np.abs(wk_) * (k_pair > 0) + 2.0 ** -19 * k_pair).all()
+    if Hq:
+        got = _np(qo)[:, done]
+        assert (np.abs(got - wq_[:, done]) <= half * np.abs(wq_[:, done]) + 2.0 ** -19 * q_pair[:, done]).all()
+        rest = qo[:, torch.from_numpy(~done).cuda()]
+        assert torch.equal(rest, before.transpose(0, 1)[:Hq, torch.from_numpy(~done).cuda()]) if in_place \
+            else bool((rest == 7.0).all())
+    if not in_place:
+        assert torch.equal(qkv, before)
+    assert np.array_equal(len_out.cpu().numpy(), lens)
+    return int(status.item())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq,at,Hq,Hk,d,page,layout,norm,axes,grid,pos", [
+    ([1], [0], 1, 1, 64, 16, "hnd", True, (64, 0, 0), (1, 1), False),
+    ([1], [333], 12, 12, 128, 64, "hnd", True, (44, 42, 42), (6, 13), False),
+    ([1] * 8, [0, 15, 16, 17, 100, 3, 64, 1000], 12, 3, 128, 16, "nhd", True, (128, 0, 0), (1, 1), False),
+    ([5, 1, 0, 33, 130], [7, 0, 12, 127, 128], 10, 5, 64, 32, "nhd", False, (24, 16, 16), (3, 4), True),
+    ([331], [69], 3, 2, 128, 128, "hnd", True, (16, 56, 56), (5, 7), False),
+    ([300, 21], [1, 640], 0, 4, 64, 64, "hnd", True, (24, 20, 20), (5, 7), False),
+    ([1560, 1560], [14040, 3], 12, 12, 128, 64, "nhd", True, (44, 42, 42), (30, 52), False),
+    ([7, 9], [2, 3], 2, 1, 64, 16, "hnd", False, (0, 0, 0), (1, 1), False)])
+def test_append(dtype, nq, at, Hq, Hk, d, page, layout, norm, axes, grid, pos):
+    assert run_append(dtype, nq, at, Hq, Hk, d, page, layout, norm, axes, grid, pos, tail=3) == 0
+
+
+def test_append_without_starts_and_in_place():
+    assert run_append("bf16", [40, 40, 40], [5, 0, 31], 4, 2, 128, 32, "hnd", True, (44, 42, 42), (3, 5), False,
+                      use_cu=False) == 0
+    assert run_append("bf16", [37], [5], 4, 2, 128, 32, "nhd", True, (44, 42, 42), (3, 5), False, in_place=True) == 0
+    assert run_append("f32", [37, 90], [5, 8], 4, 2, 64, 32, "nhd", True, (24, 20, 20), (3, 5), False, in_place=True,
+                      tail=2) == 0
+
+
+def test_append_many_sequences_and_other_theta():
+    rng = np.random.default_rng(0)
+    nq = rng.integers(0, 4, 131).tolist()
+    at = rng.integers(0, 200, 131).tolist()
+    assert run_append("bf16", nq, at, 2, 1, 128, 16, "hnd", True, (128, 0, 0), (1, 1), False, theta=500.0) == 0
+
+
+def test_append_past_the_pages_drops_rows():
+    # 4 pages of 16 a sequence: the first is full before the call, the second fills up in it
+    st = run_append("bf16", [3, 20, 5], [64, 50, 0], 2, 2, 64, 16, "hnd", True, (64, 0, 0), (1, 1), False, width=4)
+    assert st == L.DEV_BAD_LEN
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_skips_what_makes_no_sense(dtype):
+    dt, d, H, page = DT[dtype], 64, 2, 16
+    T = 12
+    k, v, q = _rand((H, T, d), 1).to(dt), _rand((H, T, d), 2).to(dt), _rand((H, T, d), 3).to(dt)
+    table = _i32([[0, 1], [2, 99], [3, 4], [5, -3]])
+    at = _i32([-1, 14, 33, 20])
+    kp, vp = pool_like(6, H, page, d, dt, "hnd", 3.0), pool_like(6, H, page, d, dt, "hnd", 5.0)
+    qo, ln, st = torch.full_like(q, 7.0), _i32([9, 9, 9, 9]), _i32([0])
+    L.fastar_paged_append(k, v, kp, vp, table, at, ln, q=q, q_out=qo, dev_status=st)
+    torch.cuda.synchronize()
+    assert st.item() == L.DEV_BAD_LEN | L.DEV_BAD_INDEX
+    assert ln.tolist() == [0, 17, 0, 23]
+    # sequence 1: rows 14, 15 go to page 2, row 16 to page 99 that is not there; 3: rows 20.. to page -3
+    assert torch.equal(kp[2, :, 14:], k[:, 3:5]) and torch.equal(vp[2, :, 14:], v[:, 3:5])
+    kp[2, :, 14:], vp[2, :, 14:] = 3.0, 5.0
+    assert bool((kp == 3.0).all()) and bool((vp == 5.0).all())
+    assert bool((qo[:, 0:3] == 7.0).all()) and bool((qo[:, 6:9] == 7.0).all())
+    assert torch.equal(qo[:, 3:6], q[:, 3:6]) and torch.equal(qo[:, 9:], q[:, 9:])
+    # starts that fall or leave the call's tokens
+    for cu in ([0, 3, 2, 5, 12], [-1, 3, 6, 9, 12], [0, 3, 6, 9, 13]):
+        kp.fill_(3.0)
+        st.zero_()
+        L.fastar_paged_append(k, v, kp, vp, table, _i32([0, 0, 0, 0]), ln, cu=_i32(cu), dev_status=st)
+        torch.cuda.synchronize()
+        assert st.item() & L.DEV_BAD_LEN
+
+
+# ---- attention ---------------------------------------------------------------------------------
+
+def attn_case(dtype, nq, at, Hk, G, d, page, layout, block, window, sinks, seed=0, use_cu=True, tail=0, garbage=None,
+              width=0, spare_rows=True):
+    """The tensors of a call: pages that no token sees have no entry, rows that none sees hold
+    `garbage`."""
+    dt, B, T = DT[dtype], len(nq), sum(nq) + tail
+    width = max(width, max(max(1, -(-(a + n) // page)) for a, n in zip(at, nq)))
+    used = []
+    for a, n in zip(at, nq):
+        m = min(a + n, width * page)
+        see = P.sees(n, a, m, block, window, sinks).any(0) if n else np.zeros(m, bool)
+        used.append(np.flatnonzero(see))
+    # needed: pages with a row between the first and the last of the window, or a sink
+    need = [sorted(set((u // page).tolist())) for u in used]
+    table, pages = tables(need, page, width, seed)
+    g = float("nan") if garbage is None else garbage
+    kp, vp = pool_like(pages, Hk, page, d, dt, layout, g), pool_like(pages, Hk, page, d, dt, layout, g)
+    for b, u in enumerate(used):
+        if len(u):
+            x = _rand((2, len(u), Hk, d), seed + 10 + b).to(dt)
+            pg, of = torch.from_numpy(table[b, u // page]).long().cuda(), torch.from_numpy(u % page).cuda()
+            kp[pg, :, of], vp[pg, :, of] = x[0], x[1]
+    q = _rand((T, Hk * G, d), seed + 1, 1.5).to(dt).transpose(0, 1)
+    cu = np.concatenate(([0], np.cumsum(nq))) if use_cu else None
+    return q, kp, vp, table, np.array(at), cu
+
+
+def run_attn(q, kp, vp, table, at, cu, scale, block, window, sinks, max_q=None, ws=True, status=0, bits=-1):
+    Hq, T, d = q.shape
+    out = torch.full((T, Hq, d), 7.0, dtype=q.dtype, device=DEV).transpose(0, 1)
+    lse = torch.full((Hq, T), 7.0, device=DEV)
+    B, Hk, page = table.shape[0], kp.shape[1], kp.shape[2]
+    mq = max_q or (int(np.diff(cu).max()) if cu is not None else T // B)
+    nb = L.workspace_bytes(L.OP_PAGED_ATTN, Hq, T, table.shape[1] * page, d, Hk, r=mq, P=B)
+    if isinstance(ws, int) and not isinstance(ws, bool):
+        nb = min(nb, ws)
+    w = torch.full((nb,), 0xA5, dtype=torch.uint8, device=DEV) if nb and ws else None
+    st = _i32([0])
+    L.fastar_paged_attn(q, kp, vp, _i32(table), _i32(at), scale, out, lse, cu=None if cu is None else _i32(cu),
+                        max_q=mq, block=block, window=window, sinks=sinks, dev_status=st, workspace=w)
+    torch.cuda.synchronize()
+    assert int(st.item()) & bits == status
+    return out, lse
+
+
+def check_attn(dtype, q, kp, vp, table, at, cu, scale, block, window, sinks, out, lse):
+    want, wl, A, E, n = P.attention(_np(q), _np(kp), _np(vp), table, at, scale, cu, block, window, sinks)
+    d = q.shape[2]
+    bf = dtype == "bf16"
+    e = (d * 2.0 ** -23 + 2.0 ** -22) * E + 2.0 ** -22
+    assert e.max() < 1 / 16
+    big = np.nan_to_num(np.abs(_np(vp)), nan=0.0).max()
+    tol = (2.0 ** -8 if bf else 2.0 ** -24) * np.abs(want) + n[None, :, None] * 2.0 ** -100 * big
+    tol += A * (4 * e + n * 2.0 ** -22 + (2.0 ** -8 if bf else 0))[..., None]
+    mine = n >= 0
+    got, gl = _np(out), _np(lse)
+    assert (np.abs(got - want) <= tol)[:, mine].all(), np.nanmax((np.abs(got - want) / (tol + 1e-300))[:, mine])
+    live = mine & (n > 0)
+    assert np.isneginf(gl[:, mine & (n == 0)]).all()
+    assert (np.abs(gl - wl) <= 2 * e + n * 2.0 ** -22 + 2.0 ** -22 * (1 + np.abs(wl)))[:, live].all()
+    assert (got[:, ~mine] == 7.0).all() and (gl[:, ~mine] == 7.0).all()       # tokens of no sequence
+
+
+MASKS = [(0, 0, 0), (1, 0, 0), (1, 64, 4), (1, 1, 0), (0, 100, 37), (16, 33, 16), (1, 16, 1000), (1000, 5, 0)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("block,window,sinks", MASKS)
+@pytest.mark.parametrize("nq,at,Hk,G,d,page,layout", [
+    ([1], [0], 1, 1, 64, 16, "hnd"), ([1], [332], 12, 1, 128, 64, "hnd"),
+    ([1] * 5, [0, 1, 130, 777, 2000], 2, 4, 128, 16, "nhd"), ([4, 0, 7, 1], [900, 3, 0, 128], 2, 4, 64, 32, "nhd"),
+    ([33, 1, 130], [7, 500, 128], 2, 2, 128, 32, "hnd"), ([257], [1000], 3, 1, 64, 128, "nhd"),
+    ([300, 129], [0, 640], 1, 3, 128, 64, "nhd")])
+def test_attention(dtype, block, window, sinks, nq, at, Hk, G, d, page, layout):
+    c = attn_case(dtype, nq, at, Hk, G, d, page, layout, block, window, sinks, seed=len(nq) + at[0], tail=2)
+    scale = 1 / math.sqrt(d)
+    out, lse = run_attn(*c, scale, block, window, sinks)
+    check_attn(dtype, *c, scale, block, window, sinks, out, lse)
+
+
+@pytest.mark.parametrize("dtype,nq,at,Hk,G,d,page,block,window,sinks", [
+    ("bf16", [1], [40000], 2, 4, 128, 64, 1, 0, 0), ("bf16", [1, 1, 1], [40000, 13, 9000], 1, 8, 64, 16, 1, 8191, 100),
+    ("bf16", [9], [20000], 1, 2, 128, 32, 1, 0, 0), ("bf16", [70], [30000], 1, 1, 128, 128, 1, 15000, 300),
+    ("bf16", [600, 40], [12000, 3000], 2, 1, 128, 64, 0, 5000, 1500), ("f32", [3, 1], [20000, 5], 2, 4, 64, 16, 1, 0, 0),
+    ("bf16", [700], [5000], 2, 1, 64, 32, 200, 3000, 100), ("f32", [40], [9000], 1, 2, 128, 32, 1, 4000, 7)])
+@pytest.mark.parametrize("ws", [True, False, 100000])
+def test_attention_over_long_sequences(dtype, nq, at, Hk, G, d, page, block, window, sinks, ws):
+    c = attn_case(dtype, nq, at, Hk, G, d, page, "hnd", block, window, sinks, seed=5)
+    scale = 1 / math.sqrt(d)
+    out, lse = run_attn(*c, scale, block, window, sinks, ws=ws)
+    check_attn(dtype, *c, scale, block, window, sinks, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [1, 5, 40, 300])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
+def test_what_a_token_does_not_see_cannot_reach_it(dtype, nq, what):
+    """K and V of single rows that some tokens see and others do not: causal tokens, a window, sinks."""
+    d, page, Hk, G, at, block, window, sinks = 64, 16, 2, 2, 600, 1, 150, 20
+    q, kp, vp, table, a, cu = attn_case(dtype, [nq], [at], Hk, G, d, page, "hnd", block, window, sinks, seed=nq)
+    scale = 1 / math.sqrt(d)
+    clean = run_attn(q, kp, vp, table, a, cu, scale, block, window, sinks)
+    see = P.sees(nq, at, at + nq, block, window, sinks)
+    for row in sorted({at + nq - 1, at + nq // 2, at - window + 1, at + nq - window, 19}):
+        if not see[:, row].any():
+            continue
+        for pool, ch in ((vp, 3), (vp, slice(0, d)), (kp, 5)):
+            pg, of = int(table[0, row // page]), row % page
+            keep = pool[pg, 1, of].clone()
+            pool[pg, 1, of, ch] = what
+            out, lse = run_attn(q, kp, vp, table, a, cu, scale, block, window, sinks)
+            pool[pg, 1, of] = keep
+            rows = torch.from_numpy(see[:, row]).cuda()
+            # tokens that do not see it, and the other KV head's, are as before, bit for bit
+            assert torch.equal(out[:G], clean[0][:G]) and torch.equal(lse[:G], clean[1][:G])
+            assert torch.equal(out[G:, ~rows], clean[0][G:, ~rows]) and torch.equal(lse[G:, ~rows], clean[1][G:, ~rows])
+            if pool is vp:
+                assert not bool(torch.isfinite(out[G:, rows][..., ch]).any())
+                if ch == 3:
+                    other = [c for c in range(d) if c != 3]
+                    assert torch.equal(out[G:, rows][..., other], clean[0][G:, rows][..., other])
+            elif what != what:
+                assert bool(torch.isnan(out[G:, rows]).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [1, 3, 30, 200])
+def test_a_query_that_is_not_finite_stays_alone(dtype, nq):
+    d, Hk, G = 128, 1, 2
+    c = attn_case(dtype, [nq], [700], Hk, G, d, 32, "hnd", 1, 300, 10, seed=9)
+    clean = run_attn(*c, 0.1, 1, 300, 10)
+    c[0][1, nq // 2, 7] = float("nan")
+    out, lse = run_attn(*c, 0.1, 1, 300, 10)
+    assert bool(torch.isnan(out[1, nq // 2]).all())
+    keep = torch.ones(2, nq, dtype=torch.bool, device=DEV)
+    keep[1, nq // 2] = False
+    assert torch.equal(out[keep], clean[0][keep]) and torch.equal(lse[keep], clean[1][keep])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [1, 40, 300])
+def test_large_and_lopsided_logits(dtype, nq):
+    """Logits of hundreds and rows of keys that rise, fall, or lie 30 below one strong key whose V is 0."""
+    d, page, n = 64, 16, 1000
+    q, kp, vp, table, a, cu = attn_case(dtype, [nq], [n - nq], 1, 1, d, page, "hnd", 0, 0, 0, seed=2)
+    row = torch.arange(n, device=DEV)
+    pg, of = torch.from_numpy(table[0]).long().cuda()[row // page], row % page
+    for shape in (row * 0.5, -row * 0.5, torch.where(row == 17, 30.0, 0.0)):
+        kp[pg, :, of] = 0
+        kp[pg, 0, of, 0] = shape.to(kp.dtype)
+        if float(shape.max()) == 30.0:
+            vp[pg[17], :, of[17]] = 0
+        q[...] = 0
+        q[:, :, 0] = 1.0
+        out, lse = run_attn(q, kp, vp, table, a, cu, 1.0, 0, 0, 0)
+        check_attn(dtype, q, kp, vp, table, a, cu, 1.0, 0, 0, 0, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_flags_what_makes_no_sense(dtype, nq):
+    d, B = 64, 3
+    c = attn_case(dtype, [nq] * B, [100, 50, 30], 1, 2, d, 16, "hnd", 1, 0, 0, seed=3)
+    q, kp, vp, table, at, cu = c
+    clean = run_attn(*c, 0.1, 1, 0, 0)
+    # a start outside the pages: the sequence is skipped
+    for bad in (-1, table.shape[1] * 16 + 1):
+        at2 = at.copy()
+        at2[1] = bad
+        out, lse = run_attn(q, kp, vp, table, at2, cu, 0.1, 1, 0, 0, status=L.DEV_BAD_LEN)
+        assert bool((out[:, nq:2 * nq] == 7.0).all()) and bool((lse[:, nq:2 * nq] == 7.0).all())
+        for s in (slice(0, nq), slice(2 * nq, 3 * nq)):
+            assert torch.equal(out[:, s], clean[0][:, s]) and torch.equal(lse[:, s], clean[1][:, s])
+    # a page that is not there: its rows count as zeros
+    for bad in (-1, kp.shape[0], 2 ** 31 - 1, -2 ** 31):
+        t2, was = table.copy(), table[0, 2]
+        t2[0, 2] = bad
+        out, lse = run_attn(q, kp, vp, t2, at, cu, 0.1, 1, 0, 0, status=L.DEV_BAD_INDEX)
+        kz, vz = kp.clone(), vp.clone()
+        kz[was], vz[was] = 0, 0
+        check_attn(dtype, q, kz, vz, table, at, cu, 0.1, 1, 0, 0, out, lse)
+    # more tokens than max_q: the first are done
+    if nq > 1:
+        out, lse = run_attn(*c, 0.1, 1, 0, 0, max_q=nq - 3, status=L.DEV_BAD_LEN)
+        for b in range(B):
+            s, r = slice(b * nq, b * nq + nq - 3), slice(b * nq + nq - 3, (b + 1) * nq)
+            assert torch.allclose(out[:, s].float(), clean[0][:, s].float(), rtol=2e-2, atol=2e-2)
+            assert bool((out[:, r] == 7.0).all()) and bool((lse[:, r] == 7.0).all())
+    # starts that fall or leave the call's tokens
+    for cu2 in ([0, nq, nq - 1, 3 * nq], [-1, nq, 2 * nq, 3 * nq], [0, nq, 2 * nq, 3 * nq + 1]):
+        # (a sequence that is left may have become longer than its pages)
+        run_attn(q, kp, vp, table, at, np.array(cu2), 0.1, 1, 0, 0, max_q=3 * nq, status=L.DEV_BAD_LEN, bits=L.DEV_BAD_LEN)
+
+
+def test_more_rows_than_the_pages_hold():
+    """Tokens whose rows were dropped see what is there."""
+    for nq, at, block, window in ((30, 50, 1, 0), (30, 50, 0, 20), (5, 64, 1, 10), (30, 50, 7, 16)):
+        c = attn_case("bf16", [nq], [at], 2, 1, 64, 16, "hnd", block, 0, 0, seed=4)
+        q, kp, vp, table, a, cu = c
+        table = np.ascontiguousarray(table[:, :4])
+        out, lse = run_attn(q, kp, vp, table, a, cu, 0.1, block, window, 0)
+        check_attn("bf16", q, kp, vp, table, a, cu, 0.1, block, window, 0, out, lse)
+
+
+@pytest.mark.parametrize("nq", [1, 20, 200])
+def test_offsets_past_32_bits(nq):
+    """A pool of 2^32 elements and more: pages at its far end, [pages, page, H, d] with H that counts."""
+    d, page, Hk, B = 128, 64, 8, 2
+    pages = 2 ** 32 // (page * Hk * d) + 40
+    kp = torch.empty(pages, page, Hk, d, dtype=torch.bfloat16, device=DEV).transpose(1, 2)
+    vp = torch.empty(pages, page, Hk, d, dtype=torch.bfloat16, device=DEV).transpose(1, 2)
+    at = np.array([500, 0])
+    table = (pages - 1 - np.arange(B * 12).reshape(B, 12)).astype(np.int32)
+    x = _rand((2, Hk, 500, d), 1).bfloat16()
+    L.fastar_paged_append(x[0], x[1], kp, vp, _i32(table[:1]), _i32([0]))
+    y = _rand((3, Hk, B * nq, d), 2).bfloat16()
+    L.fastar_paged_append(y[0], y[1], kp, vp, _i32(table), _i32(at))
+    out, lse = run_attn(y[2], kp, vp, table, at, None, 0.1, 1, 0, 0)
+    lo = int(table.min())
+    check_attn("bf16", y[2], kp[lo:], vp[lo:], table - lo, at, None, 0.1, 1, 0, 0, out, lse)
+
+
+# ---- both together --------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_rollout_through_both_calls(dtype):
+    """Chunks and single tokens of three sequences, appended and attended over, with pages handed back as
+    they leave the window; positions turn with the row."""
+    dt, B, Hk, G, d, page, window, sinks = DT[dtype], 3, 2, 2, 64, 16, 70, 20
+    width, pages = 40, 40
+    kp, vp = (pool_like(pages, Hk, page, d, dt, "nhd", float("nan")) for _ in range(2))
+    table = np.full((B, width), -1, np.int32)
+    free = list(range(pages))
+    at, len_out, status = np.zeros(B, np.int64), _i32([0] * B), _i32([0])
+    wq, wk = 1 + 0.1 * _rand((d,), 2), 1 + 0.1 * _rand((d,), 3)
+    rows = [([], []) for _ in range(B)]
+    rng = np.random.default_rng(0)
+    for step in range(12):
+        nq = [[30, 1, 45], [1, 1, 1], [0, 5, 33], [2, 17, 0]][step % 4]
+        T = sum(nq)
+        for b in range(B):
+            first = max(0, at[b] + 1 - window) if nq[b] else 0
+            for p in range(-(-sinks // page), first // page if nq[b] else 0):
+                if table[b, p] >= 0:                       # no later token sees it
+                    kp[table[b, p]], vp[table[b, p]] = float("nan"), float("nan")
+                    free.append(int(table[b, p]))
+                    table[b, p] = -1
+            for p in range(at[b] // page, -(-(at[b] + nq[b]) // page)):
+                if table[b, p] < 0:
+                    table[b, p] = free.pop(int(rng.integers(len(free))))
+        qkv = _rand((T, (G + 2) * Hk, d), 100 + step).to(dt)
+        q, k, v = (x.transpose(0, 1) for x in qkv.split((G * Hk, Hk, Hk), 1))
+        cu = np.concatenate(([0], np.cumsum(nq)))
+        before = _np(q), _np(k), _np(v)
+        L.fastar_paged_append(k, v, kp, vp, _i32(table), _i32(at), len_out, q=q, q_out=q, cu=_i32(cu), wq=wq, wk=wk,
+                              axes=(24, 20, 20), grid=(3, 4), dev_status=status)
+        out, lse = run_attn(q, kp, vp, table, at, cu, 0.125, 1, window, sinks)
+        check_attn(dtype, q, kp, vp, table, at, cu, 0.125, 1, window, sinks, out, lse)
+        for b in range(B):
+            sl = slice(cu[b], cu[b + 1])
+            p = P.positions(int(at[b]), nq[b], (3, 4))
+            if nq[b] == 0:
+                continue
+            rows[b][0].append(P.K.norm_rope(before[1][:, sl], _np(wk), 1e-6, (24, 20, 20), p, 1e4)[0])
+            rows[b][1].append(before[2][:, sl])
+            # against the whole history in 64 bits, rounded once where the cache is
+            kk, vv = np.concatenate(rows[b][0], 1), np.concatenate(rows[b][1], 1)
+            qq = P.K.norm_rope(before[0][:, sl], _np(wq), 1e-6, (24, 20, 20), p, 1e4)[0]
+            one = np.zeros((1, 1), np.int32)
+            w, _, A, _, _ = P.attention(qq, kk[None], vv[None], one, at[b:b + 1], 0.125, None, 1, window, sinks)
+            # a normed row has |x| <= 1.5 sqrt(d) (weights up to 1.5): q and k rounded to the type (and to 2^-19 of a
+            # pair before) move a logit by 2 half |q| |k| scale <= 2 half * 2.25 d * 0.125 = 36 half, and every p
+            # by e^72 half - 1 < 80 half, twice for the quotient; then p, the values and the output rounded
+            half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -18
+            assert (np.abs(_np(out)[:, sl] - w) <= half * np.abs(w) + A * 162 * half).all()
+        at += np.array(nq)
+        assert np.array_equal(len_out.cpu().numpy(), at) and status.item() == 0
+
+
+@pytest.mark.parametrize("nq,G", [(1, 1), (3, 4), (150, 2)])
+def test_captured_calls_follow_the_device_and_repeat_bit_for_bit(nq, G):
+    d, page, Hk, B, width = 128, 32, 2, 2, 40
+    kp, vp = (pool_like(B * width, Hk, page, d, torch.bfloat16, "hnd", 0.0) for _ in range(2))
+    kp.copy_(_rand(kp.shape, 1)), vp.copy_(_rand(vp.shape, 2))
+    table = _i32(np.random.default_rng(0).permutation(B * width).reshape(B, width))
+    qkv = _rand((B * nq, (G + 2) * Hk, d), 3).bfloat16()
+    q, k, v = (x.transpose(0, 1) for x in qkv.split((G * Hk, Hk, Hk), 1))
+    qo, out = torch.empty_like(q), torch.empty_like(q)
+    lse, at, ln, st = torch.empty(G * Hk, B * nq, device=DEV), _i32([0, 0]), _i32([0, 0]), _i32([0])
+    nb = L.workspace_bytes(L.OP_PAGED_ATTN, G * Hk, B * nq, width * page, d, Hk, r=nq, P=B)
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV) if nb else None
+
+    def go():
+        L.fastar_paged_append(k, v, kp, vp, table, at, ln, q=q, q_out=qo, axes=(44, 42, 42), grid=(2, 3), dev_status=st)
+        L.fastar_paged_attn(qo, kp, vp, table, at, 0.1, out, lse, block=1, window=300, sinks=7, dev_status=st,
+                            workspace=ws)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        go()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        go()
+    for a in ([0, 0], [5, 900], [1000, 33], [0, 1]):
+        at.copy_(_i32(a))
+        g.replay()
+        torch.cuda.synchronize()
+        first = [x.clone() for x in (qo, out, lse, kp, vp, ln)]
+        g.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(first, (qo, out, lse, kp, vp, ln)):
+            assert torch.equal(x, y)
+        check_attn("bf16", qo, kp, vp, table.cpu().numpy(), np.array(a), None, 0.1, 1, 300, 7, out, lse)
+    assert st.item() == 0
+
+
+def test_two_calls_on_two_streams():
+    cs = [attn_case("bf16", [1], [20000], 2, 2, 128, 32, "hnd", 1, 0, 0, seed=s) for s in (1, 2)]
+    cs.append(attn_case("bf16", [500], [5000], 2, 2, 128, 32, "hnd", 1, 0, 0, seed=3))
+    alone = [run_attn(*c, 0.1, 1, 0, 0) for c in cs]
+    outs = []
+    torch.cuda.synchronize()
+    for c in cs:
+        q, kp, vp, table, at, cu = c
+        nb = L.workspace_bytes(L.OP_PAGED_ATTN, 4, q.shape[1], table.shape[1] * 32, 128, 2, r=q.shape[1], P=1)
+        outs.append((torch.empty_like(q), _i32(table), _i32(at), torch.empty(nb + 16, dtype=torch.uint8, device=DEV),
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, (o, t, a, w, s) in zip(cs, outs):
+            with torch.cuda.stream(s):
+                L.fastar_paged_attn(c[0], c[1], c[2], t, a, 0.1, o, block=1, workspace=w)
+    torch.cuda.synchronize()
+    for o, want in zip(outs, alone):
+        assert torch.equal(o[0], want[0])
