@@ -648,7 +648,8 @@ int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d
  * ones (sinks) and gives the memory of those between back.  Pools k_pool, v_pool of `pages` pages of
  * `page` rows: element (page, h, slot, c) lies at page * page_stride + h * head_stride +
  * slot * row_stride + c (elements; the same strides for both), so that pages of [H, page, d] and of
- * [page, H, d] both work.  page is 16, 32, 64 or 128; pools and strides 16-byte aligned.
+ * [page, H, d] both work.  page is 16, 32, 64 or 128; pools and strides 16-byte aligned,
+ * strides below 2^38.
  * Row r of sequence b of B is slot r % page of page table[b * max_pages + r / page] (int32 on the
  * device); a sequence has max_pages * page rows at most (at most 2^30, FASTAR_ECAPACITY).  The T
  * tokens of a call (at most 2^30) lie behind one another, sequence b's are cu[b] .. cu[b + 1]

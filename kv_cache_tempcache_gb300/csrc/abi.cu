@@ -46,6 +46,8 @@ int check_kv4(const void* codes, const void* scales) {
   return codes && scales && aligned16(codes) && aligned16(scales) ? FASTAR_OK : FASTAR_EINVAL;
 }
 
+constexpr int64_t kPoolStride = (int64_t)1 << 38;   // elements; a tensor map's strides end at 2^40 bytes
+
 // Pools of pages, the table and the sequences of a call.
 int check_pools(const void* k, const void* v, int dtype, int d, int H, int64_t pages, int page, int64_t ps, int64_t hs,
                 int64_t rs) {
@@ -55,6 +57,7 @@ int check_pools(const void* k, const void* v, int dtype, int d, int H, int64_t p
   const int64_t es = (int64_t)esize(dtype);
   if (rs < d || ps < d || hs < 0 || (H > 1 && hs < d)) return FASTAR_EINVAL;
   if (((rs * es) & 15) || ((ps * es) & 15) || ((hs * es) & 15)) return FASTAR_EINVAL;
+  if (rs >= kPoolStride || ps >= kPoolStride || hs >= kPoolStride) return FASTAR_EINVAL;
   return FASTAR_OK;
 }
 int check_paged(int B, int64_t T, const int32_t* cu, int page, int64_t max_pages) {

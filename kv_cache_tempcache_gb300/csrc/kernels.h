@@ -288,7 +288,8 @@ struct PagedAttnArgs {
   float* part_o;                      // [splits, T, Hq, d]
   float2* part_ml;                    // [splits, T, Hq]
 };
-size_t paged_attn_workspace(int d, int Hq, int Hkv, int64_t T, int B, int max_q, int64_t cap);
+// keys: that a token sees at most
+size_t paged_attn_workspace(int d, int Hq, int Hkv, int64_t T, int B, int max_q, int64_t keys);
 cudaError_t launch_paged_attn(int dtype, int d, PagedAttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s);
 
 }  // namespace fastar

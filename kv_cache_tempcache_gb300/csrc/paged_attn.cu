@@ -97,43 +97,89 @@ cudaError_t join_go(const PagedAttnArgs& a, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Splits: one CTA a multiprocessor, none under two key tiles of a full cache.
-int splits_simple(int64_t items, int64_t cap) {
-  const int64_t want = sm_count() / items, most = cap / (2 * kSimpleKeys);
+// Rows of a KV head that take the simple kernel in bf16; in fp32 all do.
+constexpr int64_t kFewRows = 16;
+
+enum Kernel { kSimple, kTensor, kTensorAlone };
+struct Plan {
+  Kernel kernel;
+  int splits, min_tiles;
+};
+
+// Splits: one CTA a multiprocessor, none under two key tiles.
+Plan plan_simple(int64_t rows, int64_t heads, int64_t keys) {
+  const int64_t want = sm_count() / ((rows + kSimpleRows - 1) / kSimpleRows * heads), most = keys / (2 * kSimpleKeys);
   int64_t s = want < most ? want : most;
   if (s > kMaxSplits) s = kMaxSplits;
-  return s < 1 ? 1 : (int)s;
+  return Plan{kSimple, s < 1 ? 1 : (int)s, 2};
+}
+
+// Splits for the tensor-core kernel, by a model of its time: waves of CTAs (pairs of them at d = 128), each
+// a fixed part and so much a key tile; items with one row tile, half as long a tile, fill the last
+// wave's gaps; and with splits the partials' way through memory and the join.  The fewest splits
+// within 2 % of the best.  The sequences' lengths are the device's, and may be far below `keys`: min_tiles is what
+// the kernel keeps a split's key tiles to, 3 where all the splits run at once, else 40, beside which the fixed
+// part is small.
+Plan plan_tensor(int d, int64_t rows, int64_t heads, int64_t keys) {
+  const bool alone = d == 128 && rows <= 128;
+  const int cta = alone ? 1 : d / 64;     // CTAs that work as one (paged_attn_tc.cu)
+  const int64_t slots = sm_count() / cta, tiles = (keys + 127) / 128;
+  const int64_t half = (rows - 1) % (256 * cta) < 128 * cta ? heads : 0;
+  const int64_t full = (rows + 256 * cta - 1) / (256 * cta) * heads - half;
+  const double tile = 1.2, fixed = 6.0;
+  auto cost = [&](int64_t s) {
+    const int64_t waves = (full * s + slots - 1) / slots, gaps = 2 * (waves * slots - full * s);
+    const int64_t rest = half * s > gaps ? (half * s - gaps + slots - 1) / slots : 0;
+    const double one = (double)((tiles + s - 1) / s) * tile;
+    const double join = s > 1 ? 4.0 + 2e-6 * s * rows * heads * (d + 2) * 4 / 4.0 : 0.0;
+    return waves * (fixed + one) + rest * (fixed + 0.6 * one) + join;
+  };
+  int64_t most = (4 * slots + full + half - 1) / (full + half);
+  if (most > tiles) most = tiles;
+  if (most > kMaxSplits) most = kMaxSplits;
+  double best = cost(1);
+  int64_t pick = 1;
+  for (int64_t s = 2; s <= most; s += 1 + s / 8) {   // every few: this runs on each call
+    const double c = cost(s);
+    if (c < 0.98 * best) best = c, pick = s;
+  }
+  return Plan{alone ? kTensorAlone : kTensor, (int)pick, (full + half) * pick <= slots ? 3 : 40};
 }
 
 size_t split_bytes(int d, int Hq, int64_t T) { return (size_t)T * Hq * (d + 2) * sizeof(float); }
 
-int plan_splits(int d, int Hq, int Hkv, int B, int max_q, int64_t cap) {
-  const int64_t rows = (int64_t)(Hq / Hkv) * max_q;
-  return splits_simple((rows + kSimpleRows - 1) / kSimpleRows * Hkv * B, cap);
+// keys: that a token sees at most.
+Plan make_plan(int dtype, int d, int Hq, int Hkv, int B, int max_q, int64_t keys) {
+  const int64_t rows = (int64_t)(Hq / Hkv) * max_q, heads = (int64_t)Hkv * B;
+  return dtype == FASTAR_F32 || rows <= kFewRows ? plan_simple(rows, heads, keys) : plan_tensor(d, rows, heads, keys);
 }
 
 }  // namespace
 
-size_t paged_attn_workspace(int d, int Hq, int Hkv, int64_t T, int B, int max_q, int64_t cap) {
-  const int s = plan_splits(d, Hq, Hkv, B, max_q, cap);
-  return s == 1 ? 0 : s * split_bytes(d, Hq, T);
+size_t paged_attn_workspace(int d, int Hq, int Hkv, int64_t T, int B, int max_q, int64_t keys) {
+  int most = 1;
+  for (int dt : {FASTAR_F32, FASTAR_BF16}) {
+    const int s = make_plan(dt, d, Hq, Hkv, B, max_q, keys).splits;
+    most = s > most ? s : most;
+  }
+  return most == 1 ? 0 : most * split_bytes(d, Hq, T);
 }
 
 cudaError_t launch_paged_attn(int dtype, int d, PagedAttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s) {
   a.group = a.Hq / a.Hkv;
-  // keys that a token sees at most
-  int64_t most = a.cap;
-  if (a.window > 0 && (int64_t)a.window + a.sinks < most) most = (int64_t)a.window + a.sinks;
-  a.splits = ws ? plan_splits(d, a.Hq, a.Hkv, a.B, a.max_q, most) : 1;
-  const size_t each = split_bytes(d, a.Hq, a.T);
-  if (a.splits > 1 && ws_bytes / each < (size_t)a.splits) a.splits = (int)(ws_bytes / each);
+  int64_t keys = a.cap;
+  if (a.window > 0 && (int64_t)a.window + a.sinks < keys) keys = (int64_t)a.window + a.sinks;
+  const Plan plan = make_plan(dtype, d, a.Hq, a.Hkv, a.B, a.max_q, keys);
+  const size_t fit = ws ? ws_bytes / split_bytes(d, a.Hq, a.T) : 1;
+  a.splits = fit < (size_t)plan.splits ? (int)fit : plan.splits;
   if (a.splits < 1) a.splits = 1;
-  a.min_tiles = 2;
+  a.min_tiles = plan.min_tiles;
   if (a.splits > 1) {
     a.part_o = static_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * a.T * a.Hq * d);
   }
-  const cudaError_t e = launch_paged_attn_simple(dtype, d, a, s);
+  const cudaError_t e = plan.kernel == kSimple ? launch_paged_attn_simple(dtype, d, a, s)
+                                               : launch_paged_attn_tc(d, a, plan.kernel == kTensorAlone, s);
   if (e != cudaSuccess || a.splits == 1) return e;
   if (dtype == FASTAR_F32) return d == 128 ? join_go<float, 128>(a, s) : join_go<float, 64>(a, s);
   return d == 128 ? join_go<__nv_bfloat16, 128>(a, s) : join_go<__nv_bfloat16, 64>(a, s);

@@ -1,0 +1,148 @@
+// What the attention kernels on the 5th-generation tensor cores share: products, signals and TMEM of a CTA or
+// of a pair of CTAs that works as one (kCta = 1 or 2), and the arithmetic of the softmax warps.
+#pragma once
+
+#include "common.cuh"
+#include "tc.cuh"
+
+namespace fastar {
+
+template <int kCta>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (kCta == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+template <int kCta>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (kCta == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Arrives once on the barrier (of a pair: on both CTAs' barriers at this offset) when every
+// product this thread has issued is complete.
+template <int kCta>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (kCta == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            tc::smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    tc::mma_commit(bar);
+}
+// Arrives at a named barrier at which others wait.
+__device__ __forceinline__ void bar_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+template <int kCta>
+__device__ __forceinline__ void tmem_alloc512(uint32_t* dst) {
+  if (kCta == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(dst)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tc::tmem_alloc(dst, 512);
+    tc::tmem_relinquish();
+  }
+}
+template <int kCta>
+__device__ __forceinline__ void tmem_free512(uint32_t taddr) {
+  if (kCta == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+  else
+    tc::tmem_dealloc(taddr, 512);
+}
+// True in one lane of a converged warp; the compiler knows that a branch on it runs one thread
+// (a branch on the lane number makes it wrap every MMA in code that unifies its operands).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The pair's barrier.  The relaxed arrival does not wait for the thread's own loads and stores (a
+// releasing one cost 1000 to 2000 clocks): what the other CTA relies on is the initialised barriers
+// (mbar_fence_init before it) and that nothing is signalled any more.
+__device__ __forceinline__ void pair_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void pair_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// Arrives on the barrier of the pair's first CTA, where the products are issued.  What the
+// arrival announces lies in the arriving CTA's own shared memory or TMEM, is read there by
+// its own tensor core, and has been handed to the async proxy (fence.proxy.async) or to
+// tcgen05 (its before_thread_sync fence) first; so the arrival needs no fence over the
+// cluster's memory (a cluster-scope release took about 1000 clocks a tile).
+template <int kCta>
+__device__ __forceinline__ void arrive_issuer(uint64_t* bar) {
+  if (kCta == 2)
+    asm volatile(
+        "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
+        " mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(tc::smem_u32(bar))
+        : "memory");
+  else
+    tc::mbar_arrive(bar);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort));
+}
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Largest of n logits in registers.
+template <int n>
+__device__ __forceinline__ float row_max(const float* x) {
+  float m[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+  for (int i = 0; i < n; i += 2) m[(i >> 1) & 3] = max3f(m[(i >> 1) & 3], x[i], x[i + 1]);
+  return fmaxf(max3f(m[0], m[1], m[2]), m[3]);
+}
+
+// (a, b) * s + c and (a, b) + (c, d), two lanes an instruction.
+__device__ __forceinline__ void fma2(float& a, float& b, float s, float c) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mov.b64 z, {%3, %3};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(s), "f"(c));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n"
+      " mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+
+}  // namespace fastar

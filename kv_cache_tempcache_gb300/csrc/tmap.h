@@ -14,6 +14,11 @@ bool make_tmap_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d
                        uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1,
                        uint32_t box2 = 1);
 
+// The same of four dimensions (strides[i]: bytes from one index of dimension i + 1 to the next) and a
+// box of box0 x box1 x 1 x 1.
+bool make_tmap_bf16_4d(CUtensorMap* m, const void* base, const uint64_t dims[4], const uint64_t strides[3], uint32_t box0,
+                       uint32_t box1);
+
 // Streaming multiprocessors of the current device (cached per device).
 int sm_count();
 
