@@ -112,5 +112,44 @@ __device__ __forceinline__ Split split_of(int n, int s, int splits, int min_tile
   return r;
 }
 
+// bf16 kernels multiply a tile's P and V as matrices, where a weight of 0 does not keep an infinity or NaN of a row
+// that only some tokens see from the others.  So of tiles that not every token sees in full they take such
+// values out of V; this is what those add to n channels from c on of a token that sees `see`.
+template <int kTile, int n>
+__device__ __noinline__ void add_taken_out(const PagedAttnArgs& a, const Tiles<kTile>& tiles, const Split& part, int b, int h,
+                                           Sees see, int c, float* o) {
+  const int32_t* table = a.table + (int64_t)b * a.max_pages;
+  for (int j = part.j0; j < part.j1; ++j) {
+    const int key0 = tiles.key(j);
+    if (tiles.all(key0)) continue;
+    for (int key = key0; key < key0 + kTile; ++key) {
+      if (!(seen32(see, key) & 1)) continue;
+      const int page = table[key >> a.pool.page_shift];
+      if (page < 0 || page >= a.pool.pages) continue;
+      const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.pool.v) + page * a.pool.ps + h * a.pool.hs +
+                               (key & ((1 << a.pool.page_shift) - 1)) * a.pool.rs + c;
+      for (int e = 0; e < n; ++e) {
+        const float x = __bfloat162float(v[e]);
+        if (!(fabsf(x) < __int_as_float(0x7f800000))) o[e] += x;
+      }
+    }
+  }
+}
+// Eight channels of such a tile: infinities and NaN become 0; true if there was one.
+__device__ __forceinline__ bool take_out(uint4* p) {
+  const uint4 u = *p;
+  const uint32_t big = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+  if (__builtin_expect((big & 0xffffu) < 0x7f80u && (big >> 16) < 0x7f80u, 1)) return false;
+  uint32_t y[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if ((y[e] & 0x7fffu) >= 0x7f80u) y[e] &= 0xffff0000u;
+    if ((y[e] >> 16 & 0x7fffu) >= 0x7f80u) y[e] &= 0xffffu;
+  }
+  *p = make_uint4(y[0], y[1], y[2], y[3]);
+  return true;
+}
+
 }  // namespace paged
 }  // namespace fastar

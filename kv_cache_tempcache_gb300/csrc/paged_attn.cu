@@ -97,10 +97,7 @@ cudaError_t join_go(const PagedAttnArgs& a, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Rows of a KV head that take the simple kernel in bf16; in fp32 all do.
-constexpr int64_t kFewRows = 16;
-
-enum Kernel { kSimple, kTensor, kTensorAlone };
+enum Kernel { kSimple, kFew, kTensor, kTensorAlone };
 struct Plan {
   Kernel kernel;
   int splits, min_tiles;
@@ -112,6 +109,15 @@ Plan plan_simple(int64_t rows, int64_t heads, int64_t keys) {
   int64_t s = want < most ? want : most;
   if (s > kMaxSplits) s = kMaxSplits;
   return Plan{kSimple, s < 1 ? 1 : (int)s, 2};
+}
+
+// Splits for the few-rows kernel: four blocks a multiprocessor, of which two are resident, but none under eight tiles of
+// 16 keys a warp, and none at all for fewer than three of those.
+Plan plan_few(int64_t heads, int64_t keys) {
+  const int64_t want = 4 * sm_count() / heads, most = keys / (16 * 8 * kFewWarps);
+  int64_t s = want < most ? want : most;
+  if (s > kMaxSplits) s = kMaxSplits;
+  return Plan{kFew, s < 1 || most < 3 ? 1 : (int)s, 8 * kFewWarps};
 }
 
 // Splits for the tensor-core kernel, by a model of its time: waves of CTAs (pairs of them at d = 128), each
@@ -151,7 +157,8 @@ size_t split_bytes(int d, int Hq, int64_t T) { return (size_t)T * Hq * (d + 2) *
 // keys: that a token sees at most.
 Plan make_plan(int dtype, int d, int Hq, int Hkv, int B, int max_q, int64_t keys) {
   const int64_t rows = (int64_t)(Hq / Hkv) * max_q, heads = (int64_t)Hkv * B;
-  return dtype == FASTAR_F32 || rows <= kFewRows ? plan_simple(rows, heads, keys) : plan_tensor(d, rows, heads, keys);
+  if (dtype == FASTAR_F32) return plan_simple(rows, heads, keys);
+  return rows <= kFewRows ? plan_few(heads, keys) : plan_tensor(d, rows, heads, keys);
 }
 
 }  // namespace
@@ -179,6 +186,7 @@ cudaError_t launch_paged_attn(int dtype, int d, PagedAttnArgs a, void* ws, size_
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * a.T * a.Hq * d);
   }
   const cudaError_t e = plan.kernel == kSimple ? launch_paged_attn_simple(dtype, d, a, s)
+                        : plan.kernel == kFew  ? launch_paged_attn_few(d, a, s)
                                                : launch_paged_attn_tc(d, a, plan.kernel == kTensorAlone, s);
   if (e != cudaSuccess || a.splits == 1) return e;
   if (dtype == FASTAR_F32) return d == 128 ? join_go<float, 128>(a, s) : join_go<float, 64>(a, s);

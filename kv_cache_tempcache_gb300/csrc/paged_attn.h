@@ -7,6 +7,9 @@ namespace fastar {
 
 constexpr int kSimpleRows = 32, kSimpleKeys = 64;
 cudaError_t launch_paged_attn_simple(int dtype, int d, const PagedAttnArgs& a, cudaStream_t s);
+// bf16, up to kFewRows rows a KV head
+constexpr int kFewRows = 32, kFewWarps = 4;
+cudaError_t launch_paged_attn_few(int d, const PagedAttnArgs& a, cudaStream_t s);
 // bf16; alone: at d = 128 single CTAs, for up to 128 rows
 cudaError_t launch_paged_attn_tc(int d, const PagedAttnArgs& a, bool alone, cudaStream_t s);
 

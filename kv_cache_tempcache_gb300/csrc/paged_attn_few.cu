@@ -1,0 +1,341 @@
+// Softmax attention over a paged cache for few rows, as in single-token steps (bf16): up to 32 (token, query
+// head) pairs of a KV head.
+//
+// Bound: the cache's bytes.  A row tile of the tcgen05 kernel is 128 rows, so with a few it waits from
+// product to product; here the rows are the 8 columns (up to four times) of m16n8k16 products
+// (mma.sync: its rate is not what bounds this), and each warp runs alone over its share of the
+// block's key tiles of 16 rows, several of them on their way by cp.async, with its own reference, sums and
+// outputs:
+//   S^T[16 keys, 8 rows] += K[16, 16 channels] Q^T,   O^T[16 channels, 8 rows] += V^T[16, 16 keys] P^T
+// K comes by ldmatrix, V^T by its transposing form, P^T is S^T's registers after an 8 x 8 transpose
+// (movmatrix).  A tile lies in one page (pages have 16 rows or more), so a warp needs one table entry a
+// tile; it holds 32 of them, a lane each, and asks for the next 32 while it works on these.  The warps'
+// results are joined in shared memory, in warp order, at the end, and the blocks' by the join kernel.
+// Rows that no token sees are not read: they come as zeros.
+// P is bf16, as V is: 2^-8 of itself at every magnitude.  The reference moves only when a P would pass 2^kTop.
+#include <climits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "paged.cuh"
+#include "paged_attn.h"
+#include "tc.cuh"
+#include "tc_attn.cuh"
+#include "tmap.h"
+
+namespace fastar {
+
+namespace {
+
+constexpr int kKeys = 16;
+constexpr float kTop = 8.f;
+
+// NR: groups of 8 rows.
+template <int D, int NR, int W>
+struct FewLayout {
+  static constexpr int tile = kKeys * D * 2, stage = 2 * tile;      // K, V
+  static constexpr int stages = D == 64 ? 6 : 3;
+  static constexpr int ring = W * stages * stage;
+  static constexpr int ldo = D + 4;                                 // an output row: lanes of 4 rows hit other banks
+  static constexpr int red = W * 8 * NR * ldo * 4;                  // the warps' outputs, over the ring
+  static constexpr int ctl = ring > red ? ring : red;
+  static constexpr int bytes = ctl + W * 8 * NR * 8 + 16;
+};
+
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Lane (g, t) holds elements (g, 2t), (g, 2t + 1) of an 8 x 8 matrix of 16-bit values; gets (2t, g), (2t + 1, g).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// Over the eight lanes of equal t.
+__device__ __forceinline__ float group_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+__device__ __forceinline__ float group_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
+}
+
+template <int D, int NR, int W>
+__global__ void __launch_bounds__(W * 32) paged_attn_few_kernel(const PagedAttnArgs a) {
+  using Lay = FewLayout<D, NR, W>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float2* sml = reinterpret_cast<float2*>(smem + Lay::ctl);        // [W][8 NR] references and sums
+  int* poison = reinterpret_cast<int*>(smem + Lay::ctl + W * 8 * NR * 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  pdl_wait();
+  // heads side by side, then sequences, then splits
+  uint32_t u = blockIdx.x, x = u / (uint32_t)a.Hkv;
+  const int h = (int)(u - x * (uint32_t)a.Hkv);
+  u = x / (uint32_t)a.B;
+  const int b = (int)(x - u * (uint32_t)a.B), split = (int)u;
+  const paged::Seq s = paged::sequence(a.cu, a.at, a.B, a.T, a.cap, b, a.status);
+  if (s.nq > a.max_q && threadIdx.x == 0) flag_status(a.status, FASTAR_DEV_BAD_LEN);
+  const int G = a.group, rows = G * min(s.nq, a.max_q);            // at most 8 NR
+  if (rows == 0) return;
+  paged::Tiles<kKeys> tiles;
+  tiles.set(a, s, 0, (rows - 1) / G);
+  const paged::Split part = paged::split_of(tiles.n, split, a.splits, a.min_tiles);
+  const bool partial = part.used > 1;
+  if (threadIdx.x == 0) *poison = 0;
+  if (part.j0 == part.j1 && a.splits > 1) {              // no keys, or a split that is not in use
+    for (int r = threadIdx.x; r < rows; r += W * 32)
+      a.part_ml[((int64_t)split * a.T + s.t0 + r / G) * a.Hq + h * G + r % G] = make_float2(neg_inf(), 0.f);
+    return;
+  }
+  const int32_t* table = a.table + (int64_t)b * a.max_pages;
+  const int shift = a.pool.page_shift;
+  // this warp's tiles: j0 + warp, + W, ...; the pages of 32 of them, a lane each
+  const int count = part.j1 - part.j0 > warp ? (part.j1 - part.j0 - warp + W - 1) / W : 0;
+  auto pages_from = [&](int i) {
+    i += lane;
+    return i < count ? paged::page_of(table, tiles.key(part.j0 + warp + W * i) >> shift, a.pool.pages, a.status) : -1;
+  };
+  int pages = pages_from(0), next = pages_from(32);
+  // tile i into its stage: a lane moves 16 bytes of a row at a time
+  constexpr int CPR = D / 8, RPI = 32 / CPR;             // chunks of a row, rows side by side
+  const uint32_t ring = tc::smem_u32(smem) + warp * Lay::stages * Lay::stage;
+  const int lr = lane / CPR, lc = lane % CPR;
+  int asked = 0;
+  auto ask = [&]() {
+    if (asked < count) {
+      const int key0 = tiles.key(part.j0 + warp + W * asked);
+      const int page = __shfl_sync(0xffffffffu, pages, asked & 31);
+      const int64_t at = (page < 0 ? 0 : page * a.pool.ps) + h * a.pool.hs + (key0 & ((1 << shift) - 1)) * a.pool.rs + lc * 8;
+      const uint32_t dst = ring + (asked % Lay::stages) * Lay::stage;
+      const bool whole = tiles.all(key0);
+#pragma unroll
+      for (int i = 0; i < kKeys / RPI; ++i) {
+        const int row = i * RPI + lr;
+        const uint32_t n = page >= 0 && (whole || tiles.any(key0 + row)) ? 16 : 0;
+        const uint32_t to = dst + row * (D * 2) + ((lc ^ (row & 7)) << 4);
+        const int64_t from = n ? at + row * a.pool.rs : 0;
+        tc::cp_async16(to, static_cast<const __nv_bfloat16*>(a.pool.k) + from, n);
+        tc::cp_async16(to + Lay::tile, static_cast<const __nv_bfloat16*>(a.pool.v) + from, n);
+      }
+      ++asked;
+      if ((asked & 31) == 0) {
+        pages = next;
+        next = pages_from(asked + 32);
+      }
+    }
+    tc::cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < Lay::stages - 1; ++i) ask();
+  __syncthreads();                                       // poison is set up
+  // query rows: lane (g, t) holds channels 2t, 2t + 1 and 8 + 2t, 9 + 2t of each 16 of row 8 n + g
+  uint32_t qb[NR][D / 16][2];
+  int tok[NR][2];                                        // tokens of the rows 8 n + 2t, 8 n + 2t + 1
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    const int r = 8 * n + g;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+        static_cast<const __nv_bfloat16*>(a.q.p) + (int64_t)(h * G + r % G) * a.q.hs + (int64_t)(s.t0 + r / G) * a.q.ts);
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      qb[n][c][0] = r < rows ? src[c * 8 + t] : 0u;
+      qb[n][c][1] = r < rows ? src[c * 8 + 4 + t] : 0u;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) tok[n][e] = min(8 * n + 2 * t + e, rows - 1) / G;
+  }
+  float sl2 = a.scale * 1.4426950408889634f;
+  sl2 = fminf(fmaxf(sl2, 1.2e-38f), 3.0e38f);
+  float m[NR][2], l[NR][2], o[NR][D / 16][4];
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    m[n][0] = m[n][1] = neg_inf();
+    l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][c][e] = 0.f;
+  }
+  const uint32_t ldk = (lane & 15) * (D * 2), kx = (lane >> 4);            // ldmatrix rows: keys 0-15, chunks 0, 1
+  const uint32_t ldv = ((lane & 7) + ((lane >> 4) << 3)) * (D * 2), vx = (lane >> 3) & 1;
+  const uint32_t swz = lane & 7;
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    ask();
+    tc::cp_async_wait<Lay::stages - 1>();
+    __syncwarp();
+    const uint32_t kt = ring + (i % Lay::stages) * Lay::stage, vt = kt + Lay::tile;
+    const int key0 = tiles.key(part.j0 + warp + W * i);
+    float x[NR][4];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+    float x2[4] = {0.f, 0.f, 0.f, 0.f};                  // one group alone: two chains of products
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t k[4];
+      ldsm4(kt + ldk + (((2 * c + kx) ^ swz) << 4), k);
+      if (NR == 1 && (c & 1)) {
+        mma16816(x2, k, qb[0][c][0], qb[0][c][1]);
+      } else {
+#pragma unroll
+        for (int n = 0; n < NR; ++n) mma16816(x[n], k, qb[n][c][0], qb[n][c][1]);
+      }
+    }
+    if (NR == 1) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[0][e] += x2[e];
+    }
+    if (__builtin_expect(!tiles.all(key0), 0)) {
+      // lane (g, t): keys g (x[0], x[1]) and 8 + g (x[2], x[3]) of rows 2t and 2t + 1
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t bits = paged::seen32(paged::sees(a, s, tok[n][e]), key0);
+          if (!(bits >> g & 1)) x[n][e] = neg_inf();
+          if (!(bits >> (8 + g) & 1)) x[n][2 + e] = neg_inf();
+        }
+      bool found = false;
+#pragma unroll
+      for (int r = 0; r < kKeys / RPI; ++r)
+        found |= paged::take_out(reinterpret_cast<uint4*>(
+            smem + (vt - tc::smem_u32(smem)) + (r * RPI + lr) * (D * 2) + ((lc ^ ((r * RPI + lr) & 7)) << 4)));
+      if (found) *(volatile int*)poison = 1;
+      __syncwarp();
+    }
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) over |= fmaf(fmaxf(x[n][e], x[n][2 + e]), sl2, -m[n][e]) > kTop;
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mt = group_max(fmaxf(x[n][e], x[n][2 + e])) * sl2;
+          if (mt - m[n][e] > kTop) {                     // only the rows that need it
+            const float f = ex2f(m[n][e] - mt);
+            m[n][e] = mt;
+            l[n][e] *= f;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) o[n][c][e] *= f, o[n][c][2 + e] *= f;
+          }
+        }
+    }
+    uint32_t pb[NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const float n0 = m[n][0] == neg_inf() ? 0.f : -m[n][0], n1 = m[n][1] == neg_inf() ? 0.f : -m[n][1];
+      const float p0 = ex2f(fmaf(x[n][0], sl2, n0)), p1 = ex2f(fmaf(x[n][1], sl2, n1));
+      const float p2 = ex2f(fmaf(x[n][2], sl2, n0)), p3 = ex2f(fmaf(x[n][3], sl2, n1));
+      l[n][0] += p0 + p2;
+      l[n][1] += p1 + p3;
+      pb[n][0] = transpose8(pack_bf16(p0, p1));
+      pb[n][1] = transpose8(pack_bf16(p2, p3));
+    }
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t v[4];
+      ldsm4t(vt + ldv + (((2 * c + vx) ^ swz) << 4), v);
+#pragma unroll
+      for (int n = 0; n < NR; ++n) mma16816(o[n][c], v, pb[n][0], pb[n][1]);
+    }
+    __syncwarp();                                        // the stage is asked for again
+  }
+  tc::cp_async_wait<0>();
+  __syncthreads();                                       // the ring is free in every warp
+  // the warps' results side by side, then joined in warp order
+  float* so = reinterpret_cast<float*>(smem) + warp * 8 * NR * Lay::ldo;
+#pragma unroll
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * n + 2 * t + e;
+      const float sum = group_sum(l[n][e]);
+      if (g == 0) sml[warp * 8 * NR + r] = make_float2(m[n][e], sum);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        so[r * Lay::ldo + c * 16 + g] = o[n][c][e];
+        so[r * Lay::ldo + c * 16 + 8 + g] = o[n][c][2 + e];
+      }
+    }
+  __syncthreads();
+  for (int y = threadIdx.x; y < rows * (D / 4); y += W * 32) {
+    const int r = y / (D / 4), c = y % (D / 4) * 4;
+    float top = neg_inf(), sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+      if (sml[w * 8 * NR + r].y != 0.f) top = fmaxf(top, sml[w * 8 * NR + r].x);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 ml = sml[w * 8 * NR + r];
+      if (ml.y == 0.f) continue;
+      const float f = ex2f(ml.x - top);
+      const float4 q = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + (w * 8 * NR + r) * Lay::ldo + c);
+      sum = fmaf(f, ml.y, sum);
+      v[0] = fmaf(f, q.x, v[0]), v[1] = fmaf(f, q.y, v[1]), v[2] = fmaf(f, q.z, v[2]), v[3] = fmaf(f, q.w, v[3]);
+    }
+    if (__builtin_expect(*(volatile int*)poison, 0))
+      paged::add_taken_out<kKeys, 4>(a, tiles, part, b, h, paged::sees(a, s, r / G), c, v);
+    const bool live = sum > 0.f || sum != sum;
+    const int64_t tk = s.t0 + r / G, head = h * G + r % G, prow = ((int64_t)split * a.T + tk) * a.Hq + head;
+    const float mn = top * 0.6931471805599453f;
+    if (c == 0) {
+      if (partial) a.part_ml[prow] = make_float2(live ? mn : neg_inf(), sum);
+      else if (a.splits > 1) a.part_ml[prow] = make_float2(-neg_inf(), 0.f);
+      if (!partial && a.lse) a.lse[head * a.T + tk] = live ? mn + logf(sum) : neg_inf();
+    }
+    if (partial) {
+      *reinterpret_cast<float4*>(a.part_o + prow * D + c) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      const float f = live ? 1.f / sum : 0.f;
+      uint2 w2 = make_uint2(pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f));
+      if (!live) w2 = make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + head * a.o_hs + tk * a.o_ts + c) = w2;
+    }
+  }
+}
+
+template <int D, int NR>
+cudaError_t few_go(const PagedAttnArgs& a, cudaStream_t s) {
+  constexpr int W = kFewWarps;
+  const int64_t blocks = (int64_t)a.Hkv * a.B * a.splits;
+  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  cudaError_t e = opt_in_smem((const void*)paged_attn_few_kernel<D, NR, W>, FewLayout<D, NR, W>::bytes);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(paged_attn_few_kernel<D, NR, W>, dim3((unsigned)blocks), dim3(W * 32), FewLayout<D, NR, W>::bytes, s,
+                       a);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attn_few(int d, const PagedAttnArgs& a, cudaStream_t s) {
+  const int64_t rows = (int64_t)a.group * a.max_q;
+  if (rows <= 8) return d == 128 ? few_go<128, 1>(a, s) : few_go<64, 1>(a, s);
+  if (rows <= 16) return d == 128 ? few_go<128, 2>(a, s) : few_go<64, 2>(a, s);
+  return d == 128 ? few_go<128, 4>(a, s) : few_go<64, 4>(a, s);
+}
+
+}  // namespace fastar

@@ -95,12 +95,6 @@ struct Layout {
   static_assert((kOne ? vs * v_tile : ks * k_tile) >= kSoftWarps * 4096, "the outputs on their way");
 };
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // P = 2^(s sl2 - m) of 32 logits as bf16 pairs into 16 TMEM columns; adds to the row's sum.
 __device__ __forceinline__ void row_exp32(const float* x, float sl2, float nm, uint32_t dst, float& s0, float& s1) {
   uint32_t pk[16];
@@ -156,27 +150,6 @@ __device__ __forceinline__ void find_item(const PagedAttnArgs& a, Item& it, int 
   const uint32_t last = min(it.r0 + 2 * kRT * kCta, it.rows) - 1;
   it.tiles.set(a, it.s, (int)(it.r0 / (uint32_t)a.group), (int)(last / (uint32_t)a.group));
   it.part = paged::split_of(it.tiles.n, it.split, a.splits, a.min_tiles);
-}
-
-// Rows whose infinities and NaN warp 19 took out of V (tiles that not every row sees in full): what they add to
-// 16 channels of one row.
-__device__ __noinline__ void add_taken_out(const PagedAttnArgs& a, const Item& it, const paged::Sees& see, int c, float* o) {
-  const int32_t* table = a.table + (int64_t)it.b * a.max_pages;
-  for (int j = it.part.j0; j < it.part.j1; ++j) {
-    const int key0 = it.tiles.key(j);
-    if (it.tiles.all(key0)) continue;
-    for (int key = key0; key < key0 + kKT; ++key) {
-      if (!(paged::seen32(see, key) & 1)) continue;
-      const int page = table[key >> a.pool.page_shift];
-      if (page < 0 || page >= a.pool.pages) continue;
-      const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.pool.v) + page * a.pool.ps + it.h * a.pool.hs +
-                               (key & ((1 << a.pool.page_shift) - 1)) * a.pool.rs + c;
-      for (int e = 0; e < 16; ++e) {
-        const float x = __bfloat162float(v[e]);
-        if (!(fabsf(x) < __int_as_float(0x7f800000))) o[e] += x;
-      }
-    }
-  }
 }
 
 template <int D, int C>
@@ -446,7 +419,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             float q[16];                    // a copy: o's registers keep no address
 #pragma unroll
             for (int e = 0; e < 16; ++e) q[e] = o[e];
-            add_taken_out(a, it, see, half * HD + c, q);
+            paged::add_taken_out<kKT, 16>(a, it.tiles, it.part, it.b, it.h, see, half * HD + c, q);
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = q[e];
           }
@@ -568,19 +541,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                 *p = make_uint4(0, 0, 0, 0);
                 continue;
               }
-              const uint4 u = *p;
-              const uint32_t big = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
-                                            __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
-              if (__builtin_expect((big & 0xffffu) >= 0x7f80u || (big >> 16) >= 0x7f80u, 0)) {
-                found = true;
-                uint32_t y[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if ((y[e] & 0x7fffu) >= 0x7f80u) y[e] &= 0xffff0000u;
-                  if ((y[e] >> 16 & 0x7fffu) >= 0x7f80u) y[e] &= 0xffffu;
-                }
-                *p = make_uint4(y[0], y[1], y[2], y[3]);
-              }
+              found |= paged::take_out(p);
             }
           }
           tc::fence_proxy_async();
