@@ -151,7 +151,7 @@ size_t fastar_workspace_bytes(int op, int H, int64_t n, int64_t M, int d, int B,
     case FASTAR_OP_PAGED_ATTN:
       if ((d != 64 && d != 128) || B < 1 || H < 1 || H % B || M < 1 || n < 1 || r < 1 || P < 1) return 0;
       if (n > fastar::kPagedMax || H * n > INT32_MAX || r > n || P > 65535) return 0;   // the call refuses them
-      return fastar::paged_attn_workspace(d, H, B, n, (int)P, r, M < fastar::kPagedMax ? M : fastar::kPagedMax);
+      return fastar::paged_attn_workspace(d, H, B, (int)P, r, M < fastar::kPagedMax ? M : fastar::kPagedMax);
     default: return 0;
   }
 }

@@ -282,14 +282,16 @@ struct PagedAttnArgs {
   int64_t o_hs, o_ts;
   float* lse;                         // [Hq, T] or null
   int32_t* status;
-  // filled in by the launcher: query heads of a KV head, splits of the keys, the key tiles a split
-  // should have, the partials (fp32; maximum and sum)
-  int group, splits, min_tiles;
-  float* part_o;                      // [splits, T, Hq, d]
-  float2* part_ml;                    // [splits, T, Hq]
+  // filled in by the launcher
+  int group;                          // query heads of a KV head
+  int splits;                         // many rows: splits of the keys (slot = split * B + sequence)
+  int extra;                          // few rows: slots beyond one a sequence (paged.cuh), 0: none
+  int min_tiles;                      // key tiles that a split should have
+  float* part_o;                      // [slots, Hkv, group * max_q, d] partials in fp32
+  float2* part_ml;                    // [slots, Hkv, group * max_q] maximum and sum
 };
 // keys: that a token sees at most
-size_t paged_attn_workspace(int d, int Hq, int Hkv, int64_t T, int B, int max_q, int64_t keys);
+size_t paged_attn_workspace(int d, int Hq, int Hkv, int B, int max_q, int64_t keys);
 cudaError_t launch_paged_attn(int dtype, int d, PagedAttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s);
 
 }  // namespace fastar

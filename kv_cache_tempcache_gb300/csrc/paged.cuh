@@ -53,6 +53,11 @@ __device__ __forceinline__ Sees sees(const PagedAttnArgs& a, const Seq& s, int i
   return v;
 }
 
+// Where the partials of row r (of a KV head of a sequence) of slot v lie.
+__device__ __forceinline__ int64_t partial_row(const PagedAttnArgs& a, int64_t v, int h, int r) {
+  return (v * a.Hkv + h) * ((int64_t)a.group * a.max_q) + r;
+}
+
 // Which of the n <= 32 keys from `key` on are seen, as bits.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 __device__ __forceinline__ uint32_t seen32(const Sees& v, int key) {
@@ -99,8 +104,8 @@ __device__ __forceinline__ int page_of(const int32_t* row, int p, int64_t pages,
   return -1;
 }
 
-// The splits of a piece of work's n tiles that are in use, none under min_tiles tiles; tiles j0 .. j1
-// are split s's.
+// Many rows: the splits of a piece of work's n tiles that are in use, none under min_tiles tiles; tiles
+// j0 .. j1 are split s's.
 struct Split {
   int used, j0, j1;
 };
@@ -109,6 +114,80 @@ __device__ __forceinline__ Split split_of(int n, int s, int splits, int min_tile
   r.used = splits > 1 ? max(1, min(splits, n / min_tiles)) : 1;
   r.j0 = (int)((int64_t)n * s / r.used);
   r.j1 = s < r.used ? (int)((int64_t)n * (s + 1) / r.used) : r.j0;
+  return r;
+}
+
+// Few rows: what a block of slot v works on.  The blocks are dealt out by the sequences' lengths: with n_b key
+// tiles a sequence, a block takes `chunk` of them, the larger of min_tiles and what spreads all the tiles
+// over a.extra slots; sequence b has c_b = ceil(n_b / chunk) slots (at least one), side by side.  No more than
+// extra + B of them are in use, whatever the lengths.  Every warp finds its block's by itself, the same in
+// every lane; sequences in steps of 32.
+constexpr int kDealt = 256;              // sequences that are dealt out; with more, each is a slot
+struct Work {
+  int b, first, count, split;            // sequence, its first slot, its slots, this one's place among them
+};
+// The work of slot v, or (v < 0) of sequence b; false where there is none.
+template <int kTile>
+__device__ __forceinline__ bool find_work(const PagedAttnArgs& a, int v, int b, Work& w) {
+  w.split = 0;
+  w.count = 1;
+  if (a.extra == 0) {
+    w.b = w.first = v < 0 ? b : v;
+    return true;
+  }
+  const int lane = threadIdx.x & 31;
+  int n[kDealt / 32];
+  int64_t total = 0;
+#pragma unroll
+  for (int k = 0; k < kDealt / 32; ++k) {
+    n[k] = -1;                           // a sequence without tokens has no slot
+    if (32 * k >= a.B) break;
+    if (32 * k + lane < a.B) {
+      const Seq s = sequence(a.cu, a.at, a.B, a.T, a.cap, 32 * k + lane, blockIdx.x == 0 ? a.status : nullptr);
+      if (s.nq > 0) {
+        Tiles<kTile> t;
+        t.set(a, s, 0, min(s.nq, a.max_q) - 1);
+        n[k] = t.n;
+        total += t.n;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int64_t even = (total + a.extra - 1) / a.extra;
+  const int chunk = even > a.min_tiles ? (int)even : a.min_tiles;
+  int base = 0;
+  bool here = false;
+#pragma unroll
+  for (int k = 0; k < kDealt / 32; ++k) {
+    if (32 * k >= a.B) break;
+    const int c = n[k] < 0 ? 0 : max(1, (n[k] + chunk - 1) / chunk);
+    int end = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += x;
+    }
+    end += base;
+    base = __shfl_sync(0xffffffffu, end, 31);
+    const uint32_t hit = __ballot_sync(0xffffffffu, v < 0 ? 32 * k + lane == b && c > 0 : v >= end - c && v < end);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      w.b = 32 * k + src;
+      w.count = __shfl_sync(0xffffffffu, c, src);
+      w.first = __shfl_sync(0xffffffffu, end - c, src);
+      w.split = v < 0 ? 0 : v - w.first;
+      here = true;
+    }
+  }
+  return here;
+}
+// Tiles j0 .. j1 of n: one of `count` parts.
+__device__ __forceinline__ Split part_of(int n, const Work& w) {
+  Split r;
+  r.used = w.count;
+  r.j0 = (int)((int64_t)n * w.split / w.count);
+  r.j1 = (int)((int64_t)n * (w.split + 1) / w.count);
   return r;
 }
 

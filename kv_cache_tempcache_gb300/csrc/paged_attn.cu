@@ -4,8 +4,8 @@
 // The G = Hq / Hkv query heads that share a KV head see the same keys, so the rows of a piece of work
 // are (token, head) pairs, r = t * G + g: the cache is read once for the G heads, and neighbouring rows
 // see nearly the same keys.  With few rows the keys are cut into splits, a block each, whose
-// partials (sum of p v, maximum, sum of p) go to the workspace in fp32 and are joined by a second
-// launch.
+// partials (sum of p v, maximum, sum of p) go to a slot of the workspace in fp32 and are joined by a
+// second launch.
 #include <climits>
 
 #include "common.cuh"
@@ -24,8 +24,9 @@ constexpr int kMaxSplits = 256;
 // O = sum_s e^(m_s - m) o_s / sum_s e^(m_s - m) l_s over a row's partials, m = max_s m_s; one warp a
 // row, D / 32 channels a lane.  The partials are summed in the order of the splits, so results do
 // not change from run to run.  A split in which the row sees no key, or that is not in use, has
-// l = 0 and nothing in o; (inf, 0) for the first split says that the output is in place already.
-template <typename T, int D>
+// l = 0 and nothing in o.  An output that is in place already: one split (few rows), or (inf, 0)
+// for the first of them (many rows).
+template <typename T, int D, int kTile>
 __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnArgs a) {
   constexpr int CPL = D / 32;
   const int lane = threadIdx.x & 31;
@@ -35,9 +36,17 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnArgs a) 
   if (u >= per * a.B) return;
   const int b = (int)(u / per);
   const paged::Seq s = paged::sequence(a.cu, a.at, a.B, a.T, a.cap, b, nullptr);
-  const int i = (int)(u - b * per) / a.Hq, head = (int)(u - b * per) - i * a.Hq;
+  const int i = (int)((u - b * per) / a.Hq), head = (int)(u - b * per - (int64_t)i * a.Hq);
   if (i >= s.nq) return;
-  const int64_t rows = a.T * a.Hq, row = (int64_t)(s.t0 + i) * a.Hq + head;
+  paged::Work work;
+  int splits = a.splits;
+  if (kTile > 0) {                       // few rows
+    if (!paged::find_work<kTile < 1 ? 1 : kTile>(a, -1, b, work) || work.count == 1) return;
+    splits = work.count;
+  }
+  const int h = head / a.group;
+  const int64_t row0 = paged::partial_row(a, kTile > 0 ? work.first : b, h, i * a.group + head - h * a.group);
+  const int64_t step = (int64_t)(kTile > 0 ? 1 : a.B) * a.Hkv * a.group * a.max_q;    // from split to split
   constexpr int kPer = kMaxSplits / 32;
   float m = neg_inf(), l = 0.f, o[CPL];
 #pragma unroll
@@ -47,7 +56,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnArgs a) 
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     ml[k] = make_float2(neg_inf(), 0.f);
-    if (32 * k + lane < a.splits) ml[k] = a.part_ml[(32 * k + lane) * rows + row];
+    if (32 * k + lane < splits) ml[k] = a.part_ml[row0 + (32 * k + lane) * step];
     if (ml[k].y != 0.f) m = fmaxf(m, ml[k].x);
   }
   if (__any_sync(0xffffffffu, lane == 0 && ml[0].x == -neg_inf() && ml[0].y == 0.f)) return;
@@ -56,9 +65,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnArgs a) 
   const float ref = m == neg_inf() ? 0.f : m;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    if (32 * k >= a.splits) break;
+    if (32 * k >= splits) break;
     const float w = ml[k].y != 0.f ? expf(ml[k].x - ref) : 0.f;
-    const int here = a.splits - 32 * k < 32 ? a.splits - 32 * k : 32;
+    const int here = splits - 32 * k < 32 ? splits - 32 * k : 32;
 #pragma unroll 1
     for (int s0 = 0; s0 < here; s0 += 8) {
       float p[8][CPL], wt[8], ls[8];
@@ -68,7 +77,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnArgs a) 
         ls[x] = __shfl_sync(0xffffffffu, ml[k].y, src);
         wt[x] = __shfl_sync(0xffffffffu, w, src);
         const bool in = s0 + x < here && ls[x] != 0.f;
-        const float* src_o = a.part_o + ((32 * k + s0 + x) * rows + row) * D + lane * CPL;
+        const float* src_o = a.part_o + (row0 + (32 * k + s0 + x) * step) * D + lane * CPL;
 #pragma unroll
         for (int c = 0; c < CPL; ++c) p[x][c] = in ? src_o[c] : 0.f;
         if (!in) wt[x] = ls[x] = 0.f;
@@ -88,36 +97,27 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnArgs a) 
   if (lane == 0 && a.lse) a.lse[head * a.T + s.t0 + i] = live ? m + logf(l) : neg_inf();
 }
 
-template <typename T, int D>
+template <typename T, int D, int kTile>
 cudaError_t join_go(const PagedAttnArgs& a, cudaStream_t s) {
   const int64_t blocks = ((int64_t)a.B * a.max_q * a.Hq + 3) / 4;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = launch_dependent(paged_join_kernel<T, D>, dim3((unsigned)blocks), dim3(128), 0, s, a);
+  const cudaError_t e = launch_dependent(paged_join_kernel<T, D, kTile>, dim3((unsigned)blocks), dim3(128), 0, s, a);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-enum Kernel { kSimple, kFew, kTensor, kTensorAlone };
+enum Kernel { kF32, kFew, kTensor, kTensorAlone };
 struct Plan {
   Kernel kernel;
-  int splits, min_tiles;
+  int splits, extra, min_tiles;
 };
 
-// Splits: one CTA a multiprocessor, none under two key tiles.
-Plan plan_simple(int64_t rows, int64_t heads, int64_t keys) {
-  const int64_t want = sm_count() / ((rows + kSimpleRows - 1) / kSimpleRows * heads), most = keys / (2 * kSimpleKeys);
-  int64_t s = want < most ? want : most;
-  if (s > kMaxSplits) s = kMaxSplits;
-  return Plan{kSimple, s < 1 ? 1 : (int)s, 2};
-}
-
-// Splits for the few-rows kernel: four blocks a multiprocessor, of which two are resident, but none under eight tiles of
-// 16 keys a warp, and none at all for fewer than three of those.
-Plan plan_few(int64_t heads, int64_t keys) {
-  const int64_t want = 4 * sm_count() / heads, most = keys / (16 * 8 * kFewWarps);
-  int64_t s = want < most ? want : most;
-  if (s > kMaxSplits) s = kMaxSplits;
-  return Plan{kFew, s < 1 || most < 3 ? 1 : (int)s, 8 * kFewWarps};
+// Slots for few rows: `blocks` blocks in all, each of min_tiles key tiles of `tile` rows or more; none beyond one a
+// sequence where they fill the GPU, or where no sequence has three times that many.
+Plan plan_slots(Kernel kernel, int64_t units, int64_t B, int64_t keys, int64_t blocks, int tile, int min_tiles) {
+  int64_t e = B > paged::kDealt || keys < 3 * (int64_t)tile * min_tiles ? 0 : blocks / units;
+  if (e > kMaxSplits - 1) e = kMaxSplits - 1;
+  return Plan{kernel, 1, (int)e, min_tiles};
 }
 
 // Splits for the tensor-core kernel, by a model of its time: waves of CTAs (pairs of them at d = 128), each
@@ -149,48 +149,61 @@ Plan plan_tensor(int d, int64_t rows, int64_t heads, int64_t keys) {
     const double c = cost(s);
     if (c < 0.98 * best) best = c, pick = s;
   }
-  return Plan{alone ? kTensorAlone : kTensor, (int)pick, (full + half) * pick <= slots ? 3 : 40};
+  return Plan{alone ? kTensorAlone : kTensor, (int)pick, 0, (full + half) * pick <= slots ? 3 : 40};
 }
 
-size_t split_bytes(int d, int Hq, int64_t T) { return (size_t)T * Hq * (d + 2) * sizeof(float); }
+// Slots of the workspace, and the bytes of one.
+int64_t slots_of(const Plan& p, int B) { return p.extra > 0 ? p.extra + B : p.splits > 1 ? (int64_t)p.splits * B : 0; }
+size_t slot_bytes(int d, int Hq, int max_q) { return (size_t)max_q * Hq * (d + 2) * sizeof(float); }
 
 // keys: that a token sees at most.
 Plan make_plan(int dtype, int d, int Hq, int Hkv, int B, int max_q, int64_t keys) {
-  const int64_t rows = (int64_t)(Hq / Hkv) * max_q, heads = (int64_t)Hkv * B;
-  if (dtype == FASTAR_F32) return plan_simple(rows, heads, keys);
-  return rows <= kFewRows ? plan_few(heads, keys) : plan_tensor(d, rows, heads, keys);
+  const int64_t rows = (int64_t)(Hq / Hkv) * max_q;
+  if (dtype == FASTAR_F32) {
+    // one block a multiprocessor, two tiles of 64 keys
+    const int64_t units = (rows + kF32Rows - 1) / kF32Rows * Hkv;
+    return plan_slots(kF32, units, B, keys, sm_count(), kF32Keys, 2);
+  }
+  // four blocks a multiprocessor, of which two are resident; eight tiles of 16 keys a warp
+  if (rows <= kFewRows) return plan_slots(kFew, Hkv, B, keys, 4 * sm_count(), 16, 8 * kFewWarps);
+  return plan_tensor(d, rows, (int64_t)Hkv * B, keys);
 }
 
 }  // namespace
 
-size_t paged_attn_workspace(int d, int Hq, int Hkv, int64_t T, int B, int max_q, int64_t keys) {
-  int most = 1;
+size_t paged_attn_workspace(int d, int Hq, int Hkv, int B, int max_q, int64_t keys) {
+  int64_t most = 0;
   for (int dt : {FASTAR_F32, FASTAR_BF16}) {
-    const int s = make_plan(dt, d, Hq, Hkv, B, max_q, keys).splits;
-    most = s > most ? s : most;
+    const int64_t n = slots_of(make_plan(dt, d, Hq, Hkv, B, max_q, keys), B);
+    most = n > most ? n : most;
   }
-  return most == 1 ? 0 : most * split_bytes(d, Hq, T);
+  return most * slot_bytes(d, Hq, max_q);
 }
 
 cudaError_t launch_paged_attn(int dtype, int d, PagedAttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s) {
   a.group = a.Hq / a.Hkv;
   int64_t keys = a.cap;
   if (a.window > 0 && (int64_t)a.window + a.sinks < keys) keys = (int64_t)a.window + a.sinks;
-  const Plan plan = make_plan(dtype, d, a.Hq, a.Hkv, a.B, a.max_q, keys);
-  const size_t fit = ws ? ws_bytes / split_bytes(d, a.Hq, a.T) : 1;
-  a.splits = fit < (size_t)plan.splits ? (int)fit : plan.splits;
-  if (a.splits < 1) a.splits = 1;
+  Plan plan = make_plan(dtype, d, a.Hq, a.Hkv, a.B, a.max_q, keys);
+  const int64_t fit = ws ? (int64_t)(ws_bytes / slot_bytes(d, a.Hq, a.max_q)) : 0;
+  if (plan.extra > fit - a.B) plan.extra = fit > a.B ? (int)(fit - a.B) : 0;
+  if (plan.splits > fit / a.B) plan.splits = fit >= a.B ? (int)(fit / a.B) : 1;
+  a.splits = plan.splits;
+  a.extra = plan.extra;
   a.min_tiles = plan.min_tiles;
-  if (a.splits > 1) {
+  const int64_t slots = slots_of(plan, a.B);
+  if (slots > 0) {
     a.part_o = static_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)a.splits * a.T * a.Hq * d);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * a.max_q * a.Hq * d);
   }
-  const cudaError_t e = plan.kernel == kSimple ? launch_paged_attn_simple(dtype, d, a, s)
+  const cudaError_t e = plan.kernel == kF32 ? launch_paged_attn_f32(d, a, s)
                         : plan.kernel == kFew  ? launch_paged_attn_few(d, a, s)
                                                : launch_paged_attn_tc(d, a, plan.kernel == kTensorAlone, s);
-  if (e != cudaSuccess || a.splits == 1) return e;
-  if (dtype == FASTAR_F32) return d == 128 ? join_go<float, 128>(a, s) : join_go<float, 64>(a, s);
-  return d == 128 ? join_go<__nv_bfloat16, 128>(a, s) : join_go<__nv_bfloat16, 64>(a, s);
+  if (e != cudaSuccess || slots == 0) return e;
+  if (plan.kernel == kF32) return d == 128 ? join_go<float, 128, kF32Keys>(a, s) : join_go<float, 64, kF32Keys>(a, s);
+  if (plan.kernel == kFew)
+    return d == 128 ? join_go<__nv_bfloat16, 128, 16>(a, s) : join_go<__nv_bfloat16, 64, 16>(a, s);
+  return d == 128 ? join_go<__nv_bfloat16, 128, 0>(a, s) : join_go<__nv_bfloat16, 64, 0>(a, s);
 }
 
 }  // namespace fastar

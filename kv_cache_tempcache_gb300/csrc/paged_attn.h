@@ -5,8 +5,8 @@
 
 namespace fastar {
 
-constexpr int kSimpleRows = 32, kSimpleKeys = 64;
-cudaError_t launch_paged_attn_simple(int dtype, int d, const PagedAttnArgs& a, cudaStream_t s);
+constexpr int kF32Rows = 32, kF32Keys = 64;
+cudaError_t launch_paged_attn_f32(int d, const PagedAttnArgs& a, cudaStream_t s);
 // bf16, up to kFewRows rows a KV head
 constexpr int kFewRows = 32, kFewWarps = 4;
 cudaError_t launch_paged_attn_few(int d, const PagedAttnArgs& a, cudaStream_t s);

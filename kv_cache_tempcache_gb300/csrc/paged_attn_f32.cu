@@ -1,4 +1,4 @@
-// Softmax attention over a paged cache in fp32 arithmetic: 32 rows and 64 keys at a time.
+// Softmax attention over a paged cache in fp32: 32 rows and 64 keys at a time.
 //
 // Two rows a half warp: a thread forms the logits of two rows and four keys, then two rows and D / 16
 // channels of the output.  Keys that no row of the block sees are zeros in shared memory; where only
@@ -15,29 +15,30 @@ namespace fastar {
 
 namespace {
 
-constexpr int kRows = kSimpleRows, kKeys = kSimpleKeys;
+constexpr int kRows = kF32Rows, kKeys = kF32Keys;
 
 template <int D>
-struct SimpleLayout {
+struct F32Layout {
   static constexpr int ld = D + 4;                       // float4 reads of 8 rows hit 8 bank groups
   static constexpr int q = 0, k = q + kRows * ld, v = k + kKeys * ld, p = v + kKeys * ld;
   static constexpr int ldp = kKeys + 4;
   static constexpr int bytes = (p + kRows * ldp) * 4;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(256) paged_attn_simple_kernel(const PagedAttnArgs a, int row_tiles) {
-  using Lay = SimpleLayout<D>;
+template <int D>
+__global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs a, int row_tiles) {
+  using Lay = F32Layout<D>;
   extern __shared__ __align__(16) float sm[];
   float *sq = sm + Lay::q, *sk = sm + Lay::k, *sv = sm + Lay::v, *sp = sm + Lay::p;
   pdl_wait();
-  // (split, row tile from the last, sequence, head)
+  // heads side by side, then row tiles from the last, then slots
   int u = blockIdx.x;
   const int h = u % a.Hkv;
   u /= a.Hkv;
-  const int b = u % a.B;
-  u /= a.B;
-  const int split = u / row_tiles, r0 = (row_tiles - 1 - u % row_tiles) * kRows;
+  const int slot = u / row_tiles, r0 = (row_tiles - 1 - u % row_tiles) * kRows;
+  paged::Work work;
+  if (!paged::find_work<kKeys>(a, slot, 0, work)) return;
+  const int b = work.b;
   const paged::Seq s = paged::sequence(a.cu, a.at, a.B, a.T, a.cap, b, a.status);
   if (s.nq > a.max_q && threadIdx.x == 0) flag_status(a.status, FASTAR_DEV_BAD_LEN);
   const int G = a.group, rows = G * min(s.nq, a.max_q);
@@ -45,7 +46,7 @@ __global__ void __launch_bounds__(256) paged_attn_simple_kernel(const PagedAttnA
   const int rl = min(r0 + kRows, rows) - 1;
   paged::Tiles<kKeys> tiles;
   tiles.set(a, s, r0 / G, rl / G);
-  const paged::Split part = paged::split_of(tiles.n, split, a.splits, a.min_tiles);
+  const paged::Split part = paged::part_of(tiles.n, work);
   const bool partial = part.used > 1;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   paged::Sees see[2];
@@ -65,18 +66,10 @@ __global__ void __launch_bounds__(256) paged_attn_simple_kernel(const PagedAttnA
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
   }
-  if (part.j0 == part.j1) {                              // no keys, or a split that is not in use
-    if (tx == 0)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (has[i] && a.splits > 1)
-          a.part_ml[((int64_t)split * a.T + tok[i]) * a.Hq + head[i]] = make_float2(neg_inf(), 0.f);
-    if (a.splits > 1) return;
-  }
   for (int x = threadIdx.x; x < kRows * (D / 8); x += 256) {
     const int row = x / (D / 8), c = x % (D / 8) * 8, r = min(r0 + row, rl);
     float f[8];
-    load8(static_cast<const T*>(a.q.p) + (int64_t)(h * G + r % G) * a.q.hs + (int64_t)(s.t0 + r / G) * a.q.ts + c, f);
+    load8(static_cast<const float*>(a.q.p) + (int64_t)(h * G + r % G) * a.q.hs + (int64_t)(s.t0 + r / G) * a.q.ts + c, f);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sq[row * Lay::ld + c + e] = f[e];
   }
@@ -92,8 +85,8 @@ __global__ void __launch_bounds__(256) paged_attn_simple_kernel(const PagedAttnA
         const int page = paged::page_of(table, key >> a.pool.page_shift, a.pool.pages, a.status);
         if (page >= 0) {
           const int64_t at = page * a.pool.ps + h * a.pool.hs + (key & ((1 << a.pool.page_shift) - 1)) * a.pool.rs + c;
-          load8(static_cast<const T*>(a.pool.k) + at, fk);
-          load8(static_cast<const T*>(a.pool.v) + at, fv);
+          load8(static_cast<const float*>(a.pool.k) + at, fk);
+          load8(static_cast<const float*>(a.pool.v) + at, fv);
         }
       }
 #pragma unroll
@@ -165,11 +158,10 @@ __global__ void __launch_bounds__(256) paged_attn_simple_kernel(const PagedAttnA
     for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
     if (!has[i]) continue;
     const bool live = l[i] > 0.f || l[i] != l[i];
-    const int64_t row = tok[i] * a.Hq + head[i], all = a.T * a.Hq;
+    const int64_t row = paged::partial_row(a, slot, h, r0 + 2 * ty + i);
     const float mn = m[i] * 0.6931471805599453f;
     if (tx == 0) {
-      if (partial) a.part_ml[split * all + row] = make_float2(live ? mn : neg_inf(), l[i]);
-      else if (a.splits > 1) a.part_ml[split * all + row] = make_float2(-neg_inf(), 0.f);
+      if (partial) a.part_ml[row] = make_float2(live ? mn : neg_inf(), l[i]);
       if (!partial && a.lse) a.lse[head[i] * a.T + tok[i]] = live ? mn + logf(l[i]) : neg_inf();
     }
     const float f = partial ? 1.f : 1.f / l[i];
@@ -177,20 +169,20 @@ __global__ void __launch_bounds__(256) paged_attn_simple_kernel(const PagedAttnA
     for (int c = 0; c < D / 16; ++c) {
       const int ch = tx * 4 + (c >> 2) * 64 + (c & 3);
       const float y = live ? o[i][c] * f : 0.f;
-      if (partial) a.part_o[(split * all + row) * D + ch] = y;
-      else static_cast<T*>(a.out)[head[i] * a.o_hs + tok[i] * a.o_ts + ch] = from_f<T>(y);
+      if (partial) a.part_o[row * D + ch] = y;
+      else static_cast<float*>(a.out)[head[i] * a.o_hs + tok[i] * a.o_ts + ch] = y;
     }
   }
 }
 
-template <typename T, int D>
-cudaError_t simple_go(const PagedAttnArgs& a, cudaStream_t s) {
+template <int D>
+cudaError_t f32_go(const PagedAttnArgs& a, cudaStream_t s) {
   const int64_t rt = ((int64_t)a.group * a.max_q + kRows - 1) / kRows;
-  const int64_t blocks = rt * a.Hkv * a.B * a.splits;
+  const int64_t blocks = rt * a.Hkv * (a.B + a.extra);
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  cudaError_t e = opt_in_smem((const void*)paged_attn_simple_kernel<T, D>, SimpleLayout<D>::bytes);
+  cudaError_t e = opt_in_smem((const void*)paged_attn_f32_kernel<D>, F32Layout<D>::bytes);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(paged_attn_simple_kernel<T, D>, dim3((unsigned)blocks), dim3(256), SimpleLayout<D>::bytes, s, a,
+  e = launch_dependent(paged_attn_f32_kernel<D>, dim3((unsigned)blocks), dim3(256), F32Layout<D>::bytes, s, a,
                        (int)rt);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -198,9 +190,8 @@ cudaError_t simple_go(const PagedAttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_paged_attn_simple(int dtype, int d, const PagedAttnArgs& a, cudaStream_t s) {
-  if (dtype == FASTAR_BF16) return d == 128 ? simple_go<__nv_bfloat16, 128>(a, s) : simple_go<__nv_bfloat16, 64>(a, s);
-  return d == 128 ? simple_go<float, 128>(a, s) : simple_go<float, 64>(a, s);
+cudaError_t launch_paged_attn_f32(int d, const PagedAttnArgs& a, cudaStream_t s) {
+  return d == 128 ? f32_go<128>(a, s) : f32_go<64>(a, s);
 }
 
 }  // namespace fastar

@@ -87,25 +87,20 @@ __global__ void __launch_bounds__(W * 32) paged_attn_few_kernel(const PagedAttnA
   int* poison = reinterpret_cast<int*>(smem + Lay::ctl + W * 8 * NR * 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   pdl_wait();
-  // heads side by side, then sequences, then splits
-  uint32_t u = blockIdx.x, x = u / (uint32_t)a.Hkv;
-  const int h = (int)(u - x * (uint32_t)a.Hkv);
-  u = x / (uint32_t)a.B;
-  const int b = (int)(x - u * (uint32_t)a.B), split = (int)u;
+  // heads side by side, then slots
+  paged::Work work;
+  const int slot = (int)(blockIdx.x / (uint32_t)a.Hkv), h = (int)(blockIdx.x - (uint32_t)slot * (uint32_t)a.Hkv);
+  if (!paged::find_work<kKeys>(a, slot, 0, work)) return;
+  const int b = work.b;
   const paged::Seq s = paged::sequence(a.cu, a.at, a.B, a.T, a.cap, b, a.status);
   if (s.nq > a.max_q && threadIdx.x == 0) flag_status(a.status, FASTAR_DEV_BAD_LEN);
   const int G = a.group, rows = G * min(s.nq, a.max_q);            // at most 8 NR
   if (rows == 0) return;
   paged::Tiles<kKeys> tiles;
   tiles.set(a, s, 0, (rows - 1) / G);
-  const paged::Split part = paged::split_of(tiles.n, split, a.splits, a.min_tiles);
+  const paged::Split part = paged::part_of(tiles.n, work);
   const bool partial = part.used > 1;
   if (threadIdx.x == 0) *poison = 0;
-  if (part.j0 == part.j1 && a.splits > 1) {              // no keys, or a split that is not in use
-    for (int r = threadIdx.x; r < rows; r += W * 32)
-      a.part_ml[((int64_t)split * a.T + s.t0 + r / G) * a.Hq + h * G + r % G] = make_float2(neg_inf(), 0.f);
-    return;
-  }
   const int32_t* table = a.table + (int64_t)b * a.max_pages;
   const int shift = a.pool.page_shift;
   // this warp's tiles: j0 + warp, + W, ...; the pages of 32 of them, a lane each
@@ -298,11 +293,10 @@ __global__ void __launch_bounds__(W * 32) paged_attn_few_kernel(const PagedAttnA
     if (__builtin_expect(*(volatile int*)poison, 0))
       paged::add_taken_out<kKeys, 4>(a, tiles, part, b, h, paged::sees(a, s, r / G), c, v);
     const bool live = sum > 0.f || sum != sum;
-    const int64_t tk = s.t0 + r / G, head = h * G + r % G, prow = ((int64_t)split * a.T + tk) * a.Hq + head;
+    const int64_t tk = s.t0 + r / G, head = h * G + r % G, prow = paged::partial_row(a, slot, h, r);
     const float mn = top * 0.6931471805599453f;
     if (c == 0) {
       if (partial) a.part_ml[prow] = make_float2(live ? mn : neg_inf(), sum);
-      else if (a.splits > 1) a.part_ml[prow] = make_float2(-neg_inf(), 0.f);
       if (!partial && a.lse) a.lse[head * a.T + tk] = live ? mn + logf(sum) : neg_inf();
     }
     if (partial) {
@@ -319,7 +313,7 @@ __global__ void __launch_bounds__(W * 32) paged_attn_few_kernel(const PagedAttnA
 template <int D, int NR>
 cudaError_t few_go(const PagedAttnArgs& a, cudaStream_t s) {
   constexpr int W = kFewWarps;
-  const int64_t blocks = (int64_t)a.Hkv * a.B * a.splits;
+  const int64_t blocks = (int64_t)a.Hkv * (a.B + a.extra);
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
   cudaError_t e = opt_in_smem((const void*)paged_attn_few_kernel<D, NR, W>, FewLayout<D, NR, W>::bytes);
   if (e != cudaSuccess) return e;

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       const RowOf w = row_of(a, it, r);
       // what the join reads of a split that is not in use, and of the first where the output is in place
       if (a.splits > 1)
-        a.part_ml[((int64_t)it.split * a.T + it.s.t0 + w.t) * a.Hq + w.head] =
+        a.part_ml[paged::partial_row(a, (int64_t)it.split * a.B + it.b, it.h, (int)r)] =
             make_float2(it.split == 0 ? -neg_inf() : neg_inf(), 0.f);
       if (it.tiles.n == 0 && it.split == 0) store_empty<D>(a, it, w);   // no keys at all
     }
@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       // memory (the ring of K, or of V, has been used), so that they leave as whole runs
       uint8_t* stg = base + Lay::out + warp * 4096;
       uint8_t* out = partial ? reinterpret_cast<uint8_t*>(a.part_o) : static_cast<uint8_t*>(a.out);
-      const int64_t tok = it.s.t0 + at.t, prow = ((int64_t)it.split * a.T + tok) * a.Hq + at.head;
+      const int64_t tok = it.s.t0 + at.t;
+      const int64_t prow = paged::partial_row(a, (int64_t)it.split * a.B + it.b, it.h, (int)r);
       const int64_t off = !has      ? -1
                           : partial ? (prow * D + half * HD) * 4
                                     : (at.head * a.o_hs + tok * a.o_ts + half * HD) * 2;
