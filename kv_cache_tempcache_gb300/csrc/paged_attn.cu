@@ -115,7 +115,8 @@ struct Plan {
 // Slots for few rows: `blocks` blocks in all, each of min_tiles key tiles of `tile` rows or more; none beyond one a
 // sequence where they fill the GPU, or where no sequence has three times that many.
 Plan plan_slots(Kernel kernel, int64_t units, int64_t B, int64_t keys, int64_t blocks, int tile, int min_tiles) {
-  int64_t e = B > paged::kDealt || keys < 3 * (int64_t)tile * min_tiles ? 0 : blocks / units;
+  int64_t e = blocks / units - B;
+  if (B > paged::kDealt || keys < 3 * (int64_t)tile * min_tiles || e < 0) e = 0;
   if (e > kMaxSplits - 1) e = kMaxSplits - 1;
   return Plan{kernel, 1, (int)e, min_tiles};
 }

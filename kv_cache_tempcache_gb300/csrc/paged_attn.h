@@ -2,8 +2,16 @@
 #pragma once
 
 #include "kernels.h"
+#include "tmap.h"
 
 namespace fastar {
+
+// The tensor map of a bf16 pool: (channel, slot, head, page), boxes of 64 channels and `rows` slots.
+inline bool make_pool_tmap(CUtensorMap* m, const PagedAttnArgs& a, const void* pool, int d, int rows) {
+  const uint64_t dims[4] = {(uint64_t)d, (uint64_t)1 << a.pool.page_shift, (uint64_t)a.Hkv, (uint64_t)a.pool.pages};
+  const uint64_t strides[3] = {(uint64_t)a.pool.rs * 2, (uint64_t)a.pool.hs * 2, (uint64_t)a.pool.ps * 2};
+  return make_tmap_bf16_4d(m, pool, dims, strides, 64, rows);
+}
 
 constexpr int kF32Rows = 32, kF32Keys = 64;
 cudaError_t launch_paged_attn_f32(int d, const PagedAttnArgs& a, cudaStream_t s);

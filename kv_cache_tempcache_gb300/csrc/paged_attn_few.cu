@@ -4,14 +4,16 @@
 // Bound: the cache's bytes.  A row tile of the tcgen05 kernel is 128 rows, so with a few it waits from
 // product to product; here the rows are the 8 columns (up to four times) of m16n8k16 products
 // (mma.sync: its rate is not what bounds this), and each warp runs alone over its share of the
-// block's key tiles of 16 rows, several of them on their way by cp.async, with its own reference, sums and
+// block's key tiles of 16 rows, several of them on their way by TMA, with its own reference, sums and
 // outputs:
 //   S^T[16 keys, 8 rows] += K[16, 16 channels] Q^T,   O^T[16 channels, 8 rows] += V^T[16, 16 keys] P^T
 // K comes by ldmatrix, V^T by its transposing form, P^T is S^T's registers after an 8 x 8 transpose
 // (movmatrix).  A tile lies in one page (pages have 16 rows or more), so a warp needs one table entry a
 // tile; it holds 32 of them, a lane each, and asks for the next 32 while it works on these.  The warps'
 // results are joined in shared memory, in warp order, at the end, and the blocks' by the join kernel.
-// Rows that no token sees are not read: they come as zeros.
+// (With the rows moved by cp.async, 16 bytes a lane, 250 of 665 instructions a tile at 32 rows were theirs.)
+// Rows of V that no token sees become zeros in shared memory; pages that no token sees, or that are not there,
+// come as zeros.
 // P is bf16, as V is: 2^-8 of itself at every magnitude.  The reference moves only when a P would pass 2^kTop.
 #include <climits>
 
@@ -39,7 +41,8 @@ struct FewLayout {
   static constexpr int ldo = D + 4;                                 // an output row: lanes of 4 rows hit other banks
   static constexpr int red = W * 8 * NR * ldo * 4;                  // the warps' outputs, over the ring
   static constexpr int ctl = ring > red ? ring : red;
-  static constexpr int bytes = ctl + W * 8 * NR * 8 + 16;
+  static constexpr int bar = ctl + W * 8 * NR * 8 + 16;
+  static constexpr int bytes = bar + W * stages * 8 + 1024;
 };
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -80,12 +83,19 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 template <int D, int NR, int W>
-__global__ void __launch_bounds__(W * 32) paged_attn_few_kernel(const PagedAttnArgs a) {
+__global__ void __launch_bounds__(W * 32)
+    paged_attn_few_kernel(const PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap,
+                          const __grid_constant__ CUtensorMap vmap) {
   using Lay = FewLayout<D, NR, W>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float2* sml = reinterpret_cast<float2*>(smem + Lay::ctl);        // [W][8 NR] references and sums
   int* poison = reinterpret_cast<int*>(smem + Lay::ctl + W * 8 * NR * 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  if (threadIdx.x == 0) {
+    tc::tma_prefetch_desc(&kmap);
+    tc::tma_prefetch_desc(&vmap);
+  }
   pdl_wait();
   // heads side by side, then slots
   paged::Work work;
@@ -110,36 +120,32 @@ __global__ void __launch_bounds__(W * 32) paged_attn_few_kernel(const PagedAttnA
     return i < count ? paged::page_of(table, tiles.key(part.j0 + warp + W * i) >> shift, a.pool.pages, a.status) : -1;
   };
   int pages = pages_from(0), next = pages_from(32);
-  // tile i into its stage: a lane moves 16 bytes of a row at a time
-  constexpr int CPR = D / 8, RPI = 32 / CPR;             // chunks of a row, rows side by side
-  const uint32_t ring = tc::smem_u32(smem) + warp * Lay::stages * Lay::stage;
-  const int lr = lane / CPR, lc = lane % CPR;
-  int asked = 0;
+  // tile i into its stage: a lane brings a box of 16 rows and 64 channels, of K or of V
+  constexpr int NB = D / 64;
+  uint8_t* ring = smem + warp * Lay::stages * Lay::stage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::bar) + warp * Lay::stages;
+  if (lane == 0) {
+    for (int i = 0; i < Lay::stages; ++i) tc::mbar_init(&bars[i], 1);
+    tc::mbar_fence_init();
+  }
+  __syncwarp();
+  int asked = 0, to = 0;
   auto ask = [&]() {
-    if (asked < count) {
-      const int key0 = tiles.key(part.j0 + warp + W * asked);
-      const int page = __shfl_sync(0xffffffffu, pages, asked & 31);
-      const int64_t at = (page < 0 ? 0 : page * a.pool.ps) + h * a.pool.hs + (key0 & ((1 << shift) - 1)) * a.pool.rs + lc * 8;
-      const uint32_t dst = ring + (asked % Lay::stages) * Lay::stage;
-      const bool whole = tiles.all(key0);
-#pragma unroll
-      for (int i = 0; i < kKeys / RPI; ++i) {
-        const int row = i * RPI + lr;
-        const uint32_t n = page >= 0 && (whole || tiles.any(key0 + row)) ? 16 : 0;
-        const uint32_t to = dst + row * (D * 2) + ((lc ^ (row & 7)) << 4);
-        const int64_t from = n ? at + row * a.pool.rs : 0;
-        tc::cp_async16(to, static_cast<const __nv_bfloat16*>(a.pool.k) + from, n);
-        tc::cp_async16(to + Lay::tile, static_cast<const __nv_bfloat16*>(a.pool.v) + from, n);
-      }
-      ++asked;
-      if ((asked & 31) == 0) {
-        pages = next;
-        next = pages_from(asked + 32);
-      }
+    if (asked >= count) return;
+    const int key0 = tiles.key(part.j0 + warp + W * asked);
+    const int page = __shfl_sync(0xffffffffu, pages, asked & 31);
+    if (lane == 0) tc::mbar_arrive_tx(&bars[to], Lay::stage);
+    __syncwarp();
+    if (lane < 2 * NB)
+      tc::tma_load_4d(ring + to * Lay::stage + lane * (kKeys * 128), lane < NB ? &kmap : &vmap, (lane & (NB - 1)) * 64,
+                      key0 & ((1 << shift) - 1), h, page < 0 ? (int)a.pool.pages : page, &bars[to]);
+    if ((++asked & 31) == 0) {
+      pages = next;
+      next = pages_from(asked + 32);
     }
-    tc::cp_async_commit();
+    if (++to == Lay::stages) to = 0;
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < Lay::stages - 1; ++i) ask();
   __syncthreads();                                       // poison is set up
   // query rows: lane (g, t) holds channels 2t, 2t + 1 and 8 + 2t, 9 + 2t of each 16 of row 8 n + g
@@ -170,15 +176,23 @@ __global__ void __launch_bounds__(W * 32) paged_attn_few_kernel(const PagedAttnA
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][c][e] = 0.f;
   }
-  const uint32_t ldk = (lane & 15) * (D * 2), kx = (lane >> 4);            // ldmatrix rows: keys 0-15, chunks 0, 1
-  const uint32_t ldv = ((lane & 7) + ((lane >> 4) << 3)) * (D * 2), vx = (lane >> 3) & 1;
-  const uint32_t swz = lane & 7;
+  // ldmatrix addresses in a tile, by 16 channels mod 64: rows keys 0-15, chunks 0 and 1 of K; V transposed
+  uint32_t ldk[4], ldv[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    ldk[c] = tc::smem_u32(ring) + tc::sw128_off(lane & 15, 2 * c + (lane >> 4));
+    ldv[c] = tc::smem_u32(ring) + Lay::tile + tc::sw128_off((lane & 7) + ((lane >> 4) << 3), 2 * c + (lane >> 3 & 1));
+  }
+  volatile int never = 0;
+  bool ok = true;
+  int st = 0;
+  uint32_t ph = 0;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
     ask();
-    tc::cp_async_wait<Lay::stages - 1>();
-    __syncwarp();
-    const uint32_t kt = ring + (i % Lay::stages) * Lay::stage, vt = kt + Lay::tile;
+    ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[st], ph, &never)) && ok;
+    if (!ok) break;
+    const uint32_t at = st * Lay::stage;
     const int key0 = tiles.key(part.j0 + warp + W * i);
     float x[NR][4];
 #pragma unroll
@@ -187,7 +201,7 @@ __global__ void __launch_bounds__(W * 32) paged_attn_few_kernel(const PagedAttnA
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
       uint32_t k[4];
-      ldsm4(kt + ldk + (((2 * c + kx) ^ swz) << 4), k);
+      ldsm4(ldk[c & 3] + at + (c >> 2) * (kKeys * 128), k);
       if (NR == 1 && (c & 1)) {
         mma16816(x2, k, qb[0][c][0], qb[0][c][1]);
       } else {
@@ -210,11 +224,15 @@ __global__ void __launch_bounds__(W * 32) paged_attn_few_kernel(const PagedAttnA
           if (!(bits >> (8 + g) & 1)) x[n][2 + e] = neg_inf();
         }
       bool found = false;
-#pragma unroll
-      for (int r = 0; r < kKeys / RPI; ++r)
-        found |= paged::take_out(reinterpret_cast<uint4*>(
-            smem + (vt - tc::smem_u32(smem)) + (r * RPI + lr) * (D * 2) + ((lc ^ ((r * RPI + lr) & 7)) << 4)));
+#pragma unroll 1
+      for (int y = lane; y < kKeys * (D / 8); y += 32) {
+        const int row = y / (D / 8), c = y % (D / 8);
+        uint4* p = reinterpret_cast<uint4*>(ring + at + Lay::tile + (c >> 3) * (kKeys * 128) + tc::sw128_off(row, c & 7));
+        if (tiles.any(key0 + row)) found |= paged::take_out(p);
+        else *p = make_uint4(0, 0, 0, 0);
+      }
       if (found) *(volatile int*)poison = 1;
+      tc::fence_proxy_async();                           // before the stage is written by TMA again
       __syncwarp();
     }
     bool over = false;
@@ -251,13 +269,17 @@ __global__ void __launch_bounds__(W * 32) paged_attn_few_kernel(const PagedAttnA
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
       uint32_t v[4];
-      ldsm4t(vt + ldv + (((2 * c + vx) ^ swz) << 4), v);
+      ldsm4t(ldv[c & 3] + at + (c >> 2) * (kKeys * 128), v);
 #pragma unroll
       for (int n = 0; n < NR; ++n) mma16816(o[n][c], v, pb[n][0], pb[n][1]);
     }
     __syncwarp();                                        // the stage is asked for again
+    if (++st == Lay::stages) st = 0, ph ^= 1;
   }
-  tc::cp_async_wait<0>();
+  if (!ok) {                                             // what is on its way lands before the block leaves
+    flag_status(a.status, FASTAR_DEV_TIMEOUT);
+    for (int i = 0; i < Lay::stages; ++i) tc::mbar_wait(&bars[i], ph ^ (i < st), &never, 400000000LL);
+  }
   __syncthreads();                                       // the ring is free in every warp
   // the warps' results side by side, then joined in warp order
   float* so = reinterpret_cast<float*>(smem) + warp * 8 * NR * Lay::ldo;
@@ -315,10 +337,13 @@ cudaError_t few_go(const PagedAttnArgs& a, cudaStream_t s) {
   constexpr int W = kFewWarps;
   const int64_t blocks = (int64_t)a.Hkv * (a.B + a.extra);
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  CUtensorMap km, vm;
+  if (!make_pool_tmap(&km, a, a.pool.k, D, kKeys) || !make_pool_tmap(&vm, a, a.pool.v, D, kKeys))
+    return cudaErrorInvalidValue;
   cudaError_t e = opt_in_smem((const void*)paged_attn_few_kernel<D, NR, W>, FewLayout<D, NR, W>::bytes);
   if (e != cudaSuccess) return e;
   e = launch_dependent(paged_attn_few_kernel<D, NR, W>, dim3((unsigned)blocks), dim3(W * 32), FewLayout<D, NR, W>::bytes, s,
-                       a);
+                       a, km, vm);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

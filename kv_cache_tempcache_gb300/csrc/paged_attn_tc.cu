@@ -651,11 +651,8 @@ cudaError_t tc_go(const PagedAttnArgs& a, cudaStream_t s) {
   const int64_t blocks = rt * a.Hkv * a.B * a.splits * Lay::kCta;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
   const int page = 1 << a.pool.page_shift;
-  const uint64_t dims[4] = {(uint64_t)D, (uint64_t)page, (uint64_t)a.Hkv, (uint64_t)a.pool.pages};
-  const uint64_t strides[3] = {(uint64_t)a.pool.rs * 2, (uint64_t)a.pool.hs * 2, (uint64_t)a.pool.ps * 2};
   CUtensorMap km, vm;
-  if (!make_tmap_bf16_4d(&km, a.pool.k, dims, strides, 64, page < Lay::KR ? page : Lay::KR) ||
-      !make_tmap_bf16_4d(&vm, a.pool.v, dims, strides, 64, page))
+  if (!make_pool_tmap(&km, a, a.pool.k, D, page < Lay::KR ? page : Lay::KR) || !make_pool_tmap(&vm, a, a.pool.v, D, page))
     return cudaErrorInvalidValue;
   cudaError_t e = opt_in_smem((const void*)paged_attn_tc_kernel<D, C>, (int)Lay::bytes);
   if (e != cudaSuccess) return e;
