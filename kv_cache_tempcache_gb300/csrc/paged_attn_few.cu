@@ -52,6 +52,14 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// c = a b
+__device__ __forceinline__ void mma16816_first(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, "
+      "%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -120,7 +128,7 @@ __global__ void __launch_bounds__(W * 32)
     return i < count ? paged::page_of(table, tiles.key(part.j0 + warp + W * i) >> shift, a.pool.pages, a.status) : -1;
   };
   int pages = pages_from(0), next = pages_from(32);
-  // tile i into its stage: a lane brings a box of 16 rows and 64 channels, of K or of V
+  // tile i into its stage, in boxes of 16 rows and 64 channels
   constexpr int NB = D / 64;
   uint8_t* ring = smem + warp * Lay::stages * Lay::stage;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::bar) + warp * Lay::stages;
@@ -134,11 +142,15 @@ __global__ void __launch_bounds__(W * 32)
     if (asked >= count) return;
     const int key0 = tiles.key(part.j0 + warp + W * asked);
     const int page = __shfl_sync(0xffffffffu, pages, asked & 31);
-    if (lane == 0) tc::mbar_arrive_tx(&bars[to], Lay::stage);
+    if (elect_one()) {
+      tc::mbar_arrive_tx(&bars[to], Lay::stage);
+      const int row = key0 & ((1 << shift) - 1), pg = page < 0 ? (int)a.pool.pages : page;
+#pragma unroll
+      for (int c = 0; c < 2 * NB; ++c)
+        tc::tma_load_4d(ring + to * Lay::stage + c * (kKeys * 128), c < NB ? &kmap : &vmap, (c & (NB - 1)) * 64, row, h, pg,
+                        &bars[to]);
+    }
     __syncwarp();
-    if (lane < 2 * NB)
-      tc::tma_load_4d(ring + to * Lay::stage + lane * (kKeys * 128), lane < NB ? &kmap : &vmap, (lane & (NB - 1)) * 64,
-                      key0 & ((1 << shift) - 1), h, page < 0 ? (int)a.pool.pages : page, &bars[to]);
     if ((++asked & 31) == 0) {
       pages = next;
       next = pages_from(asked + 32);
@@ -166,10 +178,13 @@ __global__ void __launch_bounds__(W * 32)
   }
   float sl2 = a.scale * 1.4426950408889634f;
   sl2 = fminf(fmaxf(sl2, 1.2e-38f), 3.0e38f);
-  float m[NR][2], l[NR][2], o[NR][D / 16][4];
+  // minus the references, in log2 units; 0 while a row has seen no key (isset, a bit a row)
+  float nm[NR][2], l[NR][2], o[NR][D / 16][4];
+  uint32_t isset = 0;
+  bool all_set = false;
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
-    m[n][0] = m[n][1] = neg_inf();
+    nm[n][0] = nm[n][1] = 0.f;
     l[n][0] = l[n][1] = 0.f;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c)
@@ -194,19 +209,20 @@ __global__ void __launch_bounds__(W * 32)
     if (!ok) break;
     const uint32_t at = st * Lay::stage;
     const int key0 = tiles.key(part.j0 + warp + W * i);
-    float x[NR][4];
-#pragma unroll
-    for (int n = 0; n < NR; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
-    float x2[4] = {0.f, 0.f, 0.f, 0.f};                  // one group alone: two chains of products
+    float x[NR][4], x2[4];                               // one group alone: two chains of products
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
       uint32_t k[4];
       ldsm4(ldk[c & 3] + at + (c >> 2) * (kKeys * 128), k);
       if (NR == 1 && (c & 1)) {
-        mma16816(x2, k, qb[0][c][0], qb[0][c][1]);
+        if (c == 1) mma16816_first(x2, k, qb[0][c][0], qb[0][c][1]);
+        else mma16816(x2, k, qb[0][c][0], qb[0][c][1]);
       } else {
 #pragma unroll
-        for (int n = 0; n < NR; ++n) mma16816(x[n], k, qb[n][c][0], qb[n][c][1]);
+        for (int n = 0; n < NR; ++n) {
+          if (c == 0) mma16816_first(x[n], k, qb[n][c][0], qb[n][c][1]);
+          else mma16816(x[n], k, qb[n][c][0], qb[n][c][1]);
+        }
       }
     }
     if (NR == 1) {
@@ -235,32 +251,34 @@ __global__ void __launch_bounds__(W * 32)
       tc::fence_proxy_async();                           // before the stage is written by TMA again
       __syncwarp();
     }
-    bool over = false;
+    float over = neg_inf();
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) over |= fmaf(fmaxf(x[n][e], x[n][2 + e]), sl2, -m[n][e]) > kTop;
-    if (__any_sync(0xffffffffu, over)) {
+      for (int e = 0; e < 2; ++e) over = fmaxf(over, fmaf(fmaxf(x[n][e], x[n][2 + e]), sl2, nm[n][e]));
+    if (__any_sync(0xffffffffu, over > kTop) || !all_set) {
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          const bool set = isset >> (2 * n + e) & 1;
           const float mt = group_max(fmaxf(x[n][e], x[n][2 + e])) * sl2;
-          if (mt - m[n][e] > kTop) {                     // only the rows that need it
-            const float f = ex2f(m[n][e] - mt);
-            m[n][e] = mt;
+          if (set ? mt + nm[n][e] > kTop : mt > neg_inf()) {         // only the rows that need it
+            const float f = set ? ex2f(-nm[n][e] - mt) : 0.f;
+            nm[n][e] = -mt;
+            isset |= 1u << (2 * n + e);
             l[n][e] *= f;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) o[n][c][e] *= f, o[n][c][2 + e] *= f;
           }
         }
+      all_set = __all_sync(0xffffffffu, isset == (1u << (2 * NR)) - 1);
     }
     uint32_t pb[NR][2];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      const float n0 = m[n][0] == neg_inf() ? 0.f : -m[n][0], n1 = m[n][1] == neg_inf() ? 0.f : -m[n][1];
-      const float p0 = ex2f(fmaf(x[n][0], sl2, n0)), p1 = ex2f(fmaf(x[n][1], sl2, n1));
-      const float p2 = ex2f(fmaf(x[n][2], sl2, n0)), p3 = ex2f(fmaf(x[n][3], sl2, n1));
+      const float p0 = ex2f(fmaf(x[n][0], sl2, nm[n][0])), p1 = ex2f(fmaf(x[n][1], sl2, nm[n][1]));
+      const float p2 = ex2f(fmaf(x[n][2], sl2, nm[n][0])), p3 = ex2f(fmaf(x[n][3], sl2, nm[n][1]));
       l[n][0] += p0 + p2;
       l[n][1] += p1 + p3;
       pb[n][0] = transpose8(pack_bf16(p0, p1));
@@ -289,7 +307,7 @@ __global__ void __launch_bounds__(W * 32)
     for (int e = 0; e < 2; ++e) {
       const int r = 8 * n + 2 * t + e;
       const float sum = group_sum(l[n][e]);
-      if (g == 0) sml[warp * 8 * NR + r] = make_float2(m[n][e], sum);
+      if (g == 0) sml[warp * 8 * NR + r] = make_float2(-nm[n][e], sum);
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         so[r * Lay::ldo + c * 16 + g] = o[n][c][e];
