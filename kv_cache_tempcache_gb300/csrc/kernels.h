@@ -284,11 +284,13 @@ struct PagedAttnArgs {
   int32_t* status;
   // filled in by the launcher
   int group;                          // query heads of a KV head
-  int splits;                         // many rows: splits of the keys (slot = split * B + sequence)
+  int shares;                         // many rows: CTAs (pairs) that the work is dealt out to (paged_tc.cuh)
   int extra;                          // few rows: slots beyond one a sequence (paged.cuh), 0: none
   int min_tiles;                      // key tiles that a split should have
-  float* part_o;                      // [slots, Hkv, group * max_q, d] partials in fp32
-  float2* part_ml;                    // [slots, Hkv, group * max_q] maximum and sum
+  float* part_o;                      // partials in fp32, null: keys are not split.  Few rows: [slots, Hkv, group *
+                                      // max_q, d]; many: [2 shares, rows of an item, d]
+  float2* part_ml;                    // their maxima and sums
+  void* cuts;                         // many rows: what is joined, by share (paged_tc.cuh)
 };
 // keys: that a token sees at most
 size_t paged_attn_workspace(int d, int Hq, int Hkv, int B, int max_q, int64_t keys);

@@ -53,7 +53,7 @@ __device__ __forceinline__ Sees sees(const PagedAttnArgs& a, const Seq& s, int i
   return v;
 }
 
-// Where the partials of row r (of a KV head of a sequence) of slot v lie.
+// Few rows: where the partials of row r (of a KV head of a sequence) of slot v lie.
 __device__ __forceinline__ int64_t partial_row(const PagedAttnArgs& a, int64_t v, int h, int r) {
   return (v * a.Hkv + h) * ((int64_t)a.group * a.max_q) + r;
 }
@@ -104,18 +104,10 @@ __device__ __forceinline__ int page_of(const int32_t* row, int p, int64_t pages,
   return -1;
 }
 
-// Many rows: the splits of a piece of work's n tiles that are in use, none under min_tiles tiles; tiles
-// j0 .. j1 are split s's.
+// Tiles j0 .. j1 of a list: one of `used` parts.
 struct Split {
   int used, j0, j1;
 };
-__device__ __forceinline__ Split split_of(int n, int s, int splits, int min_tiles) {
-  Split r;
-  r.used = splits > 1 ? max(1, min(splits, n / min_tiles)) : 1;
-  r.j0 = (int)((int64_t)n * s / r.used);
-  r.j1 = s < r.used ? (int)((int64_t)n * (s + 1) / r.used) : r.j0;
-  return r;
-}
 
 // Few rows: what a block of slot v works on.  The blocks are dealt out by the sequences' lengths: with n_b key
 // tiles a sequence, a block takes `chunk` of them, the larger of min_tiles and what spreads all the tiles
@@ -182,7 +174,6 @@ __device__ __forceinline__ bool find_work(const PagedAttnArgs& a, int v, int b, 
   }
   return here;
 }
-// Tiles j0 .. j1 of n: one of `count` parts.
 __device__ __forceinline__ Split part_of(int n, const Work& w) {
   Split r;
   r.used = w.count;

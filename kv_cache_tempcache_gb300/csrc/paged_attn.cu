@@ -19,13 +19,13 @@ namespace fastar {
 namespace {
 
 constexpr int kMaxSplits = 256;
+constexpr int kMaxTensorShares = 256;    // paged_tc.cuh
 
 // ---- joining the splits ----------------------------------------------------------------------
 // O = sum_s e^(m_s - m) o_s / sum_s e^(m_s - m) l_s over a row's partials, m = max_s m_s; one warp a
 // row, D / 32 channels a lane.  The partials are summed in the order of the splits, so results do
-// not change from run to run.  A split in which the row sees no key, or that is not in use, has
-// l = 0 and nothing in o.  An output that is in place already: one split (few rows), or (inf, 0)
-// for the first of them (many rows).
+// not change from run to run.  A split in which the row sees no key has l = 0.  (The tensor-core kernel's
+// items are joined in its own file.)
 template <typename T, int D, int kTile>
 __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnArgs a) {
   constexpr int CPL = D / 32;
@@ -39,14 +39,11 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnArgs a) 
   const int i = (int)((u - b * per) / a.Hq), head = (int)(u - b * per - (int64_t)i * a.Hq);
   if (i >= s.nq) return;
   paged::Work work;
-  int splits = a.splits;
-  if (kTile > 0) {                       // few rows
-    if (!paged::find_work<kTile < 1 ? 1 : kTile>(a, -1, b, work) || work.count == 1) return;
-    splits = work.count;
-  }
+  if (!paged::find_work<kTile>(a, -1, b, work) || work.count == 1) return;
+  const int splits = work.count;
   const int h = head / a.group;
-  const int64_t row0 = paged::partial_row(a, kTile > 0 ? work.first : b, h, i * a.group + head - h * a.group);
-  const int64_t step = (int64_t)(kTile > 0 ? 1 : a.B) * a.Hkv * a.group * a.max_q;    // from split to split
+  const int64_t row0 = paged::partial_row(a, work.first, h, i * a.group + head - h * a.group);
+  const int64_t step = (int64_t)a.Hkv * a.group * a.max_q;               // from split to split
   constexpr int kPer = kMaxSplits / 32;
   float m = neg_inf(), l = 0.f, o[CPL];
 #pragma unroll
@@ -59,7 +56,6 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnArgs a) 
     if (32 * k + lane < splits) ml[k] = a.part_ml[row0 + (32 * k + lane) * step];
     if (ml[k].y != 0.f) m = fmaxf(m, ml[k].x);
   }
-  if (__any_sync(0xffffffffu, lane == 0 && ml[0].x == -neg_inf() && ml[0].y == 0.f)) return;
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   const float ref = m == neg_inf() ? 0.f : m;
@@ -109,7 +105,7 @@ cudaError_t join_go(const PagedAttnArgs& a, cudaStream_t s) {
 enum Kernel { kF32, kFew, kTensor, kTensorAlone };
 struct Plan {
   Kernel kernel;
-  int splits, extra, min_tiles;
+  int extra, min_tiles, shares;          // see PagedAttnArgs
 };
 
 // Slots for few rows: `blocks` blocks in all, each of min_tiles key tiles of `tile` rows or more; none beyond one a
@@ -118,44 +114,18 @@ Plan plan_slots(Kernel kernel, int64_t units, int64_t B, int64_t keys, int64_t b
   int64_t e = blocks / units - B;
   if (B > paged::kDealt || keys < 3 * (int64_t)tile * min_tiles || e < 0) e = 0;
   if (e > kMaxSplits - 1) e = kMaxSplits - 1;
-  return Plan{kernel, 1, (int)e, min_tiles};
+  return Plan{kernel, (int)e, min_tiles, 0};
 }
 
-// Splits for the tensor-core kernel, by a model of its time: waves of CTAs (pairs of them at d = 128), each
-// a fixed part and so much a key tile; items with one row tile, half as long a tile, fill the last
-// wave's gaps; and with splits the partials' way through memory and the join.  The fewest splits
-// within 2 % of the best.  The sequences' lengths are the device's, and may be far below `keys`: min_tiles is what
-// the kernel keeps a split's key tiles to, 3 where all the splits run at once, else 40, beside which the fixed
-// part is small.
-Plan plan_tensor(int d, int64_t rows, int64_t heads, int64_t keys) {
-  const bool alone = d == 128 && rows <= 128;
-  const int cta = alone ? 1 : d / 64;     // CTAs that work as one (paged_attn_tc.cu)
-  const int64_t slots = sm_count() / cta, tiles = (keys + 127) / 128;
-  const int64_t half = (rows - 1) % (256 * cta) < 128 * cta ? heads : 0;
-  const int64_t full = (rows + 256 * cta - 1) / (256 * cta) * heads - half;
-  const double tile = 1.2, fixed = 6.0;
-  auto cost = [&](int64_t s) {
-    const int64_t waves = (full * s + slots - 1) / slots, gaps = 2 * (waves * slots - full * s);
-    const int64_t rest = half * s > gaps ? (half * s - gaps + slots - 1) / slots : 0;
-    const double one = (double)((tiles + s - 1) / s) * tile;
-    const double join = s > 1 ? 4.0 + 2e-6 * s * rows * heads * (d + 2) * 4 / 4.0 : 0.0;
-    return waves * (fixed + one) + rest * (fixed + 0.6 * one) + join;
-  };
-  int64_t most = (4 * slots + full + half - 1) / (full + half);
-  if (most > tiles) most = tiles;
-  if (most > kMaxSplits) most = kMaxSplits;
-  double best = cost(1);
-  int64_t pick = 1;
-  for (int64_t s = 2; s <= most; s += 1 + s / 8) {   // every few: this runs on each call
-    const double c = cost(s);
-    if (c < 0.98 * best) best = c, pick = s;
-  }
-  return Plan{alone ? kTensorAlone : kTensor, (int)pick, 0, (full + half) * pick <= slots ? 3 : 40};
+// Slots of the workspace, and the bytes of one: the rows of a sequence, or of an item (with half of its share's entry
+// of what is joined).
+int64_t slots_of(const Plan& p, int B) { return p.shares > 0 ? 2 * p.shares : p.extra > 0 ? p.extra + B : 0; }
+int64_t slot_rows(const Plan& p, int d, int Hq, int max_q) {
+  return p.shares > 0 ? paged_tc_rows(d, p.kernel == kTensorAlone) : (int64_t)max_q * Hq;
 }
-
-// Slots of the workspace, and the bytes of one.
-int64_t slots_of(const Plan& p, int B) { return p.extra > 0 ? p.extra + B : p.splits > 1 ? (int64_t)p.splits * B : 0; }
-size_t slot_bytes(int d, int Hq, int max_q) { return (size_t)max_q * Hq * (d + 2) * sizeof(float); }
+size_t slot_bytes(const Plan& p, int d, int Hq, int max_q) {
+  return (size_t)slot_rows(p, d, Hq, max_q) * (d + 2) * sizeof(float) + (p.shares > 0 ? paged_tc_cut_bytes() / 2 : 0);
+}
 
 // keys: that a token sees at most.
 Plan make_plan(int dtype, int d, int Hq, int Hkv, int B, int max_q, int64_t keys) {
@@ -167,18 +137,22 @@ Plan make_plan(int dtype, int d, int Hq, int Hkv, int B, int max_q, int64_t keys
   }
   // four blocks a multiprocessor, of which two are resident; eight tiles of 16 keys a warp
   if (rows <= kFewRows) return plan_slots(kFew, Hkv, B, keys, 4 * sm_count(), 16, 8 * kFewWarps);
-  return plan_tensor(d, rows, (int64_t)Hkv * B, keys);
+  // one CTA, or pair of them, a multiprocessor or two
+  const bool alone = d == 128 && rows <= 128;
+  const int shares = d == 128 && !alone ? sm_count() / 2 : sm_count();
+  return Plan{alone ? kTensorAlone : kTensor, 0, 0, shares < kMaxTensorShares ? shares : kMaxTensorShares};
 }
 
 }  // namespace
 
 size_t paged_attn_workspace(int d, int Hq, int Hkv, int B, int max_q, int64_t keys) {
-  int64_t most = 0;
+  size_t most = 0;
   for (int dt : {FASTAR_F32, FASTAR_BF16}) {
-    const int64_t n = slots_of(make_plan(dt, d, Hq, Hkv, B, max_q, keys), B);
+    const Plan p = make_plan(dt, d, Hq, Hkv, B, max_q, keys);
+    const size_t n = slots_of(p, B) * slot_bytes(p, d, Hq, max_q);
     most = n > most ? n : most;
   }
-  return most * slot_bytes(d, Hq, max_q);
+  return most;
 }
 
 cudaError_t launch_paged_attn(int dtype, int d, PagedAttnArgs a, void* ws, size_t ws_bytes, cudaStream_t s) {
@@ -186,25 +160,24 @@ cudaError_t launch_paged_attn(int dtype, int d, PagedAttnArgs a, void* ws, size_
   int64_t keys = a.cap;
   if (a.window > 0 && (int64_t)a.window + a.sinks < keys) keys = (int64_t)a.window + a.sinks;
   Plan plan = make_plan(dtype, d, a.Hq, a.Hkv, a.B, a.max_q, keys);
-  const int64_t fit = ws ? (int64_t)(ws_bytes / slot_bytes(d, a.Hq, a.max_q)) : 0;
+  const int64_t fit = ws ? (int64_t)(ws_bytes / slot_bytes(plan, d, a.Hq, a.max_q)) : 0;
   if (plan.extra > fit - a.B) plan.extra = fit > a.B ? (int)(fit - a.B) : 0;
-  if (plan.splits > fit / a.B) plan.splits = fit >= a.B ? (int)(fit / a.B) : 1;
-  a.splits = plan.splits;
   a.extra = plan.extra;
   a.min_tiles = plan.min_tiles;
-  const int64_t slots = slots_of(plan, a.B);
+  a.shares = plan.shares;
+  // (a workspace for fewer shares: no cuts, rather than fewer CTAs)
+  const int64_t slots = plan.shares > 0 && fit < 2 * plan.shares ? 0 : slots_of(plan, a.B);
   if (slots > 0) {
+    const int64_t rows = slots * slot_rows(plan, d, a.Hq, a.max_q);
     a.part_o = static_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * a.max_q * a.Hq * d);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * d);
+    a.cuts = a.part_ml + rows;
   }
-  const cudaError_t e = plan.kernel == kF32 ? launch_paged_attn_f32(d, a, s)
-                        : plan.kernel == kFew  ? launch_paged_attn_few(d, a, s)
-                                               : launch_paged_attn_tc(d, a, plan.kernel == kTensorAlone, s);
+  if (plan.shares > 0) return launch_paged_attn_tc(d, a, plan.kernel == kTensorAlone, s);
+  const cudaError_t e = plan.kernel == kF32 ? launch_paged_attn_f32(d, a, s) : launch_paged_attn_few(d, a, s);
   if (e != cudaSuccess || slots == 0) return e;
   if (plan.kernel == kF32) return d == 128 ? join_go<float, 128, kF32Keys>(a, s) : join_go<float, 64, kF32Keys>(a, s);
-  if (plan.kernel == kFew)
-    return d == 128 ? join_go<__nv_bfloat16, 128, 16>(a, s) : join_go<__nv_bfloat16, 64, 16>(a, s);
-  return d == 128 ? join_go<__nv_bfloat16, 128, 0>(a, s) : join_go<__nv_bfloat16, 64, 0>(a, s);
+  return d == 128 ? join_go<__nv_bfloat16, 128, 16>(a, s) : join_go<__nv_bfloat16, 64, 16>(a, s);
 }
 
 }  // namespace fastar

@@ -18,7 +18,9 @@ cudaError_t launch_paged_attn_f32(int d, const PagedAttnArgs& a, cudaStream_t s)
 // bf16, up to kFewRows rows a KV head
 constexpr int kFewRows = 32, kFewWarps = 4;
 cudaError_t launch_paged_attn_few(int d, const PagedAttnArgs& a, cudaStream_t s);
-// bf16; alone: at d = 128 single CTAs, for up to 128 rows
+// bf16; alone: at d = 128 single CTAs, for up to 128 rows; the rows of an item
+int paged_tc_rows(int d, bool alone);
+size_t paged_tc_cut_bytes();            // a share's entry of PagedAttnArgs::cuts
 cudaError_t launch_paged_attn_tc(int d, const PagedAttnArgs& a, bool alone, cudaStream_t s);
 
 }  // namespace fastar

@@ -10,17 +10,23 @@
 //                logits in TMEM, the output;
 //   warp 16      owns TMEM and issues tcgen05.mma from one thread (of the pair's first CTA): S = Q K^T of
 //                both row tiles, O += P V (P from TMEM);
-//   warp 17      brings K and V by TMA, a box a lane: a box is a page, or the part of one that a tile
-//                has; pages that no row sees, or that are not there, come as zeros (a coordinate past the pool);
+//   warp 17      finds the CTA's work and brings K and V by TMA, a box a lane: a box is a page, or the part of
+//                one that a tile has; pages that no row sees, or that are not there, come as zeros (a
+//                coordinate past the pool);
 //   warp 18      hands K tiles on to the issuing CTA;
-//   warp 19      hands V tiles on, and looks into those that not every row sees in full: a key that
-//                nobody sees becomes zeros, and an infinity or NaN that only some rows see is taken out (a
-//                weight of 0 would not keep it from the others) and returns in the outputs of the rows that see it.
+//   warp 19      hands V tiles on, and looks into those that not every row sees in full: an infinity or NaN is
+//                taken out, since a weight of 0 would not keep it from the rows that do not see its key (of a key
+//                that nobody sees, with its row), and returns in the outputs of the rows that do.
 // The order of issue is PV0(j) QK0(j+1) PV1(j) QK1(j+1): while the softmax of one row tile
 // runs, the tensor cores work for the other, so a logit buffer a tile is enough and two
 // accumulators of 128 columns fit TMEM beside them.  Where the rows fill only one row tile, both halves
 // of the CTA take it: one the even key tiles, the other the odd ones, and the two results are joined
 // in shared memory at the end.
+//
+// The work is dealt out on the device (paged_tc.cuh): CTAs (pairs) that stay, one a multiprocessor, each with an equal
+// share of all the key tiles of all items, in one run; an item that a border between two shares cuts leaves
+// partials for a second launch.  While the softmax warps write an item's output, the next one's
+// keys, values and queries are on their way.
 //
 // Numbers: logits, maxima, sums and outputs are fp32.  P is bf16, as V is (a product has one type):
 // 2^-8 of itself, at every magnitude, since bf16 has fp32's exponents.
@@ -31,6 +37,7 @@
 #include "kernels.h"
 #include "paged.cuh"
 #include "paged_attn.h"
+#include "paged_tc.cuh"
 #include "tc.cuh"
 #include "tc_attn.cuh"
 #include "tmap.h"
@@ -40,6 +47,7 @@ namespace fastar {
 namespace {
 
 constexpr int kRT = 128;               // rows of a row tile in a CTA
+constexpr int kJoinRows = 16;          // of a block of the join
 constexpr int kKT = 128;               // keys of a tile
 constexpr int kSoftWarps = 16;
 constexpr int kMmaWarp = kSoftWarps, kCopyWarp = kMmaWarp + 1, kKWarp = kMmaWarp + 2, kVWarp = kMmaWarp + 3;
@@ -51,21 +59,17 @@ static_assert(512 * kRegsSoft + 128 * kRegsRest <= kThreadsT * 96, "the launch's
 // for |V| up to 2^88.
 constexpr float kTop = 8.f;
 
-// What a CTA works on (the same for both of a pair).
-struct Item {
-  paged::Seq s;
-  paged::Tiles<kKT> tiles;
-  paged::Split part;
-  uint32_t rows, r0;       // rows of the sequence's KV head, the item's first
-  int b, h, split, nt;     // sequence, KV head, split, row tiles with rows
-};
+using paged::Item;
+using paged::Share;
 
 struct alignas(16) Ctl {
   uint64_t k_land[4], k_full[4], k_empty[4], v_land[4], v_full[4], v_empty[4];
   uint64_t q_full[2], s_full[2], p_full[2][2], fin;    // by row tile (P: first 32 keys of each half, last 32)
-  Item item;
+  uint64_t item_full[paged::kItems], item_free[paged::kItems];
+  Item item[paged::kItems];                            // item x of this CTA in place x % kItems
+  int poison[paged::kItems];                           // x + 1: infinities or NaN were taken out of item x's V
   uint32_t tmem_base;
-  int abort, poison;
+  int abort;
   float ex[2][2][kRT];                                 // a row's two threads: half, row tile, row
   float mx[kRT];
 };
@@ -77,7 +81,7 @@ template <int D, int C>
 struct Layout {
   static constexpr int kCta = C;
   static constexpr bool kOne = D > 64 * C;
-  static constexpr int ks = kOne ? 3 : 4, vs = kOne ? 2 : 4;    // tiles of K and of V on their way
+  static constexpr int ks = kOne ? 2 : 4, vs = kOne ? 2 : 3;    // tiles of K and of V on their way
   static constexpr int KR = kKT / kCta, VC = D / C;
   static constexpr size_t q_tile = (size_t)kRT * D * 2, q_blk = kRT * 128;
   static constexpr size_t k_tile = (size_t)KR * D * 2, k_blk = KR * 128;
@@ -85,14 +89,11 @@ struct Layout {
   static constexpr size_t q = 0;
   static constexpr size_t k = q + (kOne ? 1 : 2) * q_tile;
   static constexpr size_t v = k + ks * k_tile;
-  // at the end: the odd tiles' output (128 rows of D floats), and 4 KB a softmax warp
-  static constexpr size_t odd_o = kOne ? k : q, out = kOne ? v : k;
-  static constexpr size_t ctl = v + vs * v_tile;
+  static constexpr size_t out = v + vs * v_tile;       // 2 KB a softmax warp
+  static constexpr size_t ctl = out + kSoftWarps * 2048;
   static constexpr size_t bytes = ctl + sizeof(Ctl) + 1024;
   static constexpr uint32_t s_col = 0, o_col = 256;   // two 128-column buffers each
   static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
-  static_assert((kOne ? ks * k_tile : 2 * q_tile) >= (size_t)kRT * D * 4, "the odd tiles' output");
-  static_assert((kOne ? vs * v_tile : ks * k_tile) >= kSoftWarps * 4096, "the outputs on their way");
 };
 
 // P = 2^(s sl2 - m) of 32 logits as bf16 pairs into 16 TMEM columns; adds to the row's sum.
@@ -110,7 +111,7 @@ __device__ __forceinline__ void row_exp32(const float* x, float sl2, float nm, u
   tmem_st16(dst, pk);
 }
 
-// Row r of the item: its token in the sequence and its query head.
+// Row r of the sequence's KV head: its token in the sequence and its query head.
 struct RowOf {
   int t, head;
 };
@@ -118,46 +119,26 @@ __device__ __forceinline__ RowOf row_of(const PagedAttnArgs& a, const Item& it, 
   const uint32_t t = r / (uint32_t)a.group;
   return RowOf{(int)t, it.h * a.group + (int)(r - t * (uint32_t)a.group)};
 }
+// Byte offset of 16-byte chunk c (0..3) of row `row` among rows of 64 bytes, so that 8 rows hit 8 bank groups.
+__device__ __forceinline__ uint32_t out_off(int row, int c) { return (uint32_t)(row * 64 + ((c ^ (row >> 1 & 3)) << 4)); }
 
-// A row that sees no key: zeros and lse = -inf.
-template <int D>
-__device__ __forceinline__ void store_empty(const PagedAttnArgs& a, const Item& it, RowOf w) {
-  const int64_t tok = it.s.t0 + w.t;
-  uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + w.head * a.o_hs + tok * a.o_ts);
+// A warp's 32 staged rows to where each goes (off bytes from out; -1: nowhere).
+__device__ __forceinline__ void store_rows(uint8_t* out, int64_t off, const uint8_t* stg, int lane) {
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) p[i] = make_uint4(0, 0, 0, 0);
-  if (a.lse) a.lse[w.head * a.T + tok] = neg_inf();
-}
-
-// The work of this block: heads side by side, then sequences, then row tiles from the last (whose rows see
-// most), then splits.
-template <int kCta>
-__device__ __forceinline__ void find_item(const PagedAttnArgs& a, Item& it, int row_tiles) {
-  uint32_t u = blockIdx.x / kCta;
-  uint32_t x = u / (uint32_t)a.Hkv;
-  it.h = (int)(u - x * (uint32_t)a.Hkv);
-  u = x / (uint32_t)a.B;
-  it.b = (int)(x - u * (uint32_t)a.B);
-  x = u / (uint32_t)row_tiles;
-  it.split = (int)x;
-  it.r0 = ((uint32_t)row_tiles - 1 - (u - x * (uint32_t)row_tiles)) * (2 * kRT * kCta);
-  it.s = paged::sequence(a.cu, a.at, a.B, a.T, a.cap, it.b, a.status);
-  if (it.s.nq > a.max_q) flag_status(a.status, FASTAR_DEV_BAD_LEN);
-  it.rows = (uint32_t)(a.group * min(it.s.nq, a.max_q));             // fits 31 bits
-  it.nt = 0;
-  if (it.r0 >= it.rows) return;
-  it.nt = it.rows - it.r0 > kRT * kCta ? 2 : 1;
-  const uint32_t last = min(it.r0 + 2 * kRT * kCta, it.rows) - 1;
-  it.tiles.set(a, it.s, (int)(it.r0 / (uint32_t)a.group), (int)(last / (uint32_t)a.group));
-  it.part = paged::split_of(it.tiles.n, it.split, a.splits, a.min_tiles);
+  for (int i = 0; i < 4; ++i) {
+    const int sr = i * 8 + (lane >> 2), ch = lane & 3;
+    const int64_t to = __shfl_sync(0xffffffffu, off, sr);
+    const uint4 v = *reinterpret_cast<const uint4*>(stg + out_off(sr, ch));
+    if (to >= 0) *reinterpret_cast<uint4*>(out + to + ch * 16) = v;
+  }
 }
 
 template <int D, int C>
 __global__ void __launch_bounds__(kThreadsT, 1)
     paged_attn_tc_kernel(const PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap,
-                         const __grid_constant__ CUtensorMap vmap, int row_tiles) {
+                         const __grid_constant__ CUtensorMap vmap) {
   using Lay = Layout<D, C>;
-  constexpr int kCta = C;
+  constexpr int kCta = C, kPer = 2 * kRT * kCta;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Ctl& sm = *reinterpret_cast<Ctl*>(base + Lay::ctl);
@@ -179,36 +160,26 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       tc::mbar_init(&sm.v_empty[i], 1);
     }
     tc::mbar_init(&sm.fin, 1);
+    for (int i = 0; i < paged::kItems; ++i) {
+      tc::mbar_init(&sm.item_full[i], 1);
+      tc::mbar_init(&sm.item_free[i], kSoftWarps + 2 + (rank == 0));     // who reads items, but the copy warp
+      sm.poison[i] = 0;
+    }
     sm.abort = 0;
-    sm.poison = 0;
     tc::mbar_fence_init();
-  }
-  pdl_wait();                            // the launch overlaps the end of the kernel before
-  if (threadIdx.x == kCopyWarp * 32) {   // one thread finds the work
-    find_item<kCta>(a, sm.item, row_tiles);
     tc::tma_prefetch_desc(&kmap);
     tc::tma_prefetch_desc(&vmap);
   }
   __syncthreads();
-  const Item& it = sm.item;
-  if (it.nt == 0) return;                                // both CTAs of a pair
-  const uint32_t rows = it.rows, r0 = it.r0;
-  const int T = it.part.j1 - it.part.j0;
-  const bool partial = it.part.used > 1, both = it.nt == 1;   // both: one row tile, even key tiles and odd key tiles
-  if (T == 0 || (a.splits > 1 && !partial)) {
-    const uint32_t r = r0 + threadIdx.x / kRT * (kRT * kCta) + rank * kRT + threadIdx.x % kRT;
-    if (threadIdx.x < 2 * kRT && r < rows) {
-      const RowOf w = row_of(a, it, r);
-      // what the join reads of a split that is not in use, and of the first where the output is in place
-      if (a.splits > 1)
-        a.part_ml[paged::partial_row(a, (int64_t)it.split * a.B + it.b, it.h, (int)r)] =
-            make_float2(it.split == 0 ? -neg_inf() : neg_inf(), 0.f);
-      if (it.tiles.n == 0 && it.split == 0) store_empty<D>(a, it, w);   // no keys at all
-    }
-    if (T == 0) return;
-  }
   if (kCta == 2) pair_arrive();                          // this CTA's barriers are ready
+  pdl_wait();                            // the launch overlaps the end of the kernel before
   volatile int* abort = &sm.abort;
+  // Item x of this CTA: null at the end, or after a wait that gave up (`ok` says which).
+  auto item_at = [&](int x, bool& ok) -> const Item* {
+    ok = wait_warp(&sm.item_full[x % paged::kItems], (x / paged::kItems) & 1, abort);
+    const Item* it = &sm.item[x % paged::kItems];
+    return ok && it->nt > 0 ? it : nullptr;
+  };
 
   if (warp < kSoftWarps) {
     // ---------------- softmax ----------------
@@ -216,164 +187,168 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     const int w = warp >> 3, half = (warp >> 2) & 1;      // row tile (or parity of the key tiles), half
     const int row = (warp & 3) * 32 + lane;
     const int pair_bar = 1 + w * 4 + (warp & 3);          // the two warps of these rows
-    const bool mine = !(both && w == 1);
-    if (mine) {
-      // Query rows: warp x of a row tile brings its rows 16 x .. on, four lanes a row, to where the product
-      // wants them; odd rows take the halves of a block's 16-byte chunks the other way round, so that
-      // 8 lanes hit 8 bank groups.
+    const int both_bar = 11 + (warp & 3);                 // with those of the other parity
+    constexpr int HD = D / 2;                             // channels of a row of O a thread takes
+    float sl2 = a.scale * 1.4426950408889634f;
+    sl2 = fminf(fmaxf(sl2, 1.2e-38f), 3.0e38f);
+    // Query rows: warp x of a row tile brings its rows 16 x .. on, four lanes a row, to where the product
+    // wants them; odd rows take the halves of a block's 16-byte chunks the other way round, so that
+    // 8 lanes hit 8 bank groups.
+    auto bring_q = [&](const Item& it) {
+      if (it.nt == 1 && w == 1) return;
       constexpr int QC = D / 32;                          // a lane's chunks of a row
       const int qr = (warp & 7) * 16 + (lane >> 2), qc = (lane & 3) ^ ((lane >> 2 & 1) << 2);
       uint8_t* qd = base + Lay::q + (size_t)w * Lay::q_tile;
 #pragma unroll 1
       for (int i = 0; i < 2; ++i) {
-        const uint32_t x = r0 + (uint32_t)(w * (kRT * kCta) + rank * kRT + qr + i * 8);
-        const RowOf from = row_of(a, it, x < rows ? x : r0);
+        const uint32_t x = it.r0 + (uint32_t)(w * (kRT * kCta) + rank * kRT + qr + i * 8);
+        const RowOf from = row_of(a, it, x < it.rows ? x : it.r0);
         const __nv_bfloat16* src =
             static_cast<const __nv_bfloat16*>(a.q.p) + from.head * a.q.hs + (int64_t)(it.s.t0 + from.t) * a.q.ts;
 #pragma unroll
         for (int j = 0; j < QC; ++j)
           tc::cp_async16(tc::smem_u32(qd + (j >> 1) * Lay::q_blk + tc::sw128_off(qr + i * 8, qc ^ ((j & 1) << 2))),
-                         src + (j >> 1) * 64 + (qc ^ ((j & 1) << 2)) * 8, x < rows ? 16 : 0);
+                         src + (j >> 1) * 64 + (qc ^ ((j & 1) << 2)) * 8, x < it.rows ? 16 : 0);
       }
       tc::cp_async_commit();
-    }
-    const uint32_t r = r0 + (both ? 0u : (uint32_t)(w * (kRT * kCta))) + (uint32_t)(rank * kRT + row);
-    const bool has = r < rows;
-    const RowOf at = row_of(a, it, has ? r : rows - 1);   // a row that is not there: as the last
-    const paged::Sees see = paged::sees(a, it.s, at.t);
-    constexpr int HD = D / 2;                             // channels of a row of O a thread takes
-    float sl2 = a.scale * 1.4426950408889634f;
-    sl2 = fminf(fmaxf(sl2, 1.2e-38f), 3.0e38f);
-    const int step = both ? 2 : 1, count = both ? (T - w + 1) >> 1 : T;      // this row tile's key tiles
-    if (mine) {
-      tc::cp_async_wait<0>();
-      tc::fence_proxy_async();
-      __syncwarp();
-    }
+    };
+    bool ok = true;
+    const Item* next = item_at(0, ok);
+    if (next && next->T > 0) bring_q(*next);
     tc::named_bar(10, (kSoftWarps + 1) * 32);             // TMEM is there
     tc::tc_fence_after();
     if (kCta == 2) pair_wait();                           // the other CTA's barriers are ready
-    if (mine && lane == 0) arrive_issuer<kCta>(&sm.q_full[w]);
     const uint32_t tmem = sm.tmem_base;
     const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_addr = lane_addr + Lay::s_col + (uint32_t)(w * 128 + half * 64);
     const uint32_t o_addr = lane_addr + Lay::o_col + (uint32_t)(w * 128 + half * HD);
-    float m = neg_inf(), l0 = 0.f, l1 = 0.f;      // m: the reference, in log2 units; -inf: no key seen yet
-    bool ok = true;
-    int j = it.part.j0 + (both ? w : 0);
+    uint32_t seen = 0, done = 0;                          // logit tiles of this row tile, items with tiles, so far
 #pragma unroll 1
-    for (int i = 0; i < count; ++i, j += step) {
-      const int key0 = it.tiles.key(j);
-      const bool cut = !it.tiles.all(key0);
-      uint32_t bits[2];
-      if (cut) {
-        bits[0] = paged::seen32(see, key0 + half * 64);
-        bits[1] = paged::seen32(see, key0 + half * 64 + 32);
-      }
-      const bool alive = wait_warp(&sm.s_full[w], i & 1, abort);
-      tc::tc_fence_after();
-      float top;                                // the largest of them, not scaled yet
-      {
-        float x[64];
-        tc::tmem_ld32(s_addr, x);
-        tc::tmem_ld32(s_addr + 32, x + 32);
-        tc::tmem_wait_ld();
-        tc::tmem_pin32(x);
-        tc::tmem_pin32(x + 32);
-        if (__builtin_expect(cut, 0)) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) x[c] = bits[c >> 5] >> (c & 31) & 1 ? x[c] : neg_inf();
-        }
-        top = row_max<64>(x);
-      }
-      // Both warps of the rows stop together when a P would pass 2^kTop (the scale is positive, so the
-      // largest logit has the largest P), or at a row's first key; of their rows only those that need
-      // it move the reference, so that no row's roundings hang on its neighbours' keys.
-      if (__builtin_expect(tc::named_bar_or(pair_bar, 64, fmaf(top, sl2, -m) > kTop || i == 0 || !alive), 0)) {
-        float mt = top * sl2;
-        sm.ex[half][w][row] = mt;
-        // the warps leave together as well
-        if (tc::named_bar_or(pair_bar, 64, !alive)) {
-          ok = false;
-          break;
-        }
-        mt = fmaxf(mt, sm.ex[half ^ 1][w][row]);
-        float f = 1.f;
-        if (mt - m > kTop) {
-          f = ex2f(m - mt);                     // 0 at the first key
-          m = mt;
-          l0 *= f;
-          l1 *= f;
-        }
+    for (int x = 0; next; ++x) {
+      const Item& it = *next;
+      const int T = it.T;
+      const bool partial = it.slot >= 0, both = it.nt == 1;   // both: one row tile, even key tiles and odd key tiles
+      const uint32_t i0 = (both ? 0u : (uint32_t)(w * (kRT * kCta))) + (uint32_t)(rank * kRT + row);
+      const bool has = it.r0 + i0 < it.rows, mine = !(both && w == 1);
+      const RowOf at = row_of(a, it, has ? it.r0 + i0 : it.rows - 1);    // a row that is not there: as the last
+      const paged::Sees see = paged::sees(a, it.s, at.t);
+      const int step = both ? 2 : 1, count = both ? (T - w + 1) >> 1 : T;      // this row tile's key tiles
+      if (mine && T > 0) {
+        tc::cp_async_wait<0>();
+        tc::fence_proxy_async();
         __syncwarp();
-        if (i > 0) {
-          // O holds the products of the tiles before: these logits were issued after them, by the
-          // same thread, and their arrival says that all it had issued is complete
+        if (lane == 0) arrive_issuer<kCta>(&sm.q_full[w]);
+      }
+      float m = neg_inf(), l0 = 0.f, l1 = 0.f;      // m: the reference, in log2 units; -inf: no key seen yet
+      int j = it.j0 + (both ? w : 0);
 #pragma unroll 1
-          for (int c = 0; c < HD; c += 16) {
-            float o[16];
-            tc::tmem_ld16(o_addr + (uint32_t)c, o);
-            tc::tmem_wait_ld();
-            tc::tmem_pin16(o);
-            uint32_t ou[16];
+      for (int i = 0; i < count; ++i, j += step) {
+        const int key0 = it.tiles.key(j);
+        const bool cut = !it.tiles.all(key0);
+        uint32_t bits[2];
+        if (cut) {
+          bits[0] = paged::seen32(see, key0 + half * 64);
+          bits[1] = paged::seen32(see, key0 + half * 64 + 32);
+        }
+        const bool alive = wait_warp(&sm.s_full[w], (seen + i) & 1, abort);
+        tc::tc_fence_after();
+        float top;                                // the largest of them, not scaled yet
+        {
+          float x[64];
+          tc::tmem_ld32(s_addr, x);
+          tc::tmem_ld32(s_addr + 32, x + 32);
+          tc::tmem_wait_ld();
+          tc::tmem_pin32(x);
+          tc::tmem_pin32(x + 32);
+          if (__builtin_expect(cut, 0)) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) ou[e] = __float_as_uint(o[e] * f);
-            tmem_st16(o_addr + (uint32_t)c, ou);
+            for (int c = 0; c < 64; ++c) x[c] = bits[c >> 5] >> (c & 31) & 1 ? x[c] : neg_inf();
           }
+          top = row_max<64>(x);
+        }
+        // Both warps of the rows stop together when a P would pass 2^kTop (the scale is positive, so the
+        // largest logit has the largest P), or at a row's first key; of their rows only those that need
+        // it move the reference, so that no row's roundings hang on its neighbours' keys.
+        if (__builtin_expect(tc::named_bar_or(pair_bar, 64, fmaf(top, sl2, -m) > kTop || i == 0 || !alive), 0)) {
+          float mt = top * sl2;
+          sm.ex[half][w][row] = mt;
+          // the warps leave together as well
+          if (tc::named_bar_or(pair_bar, 64, !alive)) {
+            ok = false;
+            break;
+          }
+          mt = fmaxf(mt, sm.ex[half ^ 1][w][row]);
+          float f = 1.f;
+          if (mt - m > kTop) {
+            f = ex2f(m - mt);                     // 0 at the first key
+            m = mt;
+            l0 *= f;
+            l1 *= f;
+          }
+          __syncwarp();
+          if (i > 0) {
+            // O holds the products of the tiles before: these logits were issued after them, by the
+            // same thread, and their arrival says that all it had issued is complete
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 16) {
+              float o[16];
+              tc::tmem_ld16(o_addr + (uint32_t)c, o);
+              tc::tmem_wait_ld();
+              tc::tmem_pin16(o);
+              uint32_t ou[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ou[e] = __float_as_uint(o[e] * f);
+              tmem_st16(o_addr + (uint32_t)c, ou);
+            }
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+            tc::named_bar(pair_bar, 64);                    // all of O is rescaled before either half's P goes
+            tc::tc_fence_after();
+          }
+        }
+        const float nm = m == neg_inf() ? 0.f : -m;
+        // P over the logits' own columns: 32 logits are read again (held since the maximum, 64 took
+        // registers that the loads and exponentials need to overlap) and become 16 columns, over
+        // logits that have been read
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float x[32];
+          tc::tmem_ld32(s_addr + (uint32_t)(32 * c), x);
+          tc::tmem_wait_ld();
+          tc::tmem_pin32(x);
+          if (__builtin_expect(cut, 0)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = bits[c] >> e & 1 ? x[e] : neg_inf();
+          }
+          row_exp32(x, sl2, nm, s_addr + (uint32_t)(16 * c), l0, l1);
           tc::tmem_wait_st();
           tc::tc_fence_before();
-          tc::named_bar(pair_bar, 64);                    // all of O is rescaled before either half's P goes
-          tc::tc_fence_after();
+          __syncwarp();
+          if (lane == 0) arrive_issuer<kCta>(&sm.p_full[w][c]);
         }
       }
-      const float nm = m == neg_inf() ? 0.f : -m;
-      // P over the logits' own columns: 32 logits are read again (held since the maximum, 64 took
-      // registers that the loads and exponentials need to overlap) and become 16 columns, over
-      // logits that have been read
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float x[32];
-        tc::tmem_ld32(s_addr + (uint32_t)(32 * c), x);
-        tc::tmem_wait_ld();
-        tc::tmem_pin32(x);
-        if (__builtin_expect(cut, 0)) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = bits[c] >> e & 1 ? x[e] : neg_inf();
-        }
-        row_exp32(x, sl2, nm, s_addr + (uint32_t)(16 * c), l0, l1);
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_issuer<kCta>(&sm.p_full[w][c]);
+      seen += (uint32_t)count;
+      if (T > 0) {
+        ok = ok && wait_warp(&sm.fin, done & 1, abort);
+        ++done;
+        tc::tc_fence_after();
       }
-    }
-    // the outputs; barriers first, so that every thread passes them whatever has failed
-    ok = wait_warp(&sm.fin, 0, abort) && ok;
-    tc::tc_fence_after();
-    float l = l0 + l1;
-    sm.ex[half][w][row] = l;
-    float4* shared_o = reinterpret_cast<float4*>(base + Lay::odd_o);   // Q, or K, has been used
-    constexpr int CH = D / 4;                                       // 16-byte chunks of a row
-    if (both && w == 1) {
-      if (half == 0) sm.mx[row] = m;
-      if (ok && count > 0)
-#pragma unroll 1
-        for (int c = 0; c < HD; c += 16) {
-          float o[16];
-          tc::tmem_ld16(o_addr + (uint32_t)c, o);
-          tc::tmem_wait_ld();
-          tc::tmem_pin16(o);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            shared_o[row * CH + (((half * HD + c) / 4 + e) ^ (row & (CH - 1)))] =
-                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        }
-    }
-    tc::named_bar(9, kSoftWarps * 32);
-    l += sm.ex[half ^ 1][w][row];
-    if (ok && !(both && w == 1)) {
+      // the next item's queries set out; Q has been used
+      bool more;
+      next = item_at(x + 1, more);
+      ok = ok && more;
+      // a group of warps that exchange results leaves together
+      float l = l0 + l1;
+      sm.ex[half][w][row] = l;
+      if (both && w == 1 && half == 0) sm.mx[row] = m;
+      if (!(both ? tc::named_bar_and(both_bar, 128, ok) : tc::named_bar_and(pair_bar, 64, ok))) {
+        ok = false;
+        break;
+      }
+      if (next && next->T > 0) bring_q(*next);
+      l += sm.ex[half ^ 1][w][row];
       float f0 = 1.f, f1 = 0.f;             // weights of this sum and of the odd tiles'
-      if (both && T > 1) {
+      if (mine && both && T > 1) {
         const float lo = sm.ex[0][1][row] + sm.ex[1][1][row], mo = sm.mx[row];
         if (lo != 0.f) {                    // the odd tiles hold a key that the row sees
           const float mn = fmaxf(m, mo);
@@ -384,80 +359,98 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         }
       }
       const bool live = l > 0.f || l != l;
-      const bool poison = *(volatile int*)&sm.poison != 0;
-      const float f = partial ? 1.f : live ? 1.f / l : 0.f;
-      // Rows of 128 bytes (32 fp32 or 64 bf16 channels; 64 bytes of 32 bf16) go through shared
-      // memory (the ring of K, or of V, has been used), so that they leave as whole runs
-      uint8_t* stg = base + Lay::out + warp * 4096;
+      const bool poison = *(volatile int*)&sm.poison[x % paged::kItems] == x + 1;
+      const float f = live ? 1.f / l : 0.f;
+      // Rows of 64 bytes (16 fp32 or 32 bf16 channels) go through shared memory, so that they leave as whole runs
+      uint8_t* stg = base + Lay::out + warp * 2048;
+      const uint8_t* odd = base + Lay::out + (warp + 8) * 2048;        // (both) the odd tiles' 16 channels
       uint8_t* out = partial ? reinterpret_cast<uint8_t*>(a.part_o) : static_cast<uint8_t*>(a.out);
-      const int64_t tok = it.s.t0 + at.t;
-      const int64_t prow = paged::partial_row(a, (int64_t)it.split * a.B + it.b, it.h, (int)r);
+      const int64_t tok = it.s.t0 + at.t, prow = (int64_t)it.slot * kPer + i0;
       const int64_t off = !has      ? -1
                           : partial ? (prow * D + half * HD) * 4
                                     : (at.head * a.o_hs + tok * a.o_ts + half * HD) * 2;
-      const int cp = partial ? 32 : HD, esz = partial ? 4 : 2;   // channels a pass
-      const int nc = HD == 64 ? 8 : cp * esz / 16;               // 16-byte chunks of a pass's row
 #pragma unroll 1
-      for (int c0 = 0; c0 < HD; c0 += cp) {
-#pragma unroll 1
-        for (int c = c0; c < c0 + cp; c += 16) {
-          float o[16];
-          __syncwarp();
-          tc::tmem_ld16(o_addr + (uint32_t)c, o);
+      for (int c = 0; c < HD; c += 32) {
+        float o[32];
+        if (count > 0) {
+          tc::tmem_ld32(o_addr + (uint32_t)c, o);
           tc::tmem_wait_ld();
-          tc::tmem_pin16(o);
-          if (f1 != 0.f) {
+          tc::tmem_pin32(o);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 v = shared_o[row * CH + (((half * HD + c) / 4 + e) ^ (row & (CH - 1)))];
-              o[4 * e] = o[4 * e] * f0 + v.x * f1;
-              o[4 * e + 1] = o[4 * e + 1] * f0 + v.y * f1;
-              o[4 * e + 2] = o[4 * e + 2] * f0 + v.z * f1;
-              o[4 * e + 3] = o[4 * e + 3] * f0 + v.w * f1;
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+        if (both) {                         // the odd tiles' part: 16 channels at a time through its warp's place
+#pragma unroll
+          for (int d = 0; d < 32; d += 16) {
+            if (w == 1) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<float4*>(stg + out_off(lane, e)) =
+                    make_float4(o[d + 4 * e], o[d + 4 * e + 1], o[d + 4 * e + 2], o[d + 4 * e + 3]);
             }
+            tc::named_bar(both_bar, 128);
+            if (w == 0 && f1 != 0.f) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float4 v = *reinterpret_cast<const float4*>(odd + out_off(lane, e));
+                o[d + 4 * e] = o[d + 4 * e] * f0 + v.x * f1;
+                o[d + 4 * e + 1] = o[d + 4 * e + 1] * f0 + v.y * f1;
+                o[d + 4 * e + 2] = o[d + 4 * e + 2] * f0 + v.z * f1;
+                o[d + 4 * e + 3] = o[d + 4 * e + 3] * f0 + v.w * f1;
+              }
+            }
+            tc::named_bar(both_bar, 128);
           }
-          if (__builtin_expect(poison, 0)) {
+          if (w == 1) continue;
+        }
+        if (__builtin_expect(poison, 0)) {
+          const paged::Split part{1, it.j0, it.j0 + it.T};
+#pragma unroll
+          for (int d = 0; d < 32; d += 16) {
             float q[16];                    // a copy: o's registers keep no address
 #pragma unroll
-            for (int e = 0; e < 16; ++e) q[e] = o[e];
-            paged::add_taken_out<kKT, 16>(a, it.tiles, it.part, it.b, it.h, see, half * HD + c, q);
+            for (int e = 0; e < 16; ++e) q[e] = o[d + e];
+            paged::add_taken_out<kKT, 16>(a, it.tiles, part, it.b, it.h, see, half * HD + c + d, q);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = q[e];
+            for (int e = 0; e < 16; ++e) o[d + e] = q[e];
           }
-          const int ch = (c - c0) * esz / 16;
-          if (partial) {
+        }
+        if (partial) {
+#pragma unroll
+          for (int d = 0; d < 32; d += 16) {
+            __syncwarp();
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<float4*>(stg + tc::sw128_off(lane, ch + e)) =
-                  make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t v[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                v[k] = live ? pack_bf16(o[8 * e + 2 * k] * f, o[8 * e + 2 * k + 1] * f) : 0u;
-              *reinterpret_cast<uint4*>(stg + tc::sw128_off(lane, ch + e)) = make_uint4(v[0], v[1], v[2], v[3]);
-            }
+              *reinterpret_cast<float4*>(stg + out_off(lane, e)) =
+                  make_float4(o[d + 4 * e], o[d + 4 * e + 1], o[d + 4 * e + 2], o[d + 4 * e + 3]);
+            __syncwarp();
+            store_rows(out + (c + d) * 4, off, stg, lane);
           }
+        } else {
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              v[k] = live ? pack_bf16(o[8 * e + 2 * k] * f, o[8 * e + 2 * k + 1] * f) : 0u;
+            *reinterpret_cast<uint4*>(stg + out_off(lane, e)) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+          __syncwarp();
+          store_rows(out + c * 2, off, stg, lane);
         }
-        __syncwarp();
-#pragma unroll 4
-        for (int i = 0; i < nc; ++i) {
-          const int sr = (i * 32 + lane) / nc, ch = (i * 32 + lane) % nc;
-          const int64_t to = __shfl_sync(0xffffffffu, off, sr);
-          const uint4 v = *reinterpret_cast<const uint4*>(stg + tc::sw128_off(sr, ch));
-          if (to >= 0) *reinterpret_cast<uint4*>(out + to + c0 * esz + ch * 16) = v;
-        }
-        __syncwarp();
       }
-      if (has && half == 0) {
+      tc::tc_fence_before();                // O has been read: the next item's products, which this warp's P let go
+      if (has && half == 0 && mine) {
         const float mn = m * 0.6931471805599453f;
         if (partial)
           a.part_ml[prow] = make_float2(live ? mn : neg_inf(), l);
         else if (a.lse)
           a.lse[at.head * a.T + tok] = live ? mn + logf(l) : neg_inf();
       }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.item_free[x % paged::kItems]);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
@@ -467,99 +460,143 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       tc::named_bar(10, (kSoftWarps + 1) * 32);
       tc::tc_fence_after();
     }
-    if (kCta == 2) pair_wait();
+    if (warp != kCopyWarp && kCta == 2) pair_wait();
     if (warp == kCopyWarp) {
-      // ---------------- K and V into shared memory ----------------
+      // ---------------- the work, and K and V into shared memory ----------------
+      Share share;
+      paged::find_share(a, share, (int)blockIdx.x / kCta, kPer);
       const int shift = a.pool.page_shift, page = 1 << shift;
       const int kr = min(page, Lay::KR), vr = min(page, kKT);      // rows of a box
       const int nk = Lay::KR / kr * (D / 64), nv = kKT / vr * (Lay::VC / 64);
-      const int32_t* table = a.table + (int64_t)it.b * a.max_pages;
       const int none = (int)a.pool.pages;                          // past the pool: the box comes as zeros
       const int kb = lane / (D / 64), kc = lane % (D / 64);        // this lane's box: rows, channels
       const int vb = lane / (Lay::VC / 64), vc = lane % (Lay::VC / 64);
-      auto page_at = [&](int key, int n) {
-        if (!it.tiles.any(key, key + n)) return none;
-        const int x = paged::page_of(table, key >> shift, a.pool.pages, a.status);
-        return x < 0 ? none : x;
-      };
       int kn = 0, vn = 0;                                          // tiles asked for
-      // the pages of a tile are looked up while the one before is asked for
-      int kp = none, vp = none;
-      auto look = [&](int i) {
-        const int key = it.tiles.key(it.part.j0 + i);
-        if (lane < nk) kp = page_at(key + rank * Lay::KR + kb * kr, kr);
-        if (lane < nv) vp = page_at(key + vb * vr, vr);
-      };
-      look(0);
-      for (int i = 0; i < T; ++i) {
-        const int key = it.tiles.key(it.part.j0 + i);
-        const int kp0 = kp, vp0 = vp;
-        if (i + 1 < T) look(i + 1);
-        int st = i % Lay::ks;
-        if (!wait_warp(&sm.k_empty[st], ((i / Lay::ks) & 1) ^ 1, abort)) break;
-        if (lane == 0) tc::mbar_arrive_tx(&sm.k_land[st], (uint32_t)Lay::k_tile);
+      bool ok = true;
+#pragma unroll 1
+      for (int x = 0; ok; ++x) {
+        Item it;
+        paged::next_item(a, share, it, kPer);
+        if (!(ok = wait_warp(&sm.item_free[x % paged::kItems], ((x / paged::kItems) & 1) ^ 1, abort))) break;
+        if (lane == 0) {
+          sm.item[x % paged::kItems] = it;
+          tc::mbar_arrive(&sm.item_full[x % paged::kItems]);
+        }
         __syncwarp();
-        if (lane < nk)
-          tc::tma_load_4d(base + Lay::k + st * Lay::k_tile + kc * Lay::k_blk + kb * kr * 128, &kmap, kc * 64,
-                          (key + rank * Lay::KR + kb * kr) & (page - 1), it.h, kp0, &sm.k_land[st]);
-        ++kn;
-        st = i % Lay::vs;
-        if (!wait_warp(&sm.v_empty[st], ((i / Lay::vs) & 1) ^ 1, abort)) break;
-        if (lane == 0) tc::mbar_arrive_tx(&sm.v_land[st], (uint32_t)Lay::v_tile);
-        __syncwarp();
-        if (lane < nv)
-          tc::tma_load_4d(base + Lay::v + st * Lay::v_tile + vc * Lay::v_blk + vb * vr * 128, &vmap,
-                          rank * Lay::VC + vc * 64, (key + vb * vr) & (page - 1), it.h, vp0, &sm.v_land[st]);
-        ++vn;
+        if (x == 0) {
+          if (rank == 0 && a.part_o) paged::write_cut(share, it, static_cast<paged::Cut*>(a.cuts) + share.p);
+          if (kCta == 2) pair_wait();
+        }
+        if (it.nt == 0) break;
+        const int32_t* table = a.table + (int64_t)it.b * a.max_pages;
+        auto page_at = [&](int key, int n) {
+          if (!it.tiles.any(key, key + n)) return none;
+          const int y = paged::page_of(table, key >> shift, a.pool.pages, a.status);
+          return y < 0 ? none : y;
+        };
+        // the pages of a tile are looked up while the one before is asked for
+        int kp = none, vp = none;
+        auto look = [&](int i) {
+          const int key = it.tiles.key(it.j0 + i);
+          if (lane < nk) kp = page_at(key + rank * Lay::KR + kb * kr, kr);
+          if (lane < nv) vp = page_at(key + vb * vr, vr);
+        };
+        if (it.T > 0) look(0);
+#pragma unroll 1
+        for (int i = 0; i < it.T; ++i) {
+          const int key = it.tiles.key(it.j0 + i);
+          const int kp0 = kp, vp0 = vp;
+          if (i + 1 < it.T) look(i + 1);
+          int st = kn % Lay::ks;
+          if (!(ok = wait_warp(&sm.k_empty[st], ((kn / Lay::ks) & 1) ^ 1, abort))) break;
+          if (lane == 0) tc::mbar_arrive_tx(&sm.k_land[st], (uint32_t)Lay::k_tile);
+          __syncwarp();
+          if (lane < nk)
+            tc::tma_load_4d(base + Lay::k + st * Lay::k_tile + kc * Lay::k_blk + kb * kr * 128, &kmap, kc * 64,
+                            (key + rank * Lay::KR + kb * kr) & (page - 1), it.h, kp0, &sm.k_land[st]);
+          ++kn;
+          st = vn % Lay::vs;
+          if (!(ok = wait_warp(&sm.v_empty[st], ((vn / Lay::vs) & 1) ^ 1, abort))) break;
+          if (lane == 0) tc::mbar_arrive_tx(&sm.v_land[st], (uint32_t)Lay::v_tile);
+          __syncwarp();
+          if (lane < nv)
+            tc::tma_load_4d(base + Lay::v + st * Lay::v_tile + vc * Lay::v_blk + vb * vr * 128, &vmap,
+                            rank * Lay::VC + vc * 64, (key + vb * vr) & (page - 1), it.h, vp0, &sm.v_land[st]);
+          ++vn;
+        }
       }
       // the last copies land before this warp leaves, whether or not anyone waits for them
       volatile int never = 0;
-      for (int x = max(0, kn - Lay::ks); x < kn; ++x)
-        tc::mbar_wait(&sm.k_land[x % Lay::ks], (x / Lay::ks) & 1, &never, 400000000LL);
-      for (int x = max(0, vn - Lay::vs); x < vn; ++x)
-        tc::mbar_wait(&sm.v_land[x % Lay::vs], (x / Lay::vs) & 1, &never, 400000000LL);
-    } else if (warp == kKWarp && lane == 0) {
+      for (int y = max(0, kn - Lay::ks); y < kn; ++y)
+        tc::mbar_wait(&sm.k_land[y % Lay::ks], (y / Lay::ks) & 1, &never, 400000000LL);
+      for (int y = max(0, vn - Lay::vs); y < vn; ++y)
+        tc::mbar_wait(&sm.v_land[y % Lay::vs], (y / Lay::vs) & 1, &never, 400000000LL);
+    } else if (warp == kKWarp) {
       // ---------------- K tiles handed on ----------------
-      for (int i = 0; i < T; ++i) {
-        if (!tc::mbar_wait(&sm.k_land[i % Lay::ks], (i / Lay::ks) & 1, abort)) break;
-        arrive_issuer<kCta>(&sm.k_full[i % Lay::ks]);
+      bool ok;
+      int n = 0;
+      for (int x = 0; const Item* it = item_at(x, ok); ++x) {
+        const int end = n + it->T;
+        for (; n < end && (ok = wait_warp(&sm.k_land[n % Lay::ks], (n / Lay::ks) & 1, abort)); ++n)
+          if (lane == 0) arrive_issuer<kCta>(&sm.k_full[n % Lay::ks]);
+        if (!ok) break;
+        if (lane == 0) tc::mbar_arrive(&sm.item_free[x % paged::kItems]);
       }
     } else if (warp == kVWarp) {
       // ---------------- V tiles looked into and handed on ----------------
-      for (int i = 0; i < T; ++i) {
-        const int st = i % Lay::vs, key0 = it.tiles.key(it.part.j0 + i);
-        if (!wait_warp(&sm.v_land[st], (i / Lay::vs) & 1, abort)) break;
-        if (!it.tiles.all(key0)) {
-          uint8_t* tile = base + Lay::v + st * Lay::v_tile;
-          bool found = false;
+      bool ok;
+      int n = 0;
+      for (int x = 0; const Item* item = item_at(x, ok); ++x) {
+        const Item& it = *item;
+        for (int i = 0; i < it.T; ++i, ++n) {
+          const int st = n % Lay::vs, key0 = it.tiles.key(it.j0 + i);
+          if (!(ok = wait_warp(&sm.v_land[st], (n / Lay::vs) & 1, abort))) break;
+          if (!it.tiles.all(key0)) {
+            uint8_t* tile = base + Lay::v + st * Lay::v_tile;
+            // 8 chunks of 8 channels of a row on their way at once
+            uint32_t big = 0;
 #pragma unroll 1
-          for (int x = lane; x < kKT; x += 32) {
-            const bool any = it.tiles.any(key0 + x);
+            for (int r = lane; r < kKT * (Lay::VC / 64); r += 32) {
+              const uint8_t* line = tile + (r >> 7) * Lay::v_blk;
+              uint4 u[8];
+#pragma unroll
+              for (int c = 0; c < 8; ++c) u[c] = *reinterpret_cast<const uint4*>(line + tc::sw128_off(r & 127, c));
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                big = __vmaxu2(big, __vmaxu2(__vmaxu2(u[c].x & 0x7fff7fffu, u[c].y & 0x7fff7fffu),
+                                             __vmaxu2(u[c].z & 0x7fff7fffu, u[c].w & 0x7fff7fffu)));
+            }
+            bool found = false;
+            if (__any_sync(0xffffffffu, (big & 0xffffu) >= 0x7f80u || (big >> 16) >= 0x7f80u)) {
 #pragma unroll 1
-            for (int c = 0; c < Lay::VC / 8; ++c) {
-              uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * Lay::v_blk + tc::sw128_off(x, c & 7));
-              if (!any) {
-                *p = make_uint4(0, 0, 0, 0);
-                continue;
+              for (int r = lane; r < kKT; r += 32) {
+                const bool any = it.tiles.any(key0 + r);
+#pragma unroll 1
+                for (int c = 0; c < Lay::VC / 8; ++c) {
+                  uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * Lay::v_blk + tc::sw128_off(r, c & 7));
+                  if (any) found |= paged::take_out(p);
+                  else *p = make_uint4(0, 0, 0, 0);
+                }
               }
-              found |= paged::take_out(p);
+            }
+            tc::fence_proxy_async();
+            if (__any_sync(0xffffffffu, found) && lane == 0) {
+              *(volatile int*)&sm.poison[x % paged::kItems] = x + 1;
+              if (kCta == 2) {               // the other CTA's rows see these channels too
+                asm volatile(
+                    "{\n .reg .b32 p;\n mapa.shared::cluster.u32 p, %0, %1;\n st.shared::cluster.u32 [p], %2;\n}\n" ::"r"(
+                        tc::smem_u32(&sm.poison[x % paged::kItems])),
+                    "r"(rank ^ 1), "r"(x + 1)
+                    : "memory");
+                asm volatile("fence.acq_rel.cluster;" ::: "memory");
+              }
             }
           }
-          tc::fence_proxy_async();
-          if (__any_sync(0xffffffffu, found) && lane == 0) {
-            *(volatile int*)&sm.poison = 1;
-            if (kCta == 2) {               // the other CTA's rows see these channels too
-              asm volatile(
-                  "{\n .reg .b32 p;\n mapa.shared::cluster.u32 p, %0, %1;\n st.shared::cluster.u32 [p], %2;\n}\n" ::"r"(
-                      tc::smem_u32(&sm.poison)),
-                  "r"(rank ^ 1), "r"(1)
-                  : "memory");
-              asm volatile("fence.acq_rel.cluster;" ::: "memory");
-            }
-          }
+          __syncwarp();
+          if (lane == 0) arrive_issuer<kCta>(&sm.v_full[st]);
         }
-        __syncwarp();
-        if (lane == 0) arrive_issuer<kCta>(&sm.v_full[st]);
+        if (!ok) break;
+        if (lane == 0) tc::mbar_arrive(&sm.item_free[x % paged::kItems]);
       }
     }
     // ---------------- MMA issue (one thread of the pair) ----------------
@@ -570,62 +607,84 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       const uint64_t k_desc = tc::sw128_desc(tc::smem_u32(base + Lay::k));
       const uint64_t v_desc = tc::sw128_mn_desc(tc::smem_u32(base + Lay::v), Lay::v_blk);
       bool ok = true;
-      const int step = both ? 2 : 1;
-      int kst[2], vst[2], count[2];                       // stages of K and V, key tiles by row tile
-      uint32_t kph[2], vph[2];
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        kst[w] = vst[w] = both ? w : 0;
-        kph[w] = vph[w] = 0;
-        count[w] = both ? (T - w + 1) >> 1 : T;
-      }
+      uint32_t tiles = 0, qn[2] = {0, 0}, pn[2] = {0, 0};  // key tiles, query and P tiles by row tile, so far
+      uint32_t items = 0;
 #pragma unroll 1
-      for (int i = -1; i < count[0] && ok; ++i) {         // P V of tile i (from 0 on), Q K^T of tile i + 1
+      for (int x = 0; ok; ++x) {
+        ok = tc::mbar_wait(&sm.item_full[x % paged::kItems], (x / paged::kItems) & 1, abort);
+        if (!ok || sm.item[x % paged::kItems].nt == 0) break;
+        const int T = sm.item[x % paged::kItems].T;
+        const bool both = sm.item[x % paged::kItems].nt == 1;
+        tc::mbar_arrive(&sm.item_free[x % paged::kItems]);     // all that is read of it
+        if (T == 0) continue;
+        const int step = both ? 2 : 1;
+        int kst[2], vst[2], count[2];                     // stages of K and V, key tiles by row tile
+        uint32_t kph[2], vph[2];
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {                     // unrolled: columns are constants
-          if (i >= 0 && i < count[w]) {
-            ok = tc::mbar_wait(&sm.v_full[vst[w]], vph[w], abort);
-            if (!ok) break;
-            const uint64_t vd = v_desc + ((vst[w] * Lay::v_tile) >> 4);
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t first = tiles + (both ? w : 0);
+          kst[w] = (int)(first % Lay::ks), kph[w] = first / Lay::ks & 1;
+          vst[w] = (int)(first % Lay::vs), vph[w] = first / Lay::vs & 1;
+          count[w] = both ? (T - w + 1) >> 1 : T;
+        }
+#pragma unroll 1
+        for (int i = -1; i < count[0] && ok; ++i) {       // P V of tile i (from 0 on), Q K^T of tile i + 1
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {                 // 32 keys of both halves at a time, as their P lands
-              ok = tc::mbar_wait(&sm.p_full[w][c], i & 1, abort);
+          for (int w = 0; w < 2; ++w) {                   // unrolled: columns are constants
+            if (i >= 0 && i < count[w]) {
+              ok = tc::mbar_wait(&sm.v_full[vst[w]], vph[w], abort);
+              if (!ok) break;
+              const uint64_t vd = v_desc + ((vst[w] * Lay::v_tile) >> 4);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {               // 32 keys of both halves at a time, as their P lands
+                ok = tc::mbar_wait(&sm.p_full[w][c], (pn[w] + i) & 1, abort);
+                if (!ok) break;
+                tc::tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int key = (k >> 1) * 64 + c * 32 + (k & 1) * 16;
+                  mma_ts<kCta>(tmem + Lay::o_col + w * 128,
+                               tmem + Lay::s_col + w * 128 + (k >> 1) * 64 + c * 16 + (k & 1) * 8, vd + ((key * 128) >> 4),
+                               idesc_pv, i > 0 || c > 0 || k > 0 ? 1u : 0u);
+                }
+              }
+              if (!ok) break;
+              if (w == 1 || both) commit<kCta>(&sm.v_empty[vst[w]]);
+              vst[w] += step;
+              if (vst[w] >= Lay::vs) vst[w] -= Lay::vs, vph[w] ^= 1;
+            }
+            if (i + 1 < count[w]) {
+              ok = (i >= 0 || (both && w == 1) || tc::mbar_wait(&sm.q_full[w], qn[w] & 1, abort)) &&
+                   tc::mbar_wait(&sm.k_full[kst[w]], kph[w], abort);
               if (!ok) break;
               tc::tc_fence_after();
+              const uint64_t qd = q_desc + (((both ? 0 : w) * Lay::q_tile) >> 4);
+              const uint64_t kd = k_desc + ((kst[w] * Lay::k_tile) >> 4);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int key = (k >> 1) * 64 + c * 32 + (k & 1) * 16;
-                mma_ts<kCta>(tmem + Lay::o_col + w * 128, tmem + Lay::s_col + w * 128 + (k >> 1) * 64 + c * 16 + (k & 1) * 8,
-                             vd + ((key * 128) >> 4), idesc_pv, i > 0 || c > 0 || k > 0 ? 1u : 0u);
-              }
+              for (int k = 0; k < D / 16; ++k)
+                mma_ss<kCta>(tmem + Lay::s_col + w * 128, qd + (((k >> 2) * Lay::q_blk + (k & 3) * 32) >> 4),
+                             kd + (((k >> 2) * Lay::k_blk + (k & 3) * 32) >> 4), idesc_qk, k > 0 ? 1u : 0u);
+              commit<kCta>(&sm.s_full[w]);
+              if (w == 1 || both) commit<kCta>(&sm.k_empty[kst[w]]);
+              kst[w] += step;
+              if (kst[w] >= Lay::ks) kst[w] -= Lay::ks, kph[w] ^= 1;
             }
-            if (!ok) break;
-            if (w == 1 || both) commit<kCta>(&sm.v_empty[vst[w]]);
-            vst[w] += step;
-            if (vst[w] >= Lay::vs) vst[w] -= Lay::vs, vph[w] ^= 1;
-          }
-          if (i + 1 < count[w]) {
-            ok = (i >= 0 || tc::mbar_wait(&sm.q_full[both ? 0 : w], 0, abort)) &&
-                 tc::mbar_wait(&sm.k_full[kst[w]], kph[w], abort);
-            if (!ok) break;
-            tc::tc_fence_after();
-            const uint64_t qd = q_desc + (((both ? 0 : w) * Lay::q_tile) >> 4);
-            const uint64_t kd = k_desc + ((kst[w] * Lay::k_tile) >> 4);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ss<kCta>(tmem + Lay::s_col + w * 128, qd + (((k >> 2) * Lay::q_blk + (k & 3) * 32) >> 4),
-                           kd + (((k >> 2) * Lay::k_blk + (k & 3) * 32) >> 4), idesc_qk, k > 0 ? 1u : 0u);
-            commit<kCta>(&sm.s_full[w]);
-            if (w == 1 || both) commit<kCta>(&sm.k_empty[kst[w]]);
-            kst[w] += step;
-            if (kst[w] >= Lay::ks) kst[w] -= Lay::ks, kph[w] ^= 1;
           }
         }
+        if (!ok) break;
+        commit<kCta>(&sm.fin);                            // the item's outputs are complete
+        ++items;
+        tiles += (uint32_t)T;
+        ++qn[0];
+        if (!both) ++qn[1];
+        pn[0] += (uint32_t)count[0], pn[1] += (uint32_t)count[1];
       }
-      // the outputs are complete; and every issued product ends before TMEM is given back
-      commit<kCta>(&sm.fin);
-      volatile int never = 0;
-      tc::mbar_wait(&sm.fin, 0, &never, 400000000LL);
+      // every issued product ends before TMEM is given back
+      if (!ok) {
+        commit<kCta>(&sm.fin);
+        volatile int never = 0;
+        tc::mbar_wait(&sm.fin, items & 1, &never, 400000000LL);
+      }
     }
   }
   tc::tc_fence_before();
@@ -643,13 +702,83 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   if (threadIdx.x == 0 && sm.abort) flag_status(a.status, FASTAR_DEV_TIMEOUT);
 }
 
+// ---- joining cut items -----------------------------------------------------------------------
+// O = sum_s e^(m_s - m) o_s / sum_s e^(m_s - m) l_s over the parts of an item, m = max_s m_s, in the order of the
+// keys; one warp a row, D / 32 channels a lane.  Bound: latency, so that what a warp's rows need of the first
+// kAtOnce parts sets out together (an item seldom has more than three).
+template <int D>
+__global__ void __launch_bounds__(256) paged_tc_join_kernel(const PagedAttnArgs a, int per) {
+  constexpr int CPL = D / 32, kAtOnce = 4, kRows = kJoinRows / 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  const paged::Cut& cut = static_cast<const paged::Cut*>(a.cuts)[blockIdx.x];
+  const int n = cut.parts, i0 = blockIdx.y * kJoinRows + warp * kRows;
+  const uint32_t r0 = cut.r0, rows = cut.rows;
+  const int t0 = cut.t0, h = cut.h;
+  if (n == 0 || r0 + i0 >= rows) return;
+  float m[kRows], l[kRows], o[kRows][CPL];
+#pragma unroll
+  for (int y = 0; y < kRows; ++y) {
+    m[y] = neg_inf();
+    l[y] = 0.f;
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) o[y][c] = 0.f;
+  }
+#pragma unroll 1
+  for (int s0 = n; s0 > 0; s0 -= kAtOnce) {               // the parts are listed from the last on
+    float2 ml[kRows][kAtOnce];
+    float p[kRows][kAtOnce][CPL];
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e) {
+      const int s = s0 - 1 - e;
+      const int64_t prow = (int64_t)cut.slots[s < 0 ? 0 : s] * per + i0;
+#pragma unroll
+      for (int y = 0; y < kRows; ++y) {
+        const bool in = s >= 0 && r0 + i0 + y < rows;
+        ml[y][e] = in ? a.part_ml[prow + y] : make_float2(neg_inf(), 0.f);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) p[y][e][c] = in ? a.part_o[(prow + y) * D + lane * CPL + c] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < kRows; ++y) {
+      float top = m[y];
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e)
+        if (ml[y][e].y != 0.f) top = fmaxf(top, ml[y][e].x);
+      const float ref = top == neg_inf() ? 0.f : top, f = expf(m[y] - ref);
+      m[y] = top;
+      l[y] *= f;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) o[y][c] *= f;
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) {
+        if (ml[y][e].y == 0.f) continue;
+        const float w = expf(ml[y][e].x - ref);
+        l[y] = fmaf(w, ml[y][e].y, l[y]);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) o[y][c] = fmaf(w, p[y][e][c], o[y][c]);
+      }
+    }
+  }
+#pragma unroll
+  for (int y = 0; y < kRows; ++y) {
+    const uint32_t r = r0 + i0 + y, t = r / (uint32_t)a.group;
+    if (r >= rows) break;
+    const bool live = l[y] > 0.f || l[y] != l[y];
+    const int64_t tok = t0 + (int)t, head = h * a.group + (int)(r - t * (uint32_t)a.group);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + head * a.o_hs + tok * a.o_ts + lane * CPL;
+#pragma unroll
+    for (int c = 0; c < CPL; c += 2)
+      *reinterpret_cast<uint32_t*>(out + c) = live ? pack_bf16(o[y][c] / l[y], o[y][c + 1] / l[y]) : 0u;
+    if (lane == 0 && a.lse) a.lse[head * a.T + tok] = live ? m[y] + logf(l[y]) : neg_inf();
+  }
+}
+
 template <int D, int C>
 cudaError_t tc_go(const PagedAttnArgs& a, cudaStream_t s) {
   using Lay = Layout<D, C>;
-  const int per = 2 * kRT * Lay::kCta;
-  const int64_t rt = ((int64_t)a.group * a.max_q + per - 1) / per;
-  const int64_t blocks = rt * a.Hkv * a.B * a.splits * Lay::kCta;
-  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  constexpr int per = 2 * kRT * Lay::kCta;
   const int page = 1 << a.pool.page_shift;
   CUtensorMap km, vm;
   if (!make_pool_tmap(&km, a, a.pool.k, D, page < Lay::KR ? page : Lay::KR) || !make_pool_tmap(&vm, a, a.pool.v, D, page))
@@ -657,7 +786,7 @@ cudaError_t tc_go(const PagedAttnArgs& a, cudaStream_t s) {
   cudaError_t e = opt_in_smem((const void*)paged_attn_tc_kernel<D, C>, (int)Lay::bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = dim3((unsigned)(a.shares * Lay::kCta));
   cfg.blockDim = dim3(kThreadsT);
   cfg.dynamicSmemBytes = Lay::bytes;
   cfg.stream = s;
@@ -669,12 +798,19 @@ cudaError_t tc_go(const PagedAttnArgs& a, cudaStream_t s) {
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<D, C>, a, km, vm, (int)rt);
+  e = cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<D, C>, a, km, vm);
+  count_launches(1);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess || !a.part_o) return e;
+  e = launch_dependent(paged_tc_join_kernel<D>, dim3((unsigned)a.shares, per / kJoinRows), dim3(256), 0, s, a, per);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
+
+int paged_tc_rows(int d, bool alone) { return d == 128 && !alone ? 512 : 256; }
+size_t paged_tc_cut_bytes() { return sizeof(paged::Cut); }
 
 cudaError_t launch_paged_attn_tc(int d, const PagedAttnArgs& a, bool alone, cudaStream_t s) {
   if (d == 64) return tc_go<64, 1>(a, s);
