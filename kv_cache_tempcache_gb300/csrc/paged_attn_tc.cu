@@ -47,7 +47,7 @@ namespace fastar {
 namespace {
 
 constexpr int kRT = 128;               // rows of a row tile in a CTA
-constexpr int kJoinRows = 16;          // of a block of the join
+constexpr int kJoinRows = 32;          // of a block of the join
 constexpr int kKT = 128;               // keys of a tile
 constexpr int kSoftWarps = 16;
 constexpr int kMmaWarp = kSoftWarps, kCopyWarp = kMmaWarp + 1, kKWarp = kMmaWarp + 2, kVWarp = kMmaWarp + 3;
@@ -252,20 +252,17 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         }
         const bool alive = wait_warp(&sm.s_full[w], (seen + i) & 1, abort);
         tc::tc_fence_after();
-        float top;                                // the largest of them, not scaled yet
-        {
-          float x[64];
-          tc::tmem_ld32(s_addr, x);
-          tc::tmem_ld32(s_addr + 32, x + 32);
-          tc::tmem_wait_ld();
-          tc::tmem_pin32(x);
-          tc::tmem_pin32(x + 32);
-          if (__builtin_expect(cut, 0)) {
+        float x[64];
+        tc::tmem_ld32(s_addr, x);
+        tc::tmem_ld32(s_addr + 32, x + 32);
+        tc::tmem_wait_ld();
+        tc::tmem_pin32(x);
+        tc::tmem_pin32(x + 32);
+        if (__builtin_expect(cut, 0)) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c) x[c] = bits[c >> 5] >> (c & 31) & 1 ? x[c] : neg_inf();
-          }
-          top = row_max<64>(x);
+          for (int c = 0; c < 64; ++c) x[c] = bits[c >> 5] >> (c & 31) & 1 ? x[c] : neg_inf();
         }
+        const float top = row_max<64>(x);         // the largest of them, not scaled yet
         // Both warps of the rows stop together when a P would pass 2^kTop (the scale is positive, so the
         // largest logit has the largest P), or at a row's first key; of their rows only those that need
         // it move the reference, so that no row's roundings hang on its neighbours' keys.
@@ -307,20 +304,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           }
         }
         const float nm = m == neg_inf() ? 0.f : -m;
-        // P over the logits' own columns: 32 logits are read again (held since the maximum, 64 took
-        // registers that the loads and exponentials need to overlap) and become 16 columns, over
-        // logits that have been read
+        // P over the logits' own columns: 32 logits become 16 columns
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float x[32];
-          tc::tmem_ld32(s_addr + (uint32_t)(32 * c), x);
-          tc::tmem_wait_ld();
-          tc::tmem_pin32(x);
-          if (__builtin_expect(cut, 0)) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = bits[c] >> e & 1 ? x[e] : neg_inf();
-          }
-          row_exp32(x, sl2, nm, s_addr + (uint32_t)(16 * c), l0, l1);
+          row_exp32(x + 32 * c, sl2, nm, s_addr + (uint32_t)(16 * c), l0, l1);
           tc::tmem_wait_st();
           tc::tc_fence_before();
           __syncwarp();
@@ -708,7 +695,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 // kAtOnce parts sets out together (an item seldom has more than three).
 template <int D>
 __global__ void __launch_bounds__(256) paged_tc_join_kernel(const PagedAttnArgs a, int per) {
-  constexpr int CPL = D / 32, kAtOnce = 4, kRows = kJoinRows / 8;
+  constexpr int CPL = D / 32, kAtOnce = 2, kRows = kJoinRows / 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   const paged::Cut& cut = static_cast<const paged::Cut*>(a.cuts)[blockIdx.x];

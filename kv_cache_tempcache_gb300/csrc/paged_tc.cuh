@@ -3,7 +3,7 @@
 //
 // An item is up to `per` rows of a (sequence, KV head): its row tiles 2 (or 1, where the rows fill half of them or
 // less), its key tiles paged.cuh's.  It counts kFixed units and kFull (kHalf) for each key tile, as its time
-// goes: 1.45 us a key tile, 0.97 with one row tile, some 6 us around them.  Items lie in a row: sequences,
+// goes: 1.45 us a key tile, 0.97 with one row tile, some 9 us around them.  Items lie in a row: sequences,
 // their row tiles, the KV heads side by side.  Share p of P is the units W p / P .. W (p + 1) / P of that row, so
 // that all shares end together, whatever the lengths: borders cut items between two key tiles (12 heads of 4680
 // tokens are 120 items on 76 pairs of CTAs: in whole items 2 waves, dealt out 1.53).  A cut leaves parts of kMinTiles
@@ -18,7 +18,7 @@
 namespace fastar {
 namespace paged {
 
-constexpr int kFixed = 24, kFull = 6, kHalf = 4, kLeast = 48, kMinTiles = 3;
+constexpr int kFixed = 36, kFull = 6, kHalf = 4, kLeast = 60, kMinTiles = 3;
 constexpr int kMaxShares = 256;          // the plan asks for no more
 constexpr int kItems = 8;                // items of a CTA that are known at once
 
