@@ -47,7 +47,6 @@ namespace fastar {
 namespace {
 
 constexpr int kRT = 128;               // rows of a row tile in a CTA
-constexpr int kJoinRows = 32;          // of a block of the join
 constexpr int kKT = 128;               // keys of a tile
 constexpr int kSoftWarps = 16;
 constexpr int kMmaWarp = kSoftWarps, kCopyWarp = kMmaWarp + 1, kKWarp = kMmaWarp + 2, kVWarp = kMmaWarp + 3;
@@ -72,6 +71,7 @@ struct alignas(16) Ctl {
   int abort;
   float ex[2][2][kRT];                                 // a row's two threads: half, row tile, row
   float mx[kRT];
+  int see[3][2][2][kRT];                               // what the row sees (kept here: the loop needs the registers)
 };
 
 // C CTAs work as one: at d = 64 one, at d = 128 a pair, or one for work of a single row tile (kOne).
@@ -81,7 +81,7 @@ template <int D, int C>
 struct Layout {
   static constexpr int kCta = C;
   static constexpr bool kOne = D > 64 * C;
-  static constexpr int ks = kOne ? 2 : 4, vs = kOne ? 2 : 3;    // tiles of K and of V on their way
+  static constexpr int ks = kOne ? 2 : 3, vs = kOne ? 2 : 4;    // tiles of K and of V on their way
   static constexpr int KR = kKT / kCta, VC = D / C;
   static constexpr size_t q_tile = (size_t)kRT * D * 2, q_blk = kRT * 128;
   static constexpr size_t k_tile = (size_t)KR * D * 2, k_blk = KR * 128;
@@ -212,7 +212,13 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       }
       tc::cp_async_commit();
     };
-    bool ok = true;
+    auto send_q = [&]() {
+      tc::cp_async_wait<0>();
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_issuer<kCta>(&sm.q_full[w]);
+    };
+    bool ok = true, q_sent = false;       // the item's queries have been handed over already
     const Item* next = item_at(0, ok);
     if (next && next->T > 0) bring_q(*next);
     tc::named_bar(10, (kSoftWarps + 1) * 32);             // TMEM is there
@@ -228,17 +234,17 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       const Item& it = *next;
       const int T = it.T;
       const bool partial = it.slot >= 0, both = it.nt == 1;   // both: one row tile, even key tiles and odd key tiles
-      const uint32_t i0 = (both ? 0u : (uint32_t)(w * (kRT * kCta))) + (uint32_t)(rank * kRT + row);
-      const bool has = it.r0 + i0 < it.rows, mine = !(both && w == 1);
-      const RowOf at = row_of(a, it, has ? it.r0 + i0 : it.rows - 1);    // a row that is not there: as the last
-      const paged::Sees see = paged::sees(a, it.s, at.t);
-      const int step = both ? 2 : 1, count = both ? (T - w + 1) >> 1 : T;      // this row tile's key tiles
-      if (mine && T > 0) {
-        tc::cp_async_wait<0>();
-        tc::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) arrive_issuer<kCta>(&sm.q_full[w]);
+      const bool mine = !(both && w == 1);
+      {
+        const uint32_t r = it.r0 + (both ? 0u : (uint32_t)(w * (kRT * kCta))) + (uint32_t)(rank * kRT + row);
+        const paged::Sees see = paged::sees(a, it.s, row_of(a, it, min(r, it.rows - 1)).t);
+        sm.see[0][half][w][row] = see.lo;
+        sm.see[1][half][w][row] = see.hi;
+        sm.see[2][half][w][row] = see.sk;
       }
+      const int step = both ? 2 : 1, count = both ? (T - w + 1) >> 1 : T;      // this row tile's key tiles
+      if (mine && T > 0 && !q_sent) send_q();
+      q_sent = false;
       float m = neg_inf(), l0 = 0.f, l1 = 0.f;      // m: the reference, in log2 units; -inf: no key seen yet
       int j = it.j0 + (both ? w : 0);
 #pragma unroll 1
@@ -247,6 +253,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const bool cut = !it.tiles.all(key0);
         uint32_t bits[2];
         if (cut) {
+          const paged::Sees see{sm.see[0][half][w][row], sm.see[1][half][w][row], sm.see[2][half][w][row]};
           bits[0] = paged::seen32(see, key0 + half * 64);
           bits[1] = paged::seen32(see, key0 + half * 64 + 32);
         }
@@ -315,15 +322,22 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         }
       }
       seen += (uint32_t)count;
+      // The next item's queries: this row tile's place is free once its last logits are there (both: once those
+      // of both halves are), so that the next item's first product follows this one's last.
+      bool more;
+      next = item_at(x + 1, more);
+      const bool early = !both && count > 0 && next && next->T > 0 && ok;
+      if (early) bring_q(*next);
       if (T > 0) {
         ok = ok && wait_warp(&sm.fin, done & 1, abort);
         ++done;
         tc::tc_fence_after();
       }
-      // the next item's queries set out; Q has been used
-      bool more;
-      next = item_at(x + 1, more);
       ok = ok && more;
+      if (early) {
+        if (!(next->nt == 1 && w == 1)) send_q();
+        q_sent = true;
+      }
       // a group of warps that exchange results leaves together
       float l = l0 + l1;
       sm.ex[half][w][row] = l;
@@ -332,7 +346,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         ok = false;
         break;
       }
-      if (next && next->T > 0) bring_q(*next);
+      if (!early && next && next->T > 0) bring_q(*next);
       l += sm.ex[half ^ 1][w][row];
       float f0 = 1.f, f1 = 0.f;             // weights of this sum and of the odd tiles'
       if (mine && both && T > 1) {
@@ -345,17 +359,17 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           m = mn;
         }
       }
+      const uint32_t i0 = (both ? 0u : (uint32_t)(w * (kRT * kCta))) + (uint32_t)(rank * kRT + row);
+      const bool has = it.r0 + i0 < it.rows;
+      const RowOf at = row_of(a, it, has ? it.r0 + i0 : it.rows - 1);    // a row that is not there: as the last
       const bool live = l > 0.f || l != l;
       const bool poison = *(volatile int*)&sm.poison[x % paged::kItems] == x + 1;
       const float f = live ? 1.f / l : 0.f;
-      // Rows of 64 bytes (16 fp32 or 32 bf16 channels) go through shared memory, so that they leave as whole runs
+      // Rows of 64 bytes (32 channels) go through shared memory, so that they leave as whole runs
       uint8_t* stg = base + Lay::out + warp * 2048;
       const uint8_t* odd = base + Lay::out + (warp + 8) * 2048;        // (both) the odd tiles' 16 channels
-      uint8_t* out = partial ? reinterpret_cast<uint8_t*>(a.part_o) : static_cast<uint8_t*>(a.out);
-      const int64_t tok = it.s.t0 + at.t, prow = (int64_t)it.slot * kPer + i0;
-      const int64_t off = !has      ? -1
-                          : partial ? (prow * D + half * HD) * 4
-                                    : (at.head * a.o_hs + tok * a.o_ts + half * HD) * 2;
+      const int64_t tok = it.s.t0 + at.t;
+      const int64_t off = has ? (at.head * a.o_hs + tok * a.o_ts + half * HD) * 2 : -1;
 #pragma unroll 1
       for (int c = 0; c < HD; c += 32) {
         float o[32];
@@ -393,6 +407,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         }
         if (__builtin_expect(poison, 0)) {
           const paged::Split part{1, it.j0, it.j0 + it.T};
+          const paged::Sees see{sm.see[0][half][w][row], sm.see[1][half][w][row], sm.see[2][half][w][row]};
 #pragma unroll
           for (int d = 0; d < 32; d += 16) {
             float q[16];                    // a copy: o's registers keep no address
@@ -403,16 +418,12 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             for (int e = 0; e < 16; ++e) o[d + e] = q[e];
           }
         }
-        if (partial) {
+        if (partial) {                      // four channels of 32 rows side by side: whole runs as they are
+          float4* p = reinterpret_cast<float4*>(a.part_o) + ((int64_t)it.slot * (D / 4) + (half * HD + c) / 4) * kPer + i0;
+          if (has) {
 #pragma unroll
-          for (int d = 0; d < 32; d += 16) {
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<float4*>(stg + out_off(lane, e)) =
-                  make_float4(o[d + 4 * e], o[d + 4 * e + 1], o[d + 4 * e + 2], o[d + 4 * e + 3]);
-            __syncwarp();
-            store_rows(out + (c + d) * 4, off, stg, lane);
+            for (int e = 0; e < 8; ++e)
+              p[(int64_t)e * kPer] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         } else {
           __syncwarp();
@@ -425,14 +436,14 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             *reinterpret_cast<uint4*>(stg + out_off(lane, e)) = make_uint4(v[0], v[1], v[2], v[3]);
           }
           __syncwarp();
-          store_rows(out + c * 2, off, stg, lane);
+          store_rows(static_cast<uint8_t*>(a.out) + c * 2, off, stg, lane);
         }
       }
       tc::tc_fence_before();                // O has been read: the next item's products, which this warp's P let go
       if (has && half == 0 && mine) {
         const float mn = m * 0.6931471805599453f;
         if (partial)
-          a.part_ml[prow] = make_float2(live ? mn : neg_inf(), l);
+          a.part_ml[(int64_t)it.slot * kPer + i0] = make_float2(live ? mn : neg_inf(), l);
         else if (a.lse)
           a.lse[at.head * a.T + tok] = live ? mn + logf(l) : neg_inf();
       }
@@ -460,6 +471,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       const int vb = lane / (Lay::VC / 64), vc = lane % (Lay::VC / 64);
       int kn = 0, vn = 0;                                          // tiles asked for
       bool ok = true;
+      // what the join needs of the first item; not before its first tiles are asked for
+      auto cut_known = [&](const Item& it) {
+        if (rank == 0 && a.part_o) paged::write_cut(share, it, static_cast<paged::Cut*>(a.cuts) + share.p, kPer);
+      };
 #pragma unroll 1
       for (int x = 0; ok; ++x) {
         Item it;
@@ -470,11 +485,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           tc::mbar_arrive(&sm.item_full[x % paged::kItems]);
         }
         __syncwarp();
-        if (x == 0) {
-          if (rank == 0 && a.part_o) paged::write_cut(share, it, static_cast<paged::Cut*>(a.cuts) + share.p);
-          if (kCta == 2) pair_wait();
+        if (it.nt == 0) {
+          if (x == 0) cut_known(it);
+          break;
         }
-        if (it.nt == 0) break;
         const int32_t* table = a.table + (int64_t)it.b * a.max_pages;
         auto page_at = [&](int key, int n) {
           if (!it.tiles.any(key, key + n)) return none;
@@ -510,8 +524,11 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             tc::tma_load_4d(base + Lay::v + st * Lay::v_tile + vc * Lay::v_blk + vb * vr * 128, &vmap,
                             rank * Lay::VC + vc * 64, (key + vb * vr) & (page - 1), it.h, vp0, &sm.v_land[st]);
           ++vn;
+          if (x == 0 && i == 0) cut_known(it);
         }
+        if (x == 0 && vn == 0) cut_known(it);                      // no tile, or a wait that gave up
       }
+      if (kCta == 2) pair_wait();
       // the last copies land before this warp leaves, whether or not anyone waits for them
       volatile int never = 0;
       for (int y = max(0, kn - Lay::ks); y < kn; ++y)
@@ -691,75 +708,59 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 
 // ---- joining cut items -----------------------------------------------------------------------
 // O = sum_s e^(m_s - m) o_s / sum_s e^(m_s - m) l_s over the parts of an item, m = max_s m_s, in the order of the
-// keys; one warp a row, D / 32 channels a lane.  Bound: latency, so that what a warp's rows need of the first
-// kAtOnce parts sets out together (an item seldom has more than three).
+// keys.  A warp takes 32 rows and 32 channels, a row a lane (as the partials lie); the outputs go through shared
+// memory.  Bound: latency; the maxima, sums and outputs of two parts set out together.
 template <int D>
 __global__ void __launch_bounds__(256) paged_tc_join_kernel(const PagedAttnArgs a, int per) {
-  constexpr int CPL = D / 32, kAtOnce = 2, kRows = kJoinRows / 8;
+  __shared__ __align__(16) uint8_t stage[8 * 2048];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   const paged::Cut& cut = static_cast<const paged::Cut*>(a.cuts)[blockIdx.x];
-  const int n = cut.parts, i0 = blockIdx.y * kJoinRows + warp * kRows;
+  const int n = cut.parts, x = blockIdx.y * 8 + warp;       // (rows, channels) of the item
+  const int c = x % (D / 32) * 32, i = x / (D / 32) * 32 + lane;
   const uint32_t r0 = cut.r0, rows = cut.rows;
   const int t0 = cut.t0, h = cut.h;
-  if (n == 0 || r0 + i0 >= rows) return;
-  float m[kRows], l[kRows], o[kRows][CPL];
+  if (n == 0 || r0 + (uint32_t)(i - lane) >= rows) return;
+  const bool has = r0 + (uint32_t)i < rows;
+  float m = neg_inf(), l = 0.f, o[32];
 #pragma unroll
-  for (int y = 0; y < kRows; ++y) {
-    m[y] = neg_inf();
-    l[y] = 0.f;
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) o[y][c] = 0.f;
-  }
+  for (int e = 0; e < 32; ++e) o[e] = 0.f;
 #pragma unroll 1
-  for (int s0 = n; s0 > 0; s0 -= kAtOnce) {               // the parts are listed from the last on
-    float2 ml[kRows][kAtOnce];
-    float p[kRows][kAtOnce][CPL];
+  for (int s = n - 1; s >= 0; --s) {                        // the parts are listed from the last on
+    const int64_t slot = cut.slots[s];
+    const float4* p = reinterpret_cast<const float4*>(a.part_o) + (slot * (D / 4) + c / 4) * per + i;
+    float2 ml = make_float2(neg_inf(), 0.f);
+    float4 v[8];
+    if (has) {
+      ml = a.part_ml[slot * per + i];
 #pragma unroll
-    for (int e = 0; e < kAtOnce; ++e) {
-      const int s = s0 - 1 - e;
-      const int64_t prow = (int64_t)cut.slots[s < 0 ? 0 : s] * per + i0;
-#pragma unroll
-      for (int y = 0; y < kRows; ++y) {
-        const bool in = s >= 0 && r0 + i0 + y < rows;
-        ml[y][e] = in ? a.part_ml[prow + y] : make_float2(neg_inf(), 0.f);
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) p[y][e][c] = in ? a.part_o[(prow + y) * D + lane * CPL + c] : 0.f;
-      }
+      for (int e = 0; e < 8; ++e) v[e] = p[(int64_t)e * per];
     }
+    if (ml.y == 0.f) continue;
+    const float top = fmaxf(m, ml.x), ref = top == neg_inf() ? 0.f : top, f = expf(m - ref), w = expf(ml.x - ref);
+    m = top;
+    l = fmaf(w, ml.y, l * f);
 #pragma unroll
-    for (int y = 0; y < kRows; ++y) {
-      float top = m[y];
-#pragma unroll
-      for (int e = 0; e < kAtOnce; ++e)
-        if (ml[y][e].y != 0.f) top = fmaxf(top, ml[y][e].x);
-      const float ref = top == neg_inf() ? 0.f : top, f = expf(m[y] - ref);
-      m[y] = top;
-      l[y] *= f;
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) o[y][c] *= f;
-#pragma unroll
-      for (int e = 0; e < kAtOnce; ++e) {
-        if (ml[y][e].y == 0.f) continue;
-        const float w = expf(ml[y][e].x - ref);
-        l[y] = fmaf(w, ml[y][e].y, l[y]);
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) o[y][c] = fmaf(w, p[y][e][c], o[y][c]);
-      }
+    for (int e = 0; e < 8; ++e) {
+      o[4 * e] = fmaf(w, v[e].x, o[4 * e] * f), o[4 * e + 1] = fmaf(w, v[e].y, o[4 * e + 1] * f);
+      o[4 * e + 2] = fmaf(w, v[e].z, o[4 * e + 2] * f), o[4 * e + 3] = fmaf(w, v[e].w, o[4 * e + 3] * f);
     }
   }
+  const bool live = l > 0.f || l != l;
+  const float f = live ? 1.f / l : 0.f;
+  const uint32_t r = has ? r0 + (uint32_t)i : rows - 1, t = r / (uint32_t)a.group;
+  const int64_t tok = t0 + (int)t, head = h * a.group + (int)(r - t * (uint32_t)a.group);
+  uint8_t* stg = stage + warp * 2048;
 #pragma unroll
-  for (int y = 0; y < kRows; ++y) {
-    const uint32_t r = r0 + i0 + y, t = r / (uint32_t)a.group;
-    if (r >= rows) break;
-    const bool live = l[y] > 0.f || l[y] != l[y];
-    const int64_t tok = t0 + (int)t, head = h * a.group + (int)(r - t * (uint32_t)a.group);
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + head * a.o_hs + tok * a.o_ts + lane * CPL;
+  for (int e = 0; e < 4; ++e) {
+    uint32_t y[4];
 #pragma unroll
-    for (int c = 0; c < CPL; c += 2)
-      *reinterpret_cast<uint32_t*>(out + c) = live ? pack_bf16(o[y][c] / l[y], o[y][c + 1] / l[y]) : 0u;
-    if (lane == 0 && a.lse) a.lse[head * a.T + tok] = live ? m[y] + logf(l[y]) : neg_inf();
+    for (int k = 0; k < 4; ++k) y[k] = live ? pack_bf16(o[8 * e + 2 * k] * f, o[8 * e + 2 * k + 1] * f) : 0u;
+    *reinterpret_cast<uint4*>(stg + out_off(lane, e)) = make_uint4(y[0], y[1], y[2], y[3]);
   }
+  __syncwarp();
+  store_rows(static_cast<uint8_t*>(a.out) + c * 2, has ? (head * a.o_hs + tok * a.o_ts) * 2 : -1, stg, lane);
+  if (has && c == 0 && a.lse) a.lse[head * a.T + tok] = live ? m + logf(l) : neg_inf();
 }
 
 template <int D, int C>
@@ -789,7 +790,7 @@ cudaError_t tc_go(const PagedAttnArgs& a, cudaStream_t s) {
   count_launches(1);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess || !a.part_o) return e;
-  e = launch_dependent(paged_tc_join_kernel<D>, dim3((unsigned)a.shares, per / kJoinRows), dim3(256), 0, s, a, per);
+  e = launch_dependent(paged_tc_join_kernel<D>, dim3((unsigned)a.shares, per / 32 * (D / 32) / 8), dim3(256), 0, s, a, per);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

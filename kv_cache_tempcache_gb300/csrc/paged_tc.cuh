@@ -2,8 +2,9 @@
 // the sequences' lengths are.
 //
 // An item is up to `per` rows of a (sequence, KV head): its row tiles 2 (or 1, where the rows fill half of them or
-// less), its key tiles paged.cuh's.  It counts kFixed units and kFull (kHalf) for each key tile, as its time
-// goes: 1.45 us a key tile, 0.97 with one row tile, some 9 us around them.  Items lie in a row: sequences,
+// less), its key tiles paged.cuh's.  It counts kFixed units and kFull (fewer with one row tile) for each key tile,
+// as its time goes: 1.4 us a key tile, 1.15 with one row tile (a pair; it waits for K and V, which it takes twice as
+// fast), some 8 us around them.  Items lie in a row: sequences,
 // their row tiles, the KV heads side by side.  Share p of P is the units W p / P .. W (p + 1) / P of that row, so
 // that all shares end together, whatever the lengths: borders cut items between two key tiles (12 heads of 4680
 // tokens are 120 items on 76 pairs of CTAs: in whole items 2 waves, dealt out 1.53).  A cut leaves parts of kMinTiles
@@ -18,7 +19,8 @@
 namespace fastar {
 namespace paged {
 
-constexpr int kFixed = 36, kFull = 6, kHalf = 4, kLeast = 60, kMinTiles = 3;
+constexpr int kFixed = 36, kFull = 6, kLeast = 60, kMinTiles = 3;
+__device__ __forceinline__ int half_units(int per) { return per == 512 ? 5 : 4; }     // pairs of CTAs, single ones
 constexpr int kMaxShares = 256;          // the plan asks for no more
 constexpr int kItems = 8;                // items of a CTA that are known at once
 
@@ -56,7 +58,7 @@ __device__ __forceinline__ int item_units(const PagedAttnArgs& a, const Seq& s, 
   if (r0 >= rows) return 0;
   nt = rows - r0 > per / 2 ? 2 : 1;
   tiles.set(a, s, r0 / a.group, (min(r0 + per, rows) - 1) / a.group);
-  return kFixed + tiles.n * (nt == 2 ? kFull : kHalf);
+  return kFixed + tiles.n * (nt == 2 ? kFull : half_units(per));
 }
 
 __device__ __forceinline__ Seq shfl_seq(const Seq& s, int from) {
@@ -162,17 +164,17 @@ __device__ __forceinline__ void find_share(const PagedAttnArgs& a, Share& sh, in
 }
 
 // The key tile of the item before which unit `unit` of the row falls.
-__device__ __forceinline__ int border_tile(const Share& sh, const Item& it, int64_t unit) {
+__device__ __forceinline__ int border_tile(const Share& sh, const Item& it, int64_t unit, int per) {
   const int64_t o = unit - it.at;
   const int n = it.tiles.n;
   if (o <= 0) return 0;
   if (o >= it.units) return n;
   if (!sh.cuts) return 2 * o <= it.units ? 0 : n;
-  const int j = o <= kFixed ? 0 : (int)(o - kFixed) / (it.nt == 2 ? kFull : kHalf);
+  const int j = o <= kFixed ? 0 : (int)(o - kFixed) / (it.nt == 2 ? kFull : half_units(per));
   return j < kMinTiles ? 0 : n - j < kMinTiles ? n : j;
 }
-__device__ __forceinline__ int border(const Share& sh, int p, const Item& it) {
-  return border_tile(sh, it, share_border(sh, p));
+__device__ __forceinline__ int border(const Share& sh, int p, const Item& it, int per) {
+  return border_tile(sh, it, share_border(sh, p), per);
 }
 
 // The share's next item, or (nt = 0) none.
@@ -187,8 +189,8 @@ __device__ __forceinline__ void next_item(const PagedAttnArgs& a, Share& sh, Ite
     it.rows = (uint32_t)rows_of(a, it.s);
     it.h = sh.h;
     it.at = sh.at;
-    it.j0 = border_tile(sh, it, sh.from);
-    it.T = border_tile(sh, it, sh.to) - it.j0;
+    it.j0 = border_tile(sh, it, sh.from, per);
+    it.T = border_tile(sh, it, sh.to, per) - it.j0;
     // (an item without keys: its start decides whose it is)
     const bool mine = it.T > 0 || (it.tiles.n == 0 && sh.from <= sh.at);
     it.slot = it.T < it.tiles.n ? 2 * sh.p + (it.j0 == 0) : -1;
@@ -218,7 +220,7 @@ struct Cut {
   uint32_t r0, rows;
   int slots[kMaxShares + 1];             // of the parts, the last first
 };
-__device__ __forceinline__ void write_cut(const Share& sh, const Item& it, Cut* cut) {
+__device__ __forceinline__ void write_cut(const Share& sh, const Item& it, Cut* cut, int per) {
   const int lane = threadIdx.x & 31;
   if (it.nt == 0 || it.j0 == 0 || it.j0 + it.T < it.tiles.n) {
     if (lane == 0) cut->parts = 0;
@@ -226,7 +228,7 @@ __device__ __forceinline__ void write_cut(const Share& sh, const Item& it, Cut* 
   }
   int n = 0, j = INT_MAX;
   for (int p = sh.p; p >= 0 && j > 0; --p) {
-    const int from = border(sh, p, it);
+    const int from = border(sh, p, it, per);
     if (from < j) {                      // a share without a key tile of the item has no part
       if (lane == 0) cut->slots[n] = 2 * p + (from == 0);
       ++n;
