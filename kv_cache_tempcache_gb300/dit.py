@@ -9,7 +9,8 @@ shape so that a chunk can be denoised end to end: every block is
     q, k, v = h W_qkv^T + b;  q, k <- RMSNorm (of the row, or of each head), rotary positions
                                                     (frame, row, column)
     x += gate1 * (SelfAttn(q, k, v) W_o^T + b)               (FAST-AR: TempCache + AnnSA, or dense
-                                                              over a bf16 or a 4-bit cache)
+                                                              over a bf16 or a 4-bit cache, or over a
+                                                              window of the last frames and the first)
     x += CrossAttn(RMSNorm(LN_affine(x) W_q^T + b), text) W_o^T + b   (FAST-AR: AnnCA, or dense)
     x += gate2 * (GELU(LN(x) * (1 + scale2) + shift2) W_1^T + b) W_2^T + b)
 with (shift, scale, gate) x 2 = the block's modulation + a projection of the timestep
@@ -31,7 +32,7 @@ from typing import List, Optional
 import torch
 
 from . import _lib as L
-from .layer import DenseLayer, FastARLayer, KV4Layer
+from .layer import DenseLayer, FastARLayer, KV4Layer, WindowLayer
 
 
 @dataclasses.dataclass(frozen=True)
@@ -51,6 +52,8 @@ class DiTConfig:
     eps: float = 1e-6
     theta: float = 10000.0
     qk_norm: str = "row"        # "row": RMS norm over all heads together; "head": of each head
+    window_frames: int = 21     # attention "window": the last frames that a token sees, the chunk's among them,
+    sink_frames: int = 3        # and the rollout's first
     # FAST-AR attention (the Wan-1.3B layer of the benchmark)
     M: int = 9360
     B: int = 64
@@ -93,8 +96,9 @@ class _Block:
 
 class DiT:
     """Parameters, buffers and the denoising step of the transformer.  attention is
-    "fastar" (TempCache + AnnSA + AnnCA per block), "dense" (append-only caches) or "dense4"
-    (append-only caches in 4 bits)."""
+    "fastar" (TempCache + AnnSA + AnnCA per block), "dense" (append-only caches), "dense4"
+    (append-only caches in 4 bits) or "window" (the last cfg.window_frames frames and the first
+    cfg.sink_frames, in caches of constant size).  dense_capacity: the rollout's rows, but for "fastar"."""
 
     def __init__(self, cfg: DiTConfig, attention: str = "fastar", seed: int = 0, device="cuda",
                  dense_capacity: int = 0):
@@ -173,6 +177,10 @@ class DiT:
             for a in self.attn:
                 a.set_centroids(torch.nn.functional.normalize(torch.randn(H, cfg.B, d, generator=g, device=dev),
                                                               dim=-1).to(bf))
+        elif attention == "window":
+            frame = cfg.grid_h * cfg.grid_w
+            self.attn = [WindowLayer(H, d, N, cfg.window_frames * frame, cfg.sink_frames * frame, max(dense_capacity, N),
+                                     cfg.text_len, dtype=bf, device=dev) for _ in range(cfg.layers)]
         else:
             cap = max(dense_capacity, N)
             layer = KV4Layer if attention == "dense4" else DenseLayer
@@ -197,6 +205,8 @@ class DiT:
     def _norm_rope(self, q, k, b):
         """RMS norm and rotary positions of the block's queries and keys, in place."""
         cfg, D = self.cfg, self.cfg.dim
+        if self._turn(b) is not None:
+            return                                         # on the way into the cache
         if cfg.qk_norm == "head":
             L.fastar_qk_norm_rope(q, k, q, k, wq=b.norm_q, wk=b.norm_k, eps=cfg.eps, axes=cfg.axes,
                                   t0_dev=self.frame_dev, grid=(cfg.grid_h, cfg.grid_w), theta=cfg.theta)
@@ -205,6 +215,13 @@ class DiT:
                               grid=(cfg.grid_h, cfg.grid_w), eps=cfg.eps, theta=cfg.theta)
         L.fastar_rmsnorm_rope(self.qkv[:, D:2 * D], cfg.d, weight=b.norm_k, rope=True, t0_dev=self.frame_dev,
                               grid=(cfg.grid_h, cfg.grid_w), eps=cfg.eps, theta=cfg.theta)
+
+    def _turn(self, b):
+        """Norm and rotation that the block's append does on the way (a window with norms of each head), or None."""
+        cfg = self.cfg
+        if self.attention != "window" or cfg.qk_norm != "head":
+            return None
+        return dict(wq=b.norm_q, wk=b.norm_k, eps=cfg.eps, axes=cfg.axes, grid=(cfg.grid_h, cfg.grid_w), theta=cfg.theta)
 
     # ---- set-up ----------------------------------------------------------------------------
     def set_text(self, text: torch.Tensor):
@@ -249,7 +266,10 @@ class DiT:
                                    scale_b=e0[1])
             L.fastar_gemm(self.h, b.qkv_w, self.qkv, bias=b.qkv_b, dev_status=st)
             self._norm_rope(q, k, b)
-            a.step_self(q, k, v, out=o, advance=advance)
+            if self.attention == "window":
+                a.step_self(q, k, v, out=o, advance=advance, turn=self._turn(b))
+            else:
+                a.step_self(q, k, v, out=o, advance=advance)
             if probe is not None:
                 probe("self", i, a, q, k, v, o)
             L.fastar_gemm(self.o, b.o_w, self.x, bias=b.o_b, R=self.x, gate_a=b.mod[2], gate_b=e0[2], dev_status=st)
@@ -283,17 +303,17 @@ class DiT:
             self._commit()
 
     def _room(self):
-        # a captured step finds its lengths on the device: a full 4-bit cache is refused here, as the
-        # dense path's append refuses it
-        if self.attention == "dense4" and self.attn[0].n + self.cfg.tokens > self.attn[0].cap:
-            raise L.FastarError("fastar_kv4_append", L.ECAPACITY)
+        # a captured step finds its lengths on the device: a full 4-bit cache, or a rollout past its
+        # length, is refused here, as the dense path's append refuses it
+        if self.attention in ("dense4", "window") and self.attn[0].n + self.cfg.tokens > self.attn[0].cap:
+            raise L.FastarError("fastar_kv4_append" if self.attention == "dense4" else "fastar_paged_append", L.ECAPACITY)
 
     def _commit(self):
         cfg = self.cfg
         for a in self.attn:
             if self.attention == "fastar":
                 a.cur = 1 - a.cur
-            elif self.attention == "dense4":
+            elif self.attention in ("dense4", "window"):
                 a.commit(cfg.tokens)
             else:
                 a.n += cfg.tokens
@@ -304,13 +324,13 @@ class DiT:
     def _graph_key(self):
         if self.attention == "fastar":
             return ("fastar", self.attn[0].cur)
-        if self.attention == "dense4":
-            return ("dense4",)                             # the lengths are on the device
+        if self.attention in ("dense4", "window"):
+            return (self.attention,)                       # the lengths are on the device
         return ("dense", self.attn[0].n)
 
     def capture(self):
         """The current denoising step as a CUDA graph (FAST-AR: one per cache half, kept;
-        dense: one per cache length; dense4: one)."""
+        dense: one per cache length; dense4 and window: one)."""
         key = self._graph_key()
         if key in self._graphs:
             return self._graphs[key]
@@ -359,6 +379,6 @@ class DiT:
     def status_word(self) -> int:
         st = int(self.status.item())
         for a in self.attn:
-            if self.attention in ("fastar", "dense4"):
+            if self.attention in ("fastar", "dense4", "window"):
                 st |= a.status()
         return st

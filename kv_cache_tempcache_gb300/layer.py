@@ -591,3 +591,125 @@ class KV4Layer:
 
     def status(self) -> int:
         return int(self.dev_status.item())
+
+
+def ring_table(rows, page, sinks, window, chunk):
+    """The pages of a rollout of `rows` rows that keeps its first `sinks` rows and its last `window` before
+    every token, in chunks of up to `chunk` tokens: (table int32 [pages of the rollout], pages in use).
+    The first rows' pages stay; the others come round as the window moves on."""
+    pages = -(-rows // page)
+    keep = min(pages, -(-sinks // page))
+    # a chunk behind `at` rows sees rows at + 1 - window .. at + chunk - 1: at most this many pages
+    ring = (max(0, window + chunk - 2) + page - 1) // page + 1
+    p = torch.arange(pages, dtype=torch.int32)
+    if pages <= keep + ring:
+        return p, pages
+    return torch.where(p < keep, p, keep + (p - keep) % ring).to(torch.int32), keep + ring
+
+
+class WindowLayer:
+    """DenseLayer with a bounded cache: the last `window` rows before a token's end and the rollout's first
+    `sinks` (the frames that a rollout holds on to), in pages that come round as the window moves on, so the cache's
+    bytes do not grow with the rollout.  rows: the rollout's length (of its page table, 4 bytes a page).  Lengths
+    live on the device, so one captured step serves every length (with advance=True each replay keeps its
+    chunk).  Hkv: heads of the cache (default H; H must be a multiple of it); block: tokens of a frame that
+    sees itself and the frames before it in the chunk, not those after it (0: the chunk sees all of
+    itself; 1: causal)."""
+
+    def __init__(self, H, d, Nq, window, sinks, rows, P, dtype=torch.bfloat16, device="cuda", scale=None, Hkv=None, block=0,
+                 page=64):
+        L.load()
+        if window < 1 or sinks < 0 or rows < 1 or Nq < 1:
+            raise ValueError("window, rows and Nq must be positive, sinks not negative")
+        dev = torch.device(device)
+        Hkv = H if Hkv is None else Hkv
+        self.H, self.Hkv, self.d, self.Nq, self.P = H, Hkv, d, Nq, P
+        self.window, self.sinks, self.block, self.page = int(window), int(sinks), int(block), int(page)
+        self.scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+        table, pages = ring_table(rows, self.page, self.sinks, self.window, Nq)
+        self.table = table.to(dev)[None].contiguous()
+        self.cap = table.numel() * self.page                               # rows of the rollout
+        self.k = torch.zeros((pages, Hkv, self.page, d), dtype=dtype, device=dev)
+        self.v = torch.zeros((pages, Hkv, self.page, d), dtype=dtype, device=dev)
+        self.len = torch.zeros(1, dtype=torch.int32, device=dev)           # committed rows
+        self.len_cur = torch.zeros(1, dtype=torch.int32, device=dev)       # with the current chunk
+        self.kp = torch.zeros((H, P, d), dtype=dtype, device=dev)
+        self.vp = torch.zeros((H, P, d), dtype=dtype, device=dev)
+        self._n = 0                      # committed rows, while the host knows them: see n
+        self._replayed = False
+        self.o_self = torch.zeros((H, Nq, d), dtype=dtype, device=dev)
+        self.o_cross = torch.zeros((H, Nq, d), dtype=dtype, device=dev)
+        self.lse_self = _f32(H, Nq, dev=dev)
+        self.lse_cross = _f32(H, Nq, dev=dev)
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+        nb = L.workspace_bytes(L.OP_PAGED_ATTN, H, Nq, min(self.cap, self.window + self.sinks), d, Hkv, r=Nq, P=1)
+        self.ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+
+    @property
+    def n(self) -> int:
+        """The committed rows.  Once a commit has been captured only the device knows how often it
+        was replayed: from then on this waits for the current stream and reads the length."""
+        return int(self.len) if self._replayed else self._n
+
+    def _keep(self, n):
+        self.len.copy_(self.len_cur)
+        if torch.cuda.is_current_stream_capturing():
+            self._replayed = True        # the copy has not run, and may run any number of times
+        elif not self._replayed:
+            self._n = n
+
+    def _append(self, k, v, **turn):
+        if k.shape[1] > self.Nq:
+            raise ValueError(f"a chunk of {k.shape[1]} tokens for a layer of {self.Nq}")
+        L.fastar_paged_append(k, v, self.k, self.v, self.table, self.len, self.len_cur, dev_status=self.dev_status, **turn)
+
+    def load_history(self, k, v):
+        """k, v [Hkv, n, d] (as the cache is to hold them): the rollout's rows so far."""
+        self.len.zero_()
+        self._n, self._replayed = 0, False
+        for a in range(0, k.shape[1], self.Nq):
+            self._append(k[:, a:a + self.Nq], v[:, a:a + self.Nq])
+            self.commit(min(self.Nq, k.shape[1] - a))
+
+    def set_prompt(self, kp, vp):
+        self.kp.copy_(kp)
+        self.vp.copy_(vp)
+
+    def commit(self, n):
+        """Keeps the n rows that the last step_self appended (of a full rollout those that it took)."""
+        self._keep(min(self._n + n, self.cap))
+
+    def step_self(self, q, k_cur, v_cur, out=None, advance: bool = True, turn=None):
+        """Appends the chunk behind the committed rows (kept with advance=True, else overwritten by the next
+        step) and attends over what each token sees -> out ([H, Nq, d] view; default o_self).  turn: wq, wk,
+        eps, axes, grid, theta of fastar_paged_append, the norm and rotation of q (in place) and k by their
+        rows in the rollout.  Rows past the rollout's length are dropped and set DEV_BAD_LEN in status()."""
+        o = self.o_self if out is None else out
+        n = q.shape[1]
+        if k_cur.shape[1] != n:
+            raise ValueError("q and k_cur must have the same tokens")
+        if turn is None:
+            self._append(k_cur, v_cur)
+        else:
+            self._append(k_cur, v_cur, q=q, q_out=q, **turn)
+        lse = self.lse_self if n == self.Nq else torch.empty(self.H, n, dtype=torch.float32, device=q.device)
+        L.fastar_paged_attn(q, self.k, self.v, self.table, self.len, self.scale, o[:, :n], lse, block=self.block,
+                            window=self.window, sinks=self.sinks, dev_status=self.dev_status, workspace=self.ws)
+        if lse is not self.lse_self:
+            self.lse_self[:, :n] = lse
+        if advance:
+            self.commit(n)
+        return o[:, :n]
+
+    def step_cross(self, q, out=None):
+        o = self.o_cross if out is None else out
+        L.fastar_dense_attn(q, self.kp, self.vp, self.P, self.scale, o, self.lse_cross)
+        return o
+
+    def step(self, q, k_cur, v_cur, advance: bool = True, turn=None):
+        self.step_self(q, k_cur, v_cur, advance=advance, turn=turn)
+        self.step_cross(q)
+        return self.o_self, self.o_cross
+
+    def status(self) -> int:
+        return int(self.dev_status.item())
