@@ -655,7 +655,7 @@ def fastar_kv4_attn(q, k_codes, k_scales, v_codes, v_scales, lens, scale, out, l
 
 
 def _refuse_paged(rows, dense, k_pool, v_pool, dt, Hk, d, table, at, cu):
-    """As _refuse, for the calls over a paged cache."""
+    """As _refuse, for the calls over a paged cache (which take a vector in any shape of its size)."""
     for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
         if t.dtype is not dt:
             raise ValueError(f"{name} must be {dt}, not {t.dtype}")
@@ -678,36 +678,36 @@ def fastar_paged_append(k, v, k_pool, v_pool, table, at, len_out=None, q=None, q
     (int32 [B]); cu [B + 1] (int32): where each sequence's tokens begin (None: T / B tokens each).  k is
     normed (wk given) and turned by its row's position on the grid, or pos [T, 3]; q [Hq, T, d] likewise into
     q_out.  len_out[b] = at[b] + its tokens."""
-    Hk, T, d = ks = _dims3("k", k)
+    ks = k.shape
+    Hk, T, d = ks if len(ks) == 3 else _dims3("k", k)
     dt, dev = k.dtype, k.get_device()
     code = _CODES[dt] if dt in _CODES else _raise_dtype(dt)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     Hq = 0 if q is None else _dims3("q", q)[0]
     qs = (Hq, T, d)
-    p_sh, p_st = k_pool.shape, k_pool.stride()
+    p_sh, p_st, t_sh = k_pool.shape, k_pool.stride(), table.shape
+    B = t_sh[0] if len(t_sh) == 2 else -1
     if not (
             dev >= 0 and dev == _device()
             and (k_st := k.stride())[2] == 1
             and v.dtype is dt and v.shape == ks and (v_st := v.stride())[2] == 1 and v.get_device() == dev
-            and len(p_sh) == 4 and p_sh[1] == Hk and p_sh[3] == d and k_pool.dtype is dt and p_st[3] == 1
+            and len(p_sh) == 4 and p_sh[1] == Hk and p_sh[3] == d and p_st[3] == 1 and k_pool.dtype is dt
             and k_pool.get_device() == dev
             and v_pool.dtype is dt and v_pool.shape == p_sh and v_pool.stride() == p_st and v_pool.get_device() == dev
-            and table.dtype is _I32 and len(t_sh := table.shape) == 2 and table.is_contiguous()
-            and table.get_device() == dev
-            and at.dtype is _I32 and at.shape == (t_sh[0],) and at.is_contiguous() and at.get_device() == dev
+            and table.dtype is _I32 and B >= 0 and table.is_contiguous() and table.get_device() == dev
+            and at.dtype is _I32 and at.numel() == B and at.is_contiguous() and at.get_device() == dev
             and (q is None or q.dtype is dt and q.shape == qs and (q_st := q.stride())[2] == 1 and q.get_device() == dev
                  and q_out.dtype is dt and q_out.shape == qs and (qo_st := q_out.stride())[2] == 1
                  and q_out.get_device() == dev)
-            and (cu is None or cu.dtype is _I32 and cu.shape == (t_sh[0] + 1,) and cu.is_contiguous()
-                 and cu.get_device() == dev)
-            and (len_out is None or len_out.dtype is _I32 and len_out.shape == (t_sh[0],) and len_out.is_contiguous()
+            and (cu is None or cu.dtype is _I32 and cu.numel() == B + 1 and cu.is_contiguous() and cu.get_device() == dev)
+            and (len_out is None or len_out.dtype is _I32 and len_out.numel() == B and len_out.is_contiguous()
                  and len_out.get_device() == dev)
-            and (wq is None or wq.dtype is _F32 and wq.shape == (d,) and wq.is_contiguous() and wq.get_device() == dev)
-            and (wk is None or wk.dtype is _F32 and wk.shape == (d,) and wk.is_contiguous() and wk.get_device() == dev)
+            and (wq is None or wq.dtype is _F32 and wq.numel() == d and wq.is_contiguous() and wq.get_device() == dev)
+            and (wk is None or wk.dtype is _F32 and wk.numel() == d and wk.is_contiguous() and wk.get_device() == dev)
             and (pos is None or pos.dtype is _I32 and pos.shape == (T, 3) and pos.is_contiguous()
                  and pos.get_device() == dev)
-            and (dev_status is None or dev_status.dtype is _I32 and dev_status.shape == (1,)
+            and (dev_status is None or dev_status.dtype is _I32 and dev_status.numel() == 1
                  and dev_status.get_device() == dev)):
         _refuse_paged([("k", k, dt, ks), ("v", v, dt, ks), ("q", q, dt, qs), ("q_out", q_out, dt, qs)],
                       [("len_out", len_out, _I32, table.shape[:1]), ("wq", wq, _F32, (d,)), ("wk", wk, _F32, (d,)),
@@ -715,7 +715,6 @@ def fastar_paged_append(k, v, k_pool, v_pool, table, at, len_out=None, q=None, q
                       k_pool, v_pool, dt, Hk, d, table, at, cu)
     if q is None:
         q_st = qo_st = (0, 0)
-    B, max_pages = t_sh
     rc = (_lib or load()).fastar_packed_call(_CALL_PAPPEND, _PACK_PAPPEND(
         code, B, T, 0 if cu is None else cu.data_ptr(), d, Hq, 0 if q is None else q.data_ptr(),
         q_st[0] if Hq > 1 else T * d, q_st[1] if T > 1 else d, 0 if q is None else q_out.data_ptr(),
@@ -723,7 +722,7 @@ def fastar_paged_append(k, v, k_pool, v_pool, table, at, len_out=None, q=None, q
         k_st[1] if T > 1 else d, v.data_ptr(), v_st[0] if Hk > 1 else T * d, v_st[1] if T > 1 else d,
         0 if wq is None else wq.data_ptr(), 0 if wk is None else wk.data_ptr(), eps, axes[0], axes[1], axes[2],
         0 if pos is None else pos.data_ptr(), grid[0], grid[1], theta, k_pool.data_ptr(), v_pool.data_ptr(), p_sh[0],
-        p_sh[2], p_st[0] if p_sh[0] > 1 else d, p_st[1] if Hk > 1 else d, p_st[2], table.data_ptr(), max_pages,
+        p_sh[2], p_st[0] if p_sh[0] > 1 else d, p_st[1] if Hk > 1 else d, p_st[2], table.data_ptr(), t_sh[1],
         at.data_ptr(), 0 if len_out is None else len_out.data_ptr(), 0 if dev_status is None else dev_status.data_ptr(),
         _current_stream(dev) if stream is None else stream.cuda_stream), _N_PAPPEND)
     if rc:
@@ -738,24 +737,24 @@ def fastar_paged_attn(q, k_pool, v_pool, table, at, scale, out, lse=None, cu=Non
     the token's end, and the first `sinks`.  cu [B + 1] as in fastar_paged_append; max_q: the most tokens
     of a sequence (None: T, with cu None T / B).  workspace: workspace_bytes(OP_PAGED_ATTN, Hq, T,
     max_pages * page, d, Hkv, r=max_q, P=B) bytes (None: the keys are not split)."""
-    Hq, T, d = qs = _dims3("q", q)
+    qs = q.shape
+    Hq, T, d = qs if len(qs) == 3 else _dims3("q", q)
     dt, dev = q.dtype, q.get_device()
     code = _CODES[dt] if dt in _CODES else _raise_dtype(dt)
-    p_sh, p_st = k_pool.shape, k_pool.stride()
+    p_sh, p_st, t_sh = k_pool.shape, k_pool.stride(), table.shape
+    B = t_sh[0] if len(t_sh) == 2 else -1
     if not (
             dev >= 0 and dev == _device()
             and (q_st := q.stride())[2] == 1
             and out.dtype is dt and out.shape == qs and (o_st := out.stride())[2] == 1 and out.get_device() == dev
-            and len(p_sh) == 4 and p_sh[3] == d and k_pool.dtype is dt and p_st[3] == 1 and k_pool.get_device() == dev
+            and len(p_sh) == 4 and p_sh[3] == d and p_st[3] == 1 and k_pool.dtype is dt and k_pool.get_device() == dev
             and v_pool.dtype is dt and v_pool.shape == p_sh and v_pool.stride() == p_st and v_pool.get_device() == dev
-            and table.dtype is _I32 and len(t_sh := table.shape) == 2 and table.is_contiguous()
-            and table.get_device() == dev
-            and at.dtype is _I32 and at.shape == (t_sh[0],) and at.is_contiguous() and at.get_device() == dev
-            and (cu is None or cu.dtype is _I32 and cu.shape == (t_sh[0] + 1,) and cu.is_contiguous()
-                 and cu.get_device() == dev)
+            and table.dtype is _I32 and B >= 0 and table.is_contiguous() and table.get_device() == dev
+            and at.dtype is _I32 and at.numel() == B and at.is_contiguous() and at.get_device() == dev
+            and (cu is None or cu.dtype is _I32 and cu.numel() == B + 1 and cu.is_contiguous() and cu.get_device() == dev)
             and (lse is None or lse.dtype is _F32 and lse.shape == (Hq, T) and lse.is_contiguous()
                  and lse.get_device() == dev)
-            and (dev_status is None or dev_status.dtype is _I32 and dev_status.shape == (1,)
+            and (dev_status is None or dev_status.dtype is _I32 and dev_status.numel() == 1
                  and dev_status.get_device() == dev)
             and (workspace is None or workspace.is_contiguous() and workspace.get_device() == dev)):
         dense = [("lse", lse, _F32, (Hq, T)), ("dev_status", dev_status, _I32, (1,))]
@@ -763,13 +762,12 @@ def fastar_paged_attn(q, k_pool, v_pool, table, at, scale, out, lse=None, cu=Non
             dense.append(("workspace", workspace, workspace.dtype, workspace.shape))
         _refuse_paged([("q", q, dt, qs), ("out", out, dt, qs)], dense, k_pool, v_pool, dt,
                       k_pool.shape[1] if k_pool.dim() == 4 else 0, d, table, at, cu)
-    B, max_pages = t_sh
     if max_q is None:
         max_q = T if cu is not None else T // max(B, 1)
     rc = (_lib or load()).fastar_packed_call(_CALL_PATTN, _PACK_PATTN(
         q.data_ptr(), code, B, T, 0 if cu is None else cu.data_ptr(), max_q, Hq, p_sh[1], d,
         q_st[0] if Hq > 1 else T * d, q_st[1] if T > 1 else d, k_pool.data_ptr(), v_pool.data_ptr(), p_sh[0], p_sh[2],
-        p_st[0] if p_sh[0] > 1 else d, p_st[1] if p_sh[1] > 1 else d, p_st[2], table.data_ptr(), max_pages,
+        p_st[0] if p_sh[0] > 1 else d, p_st[1] if p_sh[1] > 1 else d, p_st[2], table.data_ptr(), t_sh[1],
         at.data_ptr(), block, window, sinks, scale, out.data_ptr(), o_st[0] if Hq > 1 else T * d,
         o_st[1] if T > 1 else d, 0 if lse is None else lse.data_ptr(), 0 if dev_status is None else dev_status.data_ptr(),
         0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
