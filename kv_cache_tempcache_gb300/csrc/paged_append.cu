@@ -1,24 +1,34 @@
 // Tokens into the pages of their sequences, with the norm of every head of q and k and the rotation of
 // their positions on the way (qk_rope.cu has the mathematics; rope.cuh what is shared).
 //
-// Bound: HBM, each element of q, k and v read and written once.  A warp takes a token, or with few
-// tokens a part of its heads: D / 16 lanes hold a head's row, 16 channels each; the rows of q, then
-// k's, which go to their page, then v's, which are only moved there.  What a token needs besides its
-// rows (its sequence, its row, its page) hangs on one another, three loads deep: the first rows of
-// the token are on their way while it is found.
+// Bound: HBM, each element of q, k and v read and written once.  A warp takes tokens, or with few
+// tokens a part of one's heads: D / 16 lanes hold a head's row, 16 channels each; the rows of q, then
+// k's, which go to their page, then v's, which are only moved there.  A lane's channels are chunks of 16 bytes, a
+// row's lanes side by side in each (with 32 consecutive bytes a lane every load took two half sectors).  Rows come through shared memory by
+// cp.async, kSlots groups of them on their way a warp, across the borders of tokens: held in registers (three
+// groups a warp, and none on their way between two tokens) 4680 tokens of 36 heads took 16.4 us and 14,400 of
+// 72 heads 96; now 15.7 (5.5 TB/s) and 92.8 (5.7 TB/s), in replayed graphs; more slots or blocks change nothing.
+// Each lane reads back what it asked for itself, so no barrier is needed.
 #include <climits>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "paged.cuh"
 #include "rope.cuh"
+#include "tc.cuh"
 #include "tmap.h"
 
 namespace fastar {
 
 namespace {
 
-constexpr int kWarpsA = 4;
+constexpr int kWarpsA = 4, kSlots = 4, kBlocks = 5;   // warps of a block, groups of rows on their way, blocks an SM
+
+// 16 bytes of a row.
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float* f) { store8(p, f); }
+__device__ __forceinline__ void store16(float* p, const float* f) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
 
 // The sequence of a token: as many as end at or before it come earlier (cu does not fall).
 __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int64_t T, uint32_t tok, int lane) {
@@ -33,7 +43,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int64_t T, 
 
 // Inputs and outputs may be the same tensor: every lane reads its channels before it writes
 // them and no other lane does.  kAll: every pair turns.
-template <typename T, int D, bool kAll, int kAhead>
+template <typename T, int D, bool kAll>
 __global__ void __launch_bounds__(kWarpsA * 32)
     paged_append_kernel(const PagedAppendArgs a, const __grid_constant__ RopeTable tab) {
   pdl_wait();                      // the launch overlaps the end of the kernel before
@@ -65,36 +75,59 @@ __global__ void __launch_bounds__(kWarpsA * 32)
   const int64_t stride = (int64_t)gridDim.x * kWarpsA;
   // groups of rows side by side: of q, then of k, then of v
   const int gq = a.qo ? (a.Hq + RW - 1) / RW : 0, gk = (a.Hk + RW - 1) / RW, groups = gq + 2 * gk;
-  __syncthreads();
-  for (int64_t u = (int64_t)blockIdx.x * kWarpsA + (threadIdx.x >> 5); u < items; u += stride) {
+  // group lx of item lu is the next to be asked for, into slot `to`; 32 sizeof(T) / 2 bytes a lane
+  constexpr int NC = sizeof(T), EPC = 16 / NC;   // 16-byte chunks of a lane, channels of a chunk
+  extern __shared__ __align__(16) uint8_t ring[];
+  uint8_t* mine = ring + (threadIdx.x >> 5) * (kSlots * NC * 512) + lane * 16;
+  const int64_t u0 = (int64_t)blockIdx.x * kWarpsA + (threadIdx.x >> 5);
+  int64_t lu = u0;
+  int lx = (int)((uint32_t)u0 & (parts - 1)), to = 0, from = 0;
+  auto skip = [&]() {                      // (parts beyond the groups have none)
+    while (lx >= groups && lu < items) {
+      lu += stride;
+      lx = (int)((uint32_t)lu & (parts - 1));
+    }
+  };
+  skip();
+  auto ask = [&]() {
+    if (lu < items) {
+      const int side = lx < gq ? 0 : lx < gq + gk ? 1 : 2;
+      const int h = (lx - (side == 0 ? 0 : side == 1 ? gq : gq + gk)) * RW + sub;
+      if (h < (side == 0 ? a.Hq : a.Hk)) {
+        const TokView& t = side == 0 ? a.q : side == 1 ? a.k : a.v;
+        const T* p = static_cast<const T*>(t.p) + h * t.hs + (lu >> a.part_shift) * t.ts + li * EPC;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) tc::cp_async16(tc::smem_u32(mine + (to * NC + i) * 512), p + i * (D / NC), 16);
+      }
+      lx += (int)parts;
+      skip();
+    }
+    tc::cp_async_commit();
+    to = to + 1 == kSlots ? 0 : to + 1;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kSlots - 1; ++i) ask();
+  __syncthreads();                         // the tables; after the first rows are on their way
+  uint32_t turns = 0;                      // of this lane's pairs
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    turns |= (uint32_t)(axes[(2 * e / EPC * (D / NC) + li * EPC + 2 * e % EPC) / 2] < 3) << e;
+#pragma unroll 1
+  for (int64_t u = u0; u < items; u += stride) {
     const uint32_t tok = (uint32_t)(u >> a.part_shift), part = (uint32_t)u & (parts - 1);   // T fits 31 bits
-    Raw<T> v[kAhead];
-    auto load = [&](Raw<T>& r, int x) {
-      const int side = x < gq ? 0 : x < gq + gk ? 1 : 2;
-      const int h = (x - (side == 0 ? 0 : side == 1 ? gq : gq + gk)) * RW + sub;
-      const bool in = x < groups && h < (side == 0 ? a.Hq : a.Hk);
-      const TokView& t = side == 0 ? a.q : side == 1 ? a.k : a.v;
-      const T* p = static_cast<const T*>(t.p) + h * t.hs + (int64_t)tok * t.ts;
-#pragma unroll
-      for (int i = 0; i < (int)sizeof(T); ++i)
-        r.u[i] = in ? reinterpret_cast<const uint4*>(p + li * 16)[i] : make_uint4(0, 0, 0, 0);
-    };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) load(v[i], (int)(part + i * parts));
     // the token's sequence and row; tokens of none are left as they are
     const int b = sequence_of(a.cu, a.B, a.T, tok, lane);
-    if (b >= a.B) continue;
-    const paged::Seq s = paged::sequence(a.cu, a.at, a.B, a.T, cap, b, a.status);
+    const paged::Seq s = b < a.B ? paged::sequence(a.cu, a.at, a.B, a.T, cap, b, a.status) : paged::Seq{0, 0, 0};
     const int i = (int)tok - s.t0;
-    if (i < 0 || i >= s.nq) continue;
+    const bool known = i >= 0 && i < s.nq;
     const int64_t row = (int64_t)s.at + i;
     // where the row goes; -1: nowhere
     int64_t dst = -1;
-    if (row < cap) {
+    if (known && row < cap) {
       const int page = paged::page_of(a.table + (int64_t)b * a.max_pages, (int)(row >> a.pool.page_shift), a.pool.pages,
                                       a.status);
       if (page >= 0) dst = page * a.pool.ps + (row & ((1 << a.pool.page_shift) - 1)) * a.pool.rs;
-    } else {
+    } else if (known) {
       flag_status(a.status, FASTAR_DEV_BAD_LEN);
     }
     // the token's rotations: lane l forms those of pairs 2 l and 2 l + 1 (d = 64: l and no other)
@@ -123,47 +156,46 @@ __global__ void __launch_bounds__(kWarpsA * 32)
     bool norm = false;
     int side = -1;
 #pragma unroll 1
-    for (int x0 = (int)part; x0 < groups; x0 += kAhead * (int)parts) {
+    for (int x = (int)part; x < groups; x += (int)parts) {
+      ask();
+      tc::cp_async_wait<kSlots - 1>();
+      Raw<T> v;
 #pragma unroll
-      for (int n = 0; n < kAhead; ++n) {
-        const int x = x0 + n * (int)parts;
-        if (x >= groups) break;
-        const int of = x < gq ? 0 : x < gq + gk ? 1 : 2;
-        if (of == 2) {                       // v: as it is
-          const int h = (x - gq - gk) * RW + sub;
-          const Raw<T> r = v[n];
-          if (kAhead > 1) load(v[n], x + kAhead * (int)parts);
-          if (h < a.Hk && dst >= 0) {
-            uint4* p = reinterpret_cast<uint4*>(static_cast<T*>(a.pool.v) + dst + h * a.pool.hs + li * 16);
+      for (int e = 0; e < NC; ++e) v.u[e] = *reinterpret_cast<const uint4*>(mine + (from * NC + e) * 512);
+      from = from + 1 == kSlots ? 0 : from + 1;
+      if (!known) continue;
+      const int of = x < gq ? 0 : x < gq + gk ? 1 : 2;
+      if (of == 2) {                         // v: as it is
+        const int h = (x - gq - gk) * RW + sub;
+        if (h < a.Hk && dst >= 0) {
+          T* p = static_cast<T*>(a.pool.v) + dst + h * a.pool.hs + li * EPC;
 #pragma unroll
-            for (int e = 0; e < (int)sizeof(T); ++e) p[e] = r.u[e];
-          }
-          continue;
+          for (int e = 0; e < NC; ++e) *reinterpret_cast<uint4*>(p + e * (D / NC)) = v.u[e];
         }
-        if (side != of) {                    // once for q, once for k: rotations times weights
-          side = of;
-          norm = of ? a.wk != nullptr : a.wq != nullptr;
+        continue;
+      }
+      if (side != of) {                      // once for q, once for k: rotations times weights
+        side = of;
+        norm = of ? a.wk != nullptr : a.wq != nullptr;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int src = D == 128 ? li * 4 + (e >> 1) : li * 8 + e;
-            const float sn = __shfl_sync(0xffffffffu, D == 128 && (e & 1) ? sn1 : sn0, src);
-            const float cs = __shfl_sync(0xffffffffu, D == 128 && (e & 1) ? cs1 : cs0, src);
-            const float2 w2 = reinterpret_cast<const float2*>(&ws[of][li * 16])[e];
-            A[e] = cs * w2.x, B[e] = sn * w2.y, C[e] = sn * w2.x, E[e] = cs * w2.y;
-          }
+        for (int e = 0; e < 8; ++e) {
+          const int c = 2 * e / EPC * (D / NC) + li * EPC + 2 * e % EPC;         // the pair's first channel
+          const float sn = __shfl_sync(0xffffffffu, D == 128 && (e & 1) ? sn1 : sn0, c / (D / 32));
+          const float cs = __shfl_sync(0xffffffffu, D == 128 && (e & 1) ? cs1 : cs0, c / (D / 32));
+          const float2 w2 = *reinterpret_cast<const float2*>(&ws[of][c]);
+          A[e] = cs * w2.x, B[e] = sn * w2.y, C[e] = sn * w2.x, E[e] = cs * w2.y;
         }
-        float f[16];
-        expand(v[n], f);
-        if (kAhead > 1) load(v[n], x + kAhead * (int)parts);
-        const float r = norm ? rms_scale<D>(f, a.eps) : 1.f;
-        turn16<kAll>(f, A, B, C, E, r, axes + li * 8);
-        const int h = (of ? x - gq : x) * RW + sub;
-        if (h < (of ? a.Hk : a.Hq) && (of == 0 || dst >= 0)) {
-          T* p = (of ? static_cast<T*>(a.pool.k) + dst + h * a.pool.hs
-                     : static_cast<T*>(a.qo) + h * a.qo_hs + (int64_t)tok * a.qo_ts) + li * 16;
-          store8(p, f);
-          store8(p + 8, f + 8);
-        }
+      }
+      float f[16];
+      expand(v, f);
+      const float r = norm ? rms_scale<D>(f, a.eps) : 1.f;
+      turn16<kAll>(f, A, B, C, E, r, turns);
+      const int h = (of ? x - gq : x) * RW + sub;
+      if (h < (of ? a.Hk : a.Hq) && (of == 0 || dst >= 0)) {
+        T* p = (of ? static_cast<T*>(a.pool.k) + dst + h * a.pool.hs
+                   : static_cast<T*>(a.qo) + h * a.qo_hs + (int64_t)tok * a.qo_ts) + li * EPC;
+#pragma unroll
+        for (int e = 0; e < NC; ++e) store16(p + e * (D / NC), f + e * EPC);
       }
     }
   }
@@ -180,16 +212,14 @@ cudaError_t append_go(PagedAppendArgs a, const RopeTable& tab, bool all, cudaStr
   while ((1 << a.part_shift) < groups && (a.T << a.part_shift) < 16 * sms) ++a.part_shift;
   int64_t blocks = ((a.T << a.part_shift) + kWarpsA - 1) / kWarpsA;
   if (blocks < 1) blocks = 1;                // lengths alone
-  // one group a warp: as many warps as there are groups, with few registers; else four resident
-  // blocks a multiprocessor, which go on to their next tokens
-  const bool one = (1 << a.part_shift) >= groups;
-  const int64_t most = one ? 0x7fffffff : 4 * sms;
+  // resident blocks, which go on to their next tokens
+  constexpr int bytes = kWarpsA * kSlots * 512 * (int)sizeof(T);
+  const int64_t most = kBlocks * sms;
   const unsigned grid = (unsigned)(blocks < most ? blocks : most);
-  constexpr int kAhead = sizeof(T) == 2 ? 3 : 2;
-  const auto kernel = one ? all ? paged_append_kernel<T, D, true, 1> : paged_append_kernel<T, D, false, 1>
-                      : all ? paged_append_kernel<T, D, true, kAhead>
-                            : paged_append_kernel<T, D, false, kAhead>;
-  const cudaError_t e = launch_dependent(kernel, dim3(grid), dim3(kWarpsA * 32), 0, s, a, tab);
+  const auto kernel = all ? paged_append_kernel<T, D, true> : paged_append_kernel<T, D, false>;
+  cudaError_t e = opt_in_smem((const void*)kernel, bytes);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kernel, dim3(grid), dim3(kWarpsA * 32), bytes, s, a, tab);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -116,6 +116,9 @@ __global__ void __launch_bounds__(kWarpsR * 32)
     first = false;
     rotations();
     float A[8], B[8], C[8], E[8];
+    uint32_t turns = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) turns |= (uint32_t)(axes[li * 8 + e] < 3) << e;
     bool norm = false;
     int side = -1;
 #pragma unroll 1
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(kWarpsR * 32)
         expand(v[i], f);
         if (kAhead > 1) load(v[i], x + kAhead * (int)parts);
         const float r = norm ? rms_scale<D>(f, a.eps) : 1.f;
-        turn16<kAll>(f, A, B, C, E, r, axes + li * 8);
+        turn16<kAll>(f, A, B, C, E, r, turns);
         const int h = (isk ? x - gq : x) * RW + sub;
         if (h < (isk ? a.Hk : a.Hq)) {
           T* p = (isk ? static_cast<T*>(a.ko) + h * a.ko_hs + (int64_t)tok * a.ko_ts

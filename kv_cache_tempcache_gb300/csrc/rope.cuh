@@ -100,17 +100,17 @@ __device__ __forceinline__ float rms_scale(const float* f, float eps) {
   return y0 == 0.f ? 0.f : y0 * fmaf(-0.5f * z * y0, y0, 1.5f);
 }
 
-// Eight pairs turned: r (A x0 - B x1), r (C x0 + E x1), the rotations times the weights.
+// Eight pairs turned: r (A x0 - B x1), r (C x0 + E x1), the rotations times the weights.  turns: a bit a pair.
 template <bool kAll>
 __device__ __forceinline__ void turn16(float* f, const float* A, const float* B, const float* C, const float* E, float r,
-                                       const uint8_t* axes) {
+                                       uint32_t turns) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float a0 = f[2 * e], a1 = f[2 * e + 1];
     // a pair that does not turn is not multiplied by (1, 0): its neighbour may be infinite
-    const bool turns = kAll || axes[e] < 3;
-    f[2 * e] = (turns ? A[e] * a0 - B[e] * a1 : A[e] * a0) * r;
-    f[2 * e + 1] = (turns ? C[e] * a0 + E[e] * a1 : E[e] * a1) * r;
+    const bool on = kAll || (turns >> e & 1);
+    f[2 * e] = (on ? A[e] * a0 - B[e] * a1 : A[e] * a0) * r;
+    f[2 * e + 1] = (on ? C[e] * a0 + E[e] * a1 : E[e] * a1) * r;
   }
 }
 
