@@ -31,7 +31,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnArgs a) 
   constexpr int CPL = D / 32;
   const int lane = threadIdx.x & 31;
   const int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);       // (sequence, token, head)
-  pdl_wait();
+  // Where its partials lie is found while the attention still runs: at and cu come from before that, which has
+  // waited for them before it let this launch go.
   const int64_t per = (int64_t)a.max_q * a.Hq;
   if (u >= per * a.B) return;
   const int b = (int)(u / per);
@@ -44,6 +45,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnArgs a) 
   const int h = head / a.group;
   const int64_t row0 = paged::partial_row(a, work.first, h, i * a.group + head - h * a.group);
   const int64_t step = (int64_t)a.Hkv * a.group * a.max_q;               // from split to split
+  pdl_wait();                            // the partials
   constexpr int kPer = kMaxSplits / 32;
   float m = neg_inf(), l = 0.f, o[CPL];
 #pragma unroll
@@ -131,9 +133,9 @@ size_t slot_bytes(const Plan& p, int d, int Hq, int max_q) {
 Plan make_plan(int dtype, int d, int Hq, int Hkv, int B, int max_q, int64_t keys) {
   const int64_t rows = (int64_t)(Hq / Hkv) * max_q;
   if (dtype == FASTAR_F32) {
-    // one block a multiprocessor, two tiles of 64 keys
+    // two blocks a multiprocessor, a tile of 64 keys
     const int64_t units = (rows + kF32Rows - 1) / kF32Rows * Hkv;
-    return plan_slots(kF32, units, B, keys, sm_count(), kF32Keys, 2);
+    return plan_slots(kF32, units, B, keys, 2 * sm_count(), kF32Keys, 1);
   }
   // four blocks a multiprocessor, of which two are resident; eight tiles of 16 keys a warp
   if (rows <= kFewRows) return plan_slots(kFew, Hkv, B, keys, 4 * sm_count(), 16, 8 * kFewWarps);

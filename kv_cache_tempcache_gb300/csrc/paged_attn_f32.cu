@@ -1,14 +1,19 @@
 // Softmax attention over a paged cache in fp32: 32 rows and 64 keys at a time.
 //
 // Two rows a half warp: a thread forms the logits of two rows and four keys, then two rows and D / 16
-// channels of the output.  Keys that no row of the block sees are zeros in shared memory; where only
-// some rows see a key the others leave it out (not by a weight of 0: its value may be infinite).
+// channels of the output, two products an instruction.  A tile's keys and values come by cp.async while the one before
+// is worked on; where their rows lie is looked up one tile earlier still.  Rows that no row of the block
+// sees come as zeros; where only some rows see a key the others leave it out (not by a weight of 0: its value may
+// be infinite).
+// Bound: with few rows latency (a block has one or two tiles), with many the shared memory's 128 bytes a clock, of
+// which every warp takes all of a tile.
 #include <climits>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "paged.cuh"
 #include "paged_attn.h"
+#include "tc.cuh"
 #include "tmap.h"
 
 namespace fastar {
@@ -20,17 +25,28 @@ constexpr int kRows = kF32Rows, kKeys = kF32Keys;
 template <int D>
 struct F32Layout {
   static constexpr int ld = D + 4;                       // float4 reads of 8 rows hit 8 bank groups
-  static constexpr int q = 0, k = q + kRows * ld, v = k + kKeys * ld, p = v + kKeys * ld;
+  static constexpr int q = 0, kv = q + kRows * ld, stage = 2 * kKeys * ld, p = kv + 2 * stage;   // K, V; two stages
   static constexpr int ldp = kKeys + 4;
-  static constexpr int bytes = (p + kRows * ldp) * 4;
+  static constexpr int off = p + kRows * ldp;            // int64: where a tile's rows lie, two tiles'
+  static constexpr int bytes = off * 4 + 2 * kKeys * 8;
 };
+
+// Two products or sums an instruction, on pairs of registers.
+__device__ __forceinline__ void fma2(float2& c, float ax, float ay, float bx, float by) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%0, %1};\n"
+      " fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z;\n}\n"
+      : "+f"(c.x), "+f"(c.y)
+      : "f"(ax), "f"(ay), "f"(bx), "f"(by));
+}
 
 template <int D>
 __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs a, int row_tiles) {
   using Lay = F32Layout<D>;
   extern __shared__ __align__(16) float sm[];
-  float *sq = sm + Lay::q, *sk = sm + Lay::k, *sv = sm + Lay::v, *sp = sm + Lay::p;
-  pdl_wait();
+  float *sq = sm + Lay::q, *sp = sm + Lay::p;
+  int64_t* rows_at = reinterpret_cast<int64_t*>(sm + Lay::off);
+  pdl_wait();                              // the launch overlaps the end of the kernel before
+  pdl_trigger();                           // the join's CTAs may come, find their work and wait
   // heads side by side, then row tiles from the last, then slots
   int u = blockIdx.x;
   const int h = u % a.Hkv;
@@ -53,7 +69,8 @@ __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs
   int64_t tok[2];
   int head[2];
   bool has[2];
-  float m[2], l[2], o[2][D / 16];
+  float m[2], l[2];
+  float2 o[2][D / 32];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = min(r0 + 2 * ty + i, rl);
@@ -64,36 +81,56 @@ __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs
     m[i] = neg_inf();
     l[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
+    for (int c = 0; c < D / 32; ++c) o[i][c] = make_float2(0.f, 0.f);
   }
-  for (int x = threadIdx.x; x < kRows * (D / 8); x += 256) {
-    const int row = x / (D / 8), c = x % (D / 8) * 8, r = min(r0 + row, rl);
-    float f[8];
-    load8(static_cast<const float*>(a.q.p) + (int64_t)(h * G + r % G) * a.q.hs + (int64_t)(s.t0 + r / G) * a.q.ts + c, f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sq[row * Lay::ld + c + e] = f[e];
-  }
-  const float sl2 = a.scale * 1.4426950408889634f;
   const int32_t* table = a.table + (int64_t)b * a.max_pages;
+  // where row threadIdx.x of tile j lies; -1: it comes as zeros
+  auto look = [&](int j) {
+    if (threadIdx.x >= kKeys || j >= part.j1) return;
+    const int key = tiles.key(j) + (int)threadIdx.x;
+    int64_t at = -1;
+    if (tiles.any(key)) {
+      const int page = paged::page_of(table, key >> a.pool.page_shift, a.pool.pages, a.status);
+      if (page >= 0) at = page * a.pool.ps + h * a.pool.hs + (key & ((1 << a.pool.page_shift) - 1)) * a.pool.rs;
+    }
+    rows_at[(j & 1) * kKeys + threadIdx.x] = at;
+  };
+  auto bring = [&](int j) {
+    if (j < part.j1) {
+      float* to = sm + Lay::kv + (j & 1) * Lay::stage;
+      for (int x = threadIdx.x; x < kKeys * (D / 4); x += 256) {
+        const int row = x / (D / 4), c = x % (D / 4) * 4;
+        const int64_t at = rows_at[(j & 1) * kKeys + row];
+        const int64_t from = at < 0 ? 0 : at + c;
+        tc::cp_async16(tc::smem_u32(to + row * Lay::ld + c), static_cast<const float*>(a.pool.k) + from, at < 0 ? 0 : 16);
+        tc::cp_async16(tc::smem_u32(to + (kKeys + row) * Lay::ld + c), static_cast<const float*>(a.pool.v) + from,
+                       at < 0 ? 0 : 16);
+      }
+    }
+    tc::cp_async_commit();
+  };
+  look(part.j0);
+  for (int x = threadIdx.x; x < kRows * (D / 4); x += 256) {
+    const int row = x / (D / 4), c = x % (D / 4) * 4, r = min(r0 + row, rl);
+    tc::cp_async16(tc::smem_u32(sq + row * Lay::ld + c),
+                   static_cast<const float*>(a.q.p) + (int64_t)(h * G + r % G) * a.q.hs + (int64_t)(s.t0 + r / G) * a.q.ts + c,
+                   16);
+  }
+  __syncthreads();
+  bring(part.j0);                                        // with the query rows
+  look(part.j0 + 1);
+  const float sl2 = a.scale * 1.4426950408889634f;
   for (int j = part.j0; j < part.j1; ++j) {
     const int key0 = tiles.key(j);
+    __syncthreads();                                     // tile j - 1 has been used, and where j + 1's rows lie is known
+    bring(j + 1);
+    tc::cp_async_wait<1>();
     __syncthreads();
-    for (int x = threadIdx.x; x < kKeys * (D / 8); x += 256) {
-      const int row = x / (D / 8), c = x % (D / 8) * 8, key = key0 + row;
-      float fk[8] = {}, fv[8] = {};
-      if (tiles.any(key)) {
-        const int page = paged::page_of(table, key >> a.pool.page_shift, a.pool.pages, a.status);
-        if (page >= 0) {
-          const int64_t at = page * a.pool.ps + h * a.pool.hs + (key & ((1 << a.pool.page_shift) - 1)) * a.pool.rs + c;
-          load8(static_cast<const float*>(a.pool.k) + at, fk);
-          load8(static_cast<const float*>(a.pool.v) + at, fv);
-        }
-      }
+    look(j + 2);
+    const float *sk = sm + Lay::kv + (j & 1) * Lay::stage, *sv = sk + kKeys * Lay::ld;
+    float2 x2[2][4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sk[row * Lay::ld + c + e] = fk[e], sv[row * Lay::ld + c + e] = fv[e];
-    }
-    __syncthreads();
-    float x[2][4] = {};
+    for (int k = 0; k < 4; ++k) x2[0][k] = x2[1][k] = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
       const float4 q0 = *reinterpret_cast<const float4*>(&sq[2 * ty * Lay::ld + c]);
@@ -101,10 +138,15 @@ __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float4 kv = *reinterpret_cast<const float4*>(&sk[(tx + 16 * k) * Lay::ld + c]);
-        x[0][k] = fmaf(q0.x, kv.x, fmaf(q0.y, kv.y, fmaf(q0.z, kv.z, fmaf(q0.w, kv.w, x[0][k]))));
-        x[1][k] = fmaf(q1.x, kv.x, fmaf(q1.y, kv.y, fmaf(q1.z, kv.z, fmaf(q1.w, kv.w, x[1][k]))));
+        fma2(x2[0][k], q0.x, q0.y, kv.x, kv.y);
+        fma2(x2[0][k], q0.z, q0.w, kv.z, kv.w);
+        fma2(x2[1][k], q1.x, q1.y, kv.x, kv.y);
+        fma2(x2[1][k], q1.z, q1.w, kv.z, kv.w);
       }
     }
+    float x[2][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[0][k] = x2[0][k].x + x2[0][k].y, x[1][k] = x2[1][k].x + x2[1][k].y;
     uint64_t bits[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -129,29 +171,24 @@ __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs
       m[i] = mn;
       l[i] = l[i] * f + sum;
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
+      for (int c = 0; c < D / 32; ++c) o[i][c].x *= f, o[i][c].y *= f;
     }
     __syncwarp();
     const bool whole = tiles.all(key0);
-#pragma unroll 2
+#pragma unroll 4
     for (int k = 0; k < kKeys; ++k) {
       const float p0 = sp[2 * ty * Lay::ldp + k], p1 = sp[(2 * ty + 1) * Lay::ldp + k];
       const bool in0 = whole || (bits[0] >> k & 1), in1 = whole || (bits[1] >> k & 1);
 #pragma unroll
-      for (int c = 0; c < D / 16; c += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(&sv[k * Lay::ld + tx * 4 + c * 16]);
-        if (in0) {
-          o[0][c] = fmaf(p0, v.x, o[0][c]), o[0][c + 1] = fmaf(p0, v.y, o[0][c + 1]);
-          o[0][c + 2] = fmaf(p0, v.z, o[0][c + 2]), o[0][c + 3] = fmaf(p0, v.w, o[0][c + 3]);
-        }
-        if (in1) {
-          o[1][c] = fmaf(p1, v.x, o[1][c]), o[1][c + 1] = fmaf(p1, v.y, o[1][c + 1]);
-          o[1][c + 2] = fmaf(p1, v.z, o[1][c + 2]), o[1][c + 3] = fmaf(p1, v.w, o[1][c + 3]);
-        }
+      for (int c = 0; c < D / 64; ++c) {
+        const float4 v = *reinterpret_cast<const float4*>(&sv[k * Lay::ld + tx * 4 + c * 64]);
+        if (in0) fma2(o[0][2 * c], p0, p0, v.x, v.y), fma2(o[0][2 * c + 1], p0, p0, v.z, v.w);
+        if (in1) fma2(o[1][2 * c], p1, p1, v.x, v.y), fma2(o[1][2 * c + 1], p1, p1, v.z, v.w);
       }
     }
     __syncwarp();
   }
+  tc::cp_async_wait<0>();                                // (a block without a tile)
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -166,11 +203,13 @@ __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs
     }
     const float f = partial ? 1.f : 1.f / l[i];
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-      const int ch = tx * 4 + (c >> 2) * 64 + (c & 3);
-      const float y = live ? o[i][c] * f : 0.f;
-      if (partial) a.part_o[row * D + ch] = y;
-      else static_cast<float*>(a.out)[head[i] * a.o_hs + tok[i] * a.o_ts + ch] = y;
+    for (int c = 0; c < D / 64; ++c) {
+      const int ch = tx * 4 + c * 64;
+      const float2 y0 = o[i][2 * c], y1 = o[i][2 * c + 1];
+      const float4 y = live ? make_float4(y0.x * f, y0.y * f, y1.x * f, y1.y * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float* to = partial ? a.part_o + row * D + ch
+                          : static_cast<float*>(a.out) + head[i] * a.o_hs + tok[i] * a.o_ts + ch;
+      *reinterpret_cast<float4*>(to) = y;
     }
   }
 }
