@@ -665,8 +665,8 @@ int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d
  * axes, theta and accuracy as in fastar_qk_norm_rope; a token's position is pos int32 [T, 3] or, NULL, its
  * row r = at + i on the grid: frame r / (grid_h grid_w), row (r / grid_w) % grid_h, column
  * r % grid_w (grid 1 x 1: r itself turns the first axis).  v goes as it is.
- * len_out[b] = at + tokens (optional; held to the sequence's rows; no element in common with at,
- * FASTAR_EINVAL otherwise; of a skipped sequence 0).
+ * len_out[b] = at + tokens (optional; held to the sequence's rows; no element in common with at, cu or
+ * table, FASTAR_EINVAL otherwise; of a skipped sequence 0).
  * Rows past the sequence's last are dropped and set FASTAR_DEV_BAD_LEN, rows whose table
  * entry is no page are dropped and set FASTAR_DEV_BAD_INDEX; their q_out is written all the same.
  * Other rows of the pools are left as they were.  Of two tokens whose rows share a slot (two

@@ -66,6 +66,11 @@ int check_paged(int B, int64_t T, const int32_t* cu, int page, int64_t max_pages
   if (!cu && T % B) return FASTAR_EINVAL;
   return FASTAR_OK;
 }
+// Do n elements from a on and m from b on have one in common?
+bool shares(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q ? q - p < (uintptr_t)n * sizeof(int32_t) : p - q < (uintptr_t)m * sizeof(int32_t);
+}
 int held32(int64_t x) { return (int)(x < INT32_MAX ? x : INT32_MAX); }
 
 // fastar_packed_call: a 64-bit word as an argument of type T; false if an int does not fit.
@@ -887,10 +892,10 @@ int fastar_paged_append(int dtype, int B, int64_t T, const int32_t* cu, int d, i
   if (sum > 0 && !pos && (grid_h < 1 || grid_w < 1)) return FASTAR_EINVAL;
   if ((wq && !aligned16(wq)) || (wk && !aligned16(wk))) return FASTAR_EINVAL;
   if (!table || !at) return FASTAR_EINVAL;
-  if (len_out) {   // the tokens' blocks read `at` while one of them writes: no element in common
-    const uintptr_t p = reinterpret_cast<uintptr_t>(at), o = reinterpret_cast<uintptr_t>(len_out);
-    if ((p < o ? o - p : p - o) < (uintptr_t)B * sizeof(int32_t)) return FASTAR_EINVAL;
-  }
+  // the tokens' blocks read at, cu and table while one of them writes: no element in common
+  if (len_out && (shares(len_out, B, at, B) || (cu && shares(len_out, B, cu, (int64_t)B + 1)) ||
+                  shares(len_out, B, table, B * max_pages)))
+    return FASTAR_EINVAL;
   if (T == 0 && !len_out) return FASTAR_OK;
   if ((rc = check_tok(k, dtype, d, k_head_stride, k_token_stride, T, Hk))) return rc;
   if ((rc = check_tok(v, dtype, d, v_head_stride, v_token_stride, T, Hk))) return rc;

@@ -30,15 +30,19 @@ __device__ __forceinline__ void store16(float* p, const float* f) {
   *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
 }
 
-// The sequence of a token: as many as end at or before it come earlier (cu does not fall).
+// The sequence of a token: as many as end at or before it come earlier (cu does not fall).  A warp looks at 32 of them
+// at a time, spread over what is left.
 __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int64_t T, uint32_t tok, int lane) {
   if (!cu) return B == 1 ? 0 : (int)(tok / (uint32_t)(T / B));
-  int n = 0;
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    const bool before = b0 + lane < B && cu[b0 + lane + 1] <= (int)tok;
-    n += __popc(__ballot_sync(0xffffffffu, before));
+  int lo = 0, hi = B;                        // it is one of lo .. hi (hi: behind the last)
+  while (hi - lo > 32) {
+    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const int n = __popc(__ballot_sync(0xffffffffu, i < hi && cu[i + 1] <= (int)tok));
+    if (n == 0) return lo;
+    hi = min(hi, lo + n * step);             // those probes' sequences end before the token, the next one's does not
+    lo += (n - 1) * step + 1;
   }
-  return n;
+  return lo + __popc(__ballot_sync(0xffffffffu, lo + lane < hi && cu[lo + lane + 1] <= (int)tok));
 }
 
 // Inputs and outputs may be the same tensor: every lane reads its channels before it writes

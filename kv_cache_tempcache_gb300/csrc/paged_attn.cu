@@ -137,8 +137,9 @@ Plan make_plan(int dtype, int d, int Hq, int Hkv, int B, int max_q, int64_t keys
     const int64_t units = (rows + kF32Rows - 1) / kF32Rows * Hkv;
     return plan_slots(kF32, units, B, keys, 2 * sm_count(), kF32Keys, 1);
   }
-  // four blocks a multiprocessor, of which two are resident; eight tiles of 16 keys a warp
-  if (rows <= kFewRows) return plan_slots(kFew, Hkv, B, keys, 4 * sm_count(), 16, 8 * kFewWarps);
+  // two blocks a multiprocessor, all resident; eight tiles of 16 keys a warp (a few tokens of six long sequences take
+  // 89 us with two blocks, 110 with three, 102 with four, 123 with eight)
+  if (rows <= kFewRows) return plan_slots(kFew, Hkv, B, keys, 2 * sm_count(), 16, 8 * kFewWarps);
   // one CTA, or pair of them, a multiprocessor or two
   const bool alone = d == 128 && rows <= 128;
   const int shares = d == 128 && !alone ? sm_count() / 2 : sm_count();

@@ -9,7 +9,8 @@ namespace fastar {
 // The tensor map of a bf16 pool: (channel, slot, head, page), boxes of 64 channels and `rows` slots.
 inline bool make_pool_tmap(CUtensorMap* m, const PagedAttnArgs& a, const void* pool, int d, int rows) {
   const uint64_t dims[4] = {(uint64_t)d, (uint64_t)1 << a.pool.page_shift, (uint64_t)a.Hkv, (uint64_t)a.pool.pages};
-  const uint64_t strides[3] = {(uint64_t)a.pool.rs * 2, (uint64_t)a.pool.hs * 2, (uint64_t)a.pool.ps * 2};
+  // (a dimension of one element: any stride will do but 0)
+  const uint64_t strides[3] = {(uint64_t)a.pool.rs * 2, (uint64_t)(a.Hkv > 1 ? a.pool.hs : d) * 2, (uint64_t)a.pool.ps * 2};
   return make_tmap_bf16_4d(m, pool, dims, strides, 64, rows);
 }
 

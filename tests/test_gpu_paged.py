@@ -387,6 +387,70 @@ def test_offsets_past_32_bits(nq):
     check_attn("bf16", y[2], kp[lo:], vp[lo:], table - lo, at, None, 0.1, 1, 0, 0, out, lse)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_sequences_than_are_dealt_out(dtype):
+    rng = np.random.default_rng(0)
+    B = 300
+    nq, at = rng.integers(0, 3, B).tolist(), rng.integers(0, 200, B).tolist()
+    at[7], nq[7] = 3000, 2
+    c = attn_case(dtype, nq, at, 1, 2, 64, 16, "hnd", 1, 0, 0, seed=1, tail=1)
+    out, lse = run_attn(*c, 0.125, 1, 0, 0)
+    check_attn(dtype, *c, 0.125, 1, 0, 0, out, lse)
+
+
+@pytest.mark.parametrize("B,most,G,d,block,window,sinks", [(70, 100, 2, 64, 1, 90, 5), (70, 40, 4, 128, 1, 0, 0),
+                                                          (3, 1100, 8, 64, 1, 200, 20), (40, 300, 3, 128, 0, 0, 0),
+                                                          (2, 1100, 16, 128, 1, 64, 0), (33, 17, 2, 128, 1, 0, 0)])
+def test_work_of_many_and_uneven_sequences(B, most, G, d, block, window, sinks):
+    """Sequences of very different lengths, some without tokens, more than 32 of them; row tiles of one by the
+    dozen."""
+    rng = np.random.default_rng(B)
+    nq = (most * rng.random(B) ** 3).astype(int)
+    nq[rng.integers(0, B, B // 4)] = 0
+    nq[-1] = most
+    at = (800 * rng.random(B) ** 3).astype(int)
+    c = attn_case("bf16", nq.tolist(), at.tolist(), 2 if B > 3 else 1, G, d, 16, "nhd", block, window, sinks, seed=B, tail=2)
+    for ws in (True, False):
+        out, lse = run_attn(*c, 1 / math.sqrt(d), block, window, sinks, ws=ws)
+        check_attn("bf16", *c, 1 / math.sqrt(d), block, window, sinks, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [1, 3, 50])
+def test_tokens_before_the_first_sequence_and_other_strides(dtype, nq):
+    """cu that does not begin at 0, one KV head, one page, rows of q and out with gaps between, head-major."""
+    dt, d, page = DT[dtype], 64, 128
+    T = nq + 7
+    q = _rand((3, T + 2, d + 8), 1, 1.5).to(dt)[:, :T, :d]
+    out = torch.full((3, T + 3, d + 16), 7.0, dtype=dt, device=DEV)[:, :T, 8:8 + d]
+    kp, vp = (torch.full((1, 1, page, d + 8), 3.0, dtype=dt, device=DEV)[..., :d] for _ in range(2))
+    k, v = (_rand((1, T, d + 24), s).to(dt)[..., 16:16 + d] for s in (2, 3))
+    table, at, cu = np.zeros((1, 1), np.int32), np.array([20]), np.array([4, 4 + nq])
+    kp[0, 0, :20], vp[0, 0, :20] = _rand((20, d), 4).to(dt), _rand((20, d), 5).to(dt)
+    qo = torch.full((3, T, d), 9.0, dtype=dt, device=DEV)
+    L.fastar_paged_append(k, v, kp, vp, _i32(table), _i32(at), q=q, q_out=qo, cu=_i32(cu), axes=(24, 20, 20), grid=(3, 4))
+    st, lse = _i32([0]), torch.full((3, T), 7.0, device=DEV)
+    L.fastar_paged_attn(q, kp, vp, _i32(table), _i32(at), 0.125, out, lse, cu=_i32(cu), max_q=nq, block=1, window=15, sinks=2,
+                        dev_status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    want = P.append(_np(k), _np(v), np.full((1, 1, page, d), 3.0), np.full((1, 1, page, d), 3.0), table, at, cu, _np(q), None,
+                    None, 1e-6, (24, 20, 20), None, (3, 4))
+    assert np.array_equal(_np(vp)[0, 0, 20:], want[1][0, 0, 20:])
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    assert (np.abs(_np(qo) - want[2]) <= half * np.abs(want[2]) + 2.0 ** -19 * want[6])[:, 4:4 + nq].all()
+    assert bool((qo[:, :4] == 9.0).all()) and bool((qo[:, 4 + nq:] == 9.0).all())
+    check_attn(dtype, q, kp, vp, table, at, cu, 0.125, 1, 15, 2, out, lse)
+
+
+def test_positions_and_sequences_of_thousands_of_short_ones():
+    """A token each of 3000 sequences: every token finds its own."""
+    B, d, page = 3000, 64, 16
+    rng = np.random.default_rng(3)
+    nq, at = (rng.random(B) < 0.7).astype(int).tolist(), rng.integers(0, 40, B).tolist()
+    assert run_append("bf16", nq, at, 1, 1, d, page, "hnd", False, (64, 0, 0), (1, 1), False, tail=5) == 0
+
+
 # ---- both together --------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -51,6 +51,14 @@ def test_append_refusals(lib, kw, code):
     assert append(lib, **kw) == code
 
 
+@pytest.mark.parametrize("B", [2, 5])
+def test_lengths_that_are_read_and_written_share_no_element(lib, B):
+    far = dict(at=FAKE + 2 ** 20, cu=FAKE + 2 ** 21, table=FAKE + 2 ** 22, B=B, T=10, max_pages=3)
+    for name, n in (("at", B), ("cu", B + 1), ("table", 3 * B)):
+        for off in range(-4 * (B - 1), 4 * n, 4):
+            assert append(lib, **dict(far, ln=far[name] + off)) == L.EINVAL, (name, off)
+
+
 def attn(lib, q=FAKE, dtype=L.BF16, B=2, T=4, cu=FAKE, max_q=3, Hq=4, Hkv=2, d=128, qs=(512, 128), kp=FAKE, vp=FAKE + 16,
          pages=8, page=16, ps=(4096, 2048, 128), table=FAKE, max_pages=4, at=FAKE, block=0, window=0, sinks=0, scale=0.1,
          out=FAKE, os=(512, 128), ws=None, nb=0):
