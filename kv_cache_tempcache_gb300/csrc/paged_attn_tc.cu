@@ -268,7 +268,11 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         tc::tmem_pin32(x + 32);
         if (__builtin_expect(cut, 0)) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) x[c] = bits[c >> 5] >> (c & 31) & 1 ? x[c] : neg_inf();
+          for (int k = 0; k < 2; ++k)
+            if (!__all_sync(0xffffffffu, bits[k] == 0xffffffffu)) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) x[32 * k + c] = bits[k] >> c & 1 ? x[32 * k + c] : neg_inf();
+            }
         }
         const float top = row_max<64>(x);         // the largest of them, not scaled yet
         // Both warps of the rows stop together when a P would pass 2^kTop (the scale is positive, so the

@@ -2,13 +2,13 @@
 // the sequences' lengths are.
 //
 // An item is up to `per` rows of a (sequence, KV head): its row tiles 2 (or 1, where the rows fill half of them or
-// less), its key tiles paged.cuh's.  It counts kFixed units and kFull (fewer with one row tile) for each key tile,
+// less), its key tiles paged.cuh's.  It counts fixed_units and kFull (fewer with one row tile) for each key tile,
 // as its time goes: 1.4 us a key tile, 1.15 with one row tile (a pair; it waits for K and V, which it takes twice as
 // fast), some 8 us around them.  Items lie in a row: sequences,
 // their row tiles, the KV heads side by side.  Share p of P is the units W p / P .. W (p + 1) / P of that row, so
 // that all shares end together, whatever the lengths: borders cut items between two key tiles (12 heads of 4680
 // tokens are 120 items on 76 pairs of CTAs: in whole items 2 waves, dealt out 1.53).  A cut leaves parts of kMinTiles
-// key tiles or more; there are no more shares than have kLeast units each.  Without a workspace borders move to
+// key tiles or more; there are no more shares than have an item of four key tiles each.  Without a workspace borders move to
 // the nearer end of the item.
 #pragma once
 
@@ -19,8 +19,10 @@
 namespace fastar {
 namespace paged {
 
-constexpr int kFixed = 36, kFull = 6, kLeast = 60, kMinTiles = 3;
-__device__ __forceinline__ int half_units(int per) { return per == 512 ? 5 : 4; }     // pairs of CTAs, single ones
+constexpr int kFull = 6, kMinTiles = 3;
+// pairs of CTAs, single ones
+__device__ __forceinline__ int half_units(int per) { return per == 512 ? 5 : 4; }
+__device__ __forceinline__ int fixed_units(int per) { return per == 512 ? 36 : 24; }
 constexpr int kMaxShares = 256;          // the plan asks for no more
 constexpr int kItems = 8;                // items of a CTA that are known at once
 
@@ -58,7 +60,7 @@ __device__ __forceinline__ int item_units(const PagedAttnArgs& a, const Seq& s, 
   if (r0 >= rows) return 0;
   nt = rows - r0 > per / 2 ? 2 : 1;
   tiles.set(a, s, r0 / a.group, (min(r0 + per, rows) - 1) / a.group);
-  return kFixed + tiles.n * (nt == 2 ? kFull : half_units(per));
+  return fixed_units(per) + tiles.n * (nt == 2 ? kFull : half_units(per));
 }
 
 __device__ __forceinline__ Seq shfl_seq(const Seq& s, int from) {
@@ -128,7 +130,7 @@ __device__ __forceinline__ void find_share(const PagedAttnArgs& a, Share& sh, in
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   sh.all = sum * a.Hkv;
-  const int64_t most = sh.all / kLeast;
+  const int64_t most = sh.all / (fixed_units(per) + 4 * kFull);
   sh.shares = most < 1 ? 1 : most < a.shares ? (int)most : a.shares;
   sh.end = p >= sh.shares;
   sh.from = share_border(sh, p);
@@ -170,7 +172,7 @@ __device__ __forceinline__ int border_tile(const Share& sh, const Item& it, int6
   if (o <= 0) return 0;
   if (o >= it.units) return n;
   if (!sh.cuts) return 2 * o <= it.units ? 0 : n;
-  const int j = o <= kFixed ? 0 : (int)(o - kFixed) / (it.nt == 2 ? kFull : half_units(per));
+  const int fixed = fixed_units(per), j = o <= fixed ? 0 : (int)(o - fixed) / (it.nt == 2 ? kFull : half_units(per));
   return j < kMinTiles ? 0 : n - j < kMinTiles ? n : j;
 }
 __device__ __forceinline__ int border(const Share& sh, int p, const Item& it, int per) {
