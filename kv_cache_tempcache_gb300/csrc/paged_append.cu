@@ -51,7 +51,6 @@ template <typename T, int D, bool kAll>
 __global__ void __launch_bounds__(kWarpsA * 32)
     paged_append_kernel(const PagedAppendArgs a, const __grid_constant__ RopeTable tab) {
   pdl_wait();                      // the launch overlaps the end of the kernel before
-  pdl_trigger();                   // and the next one's CTAs may come and wait
   __shared__ __align__(16) uint64_t steps[64];
   __shared__ uint8_t axes[64];
   __shared__ __align__(16) float ws[2][D];

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs
   float *sq = sm + Lay::q, *sp = sm + Lay::p;
   int64_t* rows_at = reinterpret_cast<int64_t*>(sm + Lay::off);
   pdl_wait();                              // the launch overlaps the end of the kernel before
-  pdl_trigger();                           // the join's CTAs may come, find their work and wait
+  if (a.extra > 0) pdl_trigger();          // the join's CTAs may come, find their work and wait
   // heads side by side, then row tiles from the last, then slots
   int u = blockIdx.x;
   const int h = u % a.Hkv;

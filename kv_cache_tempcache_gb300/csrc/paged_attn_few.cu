@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(W * 32)
     tc::tma_prefetch_desc(&vmap);
   }
   pdl_wait();                              // the launch overlaps the end of the kernel before
-  pdl_trigger();                           // the join's CTAs may come, find their work and wait
+  if (a.extra > 0) pdl_trigger();          // the join's CTAs may come, find their work and wait
   // heads side by side, then slots
   paged::Work work;
   const int slot = (int)(blockIdx.x / (uint32_t)a.Hkv), h = (int)(blockIdx.x - (uint32_t)slot * (uint32_t)a.Hkv);

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   __syncthreads();
   if (kCta == 2) pair_arrive();                          // this CTA's barriers are ready
   pdl_wait();                            // the launch overlaps the end of the kernel before
-  pdl_trigger();                         // the join's CTAs may come and wait
+  if (a.part_o) pdl_trigger();           // the join's CTAs may come and wait
   volatile int* abort = &sm.abort;
   // Item x of this CTA: null at the end, or after a wait that gave up (`ok` says which).
   auto item_at = [&](int x, bool& ok) -> const Item* {
