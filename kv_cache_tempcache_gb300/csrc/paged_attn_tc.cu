@@ -33,8 +33,8 @@
 // warps' instructions as much as bytes.  A tile of one row tile alone waits for K and V: 1.15 us.
 // Measured, d = 128: 9728 tokens of 4 heads over 37,440 rows 413 to 430 us (1740 to 1800 TFLOP/s, 0.91 to 0.95 of the bf16 rate
 // measured for a library product); 4680 tokens of 12 heads over the same 690 us in a short run, 781 in a long one, under
-// the power limit; the first 4680 tokens in three frames 93 us; 16,384 causal tokens of 16 heads of 4 with a window of 4096 342 to
-// 354 us.  Seven ragged causal sequences of up to 777 tokens, d = 64: 47 us.
+// the power limit; the first 4680 tokens in three frames 91 us; 16,384 causal tokens of 16 heads of 4 with a window of 4096 342 to
+// 354 us.  Seven ragged causal sequences of up to 777 tokens, d = 64: 44 us.
 //
 // Numbers: logits, maxima, sums and outputs are fp32.  P is bf16, as V is (a product has one type):
 // 2^-8 of itself, at every magnitude, since bf16 has fp32's exponents.

@@ -4,12 +4,13 @@
 // An item is up to `per` rows of a (sequence, KV head): its row tiles 2 (or 1, where the rows fill half of them or
 // less), its key tiles paged.cuh's.  It counts fixed_units and kFull (fewer with one row tile) for each key tile,
 // as its time goes: 1.4 us a key tile, 1.15 with one row tile (a pair; it waits for K and V, which it takes twice as
-// fast), some 8 us around them.  Items lie in a row: sequences,
-// their row tiles, the KV heads side by side.  Share p of P is the units W p / P .. W (p + 1) / P of that row, so
+// fast), some 8 us around them (5 at d = 64).  Items lie in a row: sequences, their row tiles, the KV heads side by
+// side.  Share p of P is the units W p / P .. W (p + 1) / P of that row, so
 // that all shares end together, whatever the lengths: borders cut items between two key tiles (12 heads of 4680
 // tokens are 120 items on 76 pairs of CTAs: in whole items 2 waves, dealt out 1.53).  A cut leaves parts of kMinTiles
-// key tiles or more; there are no more shares than have an item of four key tiles each.  Without a workspace borders move to
-// the nearer end of the item.
+// key tiles or more (with three instead of one, ragged sequences of 7 key tiles a piece took 47.2 us instead of 44.4: what
+// one share lost its neighbour had to do); there are no more shares than have an item of four key tiles each.  Without a
+// workspace borders move to the nearer end of the item.
 #pragma once
 
 #include <climits>
@@ -19,10 +20,10 @@
 namespace fastar {
 namespace paged {
 
-constexpr int kFull = 6, kMinTiles = 3;
+constexpr int kFull = 6, kMinTiles = 1;
 // pairs of CTAs, single ones
 __device__ __forceinline__ int half_units(int per) { return per == 512 ? 5 : 4; }
-__device__ __forceinline__ int fixed_units(int per) { return per == 512 ? 36 : 24; }
+__device__ __forceinline__ int fixed_units(int per) { return per == 512 ? 36 : 18; }
 constexpr int kMaxShares = 256;          // the plan asks for no more
 constexpr int kItems = 8;                // items of a CTA that are known at once
 
