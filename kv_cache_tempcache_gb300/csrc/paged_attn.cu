@@ -34,18 +34,20 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnArgs a) 
   // Where its partials lie is found while the attention still runs: at and cu come from before that, which has
   // waited for them before it let this launch go.
   const int64_t per = (int64_t)a.max_q * a.Hq;
-  if (u >= per * a.B) return;
-  const int b = (int)(u / per);
+  const bool in = u < per * a.B;
+  const int b = in ? (int)(u / per) : 0;
   const paged::Seq s = paged::sequence(a.cu, a.at, a.B, a.T, a.cap, b, nullptr);
-  const int i = (int)((u - b * per) / a.Hq), head = (int)(u - b * per - (int64_t)i * a.Hq);
-  if (i >= s.nq) return;
+  const int i = in ? (int)((u - b * per) / a.Hq) : 0, head = in ? (int)(u - b * per - (int64_t)i * a.Hq) : 0;
   paged::Work work;
-  if (!paged::find_work<kTile>(a, -1, b, work) || work.count == 1) return;
+  const bool joins = in && i < s.nq && paged::find_work<kTile>(a, -1, b, work) && work.count > 1;
+  // The partials.  Rows without any wait too: a join that ended before the attention would let go what comes next in
+  // the stream.
+  pdl_wait();
+  if (!joins) return;
   const int splits = work.count;
   const int h = head / a.group;
   const int64_t row0 = paged::partial_row(a, work.first, h, i * a.group + head - h * a.group);
   const int64_t step = (int64_t)a.Hkv * a.group * a.max_q;               // from split to split
-  pdl_wait();                            // the partials
   constexpr int kPer = kMaxSplits / 32;
   float m = neg_inf(), l = 0.f, o[CPL];
 #pragma unroll

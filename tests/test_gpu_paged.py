@@ -565,3 +565,43 @@ def test_two_calls_on_two_streams():
     torch.cuda.synchronize()
     for o, want in zip(outs, alone):
         assert torch.equal(o[0], want[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq,G", [(1, 1), (3, 4), (70, 2)])
+def test_what_follows_finds_the_outputs_of_calls_with_nothing_to_join(dtype, nq, G):
+    """Short sequences with long tables: the keys could be split and are not, so that the join has nothing to do; the
+    next call reads the outputs."""
+    dt, d, page, Hk, B, width, m = DT[dtype], 128, 32, 2, 3, 200, 300
+    kp, vp = (_rand((B * width, Hk, page, d), s).to(dt) for s in (1, 2))
+    table, at, st = _i32(np.arange(B * width).reshape(B, width)), _i32([m, 0, 11]), _i32([0])
+    q = _rand((G * Hk, B * nq, d), 3).to(dt)
+    rows = _rand((2, Hk, B * nq, d), 4).to(dt)
+    out, moved = torch.empty_like(q), torch.empty_like(q)
+    nb = L.workspace_bytes(L.OP_PAGED_ATTN, G * Hk, B * nq, width * page, d, Hk, r=nq, P=B)
+    assert nb > 0
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+    far = [torch.empty_like(kp) for _ in range(2)]
+
+    def go():
+        out.fill_(9.0)
+        moved.fill_(8.0)
+        L.fastar_paged_attn(q, kp, vp, table, at, 0.1, out, block=1, dev_status=st, workspace=ws)
+        L.fastar_paged_append(rows[0], rows[1], far[0], far[1], table, at, q=out, q_out=moved, dev_status=st)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        go()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        go()
+    for _ in range(20):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(moved, out) and not bool((out == 9.0).any())
+    lse = torch.empty(G * Hk, B * nq, device=DEV)
+    L.fastar_paged_attn(q, kp, vp, table, at, 0.1, out, lse, block=1, dev_status=st, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(moved, out) and st.item() == 0
+    check_attn(dtype, q, kp, vp, table.cpu().numpy(), at.cpu().numpy(), None, 0.1, 1, 0, 0, out, lse)

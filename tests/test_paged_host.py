@@ -169,3 +169,13 @@ def test_kernels_that_wait_for_the_one_before_make_no_promise_that_nothing_write
             assert "pdl_wait()" in body and "__restrict__" not in head, (path, head)
             waiting += 1
     assert waiting == 6                                       # append, three attentions, two joins
+
+
+def test_no_block_leaves_before_it_has_waited_for_the_kernel_before():
+    # where all blocks do, the launch is over before the one that it follows, and what comes next reads its outputs
+    from kv_cache_tempcache_gb300 import build_lib
+    for path in glob.glob(os.path.join(build_lib.CSRC, "*.cu")):
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        for kernel in text.split("__global__")[1:]:
+            first = kernel.find("pdl_wait()")
+            assert first < 0 or not re.search(r"\breturn\b", kernel[:first]), (path, kernel[:200])
