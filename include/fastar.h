@@ -652,7 +652,7 @@ int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d
  * strides below 2^38.
  * Row r of sequence b of B is slot r % page of page table[b * max_pages + r / page] (int32 on the
  * device); a sequence has max_pages * page rows at most (at most 2^30, FASTAR_ECAPACITY).  The T
- * tokens of a call (at most 2^30) lie behind one another, sequence b's are cu[b] .. cu[b + 1]
+ * tokens of a call (fewer than 2^30) lie behind one another, sequence b's are cu[b] .. cu[b + 1]
  * (int32 [B + 1] on the device, not falling; NULL: T / B tokens each, T a multiple of B); at[b]
  * (int32 [B] on the device) rows come before them: token i of a sequence is its row at + i.  Tokens
  * past cu[B] belong to no sequence: nothing of theirs is read for others or written.

@@ -62,7 +62,7 @@ int check_pools(const void* k, const void* v, int dtype, int d, int H, int64_t p
 }
 int check_paged(int B, int64_t T, const int32_t* cu, int page, int64_t max_pages) {
   if (B < 1 || T < 0 || max_pages < 1 || page < 1) return FASTAR_EINVAL;
-  if (B > 65535 || T > fastar::kPagedMax || max_pages > fastar::kPagedMax / page) return FASTAR_ECAPACITY;
+  if (B > 65535 || T >= fastar::kPagedMax || max_pages > fastar::kPagedMax / page) return FASTAR_ECAPACITY;
   if (!cu && T % B) return FASTAR_EINVAL;
   return FASTAR_OK;
 }
@@ -155,7 +155,7 @@ size_t fastar_workspace_bytes(int op, int H, int64_t n, int64_t M, int d, int B,
       return fastar::kv4_attn_workspace(d, H, B, n, M);
     case FASTAR_OP_PAGED_ATTN:
       if ((d != 64 && d != 128) || B < 1 || H < 1 || H % B || M < 1 || n < 1 || r < 1 || P < 1) return 0;
-      if (n > fastar::kPagedMax || H * n > INT32_MAX || r > n || P > 65535) return 0;   // the call refuses them
+      if (n >= fastar::kPagedMax || H * n > INT32_MAX || r > n || P > 65535) return 0;   // the call refuses them
       return fastar::paged_attn_workspace(d, H, B, (int)P, r, M < fastar::kPagedMax ? M : fastar::kPagedMax);
     default: return 0;
   }

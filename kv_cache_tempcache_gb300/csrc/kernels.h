@@ -238,7 +238,7 @@ cudaError_t launch_kv4_attn_tc(int d, const Kv4AttnArgs& a, cudaStream_t s);
 cudaError_t launch_kv4_attn_few(int dtype, int d, const Kv4AttnArgs& a, cudaStream_t s);
 
 // ---- the paged cache ----------------------------------------------------------------------
-constexpr int64_t kPagedMax = (int64_t)1 << 30;    // rows of a table, tokens of a call
+constexpr int64_t kPagedMax = (int64_t)1 << 30;    // rows of a table at most; tokens of a call are fewer
 
 // Pools of pages: element (page, h, slot, c) at p + page * ps + h * hs + slot * rs + c.
 struct PagedPools {

@@ -38,7 +38,7 @@ __device__ __forceinline__ Seq sequence(const int32_t* cu, const int32_t* at, in
   return s;
 }
 
-// The rows that token i sees: [lo, hi) and [0, sk).  T and cap are at most 2^30, block at most T.
+// The rows that token i sees: [lo, hi) and [0, sk).  T is below 2^30, cap 2^30 at most, block T at most.
 struct Sees {
   int lo, hi, sk;
 };

@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs
   if (s.nq > a.max_q && threadIdx.x == 0) flag_status(a.status, FASTAR_DEV_BAD_LEN);
   const int G = a.group, rows = G * min(s.nq, a.max_q);
   if (r0 >= rows) return;
-  const int rl = min(r0 + kRows, rows) - 1;
+  const int rl = r0 + min(kRows, rows - r0) - 1;
   paged::Tiles<kKeys> tiles;
   tiles.set(a, s, r0 / G, rl / G);
   const paged::Split part = paged::part_of(tiles.n, work);
@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs
   float2 o[2][D / 32];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int r = min(r0 + 2 * ty + i, rl);
-    has[i] = r0 + 2 * ty + i <= rl;
+    const int r = r0 + min(2 * ty + i, rl - r0);
+    has[i] = 2 * ty + i <= rl - r0;
     see[i] = paged::sees(a, s, r / G);
     tok[i] = s.t0 + r / G;
     head[i] = h * G + r % G;
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs
   };
   look(part.j0);
   for (int x = threadIdx.x; x < kRows * (D / 4); x += 256) {
-    const int row = x / (D / 4), c = x % (D / 4) * 4, r = min(r0 + row, rl);
+    const int row = x / (D / 4), c = x % (D / 4) * 4, r = r0 + min(row, rl - r0);
     tc::cp_async16(tc::smem_u32(sq + row * Lay::ld + c),
                    static_cast<const float*>(a.q.p) + (int64_t)(h * G + r % G) * a.q.hs + (int64_t)(s.t0 + r / G) * a.q.ts + c,
                    16);
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs
   __syncthreads();
   bring(part.j0);                                        // with the query rows
   look(part.j0 + 1);
-  const float sl2 = a.scale * 1.4426950408889634f;
+  const float sl2 = fminf(a.scale * 1.4426950408889634f, 3.0e38f);
   for (int j = part.j0; j < part.j1; ++j) {
     const int key0 = tiles.key(j);
     __syncthreads();                                     // tile j - 1 has been used, and where j + 1's rows lie is known

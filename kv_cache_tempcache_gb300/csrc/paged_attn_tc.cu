@@ -492,7 +492,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       for (int x = 0; ok; ++x) {
         Item it;
         paged::next_item(a, share, it, kPer);
-        if (!(ok = wait_warp(&sm.item_free[x % paged::kItems], ((x / paged::kItems) & 1) ^ 1, abort))) break;
+        if (!(ok = wait_warp(&sm.item_free[x % paged::kItems], ((x / paged::kItems) & 1) ^ 1, abort))) {
+          if (x == 0) cut_known(it);
+          break;
+        }
         if (lane == 0) {
           sm.item[x % paged::kItems] = it;
           tc::mbar_arrive(&sm.item_full[x % paged::kItems]);
@@ -733,14 +736,18 @@ __global__ void __launch_bounds__(256) paged_tc_join_kernel(const PagedAttnArgs 
   const int c = x % (D / 32) * 32, i = x / (D / 32) * 32 + lane;
   const uint32_t r0 = cut.r0, rows = cut.rows;
   const int t0 = cut.t0, h = cut.h;
-  if (n == 0 || r0 + (uint32_t)(i - lane) >= rows) return;
+  // (what another call wrote over the entries, against the rules, leads to wrong outputs, but to no address outside
+  // the call's)
+  if (n <= 0 || n > a.shares || (uint32_t)h >= (uint32_t)a.Hkv || t0 < 0 || r0 + (uint32_t)(i - lane) >= rows ||
+      (int64_t)t0 + (rows - 1) / (uint32_t)a.group >= a.T)
+    return;
   const bool has = r0 + (uint32_t)i < rows;
   float m = neg_inf(), l = 0.f, o[32];
 #pragma unroll
   for (int e = 0; e < 32; ++e) o[e] = 0.f;
 #pragma unroll 1
   for (int s = n - 1; s >= 0; --s) {                        // the parts are listed from the last on
-    const int64_t slot = cut.slots[s];
+    const int64_t slot = min((uint32_t)cut.slots[s], 2 * (uint32_t)a.shares - 1);
     const float4* p = reinterpret_cast<const float4*>(a.part_o) + (slot * (D / 4) + c / 4) * per + i;
     float2 ml = make_float2(neg_inf(), 0.f);
     float4 v[8];

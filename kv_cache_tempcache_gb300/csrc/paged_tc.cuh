@@ -60,7 +60,7 @@ __device__ __forceinline__ int item_units(const PagedAttnArgs& a, const Seq& s, 
   nt = 0;
   if (r0 >= rows) return 0;
   nt = rows - r0 > per / 2 ? 2 : 1;
-  tiles.set(a, s, r0 / a.group, (min(r0 + per, rows) - 1) / a.group);
+  tiles.set(a, s, r0 / a.group, (r0 + min(per, rows - r0) - 1) / a.group);
   return fixed_units(per) + tiles.n * (nt == 2 ? kFull : half_units(per));
 }
 

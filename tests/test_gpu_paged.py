@@ -605,3 +605,14 @@ def test_what_follows_finds_the_outputs_of_calls_with_nothing_to_join(dtype, nq,
     torch.cuda.synchronize()
     assert torch.equal(moved, out) and st.item() == 0
     check_attn(dtype, q, kp, vp, table.cpu().numpy(), at.cpu().numpy(), None, 0.1, 1, 0, 0, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("scale", [3e38, 1e-44])
+def test_the_largest_and_smallest_scales(dtype, nq, scale):
+    """Queries of zeros: every key has the same weight, whatever the scale."""
+    q, kp, vp, table, at, cu = attn_case(dtype, [nq, nq], [90, 5], 2, 2, 64, 16, "hnd", 1, 0, 0)
+    q.zero_()
+    out, lse = run_attn(q, kp, vp, table, at, cu, scale * (1 - 2.0 ** -20), 1, 0, 0)
+    check_attn(dtype, q, kp, vp, table, at, cu, 1.0, 1, 0, 0, out, lse)

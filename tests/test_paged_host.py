@@ -179,3 +179,10 @@ def test_no_block_leaves_before_it_has_waited_for_the_kernel_before():
         for kernel in text.split("__global__")[1:]:
             first = kernel.find("pdl_wait()")
             assert first < 0 or not re.search(r"\breturn\b", kernel[:first]), (path, kernel[:200])
+
+
+def test_most_tokens_of_a_call(lib):
+    assert append(lib, T=2 ** 30) == attn(lib, T=2 ** 30, Hq=1, Hkv=1) == L.ECAPACITY
+    assert attn(lib, T=2 ** 30 - 2, Hq=4) == L.ECAPACITY       # rows of all heads
+    assert L.workspace_bytes(L.OP_PAGED_ATTN, 1, 2 ** 30, 100, 64, 1, r=1, P=1) == 0
+    assert L.workspace_bytes(L.OP_PAGED_ATTN, 1, 2 ** 30 - 1, 100000, 64, 1, r=2 ** 30 - 1, P=1) > 0
