@@ -6,9 +6,10 @@
 // sees come as zeros; where only some rows see a key the others leave it out (not by a weight of 0: its value may
 // be infinite).
 // Bound: with few rows latency (a block has one or two tiles), with many the shared memory's 128 bytes a clock, of
-// which every warp takes all of a tile.  Measured: up to 20 rows over 2006 rows of three sequences, d = 64, 16.7 us with the
-// join (20.2 with tiles loaded and used in turn, one product an instruction); one row over 100,000 rows of 4 heads 148 us (1.4
-// TB/s).
+// which every warp with rows takes all of a tile; weights are read four at a time, and warps without rows only bring tiles
+// (one weight at a time in all warps: 18.2 us instead of 16.7 for the first call below, 169 instead of 130 with 100,000
+// rows each).  Measured: up to 20 rows over 2006 rows of three sequences, d = 64, 16.3 us with the join in replayed graphs;
+// one row over 100,000 rows of 4 heads 90 us (2.3 TB/s).
 #include <climits>
 
 #include "common.cuh"
@@ -122,6 +123,7 @@ __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs
   bring(part.j0);                                        // with the query rows
   look(part.j0 + 1);
   const float sl2 = fminf(a.scale * 1.4426950408889634f, 3.0e38f);
+  const bool idle = (int)(threadIdx.x >> 5) * 4 > rl - r0;         // a warp without rows only brings tiles
   for (int j = part.j0; j < part.j1; ++j) {
     const int key0 = tiles.key(j);
     __syncthreads();                                     // tile j - 1 has been used, and where j + 1's rows lie is known
@@ -129,6 +131,7 @@ __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs
     tc::cp_async_wait<1>();
     __syncthreads();
     look(j + 2);
+    if (idle) continue;
     const float *sk = sm + Lay::kv + (j & 1) * Lay::stage, *sv = sk + kKeys * Lay::ld;
     float2 x2[2][4];
 #pragma unroll
@@ -177,15 +180,22 @@ __global__ void __launch_bounds__(256) paged_attn_f32_kernel(const PagedAttnArgs
     }
     __syncwarp();
     const bool whole = tiles.all(key0);
-#pragma unroll 4
-    for (int k = 0; k < kKeys; ++k) {
-      const float p0 = sp[2 * ty * Lay::ldp + k], p1 = sp[(2 * ty + 1) * Lay::ldp + k];
-      const bool in0 = whole || (bits[0] >> k & 1), in1 = whole || (bits[1] >> k & 1);
+#pragma unroll 2
+    for (int k0 = 0; k0 < kKeys; k0 += 4) {
+      const float4 p4[2] = {*reinterpret_cast<const float4*>(&sp[2 * ty * Lay::ldp + k0]),
+                            *reinterpret_cast<const float4*>(&sp[(2 * ty + 1) * Lay::ldp + k0])};
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const float4 v = *reinterpret_cast<const float4*>(&sv[k * Lay::ld + tx * 4 + c * 64]);
-        if (in0) fma2(o[0][2 * c], p0, p0, v.x, v.y), fma2(o[0][2 * c + 1], p0, p0, v.z, v.w);
-        if (in1) fma2(o[1][2 * c], p1, p1, v.x, v.y), fma2(o[1][2 * c + 1], p1, p1, v.z, v.w);
+      for (int e = 0; e < 4; ++e) {
+        const int k = k0 + e;
+        const float p0 = e == 0 ? p4[0].x : e == 1 ? p4[0].y : e == 2 ? p4[0].z : p4[0].w;
+        const float p1 = e == 0 ? p4[1].x : e == 1 ? p4[1].y : e == 2 ? p4[1].z : p4[1].w;
+        const bool in0 = whole || (bits[0] >> k & 1), in1 = whole || (bits[1] >> k & 1);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const float4 v = *reinterpret_cast<const float4*>(&sv[k * Lay::ld + tx * 4 + c * 64]);
+          if (in0) fma2(o[0][2 * c], p0, p0, v.x, v.y), fma2(o[0][2 * c + 1], p0, p0, v.z, v.w);
+          if (in1) fma2(o[1][2 * c], p1, p1, v.x, v.y), fma2(o[1][2 * c + 1], p1, p1, v.z, v.w);
+        }
       }
     }
     __syncwarp();
