@@ -263,6 +263,7 @@ struct PagedAppendArgs {
   const int32_t* at;                  // [B]
   int32_t *len_out, *status;
   int part_shift;                     // log2 of the warps per token (by the launcher)
+  int per;                            // tokens (or parts) of a warp, 0: all that come round (by the launcher)
 };
 cudaError_t launch_paged_append(int dtype, int d, PagedAppendArgs a, const int* axes, float theta, cudaStream_t s);
 

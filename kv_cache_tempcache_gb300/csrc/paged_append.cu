@@ -5,10 +5,14 @@
 // tokens a part of one's heads: D / 16 lanes hold a head's row, 16 channels each; the rows of q, then
 // k's, which go to their page, then v's, which are only moved there.  A lane's channels are chunks of 16 bytes, a
 // row's lanes side by side in each (with 32 consecutive bytes a lane every load took two half sectors).  Rows come through shared memory by
-// cp.async, kSlots groups of them on their way a warp, across the borders of tokens: held in registers (three
-// groups a warp, and none on their way between two tokens) 4680 tokens of 36 heads took 16.4 us and 14,400 of
-// 72 heads 96; now 15.7 (5.5 TB/s) and 92.8 (5.7 TB/s), in replayed graphs; more slots or blocks change nothing.
-// Each lane reads back what it asked for itself, so no barrier is needed.
+// cp.async, kSlots groups of them on their way a warp, across the borders of tokens (held in registers, three
+// groups a warp and none on their way between two tokens, 4680 tokens of 36 heads took 0.7 us longer); more slots or
+// blocks change nothing.  Each lane reads back what it asked for itself, so no barrier is needed.
+// Many tokens go to blocks that end, of a few neighbouring tokens each: the multiprocessors do not read and write equally
+// fast, and blocks that stay and take an equal share of the tokens wait for the slowest (14,400 tokens of 72 heads 93.5
+// us; now 81.1).  Measured, each call on inputs that are not in L2: 4680 tokens of 36 heads 17.5 us (4.9 TB/s; 15.7 where the
+// inputs are there), 14,400 of 72 heads 81.1 (6.5 TB/s, 0.96 of the measured copy rate); 100,000 tokens of 6 heads 121 (2.5
+// TB/s: the tokens' rotations).
 #include <climits>
 
 #include "common.cuh"
@@ -23,6 +27,7 @@ namespace fastar {
 namespace {
 
 constexpr int kWarpsA = 4, kSlots = 4, kBlocks = 5;   // warps of a block, groups of rows on their way, blocks an SM
+constexpr int kGroups = 8;               // of rows that a warp of a block that ends has at least
 
 // 16 bytes of a row.
 __device__ __forceinline__ void store16(__nv_bfloat16* p, const float* f) { store8(p, f); }
@@ -75,15 +80,16 @@ __global__ void __launch_bounds__(kWarpsA * 32)
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, li = lane % LPR;
   const uint32_t parts = 1u << a.part_shift;
-  const int64_t items = a.T << a.part_shift;
-  const int64_t stride = (int64_t)gridDim.x * kWarpsA;
+  // a block's items: `per` of each warp side by side, or (0) every grid's width of warps
+  const int64_t u0 = (int64_t)blockIdx.x * (kWarpsA * max(a.per, 1)) + (threadIdx.x >> 5), all = a.T << a.part_shift;
+  const int64_t stride = a.per ? kWarpsA : (int64_t)gridDim.x * kWarpsA;
+  const int64_t items = a.per ? min(all, (int64_t)(blockIdx.x + 1) * (kWarpsA * a.per)) : all;
   // groups of rows side by side: of q, then of k, then of v
   const int gq = a.qo ? (a.Hq + RW - 1) / RW : 0, gk = (a.Hk + RW - 1) / RW, groups = gq + 2 * gk;
   // group lx of item lu is the next to be asked for, into slot `to`; 32 sizeof(T) / 2 bytes a lane
   constexpr int NC = sizeof(T), EPC = 16 / NC;   // 16-byte chunks of a lane, channels of a chunk
   extern __shared__ __align__(16) uint8_t ring[];
   uint8_t* mine = ring + (threadIdx.x >> 5) * (kSlots * NC * 512) + lane * 16;
-  const int64_t u0 = (int64_t)blockIdx.x * kWarpsA + (threadIdx.x >> 5);
   int64_t lu = u0;
   int lx = (int)((uint32_t)u0 & (parts - 1)), to = 0, from = 0;
   auto skip = [&]() {                      // (parts beyond the groups have none)
@@ -216,13 +222,25 @@ cudaError_t append_go(PagedAppendArgs a, const RopeTable& tab, bool all, cudaStr
   while ((1 << a.part_shift) < groups && (a.T << a.part_shift) < 16 * sms) ++a.part_shift;
   int64_t blocks = ((a.T << a.part_shift) + kWarpsA - 1) / kWarpsA;
   if (blocks < 1) blocks = 1;                // lengths alone
-  // resident blocks, which go on to their next tokens: of 3 to kBlocks a multiprocessor the number that leaves
-  // their last round fullest (4680 tokens are 1.54 rounds of 5 blocks each and 1.92 of 4: 15.8 and 15.4 us)
   constexpr int bytes = kWarpsA * kSlots * 512 * (int)sizeof(T);
-  int64_t most = kBlocks * sms, best = 0;
-  for (int n = kBlocks; n >= 3; --n) {
-    const int64_t rounds = (blocks + n * sms - 1) / (n * sms), fill = (blocks << 10) / (rounds * n * sms);
-    if (fill > best) best = fill, most = n * sms;
+  int64_t most = INT_MAX;
+  a.per = 0;
+  if (blocks >= kBlocks * sms * 9 / 4) {
+    // blocks that end, from two and a quarter times as many as are resident (9360 tokens of 36 heads, 3.1 times: 32.4 us
+    // instead of 31.8, in fp32 55.3 instead of 59.9; 7200 of 72, 2.4 times: 44.0 instead of 44.4; 3600 of 72, 1.2 times: 27.3
+    // instead of 23.6); where tokens have few rows a warp takes several, so that a block's start weighs less (100,000 tokens
+    // of 6 rows: 147 us with a token each, 122 with kGroups 8, 116 with 32, but then 30,000 of 12 take 57 instead of 49)
+    const int here = (groups + (1 << a.part_shift) - 1) >> a.part_shift;
+    a.per = here < kGroups ? (kGroups + here - 1) / here : 1;
+    blocks = (blocks + a.per - 1) / a.per;
+  } else {
+    // resident blocks, which go on to their next tokens: of 3 to kBlocks a multiprocessor the number that leaves
+    // their last round fullest (4680 tokens are 1.54 rounds of 5 blocks each and 1.92 of 4: 18.2 and 17.6 us)
+    int64_t best = 0;
+    for (int n = kBlocks; n >= 3; --n) {
+      const int64_t rounds = (blocks + n * sms - 1) / (n * sms), fill = (blocks << 10) / (rounds * n * sms);
+      if (fill > best) best = fill, most = n * sms;
+    }
   }
   const unsigned grid = (unsigned)(blocks < most ? blocks : most);
   const auto kernel = all ? paged_append_kernel<T, D, true> : paged_append_kernel<T, D, false>;

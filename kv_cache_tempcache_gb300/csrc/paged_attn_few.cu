@@ -15,7 +15,7 @@
 // Rows of V that no token sees become zeros in shared memory; pages that no token sees, or that are not there,
 // come as zeros.
 // Measured: one token each of 32 sequences, 32 heads of 8, 8191 + 100 rows 143 us (6.7 TB/s, 0.99 of the measured copy rate); up
-// to 28 rows over six sequences of up to 40,000 rows 89 us (5.4 TB/s); one token over 333 rows 6.7 us, a block's start, five
+// to 28 rows over six sequences of up to 40,000 rows 89 us (5.1 TB/s); one token over 333 rows 6.7 us, a block's start, five
 // tiles a warp and the join of its warps, one after the other.
 // P is bf16, as V is: 2^-8 of itself at every magnitude.  The reference moves only when a P would pass 2^kTop.
 #include <climits>

@@ -616,3 +616,12 @@ def test_the_largest_and_smallest_scales(dtype, nq, scale):
     q.zero_()
     out, lse = run_attn(q, kp, vp, table, at, cu, scale * (1 - 2.0 ** -20), 1, 0, 0)
     check_attn(dtype, q, kp, vp, table, at, cu, 1.0, 1, 0, 0, out, lse)
+
+
+@pytest.mark.parametrize("dtype,nq,Hq,Hk,d,tail", [("bf16", [7001], 1, 1, 64, 0), ("f32", [6000, 0, 1403, 1], 2, 1, 128, 3),
+                                                   ("bf16", [1, 9999], 0, 3, 128, 1), ("bf16", [3001, 4002], 8, 8, 64, 0)])
+def test_append_of_thousands_of_tokens(dtype, nq, Hq, Hk, d, tail):
+    """More tokens than resident warps take in turn: blocks of a few neighbouring tokens, the last one not full."""
+    axes = (24, 20, 20) if d == 64 else (44, 42, 42)
+    assert run_append(dtype, nq, [5 * i for i in range(len(nq))], Hq, Hk, d, 64, "nhd", True, axes, (30, 52), False,
+                      tail=tail) == 0
