@@ -146,8 +146,9 @@ __device__ __forceinline__ bool find_work(const PagedAttnArgs& a, int v, int b, 
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const int64_t even = (total + a.extra - 1) / a.extra;
-  const int chunk = even > a.min_tiles ? (int)even : a.min_tiles;
+  // (more than the tiles of 2^30 rows is as good as those)
+  const int even = (int)min((total + a.extra - 1) / a.extra, (int64_t)1 << 28);
+  const int chunk = max(even, a.min_tiles);
   int base = 0;
   bool here = false;
 #pragma unroll
