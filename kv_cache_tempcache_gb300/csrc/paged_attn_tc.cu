@@ -31,10 +31,13 @@
 // What bounds it: a key tile is 2048 clocks of MMA a CTA at d = 128 (1.0 us at 2.07 GHz); softmax and its hand-overs make it
 // 1.41 us.  Around an item some 8 us: queries to first logits 1.3, last P to complete outputs 1.8, outputs 3.5, which are 16
 // warps' instructions as much as bytes.  A tile of one row tile alone waits for K and V: 1.15 us.
+// Of the 2850 clocks of a key tile a row tile's softmax takes 1450: its largest logit, and that of the other half's warps,
+// 490, exponentials and P 920; then its products are issued, run and reported.  Without the halves' agreement on
+// the reference it would be 4 to 8 % less.
 // Measured, d = 128: 9728 tokens of 4 heads over 37,440 rows 413 to 430 us (1740 to 1800 TFLOP/s, 0.91 to 0.95 of the bf16 rate
 // measured for a library product); 4680 tokens of 12 heads over the same 690 us in a short run, 781 in a long one, under
-// the power limit; the first 4680 tokens in three frames 91 us; 16,384 causal tokens of 16 heads of 4 with a window of 4096 342 to
-// 354 us.  Seven ragged causal sequences of up to 777 tokens, d = 64: 44 us.
+// the power limit; the first 4680 tokens in three frames 90 us; 16,384 causal tokens of 16 heads of 4 with a window of 4096 337 to
+// 350 us.  Seven ragged causal sequences of up to 777 tokens, d = 64: 43 us.
 //
 // Numbers: logits, maxima, sums and outputs are fp32.  P is bf16, as V is (a product has one type):
 // 2^-8 of itself, at every magnitude, since bf16 has fp32's exponents.
@@ -130,14 +133,12 @@ __device__ __forceinline__ RowOf row_of(const PagedAttnArgs& a, const Item& it, 
 // Byte offset of 16-byte chunk c (0..3) of row `row` among rows of 64 bytes, so that 8 rows hit 8 bank groups.
 __device__ __forceinline__ uint32_t out_off(int row, int c) { return (uint32_t)(row * 64 + ((c ^ (row >> 1 & 3)) << 4)); }
 
-// A warp's 32 staged rows to where each goes (off bytes from out; -1: nowhere).
-__device__ __forceinline__ void store_rows(uint8_t* out, int64_t off, const uint8_t* stg, int lane) {
+// A warp's 32 staged rows to where each goes: rows i * 8 + lane / 4 to to[i] bytes from out (-1: nowhere).
+__device__ __forceinline__ void store_rows(uint8_t* out, const int64_t* to, const uint8_t* stg, int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int sr = i * 8 + (lane >> 2), ch = lane & 3;
-    const int64_t to = __shfl_sync(0xffffffffu, off, sr);
-    const uint4 v = *reinterpret_cast<const uint4*>(stg + out_off(sr, ch));
-    if (to >= 0) *reinterpret_cast<uint4*>(out + to + ch * 16) = v;
+    const uint4 v = *reinterpret_cast<const uint4*>(stg + out_off(i * 8 + (lane >> 2), lane & 3));
+    if (to[i] >= 0) *reinterpret_cast<uint4*>(out + to[i] + (lane & 3) * 16) = v;
   }
 }
 
@@ -383,7 +384,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       const uint8_t* odd = base + Lay::out + (warp + 8) * 2048;        // (both) the odd tiles' 16 channels
       const int64_t tok = it.s.t0 + at.t;
       const int64_t off = has ? (at.head * a.o_hs + tok * a.o_ts + half * HD) * 2 : -1;
-#pragma unroll 1
+      int64_t to[4];                        // of the rows that this lane stores a part of
+#pragma unroll
+      for (int i = 0; i < 4; ++i) to[i] = __shfl_sync(0xffffffffu, off, i * 8 + (lane >> 2));
+#pragma unroll                              // (as a loop the whole kernel was 1 % slower: its registers were dealt out differently)
       for (int c = 0; c < HD; c += 32) {
         float o[32];
         if (count > 0) {
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             *reinterpret_cast<uint4*>(stg + out_off(lane, e)) = make_uint4(v[0], v[1], v[2], v[3]);
           }
           __syncwarp();
-          store_rows(static_cast<uint8_t*>(a.out) + c * 2, off, stg, lane);
+          store_rows(static_cast<uint8_t*>(a.out) + c * 2, to, stg, lane);
         }
       }
       tc::tc_fence_before();                // O has been read: the next item's products, which this warp's P let go
@@ -779,7 +783,11 @@ __global__ void __launch_bounds__(256) paged_tc_join_kernel(const PagedAttnArgs 
     *reinterpret_cast<uint4*>(stg + out_off(lane, e)) = make_uint4(y[0], y[1], y[2], y[3]);
   }
   __syncwarp();
-  store_rows(static_cast<uint8_t*>(a.out) + c * 2, has ? (head * a.o_hs + tok * a.o_ts) * 2 : -1, stg, lane);
+  const int64_t off = has ? (head * a.o_hs + tok * a.o_ts) * 2 : -1;
+  int64_t to[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, off, k * 8 + (lane >> 2));
+  store_rows(static_cast<uint8_t*>(a.out) + c * 2, to, stg, lane);
   if (has && c == 0 && a.lse) a.lse[head * a.T + tok] = live ? m + logf(l) : neg_inf();
 }
 
