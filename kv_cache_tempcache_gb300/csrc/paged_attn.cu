@@ -113,10 +113,12 @@ struct Plan {
 };
 
 // Slots for few rows: `blocks` blocks in all, each of min_tiles key tiles of `tile` rows or more; none beyond one a
-// sequence where they fill the GPU, or where no sequence has three times that many.
+// sequence where they fill the GPU, or where no sequence has three times that many.  With fewer to spare than there are
+// sequences, equal ones stay whole and the join is for nothing (3.5 of 30 us: 32 sequences of 1100 rows), so that only twice as
+// long ones, whose lengths may differ by more, are worth it.
 Plan plan_slots(Kernel kernel, int64_t units, int64_t B, int64_t keys, int64_t blocks, int tile, int min_tiles) {
   int64_t e = blocks / units - B;
-  if (B > paged::kDealt || keys < 3 * (int64_t)tile * min_tiles || e < 0) e = 0;
+  if (B > paged::kDealt || keys < (e < B ? 6 : 3) * (int64_t)tile * min_tiles || e < 0) e = 0;
   if (e > kMaxSplits - 1) e = kMaxSplits - 1;
   return Plan{kernel, (int)e, min_tiles, 0};
 }
@@ -139,9 +141,11 @@ Plan make_plan(int dtype, int d, int Hq, int Hkv, int B, int max_q, int64_t keys
     const int64_t units = (rows + kF32Rows - 1) / kF32Rows * Hkv;
     return plan_slots(kF32, units, B, keys, 2 * sm_count(), kF32Keys, 1);
   }
-  // two blocks a multiprocessor, all resident; eight tiles of 16 keys a warp (a few tokens of six long sequences take
-  // 89 us with two blocks, 110 with three, 102 with four, 123 with eight)
-  if (rows <= kFewRows) return plan_slots(kFew, Hkv, B, keys, 2 * sm_count(), 16, 8 * kFewWarps);
+  // two blocks a multiprocessor, all resident (a few tokens of six long sequences take 89 us with two blocks, 110 with
+  // three, 102 with four, 123 with eight); eight tiles of 16 keys a warp, or with more than one group of eight rows, where
+  // a tile takes a warp 1 us instead of 0.4, four (28 rows over six sequences of 900 rows: 20.5 us with eight, 17.8 with
+  // four; one token of 12 heads over 6000 rows: 11.8 and 12.4)
+  if (rows <= kFewRows) return plan_slots(kFew, Hkv, B, keys, 2 * sm_count(), 16, (rows <= 8 ? 8 : 4) * kFewWarps);
   // one CTA, or pair of them, a multiprocessor or two
   const bool alone = d == 128 && rows <= 128;
   const int shares = d == 128 && !alone ? sm_count() / 2 : sm_count();

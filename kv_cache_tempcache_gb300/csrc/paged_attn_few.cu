@@ -164,22 +164,57 @@ __global__ void __launch_bounds__(W * 32)
 #pragma unroll 1
   for (int i = 0; i < Lay::stages - 1; ++i) ask();
   __syncthreads();                                       // poison is set up
-  // query rows: lane (g, t) holds channels 2t, 2t + 1 and 8 + 2t, 9 + 2t of each 16 of row 8 n + g
+  // query rows: lane (g, t) holds channels 2t, 2t + 1 and 8 + 2t, 9 + 2t of each 16 of row 8 n + g.  One group's come as they
+  // are held, four bytes of eight rows at a time (one token over 333 rows 6.7 us, through a stage 7.0); more groups' by
+  // whole rows, through the stage that is not asked for yet (28 rows over six sequences of 1800 25.6 us, as they are held 27.0:
+  // each load looks up eight lines)
   uint32_t qb[NR][D / 16][2];
   int tok[NR][2];                                        // tokens of the rows 8 n + 2t, 8 n + 2t + 1
-#pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    const int r = 8 * n + g;
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(
-        static_cast<const __nv_bfloat16*>(a.q.p) + (int64_t)(h * G + r % G) * a.q.hs + (int64_t)(s.t0 + r / G) * a.q.ts);
+  const uint32_t inv = 65536u / (uint32_t)G + 1;         // r / G of r < 32, G <= 32
+  auto token = [&](int r) { return (int)((uint32_t)r * inv >> 16); };
+  if (NR == 1) {
+    const int tk = token(g);
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q.p) +
+                                                            (int64_t)(h * G + g - tk * G) * a.q.hs + (int64_t)(s.t0 + tk) * a.q.ts);
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
-      qb[n][c][0] = r < rows ? src[c * 8 + t] : 0u;
-      qb[n][c][1] = r < rows ? src[c * 8 + 4 + t] : 0u;
+      qb[0][c][0] = g < rows ? src[c * 8 + t] : 0u;
+      qb[0][c][1] = g < rows ? src[c * 8 + 4 + t] : 0u;
+    }
+  } else {
+    static_assert(8 * NR * D * 2 <= Lay::stage, "rows that fit a stage");
+    constexpr int CH = D / 8, QL = NR * D / 32;          // chunks of a row, of a lane
+    uint8_t* qs = ring + (Lay::stages - 1) * Lay::stage;
+    uint4 u[QL];
+#pragma unroll
+    for (int k = 0; k < QL; ++k) {
+      const int r = (lane + 32 * k) / CH, tk = token(r);
+      u[k] = make_uint4(0, 0, 0, 0);
+      if (r < rows)
+        u[k] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q.p) + (int64_t)(h * G + r - tk * G) * a.q.hs +
+                                               (int64_t)(s.t0 + tk) * a.q.ts + lane % CH * 8);
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) tok[n][e] = min(8 * n + 2 * t + e, rows - 1) / G;
+    for (int k = 0; k < QL; ++k) {
+      const int r = (lane + 32 * k) / CH;
+      *reinterpret_cast<uint4*>(qs + r * (2 * D) + ((lane % CH ^ (r & 7)) << 4)) = u[k];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          qb[n][c][e] = *reinterpret_cast<const uint32_t*>(qs + (8 * n + g) * (2 * D) + (((2 * c + e) ^ g) << 4) + t * 4);
+    }
+    tc::fence_proxy_async();                             // the stage is written by TMA next
+    __syncwarp();
   }
+#pragma unroll
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) tok[n][e] = token(min(8 * n + 2 * t + e, rows - 1));
   float sl2 = a.scale * 1.4426950408889634f;
   sl2 = fminf(fmaxf(sl2, 1.2e-38f), 3.0e38f);
   // minus the references, in log2 units; 0 while a row has seen no key (isset, a bit a row)
@@ -319,37 +354,50 @@ __global__ void __launch_bounds__(W * 32)
       }
     }
   __syncthreads();
-  for (int y = threadIdx.x; y < rows * (D / 4); y += W * 32) {
-    const int r = y / (D / 4), c = y % (D / 4) * 4;
-    float top = neg_inf(), sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+  // a row's weights of the warps (-1: a warp that saw none of its keys) and one over its sum (-1: no key), a thread a row, in
+  // place
+  if ((int)threadIdx.x < rows) {
+    float2* ml = sml + threadIdx.x;
+    float top = neg_inf(), sum = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w)
-      if (sml[w * 8 * NR + r].y != 0.f) top = fmaxf(top, sml[w * 8 * NR + r].x);
+      if (ml[w * 8 * NR].y != 0.f) top = fmaxf(top, ml[w * 8 * NR].x);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float2 ml = sml[w * 8 * NR + r];
-      if (ml.y == 0.f) continue;
-      const float f = ex2f(ml.x - top);
+      const float2 x = ml[w * 8 * NR];
+      const float f = x.y != 0.f ? ex2f(x.x - top) : -1.f;
+      if (x.y != 0.f) sum = fmaf(f, x.y, sum);
+      ml[w * 8 * NR].x = f;
+    }
+    const int r = (int)threadIdx.x, tk = token(r), head = h * G + r - tk * G;
+    const bool live = sum > 0.f || sum != sum;
+    const float mn = top * 0.6931471805599453f;
+    if (partial) a.part_ml[paged::partial_row(a, slot, h, r)] = make_float2(live ? mn : neg_inf(), sum);
+    if (!partial && a.lse) a.lse[head * a.T + s.t0 + tk] = live ? mn + logf(sum) : neg_inf();
+    ml[0].y = live ? 1.f / sum : -1.f;
+  }
+  __syncthreads();
+#pragma unroll 2
+  for (int y = threadIdx.x; y < rows * (D / 4); y += W * 32) {
+    const int r = y / (D / 4), c = y % (D / 4) * 4, tk = token(r);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = sml[w * 8 * NR + r].x;
+      if (f < 0.f) continue;
       const float4 q = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + (w * 8 * NR + r) * Lay::ldo + c);
-      sum = fmaf(f, ml.y, sum);
       v[0] = fmaf(f, q.x, v[0]), v[1] = fmaf(f, q.y, v[1]), v[2] = fmaf(f, q.z, v[2]), v[3] = fmaf(f, q.w, v[3]);
     }
     if (__builtin_expect(*(volatile int*)poison, 0))
-      paged::add_taken_out<kKeys, 4>(a, tiles, part, b, h, paged::sees(a, s, r / G), c, v);
-    const bool live = sum > 0.f || sum != sum;
-    const int64_t tk = s.t0 + r / G, head = h * G + r % G, prow = paged::partial_row(a, slot, h, r);
-    const float mn = top * 0.6931471805599453f;
-    if (c == 0) {
-      if (partial) a.part_ml[prow] = make_float2(live ? mn : neg_inf(), sum);
-      if (!partial && a.lse) a.lse[head * a.T + tk] = live ? mn + logf(sum) : neg_inf();
-    }
+      paged::add_taken_out<kKeys, 4>(a, tiles, part, b, h, paged::sees(a, s, tk), c, v);
     if (partial) {
-      *reinterpret_cast<float4*>(a.part_o + prow * D + c) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(a.part_o + paged::partial_row(a, slot, h, r) * D + c) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
-      const float f = live ? 1.f / sum : 0.f;
+      const float f = sml[r].y;
       uint2 w2 = make_uint2(pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f));
-      if (!live) w2 = make_uint2(0u, 0u);
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + head * a.o_hs + tk * a.o_ts + c) = w2;
+      if (f < 0.f) w2 = make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)(h * G + r - tk * G) * a.o_hs +
+                                (int64_t)(s.t0 + tk) * a.o_ts + c) = w2;
     }
   }
 }

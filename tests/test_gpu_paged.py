@@ -625,3 +625,17 @@ def test_append_of_thousands_of_tokens(dtype, nq, Hq, Hk, d, tail):
     axes = (24, 20, 20) if d == 64 else (44, 42, 42)
     assert run_append(dtype, nq, [5 * i for i in range(len(nq))], Hq, Hk, d, 64, "nhd", True, axes, (30, 52), False,
                       tail=tail) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 3, 5, 7, 9, 11, 15, 16, 31, 32])
+def test_few_rows_of_every_kind_of_group(d, G):
+    """As many tokens as 32 rows hold, of heads that share one: every row's own token and head."""
+    most = 32 // G
+    for nq in {1, (most + 1) // 2, most}:
+        c = attn_case("bf16", [nq, max(1, nq - 1)], [700, 3], 2, G, d, 16, "nhd", 1, 50, 3, seed=G)
+        out, lse = run_attn(*c, 1 / math.sqrt(d), 1, 50, 3)
+        check_attn("bf16", *c, 1 / math.sqrt(d), 1, 50, 3, out, lse)
+        c = attn_case("bf16", [nq], [1700], 1, G, d, 64, "hnd", 1, 0, 0, seed=G + 1)
+        out, lse = run_attn(*c, 1 / math.sqrt(d), 1, 0, 0)
+        check_attn("bf16", *c, 1 / math.sqrt(d), 1, 0, 0, out, lse)
