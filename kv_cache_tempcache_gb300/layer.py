@@ -666,7 +666,7 @@ class WindowLayer:
     def load_history(self, k, v):
         """k, v [Hkv, n, d] (as the cache is to hold them): the rollout's rows so far."""
         self.len.zero_()
-        self._n, self._replayed = 0, False
+        self._n = 0                      # (a commit that was captured may still be replayed: _replayed stays)
         for a in range(0, k.shape[1], self.Nq):
             self._append(k[:, a:a + self.Nq], v[:, a:a + self.Nq])
             self.commit(min(self.Nq, k.shape[1] - a))

@@ -233,3 +233,35 @@ def test_a_captured_step_of_the_layer_keeps_its_chunks():
     layer.step_self(*x[:, 2])
     torch.cuda.synchronize()
     assert layer.n == 27 and layer.len.item() == 27 and layer.status() == 0
+
+
+def test_reloading_a_layer_whose_step_was_captured():
+    """A commit that was captured may be replayed after a new history as well: the length is the device's."""
+    H, d, nq = 2, 64, 20
+    x = T._rand((3, 6, H, nq, d), 46).bfloat16()
+    eager, layer = (WindowLayer(H, d, nq, 50, 7, 300, 8, page=16) for _ in range(2))
+    bufs = [t.clone() for t in x[:, 0]]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        layer.step(*bufs, advance=False)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        layer.step(*bufs)
+    g.replay()
+    torch.cuda.synchronize()
+    assert layer.n == nq
+    for hist in (7, 33):
+        for a in (eager, layer):
+            a.load_history(*T._rand((2, H, hist, d), hist).bfloat16())
+            assert a.n == hist
+        for i in range(1, 4):
+            for b, t in zip(bufs, x[:, i]):
+                b.copy_(t)
+            g.replay()
+            want = eager.step_self(*x[:, i])
+            assert layer.n == layer.len.item() == eager.n == hist + i * nq
+            assert torch.equal(layer.o_self, want)
+        layer.step_self(*x[:, 4])                             # and a call outside the graph
+        assert layer.n == layer.len.item() == hist + 4 * nq and layer.status() == 0
