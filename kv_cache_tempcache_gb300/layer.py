@@ -702,14 +702,19 @@ class WindowLayer:
         return o[:, :n]
 
     def step_cross(self, q, out=None):
+        """Attention over the prompt -> out ([H, Nq, d] view; default o_cross), its first q.shape[1] tokens."""
         o = self.o_cross if out is None else out
-        L.fastar_dense_attn(q, self.kp, self.vp, self.P, self.scale, o, self.lse_cross)
-        return o
+        n = q.shape[1]
+        if n > self.Nq or n > o.shape[1]:
+            raise ValueError(f"{n} tokens for a layer of {self.Nq} and outputs of {o.shape[1]}")
+        lse = self.lse_cross if n == self.Nq else torch.empty(self.H, n, dtype=torch.float32, device=q.device)
+        L.fastar_dense_attn(q, self.kp, self.vp, self.P, self.scale, o[:, :n], lse)
+        if lse is not self.lse_cross:
+            self.lse_cross[:, :n] = lse
+        return o[:, :n]
 
     def step(self, q, k_cur, v_cur, advance: bool = True, turn=None):
-        self.step_self(q, k_cur, v_cur, advance=advance, turn=turn)
-        self.step_cross(q)
-        return self.o_self, self.o_cross
+        return self.step_self(q, k_cur, v_cur, advance=advance, turn=turn), self.step_cross(q)
 
     def status(self) -> int:
         return int(self.dev_status.item())

@@ -265,3 +265,37 @@ def test_reloading_a_layer_whose_step_was_captured():
             assert torch.equal(layer.o_self, want)
         layer.step_self(*x[:, 4])                             # and a call outside the graph
         assert layer.n == layer.len.item() == hist + 4 * nq and layer.status() == 0
+
+
+@pytest.mark.parametrize("n", [25, 1])
+def test_a_step_of_a_chunk_shorter_than_the_layers(n):
+    """After a full chunk: the short one's outputs, statistics and nothing of the chunk before."""
+    H, d, nq, P = 2, 64, 40, 8
+    layer, short = WindowLayer(H, d, nq, 60, 10, 500, P), WindowLayer(H, d, n, 60, 10, 500, P)
+    kp, vp = T._rand((2, H, P, d), 3).bfloat16()
+    x, y = T._rand((3, H, nq, d), 1).bfloat16(), T._rand((3, H, n, d), 2).bfloat16()
+    for a in (layer, short):
+        a.set_prompt(kp, vp)
+    short.load_history(x[1], x[2])
+    full = [t.clone() for t in layer.step(*x)]
+    assert [t.shape[1] for t in full] == [nq, nq]
+    lse = layer.lse_self.clone(), layer.lse_cross.clone()
+    got, want = layer.step(*y), short.step(*y)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert a.shape == (H, n, d) and torch.equal(a, b)
+    for a, b, before in zip((layer.lse_self, layer.lse_cross), (short.lse_self, short.lse_cross), lse):
+        assert torch.equal(a[:, :n], b) and torch.equal(a[:, n:], before[:, n:])
+    for a, before in zip((layer.o_self, layer.o_cross), full):
+        assert torch.equal(a[:, n:], before[:, n:])
+    out = torch.full((H, nq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(layer.step_cross(y[0], out=out), want[1]) and bool((out[:, n:] == 7.0).all())
+
+
+def test_cross_attention_of_more_tokens_than_the_layers_is_refused():
+    layer = WindowLayer(2, 64, 4, 60, 10, 500, 8)
+    q = T._rand((2, 5, 64), 1).bfloat16()
+    with pytest.raises(ValueError, match="tokens"):
+        layer.step_cross(q)
+    with pytest.raises(ValueError, match="tokens"):
+        layer.step_cross(q[:, :4], out=torch.empty(2, 3, 64, dtype=torch.bfloat16, device="cuda"))
