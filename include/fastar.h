@@ -656,9 +656,10 @@ int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d
  * (int32 [B + 1] on the device, not falling; NULL: T / B tokens each, T a multiple of B); at[b]
  * (int32 [B] on the device) rows come before them: token i of a sequence is its row at + i.  Tokens
  * past cu[B] belong to no sequence: nothing of theirs is read for others or written.
- *   cu that falls or leaves [0, T], or at outside [0, max_pages * page]: FASTAR_DEV_BAD_LEN, and the
- *   sequence is skipped.  A table entry outside [0, pages) where it is needed:
- *   FASTAR_DEV_BAD_INDEX.  B <= 65535 (FASTAR_ECAPACITY).  dev_status optional. */
+ *   at outside [0, max_pages * page]: FASTAR_DEV_BAD_LEN, and the sequence is skipped.  cu that falls or
+ *   leaves [0, T]: FASTAR_DEV_BAD_LEN; a sequence whose own bounds do so is skipped, and what the others'
+ *   rows behind at and outputs hold is not defined (any of them may have been left as it was).  A table
+ *   entry outside [0, pages) where it is needed: FASTAR_DEV_BAD_INDEX.  B <= 65535 (FASTAR_ECAPACITY).  dev_status optional. */
 
 /* The call's rows of k and v [Hk, T, d] into their pages, k with RMS norm (wk non-NULL) and rotary
  * positions on the way, and q [Hq, T, d] in the same way to q_out (q and q_out NULL: not).  Norm,
@@ -666,7 +667,8 @@ int fastar_kv4_attn(const void* q, int dtype, int Hq, int Hkv, int64_t nq, int d
  * row r = at + i on the grid: frame r / (grid_h grid_w), row (r / grid_w) % grid_h, column
  * r % grid_w (grid 1 x 1: r itself turns the first axis).  v goes as it is.
  * len_out[b] = at + tokens (optional; held to the sequence's rows; no element in common with at, cu or
- * table, FASTAR_EINVAL otherwise; of a skipped sequence 0).
+ * table, FASTAR_EINVAL otherwise; of a sequence skipped for its at 0; with a cu that falls or leaves [0, T] at of
+ * every other sequence, none is longer than before).
  * Rows past the sequence's last are dropped and set FASTAR_DEV_BAD_LEN, rows whose table
  * entry is no page are dropped and set FASTAR_DEV_BAD_INDEX; their q_out is written all the same.
  * Other rows of the pools are left as they were.  Of two tokens whose rows share a slot (two

@@ -68,11 +68,14 @@ __global__ void __launch_bounds__(kWarpsA * 32)
     ws[1][c] = a.wk ? a.wk[c] : 1.f;
   }
   const int64_t cap = a.max_pages << a.pool.page_shift;
-  if (blockIdx.x == 0 && a.len_out) {
+  bool lost = false;               // cu makes no sense: whose tokens are whose is not known
+  if (blockIdx.x == 0 && (a.len_out || a.status)) {
     for (int b = threadIdx.x; b < a.B; b += kWarpsA * 32) {
       const paged::Seq s = paged::sequence(a.cu, a.at, a.B, a.T, cap, b, a.status);
       const int64_t n = (int64_t)s.at + s.nq;
+      if (!a.len_out) continue;
       a.len_out[b] = (int)(n < cap ? n : cap);
+      if (a.cu) lost |= a.cu[b] < 0 || a.cu[b + 1] < a.cu[b] || a.cu[b + 1] > a.T;
     }
   }
   constexpr int LPR = D / 16;      // lanes of a row
@@ -117,7 +120,14 @@ __global__ void __launch_bounds__(kWarpsA * 32)
   };
 #pragma unroll 1
   for (int i = 0; i < kSlots - 1; ++i) ask();
-  __syncthreads();                         // the tables; after the first rows are on their way
+  // the tables are there; after the first rows are on their way
+  if (__builtin_expect(__syncthreads_or(lost), 0)) {
+    // no sequence gets longer (a token is looked for as if cu did not fall, so that any may miss rows)
+    for (int b = threadIdx.x; b < a.B; b += kWarpsA * 32) {
+      const int n = a.at[b];
+      a.len_out[b] = n >= 0 && n <= cap ? n : 0;
+    }
+  }
   uint32_t turns = 0;                      // of this lane's pairs
 #pragma unroll
   for (int e = 0; e < 8; ++e)

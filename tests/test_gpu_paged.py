@@ -639,3 +639,78 @@ def test_few_rows_of_every_kind_of_group(d, G):
         c = attn_case("bf16", [nq], [1700], 1, G, d, 64, "hnd", 1, 0, 0, seed=G + 1)
         out, lse = run_attn(*c, 1 / math.sqrt(d), 1, 0, 0)
         check_attn("bf16", *c, 1 / math.sqrt(d), 1, 0, 0, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B", [4, 300])
+def test_lengths_do_not_grow_by_a_call_whose_starts_make_no_sense(dtype, B):
+    """cu that falls or leaves the call's tokens: whose tokens are whose is not known, so no sequence gets longer; rows
+    behind the lengths may be written, of sequences whose own bounds make sense, and nothing else."""
+    dt, d, H, page, n = DT[dtype], 64, 2, 16, 3
+    T = n * B
+    k, v = _rand((H, T, d), 1).to(dt), _rand((H, T, d), 2).to(dt)
+    width = 40 if B == 4 else 80
+    table = np.random.default_rng(1).permutation(B * width).reshape(B, width).astype(np.int32)
+    at = [5 + b % 23 for b in range(B)]
+    at[2] = -1
+    good = [n * b for b in range(B + 1)]
+    mid = B - 1
+    for at_i, x in ((1, -1), (mid, n * (mid - 1) - 1), (mid, T + 1), (mid, -2 ** 31), (mid, 2 ** 31 - 1), (0, -1), (B, T + 1),
+                    (1, n * 3), (B, 0)):
+        cu = list(good)
+        cu[at_i] = x
+        bad = [b for b in range(B) if cu[b] < 0 or cu[b + 1] < cu[b] or cu[b + 1] > T]
+        assert bad
+        kp, vp = (pool_like(B * width, H, page, d, dt, "nhd", f) for f in (3.0, 5.0))
+        ln, st = _i32([-7] * B), _i32([0])
+        L.fastar_paged_append(k, v, kp, vp, _i32(table), _i32(at), ln, cu=_i32(cu), dev_status=st)
+        torch.cuda.synchronize()
+        assert st.item() == L.DEV_BAD_LEN
+        assert ln.tolist() == [max(a, 0) for a in at]
+        for pool, src, fill in ((kp, k, 3.0), (vp, v, 5.0)):
+            flat = pool.transpose(1, 2).reshape(-1, H, d)                  # slots
+            touched = (flat != fill).any(-1).any(-1).nonzero()[:, 0].tolist()
+            may = {}
+            for b in range(B):
+                if b not in bad and at[b] >= 0:
+                    for i in range(min(cu[b + 1] - cu[b], width * page - at[b])):
+                        r = at[b] + i
+                        may[int(table[b, r // page]) * page + r % page] = cu[b] + i
+            assert set(touched) <= set(may)
+            if touched:
+                assert torch.equal(flat[touched], src[:, [may[s] for s in touched]].transpose(0, 1))
+    ln = _i32([-7] * B)
+    L.fastar_paged_append(k, v, kp, vp, _i32(table), _i32(at), ln, cu=_i32(good))
+    torch.cuda.synchronize()
+    assert ln.tolist() == [a + n if a >= 0 else 0 for a in at]
+
+
+@pytest.mark.parametrize("nq", [1, 20, 60])
+@pytest.mark.parametrize("cu", [[0, 3, 2, 5, 12], [0, 3, 100, 5, 12], [-1, 3, 6, 9, 12]])
+def test_attention_of_starts_that_make_no_sense_leaves_other_tokens(nq, cu):
+    """Tokens that no sequence has whose own bounds make sense are left as they were."""
+    cu, Ts = [c * nq for c in cu], 14 * nq
+    c = attn_case("bf16", [3 * nq] * 4, [100, 50, 30, 70], 1, 2, 128, 16, "hnd", 1, 0, 0, seed=3, tail=2 * nq)
+    q, kp, vp, table, at, _ = c
+    assert q.shape[1] == Ts
+    table = np.concatenate((table, np.zeros((4, 64), np.int32)), 1)        # pages for the longest
+    out, lse = run_attn(q, kp, vp, table, at, np.array(cu), 0.1, 1, 0, 0, max_q=Ts, status=L.DEV_BAD_LEN, bits=L.DEV_BAD_LEN)
+    mine = np.zeros(Ts, bool)
+    for b in range(4):
+        if 0 <= cu[b] <= cu[b + 1] <= Ts:
+            mine[cu[b]:cu[b + 1]] = True
+    rest = torch.from_numpy(~mine).cuda()
+    assert bool((out[:, rest] == 7.0).all()) and bool((lse[:, rest] == 7.0).all())
+
+
+def test_starts_that_make_no_sense_are_told_without_lengths():
+    """The bounds of a sequence that no token is looked for in."""
+    k = _rand((1, 6, 64), 1).bfloat16()
+    kp, vp = (pool_like(8, 1, 16, 64, torch.bfloat16, "hnd", 3.0) for _ in range(2))
+    table = _i32(np.arange(8).reshape(4, 2))
+    for cu, at, want in (([-1, 0, 2, 4, 6], [0] * 4, L.DEV_BAD_LEN), ([0, 2, 2, 4, 6], [0, 33, 0, 0], L.DEV_BAD_LEN),
+                         ([0, 2, 2, 4, 6], [0, 32, 0, 0], 0), ([2, 2, 2, 4, 5], [0] * 4, 0)):
+        st = _i32([0])
+        L.fastar_paged_append(k, k, kp, vp, table, _i32(at), cu=_i32(cu), dev_status=st)
+        torch.cuda.synchronize()
+        assert st.item() == want
