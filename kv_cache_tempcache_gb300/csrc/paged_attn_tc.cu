@@ -354,14 +354,16 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       }
       // a group of warps that exchange results leaves together
       float l = l0 + l1;
-      sm.ex[half][w][row] = l;
+      // (nothing where this row tile has no key tile: the other half may still be reading the sums of the item before,
+      // and no barrier of the loop has come since)
+      if (count > 0) sm.ex[half][w][row] = l;
       if (both && w == 1 && half == 0) sm.mx[row] = m;
       if (!(both ? tc::named_bar_and(both_bar, 128, ok) : tc::named_bar_and(pair_bar, 64, ok))) {
         ok = false;
         break;
       }
       if (!early && next && next->T > 0) bring_q(*next);
-      l += sm.ex[half ^ 1][w][row];
+      if (count > 0) l += sm.ex[half ^ 1][w][row];
       float f0 = 1.f, f1 = 0.f;             // weights of this sum and of the odd tiles'
       if (mine && both && T > 1) {
         const float lo = sm.ex[0][1][row] + sm.ex[1][1][row], mo = sm.mx[row];

@@ -714,3 +714,33 @@ def test_starts_that_make_no_sense_are_told_without_lengths():
         L.fastar_paged_append(k, k, kp, vp, table, _i32(at), cu=_i32(cu), dev_status=st)
         torch.cuda.synchronize()
         assert st.item() == want
+
+
+@pytest.mark.parametrize("d,nq", [(64, 130), (128, 130), (128, 300)])
+@pytest.mark.parametrize("ws", [True, False])
+def test_values_that_are_not_finite_among_many_sequences_that_see_nothing(d, nq, ws):
+    """Sequences whose pages end before their window, a run of them between two that see their rows: pieces without
+    a key tile go by while the ones before are still written."""
+    B, page, cap, window = 700, 32, 448, 40
+    full = np.arange(B) % 9 != 4
+    at = np.where(full, cap, 430 - nq)
+    table = np.full((B, cap // page), -1, np.int32)
+    own = np.flatnonzero(~full)                              # they see rows 390 .. 429
+    table[own, 12:14] = np.arange(2 * len(own)).reshape(-1, 2)
+    kp, vp = (_rand((2 * len(own), 1, page, d), s).bfloat16() for s in (1, 2))
+    q = _rand((1, B * nq, d), 3).bfloat16()
+    clean = run_attn(q, kp, vp, table, at, None, 0.1, 0, window, 0, ws=ws)
+    tok = torch.from_numpy((own[:, None] * nq + np.arange(nq)).reshape(-1)).cuda()
+    rest = torch.ones(B * nq, dtype=torch.bool, device=DEV)
+    rest[tok] = False
+    assert bool((clean[0][:, rest] == 0).all()) and bool(torch.isneginf(clean[1][:, rest]).all())
+    check_attn("bf16", q[:, tok], kp, vp, table[own], at[own], None, 0.1, 0, window, 0, clean[0][:, tok], clean[1][:, tok])
+    bad, what = vp.clone(), float("inf")
+    bad[table[own, 12], 0, 16, 3] = what                     # row 400
+    bad[table[own, 12], 0, 17, d - 1] = -what
+    for _ in range(3):
+        out, lse = run_attn(q, kp, bad, table, at, None, 0.1, 0, window, 0, ws=ws)
+        assert torch.equal(lse, clean[1]) and torch.equal(out[:, rest], clean[0][:, rest])
+        assert bool((out[:, tok, 3] == what).all()) and bool((out[:, tok, d - 1] == -what).all())
+        keep = [c for c in range(d) if c not in (3, d - 1)]
+        assert torch.equal(out[:, tok][..., keep], clean[0][:, tok][..., keep])
