@@ -77,7 +77,10 @@ struct alignas(16) Ctl {
   uint64_t q_full[2], s_full[2], p_full[2][2], fin;    // by row tile (P: first 32 keys of each half, last 32)
   uint64_t item_full[paged::kItems], item_free[paged::kItems];
   Item item[paged::kItems];                            // item x of this CTA in place x % kItems
-  int poison[paged::kItems];                           // x + 1: infinities or NaN were taken out of item x's V
+  // n: infinities or NaN were taken out of the V of the n-th item with key tiles, in place (n - 1) % kItems.  (Not by all
+  // items: those without key tiles go by without the other CTA, which may be that far behind and find its mark gone; the
+  // tiles of V keep the CTAs of a pair within kItems of one another.)
+  int poison[paged::kItems];
   uint32_t tmem_base;
   int abort;
   float ex[2][2][kRT];                                 // a row's two threads: half, row tile, row
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       const bool has = it.r0 + i0 < it.rows;
       const RowOf at = row_of(a, it, has ? it.r0 + i0 : it.rows - 1);    // a row that is not there: as the last
       const bool live = l > 0.f || l != l;
-      const bool poison = *(volatile int*)&sm.poison[x % paged::kItems] == x + 1;
+      const bool poison = T > 0 && *(volatile int*)&sm.poison[(done - 1) % paged::kItems] == (int)done;
       const float f = live ? 1.f / l : 0.f;
       // Rows of 64 bytes (32 channels) go through shared memory, so that they leave as whole runs
       uint8_t* stg = base + Lay::out + warp * 2048;
@@ -571,9 +574,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     } else if (warp == kVWarp) {
       // ---------------- V tiles looked into and handed on ----------------
       bool ok;
-      int n = 0;
+      int n = 0, nth = 0;                                   // tiles, items with tiles so far, this one among them
       for (int x = 0; const Item* item = item_at(x, ok); ++x) {
         const Item& it = *item;
+        nth += it.T > 0;
         for (int i = 0; i < it.T; ++i, ++n) {
           const int st = n % Lay::vs, key0 = it.tiles.key(it.j0 + i);
           if (!(ok = wait_warp(&sm.v_land[st], (n / Lay::vs) & 1, abort))) break;
@@ -607,12 +611,13 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             }
             tc::fence_proxy_async();
             if (__any_sync(0xffffffffu, found) && lane == 0) {
-              *(volatile int*)&sm.poison[x % paged::kItems] = x + 1;
+              int* mark = &sm.poison[(nth - 1) % paged::kItems];
+              *(volatile int*)mark = nth;
               if (kCta == 2) {               // the other CTA's rows see these channels too
                 asm volatile(
                     "{\n .reg .b32 p;\n mapa.shared::cluster.u32 p, %0, %1;\n st.shared::cluster.u32 [p], %2;\n}\n" ::"r"(
-                        tc::smem_u32(&sm.poison[x % paged::kItems])),
-                    "r"(rank ^ 1), "r"(x + 1)
+                        tc::smem_u32(mark)),
+                    "r"(rank ^ 1), "r"(nth)
                     : "memory");
                 asm volatile("fence.acq_rel.cluster;" ::: "memory");
               }

@@ -744,3 +744,35 @@ def test_values_that_are_not_finite_among_many_sequences_that_see_nothing(d, nq,
         assert bool((out[:, tok, 3] == what).all()) and bool((out[:, tok, d - 1] == -what).all())
         keep = [c for c in range(d) if c not in (3, d - 1)]
         assert torch.equal(out[:, tok][..., keep], clean[0][:, tok][..., keep])
+
+
+@pytest.mark.parametrize("d,G,nq", [(64, 2, 70), (128, 2, 70), (128, 1, 90), (128, 3, 200)])
+def test_values_that_are_not_finite_are_those_of_their_piece(d, G, nq):
+    """Every other sequence that sees something has a NaN, in the channels of one CTA of a pair or of the other; between
+    them up to twenty that see nothing: what is taken out of one piece's V comes back to that piece."""
+    B, Hk, page, cap, window = 400, 2, 32, 256, 20
+    rng = np.random.default_rng(nq)
+    full = rng.random(B) < 0.9
+    full[:3] = False
+    own = np.flatnonzero(~full)
+    at = np.where(full, cap, 120 - nq if nq <= 120 else 0)
+    end = int(at[own[0]]) + nq
+    table = np.full((B, cap // page), -1, np.int32)
+    need = list(range(max(0, end - window) // page, (end - 1) // page + 1))
+    table[np.ix_(own, need)] = np.arange(len(own) * len(need)).reshape(-1, len(need))
+    kp, vp = (_rand((len(own) * len(need), Hk, page, d), s).bfloat16() for s in (1, 2))
+    q = _rand((Hk * G, B * nq, d), 3).bfloat16()
+    clean = run_attn(q, kp, vp, table, at, None, 0.1, 0, window, 0)
+    row, bad = end - 3, vp.clone()
+    chs = {}
+    for x, b in enumerate(own):
+        if x % 2:
+            chs[b] = 1 if x % 4 == 1 else d - 2
+            bad[int(table[b, row // page]), 1, row % page, chs[b]] = float("nan")
+    for _ in range(3):
+        out, lse = run_attn(q, kp, bad, table, at, None, 0.1, 0, window, 0)
+        assert torch.equal(lse, clean[1]) and torch.equal(out[:G], clean[0][:G])
+        want = clean[0].clone()
+        for b, ch in chs.items():
+            want[G:, b * nq:(b + 1) * nq, ch] = float("nan")
+        assert torch.equal(out.isnan(), want.isnan()) and torch.equal(out.nan_to_num(), want.nan_to_num())
