@@ -776,3 +776,55 @@ def test_values_that_are_not_finite_are_those_of_their_piece(d, G, nq):
         for b, ch in chs.items():
             want[G:, b * nq:(b + 1) * nq, ch] = float("nan")
         assert torch.equal(out.isnan(), want.isnan()) and torch.equal(out.nan_to_num(), want.nan_to_num())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,nq,page,layout", [(64, 20, 128, "nhd"), (128, 1, 16, "hnd"), (128, 10, 128, "nhd"), (128, 16, 64, "hnd"),
+                                             (128, 50, 128, "hnd"), (128, 60, 16, "nhd"), (128, 100, 128, "nhd"),
+                                             (128, 300, 16, "hnd"), (128, 700, 128, "nhd")])
+@pytest.mark.parametrize("ws", [True, False])
+def test_values_that_are_not_finite_reach_who_sees_them(dtype, d, nq, page, layout, ws):
+    """Infinities and NaN in rows of V that some tokens see and others do not, and in rows that all see: by few rows, a
+    CTA alone, a pair with one row tile and with two; in channels of both CTAs of a pair, and in all."""
+    Hk, G, at, block, window, sinks = 2, 2, 600, 1, 150, 20
+    q, kp, vp, table, a, cu = attn_case(dtype, [nq], [at], Hk, G, d, page, layout, block, window, sinks, seed=nq)
+    scale = 1 / math.sqrt(d)
+    clean = run_attn(q, kp, vp, table, a, cu, scale, block, window, sinks, ws=ws)
+    see = P.sees(nq, at, at + nq, block, window, sinks)
+    for i, row in enumerate(sorted({at + nq - 1, at + nq // 2, at - window + 1, at + nq - window, 19, 0})):
+        if not see[:, row].any():
+            continue
+        what = (float("nan"), float("inf"), float("-inf"))[i % 3]
+        for ch in ([3], [d - 5], [3, d // 2 + 1], list(range(d))):
+            pg, of = int(table[0, row // page]), row % page
+            keep = vp[pg, 1, of].clone()
+            vp[pg, 1, of, ch] = what
+            out, lse = run_attn(q, kp, vp, table, a, cu, scale, block, window, sinks, ws=ws)
+            vp[pg, 1, of] = keep
+            rows = torch.from_numpy(see[:, row]).cuda()
+            assert torch.equal(lse, clean[1]) and torch.equal(out[:G], clean[0][:G])
+            assert torch.equal(out[G:, ~rows], clean[0][G:, ~rows])
+            got = out[G:, rows]
+            assert bool(torch.isnan(got[..., ch]).all() if what != what else (got[..., ch] == what).all())
+            other = [c for c in range(d) if c not in ch]
+            assert torch.equal(got[..., other], clean[0][G:, rows][..., other])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [1, 30, 40, 100, 200, 600])
+def test_large_and_lopsided_logits_of_128_channels(dtype, nq):
+    """Logits of hundreds and rows of keys that rise, fall, or lie 30 below one strong key whose V is 0: the reference
+    moves in the middle, in every kernel for 128 channels."""
+    d, page, n = 128, 128, 1000
+    q, kp, vp, table, a, cu = attn_case(dtype, [nq], [n - nq], 1, 1, d, page, "hnd", 0, 0, 0, seed=2)
+    row = torch.arange(n, device=DEV)
+    pg, of = torch.from_numpy(table[0]).long().cuda()[row // page], row % page
+    for shape in (row * 0.5, -row * 0.5, torch.where(row == 517, 30.0, 0.0)):
+        kp[pg, :, of] = 0
+        kp[pg, 0, of, 70] = shape.to(kp.dtype)
+        if float(shape.max()) == 30.0:
+            vp[pg[517], :, of[517]] = 0
+        q[...] = 0
+        q[:, :, 70] = 1.0
+        out, lse = run_attn(q, kp, vp, table, a, cu, 1.0, 0, 0, 0)
+        check_attn(dtype, q, kp, vp, table, a, cu, 1.0, 0, 0, 0, out, lse)
