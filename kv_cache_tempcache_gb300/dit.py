@@ -179,8 +179,11 @@ class DiT:
                                                               dim=-1).to(bf))
         elif attention == "window":
             frame = cfg.grid_h * cfg.grid_w
-            self.attn = [WindowLayer(H, d, N, cfg.window_frames * frame, cfg.sink_frames * frame, max(dense_capacity, N),
-                                     cfg.text_len, dtype=bf, device=dev) for _ in range(cfg.layers)]
+            self.attn = []
+            for _ in range(cfg.layers):                    # one after the other: a workspace for all
+                self.attn.append(WindowLayer(H, d, N, cfg.window_frames * frame, cfg.sink_frames * frame,
+                                             max(dense_capacity, N), cfg.text_len, dtype=bf, device=dev,
+                                             workspace=self.attn[0].ws if self.attn else None))
         else:
             cap = max(dense_capacity, N)
             layer = KV4Layer if attention == "dense4" else DenseLayer

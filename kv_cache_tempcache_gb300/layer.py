@@ -614,10 +614,11 @@ class WindowLayer:
     live on the device, so one captured step serves every length (with advance=True each replay keeps its
     chunk).  Hkv: heads of the cache (default H; H must be a multiple of it); block: tokens of a frame that
     sees itself and the frames before it in the chunk, not those after it (0: the chunk sees all of
-    itself; 1: causal)."""
+    itself; 1: causal).  workspace: the ws of a layer of the same sizes (some 40 MB where a
+    chunk has more than a few tokens), shared by layers whose steps do not overlap on the GPU; None: its own."""
 
     def __init__(self, H, d, Nq, window, sinks, rows, P, dtype=torch.bfloat16, device="cuda", scale=None, Hkv=None, block=0,
-                 page=64):
+                 page=64, workspace=None):
         L.load()
         if window < 1 or sinks < 0 or rows < 1 or Nq < 1:
             raise ValueError("window, rows and Nq must be positive, sinks not negative")
@@ -643,7 +644,9 @@ class WindowLayer:
         self.lse_cross = _f32(H, Nq, dev=dev)
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
         nb = L.workspace_bytes(L.OP_PAGED_ATTN, H, Nq, min(self.cap, self.window + self.sinks), d, Hkv, r=Nq, P=1)
-        self.ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+        if workspace is not None and workspace.nbytes < nb:
+            raise ValueError(f"a workspace of {workspace.nbytes} bytes where {nb} are needed")
+        self.ws = workspace if workspace is not None else torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
 
     @property
     def n(self) -> int:

@@ -299,3 +299,18 @@ def test_cross_attention_of_more_tokens_than_the_layers_is_refused():
         layer.step_cross(q)
     with pytest.raises(ValueError, match="tokens"):
         layer.step_cross(q[:, :4], out=torch.empty(2, 3, 64, dtype=torch.bfloat16, device="cuda"))
+
+
+def test_the_blocks_share_a_workspace():
+    dit, _ = _dit()
+    assert dit.attn[0].ws is not None and len({a.ws.data_ptr() for a in dit.attn}) == 1
+    own = [WindowLayer(2, 64, 40, 60, 10, 500, 8) for _ in range(2)]
+    assert own[0].ws.data_ptr() != own[1].ws.data_ptr()
+    with pytest.raises(ValueError, match="workspace"):
+        WindowLayer(2, 64, 40, 60, 10, 500, 8, workspace=own[0].ws[:-16])
+    # two layers of a rollout on one workspace, step by step: as with their own
+    shared = WindowLayer(2, 64, 40, 60, 10, 500, 8, workspace=own[0].ws)
+    for i in range(3):
+        x, y = T._rand((2, 3, 2, 40, 64), i).bfloat16()
+        own[0].step_self(*x)
+        assert torch.equal(shared.step_self(*y), own[1].step_self(*y))
