@@ -14,10 +14,11 @@
 // (With the rows moved by cp.async, 16 bytes a lane, 250 of 665 instructions a tile at 32 rows were theirs.)
 // Rows of V that no token sees become zeros in shared memory; pages that no token sees, or that are not there,
 // come as zeros.
-// Measured: one token each of 32 sequences, 32 heads of 8, 8191 + 100 rows 143 us (6.7 TB/s, 0.99 of the measured copy rate); up
+// Measured: one token each of 32 sequences, 32 heads of 8, 8191 + 100 rows 147 to 149 us a call (6.4 TB/s, 0.95 of the measured copy rate); up
 // to 28 rows over six sequences of up to 40,000 rows 89 us (5.1 TB/s); one token over 333 rows 6.7 us, a block's start, five
 // tiles a warp and the join of its warps, one after the other.
-// P is bf16, as V is: 2^-8 of itself at every magnitude.  The reference moves only when a P would pass 2^kTop.
+// P is bf16, as V is, or two of them (kSplitGroups): 2^-8 or 2^-15 of itself at every magnitude.  The reference moves only when
+// a P would pass 2^kTop.
 #include <climits>
 
 #include "common.cuh"
@@ -34,6 +35,12 @@ namespace {
 
 constexpr int kKeys = 16;
 constexpr float kTop = 8.f;
+// Groups of 8 rows up to which P is two bf16 (2^-15 of itself) and P V two products.  With one bf16 a token's output was up to
+// 1.53 times as far from the exact one as fp32 weights leave it after its own rounding to bf16 (12 heads, 333 rows), with
+// two 1.00.  The second product is 0 to 0.8 % of a call's time with one group or two (32 sequences of one token 148.6 -> 149.2
+// us, 12 rows over six sequences 92.7 -> 93.8), where the bytes are what bounds it; with four 10 % (28 rows 90.0 -> 99.5), for
+// outputs that are 1.1 to 1.3 times as far off.
+constexpr int kSplitGroups = 2;
 
 // NR: groups of 8 rows.
 template <int D, int NR, int W>
@@ -81,6 +88,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
+// Weights as two bf16: their upper halves, and what those leave out.  Nothing but a weight of 0 leaves 0, so that an infinity
+// of V stays one.
+__device__ __forceinline__ uint32_t upper2(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ float left_out(float a) {
+  return fmaxf(a - __uint_as_float(__float_as_uint(a) & 0xffff0000u), fminf(a, 0x1p-126f));
+}
 // Over the eight lanes of equal t.
 __device__ __forceinline__ float group_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
@@ -98,6 +113,7 @@ __global__ void __launch_bounds__(W * 32)
     paged_attn_few_kernel(const PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap vmap) {
   using Lay = FewLayout<D, NR, W>;
+  constexpr bool kSplit = NR <= kSplitGroups;             // weights as two bf16
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float2* sml = reinterpret_cast<float2*>(smem + Lay::ctl);        // [W][8 NR] references and sums
@@ -313,22 +329,29 @@ __global__ void __launch_bounds__(W * 32)
         }
       all_set = __all_sync(0xffffffffu, isset == (1u << (2 * NR)) - 1);
     }
-    uint32_t pb[NR][2];
+    uint32_t pb[NR][2], pl[kSplit ? NR : 1][2];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       const float p0 = ex2f(fmaf(x[n][0], sl2, nm[n][0])), p1 = ex2f(fmaf(x[n][1], sl2, nm[n][1]));
       const float p2 = ex2f(fmaf(x[n][2], sl2, nm[n][0])), p3 = ex2f(fmaf(x[n][3], sl2, nm[n][1]));
       l[n][0] += p0 + p2;
       l[n][1] += p1 + p3;
-      pb[n][0] = transpose8(pack_bf16(p0, p1));
-      pb[n][1] = transpose8(pack_bf16(p2, p3));
+      pb[n][0] = transpose8(kSplit ? upper2(p0, p1) : pack_bf16(p0, p1));
+      pb[n][1] = transpose8(kSplit ? upper2(p2, p3) : pack_bf16(p2, p3));
+      if (kSplit) {
+        pl[n][0] = transpose8(pack_bf16(left_out(p0), left_out(p1)));
+        pl[n][1] = transpose8(pack_bf16(left_out(p2), left_out(p3)));
+      }
     }
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
       uint32_t v[4];
       ldsm4t(ldv[c & 3] + at + (c >> 2) * (kKeys * 128), v);
 #pragma unroll
-      for (int n = 0; n < NR; ++n) mma16816(o[n][c], v, pb[n][0], pb[n][1]);
+      for (int n = 0; n < NR; ++n) {
+        mma16816(o[n][c], v, pb[n][0], pb[n][1]);
+        if (kSplit) mma16816(o[n][c], v, pl[n][0], pl[n][1]);
+      }
     }
     __syncwarp();                                        // the stage is asked for again
     if (++st == Lay::stages) st = 0, ph ^= 1;

@@ -828,3 +828,23 @@ def test_large_and_lopsided_logits_of_128_channels(dtype, nq):
         q[:, :, 70] = 1.0
         out, lse = run_attn(q, kp, vp, table, a, cu, 1.0, 0, 0, 0)
         check_attn(dtype, q, kp, vp, table, a, cu, 1.0, 0, 0, 0, out, lse)
+
+
+@pytest.mark.parametrize("ws", [True, False])
+@pytest.mark.parametrize("nq,at,Hk,G,d,page,block,window,sinks", [
+    ([1], [332], 12, 1, 128, 64, 1, 0, 0), ([1] * 4, [2000, 5, 700, 40], 2, 4, 128, 16, 1, 500, 9),
+    ([2, 1], [60, 5000], 1, 8, 64, 32, 1, 0, 0), ([16], [3000], 3, 1, 128, 128, 1, 1000, 70), ([3], [90], 4, 5, 64, 16, 0, 0, 0),
+    ([1, 0, 1], [20000, 3, 17], 1, 16, 128, 32, 1, 0, 0)])
+def test_weights_of_a_few_rows_keep_their_precision(nq, at, Hk, G, d, page, block, window, sinks, ws):
+    """Up to 16 rows a KV head: P as two bf16, the upper half cut off and the rest (below 2^-7 of it) rounded by
+    2^-8 of itself, 2^-15 relative; else as this file's bound for bf16, the output's rounding 2^-8."""
+    assert max(nq) * G <= 16
+    c = attn_case("bf16", nq, at, Hk, G, d, page, "hnd", block, window, sinks, seed=31)
+    scale = 1 / math.sqrt(d)
+    out, lse = run_attn(*c, scale, block, window, sinks, ws=ws)
+    q, kp, vp, table, a, cu = c
+    want, _, A, E, n = P.attention(_np(q), _np(kp), _np(vp), table, a, scale, cu, block, window, sinks)
+    e = (d * 2.0 ** -23 + 2.0 ** -22) * E + 2.0 ** -22
+    big = np.nan_to_num(np.abs(_np(vp)), nan=0.0).max()
+    tol = 2.0 ** -8 * np.abs(want) + n[None, :, None] * 2.0 ** -100 * big + A * (4 * e + n * 2.0 ** -22 + 2.0 ** -15)[..., None]
+    assert (np.abs(_np(out) - want) <= tol).all(), (np.abs(_np(out) - want) / tol).max()
