@@ -695,7 +695,8 @@ int fastar_paged_append(int dtype, int B, int64_t T, const int32_t* cu, int d, i
  * pages back).  What a token does not see cannot reach its output, whatever its bits.  A row of a
  * page that is needed and missing counts as zeros (FASTAR_DEV_BAD_INDEX).
  * max_q: the most tokens of a sequence (host; FASTAR_EINVAL outside [1, T]).  Of a longer one the first max_q
- * are done, the others' outputs are left as they were, FASTAR_DEV_BAD_LEN is set.
+ * are done, the others' outputs are left as they were, FASTAR_DEV_BAD_LEN is set.  It picks the kernel for all sequences: a
+ * value far above the most costs time (several times with single tokens).
  * Every weight is held to 2^-8 of itself (bf16; 2^-15 where max_q * Hq / Hkv is at most 16) or in fp32 (dtype F32); logits,
  * maxima and sums in fp32.
  * A row of q with a NaN or an infinity gives NaN (zeros if none of its logits is above

@@ -735,7 +735,8 @@ def fastar_paged_attn(q, k_pool, v_pool, table, at, scale, out, lse=None, cu=Non
     that table [B, max_pages] names, the tokens' own rows (behind at[b] earlier ones) among them.  block: 0,
     or the tokens of a block that sees no later one (1: causal); window > 0: only the last `window` rows before
     the token's end, and the first `sinks`.  cu [B + 1] as in fastar_paged_append; max_q: the most tokens
-    of a sequence (None: T, with cu None T / B).  workspace: workspace_bytes(OP_PAGED_ATTN, Hq, T,
+    of a sequence (None: T, with cu None T / B).  It picks the kernel: give it with cu, since single tokens of many
+    sequences are several times slower as sequences of T tokens.  workspace: workspace_bytes(OP_PAGED_ATTN, Hq, T,
     max_pages * page, d, Hkv, r=max_q, P=B) bytes (None: the keys are not split)."""
     qs = q.shape
     Hq, T, d = qs if len(qs) == 3 else _dims3("q", q)

@@ -12,7 +12,8 @@
 // fast, and blocks that stay and take an equal share of the tokens wait for the slowest (14,400 tokens of 72 heads 93.5
 // us; now 81.1).  Measured, each call on inputs that are not in L2: 4680 tokens of 36 heads 17.5 us (4.9 TB/s; 15.7 where the
 // inputs are there), 14,400 of 72 heads 81.1 (6.5 TB/s, 0.96 of the measured copy rate); 100,000 tokens of 6 heads 121 (2.5
-// TB/s: the tokens' rotations).
+// TB/s: where a side has fewer heads than a warp has rows side by side, 4 at d = 128 and 8 at d = 64, lanes idle, and a token's
+// sequence, page and sines are found one after the other between two tokens; what each costs is not measured).
 #include <climits>
 
 #include "common.cuh"

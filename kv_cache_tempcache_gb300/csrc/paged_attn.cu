@@ -12,6 +12,7 @@
 #include "kernels.h"
 #include "paged.cuh"
 #include "paged_attn.h"
+#include "paged_tc.cuh"
 #include "tmap.h"
 
 namespace fastar {
@@ -19,7 +20,6 @@ namespace fastar {
 namespace {
 
 constexpr int kMaxSplits = 256;
-constexpr int kMaxTensorShares = 256;    // paged_tc.cuh
 
 // ---- joining the splits ----------------------------------------------------------------------
 // O = sum_s e^(m_s - m) o_s / sum_s e^(m_s - m) l_s over a row's partials, m = max_s m_s; one warp a
@@ -137,19 +137,20 @@ size_t slot_bytes(const Plan& p, int d, int Hq, int max_q) {
 Plan make_plan(int dtype, int d, int Hq, int Hkv, int B, int max_q, int64_t keys) {
   const int64_t rows = (int64_t)(Hq / Hkv) * max_q;
   if (dtype == FASTAR_F32) {
-    // two blocks a multiprocessor, a tile of 64 keys
+    // slots for two blocks a multiprocessor, a tile of 64 keys each or more.  At d = 64 both are resident; at d = 128 a block
+    // takes 158 KB of shared memory, one fits, and a call that uses all its slots runs in two waves
     const int64_t units = (rows + kF32Rows - 1) / kF32Rows * Hkv;
     return plan_slots(kF32, units, B, keys, 2 * sm_count(), kF32Keys, 1);
   }
-  // two blocks a multiprocessor, all resident (a few tokens of six long sequences take 89 us with two blocks, 110 with
-  // three, 102 with four, 123 with eight); eight tiles of 16 keys a warp, or with more than one group of eight rows, where
+  // two blocks a multiprocessor, all resident: one wave (28 rows over six long sequences take 89 us with two blocks, 110 with
+  // three, one and a half waves, 102 with four, two, 123 with eight); eight tiles of 16 keys a warp, or with more than one group of eight rows, where
   // a tile takes a warp 1 us instead of 0.4, four (28 rows over six sequences of 900 rows: 20.5 us with eight, 17.8 with
   // four; one token of 12 heads over 6000 rows: 11.8 and 12.4)
   if (rows <= kFewRows) return plan_slots(kFew, Hkv, B, keys, 2 * sm_count(), 16, (rows <= 8 ? 8 : 4) * kFewWarps);
   // one CTA, or pair of them, a multiprocessor or two
   const bool alone = d == 128 && rows <= 128;
   const int shares = d == 128 && !alone ? sm_count() / 2 : sm_count();
-  return Plan{alone ? kTensorAlone : kTensor, 0, 0, shares < kMaxTensorShares ? shares : kMaxTensorShares};
+  return Plan{alone ? kTensorAlone : kTensor, 0, 0, shares < paged::kMaxShares ? shares : paged::kMaxShares};
 }
 
 }  // namespace

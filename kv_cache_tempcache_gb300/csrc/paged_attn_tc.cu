@@ -35,9 +35,9 @@
 // 490, exponentials and P 920; then its products are issued, run and reported.  Without the halves' agreement on
 // the reference it would be 4 to 8 % less.
 // Measured, d = 128: 9728 tokens of 4 heads over 37,440 rows 413 to 430 us (1740 to 1800 TFLOP/s, 0.91 to 0.95 of the bf16 rate
-// measured for a library product); 4680 tokens of 12 heads over the same 690 us in a short run, 781 in a long one, under
-// the power limit; the first 4680 tokens in three frames 90 us; 16,384 causal tokens of 16 heads of 4 with a window of 4096 337 to
-// 350 us.  Seven ragged causal sequences of up to 777 tokens, d = 64: 43 us.
+// measured for a library product); 4680 tokens of 12 heads over the same 690 to 704 us in a short run, 760 to 791 in long ones, under
+// the power limit; the first 4680 tokens in three frames 90 us; 16,384 causal tokens of 16 heads of 4 with a window of 4096 339 us
+// in a short run, 349 to 362 in long ones.  Seven ragged causal sequences of up to 777 tokens, d = 64: 43 us.
 //
 // Numbers: logits, maxima, sums and outputs are fp32.  P is bf16, as V is (a product has one type):
 // 2^-8 of itself, at every magnitude, since bf16 has fp32's exponents.

@@ -4,12 +4,12 @@
 // An item is up to `per` rows of a (sequence, KV head): its row tiles 2 (or 1, where the rows fill half of them or
 // less), its key tiles paged.cuh's.  It counts fixed_units and kFull (fewer with one row tile) for each key tile,
 // as its time goes: 1.4 us a key tile, 1.15 with one row tile (a pair; it waits for K and V, which it takes twice as
-// fast), some 8 us around them (5 at d = 64).  Items lie in a row: sequences, their row tiles, the KV heads side by
+// fast), some 8 us around them (5 at d = 64; a CTA alone at d = 128 goes by the same figure, not measured for it).  Items lie in a row: sequences, their row tiles, the KV heads side by
 // side.  Share p of P is the units W p / P .. W (p + 1) / P of that row, so
 // that all shares end together, whatever the lengths: borders cut items between two key tiles (12 heads of 4680
-// tokens are 120 items on 76 pairs of CTAs: in whole items 2 waves, dealt out 1.53).  A cut leaves parts of kMinTiles
-// key tiles or more (with three instead of one, ragged sequences of 7 key tiles a piece took 47.2 us instead of 44.4: what
-// one share lost its neighbour had to do); there are no more shares than have an item of four key tiles each.  Without a
+// tokens are 120 items on 76 pairs of CTAs: in whole items 2 waves, dealt out 1.53).  A cut may leave a
+// part of one key tile (with no part below three, ragged sequences of 7 key tiles a piece took 47.2 us instead of 44.4:
+// what one share lost its neighbour had to do); there are no more shares than have an item of four key tiles each.  Without a
 // workspace borders move to the nearer end of the item.
 #pragma once
 
@@ -20,7 +20,7 @@
 namespace fastar {
 namespace paged {
 
-constexpr int kFull = 6, kMinTiles = 1;
+constexpr int kFull = 6;
 // pairs of CTAs, single ones
 __device__ __forceinline__ int half_units(int per) { return per == 512 ? 5 : 4; }
 __device__ __forceinline__ int fixed_units(int per) { return per == 512 ? 36 : 18; }
@@ -173,8 +173,8 @@ __device__ __forceinline__ int border_tile(const Share& sh, const Item& it, int6
   if (o <= 0) return 0;
   if (o >= it.units) return n;
   if (!sh.cuts) return 2 * o <= it.units ? 0 : n;
-  const int fixed = fixed_units(per), j = o <= fixed ? 0 : (int)(o - fixed) / (it.nt == 2 ? kFull : half_units(per));
-  return j < kMinTiles ? 0 : n - j < kMinTiles ? n : j;
+  const int fixed = fixed_units(per);
+  return o <= fixed ? 0 : (int)(o - fixed) / (it.nt == 2 ? kFull : half_units(per));
 }
 __device__ __forceinline__ int border(const Share& sh, int p, const Item& it, int per) {
   return border_tile(sh, it, share_border(sh, p), per);
